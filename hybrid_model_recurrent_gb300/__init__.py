@@ -9,13 +9,20 @@ the caller does not pass are allocated here.  The names follow the C ABI in
 * ``gdn_resume_from_ckpt``  resume at overlap depth d from the deepest stored state
 * ``gdn_tail_replay``       Tail-Replay from a zero state at a = m - ceil(r m)
 * ``gdn_step``              the three above for one serving step, in one launch
-* host helpers ``gdn_replay_plan``, ``gdn_select_ckpt``, status utilities.
+* host helpers ``gdn_replay_plan``, ``gdn_select_ckpt``, status utilities;
+
+and in ``include/gdn_hybrid.h`` (the other layers of a hybrid model):
+
+* ``gdn_linear_prefill``    linear attention with a decay for each head, prompts
+* ``gdn_linear_step``       the same, one token a request, states in place
+* ``gdn_prefix_attention``  attention of a batch that shares a long prefix
 
 There is no fallback: if the compiled library is missing the import of a
 compute entry point raises.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 import threading
@@ -74,6 +81,23 @@ class _Problem(ctypes.Structure):
                 ("qkv_dtype", ctypes.c_int), ("out_dtype", ctypes.c_int), ("algo", ctypes.c_int)]
 
 
+class _LinearProblem(ctypes.Structure):
+    _fields_ = [("num_seqs", ctypes.c_int32), ("num_heads", ctypes.c_int32), ("num_qk_heads", ctypes.c_int32),
+                ("d_k", ctypes.c_int32), ("d_v", ctypes.c_int32), ("cu_seqlens", _pi64),
+                ("qkv_dtype", ctypes.c_int), ("out_dtype", ctypes.c_int), ("scale", ctypes.c_float),
+                ("q_stride", ctypes.c_int64), ("k_stride", ctypes.c_int64), ("v_stride", ctypes.c_int64)]
+
+
+class _PrefixProblem(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int32), ("num_queries", ctypes.c_int32), ("num_q_heads", ctypes.c_int32),
+                ("num_kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32), ("dtype", ctypes.c_int),
+                ("prefix_len", ctypes.c_int64), ("tail_cap", ctypes.c_int64), ("max_tail", ctypes.c_int64),
+                ("softmax_scale", ctypes.c_float)] + [
+        (n, ctypes.c_int64) for n in ("q_stride_b", "q_stride_n", "q_stride_h", "kp_stride_t", "kp_stride_h",
+                                      "vp_stride_t", "vp_stride_h", "kt_stride_b", "kt_stride_t", "kt_stride_h",
+                                      "vt_stride_b", "vt_stride_t", "vt_stride_h")]
+
+
 def build(force: bool = False) -> str:
     from . import _build
     return _build.build(force=force)
@@ -122,6 +146,17 @@ def lib():
             L.gdn_debug_stall_after.restype = None
             L.gdn_status_string.argtypes = [ctypes.c_int]
             L.gdn_status_string.restype = ctypes.c_char_p
+            LP, PP = ctypes.POINTER(_LinearProblem), ctypes.POINTER(_PrefixProblem)
+            L.gdn_linear_scratch_bytes.argtypes = [LP]
+            L.gdn_linear_scratch_bytes.restype = sz
+            L.gdn_linear_prefill.argtypes = [LP, vp, vp, vp, vp, vp, pi32, i64, vp, vp, pi64, pi64, vp, vp, sz, vp, sz,
+                                             vp]
+            L.gdn_linear_step.argtypes = [LP, vp, vp, vp, vp, vp, i64, vp, vp, vp]
+            L.gdn_prefix_scratch_bytes.argtypes = [PP]
+            L.gdn_prefix_scratch_bytes.restype = sz
+            L.gdn_prefix_attention.argtypes = [PP, vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp, sz, vp]
+            for f in ("gdn_linear_prefill", "gdn_linear_step", "gdn_prefix_attention"):
+                getattr(L, f).restype = ctypes.c_int
             for f in ("gdn_prefill_ckpt", "gdn_resume_from_ckpt", "gdn_tail_replay", "gdn_step", "gdn_replay_plan",
                       "gdn_select_ckpt", "gdn_clear_status", "gdn_read_status"):
                 getattr(L, f).restype = ctypes.c_int
@@ -597,3 +632,197 @@ def gdn_adaptive_replay_plan(alpha, cu_seqlens, m, eps: float, rmax_num: int, rm
                                         _stream(stream, alpha.device))
     _check(rc, "gdn_adaptive_replay_plan")
     return k_out.tolist(), ex.tolist()
+
+
+# ---- the other layers of a hybrid model (include/gdn_hybrid.h) ---------------------------------------
+
+
+def _expect(ok: bool, message: str) -> None:
+    if not ok:
+        raise ValueError(message)
+
+
+def _on(stream, dev):
+    """Buffers made under this belong to the stream that uses them."""
+    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+
+
+def _dense(x: torch.Tensor, name: str, shape, dtype, dev) -> None:
+    _expect(tuple(x.shape) == tuple(shape) and x.dtype == dtype and x.device == dev and x.is_contiguous(),
+            f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {dev}")
+
+
+def _row_stride(x: torch.Tensor, name: str) -> int:
+    """Elements between the rows of [rows, heads, width] with heads and widths contiguous inside a row."""
+    _, h, d = x.shape
+    _expect((d == 1 or x.stride(2) == 1) and (h == 1 or x.stride(1) == d),
+            f"{name}: heads and widths must be contiguous inside a token's row")
+    if x.shape[0] <= 1:
+        return 0
+    _expect(x.stride(0) >= h * d, f"{name}: rows overlap")
+    return x.stride(0)
+
+
+def _linear_problem(q, k, v, alpha, num_seqs: int, cu, scale: float, out_dtype):
+    _expect(k.dim() == 3 and v.dim() == 3 and (q is None or q.shape == k.shape), "q, k [T, Hk, d_k] and v [T, H, d_v]")
+    _expect(k.shape[0] == v.shape[0] and (q is None or q.dtype == k.dtype) and v.dtype == k.dtype,
+            "q, k and v differ in their tokens or dtype")
+    dev = k.device
+    _expect(v.device == dev and alpha.device == dev and (q is None or q.device == dev), "tensors on different devices")
+    H = v.shape[1]
+    _expect(alpha.dtype == torch.float32 and tuple(alpha.shape) == (H,) and alpha.is_contiguous(),
+            "alpha must be contiguous fp32 [H]")
+    pr = _LinearProblem()
+    pr.num_seqs, pr.num_heads, pr.num_qk_heads, pr.d_k, pr.d_v = num_seqs, H, k.shape[1], k.shape[2], v.shape[2]
+    pr.cu_seqlens = _p64(cu)
+    pr.qkv_dtype, pr.out_dtype, pr.scale = _dtype_code(k.dtype), _dtype_code(out_dtype or k.dtype), float(scale)
+    pr.q_stride = 0 if q is None else _row_stride(q, "q")
+    pr.k_stride, pr.v_stride = _row_stride(k, "k"), _row_stride(v, "v")
+    return pr
+
+
+def gdn_linear_prefill(q, k, v, alpha, cu_seqlens, *, scale: float = 1.0, S0=None, S0_index=None, ckpt_pos=None,
+                       readout: bool = True, out_dtype: Optional[torch.dtype] = None, o=None, S_final=None,
+                       ckpt_states=None, stream=None, ws: Optional[torch.Tensor] = None):
+    """Linear attention with a decay for each head over a ragged batch of prompts (see the header):
+    S_t = alpha_h S_{t-1} + v_t k_t^T, o_t = scale S_t q_t.
+
+    q, k [T, Hk, dk] (head h of v reads head h // (H // Hk)), v [T, H, dv], alpha [H] fp32.  S0 [slots, H, dv, dk]
+    with S0_index: the slot that each sequence starts from (-1: zeros; default: its own number).  ckpt_pos: one list of
+    1-based positions per sequence.  Returns dict(o, S_final, ckpt_states) as gdn_prefill_ckpt."""
+    cu = _i64(cu_seqlens)
+    B = len(cu) - 1
+    dev = k.device
+    out_dtype = out_dtype or k.dtype
+    pr = _linear_problem(q if readout else None, k, v, alpha, B, cu, scale, out_dtype)
+    T, H, dv, dk = v.shape[0], v.shape[1], v.shape[2], k.shape[2]
+    _expect(B >= 1 and int(cu[-1]) == T, "cu_seqlens must end with the number of tokens")
+    _expect(not readout or q is not None, "a readout needs q")
+    flat, cu_ck = _flatten_ckpts(ckpt_pos, B)
+    n_ck = 0 if cu_ck is None else int(cu_ck[-1])
+    index = None
+    if S0 is not None:
+        _expect(S0.dim() == 4, "S0 must be [slots, H, d_v, d_k]")
+        _dense(S0, "S0", (S0.shape[0], H, dv, dk), torch.float32, dev)
+        if S0_index is not None:
+            index = np.ascontiguousarray(np.asarray(list(S0_index), dtype=np.int32))
+            _expect(len(index) == B, "S0_index must give one slot per sequence")
+    else:
+        _expect(S0_index is None, "S0_index without S0")
+    with _on(stream, dev):
+        if not readout:
+            o = None
+        elif o is None:
+            o = torch.empty((T, H, dv), dtype=out_dtype, device=dev)
+        if S_final is None:
+            S_final = torch.empty((B, H, dv, dk), dtype=torch.float32, device=dev)
+        if ckpt_states is None and n_ck > 0:
+            ckpt_states = torch.empty((n_ck, H, dv, dk), dtype=torch.float32, device=dev)
+        nbytes = int(lib().gdn_linear_scratch_bytes(ctypes.byref(pr)))
+        scratch = torch.empty(nbytes, dtype=torch.uint8, device=dev) if nbytes else None
+    if o is not None:
+        _dense(o, "o", (T, H, dv), out_dtype, dev)
+    _dense(S_final, "S_final", (B, H, dv, dk), torch.float32, dev)
+    if n_ck > 0:
+        _dense(ckpt_states, "ckpt_states", (n_ck, H, dv, dk), torch.float32, dev)
+    ws = ws if ws is not None else workspace(dev)
+    rc = lib().gdn_linear_prefill(
+        ctypes.byref(pr), _ptr(q if readout else None), _ptr(k), _ptr(v), _ptr(alpha), _ptr(S0),
+        None if index is None else index.ctypes.data_as(ctypes.POINTER(ctypes.c_int32)),
+        0 if S0 is None else S0.shape[0], _ptr(o), _ptr(S_final), _p64(flat) if n_ck > 0 else None, _p64(cu_ck),
+        _ptr(ckpt_states if n_ck > 0 else None), _ptr(scratch), nbytes, _ptr(ws), ws.numel(), _stream(stream, dev))
+    _check(rc, "gdn_linear_prefill")
+    return {"o": o, "S_final": S_final, "ckpt_states": ckpt_states}
+
+
+def gdn_linear_step(q, k, v, alpha, states, *, slots=None, scale: float = 1.0, out_dtype: Optional[torch.dtype] = None,
+                    o=None, stream=None):
+    """One token a request of the linear attention above, the states updated in place (see the header).
+
+    q, k [B, Hk, dk], v [B, H, dv]; states [num_slots, H, dv, dk] fp32; slots int32 [B] on the GPU (default: request b's
+    slot is b), distinct but for negative ones, which mark padding rows (output 0).  Returns o [B, H, dv]."""
+    dev = k.device
+    B = k.shape[0]
+    out_dtype = out_dtype or k.dtype
+    pr = _linear_problem(q, k, v, alpha, B, None, scale, out_dtype)
+    H, dv, dk = v.shape[1], v.shape[2], k.shape[2]
+    _expect(states.dim() == 4, "states must be [num_slots, H, d_v, d_k]")
+    _dense(states, "states", (states.shape[0], H, dv, dk), torch.float32, dev)
+    if slots is not None:
+        _dense(slots, "slots", (B,), torch.int32, dev)
+    if o is None:
+        with _on(stream, dev):
+            o = torch.empty((B, H, dv), dtype=out_dtype, device=dev)
+    else:
+        _dense(o, "o", (B, H, dv), out_dtype, dev)
+    rc = lib().gdn_linear_step(ctypes.byref(pr), _ptr(q), _ptr(k), _ptr(v), _ptr(alpha), _ptr(states), states.shape[0],
+                               _ptr(slots), _ptr(o), _stream(stream, dev))
+    _check(rc, "gdn_linear_step")
+    return o
+
+
+def _strides(x: torch.Tensor, name: str):
+    """Strides of all dimensions but the last (contiguous) one; 0 stands for one that is never used."""
+    _expect(x.shape[-1] == 1 or x.stride(-1) == 1, f"{name}: the last dimension must be contiguous")
+    out = []
+    for n, s in zip(x.shape[:-1], x.stride()[:-1]):
+        _expect(n <= 1 or s > 0, f"{name}: broadcast dimensions are not supported")
+        out.append(0 if n <= 1 else s)
+    return out
+
+
+def gdn_prefix_attention(q, k_prefix, v_prefix, k_tail=None, v_tail=None, tail_len=None, *,
+                         scale: Optional[float] = None, max_tail: Optional[int] = None, o=None, lse=None, stream=None,
+                         ws: Optional[torch.Tensor] = None):
+    """Attention of a batch that shares a long prefix (see the header).
+
+    q [B, n, Hq, D]: the n last tokens of each request; k_prefix, v_prefix [P, Hkv, D]; k_tail, v_tail [B, cap, Hkv, D]
+    with tail_len int32 [B] on the GPU (query i sees the tail's tokens 0 .. tail_len - n + i), or None.  Any strides whose
+    last dimension is contiguous and whose others are multiples of 16 bytes.  max_tail bounds tail_len (default: cap).
+    scale defaults to D ** -0.5.  Returns dict(o [B, n, Hq, D], lse [B, n, Hq] fp32)."""
+    _expect(q.dim() == 4 and k_prefix.dim() == 3 and v_prefix.shape == k_prefix.shape, "q [B, n, Hq, D], prefix [P, Hkv, D]")
+    B, n, Hq, D = q.shape
+    P, Hkv = k_prefix.shape[:2]
+    dev = q.device
+    given = [k_prefix, v_prefix]
+    cap = 0
+    if k_tail is not None:
+        _expect(v_tail is not None and tail_len is not None, "a tail needs k_tail, v_tail and tail_len")
+        _expect(k_tail.dim() == 4 and v_tail.shape == k_tail.shape and k_tail.shape[0] == B and k_tail.shape[2] == Hkv and
+                k_tail.shape[3] == D, "k_tail, v_tail [B, cap, Hkv, D]")
+        _dense(tail_len, "tail_len", (B,), torch.int32, dev)
+        given += [k_tail, v_tail]
+        cap = k_tail.shape[1]
+    else:
+        _expect(v_tail is None and tail_len is None, "a tail needs k_tail, v_tail and tail_len")
+    _expect(k_prefix.shape[2] == D, "q and the prefix differ in their width")
+    for x in given:
+        _expect(x.dtype == q.dtype and x.device == dev, "q, keys and values differ in dtype or device")
+    pr = _PrefixProblem()
+    pr.batch, pr.num_queries, pr.num_q_heads, pr.num_kv_heads, pr.head_dim = B, n, Hq, Hkv, D
+    pr.dtype = _dtype_code(q.dtype)
+    pr.prefix_len, pr.tail_cap, pr.max_tail = P, cap, cap if max_tail is None else int(max_tail)
+    pr.softmax_scale = float(D ** -0.5 if scale is None else scale)
+    pr.q_stride_b, pr.q_stride_n, pr.q_stride_h = _strides(q, "q")
+    pr.kp_stride_t, pr.kp_stride_h = _strides(k_prefix, "k_prefix")
+    pr.vp_stride_t, pr.vp_stride_h = _strides(v_prefix, "v_prefix")
+    if cap:
+        pr.kt_stride_b, pr.kt_stride_t, pr.kt_stride_h = _strides(k_tail, "k_tail")
+        pr.vt_stride_b, pr.vt_stride_t, pr.vt_stride_h = _strides(v_tail, "v_tail")
+    with _on(stream, dev):
+        if o is None:
+            o = torch.empty((B, n, Hq, D), dtype=q.dtype, device=dev)
+        if lse is None:
+            lse = torch.empty((B, n, Hq), dtype=torch.float32, device=dev)
+        nbytes = int(lib().gdn_prefix_scratch_bytes(ctypes.byref(pr)))
+        scratch = torch.empty(nbytes, dtype=torch.uint8, device=dev) if nbytes else None
+    _dense(o, "o", (B, n, Hq, D), q.dtype, dev)
+    _dense(lse, "lse", (B, n, Hq), torch.float32, dev)
+    ws = ws if ws is not None else workspace(dev)
+    has_tail = cap > 0
+    rc = lib().gdn_prefix_attention(
+        ctypes.byref(pr), _ptr(q), _ptr(k_prefix if P else None), _ptr(v_prefix if P else None),
+        _ptr(k_tail if has_tail else None), _ptr(v_tail if has_tail else None), _ptr(tail_len if has_tail else None),
+        _ptr(o), _ptr(lse), _ptr(scratch), nbytes, _ptr(ws), ws.numel(), _stream(stream, dev))
+    _check(rc, "gdn_prefix_attention")
+    return {"o": o, "lse": lse}

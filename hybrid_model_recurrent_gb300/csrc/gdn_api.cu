@@ -353,6 +353,13 @@ gdn_status run_jobs(const LaunchSpec& L, std::vector<HostJob>& jobs, cudaStream_
 
 }  // namespace
 
+// what the other host files share of this one's settings
+namespace gdn {
+uint64_t wait_limit_ns() { return g_wait_ns.load(); }
+int32_t stall_after() { return g_stall_after.load(); }
+void* encode_tiled_fn() { return reinterpret_cast<void*>(encode_fn()); }
+}  // namespace gdn
+
 // ---------------------------------------------------------------------------------------
 // host-only helpers
 // ---------------------------------------------------------------------------------------

@@ -1,0 +1,327 @@
+// gdn_linear.cu - linear attention with a decay for each head, on the FP32 pipes: the token-by-token scan for
+// every size and type, the chaining of a split scan's segments, and the single-token step.
+//
+// The scan.  Row i of S evolves only from v_{t,i}, so the rows of a head split over warps and CTAs with no
+// exchange.  A warp holds 16 rows: 4 row groups of 8 column lanes, a lane 4 rows x d_k/8 columns in registers.
+// A token costs three FP32 operations per state element (decay, update, readout) and one reduction of the
+// readout over the 8 column lanes: 4 shuffles for 16 rows.  The recurrence itself is one multiply and one FMA
+// deep, so the reductions of successive tokens overlap.  q, k and v arrive by cp.async in tiles of 16
+// (fp32) or 32 (bf16) tokens, double buffered.
+#include <cuda_bf16.h>
+
+#include <algorithm>
+#include <type_traits>
+
+#include "gdn_linear.cuh"
+
+namespace gdn {
+namespace lin {
+namespace {
+
+__device__ __forceinline__ uint32_t saddr(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
+// 16-byte (or 8-byte) asynchronous copy; bytes = 0 fills with zeros
+template <int BYTES>
+__device__ __forceinline__ void cp_async(void* dst, const void* src, int bytes) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(saddr(dst)), "l"(src), "n"(BYTES), "r"(bytes)
+                 : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// N consecutive values as fp32
+template <int N>
+__device__ __forceinline__ void load_vec(const float* p, float (&x)[N]) {
+#pragma unroll
+    for (int i = 0; i < N; i += 4) {
+        const float4 f = *reinterpret_cast<const float4*>(p + i);
+        x[i] = f.x, x[i + 1] = f.y, x[i + 2] = f.z, x[i + 3] = f.w;
+    }
+}
+template <int N>
+__device__ __forceinline__ void load_vec(const __nv_bfloat16* p, float (&x)[N]) {
+    static_assert(N == 4 || N == 8, "8 or 16 bytes");
+    uint32_t w[N / 2];
+    if constexpr (N == 8) {
+        const uint4 u = *reinterpret_cast<const uint4*>(p);
+        w[0] = u.x, w[1] = u.y, w[2] = u.z, w[3] = u.w;
+    } else {
+        const uint2 u = *reinterpret_cast<const uint2*>(p);
+        w[0] = u.x, w[1] = u.y;
+    }
+#pragma unroll
+    for (int i = 0; i < N / 2; ++i) {
+        x[2 * i] = __uint_as_float(w[i] << 16);
+        x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    }
+}
+__device__ __forceinline__ void store_out(float* p, float x) { *p = x; }
+__device__ __forceinline__ void store_out(__nv_bfloat16* p, float x) { *p = __float2bfloat16_rn(x); }
+
+// The columns that a lane holds: NV pieces of VW consecutive ones, piece i at (c + 8 i) VW, so that the 8 column
+// lanes of a row group read 128 consecutive bytes of a fp32 (or 16-byte pieces of a bf16) vector at a time.
+template <int DK, typename T>
+struct Cols {
+    static constexpr int CT = DK / 8;
+    static constexpr int VW = std::is_same<T, float>::value ? 4 : (CT < 8 ? CT : 8);
+    static constexpr int NV = CT / VW;
+    __device__ static __forceinline__ int at(int c, int i) { return (c + 8 * i) * VW; }
+    __device__ static __forceinline__ void load(const T* row, int c, float (&x)[CT]) {
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            float y[VW];
+            load_vec<VW>(row + at(c, i), y);
+#pragma unroll
+            for (int j = 0; j < VW; ++j) x[i * VW + j] = y[j];
+        }
+    }
+    __device__ static __forceinline__ void load_state(const float* row, int c, float (&x)[CT]) {
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            float y[VW];
+            load_vec<VW>(row + at(c, i), y);
+#pragma unroll
+            for (int j = 0; j < VW; ++j) x[i * VW + j] = y[j];
+        }
+    }
+    __device__ static __forceinline__ void store_state(float* row, int c, const float (&x)[CT]) {
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+#pragma unroll
+            for (int j = 0; j < VW; j += 4)
+                *reinterpret_cast<float4*>(row + at(c, i) + j) =
+                    make_float4(x[i * VW + j], x[i * VW + j + 1], x[i * VW + j + 2], x[i * VW + j + 3]);
+    }
+};
+
+// Sums of four rows' partial values over the 8 column lanes: each round keeps half of the rows and sends the
+// other half, so lane c ends with row (c >> 1)'s sum (lanes c and c ^ 1 the same one).
+__device__ __forceinline__ float reduce_rows(const float (&p)[4], int c) {
+    const bool u4 = c & 4, u2 = c & 2;
+    float a = u4 ? p[2] : p[0], b = u4 ? p[3] : p[1];
+    a += __shfl_xor_sync(0xffffffffu, u4 ? p[0] : p[2], 4);
+    b += __shfl_xor_sync(0xffffffffu, u4 ? p[1] : p[3], 4);
+    float x = (u2 ? b : a) + __shfl_xor_sync(0xffffffffu, u2 ? a : b, 2);
+    return x + __shfl_xor_sync(0xffffffffu, x, 1);
+}
+
+template <int DK, typename T, typename OutT>
+__global__ void __launch_bounds__(128) linear_scan_kernel(const __grid_constant__ Params p) {
+    using CM = Cols<DK, T>;
+    constexpr int CT = CM::CT;
+    constexpr int kPiece = 16 / (int)sizeof(T);         // elements of a 16-byte copy
+    constexpr int kTile = sizeof(T) == 4 ? 16 : 32;     // tokens of a staged tile (within 48 KB of static memory)
+    __shared__ __align__(16) T sk[2][kTile][DK];
+    __shared__ __align__(16) T sq[2][kTile][DK];
+    __shared__ __align__(16) T sv[2][kTile][64];
+
+    const int RB = p.rows_per_cta;
+    const int blocks = p.dv / RB;
+    const int rb = blockIdx.x % blocks;
+    const int h = (blockIdx.x / blocks) % p.H;
+    const Job& job = p.jobs[blockIdx.x / (blocks * p.H)];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int c = lane & 7, rg = lane >> 3;
+    const int row0 = rb * RB + warp * kWarpRows + rg * 4;   // first of this lane's 4 state rows
+    const int hk = h / p.rep;
+    const int len = job.len;
+    const bool rd = p.o != nullptr;
+    const float a = p.alpha[h];
+    const size_t head = (size_t)h * p.dv * DK;
+
+    float S[4][CT];
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+        if (job.s0) {
+            CM::load_state(job.s0 + head + (size_t)(row0 + r) * DK, c, S[r]);
+        } else {
+#pragma unroll
+            for (int j = 0; j < CT; ++j) S[r][j] = 0.f;
+        }
+    }
+
+    const T* gk = static_cast<const T*>(p.k) + job.tok_begin * p.k_stride + (int64_t)hk * DK;
+    const T* gq = rd ? static_cast<const T*>(p.q) + job.tok_begin * p.q_stride + (int64_t)hk * DK : nullptr;
+    const T* gv = static_cast<const T*>(p.v) + job.tok_begin * p.v_stride + (int64_t)h * p.dv + rb * RB;
+    OutT* go = rd ? static_cast<OutT*>(p.o) + (job.tok_begin * p.H + h) * (int64_t)p.dv + row0 : nullptr;
+
+    auto stage = [&](int tile) {
+        const int t0 = tile * kTile, buf = tile & 1;
+        for (int i = tid; i < kTile * (DK / kPiece); i += blockDim.x) {
+            const int t = i / (DK / kPiece), x = (i % (DK / kPiece)) * kPiece;
+            const int ts = min(t0 + t, len - 1);   // past the end: a valid address, nothing copied
+            const int n = t0 + t < len ? 16 : 0;
+            cp_async<16>(&sk[buf][t][x], gk + (int64_t)ts * p.k_stride + x, n);
+            if (rd) cp_async<16>(&sq[buf][t][x], gq + (int64_t)ts * p.q_stride + x, n);
+        }
+        for (int i = tid; i < kTile * (RB / kPiece); i += blockDim.x) {
+            const int t = i / (RB / kPiece), x = (i % (RB / kPiece)) * kPiece;
+            const int ts = min(t0 + t, len - 1);
+            cp_async<16>(&sv[buf][t][x], gv + (int64_t)ts * p.v_stride + x, t0 + t < len ? 16 : 0);
+        }
+        cp_commit();
+    };
+
+    const int tiles = (len + kTile - 1) / kTile;
+    int ck = job.ck_begin;
+    const int ck_end = job.ck_begin + job.ck_count;
+    int next_ck = ck < ck_end ? p.ckpts[ck].pos : INT32_MAX;
+    if (tiles > 0) stage(0);
+    for (int tile = 0; tile < tiles; ++tile) {
+        if (tile + 1 < tiles) {
+            stage(tile + 1);
+            cp_wait<1>();
+        } else {
+            cp_wait<0>();
+        }
+        __syncthreads();
+        const int buf = tile & 1, n = min(kTile, len - tile * kTile);
+        for (int t = 0; t < n; ++t) {
+            float kk[CT], vv[4];
+            CM::load(sk[buf][t], c, kk);
+            load_vec<4>(&sv[buf][t][warp * kWarpRows + rg * 4], vv);
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+#pragma unroll
+                for (int j = 0; j < CT; ++j) S[r][j] = fmaf(vv[r], kk[j], a * S[r][j]);
+            if (rd) {
+                float qq[CT], part[4];
+                CM::load(sq[buf][t], c, qq);
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    float x = 0.f;
+#pragma unroll
+                    for (int j = 0; j < CT; ++j) x = fmaf(S[r][j], qq[j], x);
+                    part[r] = x;
+                }
+                const float x = reduce_rows(part, c);
+                if ((c & 1) == 0) store_out(go + (int64_t)(tile * kTile + t) * p.H * p.dv + (c >> 1), x * p.scale);
+            }
+            if (tile * kTile + t + 1 == next_ck) {
+                float* dst = p.ckpt_states + (size_t)p.ckpts[ck].slot * p.H * p.dv * DK + head;
+#pragma unroll
+                for (int r = 0; r < 4; ++r) CM::store_state(dst + (size_t)(row0 + r) * DK, c, S[r]);
+                ++ck;
+                next_ck = ck < ck_end ? p.ckpts[ck].pos : INT32_MAX;
+            }
+        }
+        __syncthreads();   // the next tile's copies overwrite this buffer
+    }
+    if (job.s_final) {
+#pragma unroll
+        for (int r = 0; r < 4; ++r) CM::store_state(job.s_final + head + (size_t)(row0 + r) * DK, c, S[r]);
+    }
+}
+
+// Initial states of a split scan's segments: start_{j+1} = alpha^L start_j + own_j, in place (slot j holds own_j and
+// receives start_{j+1}).  One thread takes four elements of one head's state through all segments; bound by the
+// traffic of the states.  alpha^L is formed in fp64: its exponent would lose up to 2^-24 |L log2 alpha| in fp32.
+__global__ void __launch_bounds__(128) chain_kernel(const __grid_constant__ ChainParams p) {
+    const int per_head = p.state / 4;
+    const int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
+    if (i >= (int64_t)p.n_scans * p.H * per_head) return;
+    const int e = (int)(i % per_head) * 4;
+    const int h = (int)(i / per_head % p.H);
+    const Chain& sc = p.scans[i / per_head / p.H];
+    const float w = (float)pow((double)p.alpha[h], (double)p.seg_len);
+    const size_t all = (size_t)p.H * p.state, off = (size_t)h * p.state + e;
+    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (sc.s0) x = *reinterpret_cast<const float4*>(sc.s0 + off);
+    float* st = p.states + (size_t)sc.slot * all + off;
+    for (int j = 0; j < sc.n; ++j, st += all) {
+        const float4 y = *reinterpret_cast<const float4*>(st);
+        x.x = fmaf(w, x.x, y.x), x.y = fmaf(w, x.y, y.y), x.z = fmaf(w, x.z, y.z), x.w = fmaf(w, x.w, y.w);
+        *reinterpret_cast<float4*>(st) = x;
+    }
+}
+
+// One token a request.  A warp takes 16 rows of one (request, head)'s state, held as in the scan, with every load
+// issued before the first use; bound by the state's traffic (read and written once).
+template <int DK, typename T, typename OutT>
+__global__ void __launch_bounds__(128) linear_step_kernel(const __grid_constant__ StepParams p) {
+    using CM = Cols<DK, T>;
+    constexpr int CT = CM::CT;
+    const int lane = threadIdx.x & 31;
+    const int c = lane & 7, rg = lane >> 3;
+    const int per_head = p.dv / kWarpRows;
+    const int64_t w = (int64_t)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);
+    if (w >= (int64_t)p.B * p.H * per_head) return;
+    const int row0 = (int)(w % per_head) * kWarpRows + rg * 4;
+    const int h = (int)(w / per_head % p.H);
+    const int b = (int)(w / per_head / p.H);
+    OutT* o = static_cast<OutT*>(p.o) + ((int64_t)b * p.H + h) * p.dv + row0;
+    const int64_t slot = p.slots ? p.slots[b] : b;
+    if (slot < 0 || slot >= p.num_slots) {
+        if ((c & 1) == 0) store_out(o + (c >> 1), 0.f);
+        return;
+    }
+    float* st = p.states + ((slot * p.H + h) * p.dv + row0) * DK;
+    float S[4][CT], kk[CT], qq[CT], vv[4];
+#pragma unroll
+    for (int r = 0; r < 4; ++r) CM::load_state(st + r * DK, c, S[r]);
+    const int hk = h / p.rep;
+    CM::load(static_cast<const T*>(p.k) + b * p.k_stride + (int64_t)hk * DK, c, kk);
+    CM::load(static_cast<const T*>(p.q) + b * p.q_stride + (int64_t)hk * DK, c, qq);
+    load_vec<4>(static_cast<const T*>(p.v) + b * p.v_stride + (int64_t)h * p.dv + row0, vv);
+    const float a = p.alpha[h];
+    float part[4];
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+        float x = 0.f;
+#pragma unroll
+        for (int j = 0; j < CT; ++j) {
+            S[r][j] = fmaf(vv[r], kk[j], a * S[r][j]);
+            x = fmaf(S[r][j], qq[j], x);
+        }
+        part[r] = x;
+        CM::store_state(st + r * DK, c, S[r]);
+    }
+    const float x = reduce_rows(part, c);
+    if ((c & 1) == 0) store_out(o + (c >> 1), x * p.scale);
+}
+
+template <int DK>
+cudaError_t scan_types(const Params& p, bool in_bf16, bool out_bf16, cudaStream_t s) {
+    const int grid = p.n_jobs * p.H * (p.dv / p.rows_per_cta);
+    const int threads = 32 * (p.rows_per_cta / kWarpRows);
+    if (in_bf16 && out_bf16) linear_scan_kernel<DK, __nv_bfloat16, __nv_bfloat16><<<grid, threads, 0, s>>>(p);
+    else if (in_bf16) linear_scan_kernel<DK, __nv_bfloat16, float><<<grid, threads, 0, s>>>(p);
+    else if (out_bf16) linear_scan_kernel<DK, float, __nv_bfloat16><<<grid, threads, 0, s>>>(p);
+    else linear_scan_kernel<DK, float, float><<<grid, threads, 0, s>>>(p);
+    return cudaGetLastError();
+}
+
+template <int DK>
+cudaError_t step_types(const StepParams& p, bool in_bf16, bool out_bf16, cudaStream_t s) {
+    const int64_t warps = (int64_t)p.B * p.H * (p.dv / kWarpRows);
+    const int per = 4;
+    const int grid = (int)((warps + per - 1) / per), threads = 32 * per;
+    if (in_bf16 && out_bf16) linear_step_kernel<DK, __nv_bfloat16, __nv_bfloat16><<<grid, threads, 0, s>>>(p);
+    else if (in_bf16) linear_step_kernel<DK, __nv_bfloat16, float><<<grid, threads, 0, s>>>(p);
+    else if (out_bf16) linear_step_kernel<DK, float, __nv_bfloat16><<<grid, threads, 0, s>>>(p);
+    else linear_step_kernel<DK, float, float><<<grid, threads, 0, s>>>(p);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_simt(const Params& p, int dk, bool in_bf16, bool out_bf16, cudaStream_t stream) {
+    if (dk == 32) return scan_types<32>(p, in_bf16, out_bf16, stream);
+    if (dk == 64) return scan_types<64>(p, in_bf16, out_bf16, stream);
+    return scan_types<128>(p, in_bf16, out_bf16, stream);
+}
+cudaError_t launch_step(const StepParams& p, int dk, bool in_bf16, bool out_bf16, cudaStream_t stream) {
+    if (dk == 32) return step_types<32>(p, in_bf16, out_bf16, stream);
+    if (dk == 64) return step_types<64>(p, in_bf16, out_bf16, stream);
+    return step_types<128>(p, in_bf16, out_bf16, stream);
+}
+cudaError_t launch_chain(const ChainParams& p, cudaStream_t stream) {
+    const int64_t n = (int64_t)p.n_scans * p.H * (p.state / 4);
+    chain_kernel<<<(unsigned)((n + 127) / 128), 128, 0, stream>>>(p);
+    return cudaGetLastError();
+}
+
+}  // namespace lin
+}  // namespace gdn

@@ -1,0 +1,59 @@
+// gdn_prefix.cuh - attention for a batch that shares a long prefix: the parameter block and launchers shared by
+// the kernels (gdn_prefix.cu: every size and type, and the join; gdn_prefix_tc.cu: tensor cores) and the host
+// side (gdn_hybrid_api.cu).
+//
+// The work falls into parts: `pre_splits` ranges of the prefix, taken by the stacked query rows of all requests,
+// and `tail_splits` ranges of each request's own tail, taken by its own rows.  A part leaves, for every query row,
+// the maximum m of its scores (times log2 e), l = sum 2^(x - m) and the unnormalised sum of values; the join adds the
+// parts up.  Query rows of one key/value head are ordered by request, query and head of the group.
+#pragma once
+
+#include <cuda.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+namespace gdn {
+namespace prefix {
+
+struct Params {
+    CUtensorMap tm_kp, tm_vp, tm_kt, tm_vt;   // tensor-core kernel only
+    const void* q;
+    const void* kp;
+    const void* vp;
+    const void* kt;
+    const void* vt;
+    int64_t q_sb, q_sn, q_sh;                  // strides in elements
+    int64_t kp_st, kp_sh, vp_st, vp_sh;
+    int64_t kt_sb, kt_st, kt_sh, vt_sb, vt_st, vt_sh;
+    const int32_t* tail_len;
+    void* o;           // [B, n, Hq, D]
+    float* lse;        // [B, n, Hq] or nullptr
+    float* part_o;     // [parts][B n Hq][D]
+    float2* part_ml;   // [parts][B n Hq]: m, l (l = 0: an empty part, whose part_o is not read)
+    unsigned int* status;
+    unsigned long long wait_limit_ns;
+    int64_t prefix_len, max_tail;
+    float scale_log2;               // softmax_scale * log2 e
+    int32_t B, n, Hq, Hkv, G;       // G = Hq / Hkv
+    int32_t pre_splits, pre_chunk;  // prefix range s: [s * pre_chunk, (s + 1) * pre_chunk) cut at prefix_len
+    int32_t tail_splits;            // tail range s of S: a share of the request's own length (tail_range)
+    int32_t pre_tiles, tail_tiles;  // row tiles of the stacked rows, and of one request's rows
+    int32_t stall_after;
+};
+
+// Range s of `splits` of a tail of `len` tokens: equal shares, rounded up to whole tiles of `tile` tokens.
+__host__ __device__ inline void tail_range(int len, int splits, int tile, int s, int* lo, int* hi) {
+    const int share = ((len + splits - 1) / splits + tile - 1) / tile * tile;
+    const long long a = (long long)s * share, b = a + share;
+    *lo = a < len ? (int)a : len;
+    *hi = b < len ? (int)b : len;
+}
+
+constexpr int kSimtRows = 16;    // query rows of a tile of the FP32-pipe kernel
+constexpr int kSimtKeys = 32;    // tokens of a staged tile
+
+cudaError_t launch_simt(const Params& p, int D, bool bf16, cudaStream_t stream);
+cudaError_t launch_join(const Params& p, int D, bool bf16, int parts, cudaStream_t stream);
+
+}  // namespace prefix
+}  // namespace gdn
