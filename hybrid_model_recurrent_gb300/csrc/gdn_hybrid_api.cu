@@ -250,9 +250,12 @@ gdn_status linear_prefill(const gdn_linear_problem* p, const void* q, const void
 // ---- shared-prefix attention ------------------------------------------------------------
 
 struct PrefixPlan {
+    bool tc, joined;
+    int pre_rt, tail_rt;   // tensor cores: row tiles of a CTA
     int pre_splits, pre_chunk, tail_splits, pre_tiles, tail_tiles;
-    int64_t rows;    // query rows of all heads
+    int64_t rows;          // query rows of all heads
     size_t ml_off, o_off, total;
+    int parts() const { return pre_splits + tail_splits; }
 };
 
 gdn_status check_prefix(const gdn_prefix_problem* p, gdn_prefix_problem& f) {
@@ -283,26 +286,86 @@ gdn_status check_prefix(const gdn_prefix_problem* p, gdn_prefix_problem& f) {
     return GDN_OK;
 }
 
+// In how many ranges to cut `tiles` tiles of tokens that `items` row tiles take, with `slots` CTAs at once: the fewest
+// tile times, counting whole waves, two tile times for a CTA's start and end, and the join's reading and writing of
+// each range's partial sums (at about 10 TB/s from L2, against a tile time of about 1.2 us).
+int best_splits(int64_t tiles, int64_t items, int64_t slots, int64_t part_bytes) {
+    int64_t best = 1;
+    double best_cost = 1e300;
+    for (int64_t s = 1; s <= std::min<int64_t>(tiles, 256); ++s) {
+        const int64_t per = ceil_div(tiles, s);
+        if (ceil_div(tiles, per) != s) continue;   // the same ranges as fewer splits
+        const double cost = (double)ceil_div(items * s, slots) * (double)(per + 2) + (double)(s * part_bytes) / 1.2e7;
+        if (cost < best_cost) best_cost = cost, best = s;
+    }
+    return (int)best;
+}
+
 PrefixPlan plan_prefix(const gdn_prefix_problem& f) {
     PrefixPlan pl{};
     pl.rows = (int64_t)f.batch * f.num_queries * f.num_q_heads;
-    const int64_t group = f.num_q_heads / f.num_kv_heads, RT = gdn::prefix::kSimtRows, unit = 256, target = kSms * 8;
-    pl.pre_tiles = (int)ceil_div((int64_t)f.batch * f.num_queries * group, RT);
-    pl.tail_tiles = (int)ceil_div((int64_t)f.num_queries * group, RT);
-    auto splits = [&](int64_t len, int64_t items) {
-        return std::max<int64_t>(1, std::min({ceil_div(len, unit), target / std::max<int64_t>(items, 1), (int64_t)256}));
-    };
+    const int64_t group = f.num_q_heads / f.num_kv_heads, own = f.num_queries * group, stacked = own * f.batch;
+    pl.tc = f.dtype == GDN_BF16 && f.head_dim >= 64;
+    pl.pre_rt = pl.tail_rt = 1;
+    const int64_t part_bytes = pl.rows * (f.head_dim * 4 + 8) * 2;
+    int64_t unit;   // tokens of a tile
+    int64_t pre_slots, tail_slots;
+    if (pl.tc) {
+        unit = gdn::prefix::kTcKeys;
+        // A request with a whole row tile of its own needs no stacking: when such tiles fill the GPU, each takes prefix
+        // and tail in one go and writes its rows itself.
+        const int64_t pairs = ceil_div(own, 2 * gdn::prefix::kTcRows);
+        if (own > gdn::prefix::kTcRows && f.batch * f.num_kv_heads * pairs >= kSms && f.prefix_len + f.max_tail > 0) {
+            pl.joined = true;
+            pl.tail_rt = 2;
+            pl.tail_tiles = (int)pairs;
+            pl.tail_splits = 1;
+            return pl;
+        }
+        // two row tiles a CTA halve the reads of keys and values; one leaves room for two CTAs
+        pl.pre_rt = stacked > gdn::prefix::kTcRows ? 2 : 1;
+        pl.tail_rt = own > gdn::prefix::kTcRows ? 2 : 1;
+        pl.pre_tiles = (int)ceil_div(stacked, pl.pre_rt * gdn::prefix::kTcRows);
+        pl.tail_tiles = (int)ceil_div(own, pl.tail_rt * gdn::prefix::kTcRows);
+        pre_slots = kSms * (3 - pl.pre_rt), tail_slots = kSms * (3 - pl.tail_rt);
+    } else {
+        unit = gdn::prefix::kSimtKeys;
+        pl.pre_tiles = (int)ceil_div(stacked, gdn::prefix::kSimtRows);
+        pl.tail_tiles = (int)ceil_div(own, gdn::prefix::kSimtRows);
+        pre_slots = tail_slots = kSms * 5;   // CTAs that 43 KB of shared memory let run at once
+    }
     if (f.prefix_len > 0) {
-        const int64_t s = splits(f.prefix_len, (int64_t)f.num_kv_heads * pl.pre_tiles);
-        pl.pre_chunk = (int)(ceil_div(ceil_div(f.prefix_len, s), 128) * 128);
+        const int64_t tiles = ceil_div(f.prefix_len, unit);
+        const int s = best_splits(tiles, (int64_t)f.num_kv_heads * pl.pre_tiles, pre_slots, part_bytes);
+        pl.pre_chunk = (int)(ceil_div(tiles, s) * unit);
         pl.pre_splits = (int)ceil_div(f.prefix_len, pl.pre_chunk);
     }
-    if (f.max_tail > 0) pl.tail_splits = (int)splits(f.max_tail, (int64_t)f.batch * f.num_kv_heads * pl.tail_tiles);
-    const int64_t parts = pl.pre_splits + pl.tail_splits;
+    if (f.max_tail > 0)
+        pl.tail_splits = best_splits(ceil_div(f.max_tail, unit), (int64_t)f.batch * f.num_kv_heads * pl.tail_tiles,
+                                     tail_slots, part_bytes);
+    const int64_t parts = pl.parts();
+    if (parts == 0 || (pl.tc && parts == 1)) return pl;
     pl.ml_off = 0;
     pl.o_off = (size_t)ceil_div(parts * pl.rows * 8, 256) * 256;
-    pl.total = parts ? pl.o_off + (size_t)parts * pl.rows * f.head_dim * 4 : 0;
+    pl.total = pl.o_off + (size_t)parts * pl.rows * f.head_dim * 4;
     return pl;
+}
+
+// [tokens, heads, D] or [requests, tokens, heads, D] as a tensor map of boxes of 128 tokens x 64 columns
+bool prefix_map(CUtensorMap* m, const void* base, const gdn_prefix_problem& f, int64_t tokens, int64_t st, int64_t sh,
+                int64_t sb) {
+    auto enc = reinterpret_cast<CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                             const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                             CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill)>(
+        gdn::encode_tiled_fn());
+    if (!enc) return false;
+    const cuuint64_t dims[4] = {(cuuint64_t)f.head_dim, (cuuint64_t)f.num_kv_heads, (cuuint64_t)tokens,
+                                (cuuint64_t)f.batch};
+    const cuuint64_t strides[3] = {(cuuint64_t)(sh * 2), (cuuint64_t)(st * 2), (cuuint64_t)(sb * 2)};
+    const cuuint32_t box[4] = {64, 1, (cuuint32_t)gdn::prefix::kTcKeys, 1}, one[4] = {1, 1, 1, 1};
+    return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, sb ? 4 : 3, const_cast<void*>(base), dims, strides, box, one,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 gdn_status prefix_attention(const gdn_prefix_problem* p, const void* q, const void* k_prefix, const void* v_prefix,
@@ -319,7 +382,7 @@ gdn_status prefix_attention(const gdn_prefix_problem* p, const void* q, const vo
                            !aligned(tail_len, 4)))
         return GDN_ERR_INVALID_ARG;
     const PrefixPlan pl = plan_prefix(f);
-    if (pl.total > 0 && (!scratch || !aligned(scratch, 16) || scratch_bytes < pl.total)) return GDN_ERR_INVALID_ARG;
+    if (pl.total > 0 && (!scratch || !aligned(scratch, 32) || scratch_bytes < pl.total)) return GDN_ERR_INVALID_ARG;
     const int64_t items = f.num_kv_heads * ((int64_t)pl.pre_splits * pl.pre_tiles + (int64_t)pl.tail_splits * pl.tail_tiles * f.batch);
     if (items >= (1ll << 31)) return GDN_ERR_UNSUPPORTED;
 
@@ -345,10 +408,33 @@ gdn_status prefix_attention(const gdn_prefix_problem* p, const void* q, const vo
     prm->pre_splits = pl.pre_splits, prm->pre_chunk = pl.pre_chunk, prm->tail_splits = pl.tail_splits;
     prm->pre_tiles = pl.pre_tiles, prm->tail_tiles = pl.tail_tiles;
     const bool bf16 = f.dtype == GDN_BF16;
-    if (gdn::prefix::launch_simt(*prm, f.head_dim, bf16, stream) != cudaSuccess) return GDN_ERR_CUDA;
-    return gdn::prefix::launch_join(*prm, f.head_dim, bf16, pl.pre_splits + pl.tail_splits, stream) == cudaSuccess
-               ? GDN_OK
-               : GDN_ERR_CUDA;
+    const int64_t pre_items = (int64_t)f.num_kv_heads * pl.pre_splits * pl.pre_tiles;
+    const int64_t tail_items = items - pre_items;
+    if (pl.tc) {
+        bool maps = true;
+        if (f.prefix_len > 0)
+            maps = prefix_map(&prm->tm_kp, k_prefix, f, f.prefix_len, f.kp_stride_t, f.kp_stride_h, 0) &&
+                   prefix_map(&prm->tm_vp, v_prefix, f, f.prefix_len, f.vp_stride_t, f.vp_stride_h, 0);
+        if (maps && f.max_tail > 0)
+            maps = prefix_map(&prm->tm_kt, k_tail, f, f.tail_cap, f.kt_stride_t, f.kt_stride_h, f.kt_stride_b) &&
+                   prefix_map(&prm->tm_vt, v_tail, f, f.tail_cap, f.vt_stride_t, f.vt_stride_h, f.vt_stride_b);
+        if (!maps) return GDN_ERR_CUDA;
+        const bool direct = pl.parts() == 1;
+        cudaError_t e;
+        if (pl.pre_rt == pl.tail_rt || pre_items == 0 || tail_items == 0) {
+            e = gdn::prefix::launch_tc(*prm, f.head_dim, pre_items ? pl.pre_rt : pl.tail_rt, pre_items, tail_items,
+                                       pl.joined, direct, stream);
+        } else {
+            e = gdn::prefix::launch_tc(*prm, f.head_dim, pl.pre_rt, pre_items, 0, false, direct, stream);
+            if (e == cudaSuccess)
+                e = gdn::prefix::launch_tc(*prm, f.head_dim, pl.tail_rt, 0, tail_items, false, direct, stream);
+        }
+        if (e != cudaSuccess) return GDN_ERR_CUDA;
+        if (direct) return GDN_OK;
+    } else if (gdn::prefix::launch_simt(*prm, f.head_dim, bf16, stream) != cudaSuccess) {
+        return GDN_ERR_CUDA;
+    }
+    return gdn::prefix::launch_join(*prm, f.head_dim, bf16, pl.parts(), stream) == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
 }
 
 }  // namespace

@@ -1,0 +1,449 @@
+// gdn_prefix_tc.cu - attention for a batch that shares a long prefix, on the 5th-generation tensor cores (bf16,
+// head_dim 64 or 128).
+//
+// A CTA takes NT tiles of 128 query rows of one key/value head (stacked over requests, queries and the heads of the
+// group) against a range of the prefix, a range of one request's tail, or both in turn, in tiles of 128 tokens:
+//     S = Q K^T  (TMEM, fp32)  ->  P = 2^(x - m) (bf16, over S's own columns)  ->  O += P V  (TMEM, fp32)
+// one pass over keys and values with each row's running maximum m and sum l.  A thread owns a row, so the statistics
+// need no exchange.  O is rescaled only when a row's maximum has risen by more than 2^8 since m was set: until then the
+// weights are at most 2^8 and only their common scale differs.  Scores, statistics and sums are fp32; the weights are
+// rounded to bf16 for the product (half a step, 2^-8 of each weight), as the tensor cores take them.
+//
+// Roles: warps 0 .. 4 NT - 1 softmax (one warpgroup a row tile), then one MMA-issuing thread and one copying thread.
+// K and V tiles arrive by TMA in a ring of ST tiles; with NT = 2 both row tiles use each tile, and one tile's softmax
+// runs beside the other's products.  With NT = 1 two CTAs share a multiprocessor and overlap each other instead.
+//
+// A masked token's score is replaced (not multiplied), and value rows past the range are zeroed in shared memory
+// before the product, so nothing that lies past a tail's end reaches a result.
+//
+// Every wait is bounded: a role that gives up sets the CTA's abort flag and the sticky status, every role leaves its
+// loop, copies and products in flight are waited for, and TMEM is freed.
+#include <cuda_bf16.h>
+
+#include <cmath>
+
+#include "gdn_chunk_tc.cuh"
+#include "gdn_prefix.cuh"
+
+namespace gdn {
+namespace prefix {
+namespace {
+
+using tc::idesc;
+using tc::proxy_fence;
+using tc::sdesc;
+using tc::sw128;
+using tc::tc_fence_after;
+using tc::tc_fence_before;
+using tc::tmem_ld32;
+using tc::tmem_ld32x2;
+using tc::tmem_st16;
+using tc::tmem_st32;
+using tc::tmem_st_wait;
+using tc::umma_commit;
+using tc::umma_ss;
+using tc::umma_ts;
+
+constexpr int kRows = 128;   // rows of a tile
+constexpr int kKeys = 128;   // tokens of a tile
+constexpr float kRise = 8.f; // O is rescaled when a maximum has risen by more than this (log2)
+
+template <int D, int NT>
+struct Cfg {
+    static constexpr int kTile = kKeys * D * 2;                            // bytes of a K, V or Q tile
+    static constexpr int ST = NT == 2 ? (D == 128 ? 5 : 8) : (D == 128 ? 2 : 5);
+    static constexpr int kRing = NT * kTile;                               // after the Q tiles
+    static constexpr int kBar = kRing + ST * kTile;
+    static constexpr int kSmem = kBar + 256 + 1024;
+    static constexpr int kThreads = NT * 128 + 64;
+    static constexpr int kTmem = NT == 2 ? 512 : 256;
+    static constexpr uint32_t kO = NT * 128;                               // TMEM: S of each row tile, then O of each
+    static_assert(kSmem <= 232448 / (NT == 1 ? 2 : 1) - (NT == 1 ? 1024 : 0), "shared memory");
+};
+
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ uint32_t pack2(float a, float b) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* tm, int x, int y, int z, int w, uint64_t* bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], "
+        "[%6];" ::"r"(smem_addr(dst)),
+        "l"(reinterpret_cast<uint64_t>(tm)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(smem_addr(bar))
+        : "memory");
+}
+// bounded wait of one thread; gives up when another role has given up
+__device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity, volatile int* abort_flag, uint64_t limit) {
+    if (mbar_try_wait(bar, parity)) return true;
+    const uint64_t t0 = global_ns();
+    for (;;) {
+        if (mbar_try_wait_suspend(bar, parity, 2000)) return true;
+        if (*abort_flag) return false;
+        if (global_ns() - t0 > limit) {
+            *abort_flag = 1;
+            return false;
+        }
+    }
+}
+__device__ __forceinline__ bool warp_wait_bar(uint64_t* bar, uint32_t parity, volatile int* abort_flag, uint64_t limit) {
+    return __all_sync(0xffffffffu, wait_bar(bar, parity, abort_flag, limit));
+}
+// 32 bytes of one row (32-byte aligned)
+__device__ __forceinline__ void st_row8(void* p, uint32_t a, uint32_t b, uint32_t c, uint32_t d, uint32_t e, uint32_t f,
+                                        uint32_t g, uint32_t h) {
+    asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(a), "r"(b), "r"(c), "r"(d), "r"(e),
+                 "r"(f), "r"(g), "r"(h)
+                 : "memory");
+}
+
+template <int D, int NT>
+__global__ void __launch_bounds__(Cfg<D, NT>::kThreads, NT == 1 ? 2 : 1)
+    prefix_tc_kernel(const __grid_constant__ Params p, const int pre_items, const bool joined, const bool direct) {
+    using F = Cfg<D, NT>;
+    extern __shared__ unsigned char smem_raw[];
+    unsigned char* smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
+    const uint32_t sbase = smem_addr(smem);
+    uint64_t* full = reinterpret_cast<uint64_t*>(smem + F::kBar);   // [ST] a K or V tile landed
+    uint64_t* empty = full + F::ST;                                  // [ST] every product that reads it is done
+    uint64_t* s_full = empty + F::ST;                                // [NT] S (and every earlier product) done
+    uint64_t* p_ready = s_full + NT;                                 // [NT] P written, O rescaled, V's end zeroed
+    uint64_t* q_ready = p_ready + NT;                                // Q tiles written
+    uint64_t* o_full = q_ready + 1;                                  // every product done
+    uint32_t* tslot = reinterpret_cast<uint32_t*>(o_full + 1);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(tslot + 1);
+    int* issued = reinterpret_cast<int*>(tslot + 2);                 // tiles whose copy was issued
+    static_assert((2 * F::ST + 2 * NT + 2) * 8 + 12 <= 256, "barrier area");
+
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int nG = p.n * p.G;
+    // ---- the item: rows [row0, ..) of `rows`, prefix tokens [lo1, hi1), tail tokens [lo2, hi2) of request b0 ----
+    int item = blockIdx.x;
+    const bool stacked = item < pre_items;   // rows of all requests (prefix only), else one request's
+    int h, b0 = 0, part, len = 0, lo1 = 0, hi1 = 0, lo2 = 0, hi2 = 0;
+    int64_t rows, row0;
+    if (stacked) {
+        h = item % p.Hkv, item /= p.Hkv;
+        rows = (int64_t)p.B * nG;
+        row0 = (int64_t)(item % p.pre_tiles) * (NT * kRows);
+        part = item / p.pre_tiles;
+        lo1 = part * p.pre_chunk;
+        hi1 = (int)min((int64_t)lo1 + p.pre_chunk, p.prefix_len);
+    } else {
+        item -= pre_items;
+        h = item % p.Hkv, item /= p.Hkv;
+        rows = nG;
+        row0 = (int64_t)(item % p.tail_tiles) * (NT * kRows), item /= p.tail_tiles;
+        b0 = item % p.B;
+        part = item / p.B;
+        len = p.max_tail > 0 ? min(max(p.tail_len[b0], 0), (int)p.max_tail) : 0;
+        if (joined) {
+            hi1 = (int)p.prefix_len;
+            // what the tile's last row sees
+            const int last = (int)(min(row0 + NT * kRows, rows) - 1) / p.G;
+            hi2 = min(len, max(0, len - p.n + last + 1));
+        } else {
+            tail_range(len, p.tail_splits, kKeys, part, &lo2, &hi2);
+        }
+        part += p.pre_splits;
+    }
+    const int n1 = (hi1 - lo1 + kKeys - 1) / kKeys;
+    const int n_tiles = n1 + (hi2 - lo2 + kKeys - 1) / kKeys;
+    const uint64_t limit = p.wait_limit_ns;
+
+    if (warp == 0) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(tslot)),
+                     "r"(F::kTmem));
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+    }
+    if (tid == 0) {
+        for (int i = 0; i < F::ST; ++i) mbar_init(&full[i], 1), mbar_init(&empty[i], 1);
+        for (int i = 0; i < NT; ++i) mbar_init(&s_full[i], 1), mbar_init(&p_ready[i], 128);
+        mbar_init(q_ready, NT * 128);
+        mbar_init(o_full, 1);
+        *abort_flag = 0;
+        *issued = 0;
+        fence_barrier_init();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tbase = *tslot;
+
+    if (warp == NT * 4) {
+        // ---- products ----
+        if (lane == 0 && n_tiles > 0) {
+            bool ok = wait_bar(q_ready, 0, abort_flag, limit);
+            auto slot_at = [&](int seq) { return sbase + F::kRing + (uint32_t)(seq % F::ST) * F::kTile; };
+            auto scores = [&](int a, int j) {
+                const uint32_t q = sbase + a * F::kTile, k = slot_at(2 * j);
+#pragma unroll
+                for (int kk = 0; kk < D / 16; ++kk) {
+                    const uint32_t off = (uint32_t)((kk >> 2) * 16384 + (kk & 3) * 32);   // 64-column blocks of 128 rows
+                    umma_ss(tbase + a * 128, sdesc(q + off, 16, 1024), sdesc(k + off, 16, 1024), idesc(kKeys, false, false),
+                            kk > 0);
+                }
+                umma_commit(&s_full[a]);
+            };
+            auto values = [&](int a, int j) {
+                const uint32_t v = slot_at(2 * j + 1);
+#pragma unroll
+                for (int kt = 0; kt < kKeys / 16; ++kt)
+                    umma_ts(tbase + F::kO + a * D, tbase + a * 128 + 8 * kt, sdesc(v + kt * 2048, 16384, 1024),
+                            idesc(D, false, true), j > 0 || kt > 0);
+            };
+            if (ok) ok = wait_bar(&full[0], 0, abort_flag, limit);
+            if (ok) {
+                for (int a = 0; a < NT; ++a) scores(a, 0);
+                umma_commit(&empty[0]);
+            }
+            for (int j = 0; ok && j < n_tiles; ++j) {
+                const int vs = 2 * j + 1, ks = 2 * j + 2;
+                ok = wait_bar(&full[vs % F::ST], (uint32_t)((vs / F::ST) & 1), abort_flag, limit);
+                for (int a = 0; ok && a < NT; ++a) {
+                    ok = wait_bar(&p_ready[a], (uint32_t)(j & 1), abort_flag, limit);
+                    if (!ok) break;
+                    tc_fence_after();
+                    values(a, j);
+                    if (a == NT - 1) umma_commit(&empty[vs % F::ST]);
+                    if (j + 1 < n_tiles) {
+                        if (a == 0) ok = wait_bar(&full[ks % F::ST], (uint32_t)((ks / F::ST) & 1), abort_flag, limit);
+                        if (!ok) break;
+                        scores(a, j + 1);
+                        if (a == NT - 1) umma_commit(&empty[ks % F::ST]);
+                    }
+                }
+            }
+            umma_commit(o_full);   // also after giving up: the end waits for the products in flight
+        }
+    } else if (warp == NT * 4 + 1) {
+        // ---- copies: K_0, V_0, K_1, V_1, ... ----
+        if (lane == 0) {
+            for (int seq = 0; seq < 2 * n_tiles; ++seq) {
+                const int s = seq % F::ST, j = seq >> 1;
+                if (p.stall_after >= 0 && j >= p.stall_after) break;   // testing hook
+                if (seq >= F::ST && !wait_bar(&empty[s], (uint32_t)((seq / F::ST - 1) & 1), abort_flag, limit)) break;
+                unsigned char* dst = smem + F::kRing + s * F::kTile;
+                mbar_arrive_expect_tx(&full[s], F::kTile);
+                const bool v = seq & 1;
+#pragma unroll
+                for (int c = 0; c < D / 64; ++c) {
+                    if (j < n1)
+                        tma_load_3d(dst + c * 16384, v ? &p.tm_vp : &p.tm_kp, c * 64, h, lo1 + j * kKeys, &full[s]);
+                    else
+                        tma_load_4d(dst + c * 16384, v ? &p.tm_vt : &p.tm_kt, c * 64, h, lo2 + (j - n1) * kKeys, b0, &full[s]);
+                }
+                *issued = seq + 1;
+            }
+        }
+    } else {
+        // ---- softmax of row tile a; this thread's row ----
+        const int a = warp >> 2, r = tid & 127;
+        const int64_t R = row0 + a * kRows + r;
+        const bool valid = R < rows;
+        const int b = stacked ? (int)(R / nG) : b0, e = (int)(R % nG), qi = e / p.G, head = h * p.G + e % p.G;
+        const int vis2 = min(hi2, max(0, len - p.n + qi + 1));   // tail tokens that this row sees end here
+        const int64_t at = ((int64_t)b * p.n + qi) * p.Hq + head;
+        const uint32_t trow = tbase + ((uint32_t)(32 * (warp & 3)) << 16);
+        const bool busy = __any_sync(0xffffffffu, valid);   // a warp without rows only keeps the barriers going
+        // Q; negated where the scale is negative, so that a maximum of scores is one of products
+        {
+            const bool neg = p.scale_log2 < 0.f;
+            const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(p.q) + (valid ? b * p.q_sb + qi * p.q_sn + head * p.q_sh : 0);
+            unsigned char* dst = smem + a * F::kTile;
+#pragma unroll
+            for (int c = 0; c < D / 8; ++c) {
+                uint4 x = valid ? *reinterpret_cast<const uint4*>(src + 8 * c) : make_uint4(0, 0, 0, 0);
+                if (neg) x.x ^= 0x80008000u, x.y ^= 0x80008000u, x.z ^= 0x80008000u, x.w ^= 0x80008000u;
+                *reinterpret_cast<uint4*>(dst + (c >> 3) * 16384 + sw128(r, (c & 7) * 8)) = x;
+            }
+            proxy_fence();
+            mbar_arrive(q_ready);
+        }
+        // (a scale of 0 as the smallest normal number: every weight is 1, and a hidden token's -infinity stays that)
+        const float scale = fmaxf(fabsf(p.scale_log2), 1.17549435e-38f);
+        float m = -INFINITY, l = 0.f;
+        bool ok = true;
+        for (int j = 0; j < n_tiles; ++j) {
+            const int t0 = j < n1 ? lo1 + j * kKeys : lo2 + (j - n1) * kKeys;
+            if (!warp_wait_bar(&s_full[a], (uint32_t)(j & 1), abort_flag, limit)) {
+                ok = false;
+                break;
+            }
+            tc_fence_after();
+            if (busy) {
+                // The scores are read twice, for the maximum and for the weights: 64 at a time leave room in the 168
+                // registers that 10 warps (or two CTAs of 6) may use; all 128 held at once spilled 300 bytes.
+                const int seen = valid ? (j < n1 ? hi1 : vis2) - t0 : kKeys;
+                const bool hide = __any_sync(0xffffffffu, seen < kKeys);
+                auto load = [&](int half, float (&x0)[32], float (&x1)[32]) {
+                    tmem_ld32x2(trow + a * 128 + 64 * half, trow + a * 128 + 64 * half + 32, x0, x1);
+                    if (hide) {
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) {
+                            if (64 * half + i >= seen) x0[i] = -INFINITY;
+                            if (64 * half + 32 + i >= seen) x1[i] = -INFINITY;
+                        }
+                    }
+                };
+                float t[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {
+                    float x0[32], x1[32];
+                    load(half, x0, x1);
+#pragma unroll
+                    for (int i = 0; i < 32; i += 2) {
+                        t[0] = fmaxf(t[0], x0[i]), t[1] = fmaxf(t[1], x0[i + 1]);
+                        t[2] = fmaxf(t[2], x1[i]), t[3] = fmaxf(t[3], x1[i + 1]);
+                    }
+                }
+                float top = fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3]));
+                top *= scale;
+                const bool rise = top > m + kRise || m == -INFINITY;
+                if (__any_sync(0xffffffffu, rise)) {
+                    const float mn = rise ? fmaxf(m, top) : m;
+                    const float f = mn == -INFINITY ? 1.f : ex2(m - mn);
+                    m = mn;
+                    l *= f;
+                    if (j > 0) {   // every earlier product into O is done: s_full came after them
+#pragma unroll
+                        for (int c = 0; c < D / 32; ++c) {
+                            float o[32];
+                            tmem_ld32(trow + F::kO + a * D + 32 * c, o);
+#pragma unroll
+                            for (int i = 0; i < 32; ++i) o[i] *= f;
+                            tmem_st32(trow + F::kO + a * D + 32 * c, o);
+                        }
+                    }
+                }
+                const float base = m == -INFINITY ? 0.f : m;
+                float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {
+                    float x0[32], x1[32];
+                    load(half, x0, x1);
+                    uint32_t w0[16], w1[16];
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        const float e0 = ex2(fmaf(x0[2 * i], scale, -base)), e1 = ex2(fmaf(x0[2 * i + 1], scale, -base));
+                        const float e2 = ex2(fmaf(x1[2 * i], scale, -base)), e3 = ex2(fmaf(x1[2 * i + 1], scale, -base));
+                        sum[0] += e0, sum[1] += e1, sum[2] += e2, sum[3] += e3;
+                        w0[i] = pack2(e0, e1), w1[i] = pack2(e2, e3);
+                    }
+                    tmem_st16(trow + a * 128 + 32 * half, w0);
+                    tmem_st16(trow + a * 128 + 32 * half + 16, w1);
+                }
+                l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+                tmem_st_wait();
+            }
+            if (a == 0 && j >= n1 && t0 + kKeys > hi2) {
+                // the tail's last tile: zero the value rows past the range
+                const int vs = 2 * j + 1;
+                if (!warp_wait_bar(&full[vs % F::ST], (uint32_t)((vs / F::ST) & 1), abort_flag, limit)) {
+                    ok = false;
+                    break;
+                }
+                if (r >= hi2 - t0) {
+                    unsigned char* v = smem + F::kRing + (vs % F::ST) * F::kTile + r * 128;
+#pragma unroll
+                    for (int c = 0; c < D / 64; ++c)
+#pragma unroll
+                        for (int i = 0; i < 8; ++i)
+                            *reinterpret_cast<uint4*>(v + c * 16384 + 16 * i) = make_uint4(0, 0, 0, 0);
+                }
+                proxy_fence();
+            }
+            tc_fence_before();
+            mbar_arrive(&p_ready[a]);
+        }
+        if (n_tiles > 0 && ok) ok = warp_wait_bar(o_full, 0, abort_flag, limit);
+        ok = ok && *abort_flag == 0;
+        ok = __all_sync(0xffffffffu, ok);
+        if (ok && busy) {
+            tc_fence_after();
+            const bool some = l != 0.f;
+            const float inv = some ? 1.f / l : 0.f;
+            if (valid && !direct) p.part_ml[part * ((int64_t)p.B * p.n * p.Hq) + at] = make_float2(m, l);
+            if (valid && direct && p.lse) p.lse[at] = some ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
+            if (n_tiles > 0 || direct) {
+#pragma unroll
+                for (int c = 0; c < D / 32; ++c) {
+                    float o[32];
+                    if (n_tiles > 0) {
+                        tmem_ld32(trow + F::kO + a * D + 32 * c, o);
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) o[i] = 0.f;
+                    }
+                    if (valid && direct) {
+                        uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.o) + at * D + 32 * c);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            uint32_t w[4];
+#pragma unroll
+                            for (int k = 0; k < 4; ++k)
+                                w[k] = some ? pack2(o[8 * i + 2 * k] * inv, o[8 * i + 2 * k + 1] * inv) : 0u;
+                            dst[i] = make_uint4(w[0], w[1], w[2], w[3]);
+                        }
+                    } else if (valid) {
+                        float* dst = p.part_o + (part * ((int64_t)p.B * p.n * p.Hq) + at) * D + 32 * c;
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            st_row8(dst + 8 * i, __float_as_uint(o[8 * i]), __float_as_uint(o[8 * i + 1]),
+                                    __float_as_uint(o[8 * i + 2]), __float_as_uint(o[8 * i + 3]),
+                                    __float_as_uint(o[8 * i + 4]), __float_as_uint(o[8 * i + 5]),
+                                    __float_as_uint(o[8 * i + 6]), __float_as_uint(o[8 * i + 7]));
+                    }
+                }
+            }
+        }
+    }
+
+    // ---- leave only with no copy and no product still writing into this CTA's shared memory or TMEM ----
+    tc_fence_before();
+    __syncthreads();
+    if (tid == 0 && *abort_flag) {
+        const uint64_t drain = limit > kDrainLimitNs ? limit : kDrainLimitNs;
+        for (int seq = max(0, *issued - F::ST); seq < *issued; ++seq)
+            tc::drain_phase(&full[seq % F::ST], (uint32_t)((seq / F::ST) & 1), drain);
+        tc::drain_phase(o_full, 0, drain);
+        atomicOr(p.status, STATUS_TIMEOUT);
+    }
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 0)
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tbase), "r"(F::kTmem));
+}
+
+template <int D, int NT>
+cudaError_t launch(const Params& p, int64_t pre_items, int64_t tail_items, bool joined, bool direct, cudaStream_t s) {
+    using F = Cfg<D, NT>;
+    if (pre_items + tail_items == 0) return cudaSuccess;
+    auto kern = prefix_tc_kernel<D, NT>;
+    static std::atomic<int> optin[kMaxOptinDevices];
+    const cudaError_t e = smem_optin(reinterpret_cast<const void*>(kern), F::kSmem, optin);
+    if (e != cudaSuccess) return e;
+    kern<<<(unsigned)(pre_items + tail_items), F::kThreads, F::kSmem, s>>>(p, (int)pre_items, joined, direct);
+    return cudaGetLastError();
+}
+template <int D>
+cudaError_t launch_d(const Params& p, int row_tiles, int64_t pre_items, int64_t tail_items, bool joined, bool direct,
+                     cudaStream_t s) {
+    return row_tiles == 2 ? launch<D, 2>(p, pre_items, tail_items, joined, direct, s)
+                          : launch<D, 1>(p, pre_items, tail_items, joined, direct, s);
+}
+
+}  // namespace
+
+cudaError_t launch_tc(const Params& p, int D, int row_tiles, int64_t pre_items, int64_t tail_items, bool joined,
+                      bool direct, cudaStream_t s) {
+    return D == 64 ? launch_d<64>(p, row_tiles, pre_items, tail_items, joined, direct, s)
+                   : launch_d<128>(p, row_tiles, pre_items, tail_items, joined, direct, s);
+}
+
+}  // namespace prefix
+}  // namespace gdn

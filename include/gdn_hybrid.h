@@ -124,7 +124,7 @@ gdn_status gdn_linear_step(const gdn_linear_problem* p, const void* q, const voi
  *  tail_len     device int32 [B]; may be NULL when max_tail = 0
  *  o            device [B, n, Hq, D], dtype, packed
  *  lse          device [B, n, Hq] fp32, or NULL
- *  scratch      device, 16-byte aligned, gdn_prefix_scratch_bytes(p) bytes (partial sums)
+ *  scratch      device, 32-byte aligned, gdn_prefix_scratch_bytes(p) bytes (partial sums)
  *
  * Nothing is read from the device on the host, so the call can be captured into a graph.
  */

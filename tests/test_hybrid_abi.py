@@ -146,7 +146,7 @@ def test_prefix_problem_refusals(L, prob, want):
 @pytest.mark.parametrize("call", [
     dict(q=None), dict(kp=None), dict(vp=None), dict(kt=None), dict(vt=None), dict(tail=None), dict(o=None), dict(ws=None),
     dict(nws=255), dict(scratch=None), dict(nscratch=0), dict(q=8), dict(kp=2), dict(vp=4), dict(kt=8), dict(vt=8),
-    dict(tail=2), dict(o=8), dict(lse=2), dict(scratch=8), dict(ws=8),
+    dict(tail=2), dict(o=8), dict(lse=2), dict(scratch=8), dict(scratch=16), dict(ws=8),
 ])
 def test_prefix_attention_refusals(L, call):
     assert _attend(L, _pre(), **call) == INV
