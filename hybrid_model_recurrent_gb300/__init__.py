@@ -647,38 +647,36 @@ def _on(stream, dev):
     return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
 
 
-def _dense(x: torch.Tensor, name: str, shape, dtype, dev) -> None:
-    _expect(tuple(x.shape) == tuple(shape) and x.dtype == dtype and x.device == dev and x.is_contiguous(),
-            f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {dev}")
+def _dense(x: torch.Tensor, name: str, shape: tuple, dtype, dev) -> None:
+    if x.shape != shape or x.dtype != dtype or x.device != dev or not x.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {shape} on {dev}")
 
 
 def _row_stride(x: torch.Tensor, name: str) -> int:
     """Elements between the rows of [rows, heads, width] with heads and widths contiguous inside a row."""
-    _, h, d = x.shape
-    _expect((d == 1 or x.stride(2) == 1) and (h == 1 or x.stride(1) == d),
-            f"{name}: heads and widths must be contiguous inside a token's row")
-    if x.shape[0] <= 1:
+    if x.is_contiguous():
         return 0
-    _expect(x.stride(0) >= h * d, f"{name}: rows overlap")
-    return x.stride(0)
+    n, h, d = x.shape
+    st, sh, sd = x.stride()
+    if (d > 1 and sd != 1) or (h > 1 and sh != d):
+        raise ValueError(f"{name}: heads and widths must be contiguous inside a token's row")
+    if n <= 1:
+        return 0
+    if st < h * d:
+        raise ValueError(f"{name}: rows overlap")
+    return st
 
 
 def _linear_problem(q, k, v, alpha, num_seqs: int, cu, scale: float, out_dtype):
-    _expect(k.dim() == 3 and v.dim() == 3 and (q is None or q.shape == k.shape), "q, k [T, Hk, d_k] and v [T, H, d_v]")
-    _expect(k.shape[0] == v.shape[0] and (q is None or q.dtype == k.dtype) and v.dtype == k.dtype,
-            "q, k and v differ in their tokens or dtype")
-    dev = k.device
-    _expect(v.device == dev and alpha.device == dev and (q is None or q.device == dev), "tensors on different devices")
-    H = v.shape[1]
-    _expect(alpha.dtype == torch.float32 and tuple(alpha.shape) == (H,) and alpha.is_contiguous(),
-            "alpha must be contiguous fp32 [H]")
-    pr = _LinearProblem()
-    pr.num_seqs, pr.num_heads, pr.num_qk_heads, pr.d_k, pr.d_v = num_seqs, H, k.shape[1], k.shape[2], v.shape[2]
-    pr.cu_seqlens = _p64(cu)
-    pr.qkv_dtype, pr.out_dtype, pr.scale = _dtype_code(k.dtype), _dtype_code(out_dtype or k.dtype), float(scale)
-    pr.q_stride = 0 if q is None else _row_stride(q, "q")
-    pr.k_stride, pr.v_stride = _row_stride(k, "k"), _row_stride(v, "v")
-    return pr
+    dev, dt, ks, vs = k.device, k.dtype, k.shape, v.shape
+    if len(ks) != 3 or len(vs) != 3 or ks[0] != vs[0] or v.dtype != dt or v.device != dev or (
+            q is not None and (q.shape != ks or q.dtype != dt or q.device != dev)):
+        raise ValueError("q, k [T, Hk, d_k] and v [T, H, d_v] must agree in their tokens, dtype and device")
+    _dense(alpha, "alpha", (vs[1],), torch.float32, dev)
+    code = _dtype_code(dt)
+    return _LinearProblem(num_seqs, vs[1], ks[1], ks[2], vs[2], _p64(cu), code,
+                          code if out_dtype is dt else _dtype_code(out_dtype), scale,
+                          0 if q is None else _row_stride(q, "q"), _row_stride(k, "k"), _row_stride(v, "v"))
 
 
 def gdn_linear_prefill(q, k, v, alpha, cu_seqlens, *, scale: float = 1.0, S0=None, S0_index=None, ckpt_pos=None,
@@ -742,33 +740,41 @@ def gdn_linear_step(q, k, v, alpha, states, *, slots=None, scale: float = 1.0, o
     q, k [B, Hk, dk], v [B, H, dv]; states [num_slots, H, dv, dk] fp32; slots int32 [B] on the GPU (default: request b's
     slot is b), distinct but for negative ones, which mark padding rows (output 0).  Returns o [B, H, dv]."""
     dev = k.device
-    B = k.shape[0]
     out_dtype = out_dtype or k.dtype
-    pr = _linear_problem(q, k, v, alpha, B, None, scale, out_dtype)
-    H, dv, dk = v.shape[1], v.shape[2], k.shape[2]
-    _expect(states.dim() == 4, "states must be [num_slots, H, d_v, d_k]")
-    _dense(states, "states", (states.shape[0], H, dv, dk), torch.float32, dev)
+    pr = _linear_problem(q, k, v, alpha, k.shape[0], None, scale, out_dtype)
+    B, H, dv = v.shape
+    n = states.shape[0]
+    _dense(states, "states", (n, H, dv, k.shape[2]), torch.float32, dev)
     if slots is not None:
         _dense(slots, "slots", (B,), torch.int32, dev)
-    if o is None:
-        with _on(stream, dev):
-            o = torch.empty((B, H, dv), dtype=out_dtype, device=dev)
-    else:
+    if o is not None:
         _dense(o, "o", (B, H, dv), out_dtype, dev)
-    rc = lib().gdn_linear_step(ctypes.byref(pr), _ptr(q), _ptr(k), _ptr(v), _ptr(alpha), _ptr(states), states.shape[0],
-                               _ptr(slots), _ptr(o), _stream(stream, dev))
-    _check(rc, "gdn_linear_step")
+    elif stream is None:
+        o = torch.empty((B, H, dv), dtype=out_dtype, device=dev)
+    else:
+        with torch.cuda.stream(stream):
+            o = torch.empty((B, H, dv), dtype=out_dtype, device=dev)
+    rc = lib().gdn_linear_step(ctypes.byref(pr), q.data_ptr(), k.data_ptr(), v.data_ptr(), alpha.data_ptr(),
+                               states.data_ptr(), n, None if slots is None else slots.data_ptr(), o.data_ptr(),
+                               (stream or torch.cuda.current_stream(dev)).cuda_stream)
+    if rc != GDN_OK:
+        raise GdnError(rc, "gdn_linear_step")
     return o
 
 
 def _strides(x: torch.Tensor, name: str):
-    """Strides of all dimensions but the last (contiguous) one; 0 stands for one that is never used."""
-    _expect(x.shape[-1] == 1 or x.stride(-1) == 1, f"{name}: the last dimension must be contiguous")
-    out = []
-    for n, s in zip(x.shape[:-1], x.stride()[:-1]):
-        _expect(n <= 1 or s > 0, f"{name}: broadcast dimensions are not supported")
-        out.append(0 if n <= 1 else s)
-    return out
+    """Strides of all dimensions but the last (contiguous) one; 0: packed, or never used."""
+    if x.is_contiguous():
+        return (0,) * (x.dim() - 1)
+    shape, st = x.shape, x.stride()
+    if shape[-1] > 1 and st[-1] != 1:
+        raise ValueError(f"{name}: the last dimension must be contiguous")
+    if any(n > 1 and s <= 0 for n, s in zip(shape[:-1], st)):
+        raise ValueError(f"{name}: broadcast dimensions are not supported")
+    if any(n == 0 for n in shape):
+        return (0,) * (x.dim() - 1)
+    # the stride of a dimension of one element is never used; any positive multiple of the others' alignment will do
+    return tuple(s if n > 1 else shape[-1] for n, s in zip(shape[:-1], st))
 
 
 def gdn_prefix_attention(q, k_prefix, v_prefix, k_tail=None, v_tail=None, tail_len=None, *,
@@ -780,35 +786,30 @@ def gdn_prefix_attention(q, k_prefix, v_prefix, k_tail=None, v_tail=None, tail_l
     with tail_len int32 [B] on the GPU (query i sees the tail's tokens 0 .. tail_len - n + i), or None.  Any strides whose
     last dimension is contiguous and whose others are multiples of 16 bytes.  max_tail bounds tail_len (default: cap).
     scale defaults to D ** -0.5.  Returns dict(o [B, n, Hq, D], lse [B, n, Hq] fp32)."""
-    _expect(q.dim() == 4 and k_prefix.dim() == 3 and v_prefix.shape == k_prefix.shape, "q [B, n, Hq, D], prefix [P, Hkv, D]")
+    _expect(q.dim() == 4 and k_prefix.dim() == 3, "q must be [B, n, Hq, D] and the prefix [P, Hkv, D]")
     B, n, Hq, D = q.shape
-    P, Hkv = k_prefix.shape[:2]
-    dev = q.device
-    given = [k_prefix, v_prefix]
+    P, Hkv, Dk = k_prefix.shape
+    dev, dt = q.device, q.dtype
+    if Dk != D or v_prefix.shape != k_prefix.shape:
+        raise ValueError("k_prefix and v_prefix must be [P, Hkv, D], of q's width")
+    if k_prefix.dtype != dt or v_prefix.dtype != dt or k_prefix.device != dev or v_prefix.device != dev:
+        raise ValueError("q, keys and values differ in dtype or device")
     cap = 0
+    kts = vts = (0, 0, 0)
     if k_tail is not None:
-        _expect(v_tail is not None and tail_len is not None, "a tail needs k_tail, v_tail and tail_len")
-        _expect(k_tail.dim() == 4 and v_tail.shape == k_tail.shape and k_tail.shape[0] == B and k_tail.shape[2] == Hkv and
-                k_tail.shape[3] == D, "k_tail, v_tail [B, cap, Hkv, D]")
-        _dense(tail_len, "tail_len", (B,), torch.int32, dev)
-        given += [k_tail, v_tail]
+        _expect(v_tail is not None and tail_len is not None and k_tail.dim() == 4, "a tail needs k_tail, v_tail and tail_len")
         cap = k_tail.shape[1]
+        if k_tail.shape != (B, cap, Hkv, D) or v_tail.shape != k_tail.shape:
+            raise ValueError("k_tail and v_tail must be [B, cap, Hkv, D]")
+        if k_tail.dtype != dt or v_tail.dtype != dt or k_tail.device != dev or v_tail.device != dev:
+            raise ValueError("q, keys and values differ in dtype or device")
+        _dense(tail_len, "tail_len", (B,), torch.int32, dev)
+        kts, vts = _strides(k_tail, "k_tail"), _strides(v_tail, "v_tail")
     else:
         _expect(v_tail is None and tail_len is None, "a tail needs k_tail, v_tail and tail_len")
-    _expect(k_prefix.shape[2] == D, "q and the prefix differ in their width")
-    for x in given:
-        _expect(x.dtype == q.dtype and x.device == dev, "q, keys and values differ in dtype or device")
-    pr = _PrefixProblem()
-    pr.batch, pr.num_queries, pr.num_q_heads, pr.num_kv_heads, pr.head_dim = B, n, Hq, Hkv, D
-    pr.dtype = _dtype_code(q.dtype)
-    pr.prefix_len, pr.tail_cap, pr.max_tail = P, cap, cap if max_tail is None else int(max_tail)
-    pr.softmax_scale = float(D ** -0.5 if scale is None else scale)
-    pr.q_stride_b, pr.q_stride_n, pr.q_stride_h = _strides(q, "q")
-    pr.kp_stride_t, pr.kp_stride_h = _strides(k_prefix, "k_prefix")
-    pr.vp_stride_t, pr.vp_stride_h = _strides(v_prefix, "v_prefix")
-    if cap:
-        pr.kt_stride_b, pr.kt_stride_t, pr.kt_stride_h = _strides(k_tail, "k_tail")
-        pr.vt_stride_b, pr.vt_stride_t, pr.vt_stride_h = _strides(v_tail, "v_tail")
+    pr = _PrefixProblem(B, n, Hq, Hkv, D, _dtype_code(dt), P, cap, cap if max_tail is None else max_tail,
+                        D ** -0.5 if scale is None else scale, *_strides(q, "q"), *_strides(k_prefix, "k_prefix"),
+                        *_strides(v_prefix, "v_prefix"), *kts, *vts)
     with _on(stream, dev):
         if o is None:
             o = torch.empty((B, n, Hq, D), dtype=q.dtype, device=dev)
@@ -819,10 +820,10 @@ def gdn_prefix_attention(q, k_prefix, v_prefix, k_tail=None, v_tail=None, tail_l
     _dense(o, "o", (B, n, Hq, D), q.dtype, dev)
     _dense(lse, "lse", (B, n, Hq), torch.float32, dev)
     ws = ws if ws is not None else workspace(dev)
-    has_tail = cap > 0
     rc = lib().gdn_prefix_attention(
-        ctypes.byref(pr), _ptr(q), _ptr(k_prefix if P else None), _ptr(v_prefix if P else None),
-        _ptr(k_tail if has_tail else None), _ptr(v_tail if has_tail else None), _ptr(tail_len if has_tail else None),
-        _ptr(o), _ptr(lse), _ptr(scratch), nbytes, _ptr(ws), ws.numel(), _stream(stream, dev))
+        ctypes.byref(pr), q.data_ptr(), k_prefix.data_ptr() if P else None, v_prefix.data_ptr() if P else None,
+        k_tail.data_ptr() if cap else None, v_tail.data_ptr() if cap else None, tail_len.data_ptr() if cap else None,
+        o.data_ptr(), lse.data_ptr(), _ptr(scratch), nbytes, ws.data_ptr(), ws.numel(),
+        (stream or torch.cuda.current_stream(dev)).cuda_stream)
     _check(rc, "gdn_prefix_attention")
     return {"o": o, "lse": lse}

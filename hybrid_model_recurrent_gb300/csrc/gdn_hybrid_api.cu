@@ -77,7 +77,8 @@ gdn_status check_lengths(const gdn_linear_problem* p) {
 
 // How a prefill's scans are cut.  seg_len 0: one job a sequence.
 struct LinPlan {
-    int rows_per_cta;
+    bool tc;            // the tensor-core kernel
+    int rows_per_cta;   // state rows of a CTA
     int64_t seg_len;
     int64_t slots;   // states of all segments but the last of each sequence
 };
@@ -88,9 +89,11 @@ LinPlan plan_linear(const gdn_linear_problem* p) {
     const int64_t T = p->cu_seqlens[B];
     int64_t longest = 0;
     for (int b = 0; b < B; ++b) longest = std::max(longest, p->cu_seqlens[b + 1] - p->cu_seqlens[b]);
-    // CTAs of 64 state rows when that still gives two a multiprocessor, else smaller ones
-    pl.rows_per_cta = std::min(64, p->d_v);
-    while (pl.rows_per_cta > 16 && (int64_t)B * p->num_heads * (p->d_v / pl.rows_per_cta) < 2 * kSms) pl.rows_per_cta /= 2;
+    // The tensor-core kernel rounds the readout's operands to bf16, which a bf16 output hides and an fp32 one does not.
+    pl.tc = p->d_k == 128 && p->d_v == 128 && p->qkv_dtype == GDN_BF16 && p->out_dtype == GDN_BF16;
+    // FP32 pipes: CTAs of 64 state rows when that still gives two a multiprocessor, else smaller ones
+    pl.rows_per_cta = pl.tc ? 128 : std::min(64, p->d_v);
+    while (!pl.tc && pl.rows_per_cta > 16 && (int64_t)B * p->num_heads * (p->d_v / pl.rows_per_cta) < 2 * kSms) pl.rows_per_cta /= 2;
     const int64_t per_seq = (int64_t)p->num_heads * (p->d_v / pl.rows_per_cta);
     // A scan is sequential, so a call with few long ones leaves multiprocessors idle.  Its scans are then cut into
     // segments: each segment's own state from zero (keys and values read once more), the chain of the states, and all
@@ -111,6 +114,24 @@ struct LinHostJob {
     gdn::lin::Job job;
     std::vector<gdn::lin::Ckpt> ckpts;
 };
+
+using EncodeFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
+                              const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                              CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+// bf16 tensor map over `rank` dimensions (the innermost of them contiguous), boxes of 64 columns x 1 head x `tokens`
+// (x 1 request), 128-byte swizzle; strides of the outer dimensions in elements
+bool bf16_map(CUtensorMap* m, const void* base, int rank, const int64_t (&dim)[4], const int64_t (&stride)[3], int tokens) {
+    const auto enc = reinterpret_cast<EncodeFn>(gdn::encode_tiled_fn());
+    if (!enc) return false;
+    cuuint64_t dims[4], strides[3];
+    for (int i = 0; i < 4; ++i) dims[i] = (cuuint64_t)std::max<int64_t>(dim[i], 1);
+    for (int i = 0; i < 3; ++i) strides[i] = (cuuint64_t)(stride[i] * 2);
+    const cuuint32_t box[4] = {64, 1, (cuuint32_t)tokens, 1}, one[4] = {1, 1, 1, 1};
+    return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, (cuuint32_t)rank, const_cast<void*>(base), dims, strides, box, one,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
 
 // Batch jobs into parameter blocks, longest first.
 template <class F>
@@ -228,7 +249,16 @@ gdn_status linear_prefill(const gdn_linear_problem* p, const void* q, const void
     prm->dv = p->d_v;
     prm->rows_per_cta = pl.rows_per_cta;
     const bool in_bf16 = p->qkv_dtype == GDN_BF16, out_bf16 = p->out_dtype == GDN_BF16;
-    auto launch = [&](const gdn::lin::Params& pr) { return gdn::lin::launch_simt(pr, p->d_k, in_bf16, out_bf16, stream); };
+    if (pl.tc && T > 0) {
+        const int Hk = p->num_qk_heads;
+        bool maps = bf16_map(&prm->tm_k, k, 3, {128, Hk, T, 1}, {128, sd.k, 0}, 128) &&
+                    bf16_map(&prm->tm_v, v, 3, {128, H, T, 1}, {128, sd.v, 0}, 128);
+        if (maps && o) maps = bf16_map(&prm->tm_q, q, 3, {128, Hk, T, 1}, {128, sd.q, 0}, 128);
+        if (!maps) return GDN_ERR_CUDA;
+    }
+    auto launch = [&](const gdn::lin::Params& pr) {
+        return pl.tc ? gdn::lin::launch_tc(pr, stream) : gdn::lin::launch_simt(pr, p->d_k, in_bf16, out_bf16, stream);
+    };
     if (!own.empty()) {
         prm->o = nullptr;
         if ((st = launch_jobs(*prm, own, launch)) != GDN_OK) return st;
@@ -351,23 +381,6 @@ PrefixPlan plan_prefix(const gdn_prefix_problem& f) {
     return pl;
 }
 
-// [tokens, heads, D] or [requests, tokens, heads, D] as a tensor map of boxes of 128 tokens x 64 columns
-bool prefix_map(CUtensorMap* m, const void* base, const gdn_prefix_problem& f, int64_t tokens, int64_t st, int64_t sh,
-                int64_t sb) {
-    auto enc = reinterpret_cast<CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
-                                             const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
-                                             CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill)>(
-        gdn::encode_tiled_fn());
-    if (!enc) return false;
-    const cuuint64_t dims[4] = {(cuuint64_t)f.head_dim, (cuuint64_t)f.num_kv_heads, (cuuint64_t)tokens,
-                                (cuuint64_t)f.batch};
-    const cuuint64_t strides[3] = {(cuuint64_t)(sh * 2), (cuuint64_t)(st * 2), (cuuint64_t)(sb * 2)};
-    const cuuint32_t box[4] = {64, 1, (cuuint32_t)gdn::prefix::kTcKeys, 1}, one[4] = {1, 1, 1, 1};
-    return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, sb ? 4 : 3, const_cast<void*>(base), dims, strides, box, one,
-               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
 gdn_status prefix_attention(const gdn_prefix_problem* p, const void* q, const void* k_prefix, const void* v_prefix,
                             const void* k_tail, const void* v_tail, const int32_t* tail_len, void* o, float* lse,
                             void* scratch, size_t scratch_bytes, void* workspace, size_t ws_bytes, cudaStream_t stream) {
@@ -412,12 +425,16 @@ gdn_status prefix_attention(const gdn_prefix_problem* p, const void* q, const vo
     const int64_t tail_items = items - pre_items;
     if (pl.tc) {
         bool maps = true;
+        const int64_t D = f.head_dim, Hkv = f.num_kv_heads, pre_dim[4] = {D, Hkv, f.prefix_len, 1},
+                      tail_dim[4] = {D, Hkv, f.tail_cap, f.batch};
         if (f.prefix_len > 0)
-            maps = prefix_map(&prm->tm_kp, k_prefix, f, f.prefix_len, f.kp_stride_t, f.kp_stride_h, 0) &&
-                   prefix_map(&prm->tm_vp, v_prefix, f, f.prefix_len, f.vp_stride_t, f.vp_stride_h, 0);
+            maps = bf16_map(&prm->tm_kp, k_prefix, 3, pre_dim, {f.kp_stride_h, f.kp_stride_t, 0}, gdn::prefix::kTcKeys) &&
+                   bf16_map(&prm->tm_vp, v_prefix, 3, pre_dim, {f.vp_stride_h, f.vp_stride_t, 0}, gdn::prefix::kTcKeys);
         if (maps && f.max_tail > 0)
-            maps = prefix_map(&prm->tm_kt, k_tail, f, f.tail_cap, f.kt_stride_t, f.kt_stride_h, f.kt_stride_b) &&
-                   prefix_map(&prm->tm_vt, v_tail, f, f.tail_cap, f.vt_stride_t, f.vt_stride_h, f.vt_stride_b);
+            maps = bf16_map(&prm->tm_kt, k_tail, 4, tail_dim, {f.kt_stride_h, f.kt_stride_t, f.kt_stride_b},
+                            gdn::prefix::kTcKeys) &&
+                   bf16_map(&prm->tm_vt, v_tail, 4, tail_dim, {f.vt_stride_h, f.vt_stride_t, f.vt_stride_b},
+                            gdn::prefix::kTcKeys);
         if (!maps) return GDN_ERR_CUDA;
         const bool direct = pl.parts() == 1;
         cudaError_t e;

@@ -217,15 +217,23 @@ __global__ void __launch_bounds__(128) linear_scan_kernel(const __grid_constant_
 
 // Initial states of a split scan's segments: start_{j+1} = alpha^L start_j + own_j, in place (slot j holds own_j and
 // receives start_{j+1}).  One thread takes four elements of one head's state through all segments; bound by the
-// traffic of the states.  alpha^L is formed in fp64: its exponent would lose up to 2^-24 |L log2 alpha| in fp32.
+// traffic of the states.  alpha^L is formed by binary powers in fp64 (once a block, which lies within one
+// head) and rounded once.
 __global__ void __launch_bounds__(128) chain_kernel(const __grid_constant__ ChainParams p) {
     const int per_head = p.state / 4;
-    const int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
-    if (i >= (int64_t)p.n_scans * p.H * per_head) return;
+    const int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;   // per_head is a multiple of the block
     const int e = (int)(i % per_head) * 4;
     const int h = (int)(i / per_head % p.H);
     const Chain& sc = p.scans[i / per_head / p.H];
-    const float w = (float)pow((double)p.alpha[h], (double)p.seg_len);
+    __shared__ float w_sh;
+    if (threadIdx.x == 0) {
+        double y = 1.0, sq = (double)p.alpha[h];
+        for (int k = p.seg_len; k; k >>= 1, sq *= sq)
+            if (k & 1) y *= sq;
+        w_sh = (float)y;
+    }
+    __syncthreads();
+    const float w = w_sh;
     const size_t all = (size_t)p.H * p.state, off = (size_t)h * p.state + e;
     float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
     if (sc.s0) x = *reinterpret_cast<const float4*>(sc.s0 + off);
