@@ -253,7 +253,9 @@ gdn_status linear_prefill(const gdn_linear_problem* p, const void* q, const void
         const int Hk = p->num_qk_heads;
         bool maps = bf16_map(&prm->tm_k, k, 3, {128, Hk, T, 1}, {128, sd.k, 0}, 128) &&
                     bf16_map(&prm->tm_v, v, 3, {128, H, T, 1}, {128, sd.v, 0}, 128);
-        if (maps && o) maps = bf16_map(&prm->tm_q, q, 3, {128, Hk, T, 1}, {128, sd.q, 0}, 128);
+        if (maps && o)
+            maps = bf16_map(&prm->tm_q, q, 3, {128, Hk, T, 1}, {128, sd.q, 0}, 128) &&
+                   bf16_map(&prm->tm_o, o, 3, {128, H, T, 1}, {128, (int64_t)H * 128, 0}, 128);
         if (!maps) return GDN_ERR_CUDA;
     }
     auto launch = [&](const gdn::lin::Params& pr) {

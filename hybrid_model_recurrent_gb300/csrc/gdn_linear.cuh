@@ -31,7 +31,7 @@ struct Ckpt {
 };
 
 struct Params {
-    CUtensorMap tm_q, tm_k, tm_v;   // tensor-core kernel only: [T, heads, d], box (64, 1, 128), 128-byte swizzle
+    CUtensorMap tm_q, tm_k, tm_v, tm_o;   // tensor-core kernel only: [T, heads, d], box (64, 1, 128), 128-byte swizzle
     const void* q;                  // [T] rows of `q_stride` elements
     const void* k;
     const void* v;

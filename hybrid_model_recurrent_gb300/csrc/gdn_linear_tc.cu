@@ -60,8 +60,8 @@ constexpr int ST = 5;                       // tiles of the ring
 constexpr int kThreads = 14 * 32;
 constexpr int OFF_KLO = ST * kTile;         // K' lo
 constexpr int OFF_S = OFF_KLO + kTile;      // bf16 S
-constexpr int OFF_POW = OFF_S + kTile;      // a^0 .. a^128
-constexpr int OFF_BAR = OFF_POW + 544;
+constexpr int OFF_POW = OFF_S + kTile;      // a^0 .. a^128, then a^128 .. a^0
+constexpr int OFF_BAR = OFF_POW + 2 * 528;
 constexpr int kSmem = OFF_BAR + 256 + 1024;
 static_assert(kSmem <= 232448, "227 KB of shared memory per block");
 constexpr uint32_t T_S = 0, T_G = 128, T_O1 = 256, T_O2 = 384;
@@ -78,6 +78,12 @@ __device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity, volatil
             return false;
         }
     }
+}
+__device__ __forceinline__ void tma_store_3d(const void* src, const CUtensorMap* tm, int x, int y, int z) {
+    asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(
+                     reinterpret_cast<uint64_t>(tm)),
+                 "r"(x), "r"(y), "r"(z), "r"(smem_addr(src))
+                 : "memory");
 }
 __device__ __forceinline__ uint32_t pack2(float a, float b) {
     const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
@@ -110,7 +116,8 @@ __global__ void __launch_bounds__(kThreads, 1) linear_tc_kernel(const __grid_con
     extern __shared__ unsigned char smem_raw[];
     unsigned char* smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
     const uint32_t sbase = smem_addr(smem);
-    float* pw = reinterpret_cast<float*>(smem + OFF_POW);
+    float* pw = reinterpret_cast<float*>(smem + OFF_POW);   // pw[i] = a^i
+    float* wp = pw + 132;                                   // wp[i] = a^(128 - i)
     uint64_t* full = reinterpret_cast<uint64_t*>(smem + OFF_BAR);   // [ST] a tile landed
     uint64_t* empty = full + ST;        // [ST] every product that reads it is done
     uint64_t* g_done = empty + ST;      // G
@@ -120,11 +127,12 @@ __global__ void __launch_bounds__(kThreads, 1) linear_tc_kernel(const __grid_con
     uint64_t* p_ready = s_ready + 1;    // tokens: P written
     uint64_t* k_ready = p_ready + 1;    // keys: K' written, value rows zeroed
     uint64_t* o_free = k_ready + 1;     // tokens: O1 and O2 read
-    uint64_t* end = o_free + 1;         // every product done
+    uint64_t* o_staged = o_free + 1;    // tokens: the chunk's output in the spent Q tile
+    uint64_t* end = o_staged + 1;       // every product done
     uint32_t* tslot = reinterpret_cast<uint32_t*>(end + 1);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tslot + 1);
     int* issued = reinterpret_cast<int*>(tslot + 2);
-    static_assert((2 * ST + 8) * 8 + 12 <= 256, "barrier area");
+    static_assert((2 * ST + 9) * 8 + 12 <= 256, "barrier area");
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int h = blockIdx.x % p.H;
@@ -139,7 +147,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_tc_kernel(const __grid_con
     }
     if (tid == 0) {
         for (int i = 0; i < 2 * ST + 3; ++i) mbar_init(&full[i], 1);
-        for (uint64_t* b : {s_ready, p_ready, k_ready, o_free}) mbar_init(b, 128);
+        for (uint64_t* b : {s_ready, p_ready, k_ready, o_free, o_staged}) mbar_init(b, 128);
         mbar_init(end, 1);
         *abort_flag = 0;
         *issued = 0;
@@ -150,7 +158,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_tc_kernel(const __grid_con
         double x = 1.0, sq = (double)p.alpha[h];
         for (int i = tid - 128; i; i >>= 1, sq *= sq)
             if (i & 1) x *= sq;
-        pw[tid - 128] = (float)x;
+        pw[tid - 128] = wp[kTok - (tid - 128)] = (float)x;
     }
     tc_fence_before();
     __syncthreads();
@@ -169,7 +177,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_tc_kernel(const __grid_con
         // ---- state ----
         const size_t state_off = ((size_t)h * D + row) * D;
         auto dump = [&](float* dst) {   // this thread's row, from TMEM
-#pragma unroll
+#pragma unroll 1
             for (int c = 0; c < 4; ++c) {
                 float v[32];
                 tmem_ld32(trow + T_S + 32 * c, v);
@@ -178,6 +186,21 @@ __global__ void __launch_bounds__(kThreads, 1) linear_tc_kernel(const __grid_con
                     *reinterpret_cast<float4*>(dst + 32 * c + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
             }
         };
+        if (w.more()) {
+            // the initial state into TMEM, so that the first chunk is like the others
+#pragma unroll 1
+            for (int c = 0; c < 4; ++c) {
+                float v[32];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const float4 x = job.s0 ? reinterpret_cast<const float4*>(job.s0 + state_off + 32 * c)[i]
+                                            : make_float4(0.f, 0.f, 0.f, 0.f);
+                    v[4 * i] = x.x, v[4 * i + 1] = x.y, v[4 * i + 2] = x.z, v[4 * i + 3] = x.w;
+                }
+                tmem_st32(trow + T_S + 32 * c, v);
+            }
+            tmem_st_wait();
+        }
         bool ok = true;
         int j = 0, slot = -1;   // slot: where the last chunk's state is dumped
         for (; w.more(); w.next(), ++j) {
@@ -187,36 +210,30 @@ __global__ void __launch_bounds__(kThreads, 1) linear_tc_kernel(const __grid_con
                 tc_fence_after();
                 if (slot >= 0) dump(p.ckpt_states + (size_t)slot * p.H * D * D + state_off);
             }
-            const float decay = pw[w.n];
+            const float2 decay = make_float2(pw[w.n], pw[w.n]);
+#pragma unroll 1
+            for (int c = 0; c < 2; ++c) {
+                float v[2][32];
+                tmem_ld32x2(trow + T_S + 64 * c, trow + T_S + 64 * c + 32, v[0], v[1]);
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                float v[32];
-                if (j > 0) {
-                    tmem_ld32(trow + T_S + 32 * c, v);
-                } else if (job.s0) {
-                    const float4* src = reinterpret_cast<const float4*>(job.s0 + state_off + 32 * c);
+                for (int k = 0; k < 2; ++k) {
+                    if (READOUT) {
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const float4 x = src[i];
-                        v[4 * i] = x.x, v[4 * i + 1] = x.y, v[4 * i + 2] = x.z, v[4 * i + 3] = x.w;
+                        for (int i = 0; i < 32; i += 8)
+                            *reinterpret_cast<uint4*>(smem + OFF_S + c * 16384 + sw128(row, k * 32 + i)) =
+                                make_uint4(pack2(v[k][i], v[k][i + 1]), pack2(v[k][i + 2], v[k][i + 3]),
+                                           pack2(v[k][i + 4], v[k][i + 5]), pack2(v[k][i + 6], v[k][i + 7]));
                     }
-                } else {
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) v[i] = 0.f;
+                    for (int i = 0; i < 32; i += 2) {
+                        const float2 x = __fmul2_rn(make_float2(v[k][i], v[k][i + 1]), decay);
+                        v[k][i] = x.x, v[k][i + 1] = x.y;
+                    }
+                    tmem_st32(trow + T_S + 64 * c + 32 * k, v[k]);
                 }
-                if (READOUT) {
-#pragma unroll
-                    for (int i = 0; i < 32; i += 8)
-                        *reinterpret_cast<uint4*>(smem + OFF_S + (c >> 1) * 16384 + sw128(row, (c & 1) * 32 + i)) =
-                            make_uint4(pack2(v[i], v[i + 1]), pack2(v[i + 2], v[i + 3]), pack2(v[i + 4], v[i + 5]),
-                                       pack2(v[i + 6], v[i + 7]));
-                }
-#pragma unroll
-                for (int i = 0; i < 32; ++i) v[i] *= decay;
-                tmem_st32(trow + T_S + 32 * c, v);
             }
             tmem_st_wait();
-            proxy_fence();
+            if (READOUT) proxy_fence();
             tc_fence_before();
             mbar_arrive(s_ready);
             slot = w.dump() ? p.ckpts[w.ck].slot : -1;
@@ -239,10 +256,20 @@ __global__ void __launch_bounds__(kThreads, 1) linear_tc_kernel(const __grid_con
         if (READOUT) {
             const int rb = warp & 3;
             const float rowf = pw[lane], inter = pw[row + 1] * p.scale;
+            const float2 inter2 = make_float2(inter, inter), scale2 = make_float2(p.scale, p.scale);
+            int held = -1;   // ring slot of the last chunk's Q tile, until its output has been copied out of it
+            auto release = [&] {
+                if (held >= 0) {
+                    asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+                    mbar_arrive(&empty[held]);
+                    held = -1;
+                }
+                __syncwarp();
+            };
             for (int j = 0; w.more(); w.next(), ++j) {
                 if (!warp_wait(g_done, j)) break;
                 tc_fence_after();
-#pragma unroll
+#pragma unroll 1
                 for (int cb = 0; cb < 4; ++cb) {
                     uint32_t pk[16];
                     if (cb <= rb) {
@@ -250,15 +277,22 @@ __global__ void __launch_bounds__(kThreads, 1) linear_tc_kernel(const __grid_con
                         tmem_ld32(trow + T_G + 32 * cb, g);
                         if (cb < rb) {
                             // a^{t-s} = a^{lane} a^{32 (rb - cb) - i}: both exponents are at least 0
-                            const float* col = pw + 32 * (rb - cb);
+                            const float4* col = reinterpret_cast<const float4*>(wp + kTok - 32 * (rb - cb));
+                            const float2 rf = make_float2(rowf, rowf);
 #pragma unroll
-                            for (int i = 0; i < 32; ++i) g[i] *= rowf * col[-i];
+                            for (int i = 0; i < 8; ++i) {
+                                const float4 x = col[i];
+                                const float2 y0 = __fmul2_rn(__fmul2_rn(make_float2(x.x, x.y), rf), make_float2(g[4 * i], g[4 * i + 1]));
+                                const float2 y1 = __fmul2_rn(__fmul2_rn(make_float2(x.z, x.w), rf), make_float2(g[4 * i + 2], g[4 * i + 3]));
+                                pk[2 * i] = pack2(y0.x, y0.y), pk[2 * i + 1] = pack2(y1.x, y1.y);
+                            }
                         } else {
+                            const float* d = wp + kTok - lane;   // d[i] = a^{lane - i}, not read past the diagonal
 #pragma unroll
-                            for (int i = 0; i < 32; ++i) g[i] = i <= lane ? g[i] * pw[max(lane - i, 0)] : 0.f;
+                            for (int i = 0; i < 32; ++i) g[i] = i <= lane ? g[i] * d[i] : 0.f;
+#pragma unroll
+                            for (int i = 0; i < 16; ++i) pk[i] = pack2(g[2 * i], g[2 * i + 1]);
                         }
-#pragma unroll
-                        for (int i = 0; i < 16; ++i) pk[i] = pack2(g[2 * i], g[2 * i + 1]);
                     } else {
 #pragma unroll
                         for (int i = 0; i < 16; ++i) pk[i] = 0u;
@@ -268,28 +302,54 @@ __global__ void __launch_bounds__(kThreads, 1) linear_tc_kernel(const __grid_con
                 tmem_st_wait();
                 tc_fence_before();
                 mbar_arrive(p_ready);
+                release();
                 if (!warp_wait(o_done, j)) break;
                 tc_fence_after();
+                const int qs = PER * j + 1;
+                const bool whole = w.n == kTok;
                 __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.o) + ((job.tok_begin + w.pos + row) * p.H + h) * (int64_t)D;
-#pragma unroll
+                // A whole chunk is staged in its spent Q tile and copied out by TMA: a thread holds a row, and 16-byte
+                // stores of 32 rows at a time took 3100 of the 8300 cycles of a chunk.  A cut one is stored directly.
+#pragma unroll 1
                 for (int c = 0; c < 4; ++c) {
                     float x[32], y[32];
                     tmem_ld32x2(trow + T_O1 + 32 * c, trow + T_O2 + 32 * c, x, y);
-                    if (row < w.n) {
+                    unsigned char* piece = smem + tile(qs) + (c >> 1) * 16384;
 #pragma unroll
-                        for (int i = 0; i < 32; i += 8) {
-                            uint32_t u[4];
+                    for (int i = 0; i < 32; i += 8) {
+                        uint32_t u[4];
 #pragma unroll
-                            for (int e = 0; e < 4; ++e)
-                                u[e] = pack2(fmaf(inter, x[i + 2 * e], p.scale * y[i + 2 * e]),
-                                             fmaf(inter, x[i + 2 * e + 1], p.scale * y[i + 2 * e + 1]));
-                            *reinterpret_cast<uint4*>(dst + 32 * c + i) = make_uint4(u[0], u[1], u[2], u[3]);
+                        for (int e = 0; e < 4; ++e) {
+                            const int k = i + 2 * e;
+                            const float2 z = __ffma2_rn(inter2, make_float2(x[k], x[k + 1]),
+                                                        __fmul2_rn(scale2, make_float2(y[k], y[k + 1])));
+                            u[e] = pack2(z.x, z.y);
                         }
+                        const uint4 q4 = make_uint4(u[0], u[1], u[2], u[3]);
+                        if (whole)
+                            *reinterpret_cast<uint4*>(piece + sw128(row, (c & 1) * 32 + i)) = q4;
+                        else if (row < w.n)
+                            *reinterpret_cast<uint4*>(dst + 32 * c + i) = q4;
                     }
                 }
+                proxy_fence();
                 tc_fence_before();
                 mbar_arrive(o_free);
+                mbar_arrive(o_staged);
+                bool staged = true;
+                if (tid == 128) {
+                    staged = wait_bar(o_staged, (uint32_t)j & 1u, abort_flag, limit);
+                    if (staged && whole) {
+                        const int t0 = (int)(job.tok_begin + w.pos);
+                        tma_store_3d(smem + tile(qs), &p.tm_o, 0, h, t0);
+                        tma_store_3d(smem + tile(qs) + 16384, &p.tm_o, 64, h, t0);
+                        asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+                    }
+                    held = qs % ST;
+                }
+                if (!__all_sync(0xffffffffu, staged)) break;
             }
+            release();
         }
     } else if (warp < 12) {
         // ---- keys: row = token s ----
@@ -303,18 +363,28 @@ __global__ void __launch_bounds__(kThreads, 1) linear_tc_kernel(const __grid_con
             const float f = in ? pw[w.n - 1 - row] : 0.f;
             unsigned char* hi = smem + tile(ks);
             unsigned char* lo = smem + OFF_KLO;
+            const float2 f2 = make_float2(f, f);
+#pragma unroll 1
+            for (int c0 = 0; c0 < 4; ++c0) {
+                // all loads of a quarter row before its stores: the compiler may not move a load over a store
+                uint4 x[4];
+                const uint32_t off = (c0 >> 1) * 16384 + row * 128;
 #pragma unroll
-            for (int c = 0; c < 16; ++c) {
-                const uint32_t off = (c >> 3) * 16384 + sw128(row, (c & 7) * 8);
-                const uint4 x = *reinterpret_cast<const uint4*>(hi + off);
-                uint32_t a[4] = {x.x, x.y, x.z, x.w}, b[4];
+                for (int c = 0; c < 4; ++c)   // past the chunk: another chunk's or sequence's keys, not taken in
+                    x[c] = in ? *reinterpret_cast<const uint4*>(hi + off + (((4 * (c0 & 1) + c) ^ (row & 7)) << 4))
+                              : make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const float2 k2 = bf16x2_to_float2(a[i]);
-                    split_pair(in ? k2.x * f : 0.f, in ? k2.y * f : 0.f, a[i], b[i]);
+                for (int c = 0; c < 4; ++c) {
+                    uint32_t a[4] = {x[c].x, x[c].y, x[c].z, x[c].w}, b[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const float2 y = __fmul2_rn(bf16x2_to_float2(a[i]), f2);
+                        split_pair(y.x, y.y, a[i], b[i]);
+                    }
+                    const uint32_t at = off + (((4 * (c0 & 1) + c) ^ (row & 7)) << 4);
+                    *reinterpret_cast<uint4*>(hi + at) = make_uint4(a[0], a[1], a[2], a[3]);
+                    *reinterpret_cast<uint4*>(lo + at) = make_uint4(b[0], b[1], b[2], b[3]);
                 }
-                *reinterpret_cast<uint4*>(hi + off) = make_uint4(a[0], a[1], a[2], a[3]);
-                *reinterpret_cast<uint4*>(lo + off) = make_uint4(b[0], b[1], b[2], b[3]);
             }
             if (w.n < kTok) {
                 if (!warp_wait(&full[vs % ST], full_parity(vs))) break;
@@ -354,9 +424,18 @@ __global__ void __launch_bounds__(kThreads, 1) linear_tc_kernel(const __grid_con
                         const uint32_t off = (uint32_t)((kk >> 2) * 16384 + (kk & 3) * 32);
                         umma_ss(tbase + T_O1, sdesc(q + off, 16, 1024), sdesc(sbase + OFF_S + off, 16, 1024), id, kk > 0);
                     }
-                    umma_commit(&empty[qs % ST]);
                 }
-                if (!wait(k_ready, j) || !wait(&full[vs % ST], full_parity(vs))) break;
+                if (!wait(&full[vs % ST], full_parity(vs))) break;
+                if (READOUT) {
+                    if (!wait(p_ready, j)) break;
+                    if (w.n < kTok && !wait(k_ready, j)) break;   // a cut chunk's value rows are zeroed by then
+                    tc_fence_after();
+#pragma unroll
+                    for (int kt = 0; kt < 8; ++kt)
+                        umma_ts(tbase + T_O2, tbase + T_G + 8 * kt, sdesc(v + kt * 2048, 16384, 1024), id_b, kt > 0);
+                    umma_commit(o_done);
+                }
+                if (!wait(k_ready, j)) break;
                 tc_fence_after();
 #pragma unroll
                 for (int kt = 0; kt < 8; ++kt) {
@@ -366,14 +445,6 @@ __global__ void __launch_bounds__(kThreads, 1) linear_tc_kernel(const __grid_con
                 }
                 umma_commit(st_done);
                 umma_commit(&empty[ks % ST]);
-                if (READOUT) {
-                    if (!wait(p_ready, j)) break;
-                    tc_fence_after();
-#pragma unroll
-                    for (int kt = 0; kt < 8; ++kt)
-                        umma_ts(tbase + T_O2, tbase + T_G + 8 * kt, sdesc(v + kt * 2048, 16384, 1024), id_b, kt > 0);
-                    umma_commit(o_done);
-                }
                 umma_commit(&empty[vs % ST]);
             }
             umma_commit(end);   // also after giving up: the end waits for the products in flight
