@@ -15,7 +15,7 @@ SOURCES = ["gdn_api.cu", "gdn_noalloc.cu", "gdn_placement.cpp", "gdn_group.cu", 
            "gdn_linear.cu", "gdn_linear_tc.cu", "gdn_prefix.cu",
            "gdn_prefix_tc.cu"]
 HEADERS = [os.path.join(CSRC, f) for f in ("gdn_kernel.cuh", "gdn_chunk.cuh", "gdn_chunk_tc.cuh", "gdn_group.cuh",
-                                           "gdn_linear.cuh", "gdn_prefix.cuh")] + [
+                                           "gdn_linear.cuh", "gdn_prefix.cuh", "gdn_tc_util.cuh")] + [
     os.path.join(ROOT, "include", f) for f in ("gdn_scan.h", "gdn_hybrid.h")]
 NVCC_FLAGS = ["-gencode", "arch=compute_103a,code=sm_103a", "-O3", "-lineinfo", "-std=c++17",
               "-Xcompiler", "-fPIC,-fvisibility=hidden", "-I", os.path.join(ROOT, "include")]

@@ -10,28 +10,36 @@
 //
 // Every power of a is at most 1, so no decay in [0, 1] leaves the range of fp32.  A chunk ends after 128 tokens, at a
 // checkpoint and at the end of its job.  Products, all M = 128 with fp32 sums in TMEM:
-//     G = Q K^T;  O1 = Q S^T;  O2 = P V, P = G masked and decayed;  S += V^T K' with K' = diag(a^{n-1-s}) K
-// K' is not exact in bf16: it is split into hi + lo halves and both are multiplied, so a state loses 2^-16 of an added
+//     G = Q K^T;  O = Q S^T, its rows scaled by a^{t+1} in place, O += P V with P = G masked and decayed;
+//     S += V'^T K with V' = diag(a^{n-1-s}) V
+// V' is not exact in bf16: it is split into hi + lo halves and both are multiplied, so a state loses 2^-16 of an added
 // term, as the delta rule scan's does.  P and the copy of S that the readout multiplies are rounded to bf16 once (half a
 // step, 2^-8 of each term): the readout itself is rounded to bf16, and its error stays of that order.
 //
-// One CTA takes one (job, head) from its first chunk to its last.  Roles:
-//   state  (warps 0-3):  S out of TMEM into its bf16 copy, S scaled by a^n in place; checkpoints, initial, final state
-//   tokens (warps 4-7):  G -> P in TMEM; the readout a^{t+1} O1 + O2 to memory
-//   keys   (warps 8-11): K -> K' hi (in place) and lo; value rows past a cut chunk zeroed
-//   one thread that issues the products, one that issues the copies (TMA, a ring of 5 tiles in the order K, Q, V)
-// They hand over through mbarriers, one phase a chunk.  The state's own chain (S and K' converted, O1 and the update
-// multiplied) is the critical path; G, P and O2 of a chunk run beside it.
+// What bounds it: shared memory's 128 bytes a cycle, of which a product with both operands there takes nearly all.  So
+// P and V'^T are operands in TMEM: with K' = diag(.) K split in shared memory instead (written, and read again beside V),
+// a chunk moved 590 KB through shared memory, now 430 KB, and the room of K' gives every input tile a second buffer.
 //
-// A sequence's tiles may reach past its end into its neighbour's tokens: P and K' are replaced by zeros there and the
-// value rows are zeroed, so a neighbour's values, infinities and NaN included, never reach a result.
+// One CTA takes one (job, head) from its first chunk to its last.  Roles:
+//   state  (warps 0-3):  S out of TMEM into its bf16 copy, S scaled by a^n in place; V^T -> V' hi and lo in TMEM;
+//                        checkpoints, initial, final state; key and value rows past a cut chunk zeroed
+//   tokens (warps 4-7):  the first half of G's columns -> P in TMEM; a^{t+1} into O
+//   output (warps 8-11): the second half of them; O to memory, staged for TMA
+//   one thread each that issues the products, the copies of K and V, of Q and of staged output
+// They hand over through mbarriers, one phase a chunk, and no barrier completes a phase before everyone who waits for
+// the last one has seen it (a parity tells only two phases apart).  The state's own chain (S and V' converted, Q S^T and
+// the update multiplied) is the critical path; G, P and P V of a chunk run beside it.  Each role's chunk is written as
+// short rolled loops: unrolled, the roles' code streamed through the instruction cache once a chunk, 1.5 times as slow.
+//
+// A sequence's tiles may reach past its end into its neighbour's tokens: P and V' are replaced by zeros there and the
+// key and value rows are zeroed, so a neighbour's values, infinities and NaN included, never reach a result.
 //
 // Every wait is bounded: a role that gives up sets the abort flag, every role leaves, copies and products in flight
 // are waited for, TMEM is freed and the sticky status is set.
 #include <cuda_bf16.h>
 
-#include "gdn_chunk_tc.cuh"
 #include "gdn_linear.cuh"
+#include "gdn_tc_util.cuh"
 
 namespace gdn {
 namespace lin {
@@ -39,7 +47,6 @@ namespace {
 
 using tc::idesc;
 using tc::proxy_fence;
-using tc::sdesc;
 using tc::split_pair;
 using tc::sw128;
 using tc::tc_fence_after;
@@ -52,42 +59,47 @@ using tc::tmem_st_wait;
 using tc::umma_commit;
 using tc::umma_ss;
 using tc::umma_ts;
+using tcu::cols_step;
+using tcu::elect_one;
+using tcu::pack2;
+using tcu::rows_step;
+using tcu::store32;
+using tcu::tile_desc;
+using tcu::wait_bar;
 
 constexpr int D = 128;
 constexpr int kTok = 128;                   // tokens of a chunk
 constexpr int kTile = kTok * D * 2;         // bytes of a K, Q, V, K' or S tile: two 64-column blocks of [128][128 B]
-constexpr int ST = 5;                       // tiles of the ring
-constexpr int kThreads = 14 * 32;
-constexpr int OFF_KLO = ST * kTile;         // K' lo
-constexpr int OFF_S = OFF_KLO + kTile;      // bf16 S
-constexpr int OFF_POW = OFF_S + kTile;      // a^0 .. a^128, then a^128 .. a^0
-constexpr int OFF_BAR = OFF_POW + 2 * 528;
+constexpr int kThreads = 16 * 32;
+constexpr int OFF_O = 5 * kTile;            // after the input tiles (with a readout): staged output
+constexpr int OFF_S = 6 * kTile;            // the bf16 copy of S
+constexpr int OFF_POW = 7 * kTile;          // a^0 .. a^128; a^128 .. a^0; a^127 .. a^0
+constexpr int OFF_BAR = OFF_POW + 3 * 528;
 constexpr int kSmem = OFF_BAR + 256 + 1024;
 static_assert(kSmem <= 232448, "227 KB of shared memory per block");
-constexpr uint32_t T_S = 0, T_G = 128, T_O1 = 256, T_O2 = 384;
+// P, a block of 32 tokens (16 columns) at a time, goes over columns of G that only the writing role reads: blocks 0 and 1
+// over G's first 32 columns (tokens), 2 and 3 over the third (output)
+__host__ __device__ constexpr uint32_t p_block(int cb) { return 128u + 16u * cb + (cb >= 2 ? 32u : 0u); }
+constexpr uint32_t T_S = 0, T_G = 128, T_O = 256, T_VH = 384, T_VL = 448;
 
-// bounded wait of one thread; gives up when another role has given up
-__device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity, volatile int* abort_flag, uint64_t limit) {
-    if (mbar_try_wait(bar, parity)) return true;
-    const uint64_t t0 = global_ns();
-    for (;;) {
-        if (mbar_try_wait_suspend(bar, parity, 2000)) return true;
-        if (*abort_flag) return false;
-        if (global_ns() - t0 > limit) {
-            *abort_flag = 1;
-            return false;
-        }
-    }
-}
 __device__ __forceinline__ void tma_store_3d(const void* src, const CUtensorMap* tm, int x, int y, int z) {
     asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(
                      reinterpret_cast<uint64_t>(tm)),
                  "r"(x), "r"(y), "r"(z), "r"(smem_addr(src))
                  : "memory");
 }
-__device__ __forceinline__ uint32_t pack2(float a, float b) {
-    const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
-    return *reinterpret_cast<const uint32_t*>(&h);
+
+// four 8 x 8 matrices of 16-bit elements, transposed: register m of lane l holds rows 2 (l % 4), + 1 of column l / 4
+__device__ __forceinline__ void ldsm_x4_trans(uint32_t addr, uint32_t (&r)[4]) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+// 16 TMEM lanes x 16 columns: register 2 g + k of lane l goes to TMEM lane 8 k + l / 4, column 4 g + l % 4
+__device__ __forceinline__ void tmem_st_16x128b_x4(uint32_t taddr, const uint32_t (&r)[8]) {
+    asm volatile("tcgen05.st.sync.aligned.16x128b.x4.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(r[0]), "r"(r[1]),
+                 "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]));
 }
 
 // the chunks of a job, walked alike by every role
@@ -112,27 +124,31 @@ struct Walk {
 
 template <bool READOUT>
 __global__ void __launch_bounds__(kThreads, 1) linear_tc_kernel(const __grid_constant__ Params p) {
-    constexpr int PER = READOUT ? 3 : 2;   // tiles a chunk: K, Q, V or K, V
+    constexpr int NB = READOUT ? 2 : 3;               // buffers of K and of V (Q is spent early in its chunk: one)
+    constexpr int NT = READOUT ? 2 * NB + 1 : 2 * NB; // input tiles
     extern __shared__ unsigned char smem_raw[];
     unsigned char* smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
     const uint32_t sbase = smem_addr(smem);
     float* pw = reinterpret_cast<float*>(smem + OFF_POW);   // pw[i] = a^i
     float* wp = pw + 132;                                   // wp[i] = a^(128 - i)
-    uint64_t* full = reinterpret_cast<uint64_t*>(smem + OFF_BAR);   // [ST] a tile landed
-    uint64_t* empty = full + ST;        // [ST] every product that reads it is done
-    uint64_t* g_done = empty + ST;      // G
-    uint64_t* st_done = g_done + 1;     // the state's update (and O1 before it)
-    uint64_t* o_done = st_done + 1;     // O1 and O2
+    float* vp = wp + 132;                                   // vp[i] = a^(127 - i): both orders of 16-byte pieces
+    uint64_t* full = reinterpret_cast<uint64_t*>(smem + OFF_BAR);   // [NT] an input tile landed
+    uint64_t* empty = full + NT;        // [NT] everything that reads it is done
+    uint64_t* g_done = empty + NT;      // G
+    uint64_t* q_done = g_done + 1;      // Q S^T
+    uint64_t* st_done = q_done + 1;     // the state's update (and Q S^T before it)
+    uint64_t* o_done = st_done + 1;     // O
     uint64_t* s_ready = o_done + 1;     // state: the bf16 copy written, S scaled
-    uint64_t* p_ready = s_ready + 1;    // tokens: P written
-    uint64_t* k_ready = p_ready + 1;    // keys: K' written, value rows zeroed
-    uint64_t* o_free = k_ready + 1;     // tokens: O1 and O2 read
-    uint64_t* o_staged = o_free + 1;    // tokens: the chunk's output in the spent Q tile
-    uint64_t* end = o_staged + 1;       // every product done
+    uint64_t* p_ready = s_ready + 1;    // tokens, output: P written, O scaled
+    uint64_t* v_ready = p_ready + 1;    // state: V' written, key and value rows zeroed
+    uint64_t* o_free = v_ready + 1;     // output: O read
+    uint64_t* o_staged = o_free + 1;    // output: a chunk's output staged
+    uint64_t* o_left = o_staged + 1;    // the staged output has been copied out
+    uint64_t* end = o_left + 1;         // every product done
     uint32_t* tslot = reinterpret_cast<uint32_t*>(end + 1);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tslot + 1);
-    int* issued = reinterpret_cast<int*>(tslot + 2);
-    static_assert((2 * ST + 9) * 8 + 12 <= 256, "barrier area");
+    int* issued = reinterpret_cast<int*>(tslot + 2);   // [3] chunks whose K, V, Q copy was issued
+    static_assert((2 * NT + 11) * 8 + 20 <= 256, "barrier area");
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int h = blockIdx.x % p.H;
@@ -146,11 +162,13 @@ __global__ void __launch_bounds__(kThreads, 1) linear_tc_kernel(const __grid_con
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
     }
     if (tid == 0) {
-        for (int i = 0; i < 2 * ST + 3; ++i) mbar_init(&full[i], 1);
-        for (uint64_t* b : {s_ready, p_ready, k_ready, o_free, o_staged}) mbar_init(b, 128);
+        for (int i = 0; i < 2 * NT + 4; ++i) mbar_init(&full[i], 1);
+        mbar_init(o_left, 1);
+        for (uint64_t* b : {s_ready, v_ready, o_free, o_staged}) mbar_init(b, 128);
+        mbar_init(p_ready, 256);
         mbar_init(end, 1);
         *abort_flag = 0;
-        *issued = 0;
+        issued[0] = issued[1] = issued[2] = 0;
         fence_barrier_init();
     }
     if (tid >= 128 && tid - 128 <= kTok) {
@@ -158,7 +176,9 @@ __global__ void __launch_bounds__(kThreads, 1) linear_tc_kernel(const __grid_con
         double x = 1.0, sq = (double)p.alpha[h];
         for (int i = tid - 128; i; i >>= 1, sq *= sq)
             if (i & 1) x *= sq;
-        pw[tid - 128] = wp[kTok - (tid - 128)] = (float)x;
+        const int i = tid - 128;
+        pw[i] = wp[kTok - i] = (float)x;
+        if (i < kTok) vp[kTok - 1 - i] = (float)x;
     }
     tc_fence_before();
     __syncthreads();
@@ -166,12 +186,90 @@ __global__ void __launch_bounds__(kThreads, 1) linear_tc_kernel(const __grid_con
     const uint32_t tbase = *tslot;
     const uint32_t trow = tbase + ((uint32_t)(32 * (warp & 3)) << 16);   // this warp's lane quarter
     const int row = tid & 127;                                           // this thread's TMEM lane or tile row
-    auto tile = [&](int seq) { return (uint32_t)(seq % ST) * kTile; };
+    // chunk j's input tiles (0 K, 1 V, 2 Q): index of the tile and its barriers, offset, phase
+    auto bar = [&](int in, int j) { return in == 2 ? 2 * NB : in * NB + j % NB; };
+    auto at = [&](int in, int j) { return (uint32_t)(bar(in, j) * kTile); };
+    auto phase = [&](int in, int j) { return in == 2 ? j : j / NB; };
     auto warp_wait = [&](uint64_t* bar, int parity) {
-        return __all_sync(0xffffffffu, wait_bar(bar, (uint32_t)parity & 1u, abort_flag, limit)) != 0;
+        return tcu::warp_wait_bar(bar, (uint32_t)parity & 1u, abort_flag, limit);
     };
-    auto full_parity = [&](int seq) { return (seq / ST) & 1; };
     Walk w(p, job);
+    // Tokens 32 sb .. of V'^T, this warp's 32 value dimensions (TMEM lanes): transposed on the way from shared memory by
+    // ldmatrix, whose fragment (lane l: dimension l / 4, token pair l % 4 of an 8 x 8 matrix) is the 16x128b form's.
+    auto scale_values = [&](int j, int n, int sb) {
+        const int q4 = warp & 3, pr = lane & 3;
+        // row addresses: token 8 g + (lane & 7) of the block, dimensions 8 (lane / 8) .. of this warp's 32
+        const uint32_t src = sbase + at(1, j) + (q4 >> 1) * 16384 + (32 * sb + (lane & 7)) * 128 +
+                             ((((q4 & 1) * 4 + (lane >> 3)) ^ (lane & 7)) << 4);
+        uint32_t hi[2][8], lo[2][8];   // [16 dimensions][8-token group g, 8 dimensions of those]
+        // every load first: one at a time, each of the four would wait out its latency and its arithmetic's
+        uint32_t v[4][4];
+        float2 f[4];
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+            ldsm_x4_trans(src + g * 8 * 128, v[g]);
+            f[g] = *reinterpret_cast<const float2*>(vp + 32 * sb + 8 * g + 2 * pr);   // a^{127-s}, a^{126-s}
+        }
+        if (n < kTok) {
+#pragma unroll
+            for (int g = 0; g < 4; ++g) {
+                const int s = 32 * sb + 8 * g + 2 * pr;   // this lane's tokens s and s + 1
+                f[g].x = pw[max(n - 1 - s, 0)], f[g].y = pw[max(n - 2 - s, 0)];
+                // past the chunk: another chunk's or sequence's values, not taken in
+                const uint32_t in = (s < n ? 0xffffu : 0u) | (s + 1 < n ? 0xffff0000u : 0u);
+#pragma unroll
+                for (int m = 0; m < 4; ++m) v[g][m] &= in;
+            }
+        }
+#pragma unroll
+        for (int g = 0; g < 4; ++g)
+#pragma unroll
+            for (int m = 0; m < 4; ++m) {
+                const float2 z = __fmul2_rn(bf16x2_to_float2(v[g][m]), f[g]);
+                split_pair(z.x, z.y, hi[m >> 1][2 * g + (m & 1)], lo[m >> 1][2 * g + (m & 1)]);
+            }
+#pragma unroll
+        for (int m = 0; m < 2; ++m) {
+            tmem_st_16x128b_x4(trow + (16u * m << 16) + T_VH + 16 * sb, hi[m]);
+            tmem_st_16x128b_x4(trow + (16u * m << 16) + T_VL + 16 * sb, lo[m]);
+        }
+    };
+    // Column block cb of P over G's columns, for this warp's token rows [32 rb, 32 rb + 32), lane a row; diag[i] =
+    // a^{lane - i}, the same in every chunk.
+    auto decay_scores = [&](int cb, float rowf, const float (&diag)[32]) {
+        const int rb = warp & 3;
+        uint32_t pk[16];
+        if (cb <= rb) {
+            float g[32];
+            if (cb < rb) {
+                // a^{t-s} = a^{lane} a^{32 (rb - cb) - i}: both exponents are at least 0
+                const float4* col = reinterpret_cast<const float4*>(wp + kTok - 32 * (rb - cb));
+                const float2 rf = make_float2(rowf, rowf);
+                float2 f[16];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const float4 x = col[i];
+                    f[2 * i] = __fmul2_rn(make_float2(x.x, x.y), rf), f[2 * i + 1] = __fmul2_rn(make_float2(x.z, x.w), rf);
+                }
+                tmem_ld32(trow + T_G + 32 * cb, g);
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    const float2 y = __fmul2_rn(f[i], make_float2(g[2 * i], g[2 * i + 1]));
+                    pk[i] = pack2(y.x, y.y);
+                }
+            } else {
+                tmem_ld32(trow + T_G + 32 * cb, g);
+#pragma unroll
+                for (int i = 0; i < 32; ++i) g[i] = i <= lane ? g[i] * diag[i] : 0.f;
+#pragma unroll
+                for (int i = 0; i < 16; ++i) pk[i] = pack2(g[2 * i], g[2 * i + 1]);
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) pk[i] = 0u;
+        }
+        tmem_st16(trow + p_block(cb), pk);
+    };
 
     if (warp < 4) {
         // ---- state ----
@@ -236,6 +334,28 @@ __global__ void __launch_bounds__(kThreads, 1) linear_tc_kernel(const __grid_con
             if (READOUT) proxy_fence();
             tc_fence_before();
             mbar_arrive(s_ready);
+            // then V', on the chain as well
+            ok = warp_wait(&full[bar(1, j)], phase(1, j));
+            if (!ok) break;
+#pragma unroll 1
+            for (int sb = 0; sb < 4; ++sb) scale_values(j, w.n, sb);
+            if (w.n < kTok) {
+                ok = warp_wait(&full[bar(0, j)], phase(0, j));
+                if (!ok) break;
+                if (row >= w.n) {
+#pragma unroll 1
+                    for (int in = 0; in < 2; ++in) {
+                        unsigned char* x = smem + at(in, j) + row * 128;
+#pragma unroll
+                        for (int c = 0; c < 16; ++c)
+                            *reinterpret_cast<uint4*>(x + (c >> 3) * 16384 + (c & 7) * 16) = make_uint4(0, 0, 0, 0);
+                    }
+                }
+                proxy_fence();
+            }
+            tmem_st_wait();
+            tc_fence_before();
+            mbar_arrive(v_ready);
             slot = w.dump() ? p.ckpts[w.ck].slot : -1;
         }
         if (ok && j > 0) {
@@ -254,219 +374,181 @@ __global__ void __launch_bounds__(kThreads, 1) linear_tc_kernel(const __grid_con
     } else if (warp < 8) {
         // ---- tokens: lane = token row, this warp's rows are [32 rb, 32 rb + 32) ----
         if (READOUT) {
-            const int rb = warp & 3;
-            const float rowf = pw[lane], inter = pw[row + 1] * p.scale;
-            const float2 inter2 = make_float2(inter, inter), scale2 = make_float2(p.scale, p.scale);
-            int held = -1;   // ring slot of the last chunk's Q tile, until its output has been copied out of it
-            auto release = [&] {
-                if (held >= 0) {
-                    asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
-                    mbar_arrive(&empty[held]);
-                    held = -1;
-                }
-                __syncwarp();
-            };
+            const float rowf = pw[lane], inter = pw[row + 1];
+            const float2 inter2 = make_float2(inter, inter);
+            float diag[32];
+#pragma unroll
+            for (int i = 0; i < 32; ++i) diag[i] = pw[max(lane - i, 0)];
             for (int j = 0; w.more(); w.next(), ++j) {
                 if (!warp_wait(g_done, j)) break;
                 tc_fence_after();
 #pragma unroll 1
-                for (int cb = 0; cb < 4; ++cb) {
-                    uint32_t pk[16];
-                    if (cb <= rb) {
-                        float g[32];
-                        tmem_ld32(trow + T_G + 32 * cb, g);
-                        if (cb < rb) {
-                            // a^{t-s} = a^{lane} a^{32 (rb - cb) - i}: both exponents are at least 0
-                            const float4* col = reinterpret_cast<const float4*>(wp + kTok - 32 * (rb - cb));
-                            const float2 rf = make_float2(rowf, rowf);
+                for (int cb = 0; cb < 2; ++cb) decay_scores(cb, rowf, diag);
+                if (!warp_wait(q_done, j)) break;
+                tc_fence_after();
+#pragma unroll 1
+                for (int c = 0; c < 4; ++c) {
+                    float x[32];
+                    tmem_ld32(trow + T_O + 32 * c, x);
 #pragma unroll
-                            for (int i = 0; i < 8; ++i) {
-                                const float4 x = col[i];
-                                const float2 y0 = __fmul2_rn(__fmul2_rn(make_float2(x.x, x.y), rf), make_float2(g[4 * i], g[4 * i + 1]));
-                                const float2 y1 = __fmul2_rn(__fmul2_rn(make_float2(x.z, x.w), rf), make_float2(g[4 * i + 2], g[4 * i + 3]));
-                                pk[2 * i] = pack2(y0.x, y0.y), pk[2 * i + 1] = pack2(y1.x, y1.y);
-                            }
-                        } else {
-                            const float* d = wp + kTok - lane;   // d[i] = a^{lane - i}, not read past the diagonal
-#pragma unroll
-                            for (int i = 0; i < 32; ++i) g[i] = i <= lane ? g[i] * d[i] : 0.f;
-#pragma unroll
-                            for (int i = 0; i < 16; ++i) pk[i] = pack2(g[2 * i], g[2 * i + 1]);
-                        }
-                    } else {
-#pragma unroll
-                        for (int i = 0; i < 16; ++i) pk[i] = 0u;
+                    for (int i = 0; i < 32; i += 2) {
+                        const float2 z = __fmul2_rn(inter2, make_float2(x[i], x[i + 1]));
+                        x[i] = z.x, x[i + 1] = z.y;
                     }
-                    tmem_st16(trow + T_G + 16 * cb, pk);   // over the columns of G that are read by now
+                    tmem_st32(trow + T_O + 32 * c, x);
                 }
                 tmem_st_wait();
                 tc_fence_before();
                 mbar_arrive(p_ready);
-                release();
-                if (!warp_wait(o_done, j)) break;
-                tc_fence_after();
-                const int qs = PER * j + 1;
-                const bool whole = w.n == kTok;
-                __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.o) + ((job.tok_begin + w.pos + row) * p.H + h) * (int64_t)D;
-                // A whole chunk is staged in its spent Q tile and copied out by TMA: a thread holds a row, and 16-byte
-                // stores of 32 rows at a time took 3100 of the 8300 cycles of a chunk.  A cut one is stored directly.
-#pragma unroll 1
-                for (int c = 0; c < 4; ++c) {
-                    float x[32], y[32];
-                    tmem_ld32x2(trow + T_O1 + 32 * c, trow + T_O2 + 32 * c, x, y);
-                    unsigned char* piece = smem + tile(qs) + (c >> 1) * 16384;
-#pragma unroll
-                    for (int i = 0; i < 32; i += 8) {
-                        uint32_t u[4];
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const int k = i + 2 * e;
-                            const float2 z = __ffma2_rn(inter2, make_float2(x[k], x[k + 1]),
-                                                        __fmul2_rn(scale2, make_float2(y[k], y[k + 1])));
-                            u[e] = pack2(z.x, z.y);
-                        }
-                        const uint4 q4 = make_uint4(u[0], u[1], u[2], u[3]);
-                        if (whole)
-                            *reinterpret_cast<uint4*>(piece + sw128(row, (c & 1) * 32 + i)) = q4;
-                        else if (row < w.n)
-                            *reinterpret_cast<uint4*>(dst + 32 * c + i) = q4;
-                    }
-                }
-                proxy_fence();
-                tc_fence_before();
-                mbar_arrive(o_free);
-                mbar_arrive(o_staged);
-                bool staged = true;
-                if (tid == 128) {
-                    staged = wait_bar(o_staged, (uint32_t)j & 1u, abort_flag, limit);
-                    if (staged && whole) {
-                        const int t0 = (int)(job.tok_begin + w.pos);
-                        tma_store_3d(smem + tile(qs), &p.tm_o, 0, h, t0);
-                        tma_store_3d(smem + tile(qs) + 16384, &p.tm_o, 64, h, t0);
-                        asm volatile("cp.async.bulk.commit_group;" ::: "memory");
-                    }
-                    held = qs % ST;
-                }
-                if (!__all_sync(0xffffffffu, staged)) break;
             }
-            release();
         }
     } else if (warp < 12) {
-        // ---- keys: row = token s ----
-        for (int j = 0; w.more(); w.next(), ++j) {
-            const int ks = PER * j, vs = PER * j + PER - 1;
-            // G has read K; the last update has read K' lo
-            if (READOUT && !warp_wait(g_done, j)) break;
-            if (!warp_wait(&full[ks % ST], full_parity(ks))) break;
-            if (j > 0 && !warp_wait(st_done, j - 1)) break;
-            const bool in = row < w.n;
-            const float f = in ? pw[w.n - 1 - row] : 0.f;
-            unsigned char* hi = smem + tile(ks);
-            unsigned char* lo = smem + OFF_KLO;
-            const float2 f2 = make_float2(f, f);
-#pragma unroll 1
-            for (int c0 = 0; c0 < 4; ++c0) {
-                // all loads of a quarter row before its stores: the compiler may not move a load over a store
-                uint4 x[4];
-                const uint32_t off = (c0 >> 1) * 16384 + row * 128;
+        // ---- output: lane = token row ----
+        if (READOUT) {
+            const bool wide = (reinterpret_cast<uintptr_t>(p.o) & 31) == 0;
+            const float2 scale2 = make_float2(p.scale, p.scale);
+            const float rowf = pw[lane];
+            float diag[32];
 #pragma unroll
-                for (int c = 0; c < 4; ++c)   // past the chunk: another chunk's or sequence's keys, not taken in
-                    x[c] = in ? *reinterpret_cast<const uint4*>(hi + off + (((4 * (c0 & 1) + c) ^ (row & 7)) << 4))
-                              : make_uint4(0u, 0u, 0u, 0u);
+            for (int i = 0; i < 32; ++i) diag[i] = pw[max(lane - i, 0)];
+            for (int j = 0; w.more(); w.next(), ++j) {
+                if (!warp_wait(g_done, j)) break;
+                tc_fence_after();
+#pragma unroll 1
+                for (int cb = 2; cb < 4; ++cb) decay_scores(cb, rowf, diag);
+                tmem_st_wait();
+                tc_fence_before();
+                mbar_arrive(p_ready);
+                if (!warp_wait(o_done, j)) break;
+                tc_fence_after();
+                // the whole row into registers first, so that the next chunk's O can begin before the stores are through
+                uint32_t u[8][8];
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {
-                    uint32_t a[4] = {x[c].x, x[c].y, x[c].z, x[c].w}, b[4];
+                    float x[32];
+                    tmem_ld32(trow + T_O + 32 * c, x);
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const float2 y = __fmul2_rn(bf16x2_to_float2(a[i]), f2);
-                        split_pair(y.x, y.y, a[i], b[i]);
+                    for (int i = 0; i < 16; ++i) {
+                        const float2 z = __fmul2_rn(scale2, make_float2(x[2 * i], x[2 * i + 1]));
+                        u[2 * c + (i >> 3)][i & 7] = pack2(z.x, z.y);
                     }
-                    const uint32_t at = off + (((4 * (c0 & 1) + c) ^ (row & 7)) << 4);
-                    *reinterpret_cast<uint4*>(hi + at) = make_uint4(a[0], a[1], a[2], a[3]);
-                    *reinterpret_cast<uint4*>(lo + at) = make_uint4(b[0], b[1], b[2], b[3]);
                 }
-            }
-            if (w.n < kTok) {
-                if (!warp_wait(&full[vs % ST], full_parity(vs))) break;
-                if (!in) {
-                    unsigned char* v = smem + tile(vs) + row * 128;
+                tc_fence_before();
+                mbar_arrive(o_free);
+                // A whole chunk is staged and copied out by TMA: a thread holds a row, and stores of 32 rows at a time,
+                // 32 bytes each, kept the load/store unit from everyone for 1200 cycles.  A cut one is stored like that.
+                if (j > 0 && !warp_wait(o_left, j - 1)) break;
+                if (w.n == kTok) {
 #pragma unroll
                     for (int c = 0; c < 16; ++c)
-                        *reinterpret_cast<uint4*>(v + (c >> 3) * 16384 + (c & 7) * 16) = make_uint4(0, 0, 0, 0);
+                        *reinterpret_cast<uint4*>(smem + OFF_O + (c >> 3) * 16384 + sw128(row, (c & 7) * 8)) =
+                            make_uint4(u[c >> 1][(c & 1) * 4], u[c >> 1][(c & 1) * 4 + 1], u[c >> 1][(c & 1) * 4 + 2],
+                                       u[c >> 1][(c & 1) * 4 + 3]);
+                    proxy_fence();
+                } else if (row < w.n) {
+                    __nv_bfloat16* dst =
+                        static_cast<__nv_bfloat16*>(p.o) + ((job.tok_begin + w.pos + row) * p.H + h) * (int64_t)D;
+#pragma unroll
+                    for (int c = 0; c < 8; ++c) store32(dst + 16 * c, u[c], wide);
                 }
+                mbar_arrive(o_staged);
             }
-            proxy_fence();
-            mbar_arrive(k_ready);
         }
     } else if (warp == 12) {
-        // ---- products ----
-        if (lane == 0) {
-            const uint32_t id = idesc(D, false, false), id_b = idesc(D, false, true), id_ab = idesc(D, true, true);
-            auto wait = [&](uint64_t* bar, int parity) { return wait_bar(bar, (uint32_t)parity & 1u, abort_flag, limit); };
-            for (int j = 0; w.more(); w.next(), ++j) {
-                const int ks = PER * j, qs = ks + 1, vs = PER * j + PER - 1;
-                const uint32_t k = sbase + tile(ks), q = sbase + tile(qs), v = sbase + tile(vs);
-                if (READOUT) {
-                    if (!wait(&full[ks % ST], full_parity(ks)) || !wait(&full[qs % ST], full_parity(qs))) break;
+        // ---- products (the whole warp walks along, one elected lane issues) ----
+        const uint32_t id = idesc(D, false, false), id_b = idesc(D, false, true);
+        const uint64_t s_desc = tile_desc(sbase + OFF_S, false);
+        auto scores = [&](int j) {   // G of chunk j
+            if (!warp_wait(&full[bar(0, j)], phase(0, j)) || !warp_wait(&full[bar(2, j)], phase(2, j))) return false;
+            const uint64_t q = tile_desc(sbase + at(2, j), false), k = tile_desc(sbase + at(0, j), false);
+            if (elect_one()) {
 #pragma unroll
-                    for (int kk = 0; kk < 8; ++kk) {
-                        const uint32_t off = (uint32_t)((kk >> 2) * 16384 + (kk & 3) * 32);
-                        umma_ss(tbase + T_G, sdesc(q + off, 16, 1024), sdesc(k + off, 16, 1024), id, kk > 0);
-                    }
-                    umma_commit(g_done);
-                }
-                if (!wait(s_ready, j)) break;
-                if (READOUT) {
-                    if (j > 0 && !wait(o_free, j - 1)) break;
-                    tc_fence_after();
-#pragma unroll
-                    for (int kk = 0; kk < 8; ++kk) {
-                        const uint32_t off = (uint32_t)((kk >> 2) * 16384 + (kk & 3) * 32);
-                        umma_ss(tbase + T_O1, sdesc(q + off, 16, 1024), sdesc(sbase + OFF_S + off, 16, 1024), id, kk > 0);
-                    }
-                }
-                if (!wait(&full[vs % ST], full_parity(vs))) break;
-                if (READOUT) {
-                    if (!wait(p_ready, j)) break;
-                    if (w.n < kTok && !wait(k_ready, j)) break;   // a cut chunk's value rows are zeroed by then
-                    tc_fence_after();
-#pragma unroll
-                    for (int kt = 0; kt < 8; ++kt)
-                        umma_ts(tbase + T_O2, tbase + T_G + 8 * kt, sdesc(v + kt * 2048, 16384, 1024), id_b, kt > 0);
-                    umma_commit(o_done);
-                }
-                if (!wait(k_ready, j)) break;
+                for (int i = 0; i < 8; ++i) umma_ss(tbase + T_G, cols_step(q, i), cols_step(k, i), id, i > 0);
+                umma_commit(g_done);
+            }
+            return true;
+        };
+        bool ok = !READOUT || !w.more() || scores(0);
+        for (int j = 0; ok && w.more(); ++j) {
+            w.next();
+            ok = warp_wait(s_ready, j);
+            if (!ok) break;
+            if (READOUT) {
+                ok = j == 0 || warp_wait(o_free, j - 1);
+                if (!ok) break;
                 tc_fence_after();
+                const uint64_t q = tile_desc(sbase + at(2, j), false);
+                if (elect_one()) {
 #pragma unroll
-                for (int kt = 0; kt < 8; ++kt) {
-                    const uint64_t av = sdesc(v + kt * 2048, 16384, 1024);
-                    umma_ss(tbase + T_S, av, sdesc(k + kt * 2048, 16384, 1024), id_ab, 1);
-                    umma_ss(tbase + T_S, av, sdesc(sbase + OFF_KLO + kt * 2048, 16384, 1024), id_ab, 1);
+                    for (int i = 0; i < 8; ++i) umma_ss(tbase + T_O, cols_step(q, i), cols_step(s_desc, i), id, i > 0);
+                    umma_commit(q_done);
+                    umma_commit(&empty[bar(2, j)]);
+                }
+            }
+            ok = warp_wait(v_ready, j) && warp_wait(&full[bar(0, j)], phase(0, j));
+            if (!ok) break;
+            tc_fence_after();
+            const uint64_t k = tile_desc(sbase + at(0, j), true), v = tile_desc(sbase + at(1, j), true);
+            if (elect_one()) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    umma_ts(tbase + T_S, tbase + T_VH + 8 * i, rows_step(k, i), id_b, 1);
+                    umma_ts(tbase + T_S, tbase + T_VL + 8 * i, rows_step(k, i), id_b, 1);
                 }
                 umma_commit(st_done);
-                umma_commit(&empty[ks % ST]);
-                umma_commit(&empty[vs % ST]);
+                umma_commit(&empty[bar(0, j)]);
             }
-            umma_commit(end);   // also after giving up: the end waits for the products in flight
+            if (READOUT) {
+                ok = warp_wait(p_ready, j) && warp_wait(&full[bar(1, j)], phase(1, j));
+                if (!ok) break;
+                tc_fence_after();
+            }
+            if (elect_one()) {
+                if (READOUT) {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) umma_ts(tbase + T_O, tbase + p_block(i >> 1) + 8 * (i & 1), rows_step(v, i), id_b, 1);
+                    umma_commit(o_done);
+                }
+                umma_commit(&empty[bar(1, j)]);
+            }
+            if (READOUT) ok = !w.more() || scores(j + 1);
         }
-    } else if (lane == 0) {
-        // ---- copies ----
+        if (elect_one()) umma_commit(end);   // also after giving up: the end waits for the products in flight
+    } else if (warp == 14) {
+        // ---- staged output to memory ----
+        if (READOUT && lane == 0) {
+            for (int j = 0; w.more(); w.next(), ++j) {
+                if (!wait_bar(o_staged, (uint32_t)j & 1u, abort_flag, limit)) break;
+                if (w.n == kTok) {
+                    const int t0 = (int)(job.tok_begin + w.pos);
+                    tma_store_3d(smem + OFF_O, &p.tm_o, 0, h, t0);
+                    tma_store_3d(smem + OFF_O + 16384, &p.tm_o, 64, h, t0);
+                    asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+                    asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+                }
+                mbar_arrive(o_left);
+            }
+        }
+    } else if (lane == 0 && (warp == 13 || READOUT)) {
+        // ---- copies: warp 13 K and V, warp 15 Q, whose buffer comes free at another time of the chunk ----
+        const int first = warp == 13 ? 0 : 2, last = warp == 13 ? 1 : 2;
         bool ok = true;
         for (int j = 0; ok && w.more(); w.next(), ++j) {
             if (p.stall_after >= 0 && j >= p.stall_after) break;   // testing hook
             const int t0 = (int)(job.tok_begin + w.pos);
-            for (int i = 0; i < PER; ++i) {
-                const int seq = PER * j + i, s = seq % ST;
-                if (seq >= ST && !wait_bar(&empty[s], (uint32_t)((seq / ST - 1) & 1), abort_flag, limit)) {
+            for (int in = first; in <= last; ++in) {
+                if (phase(in, j) > 0 &&
+                    !wait_bar(&empty[bar(in, j)], (uint32_t)(phase(in, j) - 1) & 1u, abort_flag, limit)) {
                     ok = false;
                     break;
                 }
-                const CUtensorMap* tm = i == 0 ? &p.tm_k : i == PER - 1 ? &p.tm_v : &p.tm_q;
-                const int head = i == PER - 1 ? h : hk;
-                mbar_arrive_expect_tx(&full[s], kTile);
-                tma_load_3d(smem + s * kTile, tm, 0, head, t0, &full[s]);
-                tma_load_3d(smem + s * kTile + 16384, tm, 64, head, t0, &full[s]);
-                *issued = seq + 1;
+                const CUtensorMap* tm = in == 0 ? &p.tm_k : in == 1 ? &p.tm_v : &p.tm_q;
+                const int head = in == 1 ? h : hk;
+                uint64_t* b = &full[bar(in, j)];
+                mbar_arrive_expect_tx(b, kTile);
+                tma_load_3d(smem + at(in, j), tm, 0, head, t0, b);
+                tma_load_3d(smem + at(in, j) + 16384, tm, 64, head, t0, b);
+                issued[in] = j + 1;
             }
         }
     }
@@ -476,8 +558,9 @@ __global__ void __launch_bounds__(kThreads, 1) linear_tc_kernel(const __grid_con
     __syncthreads();
     if (tid == 0 && *abort_flag) {
         const uint64_t drain = limit > kDrainLimitNs ? limit : kDrainLimitNs;
-        for (int seq = max(0, *issued - ST); seq < *issued; ++seq)
-            tc::drain_phase(&full[seq % ST], (uint32_t)((seq / ST) & 1), drain);
+        for (int in = 0; in < 3; ++in)
+            for (int j = max(0, issued[in] - (in == 2 ? 1 : NB)); j < issued[in]; ++j)
+                tc::drain_phase(&full[bar(in, j)], (uint32_t)phase(in, j) & 1u, drain);
         tc::drain_phase(end, 0, drain);
         atomicOr(p.status, STATUS_TIMEOUT);
     }

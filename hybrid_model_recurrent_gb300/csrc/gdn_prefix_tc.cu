@@ -22,8 +22,8 @@
 
 #include <cmath>
 
-#include "gdn_chunk_tc.cuh"
 #include "gdn_prefix.cuh"
+#include "gdn_tc_util.cuh"
 
 namespace gdn {
 namespace prefix {
@@ -31,7 +31,6 @@ namespace {
 
 using tc::idesc;
 using tc::proxy_fence;
-using tc::sdesc;
 using tc::sw128;
 using tc::tc_fence_after;
 using tc::tc_fence_before;
@@ -43,6 +42,14 @@ using tc::tmem_st_wait;
 using tc::umma_commit;
 using tc::umma_ss;
 using tc::umma_ts;
+using tcu::cols_step;
+using tcu::elect_one;
+using tcu::pack2;
+using tcu::rows_step;
+using tcu::store32;
+using tcu::tile_desc;
+using tcu::wait_bar;
+using tcu::warp_wait_bar;
 
 constexpr int kRows = 128;   // rows of a tile
 constexpr int kKeys = 128;   // tokens of a tile
@@ -66,10 +73,6 @@ __device__ __forceinline__ float ex2(float x) {
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
-__device__ __forceinline__ uint32_t pack2(float a, float b) {
-    const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
-    return *reinterpret_cast<const uint32_t*>(&h);
-}
 __device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* tm, int x, int y, int z, int w, uint64_t* bar) {
     asm volatile(
         "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], "
@@ -77,30 +80,6 @@ __device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* tm, in
         "l"(reinterpret_cast<uint64_t>(tm)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(smem_addr(bar))
         : "memory");
 }
-// bounded wait of one thread; gives up when another role has given up
-__device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity, volatile int* abort_flag, uint64_t limit) {
-    if (mbar_try_wait(bar, parity)) return true;
-    const uint64_t t0 = global_ns();
-    for (;;) {
-        if (mbar_try_wait_suspend(bar, parity, 2000)) return true;
-        if (*abort_flag) return false;
-        if (global_ns() - t0 > limit) {
-            *abort_flag = 1;
-            return false;
-        }
-    }
-}
-__device__ __forceinline__ bool warp_wait_bar(uint64_t* bar, uint32_t parity, volatile int* abort_flag, uint64_t limit) {
-    return __all_sync(0xffffffffu, wait_bar(bar, parity, abort_flag, limit));
-}
-// 32 bytes of one row (32-byte aligned)
-__device__ __forceinline__ void st_row8(void* p, uint32_t a, uint32_t b, uint32_t c, uint32_t d, uint32_t e, uint32_t f,
-                                        uint32_t g, uint32_t h) {
-    asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(a), "r"(b), "r"(c), "r"(d), "r"(e),
-                 "r"(f), "r"(g), "r"(h)
-                 : "memory");
-}
-
 template <int D, int NT>
 __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, NT == 1 ? 2 : 1)
     prefix_tc_kernel(const __grid_constant__ Params p, const int pre_items, const bool joined, const bool direct) {
@@ -175,50 +154,56 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, NT == 1 ? 2 : 1)
     const uint32_t tbase = *tslot;
 
     if (warp == NT * 4) {
-        // ---- products ----
-        if (lane == 0 && n_tiles > 0) {
-            bool ok = wait_bar(q_ready, 0, abort_flag, limit);
+        // ---- products (the whole warp walks along, one elected lane issues) ----
+        if (n_tiles > 0) {
+            bool ok = warp_wait_bar(q_ready, 0, abort_flag, limit);
             auto slot_at = [&](int seq) { return sbase + F::kRing + (uint32_t)(seq % F::ST) * F::kTile; };
             auto scores = [&](int a, int j) {
-                const uint32_t q = sbase + a * F::kTile, k = slot_at(2 * j);
+                const uint64_t q = tile_desc(sbase + a * F::kTile, false), k = tile_desc(slot_at(2 * j), false);
+                if (elect_one()) {
 #pragma unroll
-                for (int kk = 0; kk < D / 16; ++kk) {
-                    const uint32_t off = (uint32_t)((kk >> 2) * 16384 + (kk & 3) * 32);   // 64-column blocks of 128 rows
-                    umma_ss(tbase + a * 128, sdesc(q + off, 16, 1024), sdesc(k + off, 16, 1024), idesc(kKeys, false, false),
-                            kk > 0);
+                    for (int i = 0; i < D / 16; ++i)
+                        umma_ss(tbase + a * 128, cols_step(q, i), cols_step(k, i), idesc(kKeys, false, false), i > 0);
+                    umma_commit(&s_full[a]);
                 }
-                umma_commit(&s_full[a]);
             };
             auto values = [&](int a, int j) {
-                const uint32_t v = slot_at(2 * j + 1);
+                const uint64_t v = tile_desc(slot_at(2 * j + 1), true);
+                if (elect_one()) {
 #pragma unroll
-                for (int kt = 0; kt < kKeys / 16; ++kt)
-                    umma_ts(tbase + F::kO + a * D, tbase + a * 128 + 8 * kt, sdesc(v + kt * 2048, 16384, 1024),
-                            idesc(D, false, true), j > 0 || kt > 0);
+                    for (int i = 0; i < kKeys / 16; ++i)
+                        umma_ts(tbase + F::kO + a * D, tbase + a * 128 + 8 * i, rows_step(v, i), idesc(D, false, true),
+                                j > 0 || i > 0);
+                }
             };
-            if (ok) ok = wait_bar(&full[0], 0, abort_flag, limit);
+            auto done = [&](uint64_t* bar) {
+                if (elect_one()) umma_commit(bar);
+            };
+            if (ok) ok = warp_wait_bar(&full[0], 0, abort_flag, limit);
             if (ok) {
+#pragma unroll
                 for (int a = 0; a < NT; ++a) scores(a, 0);
-                umma_commit(&empty[0]);
+                done(&empty[0]);
             }
             for (int j = 0; ok && j < n_tiles; ++j) {
                 const int vs = 2 * j + 1, ks = 2 * j + 2;
-                ok = wait_bar(&full[vs % F::ST], (uint32_t)((vs / F::ST) & 1), abort_flag, limit);
-                for (int a = 0; ok && a < NT; ++a) {
-                    ok = wait_bar(&p_ready[a], (uint32_t)(j & 1), abort_flag, limit);
+                ok = warp_wait_bar(&full[vs % F::ST], (uint32_t)((vs / F::ST) & 1), abort_flag, limit);
+#pragma unroll
+                for (int a = 0; a < NT; ++a) {
+                    ok = ok && warp_wait_bar(&p_ready[a], (uint32_t)(j & 1), abort_flag, limit);
                     if (!ok) break;
                     tc_fence_after();
                     values(a, j);
-                    if (a == NT - 1) umma_commit(&empty[vs % F::ST]);
+                    if (a == NT - 1) done(&empty[vs % F::ST]);
                     if (j + 1 < n_tiles) {
-                        if (a == 0) ok = wait_bar(&full[ks % F::ST], (uint32_t)((ks / F::ST) & 1), abort_flag, limit);
+                        if (a == 0) ok = warp_wait_bar(&full[ks % F::ST], (uint32_t)((ks / F::ST) & 1), abort_flag, limit);
                         if (!ok) break;
                         scores(a, j + 1);
-                        if (a == NT - 1) umma_commit(&empty[ks % F::ST]);
+                        if (a == NT - 1) done(&empty[ks % F::ST]);
                     }
                 }
             }
-            umma_commit(o_full);   // also after giving up: the end waits for the products in flight
+            done(o_full);   // also after giving up: the end waits for the products in flight
         }
     } else if (warp == NT * 4 + 1) {
         // ---- copies: K_0, V_0, K_1, V_1, ... ----
@@ -380,23 +365,25 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, NT == 1 ? 2 : 1)
                         for (int i = 0; i < 32; ++i) o[i] = 0.f;
                     }
                     if (valid && direct) {
-                        uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.o) + at * D + 32 * c);
+                        __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.o) + at * D + 32 * c;
+                        const bool wide = (reinterpret_cast<uintptr_t>(p.o) & 31) == 0;
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            uint32_t w[4];
+                        for (int i = 0; i < 32; i += 16) {
+                            uint32_t u[8];
 #pragma unroll
-                            for (int k = 0; k < 4; ++k)
-                                w[k] = some ? pack2(o[8 * i + 2 * k] * inv, o[8 * i + 2 * k + 1] * inv) : 0u;
-                            dst[i] = make_uint4(w[0], w[1], w[2], w[3]);
+                            for (int k = 0; k < 8; ++k)
+                                u[k] = some ? pack2(o[i + 2 * k] * inv, o[i + 2 * k + 1] * inv) : 0u;
+                            store32(dst + i, u, wide);
                         }
                     } else if (valid) {
                         float* dst = p.part_o + (part * ((int64_t)p.B * p.n * p.Hq) + at) * D + 32 * c;
 #pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            st_row8(dst + 8 * i, __float_as_uint(o[8 * i]), __float_as_uint(o[8 * i + 1]),
-                                    __float_as_uint(o[8 * i + 2]), __float_as_uint(o[8 * i + 3]),
-                                    __float_as_uint(o[8 * i + 4]), __float_as_uint(o[8 * i + 5]),
-                                    __float_as_uint(o[8 * i + 6]), __float_as_uint(o[8 * i + 7]));
+                        for (int i = 0; i < 32; i += 8) {
+                            uint32_t u[8];
+#pragma unroll
+                            for (int k = 0; k < 8; ++k) u[k] = __float_as_uint(o[i + k]);
+                            store32(dst + i, u, true);
+                        }
                     }
                 }
             }
