@@ -106,6 +106,8 @@ def build(force: bool = False) -> str:
 def lib():
     """The loaded C library; raises if it has not been built."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             if not os.path.exists(LIB_PATH):
@@ -642,6 +644,13 @@ def _expect(ok: bool, message: str) -> None:
         raise ValueError(message)
 
 
+def _raw_stream(stream, dev) -> int:
+    """cudaStream_t of `stream`, or of the current stream of `dev` (without building a Stream object)."""
+    if stream is not None:
+        return stream.cuda_stream
+    return torch._C._cuda_getCurrentRawStream(dev.index if dev.index is not None else torch.cuda.current_device())
+
+
 def _on(stream, dev):
     """Buffers made under this belong to the stream that uses them."""
     return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
@@ -756,7 +765,7 @@ def gdn_linear_step(q, k, v, alpha, states, *, slots=None, scale: float = 1.0, o
             o = torch.empty((B, H, dv), dtype=out_dtype, device=dev)
     rc = lib().gdn_linear_step(ctypes.byref(pr), q.data_ptr(), k.data_ptr(), v.data_ptr(), alpha.data_ptr(),
                                states.data_ptr(), n, None if slots is None else slots.data_ptr(), o.data_ptr(),
-                               (stream or torch.cuda.current_stream(dev)).cuda_stream)
+                               _raw_stream(stream, dev))
     if rc != GDN_OK:
         raise GdnError(rc, "gdn_linear_step")
     return o
@@ -824,6 +833,6 @@ def gdn_prefix_attention(q, k_prefix, v_prefix, k_tail=None, v_tail=None, tail_l
         ctypes.byref(pr), q.data_ptr(), k_prefix.data_ptr() if P else None, v_prefix.data_ptr() if P else None,
         k_tail.data_ptr() if cap else None, v_tail.data_ptr() if cap else None, tail_len.data_ptr() if cap else None,
         o.data_ptr(), lse.data_ptr(), _ptr(scratch), nbytes, ws.data_ptr(), ws.numel(),
-        (stream or torch.cuda.current_stream(dev)).cuda_stream)
+        _raw_stream(stream, dev))
     _check(rc, "gdn_prefix_attention")
     return {"o": o, "lse": lse}

@@ -486,7 +486,7 @@ GDN_EXPORT gdn_status gdn_linear_step(const gdn_linear_problem* p, const void* q
     if (!aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(alpha, 4) || !aligned(states, 16) ||
         !aligned(o, 16) || !aligned(slots, 4))
         return GDN_ERR_INVALID_ARG;
-    if ((int64_t)p->num_seqs * p->num_heads * (p->d_v / gdn::lin::kWarpRows) >= (1ll << 31)) return GDN_ERR_UNSUPPORTED;
+    if ((int64_t)p->num_seqs * p->num_heads * (p->d_v / 8) >= (1ll << 31)) return GDN_ERR_UNSUPPORTED;
     gdn::lin::StepParams s{};
     s.q = q, s.k = k, s.v = v;
     s.q_stride = sd.q, s.k_stride = sd.k, s.v_stride = sd.v;

@@ -141,32 +141,49 @@ __global__ void __launch_bounds__(128) prefix_part_kernel(const __grid_constant_
     }
 }
 
-// o = sum_p 2^(m_p - m) o_p / sum_p 2^(m_p - m) l_p: one warp a query row; bound by reading the parts (from L2).
+// o = sum_p 2^(m_p - m) o_p / sum_p 2^(m_p - m) l_p: one warp a query row, a lane D/32 columns; bound by reading the
+// parts (from L2).  The lanes hold 32 parts' weights at a time and hand them round, so that the parts' rows are loaded
+// several at once, not each behind its weight.
 template <int D, typename T>
 __global__ void __launch_bounds__(128) prefix_join_kernel(const __grid_constant__ Params p, int parts) {
     constexpr int CL = D / 32;
+    struct alignas(CL * 4) Row {
+        float x[CL];
+    };
     const int lane = threadIdx.x & 31;
     const int64_t row = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
     const int64_t all = (int64_t)p.B * p.n * p.Hq;
     if (row >= all) return;
-    float m = -INFINITY;
-    for (int s = lane; s < parts; s += 32) {
-        const float2 ml = p.part_ml[s * all + row];
-        if (ml.y != 0.f) m = fmaxf(m, ml.x);
-    }
-#pragma unroll
-    for (int d = 16; d; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
-    float l = 0.f, acc[CL];
+    float m = -INFINITY, l = 0.f, acc[CL];
 #pragma unroll
     for (int j = 0; j < CL; ++j) acc[j] = 0.f;
-    for (int s = 0; s < parts; ++s) {
-        const float2 ml = p.part_ml[s * all + row];
-        if (ml.y == 0.f) continue;   // (a NaN sum is taken in)
-        const float f = exp2f(ml.x - m);
-        l = fmaf(f, ml.y, l);
-        const float* src = p.part_o + (s * all + row) * D + lane * CL;
+    for (int s0 = 0; s0 < parts; s0 += 32) {
+        // (an empty part has l = 0 and unwritten values, which are not read; a NaN sum is taken in)
+        const float2 ml = s0 + lane < parts ? p.part_ml[(s0 + lane) * all + row] : make_float2(-INFINITY, 0.f);
+        float top = ml.y != 0.f ? ml.x : -INFINITY;
 #pragma unroll
-        for (int j = 0; j < CL; ++j) acc[j] = fmaf(f, src[j], acc[j]);
+        for (int d = 16; d; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+        const float mn = fmaxf(m, top);
+        const float base = mn == -INFINITY ? 0.f : mn;
+        const float w = ml.y != 0.f ? exp2f(ml.x - base) : 0.f, f = exp2f(m - base);
+        m = mn;
+        l = l * f;
+#pragma unroll
+        for (int j = 0; j < CL; ++j) acc[j] *= f;
+        float lw = ml.y != 0.f ? w * ml.y : 0.f;
+#pragma unroll
+        for (int d = 16; d; d >>= 1) lw += __shfl_xor_sync(0xffffffffu, lw, d);
+        l += lw;
+        const unsigned live = __ballot_sync(0xffffffffu, ml.y != 0.f);
+        const int n = min(32, parts - s0);
+#pragma unroll 4
+        for (int i = 0; i < n; ++i) {
+            const float wi = __shfl_sync(0xffffffffu, w, i);
+            Row r{};
+            if (live >> i & 1) r = *reinterpret_cast<const Row*>(p.part_o + ((s0 + i) * all + row) * D + lane * CL);
+#pragma unroll
+            for (int j = 0; j < CL; ++j) acc[j] = fmaf(wi, r.x[j], acc[j]);
+        }
     }
     const float inv = l == 0.f ? 0.f : 1.f / l;
     T* o = static_cast<T*>(p.o) + row * D + lane * CL;
