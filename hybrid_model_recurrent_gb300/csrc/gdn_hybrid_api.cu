@@ -24,7 +24,7 @@ void* encode_tiled_fn();
 
 namespace {
 
-constexpr int kSms = 152;
+constexpr int kSms = gdn::prefix::kSms;
 
 bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 bool supported_d(int d) { return d == 32 || d == 64 || d == 128; }
@@ -442,18 +442,18 @@ gdn_status prefix_attention(const gdn_prefix_problem* p, const void* q, const vo
         cudaError_t e;
         if (pl.pre_rt == pl.tail_rt || pre_items == 0 || tail_items == 0) {
             e = gdn::prefix::launch_tc(*prm, f.head_dim, pre_items ? pl.pre_rt : pl.tail_rt, pre_items, tail_items,
-                                       pl.joined, direct, stream);
+                                       pl.joined, direct, false, stream);
         } else {
-            e = gdn::prefix::launch_tc(*prm, f.head_dim, pl.pre_rt, pre_items, 0, false, direct, stream);
+            e = gdn::prefix::launch_tc(*prm, f.head_dim, pl.pre_rt, pre_items, 0, false, direct, false, stream);
             if (e == cudaSuccess)
-                e = gdn::prefix::launch_tc(*prm, f.head_dim, pl.tail_rt, 0, tail_items, false, direct, stream);
+                e = gdn::prefix::launch_tc(*prm, f.head_dim, pl.tail_rt, 0, tail_items, false, direct, true, stream);
         }
         if (e != cudaSuccess) return GDN_ERR_CUDA;
         if (direct) return GDN_OK;
     } else if (gdn::prefix::launch_simt(*prm, f.head_dim, bf16, stream) != cudaSuccess) {
         return GDN_ERR_CUDA;
     }
-    return gdn::prefix::launch_join(*prm, f.head_dim, bf16, pl.parts(), stream) == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
+    return gdn::prefix::launch_join(*prm, f.head_dim, bf16, pl.parts(), pl.tc, stream) == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
 }
 
 }  // namespace

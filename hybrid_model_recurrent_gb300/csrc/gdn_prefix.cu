@@ -153,6 +153,7 @@ __global__ void __launch_bounds__(128) prefix_join_kernel(const __grid_constant_
     const int lane = threadIdx.x & 31;
     const int64_t row = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
     const int64_t all = (int64_t)p.B * p.n * p.Hq;
+    asm volatile("griddepcontrol.wait;" ::: "memory");   // the parts (nothing to wait for in a plain launch)
     if (row >= all) return;
     float m = -INFINITY, l = 0.f, acc[CL];
 #pragma unroll
@@ -200,10 +201,18 @@ cudaError_t part(const Params& p, cudaStream_t s) {
     return cudaGetLastError();
 }
 template <int D, typename T>
-cudaError_t join(const Params& p, int parts, cudaStream_t s) {
+cudaError_t join(const Params& p, int parts, bool beside, cudaStream_t s) {
     const int64_t rows = (int64_t)p.B * p.n * p.Hq;
-    prefix_join_kernel<D, T><<<(unsigned)((rows + 3) / 4), 128, 0, s>>>(p, parts);
-    return cudaGetLastError();
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)((rows + 3) / 4));
+    cfg.blockDim = dim3(128);
+    cfg.stream = s;
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = beside ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, prefix_join_kernel<D, T>, p, parts);
 }
 
 }  // namespace
@@ -213,10 +222,10 @@ cudaError_t launch_simt(const Params& p, int D, bool bf16, cudaStream_t s) {
     if (D == 64) return bf16 ? part<64, __nv_bfloat16>(p, s) : part<64, float>(p, s);
     return bf16 ? part<128, __nv_bfloat16>(p, s) : part<128, float>(p, s);
 }
-cudaError_t launch_join(const Params& p, int D, bool bf16, int parts, cudaStream_t s) {
-    if (D == 32) return bf16 ? join<32, __nv_bfloat16>(p, parts, s) : join<32, float>(p, parts, s);
-    if (D == 64) return bf16 ? join<64, __nv_bfloat16>(p, parts, s) : join<64, float>(p, parts, s);
-    return bf16 ? join<128, __nv_bfloat16>(p, parts, s) : join<128, float>(p, parts, s);
+cudaError_t launch_join(const Params& p, int D, bool bf16, int parts, bool beside, cudaStream_t s) {
+    if (D == 32) return bf16 ? join<32, __nv_bfloat16>(p, parts, beside, s) : join<32, float>(p, parts, beside, s);
+    if (D == 64) return bf16 ? join<64, __nv_bfloat16>(p, parts, beside, s) : join<64, float>(p, parts, beside, s);
+    return bf16 ? join<128, __nv_bfloat16>(p, parts, beside, s) : join<128, float>(p, parts, beside, s);
 }
 
 }  // namespace prefix

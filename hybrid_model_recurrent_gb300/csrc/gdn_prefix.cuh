@@ -52,15 +52,18 @@ __host__ __device__ inline void tail_range(int len, int splits, int tile, int s,
 constexpr int kSimtRows = 16;    // query rows of a tile of the FP32-pipe kernel
 constexpr int kSimtKeys = 32;    // tokens of a staged tile
 
+constexpr int kSms = 152;        // multiprocessors of a GB300: the wave that a persistent grid fills
 constexpr int kTcRows = 128;     // query rows of a row tile, and tokens of a tile, of the tensor-core kernel
 constexpr int kTcKeys = 128;
 
 cudaError_t launch_simt(const Params& p, int D, bool bf16, cudaStream_t stream);
 // `row_tiles` (1 or 2) row tiles a CTA.  joined: an item takes the whole prefix and then the whole tail of one request's
-// rows (pre_items = 0); direct: the items write o and lse themselves (one part in all)
+// rows (pre_items = 0); direct: the items write o and lse themselves (one part in all); beside: may run beside the launch
+// before it on the stream, and ends after it
 cudaError_t launch_tc(const Params& p, int D, int row_tiles, int64_t pre_items, int64_t tail_items, bool joined,
-                      bool direct, cudaStream_t stream);
-cudaError_t launch_join(const Params& p, int D, bool bf16, int parts, cudaStream_t stream);
+                      bool direct, bool beside, cudaStream_t stream);
+// `beside`: launched so that it starts up beside the parts (which let it) and waits for them itself
+cudaError_t launch_join(const Params& p, int D, bool bf16, int parts, bool beside, cudaStream_t stream);
 
 }  // namespace prefix
 }  // namespace gdn

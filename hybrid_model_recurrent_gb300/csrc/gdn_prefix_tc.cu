@@ -11,7 +11,8 @@
 //
 // Roles: warps 0 .. 4 NT - 1 softmax (one warpgroup a row tile), then one MMA-issuing thread and one copying thread.
 // K and V tiles arrive by TMA in a ring of ST tiles; with NT = 2 both row tiles use each tile, and one tile's softmax
-// runs beside the other's products.  With NT = 1 two CTAs share a multiprocessor and overlap each other instead.
+// runs beside the other's products.  With NT = 1 two CTAs share a multiprocessor and overlap each other instead.  The
+// grid is one wave and each CTA takes items in turn, the copies running ahead into the next one.
 //
 // A masked token's score is replaced (not multiplied), and value rows past the range are zeroed in shared memory
 // before the product, so nothing that lies past a tail's end reaches a result.
@@ -20,6 +21,7 @@
 // loop, copies and products in flight are waited for, and TMEM is freed.
 #include <cuda_bf16.h>
 
+#include <algorithm>
 #include <cmath>
 
 #include "gdn_prefix.cuh"
@@ -80,9 +82,52 @@ __device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* tm, in
         "l"(reinterpret_cast<uint64_t>(tm)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(smem_addr(bar))
         : "memory");
 }
+// What one item computes: rows [row0, row0 + NT 128) of `rows`, against prefix tokens [lo1, hi1) and tail tokens
+// [lo2, hi2) of request b0, in n_tiles tiles, the first n1 of them the prefix's.
+struct Item {
+    bool stacked;   // rows of all requests (prefix only), else one request's
+    int h, b0, part, len, lo1, hi1, lo2, hi2, rows, row0, n1, n_tiles;
+};
+template <int NT>
+__device__ __forceinline__ Item item_at(const Params& p, int item, int pre_items, bool joined) {
+    Item x;
+    const int nG = p.n * p.G;
+    x.stacked = item < pre_items;
+    x.b0 = x.len = x.lo1 = x.hi1 = x.lo2 = x.hi2 = 0;
+    if (x.stacked) {
+        x.h = item % p.Hkv, item /= p.Hkv;
+        x.rows = p.B * nG;
+        x.row0 = item % p.pre_tiles * (NT * kRows);
+        x.part = item / p.pre_tiles;
+        x.lo1 = x.part * p.pre_chunk;
+        x.hi1 = (int)min((int64_t)x.lo1 + p.pre_chunk, p.prefix_len);
+    } else {
+        item -= pre_items;
+        x.h = item % p.Hkv, item /= p.Hkv;
+        x.rows = nG;
+        x.row0 = item % p.tail_tiles * (NT * kRows), item /= p.tail_tiles;
+        x.b0 = item % p.B;
+        x.part = item / p.B;
+        x.len = p.max_tail > 0 ? min(max(p.tail_len[x.b0], 0), (int)p.max_tail) : 0;
+        if (joined) {
+            x.hi1 = (int)p.prefix_len;
+            // what the tile's last row sees
+            const int last = (min(x.row0 + NT * kRows, x.rows) - 1) / p.G;
+            x.hi2 = min(x.len, max(0, x.len - p.n + last + 1));
+        } else {
+            tail_range(x.len, p.tail_splits, kKeys, x.part, &x.lo2, &x.hi2);
+        }
+        x.part += p.pre_splits;
+    }
+    x.n1 = (x.hi1 - x.lo1 + kKeys - 1) / kKeys;
+    x.n_tiles = x.n1 + (x.hi2 - x.lo2 + kKeys - 1) / kKeys;
+    return x;
+}
+
 template <int D, int NT>
 __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, NT == 1 ? 2 : 1)
-    prefix_tc_kernel(const __grid_constant__ Params p, const int pre_items, const bool joined, const bool direct) {
+    prefix_tc_kernel(const __grid_constant__ Params p, const int pre_items, const int items, const bool joined,
+                     const bool direct) {
     using F = Cfg<D, NT>;
     extern __shared__ unsigned char smem_raw[];
     unsigned char* smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
@@ -91,48 +136,17 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, NT == 1 ? 2 : 1)
     uint64_t* empty = full + F::ST;                                  // [ST] every product that reads it is done
     uint64_t* s_full = empty + F::ST;                                // [NT] S (and every earlier product) done
     uint64_t* p_ready = s_full + NT;                                 // [NT] P written, O rescaled, V's end zeroed
-    uint64_t* q_ready = p_ready + NT;                                // Q tiles written
-    uint64_t* o_full = q_ready + 1;                                  // every product done
+    uint64_t* q_ready = p_ready + NT;                                // an item's Q tiles written
+    uint64_t* o_full = q_ready + 1;                                  // every product of an item done
     uint32_t* tslot = reinterpret_cast<uint32_t*>(o_full + 1);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tslot + 1);
     int* issued = reinterpret_cast<int*>(tslot + 2);                 // tiles whose copy was issued
-    static_assert((2 * F::ST + 2 * NT + 2) * 8 + 12 <= 256, "barrier area");
+    uint64_t* end = reinterpret_cast<uint64_t*>(tslot + 4);          // every product done
+    static_assert((2 * F::ST + 2 * NT + 2) * 8 + 24 <= 256, "barrier area");
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int nG = p.n * p.G;
-    // ---- the item: rows [row0, ..) of `rows`, prefix tokens [lo1, hi1), tail tokens [lo2, hi2) of request b0 ----
-    int item = blockIdx.x;
-    const bool stacked = item < pre_items;   // rows of all requests (prefix only), else one request's
-    int h, b0 = 0, part, len = 0, lo1 = 0, hi1 = 0, lo2 = 0, hi2 = 0;
-    int64_t rows, row0;
-    if (stacked) {
-        h = item % p.Hkv, item /= p.Hkv;
-        rows = (int64_t)p.B * nG;
-        row0 = (int64_t)(item % p.pre_tiles) * (NT * kRows);
-        part = item / p.pre_tiles;
-        lo1 = part * p.pre_chunk;
-        hi1 = (int)min((int64_t)lo1 + p.pre_chunk, p.prefix_len);
-    } else {
-        item -= pre_items;
-        h = item % p.Hkv, item /= p.Hkv;
-        rows = nG;
-        row0 = (int64_t)(item % p.tail_tiles) * (NT * kRows), item /= p.tail_tiles;
-        b0 = item % p.B;
-        part = item / p.B;
-        len = p.max_tail > 0 ? min(max(p.tail_len[b0], 0), (int)p.max_tail) : 0;
-        if (joined) {
-            hi1 = (int)p.prefix_len;
-            // what the tile's last row sees
-            const int last = (int)(min(row0 + NT * kRows, rows) - 1) / p.G;
-            hi2 = min(len, max(0, len - p.n + last + 1));
-        } else {
-            tail_range(len, p.tail_splits, kKeys, part, &lo2, &hi2);
-        }
-        part += p.pre_splits;
-    }
-    const int n1 = (hi1 - lo1 + kKeys - 1) / kKeys;
-    const int n_tiles = n1 + (hi2 - lo2 + kKeys - 1) / kKeys;
     const uint64_t limit = p.wait_limit_ns;
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");   // what follows waits for this grid by itself
 
     if (warp == 0) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(tslot)),
@@ -144,6 +158,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, NT == 1 ? 2 : 1)
         for (int i = 0; i < NT; ++i) mbar_init(&s_full[i], 1), mbar_init(&p_ready[i], 128);
         mbar_init(q_ready, NT * 128);
         mbar_init(o_full, 1);
+        mbar_init(end, 1);
         *abort_flag = 0;
         *issued = 0;
         fence_barrier_init();
@@ -152,238 +167,254 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, NT == 1 ? 2 : 1)
     __syncthreads();
     tc_fence_after();
     const uint32_t tbase = *tslot;
+    auto warp_wait = [&](uint64_t* bar, int parity) { return warp_wait_bar(bar, (uint32_t)parity & 1u, abort_flag, limit); };
 
+    // Every role walks the CTA's items; tiles are counted through all of them (it: tiles so far, K of tile i is copy 2 i,
+    // V copy 2 i + 1), so the copies of the next item begin while the last one is still computed.
     if (warp == NT * 4) {
         // ---- products (the whole warp walks along, one elected lane issues) ----
-        if (n_tiles > 0) {
-            bool ok = warp_wait_bar(q_ready, 0, abort_flag, limit);
-            auto slot_at = [&](int seq) { return sbase + F::kRing + (uint32_t)(seq % F::ST) * F::kTile; };
-            auto scores = [&](int a, int j) {
-                const uint64_t q = tile_desc(sbase + a * F::kTile, false), k = tile_desc(slot_at(2 * j), false);
-                if (elect_one()) {
+        auto slot_at = [&](int seq) { return sbase + F::kRing + (uint32_t)(seq % F::ST) * F::kTile; };
+        auto landed = [&](int seq) { return warp_wait(&full[seq % F::ST], seq / F::ST); };
+        auto done = [&](uint64_t* bar) {
+            if (elect_one()) umma_commit(bar);
+        };
+        auto scores = [&](int a, int i) {
+            const uint64_t q = tile_desc(sbase + a * F::kTile, false), k = tile_desc(slot_at(2 * i), false);
+            if (elect_one()) {
 #pragma unroll
-                    for (int i = 0; i < D / 16; ++i)
-                        umma_ss(tbase + a * 128, cols_step(q, i), cols_step(k, i), idesc(kKeys, false, false), i > 0);
-                    umma_commit(&s_full[a]);
-                }
-            };
-            auto values = [&](int a, int j) {
-                const uint64_t v = tile_desc(slot_at(2 * j + 1), true);
-                if (elect_one()) {
-#pragma unroll
-                    for (int i = 0; i < kKeys / 16; ++i)
-                        umma_ts(tbase + F::kO + a * D, tbase + a * 128 + 8 * i, rows_step(v, i), idesc(D, false, true),
-                                j > 0 || i > 0);
-                }
-            };
-            auto done = [&](uint64_t* bar) {
-                if (elect_one()) umma_commit(bar);
-            };
-            if (ok) ok = warp_wait_bar(&full[0], 0, abort_flag, limit);
-            if (ok) {
-#pragma unroll
-                for (int a = 0; a < NT; ++a) scores(a, 0);
-                done(&empty[0]);
+                for (int s = 0; s < D / 16; ++s)
+                    umma_ss(tbase + a * 128, cols_step(q, s), cols_step(k, s), idesc(kKeys, false, false), s > 0);
+                umma_commit(&s_full[a]);
+                if (a == NT - 1) umma_commit(&empty[2 * i % F::ST]);
             }
-            for (int j = 0; ok && j < n_tiles; ++j) {
-                const int vs = 2 * j + 1, ks = 2 * j + 2;
-                ok = warp_wait_bar(&full[vs % F::ST], (uint32_t)((vs / F::ST) & 1), abort_flag, limit);
+        };
+        bool ok = true;
+        int it = 0, nth = 0;
+        for (int item = blockIdx.x; ok && item < items; item += gridDim.x) {
+            const int n = item_at<NT>(p, item, pre_items, joined).n_tiles;
+            if (n == 0) continue;
+            ok = warp_wait(q_ready, nth) && landed(2 * it);
+            if (!ok) break;
+#pragma unroll
+            for (int a = 0; a < NT; ++a) scores(a, it);
+            for (int j = 0; ok && j < n; ++j) {
+                const int i = it + j, vs = 2 * i + 1;
+                ok = landed(vs);
 #pragma unroll
                 for (int a = 0; a < NT; ++a) {
-                    ok = ok && warp_wait_bar(&p_ready[a], (uint32_t)(j & 1), abort_flag, limit);
+                    ok = ok && warp_wait(&p_ready[a], i);
                     if (!ok) break;
                     tc_fence_after();
-                    values(a, j);
-                    if (a == NT - 1) done(&empty[vs % F::ST]);
-                    if (j + 1 < n_tiles) {
-                        if (a == 0) ok = warp_wait_bar(&full[ks % F::ST], (uint32_t)((ks / F::ST) & 1), abort_flag, limit);
+                    const uint64_t v = tile_desc(slot_at(vs), true);
+                    if (elect_one()) {
+#pragma unroll
+                        for (int s = 0; s < kKeys / 16; ++s)
+                            umma_ts(tbase + F::kO + a * D, tbase + a * 128 + 8 * s, rows_step(v, s), idesc(D, false, true),
+                                    j > 0 || s > 0);
+                        if (a == NT - 1) umma_commit(&empty[vs % F::ST]);
+                    }
+                    if (j + 1 < n) {
+                        if (a == 0) ok = landed(2 * i + 2);
                         if (!ok) break;
-                        scores(a, j + 1);
-                        if (a == NT - 1) done(&empty[ks % F::ST]);
+                        scores(a, i + 1);
                     }
                 }
             }
-            done(o_full);   // also after giving up: the end waits for the products in flight
+            if (!ok) break;
+            done(o_full);
+            it += n, ++nth;
         }
+        done(end);   // also after giving up: the end waits for the products in flight
     } else if (warp == NT * 4 + 1) {
-        // ---- copies: K_0, V_0, K_1, V_1, ... ----
+        // ---- copies ----
         if (lane == 0) {
-            for (int seq = 0; seq < 2 * n_tiles; ++seq) {
-                const int s = seq % F::ST, j = seq >> 1;
-                if (p.stall_after >= 0 && j >= p.stall_after) break;   // testing hook
-                if (seq >= F::ST && !wait_bar(&empty[s], (uint32_t)((seq / F::ST - 1) & 1), abort_flag, limit)) break;
-                unsigned char* dst = smem + F::kRing + s * F::kTile;
-                mbar_arrive_expect_tx(&full[s], F::kTile);
-                const bool v = seq & 1;
+            bool ok = true;
+            int seq = 0;
+            for (int item = blockIdx.x; ok && item < items; item += gridDim.x) {
+                const Item x = item_at<NT>(p, item, pre_items, joined);
+                for (int c = 0; c < 2 * x.n_tiles; ++c, ++seq) {
+                    const int s = seq % F::ST, j = c >> 1;
+                    ok = !(p.stall_after >= 0 && j >= p.stall_after) &&   // testing hook
+                         (seq < F::ST || wait_bar(&empty[s], (uint32_t)((seq / F::ST - 1) & 1), abort_flag, limit));
+                    if (!ok) break;
+                    unsigned char* dst = smem + F::kRing + s * F::kTile;
+                    mbar_arrive_expect_tx(&full[s], F::kTile);
+                    const bool v = c & 1;
 #pragma unroll
-                for (int c = 0; c < D / 64; ++c) {
-                    if (j < n1)
-                        tma_load_3d(dst + c * 16384, v ? &p.tm_vp : &p.tm_kp, c * 64, h, lo1 + j * kKeys, &full[s]);
-                    else
-                        tma_load_4d(dst + c * 16384, v ? &p.tm_vt : &p.tm_kt, c * 64, h, lo2 + (j - n1) * kKeys, b0, &full[s]);
+                    for (int k = 0; k < D / 64; ++k) {
+                        if (j < x.n1)
+                            tma_load_3d(dst + k * 16384, v ? &p.tm_vp : &p.tm_kp, k * 64, x.h, x.lo1 + j * kKeys, &full[s]);
+                        else
+                            tma_load_4d(dst + k * 16384, v ? &p.tm_vt : &p.tm_kt, k * 64, x.h, x.lo2 + (j - x.n1) * kKeys, x.b0,
+                                        &full[s]);
+                    }
+                    *issued = seq + 1;
                 }
-                *issued = seq + 1;
             }
         }
     } else {
         // ---- softmax of row tile a; this thread's row ----
         const int a = warp >> 2, r = tid & 127;
-        const int64_t R = row0 + a * kRows + r;
-        const bool valid = R < rows;
-        const int b = stacked ? (int)(R / nG) : b0, e = (int)(R % nG), qi = e / p.G, head = h * p.G + e % p.G;
-        const int vis2 = min(hi2, max(0, len - p.n + qi + 1));   // tail tokens that this row sees end here
-        const int64_t at = ((int64_t)b * p.n + qi) * p.Hq + head;
         const uint32_t trow = tbase + ((uint32_t)(32 * (warp & 3)) << 16);
-        const bool busy = __any_sync(0xffffffffu, valid);   // a warp without rows only keeps the barriers going
-        // Q; negated where the scale is negative, so that a maximum of scores is one of products
-        {
-            const bool neg = p.scale_log2 < 0.f;
-            const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(p.q) + (valid ? b * p.q_sb + qi * p.q_sn + head * p.q_sh : 0);
-            unsigned char* dst = smem + a * F::kTile;
-#pragma unroll
-            for (int c = 0; c < D / 8; ++c) {
-                uint4 x = valid ? *reinterpret_cast<const uint4*>(src + 8 * c) : make_uint4(0, 0, 0, 0);
-                if (neg) x.x ^= 0x80008000u, x.y ^= 0x80008000u, x.z ^= 0x80008000u, x.w ^= 0x80008000u;
-                *reinterpret_cast<uint4*>(dst + (c >> 3) * 16384 + sw128(r, (c & 7) * 8)) = x;
-            }
-            proxy_fence();
-            mbar_arrive(q_ready);
-        }
         // (a scale of 0 as the smallest normal number: every weight is 1, and a hidden token's -infinity stays that)
         const float scale = fmaxf(fabsf(p.scale_log2), 1.17549435e-38f);
-        float m = -INFINITY, l = 0.f;
+        const int nG = p.n * p.G;
+        const int64_t all = (int64_t)p.B * p.n * p.Hq;
         bool ok = true;
-        for (int j = 0; j < n_tiles; ++j) {
-            const int t0 = j < n1 ? lo1 + j * kKeys : lo2 + (j - n1) * kKeys;
-            if (!warp_wait_bar(&s_full[a], (uint32_t)(j & 1), abort_flag, limit)) {
-                ok = false;
-                break;
-            }
-            tc_fence_after();
-            if (busy) {
-                // The scores are read twice, for the maximum and for the weights: 64 at a time leave room in the 168
-                // registers that 10 warps (or two CTAs of 6) may use; all 128 held at once spilled 300 bytes.
-                const int seen = valid ? (j < n1 ? hi1 : vis2) - t0 : kKeys;
-                const bool hide = __any_sync(0xffffffffu, seen < kKeys);
-                auto load = [&](int half, float (&x0)[32], float (&x1)[32]) {
-                    tmem_ld32x2(trow + a * 128 + 64 * half, trow + a * 128 + 64 * half + 32, x0, x1);
-                    if (hide) {
+        int it = 0, nth = 0;
+        for (int item = blockIdx.x; ok && item < items; item += gridDim.x) {
+            const Item x = item_at<NT>(p, item, pre_items, joined);
+            const int R = x.row0 + a * kRows + r;
+            const bool valid = R < x.rows;
+            const int b = x.stacked ? R / nG : x.b0, e = R % nG, qi = e / p.G, head = x.h * p.G + e % p.G;
+            const int vis2 = min(x.hi2, max(0, x.len - p.n + qi + 1));   // tail tokens that this row sees end here
+            const int64_t at = ((int64_t)b * p.n + qi) * p.Hq + head;
+            const bool busy = __any_sync(0xffffffffu, valid);   // a warp without rows only keeps the barriers going
+            // Q, its tile free since the last item's last scores; negated where the scale is negative, so that a maximum of
+            // scores is one of products
+            if (x.n_tiles > 0) {
+                const bool neg = p.scale_log2 < 0.f;
+                const __nv_bfloat16* src =
+                    static_cast<const __nv_bfloat16*>(p.q) + (valid ? b * p.q_sb + qi * p.q_sn + head * p.q_sh : 0);
+                unsigned char* dst = smem + a * F::kTile;
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) {
-                            if (64 * half + i >= seen) x0[i] = -INFINITY;
-                            if (64 * half + 32 + i >= seen) x1[i] = -INFINITY;
-                        }
-                    }
-                };
-                float t[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-                for (int half = 0; half < 2; ++half) {
-                    float x0[32], x1[32];
-                    load(half, x0, x1);
-#pragma unroll
-                    for (int i = 0; i < 32; i += 2) {
-                        t[0] = fmaxf(t[0], x0[i]), t[1] = fmaxf(t[1], x0[i + 1]);
-                        t[2] = fmaxf(t[2], x1[i]), t[3] = fmaxf(t[3], x1[i + 1]);
-                    }
-                }
-                float top = fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3]));
-                top *= scale;
-                const bool rise = top > m + kRise || m == -INFINITY;
-                if (__any_sync(0xffffffffu, rise)) {
-                    const float mn = rise ? fmaxf(m, top) : m;
-                    const float f = mn == -INFINITY ? 1.f : ex2(m - mn);
-                    m = mn;
-                    l *= f;
-                    if (j > 0) {   // every earlier product into O is done: s_full came after them
-#pragma unroll
-                        for (int c = 0; c < D / 32; ++c) {
-                            float o[32];
-                            tmem_ld32(trow + F::kO + a * D + 32 * c, o);
-#pragma unroll
-                            for (int i = 0; i < 32; ++i) o[i] *= f;
-                            tmem_st32(trow + F::kO + a * D + 32 * c, o);
-                        }
-                    }
-                }
-                const float base = m == -INFINITY ? 0.f : m;
-                float sum[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                for (int half = 0; half < 2; ++half) {
-                    float x0[32], x1[32];
-                    load(half, x0, x1);
-                    uint32_t w0[16], w1[16];
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        const float e0 = ex2(fmaf(x0[2 * i], scale, -base)), e1 = ex2(fmaf(x0[2 * i + 1], scale, -base));
-                        const float e2 = ex2(fmaf(x1[2 * i], scale, -base)), e3 = ex2(fmaf(x1[2 * i + 1], scale, -base));
-                        sum[0] += e0, sum[1] += e1, sum[2] += e2, sum[3] += e3;
-                        w0[i] = pack2(e0, e1), w1[i] = pack2(e2, e3);
-                    }
-                    tmem_st16(trow + a * 128 + 32 * half, w0);
-                    tmem_st16(trow + a * 128 + 32 * half + 16, w1);
-                }
-                l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-                tmem_st_wait();
-            }
-            if (a == 0 && j >= n1 && t0 + kKeys > hi2) {
-                // the tail's last tile: zero the value rows past the range
-                const int vs = 2 * j + 1;
-                if (!warp_wait_bar(&full[vs % F::ST], (uint32_t)((vs / F::ST) & 1), abort_flag, limit)) {
-                    ok = false;
-                    break;
-                }
-                if (r >= hi2 - t0) {
-                    unsigned char* v = smem + F::kRing + (vs % F::ST) * F::kTile + r * 128;
-#pragma unroll
-                    for (int c = 0; c < D / 64; ++c)
-#pragma unroll
-                        for (int i = 0; i < 8; ++i)
-                            *reinterpret_cast<uint4*>(v + c * 16384 + 16 * i) = make_uint4(0, 0, 0, 0);
+                for (int c = 0; c < D / 8; ++c) {
+                    uint4 y = valid ? *reinterpret_cast<const uint4*>(src + 8 * c) : make_uint4(0, 0, 0, 0);
+                    if (neg) y.x ^= 0x80008000u, y.y ^= 0x80008000u, y.z ^= 0x80008000u, y.w ^= 0x80008000u;
+                    *reinterpret_cast<uint4*>(dst + (c >> 3) * 16384 + sw128(r, (c & 7) * 8)) = y;
                 }
                 proxy_fence();
+                mbar_arrive(q_ready);
             }
-            tc_fence_before();
-            mbar_arrive(&p_ready[a]);
-        }
-        if (n_tiles > 0 && ok) ok = warp_wait_bar(o_full, 0, abort_flag, limit);
-        ok = ok && *abort_flag == 0;
-        ok = __all_sync(0xffffffffu, ok);
-        if (ok && busy) {
-            tc_fence_after();
+            float m = -INFINITY, l = 0.f;
+            for (int j = 0; j < x.n_tiles; ++j, ++it) {
+                const int t0 = j < x.n1 ? x.lo1 + j * kKeys : x.lo2 + (j - x.n1) * kKeys;
+                ok = warp_wait(&s_full[a], it);
+                if (!ok) break;
+                tc_fence_after();
+                if (busy) {
+                    // The scores are read twice, for the maximum and for the weights: 64 at a time leave room in the 168
+                    // registers that 10 warps (or two CTAs of 6) may use; all 128 held at once spilled 300 bytes.
+                    const int seen = valid ? (j < x.n1 ? x.hi1 : vis2) - t0 : kKeys;
+                    const bool hide = __any_sync(0xffffffffu, seen < kKeys);
+                    auto load = [&](int half, float (&x0)[32], float (&x1)[32]) {
+                        tmem_ld32x2(trow + a * 128 + 64 * half, trow + a * 128 + 64 * half + 32, x0, x1);
+                        if (hide) {
+#pragma unroll
+                            for (int i = 0; i < 32; ++i) {
+                                if (64 * half + i >= seen) x0[i] = -INFINITY;
+                                if (64 * half + 32 + i >= seen) x1[i] = -INFINITY;
+                            }
+                        }
+                    };
+                    float t[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                    for (int half = 0; half < 2; ++half) {
+                        float x0[32], x1[32];
+                        load(half, x0, x1);
+#pragma unroll
+                        for (int i = 0; i < 32; i += 2) {
+                            t[0] = fmaxf(t[0], x0[i]), t[1] = fmaxf(t[1], x0[i + 1]);
+                            t[2] = fmaxf(t[2], x1[i]), t[3] = fmaxf(t[3], x1[i + 1]);
+                        }
+                    }
+                    float top = fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3]));
+                    top *= scale;
+                    const bool rise = top > m + kRise || m == -INFINITY;
+                    if (__any_sync(0xffffffffu, rise)) {
+                        const float mn = rise ? fmaxf(m, top) : m;
+                        const float f = mn == -INFINITY ? 1.f : ex2(m - mn);
+                        m = mn;
+                        l *= f;
+                        if (j > 0) {   // every earlier product into O is done: s_full came after them
+#pragma unroll
+                            for (int c = 0; c < D / 32; ++c) {
+                                float o[32];
+                                tmem_ld32(trow + F::kO + a * D + 32 * c, o);
+#pragma unroll
+                                for (int i = 0; i < 32; ++i) o[i] *= f;
+                                tmem_st32(trow + F::kO + a * D + 32 * c, o);
+                            }
+                        }
+                    }
+                    const float base = m == -INFINITY ? 0.f : m;
+                    float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                    for (int half = 0; half < 2; ++half) {
+                        float x0[32], x1[32];
+                        load(half, x0, x1);
+                        uint32_t w0[16], w1[16];
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) {
+                            const float e0 = ex2(fmaf(x0[2 * i], scale, -base)), e1 = ex2(fmaf(x0[2 * i + 1], scale, -base));
+                            const float e2 = ex2(fmaf(x1[2 * i], scale, -base)), e3 = ex2(fmaf(x1[2 * i + 1], scale, -base));
+                            sum[0] += e0, sum[1] += e1, sum[2] += e2, sum[3] += e3;
+                            w0[i] = pack2(e0, e1), w1[i] = pack2(e2, e3);
+                        }
+                        tmem_st16(trow + a * 128 + 32 * half, w0);
+                        tmem_st16(trow + a * 128 + 32 * half + 16, w1);
+                    }
+                    l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+                    tmem_st_wait();
+                }
+                if (a == 0 && j >= x.n1 && t0 + kKeys > x.hi2) {
+                    // the tail's last tile: zero the value rows past the range
+                    const int vs = 2 * it + 1;
+                    ok = warp_wait(&full[vs % F::ST], vs / F::ST);
+                    if (!ok) break;
+                    if (r >= x.hi2 - t0) {
+                        unsigned char* v = smem + F::kRing + (vs % F::ST) * F::kTile + r * 128;
+#pragma unroll
+                        for (int c = 0; c < D / 64; ++c)
+#pragma unroll
+                            for (int i = 0; i < 8; ++i)
+                                *reinterpret_cast<uint4*>(v + c * 16384 + 16 * i) = make_uint4(0, 0, 0, 0);
+                    }
+                    proxy_fence();
+                }
+                tc_fence_before();
+                mbar_arrive(&p_ready[a]);
+            }
+            if (!ok) break;
+            if (x.n_tiles > 0) {
+                ok = warp_wait(o_full, nth++);
+                if (!ok) break;
+                tc_fence_after();
+            }
+            if (!busy) continue;
             const bool some = l != 0.f;
             const float inv = some ? 1.f / l : 0.f;
-            if (valid && !direct) p.part_ml[part * ((int64_t)p.B * p.n * p.Hq) + at] = make_float2(m, l);
+            if (valid && !direct) p.part_ml[x.part * all + at] = make_float2(m, l);
             if (valid && direct && p.lse) p.lse[at] = some ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
-            if (n_tiles > 0 || direct) {
+            if (x.n_tiles == 0 && !direct) continue;
+#pragma unroll 1
+            for (int c = 0; c < D / 32; ++c) {
+                float o[32];
+                if (x.n_tiles > 0) {
+                    tmem_ld32(trow + F::kO + a * D + 32 * c, o);
+                } else {
 #pragma unroll
-                for (int c = 0; c < D / 32; ++c) {
-                    float o[32];
-                    if (n_tiles > 0) {
-                        tmem_ld32(trow + F::kO + a * D + 32 * c, o);
-                    } else {
+                    for (int i = 0; i < 32; ++i) o[i] = 0.f;
+                }
+                if (valid && direct) {
+                    __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.o) + at * D + 32 * c;
+                    const bool wide = (reinterpret_cast<uintptr_t>(p.o) & 31) == 0;
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) o[i] = 0.f;
+                    for (int i = 0; i < 32; i += 16) {
+                        uint32_t u[8];
+#pragma unroll
+                        for (int k = 0; k < 8; ++k)
+                            u[k] = some ? pack2(o[i + 2 * k] * inv, o[i + 2 * k + 1] * inv) : 0u;
+                        store32(dst + i, u, wide);
                     }
-                    if (valid && direct) {
-                        __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.o) + at * D + 32 * c;
-                        const bool wide = (reinterpret_cast<uintptr_t>(p.o) & 31) == 0;
+                } else if (valid) {
+                    float* dst = p.part_o + (x.part * all + at) * D + 32 * c;
 #pragma unroll
-                        for (int i = 0; i < 32; i += 16) {
-                            uint32_t u[8];
+                    for (int i = 0; i < 32; i += 8) {
+                        uint32_t u[8];
 #pragma unroll
-                            for (int k = 0; k < 8; ++k)
-                                u[k] = some ? pack2(o[i + 2 * k] * inv, o[i + 2 * k + 1] * inv) : 0u;
-                            store32(dst + i, u, wide);
-                        }
-                    } else if (valid) {
-                        float* dst = p.part_o + (part * ((int64_t)p.B * p.n * p.Hq) + at) * D + 32 * c;
-#pragma unroll
-                        for (int i = 0; i < 32; i += 8) {
-                            uint32_t u[8];
-#pragma unroll
-                            for (int k = 0; k < 8; ++k) u[k] = __float_as_uint(o[i + k]);
-                            store32(dst + i, u, true);
-                        }
+                        for (int k = 0; k < 8; ++k) u[k] = __float_as_uint(o[i + k]);
+                        store32(dst + i, u, true);
                     }
                 }
             }
@@ -393,12 +424,17 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, NT == 1 ? 2 : 1)
     // ---- leave only with no copy and no product still writing into this CTA's shared memory or TMEM ----
     tc_fence_before();
     __syncthreads();
-    if (tid == 0 && *abort_flag) {
-        const uint64_t drain = limit > kDrainLimitNs ? limit : kDrainLimitNs;
-        for (int seq = max(0, *issued - F::ST); seq < *issued; ++seq)
-            tc::drain_phase(&full[seq % F::ST], (uint32_t)((seq / F::ST) & 1), drain);
-        tc::drain_phase(o_full, 0, drain);
-        atomicOr(p.status, STATUS_TIMEOUT);
+    if (tid == 0) {
+        if (*abort_flag) {
+            const uint64_t drain = limit > kDrainLimitNs ? limit : kDrainLimitNs;
+            for (int seq = max(0, *issued - F::ST); seq < *issued; ++seq)
+                tc::drain_phase(&full[seq % F::ST], (uint32_t)((seq / F::ST) & 1), drain);
+            tc::drain_phase(end, 0, drain);
+            atomicOr(p.status, STATUS_TIMEOUT);
+        }
+        // When this grid was started beside the one before it (the other parts of the same call), it ends after that one,
+        // so that the join, which waits for this grid alone, finds both.
+        asm volatile("griddepcontrol.wait;" ::: "memory");
     }
     __syncthreads();
     tc_fence_after();
@@ -407,29 +443,40 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, NT == 1 ? 2 : 1)
 }
 
 template <int D, int NT>
-cudaError_t launch(const Params& p, int64_t pre_items, int64_t tail_items, bool joined, bool direct, cudaStream_t s) {
+cudaError_t launch(const Params& p, int64_t pre_items, int64_t tail_items, bool joined, bool direct, bool beside,
+                   cudaStream_t s) {
     using F = Cfg<D, NT>;
     if (pre_items + tail_items == 0) return cudaSuccess;
     auto kern = prefix_tc_kernel<D, NT>;
     static std::atomic<int> optin[kMaxOptinDevices];
     const cudaError_t e = smem_optin(reinterpret_cast<const void*>(kern), F::kSmem, optin);
     if (e != cudaSuccess) return e;
-    kern<<<(unsigned)(pre_items + tail_items), F::kThreads, F::kSmem, s>>>(p, (int)pre_items, joined, direct);
-    return cudaGetLastError();
+    const int items = (int)(pre_items + tail_items);
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)std::min(items, kSms * (3 - NT)));
+    cfg.blockDim = dim3(F::kThreads);
+    cfg.dynamicSmemBytes = F::kSmem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = beside ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, kern, p, (int)pre_items, items, joined, direct);
 }
 template <int D>
 cudaError_t launch_d(const Params& p, int row_tiles, int64_t pre_items, int64_t tail_items, bool joined, bool direct,
-                     cudaStream_t s) {
-    return row_tiles == 2 ? launch<D, 2>(p, pre_items, tail_items, joined, direct, s)
-                          : launch<D, 1>(p, pre_items, tail_items, joined, direct, s);
+                     bool beside, cudaStream_t s) {
+    return row_tiles == 2 ? launch<D, 2>(p, pre_items, tail_items, joined, direct, beside, s)
+                          : launch<D, 1>(p, pre_items, tail_items, joined, direct, beside, s);
 }
 
 }  // namespace
 
 cudaError_t launch_tc(const Params& p, int D, int row_tiles, int64_t pre_items, int64_t tail_items, bool joined,
-                      bool direct, cudaStream_t s) {
-    return D == 64 ? launch_d<64>(p, row_tiles, pre_items, tail_items, joined, direct, s)
-                   : launch_d<128>(p, row_tiles, pre_items, tail_items, joined, direct, s);
+                      bool direct, bool beside, cudaStream_t s) {
+    return D == 64 ? launch_d<64>(p, row_tiles, pre_items, tail_items, joined, direct, beside, s)
+                   : launch_d<128>(p, row_tiles, pre_items, tail_items, joined, direct, beside, s);
 }
 
 }  // namespace prefix
