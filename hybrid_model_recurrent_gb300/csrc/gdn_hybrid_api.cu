@@ -285,6 +285,7 @@ struct PrefixPlan {
     bool tc, joined;
     int pre_rt, tail_rt;   // tensor cores: row tiles of a CTA
     int pre_splits, pre_chunk, tail_splits, pre_tiles, tail_tiles;
+    int groups;            // groups of 32 stacked rows of a key/value head
     int64_t rows;          // query rows of all heads
     size_t ml_off, o_off, total;
     int parts() const { return pre_splits + tail_splits; }
@@ -337,6 +338,7 @@ PrefixPlan plan_prefix(const gdn_prefix_problem& f) {
     PrefixPlan pl{};
     pl.rows = (int64_t)f.batch * f.num_queries * f.num_q_heads;
     const int64_t group = f.num_q_heads / f.num_kv_heads, own = f.num_queries * group, stacked = own * f.batch;
+    pl.groups = (int)ceil_div(stacked, 32);
     pl.tc = f.dtype == GDN_BF16 && f.head_dim >= 64;
     pl.pre_rt = pl.tail_rt = 1;
     const int64_t part_bytes = pl.rows * (f.head_dim * 4 + 8) * 2;
@@ -378,8 +380,9 @@ PrefixPlan plan_prefix(const gdn_prefix_problem& f) {
     const int64_t parts = pl.parts();
     if (parts == 0 || (pl.tc && parts == 1)) return pl;
     pl.ml_off = 0;
-    pl.o_off = (size_t)ceil_div(parts * pl.rows * 8, 256) * 256;
-    pl.total = pl.o_off + (size_t)parts * pl.rows * f.head_dim * 4;
+    const int64_t rows = parts * f.num_kv_heads * pl.groups * 32;   // groups of 32 stacked rows
+    pl.o_off = (size_t)rows * 8;
+    pl.total = pl.o_off + (size_t)rows * f.head_dim * 4;
     return pl;
 }
 
@@ -399,7 +402,8 @@ gdn_status prefix_attention(const gdn_prefix_problem* p, const void* q, const vo
     const PrefixPlan pl = plan_prefix(f);
     if (pl.total > 0 && (!scratch || !aligned(scratch, 32) || scratch_bytes < pl.total)) return GDN_ERR_INVALID_ARG;
     const int64_t items = f.num_kv_heads * ((int64_t)pl.pre_splits * pl.pre_tiles + (int64_t)pl.tail_splits * pl.tail_tiles * f.batch);
-    if (items >= (1ll << 31)) return GDN_ERR_UNSUPPORTED;
+    if (items >= (1ll << 31) || (int64_t)f.num_kv_heads * pl.groups * (f.head_dim / 8) >= (1ll << 31))
+        return GDN_ERR_UNSUPPORTED;
 
     auto prm = std::make_unique<gdn::prefix::Params>();
     std::memset(prm.get(), 0, sizeof(gdn::prefix::Params));
@@ -421,7 +425,11 @@ gdn_status prefix_attention(const gdn_prefix_problem* p, const void* q, const vo
     prm->B = f.batch, prm->n = f.num_queries, prm->Hq = f.num_q_heads, prm->Hkv = f.num_kv_heads;
     prm->G = f.num_q_heads / f.num_kv_heads;
     prm->pre_splits = pl.pre_splits, prm->pre_chunk = pl.pre_chunk, prm->tail_splits = pl.tail_splits;
-    prm->pre_tiles = pl.pre_tiles, prm->tail_tiles = pl.tail_tiles;
+    prm->pre_tiles = pl.pre_tiles, prm->tail_tiles = pl.tail_tiles, prm->groups = pl.groups;
+    prm->by_hkv.set(f.num_kv_heads), prm->by_b.set(f.batch), prm->by_g.set(prm->G);
+    prm->by_ng.set((uint32_t)(f.num_queries * prm->G));
+    prm->by_pre_tiles.set(std::max(pl.pre_tiles, 1)), prm->by_tail_tiles.set(std::max(pl.tail_tiles, 1));
+    prm->by_tail_splits.set(std::max(pl.tail_splits, 1));
     const bool bf16 = f.dtype == GDN_BF16;
     const int64_t pre_items = (int64_t)f.num_kv_heads * pl.pre_splits * pl.pre_tiles;
     const int64_t tail_items = items - pre_items;

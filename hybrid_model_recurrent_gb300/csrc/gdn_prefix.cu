@@ -52,7 +52,7 @@ __global__ void __launch_bounds__(128) prefix_part_kernel(const __grid_constant_
         split = item / p.B;
         rows = nG;
         len = min(max(p.tail_len[b0], 0), (int)p.max_tail);
-        tail_range(len, p.tail_splits, KT, split, &lo, &hi);
+        tail_range(p, len, KT, split, &lo, &hi);
         gk = static_cast<const T*>(p.kt) + b0 * p.kt_sb + h * p.kt_sh, ks = p.kt_st;
         gv = static_cast<const T*>(p.vt) + b0 * p.vt_sb + h * p.vt_sh, vs = p.vt_st;
         split += p.pre_splits;
@@ -126,71 +126,85 @@ __global__ void __launch_bounds__(128) prefix_part_kernel(const __grid_constant_
         }
         __syncwarp();
     }
-    const int64_t all = (int64_t)p.B * p.n * p.Hq;
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
         const int64_t row = row0 + warp * 4 + r;
 #pragma unroll
         for (int d = 16; d; d >>= 1) l[r] += __shfl_xor_sync(0xffffffffu, l[r], d);
         if (row >= rows) continue;
-        const int b = pre ? (int)(row / nG) : b0, e = (int)(row % nG);
-        const int64_t at = split * all + ((int64_t)b * p.n + e / p.G) * p.Hq + h * p.G + e % p.G;
-        if (lane == 0) p.part_ml[at] = make_float2(m[r], l[r]);
+        const int stacked = (int)(pre ? row : (int64_t)b0 * nG + row);
+        const int64_t group = part_group(p, split, h, stacked);
+        if (lane == 0) p.part_ml[group * 32 + (stacked & 31)] = make_float2(m[r], l[r]);
 #pragma unroll
-        for (int j = 0; j < CL; ++j) p.part_o[at * D + lane + 32 * j] = acc[r][j];
+        for (int j = 0; j < CL; ++j) p.part_o[(group * D + lane + 32 * j) * 32 + (stacked & 31)] = acc[r][j];
     }
 }
 
-// o = sum_p 2^(m_p - m) o_p / sum_p 2^(m_p - m) l_p: one warp a query row, a lane D/32 columns; bound by reading the
-// parts (from L2).  The lanes hold 32 parts' weights at a time and hand them round, so that the parts' rows are loaded
-// several at once, not each behind its weight.
+// o = sum_p 2^(m_p - m) o_p / sum_p 2^(m_p - m) l_p.  A CTA joins 8 columns of a group of 32 rows, lane = row, whole lines
+// at a time; its 8 warps share the parts and add up in shared memory, so that few rows of many parts are not read one
+// behind the other.  Bound by reading the parts (from L2).
+constexpr int kJoinCols = 8, kJoinWarps = 8;
 template <int D, typename T>
-__global__ void __launch_bounds__(128) prefix_join_kernel(const __grid_constant__ Params p, int parts) {
-    constexpr int CL = D / 32;
-    struct alignas(CL * 4) Row {
-        float x[CL];
-    };
-    const int lane = threadIdx.x & 31;
-    const int64_t row = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
-    const int64_t all = (int64_t)p.B * p.n * p.Hq;
+__global__ void __launch_bounds__(32 * kJoinWarps) prefix_join_kernel(const __grid_constant__ Params p, int parts) {
+    constexpr int CC = kJoinCols, W = kJoinWarps;
+    __shared__ float top[W][32], sum[W][CC + 1][32];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int c0 = blockIdx.x % (D / CC) * CC;
+    const int g = blockIdx.x / (D / CC) % p.groups, h = blockIdx.x / (D / CC) / p.groups;
+    const int nG = p.n * p.G, row = g * 32 + lane;
+    const bool valid = row < p.B * nG;
+    const int64_t step = (int64_t)p.Hkv * p.groups, first = (int64_t)h * p.groups + g;
     asm volatile("griddepcontrol.wait;" ::: "memory");   // the parts (nothing to wait for in a plain launch)
-    if (row >= all) return;
-    float m = -INFINITY, l = 0.f, acc[CL];
-#pragma unroll
-    for (int j = 0; j < CL; ++j) acc[j] = 0.f;
-    for (int s0 = 0; s0 < parts; s0 += 32) {
-        // (an empty part has l = 0 and unwritten values, which are not read; a NaN sum is taken in)
-        const float2 ml = s0 + lane < parts ? p.part_ml[(s0 + lane) * all + row] : make_float2(-INFINITY, 0.f);
-        float top = ml.y != 0.f ? ml.x : -INFINITY;
-#pragma unroll
-        for (int d = 16; d; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
-        const float mn = fmaxf(m, top);
-        const float base = mn == -INFINITY ? 0.f : mn;
-        const float w = ml.y != 0.f ? exp2f(ml.x - base) : 0.f, f = exp2f(m - base);
-        m = mn;
-        l = l * f;
-#pragma unroll
-        for (int j = 0; j < CL; ++j) acc[j] *= f;
-        float lw = ml.y != 0.f ? w * ml.y : 0.f;
-#pragma unroll
-        for (int d = 16; d; d >>= 1) lw += __shfl_xor_sync(0xffffffffu, lw, d);
-        l += lw;
-        const unsigned live = __ballot_sync(0xffffffffu, ml.y != 0.f);
-        const int n = min(32, parts - s0);
+    const float2* ml = p.part_ml + first * 32 + lane;
+    float m = -INFINITY;
 #pragma unroll 4
-        for (int i = 0; i < n; ++i) {
-            const float wi = __shfl_sync(0xffffffffu, w, i);
-            Row r{};
-            if (live >> i & 1) r = *reinterpret_cast<const Row*>(p.part_o + ((s0 + i) * all + row) * D + lane * CL);
+    for (int s = warp; s < parts; s += W) {
+        const float2 x = valid ? ml[s * step * 32] : make_float2(0.f, 0.f);
+        if (x.y != 0.f) m = fmaxf(m, x.x);   // (a NaN sum counts as one)
+    }
+    top[warp][lane] = m;
+    __syncthreads();
 #pragma unroll
-            for (int j = 0; j < CL; ++j) acc[j] = fmaf(wi, r.x[j], acc[j]);
+    for (int k = 0; k < W; ++k) m = fmaxf(m, top[k][lane]);
+    const float base = m == -INFINITY ? 0.f : m;
+    float l = 0.f, acc[CC];
+#pragma unroll
+    for (int j = 0; j < CC; ++j) acc[j] = 0.f;
+#pragma unroll 2
+    for (int s = warp; s < parts; s += W) {
+        const float2 x = valid ? ml[s * step * 32] : make_float2(0.f, 0.f);
+        const float* src = p.part_o + ((s * step + first) * D + c0) * 32 + lane;
+        const bool some = x.y != 0.f;   // an empty part's values were not written
+        const float w = some ? exp2f(x.x - base) : 0.f;
+        l += some ? w * x.y : 0.f;
+#pragma unroll
+        for (int j = 0; j < CC; ++j) {
+            const float y = some ? src[32 * j] : 0.f;
+            acc[j] = fmaf(w, y, acc[j]);
         }
     }
-    const float inv = l == 0.f ? 0.f : 1.f / l;
-    T* o = static_cast<T*>(p.o) + row * D + lane * CL;
 #pragma unroll
-    for (int j = 0; j < CL; ++j) put(o + j, acc[j] * inv);
-    if (p.lse && lane == 0) p.lse[row] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
+    for (int j = 0; j < CC; ++j) sum[warp][j][lane] = acc[j];
+    sum[warp][CC][lane] = l;
+    __syncthreads();
+    if (warp != 0 || !valid) return;
+#pragma unroll
+    for (int k = 1; k < W; ++k) {
+        l += sum[k][CC][lane];
+#pragma unroll
+        for (int j = 0; j < CC; ++j) acc[j] += sum[k][j][lane];
+    }
+    int e, k;
+    const int b = p.by_ng.divmod(row, &e), i = p.by_g.divmod(e, &k);
+    const int64_t at = ((int64_t)b * p.n + i) * p.Hq + h * p.G + k;
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    struct alignas(16) Out {
+        T x[CC];
+    } out;
+#pragma unroll
+    for (int j = 0; j < CC; ++j) put(&out.x[j], acc[j] * inv);
+    *reinterpret_cast<Out*>(static_cast<T*>(p.o) + at * D + c0) = out;
+    if (p.lse && c0 == 0) p.lse[at] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
 }
 
 template <int D, typename T>
@@ -202,10 +216,9 @@ cudaError_t part(const Params& p, cudaStream_t s) {
 }
 template <int D, typename T>
 cudaError_t join(const Params& p, int parts, bool beside, cudaStream_t s) {
-    const int64_t rows = (int64_t)p.B * p.n * p.Hq;
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((unsigned)((rows + 3) / 4));
-    cfg.blockDim = dim3(128);
+    cfg.gridDim = dim3((unsigned)(p.Hkv * p.groups * (D / kJoinCols)));
+    cfg.blockDim = dim3(32 * kJoinWarps);
     cfg.stream = s;
     cudaLaunchAttribute attr{};
     attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;

@@ -64,7 +64,9 @@ struct Cfg {
     static constexpr int kRing = NT * kTile;                               // after the Q tiles
     static constexpr int kBar = kRing + ST * kTile;
     static constexpr int kSmem = kBar + 256 + 1024;
-    static constexpr int kThreads = NT * 128 + 64;
+    // softmax warpgroups, then a warp that issues products and one that issues copies; with NT = 2 two idle warps fill up
+    // their warpgroup, which then hands registers to the others
+    static constexpr int kThreads = NT == 2 ? 384 : 192;
     static constexpr int kTmem = NT == 2 ? 512 : 256;
     static constexpr uint32_t kO = NT * 128;                               // TMEM: S of each row tile, then O of each
     static_assert(kSmem <= 232448 / (NT == 1 ? 2 : 1) - (NT == 1 ? 1024 : 0), "shared memory");
@@ -91,34 +93,33 @@ struct Item {
 template <int NT>
 __device__ __forceinline__ Item item_at(const Params& p, int item, int pre_items, bool joined) {
     Item x;
-    const int nG = p.n * p.G;
+    const int nG = (int)p.by_ng.d;
     x.stacked = item < pre_items;
     x.b0 = x.len = x.lo1 = x.hi1 = x.lo2 = x.hi2 = 0;
+    int tile;
     if (x.stacked) {
-        x.h = item % p.Hkv, item /= p.Hkv;
+        item = p.by_hkv.divmod(item, &x.h);
+        x.part = p.by_pre_tiles.divmod(item, &tile);
         x.rows = p.B * nG;
-        x.row0 = item % p.pre_tiles * (NT * kRows);
-        x.part = item / p.pre_tiles;
         x.lo1 = x.part * p.pre_chunk;
         x.hi1 = (int)min((int64_t)x.lo1 + p.pre_chunk, p.prefix_len);
     } else {
-        item -= pre_items;
-        x.h = item % p.Hkv, item /= p.Hkv;
+        item = p.by_hkv.divmod(item - pre_items, &x.h);
+        item = p.by_tail_tiles.divmod(item, &tile);
+        x.part = p.by_b.divmod(item, &x.b0);
         x.rows = nG;
-        x.row0 = item % p.tail_tiles * (NT * kRows), item /= p.tail_tiles;
-        x.b0 = item % p.B;
-        x.part = item / p.B;
         x.len = p.max_tail > 0 ? min(max(p.tail_len[x.b0], 0), (int)p.max_tail) : 0;
         if (joined) {
             x.hi1 = (int)p.prefix_len;
             // what the tile's last row sees
-            const int last = (min(x.row0 + NT * kRows, x.rows) - 1) / p.G;
+            const int last = p.by_g.div(min((tile + 1) * NT * kRows, x.rows) - 1);
             x.hi2 = min(x.len, max(0, x.len - p.n + last + 1));
         } else {
-            tail_range(x.len, p.tail_splits, kKeys, x.part, &x.lo2, &x.hi2);
+            tail_range(p, x.len, kKeys, x.part, &x.lo2, &x.hi2);
         }
         x.part += p.pre_splits;
     }
+    x.row0 = tile * (NT * kRows);
     x.n1 = (x.hi1 - x.lo1 + kKeys - 1) / kKeys;
     x.n_tiles = x.n1 + (x.hi2 - x.lo2 + kKeys - 1) / kKeys;
     return x;
@@ -142,7 +143,8 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, NT == 1 ? 2 : 1)
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tslot + 1);
     int* issued = reinterpret_cast<int*>(tslot + 2);                 // tiles whose copy was issued
     uint64_t* end = reinterpret_cast<uint64_t*>(tslot + 4);          // every product done
-    static_assert((2 * F::ST + 2 * NT + 2) * 8 + 24 <= 256, "barrier area");
+    uint64_t* q_asked = end + 1;                                     // the first item's Q loads are under way
+    static_assert((2 * F::ST + 2 * NT + 2) * 8 + 32 <= 256, "barrier area");
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const uint64_t limit = p.wait_limit_ns;
@@ -153,12 +155,17 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, NT == 1 ? 2 : 1)
                      "r"(F::kTmem));
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
     }
+    if (warp == NT * 4 + 1 && lane == 0) {
+        for (const CUtensorMap* tm : {&p.tm_kp, &p.tm_vp, &p.tm_kt, &p.tm_vt})
+            asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(tm)) : "memory");
+    }
     if (tid == 0) {
         for (int i = 0; i < F::ST; ++i) mbar_init(&full[i], 1), mbar_init(&empty[i], 1);
         for (int i = 0; i < NT; ++i) mbar_init(&s_full[i], 1), mbar_init(&p_ready[i], 128);
         mbar_init(q_ready, NT * 128);
         mbar_init(o_full, 1);
         mbar_init(end, 1);
+        mbar_init(q_asked, NT * 128);
         *abort_flag = 0;
         *issued = 0;
         fence_barrier_init();
@@ -169,119 +176,139 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, NT == 1 ? 2 : 1)
     const uint32_t tbase = *tslot;
     auto warp_wait = [&](uint64_t* bar, int parity) { return warp_wait_bar(bar, (uint32_t)parity & 1u, abort_flag, limit); };
 
+    // 384 threads start with 168 registers each (64512 in all): 256 x 200 + 128 x 96 = 63488
+    constexpr bool kKeep = NT == 2;   // a row's 128 scores stay in registers between the maximum and the weights
+
     // Every role walks the CTA's items; tiles are counted through all of them (it: tiles so far, K of tile i is copy 2 i,
     // V copy 2 i + 1), so the copies of the next item begin while the last one is still computed.
-    if (warp == NT * 4) {
-        // ---- products (the whole warp walks along, one elected lane issues) ----
-        auto slot_at = [&](int seq) { return sbase + F::kRing + (uint32_t)(seq % F::ST) * F::kTile; };
-        auto landed = [&](int seq) { return warp_wait(&full[seq % F::ST], seq / F::ST); };
-        auto done = [&](uint64_t* bar) {
-            if (elect_one()) umma_commit(bar);
-        };
-        auto scores = [&](int a, int i) {
-            const uint64_t q = tile_desc(sbase + a * F::kTile, false), k = tile_desc(slot_at(2 * i), false);
-            if (elect_one()) {
+    if (warp >= NT * 4) {
+        if constexpr (kKeep) asm volatile("setmaxnreg.dec.sync.aligned.u32 96;");
+        if (warp == NT * 4) {
+            // ---- products (the whole warp walks along, one elected lane issues) ----
+            auto slot_at = [&](int seq) { return sbase + F::kRing + (uint32_t)(seq % F::ST) * F::kTile; };
+            auto landed = [&](int seq) { return warp_wait(&full[seq % F::ST], seq / F::ST); };
+            auto done = [&](uint64_t* bar) {
+                if (elect_one()) umma_commit(bar);
+            };
+            auto scores = [&](int a, int i) {
+                const uint64_t q = tile_desc(sbase + a * F::kTile, false), k = tile_desc(slot_at(2 * i), false);
+                if (elect_one()) {
 #pragma unroll
-                for (int s = 0; s < D / 16; ++s)
-                    umma_ss(tbase + a * 128, cols_step(q, s), cols_step(k, s), idesc(kKeys, false, false), s > 0);
-                umma_commit(&s_full[a]);
-                if (a == NT - 1) umma_commit(&empty[2 * i % F::ST]);
-            }
-        };
-        bool ok = true;
-        int it = 0, nth = 0;
-        for (int item = blockIdx.x; ok && item < items; item += gridDim.x) {
-            const int n = item_at<NT>(p, item, pre_items, joined).n_tiles;
-            if (n == 0) continue;
-            ok = warp_wait(q_ready, nth) && landed(2 * it);
-            if (!ok) break;
+                    for (int s = 0; s < D / 16; ++s)
+                        umma_ss(tbase + a * 128, cols_step(q, s), cols_step(k, s), idesc(kKeys, false, false), s > 0);
+                    umma_commit(&s_full[a]);
+                    if (a == NT - 1) umma_commit(&empty[2 * i % F::ST]);
+                }
+            };
+            bool ok = true;
+            int it = 0, nth = 0;
+            for (int item = blockIdx.x; ok && item < items; item += gridDim.x) {
+                const int n = item_at<NT>(p, item, pre_items, joined).n_tiles;
+                if (n == 0) continue;
+                ok = warp_wait(q_ready, nth) && landed(2 * it);
+                if (!ok) break;
 #pragma unroll
-            for (int a = 0; a < NT; ++a) scores(a, it);
-            for (int j = 0; ok && j < n; ++j) {
-                const int i = it + j, vs = 2 * i + 1;
-                ok = landed(vs);
+                for (int a = 0; a < NT; ++a) scores(a, it);
+                for (int j = 0; ok && j < n; ++j) {
+                    const int i = it + j, vs = 2 * i + 1;
+                    ok = landed(vs);
 #pragma unroll
-                for (int a = 0; a < NT; ++a) {
-                    ok = ok && warp_wait(&p_ready[a], i);
-                    if (!ok) break;
-                    tc_fence_after();
-                    const uint64_t v = tile_desc(slot_at(vs), true);
-                    if (elect_one()) {
-#pragma unroll
-                        for (int s = 0; s < kKeys / 16; ++s)
-                            umma_ts(tbase + F::kO + a * D, tbase + a * 128 + 8 * s, rows_step(v, s), idesc(D, false, true),
-                                    j > 0 || s > 0);
-                        if (a == NT - 1) umma_commit(&empty[vs % F::ST]);
-                    }
-                    if (j + 1 < n) {
-                        if (a == 0) ok = landed(2 * i + 2);
+                    for (int a = 0; a < NT; ++a) {
+                        ok = ok && warp_wait(&p_ready[a], i);
                         if (!ok) break;
-                        scores(a, i + 1);
+                        tc_fence_after();
+                        const uint64_t v = tile_desc(slot_at(vs), true);
+                        if (elect_one()) {
+#pragma unroll
+                            for (int s = 0; s < kKeys / 16; ++s)
+                                umma_ts(tbase + F::kO + a * D, tbase + a * 128 + 8 * s, rows_step(v, s), idesc(D, false, true),
+                                        j > 0 || s > 0);
+                            if (a == NT - 1) umma_commit(&empty[vs % F::ST]);
+                        }
+                        if (j + 1 < n) {
+                            if (a == 0) ok = landed(2 * i + 2);
+                            if (!ok) break;
+                            scores(a, i + 1);
+                        }
                     }
                 }
+                if (!ok) break;
+                done(o_full);
+                it += n, ++nth;
             }
-            if (!ok) break;
-            done(o_full);
-            it += n, ++nth;
-        }
-        done(end);   // also after giving up: the end waits for the products in flight
-    } else if (warp == NT * 4 + 1) {
-        // ---- copies ----
-        if (lane == 0) {
-            bool ok = true;
-            int seq = 0;
-            for (int item = blockIdx.x; ok && item < items; item += gridDim.x) {
-                const Item x = item_at<NT>(p, item, pre_items, joined);
-                for (int c = 0; c < 2 * x.n_tiles; ++c, ++seq) {
-                    const int s = seq % F::ST, j = c >> 1;
-                    ok = !(p.stall_after >= 0 && j >= p.stall_after) &&   // testing hook
-                         (seq < F::ST || wait_bar(&empty[s], (uint32_t)((seq / F::ST - 1) & 1), abort_flag, limit));
-                    if (!ok) break;
-                    unsigned char* dst = smem + F::kRing + s * F::kTile;
-                    mbar_arrive_expect_tx(&full[s], F::kTile);
-                    const bool v = c & 1;
+            done(end);   // also after giving up: the end waits for the products in flight
+        } else if (warp == NT * 4 + 1) {
+            // ---- copies ----
+            if (lane == 0) {
+                bool ok = true;
+                int seq = 0;   // (the copies of a whole wave, asked for first, keep the Q loads waiting for 5 us)
+                for (int item = blockIdx.x; ok && item < items; item += gridDim.x) {
+                    const Item x = item_at<NT>(p, item, pre_items, joined);
+                    for (int c = 0; c < 2 * x.n_tiles; ++c, ++seq) {
+                        const int s = seq % F::ST, j = c >> 1;
+                        ok = !(p.stall_after >= 0 && j >= p.stall_after) &&   // testing hook
+                             (seq > 0 || wait_bar(q_asked, 0, abort_flag, limit)) &&
+                             (seq < F::ST || wait_bar(&empty[s], (uint32_t)((seq / F::ST - 1) & 1), abort_flag, limit));
+                        if (!ok) break;
+                        unsigned char* dst = smem + F::kRing + s * F::kTile;
+                        mbar_arrive_expect_tx(&full[s], F::kTile);
+                        const bool v = c & 1;
 #pragma unroll
-                    for (int k = 0; k < D / 64; ++k) {
-                        if (j < x.n1)
-                            tma_load_3d(dst + k * 16384, v ? &p.tm_vp : &p.tm_kp, k * 64, x.h, x.lo1 + j * kKeys, &full[s]);
-                        else
-                            tma_load_4d(dst + k * 16384, v ? &p.tm_vt : &p.tm_kt, k * 64, x.h, x.lo2 + (j - x.n1) * kKeys, x.b0,
-                                        &full[s]);
+                        for (int k = 0; k < D / 64; ++k) {
+                            if (j < x.n1)
+                                tma_load_3d(dst + k * 16384, v ? &p.tm_vp : &p.tm_kp, k * 64, x.h, x.lo1 + j * kKeys, &full[s]);
+                            else
+                                tma_load_4d(dst + k * 16384, v ? &p.tm_vt : &p.tm_kt, k * 64, x.h, x.lo2 + (j - x.n1) * kKeys, x.b0,
+                                            &full[s]);
+                        }
+                        *issued = seq + 1;
                     }
-                    *issued = seq + 1;
                 }
             }
         }
     } else {
         // ---- softmax of row tile a; this thread's row ----
+        if constexpr (kKeep) asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
         const int a = warp >> 2, r = tid & 127;
         const uint32_t trow = tbase + ((uint32_t)(32 * (warp & 3)) << 16);
         // (a scale of 0 as the smallest normal number: every weight is 1, and a hidden token's -infinity stays that)
         const float scale = fmaxf(fabsf(p.scale_log2), 1.17549435e-38f);
-        const int nG = p.n * p.G;
-        const int64_t all = (int64_t)p.B * p.n * p.Hq;
-        bool ok = true;
+        const int nG = (int)p.by_ng.d;
+        bool ok = true, first = true;
         int it = 0, nth = 0;
         for (int item = blockIdx.x; ok && item < items; item += gridDim.x) {
             const Item x = item_at<NT>(p, item, pre_items, joined);
             const int R = x.row0 + a * kRows + r;
             const bool valid = R < x.rows;
-            const int b = x.stacked ? R / nG : x.b0, e = R % nG, qi = e / p.G, head = x.h * p.G + e % p.G;
+            int e, g;
+            const int bs = p.by_ng.divmod(R, &e), b = x.stacked ? bs : x.b0;   // (one request's rows are below n G, or invalid)
+            const int qi = p.by_g.divmod(e, &g), head = x.h * p.G + g;
             const int vis2 = min(x.hi2, max(0, x.len - p.n + qi + 1));   // tail tokens that this row sees end here
             const int64_t at = ((int64_t)b * p.n + qi) * p.Hq + head;
             const bool busy = __any_sync(0xffffffffu, valid);   // a warp without rows only keeps the barriers going
             // Q, its tile free since the last item's last scores; negated where the scale is negative, so that a maximum of
             // scores is one of products
             if (x.n_tiles > 0) {
-                const bool neg = p.scale_log2 < 0.f;
-                const __nv_bfloat16* src =
-                    static_cast<const __nv_bfloat16*>(p.q) + (valid ? b * p.q_sb + qi * p.q_sn + head * p.q_sh : 0);
-                unsigned char* dst = smem + a * F::kTile;
+                // a warp loads its own 32 rows, 16 bytes a lane, as many rows at a time as its lanes cover (each lane knows
+                // one row's address)
+                constexpr int kLanes = D / 8, kAtOnce = 32 / kLanes, kLoads = 32 / kAtOnce;
+                const uint32_t flip = p.scale_log2 < 0.f ? 0x80008000u : 0u;
+                const int64_t own = valid ? b * p.q_sb + qi * p.q_sn + head * p.q_sh : -1;
+                const int c = lane % kLanes;
+                uint4 y[kLoads];
 #pragma unroll
-                for (int c = 0; c < D / 8; ++c) {
-                    uint4 y = valid ? *reinterpret_cast<const uint4*>(src + 8 * c) : make_uint4(0, 0, 0, 0);
-                    if (neg) y.x ^= 0x80008000u, y.y ^= 0x80008000u, y.z ^= 0x80008000u, y.w ^= 0x80008000u;
-                    *reinterpret_cast<uint4*>(dst + (c >> 3) * 16384 + sw128(r, (c & 7) * 8)) = y;
+                for (int i = 0; i < kLoads; ++i) {
+                    const int64_t off = __shfl_sync(0xffffffffu, own, i * kAtOnce + lane / kLanes);
+                    y[i] = off >= 0 ? *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.q) + off + 8 * c)
+                                    : make_uint4(0, 0, 0, 0);
+                }
+                if (first) mbar_arrive(q_asked);
+                first = false;
+#pragma unroll
+                for (int i = 0; i < kLoads; ++i) {
+                    const int row = (r & 96) + i * kAtOnce + lane / kLanes;
+                    *reinterpret_cast<uint4*>(smem + a * F::kTile + (c >> 3) * 16384 + row * 128 + (((c & 7) ^ (row & 7)) << 4)) =
+                        make_uint4(y[i].x ^ flip, y[i].y ^ flip, y[i].z ^ flip, y[i].w ^ flip);
                 }
                 proxy_fence();
                 mbar_arrive(q_ready);
@@ -293,33 +320,33 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, NT == 1 ? 2 : 1)
                 if (!ok) break;
                 tc_fence_after();
                 if (busy) {
-                    // The scores are read twice, for the maximum and for the weights: 64 at a time leave room in the 168
-                    // registers that 10 warps (or two CTAs of 6) may use; all 128 held at once spilled 300 bytes.
+                    // With NT = 2 a row's scores stay in registers; with NT = 1 (two CTAs of 6 warps and 168 registers a
+                    // thread) they are read again for the weights.
                     const int seen = valid ? (j < x.n1 ? x.hi1 : vis2) - t0 : kKeys;
                     const bool hide = __any_sync(0xffffffffu, seen < kKeys);
-                    auto load = [&](int half, float (&x0)[32], float (&x1)[32]) {
-                        tmem_ld32x2(trow + a * 128 + 64 * half, trow + a * 128 + 64 * half + 32, x0, x1);
+                    float s[kKeep ? 4 : 2][32];
+                    auto load = [&](int half, float (&s0)[32], float (&s1)[32]) {
+                        tmem_ld32x2(trow + a * 128 + 64 * half, trow + a * 128 + 64 * half + 32, s0, s1);
                         if (hide) {
 #pragma unroll
                             for (int i = 0; i < 32; ++i) {
-                                if (64 * half + i >= seen) x0[i] = -INFINITY;
-                                if (64 * half + 32 + i >= seen) x1[i] = -INFINITY;
+                                if (64 * half + i >= seen) s0[i] = -INFINITY;
+                                if (64 * half + 32 + i >= seen) s1[i] = -INFINITY;
                             }
                         }
                     };
                     float t[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
                     for (int half = 0; half < 2; ++half) {
-                        float x0[32], x1[32];
-                        load(half, x0, x1);
+                        float(&s0)[32] = s[kKeep ? 2 * half : 0], (&s1)[32] = s[kKeep ? 2 * half + 1 : 1];
+                        load(half, s0, s1);
 #pragma unroll
                         for (int i = 0; i < 32; i += 2) {
-                            t[0] = fmaxf(t[0], x0[i]), t[1] = fmaxf(t[1], x0[i + 1]);
-                            t[2] = fmaxf(t[2], x1[i]), t[3] = fmaxf(t[3], x1[i + 1]);
+                            t[0] = fmaxf(fmaxf(t[0], s0[i]), s0[i + 1]);
+                            t[1 + (i & 2)] = fmaxf(fmaxf(t[1 + (i & 2)], s1[i]), s1[i + 1]);
                         }
                     }
-                    float top = fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3]));
-                    top *= scale;
+                    const float top = fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3])) * scale;
                     const bool rise = top > m + kRise || m == -INFINITY;
                     if (__any_sync(0xffffffffu, rise)) {
                         const float mn = rise ? fmaxf(m, top) : m;
@@ -327,7 +354,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, NT == 1 ? 2 : 1)
                         m = mn;
                         l *= f;
                         if (j > 0) {   // every earlier product into O is done: s_full came after them
-#pragma unroll
+#pragma unroll 1
                             for (int c = 0; c < D / 32; ++c) {
                                 float o[32];
                                 tmem_ld32(trow + F::kO + a * D + 32 * c, o);
@@ -338,23 +365,25 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, NT == 1 ? 2 : 1)
                         }
                     }
                     const float base = m == -INFINITY ? 0.f : m;
-                    float sum[4] = {0.f, 0.f, 0.f, 0.f};
+                    const float2 scale2 = make_float2(scale, scale), base2 = make_float2(-base, -base);
+                    float2 sum0 = make_float2(0.f, 0.f), sum1 = sum0;
 #pragma unroll
                     for (int half = 0; half < 2; ++half) {
-                        float x0[32], x1[32];
-                        load(half, x0, x1);
+                        float(&s0)[32] = s[kKeep ? 2 * half : 0], (&s1)[32] = s[kKeep ? 2 * half + 1 : 1];
+                        if (!kKeep) load(half, s0, s1);
                         uint32_t w0[16], w1[16];
 #pragma unroll
                         for (int i = 0; i < 16; ++i) {
-                            const float e0 = ex2(fmaf(x0[2 * i], scale, -base)), e1 = ex2(fmaf(x0[2 * i + 1], scale, -base));
-                            const float e2 = ex2(fmaf(x1[2 * i], scale, -base)), e3 = ex2(fmaf(x1[2 * i + 1], scale, -base));
-                            sum[0] += e0, sum[1] += e1, sum[2] += e2, sum[3] += e3;
-                            w0[i] = pack2(e0, e1), w1[i] = pack2(e2, e3);
+                            float2 e = __ffma2_rn(make_float2(s0[2 * i], s0[2 * i + 1]), scale2, base2);
+                            float2 g = __ffma2_rn(make_float2(s1[2 * i], s1[2 * i + 1]), scale2, base2);
+                            e = make_float2(ex2(e.x), ex2(e.y)), g = make_float2(ex2(g.x), ex2(g.y));
+                            sum0 = __fadd2_rn(sum0, e), sum1 = __fadd2_rn(sum1, g);
+                            w0[i] = pack2(e.x, e.y), w1[i] = pack2(g.x, g.y);
                         }
                         tmem_st16(trow + a * 128 + 32 * half, w0);
                         tmem_st16(trow + a * 128 + 32 * half + 16, w1);
                     }
-                    l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+                    l += (sum0.x + sum0.y) + (sum1.x + sum1.y);
                     tmem_st_wait();
                 }
                 if (a == 0 && j >= x.n1 && t0 + kKeys > x.hi2) {
@@ -384,7 +413,9 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, NT == 1 ? 2 : 1)
             if (!busy) continue;
             const bool some = l != 0.f;
             const float inv = some ? 1.f / l : 0.f;
-            if (valid && !direct) p.part_ml[x.part * all + at] = make_float2(m, l);
+            const int64_t group = part_group(p, x.part, x.h, x.stacked ? R : x.b0 * nG + R);
+            const int in_group = (x.stacked ? R : x.b0 * nG + R) & 31;
+            if (valid && !direct) p.part_ml[group * 32 + in_group] = make_float2(m, l);
             if (valid && direct && p.lse) p.lse[at] = some ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
             if (x.n_tiles == 0 && !direct) continue;
 #pragma unroll 1
@@ -408,14 +439,9 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, NT == 1 ? 2 : 1)
                         store32(dst + i, u, wide);
                     }
                 } else if (valid) {
-                    float* dst = p.part_o + (x.part * all + at) * D + 32 * c;
+                    float* dst = p.part_o + (group * D + 32 * c) * 32 + in_group;
 #pragma unroll
-                    for (int i = 0; i < 32; i += 8) {
-                        uint32_t u[8];
-#pragma unroll
-                        for (int k = 0; k < 8; ++k) u[k] = __float_as_uint(o[i + k]);
-                        store32(dst + i, u, true);
-                    }
+                    for (int i = 0; i < 32; ++i) dst[32 * i] = o[i];
                 }
             }
         }
