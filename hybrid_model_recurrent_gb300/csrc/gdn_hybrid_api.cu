@@ -90,9 +90,9 @@ LinPlan plan_linear(const gdn_linear_problem* p) {
     int64_t longest = 0;
     for (int b = 0; b < B; ++b) longest = std::max(longest, p->cu_seqlens[b + 1] - p->cu_seqlens[b]);
     // The tensor-core kernel rounds the readout's operands to bf16, which a bf16 output hides and an fp32 one does not.
-    pl.tc = p->d_k == 128 && p->d_v == 128 && p->qkv_dtype == GDN_BF16 && p->out_dtype == GDN_BF16;
+    pl.tc = p->d_k >= 64 && p->d_v >= 64 && p->qkv_dtype == GDN_BF16 && p->out_dtype == GDN_BF16;
     // FP32 pipes: CTAs of 64 state rows when that still gives two a multiprocessor, else smaller ones
-    pl.rows_per_cta = pl.tc ? 128 : std::min(64, p->d_v);
+    pl.rows_per_cta = pl.tc ? p->d_v : std::min(64, p->d_v);
     while (!pl.tc && pl.rows_per_cta > 16 && (int64_t)B * p->num_heads * (p->d_v / pl.rows_per_cta) < 2 * kSms) pl.rows_per_cta /= 2;
     const int64_t per_seq = (int64_t)p->num_heads * (p->d_v / pl.rows_per_cta);
     // A scan is sequential, so a call with few long ones leaves multiprocessors idle.  Its scans are then cut into
@@ -251,15 +251,15 @@ gdn_status linear_prefill(const gdn_linear_problem* p, const void* q, const void
     const bool in_bf16 = p->qkv_dtype == GDN_BF16, out_bf16 = p->out_dtype == GDN_BF16;
     if (pl.tc && T > 0) {
         const int Hk = p->num_qk_heads;
-        bool maps = bf16_map(&prm->tm_k, k, 3, {128, Hk, T, 1}, {128, sd.k, 0}, 128) &&
-                    bf16_map(&prm->tm_v, v, 3, {128, H, T, 1}, {128, sd.v, 0}, 128);
+        bool maps = bf16_map(&prm->tm_k, k, 3, {p->d_k, Hk, T, 1}, {p->d_k, sd.k, 0}, 128) &&
+                    bf16_map(&prm->tm_v, v, 3, {p->d_v, H, T, 1}, {p->d_v, sd.v, 0}, 128);
         if (maps && o)
-            maps = bf16_map(&prm->tm_q, q, 3, {128, Hk, T, 1}, {128, sd.q, 0}, 128) &&
-                   bf16_map(&prm->tm_o, o, 3, {128, H, T, 1}, {128, (int64_t)H * 128, 0}, 128);
+            maps = bf16_map(&prm->tm_q, q, 3, {p->d_k, Hk, T, 1}, {p->d_k, sd.q, 0}, 128) &&
+                   bf16_map(&prm->tm_o, o, 3, {p->d_v, H, T, 1}, {p->d_v, (int64_t)H * p->d_v, 0}, 128);
         if (!maps) return GDN_ERR_CUDA;
     }
     auto launch = [&](const gdn::lin::Params& pr) {
-        return pl.tc ? gdn::lin::launch_tc(pr, stream) : gdn::lin::launch_simt(pr, p->d_k, in_bf16, out_bf16, stream);
+        return pl.tc ? gdn::lin::launch_tc(pr, p->d_k, stream) : gdn::lin::launch_simt(pr, p->d_k, in_bf16, out_bf16, stream);
     };
     if (!own.empty()) {
         prm->o = nullptr;

@@ -107,7 +107,7 @@ __device__ __forceinline__ float reduce_rows(const float (&p)[4], int c) {
     return x + __shfl_xor_sync(0xffffffffu, x, 1);
 }
 
-template <int DK, typename T, typename OutT>
+template <int DK, bool READOUT, typename T, typename OutT>
 __global__ void __launch_bounds__(128) linear_scan_kernel(const __grid_constant__ Params p) {
     using CM = Cols<DK, T>;
     constexpr int CT = CM::CT;
@@ -127,7 +127,6 @@ __global__ void __launch_bounds__(128) linear_scan_kernel(const __grid_constant_
     const int row0 = rb * RB + warp * kWarpRows + rg * 4;   // first of this lane's 4 state rows
     const int hk = h / p.rep;
     const int len = job.len;
-    const bool rd = p.o != nullptr;
     const float a = p.alpha[h];
     const size_t head = (size_t)h * p.dv * DK;
 
@@ -143,9 +142,9 @@ __global__ void __launch_bounds__(128) linear_scan_kernel(const __grid_constant_
     }
 
     const T* gk = static_cast<const T*>(p.k) + job.tok_begin * p.k_stride + (int64_t)hk * DK;
-    const T* gq = rd ? static_cast<const T*>(p.q) + job.tok_begin * p.q_stride + (int64_t)hk * DK : nullptr;
+    const T* gq = READOUT ? static_cast<const T*>(p.q) + job.tok_begin * p.q_stride + (int64_t)hk * DK : nullptr;
     const T* gv = static_cast<const T*>(p.v) + job.tok_begin * p.v_stride + (int64_t)h * p.dv + rb * RB;
-    OutT* go = rd ? static_cast<OutT*>(p.o) + (job.tok_begin * p.H + h) * (int64_t)p.dv + row0 : nullptr;
+    OutT* go = READOUT ? static_cast<OutT*>(p.o) + (job.tok_begin * p.H + h) * (int64_t)p.dv + row0 : nullptr;
 
     auto stage = [&](int tile) {
         const int t0 = tile * kTile, buf = tile & 1;
@@ -154,7 +153,7 @@ __global__ void __launch_bounds__(128) linear_scan_kernel(const __grid_constant_
             const int ts = min(t0 + t, len - 1);   // past the end: a valid address, nothing copied
             const int n = t0 + t < len ? 16 : 0;
             cp_async<16>(&sk[buf][t][x], gk + (int64_t)ts * p.k_stride + x, n);
-            if (rd) cp_async<16>(&sq[buf][t][x], gq + (int64_t)ts * p.q_stride + x, n);
+            if (READOUT) cp_async<16>(&sq[buf][t][x], gq + (int64_t)ts * p.q_stride + x, n);
         }
         for (int i = tid; i < kTile * (RB / kPiece); i += blockDim.x) {
             const int t = i / (RB / kPiece), x = (i % (RB / kPiece)) * kPiece;
@@ -178,7 +177,7 @@ __global__ void __launch_bounds__(128) linear_scan_kernel(const __grid_constant_
         }
         __syncthreads();
         const int buf = tile & 1, n = min(kTile, len - tile * kTile);
-        for (int t = 0; t < n; ++t) {
+        auto token = [&](int t) {
             float kk[CT], vv[4];
             CM::load(sk[buf][t], c, kk);
             load_vec<4>(&sv[buf][t][warp * kWarpRows + rg * 4], vv);
@@ -186,7 +185,7 @@ __global__ void __launch_bounds__(128) linear_scan_kernel(const __grid_constant_
             for (int r = 0; r < 4; ++r)
 #pragma unroll
                 for (int j = 0; j < CT; ++j) S[r][j] = fmaf(vv[r], kk[j], a * S[r][j]);
-            if (rd) {
+            if constexpr (READOUT) {
                 float qq[CT], part[4];
                 CM::load(sq[buf][t], c, qq);
 #pragma unroll
@@ -199,7 +198,18 @@ __global__ void __launch_bounds__(128) linear_scan_kernel(const __grid_constant_
                 const float x = reduce_rows(part, c);
                 if ((c & 1) == 0) store_out(go + (int64_t)(tile * kTile + t) * p.H * p.dv + (c >> 1), x * p.scale);
             }
-            if (tile * kTile + t + 1 == next_ck) {
+        };
+        for (int t = 0; t < n;) {
+            // up to the next checkpoint without a branch, several tokens at a time: a token's loads, its reduction and its
+            // store have no part in the recurrence and overlap the next token's
+            const int stop = min(n, next_ck - tile * kTile);
+            constexpr int U = CT >= 16 ? 2 : 4;
+            for (; t + U <= stop; t += U) {
+#pragma unroll
+                for (int u = 0; u < U; ++u) token(t + u);
+            }
+            for (; t < stop; ++t) token(t);
+            if (tile * kTile + t == next_ck) {
                 float* dst = p.ckpt_states + (size_t)p.ckpts[ck].slot * p.H * p.dv * DK + head;
 #pragma unroll
                 for (int r = 0; r < 4; ++r) CM::store_state(dst + (size_t)(row0 + r) * DK, c, S[r]);
@@ -307,10 +317,11 @@ template <int DK>
 cudaError_t scan_types(const Params& p, bool in_bf16, bool out_bf16, cudaStream_t s) {
     const int grid = p.n_jobs * p.H * (p.dv / p.rows_per_cta);
     const int threads = 32 * (p.rows_per_cta / kWarpRows);
-    if (in_bf16 && out_bf16) linear_scan_kernel<DK, __nv_bfloat16, __nv_bfloat16><<<grid, threads, 0, s>>>(p);
-    else if (in_bf16) linear_scan_kernel<DK, __nv_bfloat16, float><<<grid, threads, 0, s>>>(p);
-    else if (out_bf16) linear_scan_kernel<DK, float, __nv_bfloat16><<<grid, threads, 0, s>>>(p);
-    else linear_scan_kernel<DK, float, float><<<grid, threads, 0, s>>>(p);
+    auto run = [&](auto kernel) { kernel<<<grid, threads, 0, s>>>(p); };
+    using B = __nv_bfloat16;
+    if (!p.o) in_bf16 ? run(linear_scan_kernel<DK, false, B, float>) : run(linear_scan_kernel<DK, false, float, float>);
+    else if (in_bf16) out_bf16 ? run(linear_scan_kernel<DK, true, B, B>) : run(linear_scan_kernel<DK, true, B, float>);
+    else out_bf16 ? run(linear_scan_kernel<DK, true, float, B>) : run(linear_scan_kernel<DK, true, float, float>);
     return cudaGetLastError();
 }
 

@@ -86,8 +86,8 @@ struct StepParams {
 constexpr int kWarpRows = 16;
 
 cudaError_t launch_simt(const Params& p, int dk, bool in_bf16, bool out_bf16, cudaStream_t stream);
-// d_k = d_v = 128, bf16 in and out (gdn_linear_tc.cu)
-cudaError_t launch_tc(const Params& p, cudaStream_t stream);
+// d_k, d_v of 64 or 128, bf16 in and out (gdn_linear_tc.cu)
+cudaError_t launch_tc(const Params& p, int dk, cudaStream_t stream);
 cudaError_t launch_chain(const ChainParams& p, cudaStream_t stream);
 cudaError_t launch_step(const StepParams& p, int dk, bool in_bf16, bool out_bf16, cudaStream_t stream);
 

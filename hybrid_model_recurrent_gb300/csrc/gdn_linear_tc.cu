@@ -1,5 +1,5 @@
 // gdn_linear_tc.cu - linear attention with a decay for each head, chunked form on the 5th-generation tensor cores
-// (d_k = d_v = 128, bf16 in and out).
+// (d_k, d_v of 64 or 128, bf16 in and out).
 //
 //     S_t = a S_{t-1} + v_t k_t^T,   o_t = scale S_t q_t
 //
@@ -67,9 +67,8 @@ using tcu::store32;
 using tcu::tile_desc;
 using tcu::wait_bar;
 
-constexpr int D = 128;
 constexpr int kTok = 128;                   // tokens of a chunk
-constexpr int kTile = kTok * D * 2;         // bytes of a K, Q, V, K' or S tile: two 64-column blocks of [128][128 B]
+constexpr int kTile = kTok * 128 * 2;       // bytes of a tile: two 64-column blocks of [128][128 B] (one used at width 64)
 constexpr int kThreads = 16 * 32;
 constexpr int OFF_O = 5 * kTile;            // after the input tiles (with a readout): staged output
 constexpr int OFF_S = 6 * kTile;            // the bf16 copy of S
@@ -122,7 +121,7 @@ struct Walk {
     }
 };
 
-template <bool READOUT>
+template <int DK, int DV, bool READOUT>
 __global__ void __launch_bounds__(kThreads, 1) linear_tc_kernel(const __grid_constant__ Params p) {
     constexpr int NB = READOUT ? 2 : 3;               // buffers of K and of V (Q is spent early in its chunk: one)
     constexpr int NT = READOUT ? 2 * NB + 1 : 2 * NB; // input tiles
@@ -198,6 +197,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_tc_kernel(const __grid_con
     // ldmatrix, whose fragment (lane l: dimension l / 4, token pair l % 4 of an 8 x 8 matrix) is the 16x128b form's.
     auto scale_values = [&](int j, int n, int sb) {
         const int q4 = warp & 3, pr = lane & 3;
+        if (32 * q4 >= DV) return;   // rows past d_v: never read
         // row addresses: token 8 g + (lane & 7) of the block, dimensions 8 (lane / 8) .. of this warp's 32
         const uint32_t src = sbase + at(1, j) + (q4 >> 1) * 16384 + (32 * sb + (lane & 7)) * 128 +
                              ((((q4 & 1) * 4 + (lane >> 3)) ^ (lane & 7)) << 4);
@@ -273,31 +273,61 @@ __global__ void __launch_bounds__(kThreads, 1) linear_tc_kernel(const __grid_con
 
     if (warp < 4) {
         // ---- state ----
-        const size_t state_off = ((size_t)h * D + row) * D;
-        auto dump = [&](float* dst) {   // this thread's row, from TMEM
+        const bool mine = row < DV;   // whole warps: lanes past d_v hold nothing that is read
+        const size_t warp_off = ((size_t)h * DV + 32 * warp) * DK;
+        // A thread holds a row, and 32 rows' 16 bytes at a time would take the load/store unit 32 lines an instruction, so
+        // 32 x 32 pieces of the state pass through this warp's rows of the S tile, which is free then (two pieces in turn).
+        unsigned char* const piece = smem + OFF_S + 32 * warp * 128;
+        const int pr = lane >> 3, pc = lane & 7;   // by lines: row 4 k + pr, 16-byte column pc
+        auto by_row = [&](int c, int i) {
+            return reinterpret_cast<float4*>(piece + (c & 1) * 16384 + lane * 128 + ((i ^ (lane & 7)) << 4));
+        };
+        auto by_line = [&](int c, int k) {
+            const int r = 4 * k + pr;
+            return reinterpret_cast<float4*>(piece + (c & 1) * 16384 + r * 128 + ((pc ^ (r & 7)) << 4));
+        };
+        auto dump = [&](float* dst) {   // this warp's rows of TMEM to dst
+            if (!mine) return;
+            dst += warp_off + pr * DK + 4 * pc;
 #pragma unroll 1
-            for (int c = 0; c < 4; ++c) {
+            for (int c = 0; c < DK / 32; ++c) {
                 float v[32];
                 tmem_ld32(trow + T_S + 32 * c, v);
 #pragma unroll
-                for (int i = 0; i < 32; i += 4)
-                    *reinterpret_cast<float4*>(dst + 32 * c + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+                for (int i = 0; i < 8; ++i) *by_row(c, i) = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+                __syncwarp();
+#pragma unroll
+                for (int k = 0; k < 8; ++k) *reinterpret_cast<float4*>(dst + 4 * k * DK + 32 * c) = *by_line(c, k);
             }
+            __syncwarp();
         };
-        if (w.more()) {
+        if (w.more() && mine) {
             // the initial state into TMEM, so that the first chunk is like the others
 #pragma unroll 1
-            for (int c = 0; c < 4; ++c) {
-                float v[32];
+            for (int c0 = 0; c0 < DK / 32; c0 += 2) {
+                if (job.s0) {
+                    const float* src = job.s0 + warp_off + pr * DK + 4 * pc + 32 * c0;
+                    float4 x[16];
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const float4 x = job.s0 ? reinterpret_cast<const float4*>(job.s0 + state_off + 32 * c)[i]
-                                            : make_float4(0.f, 0.f, 0.f, 0.f);
-                    v[4 * i] = x.x, v[4 * i + 1] = x.y, v[4 * i + 2] = x.z, v[4 * i + 3] = x.w;
+                    for (int i = 0; i < 16; ++i) x[i] = *reinterpret_cast<const float4*>(src + 4 * (i & 7) * DK + 32 * (i >> 3));
+                    __syncwarp();
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) *by_line(i >> 3, i & 7) = x[i];
+                    __syncwarp();
                 }
-                tmem_st32(trow + T_S + 32 * c, v);
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    float v[32];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const float4 x = job.s0 ? *by_row(c, i) : make_float4(0.f, 0.f, 0.f, 0.f);
+                        v[4 * i] = x.x, v[4 * i + 1] = x.y, v[4 * i + 2] = x.z, v[4 * i + 3] = x.w;
+                    }
+                    tmem_st32(trow + T_S + 32 * (c0 + c), v);
+                }
             }
             tmem_st_wait();
+            __syncwarp();
         }
         bool ok = true;
         int j = 0, slot = -1;   // slot: where the last chunk's state is dumped
@@ -306,11 +336,11 @@ __global__ void __launch_bounds__(kThreads, 1) linear_tc_kernel(const __grid_con
                 ok = warp_wait(st_done, j - 1);
                 if (!ok) break;
                 tc_fence_after();
-                if (slot >= 0) dump(p.ckpt_states + (size_t)slot * p.H * D * D + state_off);
+                if (slot >= 0) dump(p.ckpt_states + (size_t)slot * p.H * DV * DK);
             }
             const float2 decay = make_float2(pw[w.n], pw[w.n]);
 #pragma unroll 1
-            for (int c = 0; c < 2; ++c) {
+            for (int c = 0; c < (mine ? DK / 64 : 0); ++c) {
                 float v[2][32];
                 tmem_ld32x2(trow + T_S + 64 * c, trow + T_S + 64 * c + 32, v[0], v[1]);
 #pragma unroll
@@ -362,14 +392,14 @@ __global__ void __launch_bounds__(kThreads, 1) linear_tc_kernel(const __grid_con
             ok = warp_wait(st_done, j - 1);
             if (ok) {
                 tc_fence_after();
-                if (slot >= 0) dump(p.ckpt_states + (size_t)slot * p.H * D * D + state_off);
-                if (job.s_final) dump(job.s_final + state_off);
+                if (slot >= 0) dump(p.ckpt_states + (size_t)slot * p.H * DV * DK);
+                if (job.s_final) dump(job.s_final);
             }
-        } else if (ok && job.s_final) {
+        } else if (ok && job.s_final && mine) {
             // no tokens: the final state is the initial one
-            for (int i = 0; i < D; i += 4)
-                *reinterpret_cast<float4*>(job.s_final + state_off + i) =
-                    job.s0 ? *reinterpret_cast<const float4*>(job.s0 + state_off + i) : make_float4(0.f, 0.f, 0.f, 0.f);
+            for (int i = lane; i < 32 * DK / 4; i += 32)
+                reinterpret_cast<float4*>(job.s_final + warp_off)[i] =
+                    job.s0 ? reinterpret_cast<const float4*>(job.s0 + warp_off)[i] : make_float4(0.f, 0.f, 0.f, 0.f);
         }
     } else if (warp < 8) {
         // ---- tokens: lane = token row, this warp's rows are [32 rb, 32 rb + 32) ----
@@ -387,7 +417,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_tc_kernel(const __grid_con
                 if (!warp_wait(q_done, j)) break;
                 tc_fence_after();
 #pragma unroll 1
-                for (int c = 0; c < 4; ++c) {
+                for (int c = 0; c < DV / 32; ++c) {
                     float x[32];
                     tmem_ld32(trow + T_O + 32 * c, x);
 #pragma unroll
@@ -422,9 +452,9 @@ __global__ void __launch_bounds__(kThreads, 1) linear_tc_kernel(const __grid_con
                 if (!warp_wait(o_done, j)) break;
                 tc_fence_after();
                 // the whole row into registers first, so that the next chunk's O can begin before the stores are through
-                uint32_t u[8][8];
+                uint32_t u[DV / 16][8];
 #pragma unroll
-                for (int c = 0; c < 4; ++c) {
+                for (int c = 0; c < DV / 32; ++c) {
                     float x[32];
                     tmem_ld32(trow + T_O + 32 * c, x);
 #pragma unroll
@@ -440,30 +470,31 @@ __global__ void __launch_bounds__(kThreads, 1) linear_tc_kernel(const __grid_con
                 if (j > 0 && !warp_wait(o_left, j - 1)) break;
                 if (w.n == kTok) {
 #pragma unroll
-                    for (int c = 0; c < 16; ++c)
+                    for (int c = 0; c < DV / 8; ++c)
                         *reinterpret_cast<uint4*>(smem + OFF_O + (c >> 3) * 16384 + sw128(row, (c & 7) * 8)) =
                             make_uint4(u[c >> 1][(c & 1) * 4], u[c >> 1][(c & 1) * 4 + 1], u[c >> 1][(c & 1) * 4 + 2],
                                        u[c >> 1][(c & 1) * 4 + 3]);
                     proxy_fence();
                 } else if (row < w.n) {
                     __nv_bfloat16* dst =
-                        static_cast<__nv_bfloat16*>(p.o) + ((job.tok_begin + w.pos + row) * p.H + h) * (int64_t)D;
+                        static_cast<__nv_bfloat16*>(p.o) + ((job.tok_begin + w.pos + row) * p.H + h) * (int64_t)DV;
 #pragma unroll
-                    for (int c = 0; c < 8; ++c) store32(dst + 16 * c, u[c], wide);
+                    for (int c = 0; c < DV / 16; ++c) store32(dst + 16 * c, u[c], wide);
                 }
                 mbar_arrive(o_staged);
             }
         }
     } else if (warp == 12) {
         // ---- products (the whole warp walks along, one elected lane issues) ----
-        const uint32_t id = idesc(D, false, false), id_b = idesc(D, false, true);
+        const uint32_t id_g = idesc(kTok, false, false), id_q = idesc(DV, false, false), id_o = idesc(DV, false, true),
+                       id_s = idesc(DK, false, true);
         const uint64_t s_desc = tile_desc(sbase + OFF_S, false);
         auto scores = [&](int j) {   // G of chunk j
             if (!warp_wait(&full[bar(0, j)], phase(0, j)) || !warp_wait(&full[bar(2, j)], phase(2, j))) return false;
             const uint64_t q = tile_desc(sbase + at(2, j), false), k = tile_desc(sbase + at(0, j), false);
             if (elect_one()) {
 #pragma unroll
-                for (int i = 0; i < 8; ++i) umma_ss(tbase + T_G, cols_step(q, i), cols_step(k, i), id, i > 0);
+                for (int i = 0; i < DK / 16; ++i) umma_ss(tbase + T_G, cols_step(q, i), cols_step(k, i), id_g, i > 0);
                 umma_commit(g_done);
             }
             return true;
@@ -480,7 +511,8 @@ __global__ void __launch_bounds__(kThreads, 1) linear_tc_kernel(const __grid_con
                 const uint64_t q = tile_desc(sbase + at(2, j), false);
                 if (elect_one()) {
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) umma_ss(tbase + T_O, cols_step(q, i), cols_step(s_desc, i), id, i > 0);
+                    for (int i = 0; i < DK / 16; ++i)
+                        umma_ss(tbase + T_O, cols_step(q, i), cols_step(s_desc, i), id_q, i > 0);
                     umma_commit(q_done);
                     umma_commit(&empty[bar(2, j)]);
                 }
@@ -492,8 +524,8 @@ __global__ void __launch_bounds__(kThreads, 1) linear_tc_kernel(const __grid_con
             if (elect_one()) {
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
-                    umma_ts(tbase + T_S, tbase + T_VH + 8 * i, rows_step(k, i), id_b, 1);
-                    umma_ts(tbase + T_S, tbase + T_VL + 8 * i, rows_step(k, i), id_b, 1);
+                    umma_ts(tbase + T_S, tbase + T_VH + 8 * i, rows_step(k, i), id_s, 1);
+                    umma_ts(tbase + T_S, tbase + T_VL + 8 * i, rows_step(k, i), id_s, 1);
                 }
                 umma_commit(st_done);
                 umma_commit(&empty[bar(0, j)]);
@@ -506,7 +538,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_tc_kernel(const __grid_con
             if (elect_one()) {
                 if (READOUT) {
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) umma_ts(tbase + T_O, tbase + p_block(i >> 1) + 8 * (i & 1), rows_step(v, i), id_b, 1);
+                    for (int i = 0; i < 8; ++i) umma_ts(tbase + T_O, tbase + p_block(i >> 1) + 8 * (i & 1), rows_step(v, i), id_o, 1);
                     umma_commit(o_done);
                 }
                 umma_commit(&empty[bar(1, j)]);
@@ -521,8 +553,8 @@ __global__ void __launch_bounds__(kThreads, 1) linear_tc_kernel(const __grid_con
                 if (!wait_bar(o_staged, (uint32_t)j & 1u, abort_flag, limit)) break;
                 if (w.n == kTok) {
                     const int t0 = (int)(job.tok_begin + w.pos);
-                    tma_store_3d(smem + OFF_O, &p.tm_o, 0, h, t0);
-                    tma_store_3d(smem + OFF_O + 16384, &p.tm_o, 64, h, t0);
+#pragma unroll
+                    for (int x = 0; x < DV / 64; ++x) tma_store_3d(smem + OFF_O + x * 16384, &p.tm_o, 64 * x, h, t0);
                     asm volatile("cp.async.bulk.commit_group;" ::: "memory");
                     asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
                 }
@@ -545,9 +577,9 @@ __global__ void __launch_bounds__(kThreads, 1) linear_tc_kernel(const __grid_con
                 const CUtensorMap* tm = in == 0 ? &p.tm_k : in == 1 ? &p.tm_v : &p.tm_q;
                 const int head = in == 1 ? h : hk;
                 uint64_t* b = &full[bar(in, j)];
-                mbar_arrive_expect_tx(b, kTile);
-                tma_load_3d(smem + at(in, j), tm, 0, head, t0, b);
-                tma_load_3d(smem + at(in, j) + 16384, tm, 64, head, t0, b);
+                const int blocks = (in == 1 ? DV : DK) / 64;
+                mbar_arrive_expect_tx(b, blocks * 16384);
+                for (int x = 0; x < blocks; ++x) tma_load_3d(smem + at(in, j) + x * 16384, tm, 64 * x, head, t0, b);
                 issued[in] = j + 1;
             }
         }
@@ -569,19 +601,26 @@ __global__ void __launch_bounds__(kThreads, 1) linear_tc_kernel(const __grid_con
     if (warp == 0) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tbase), "r"(512));
 }
 
-template <bool READOUT>
+template <int DK, int DV, bool READOUT>
 cudaError_t launch(const Params& p, cudaStream_t s) {
-    auto kern = linear_tc_kernel<READOUT>;
+    auto kern = linear_tc_kernel<DK, DV, READOUT>;
     static std::atomic<int> optin[kMaxOptinDevices];
     const cudaError_t e = smem_optin(reinterpret_cast<const void*>(kern), kSmem, optin);
     if (e != cudaSuccess) return e;
     kern<<<p.n_jobs * p.H, kThreads, kSmem, s>>>(p);
     return cudaGetLastError();
 }
+template <int DK, int DV>
+cudaError_t launch_d(const Params& p, cudaStream_t s) {
+    return p.o ? launch<DK, DV, true>(p, s) : launch<DK, DV, false>(p, s);
+}
 
 }  // namespace
 
-cudaError_t launch_tc(const Params& p, cudaStream_t stream) { return p.o ? launch<true>(p, stream) : launch<false>(p, stream); }
+cudaError_t launch_tc(const Params& p, int dk, cudaStream_t s) {
+    if (dk == 128) return p.dv == 128 ? launch_d<128, 128>(p, s) : launch_d<128, 64>(p, s);
+    return p.dv == 128 ? launch_d<64, 128>(p, s) : launch_d<64, 64>(p, s);
+}
 
 }  // namespace lin
 }  // namespace gdn
