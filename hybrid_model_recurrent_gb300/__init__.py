@@ -206,9 +206,12 @@ def _dtype_code(dt: torch.dtype) -> int:
 def workspace(device, nbytes: int = 0) -> torch.Tensor:
     """The cached per-device workspace (holds the sticky device status word), grown to at least
     `nbytes`; growing keeps the status word."""
-    device = torch.device(device)
+    if type(device) is not torch.device:
+        device = torch.device(device)
     idx = device.index if device.index is not None else torch.cuda.current_device()
     ws = _workspaces.get(idx)
+    if ws is not None and ws.numel() >= nbytes:
+        return ws
     need = max(int(lib().gdn_workspace_size()), int(nbytes))
     if ws is None or ws.numel() < need:
         new = torch.zeros(need, dtype=torch.uint8, device=torch.device("cuda", idx))
@@ -639,6 +642,12 @@ def gdn_adaptive_replay_plan(alpha, cu_seqlens, m, eps: float, rmax_num: int, rm
 # ---- the other layers of a hybrid model (include/gdn_hybrid.h) ---------------------------------------
 
 
+def _c64(values):
+    """A host array of int64 for the library (cheaper to make than a numpy array and a cast of its address)."""
+    values = [int(x) for x in values]
+    return (ctypes.c_int64 * len(values))(*values)
+
+
 def _expect(ok: bool, message: str) -> None:
     if not ok:
         raise ValueError(message)
@@ -683,7 +692,7 @@ def _linear_problem(q, k, v, alpha, num_seqs: int, cu, scale: float, out_dtype):
         raise ValueError("q, k [T, Hk, d_k] and v [T, H, d_v] must agree in their tokens, dtype and device")
     _dense(alpha, "alpha", (vs[1],), torch.float32, dev)
     code = _dtype_code(dt)
-    return _LinearProblem(num_seqs, vs[1], ks[1], ks[2], vs[2], _p64(cu), code,
+    return _LinearProblem(num_seqs, vs[1], ks[1], ks[2], vs[2], cu, code,
                           code if out_dtype is dt else _dtype_code(out_dtype), scale,
                           0 if q is None else _row_stride(q, "q"), _row_stride(k, "k"), _row_stride(v, "v"))
 
@@ -697,48 +706,65 @@ def gdn_linear_prefill(q, k, v, alpha, cu_seqlens, *, scale: float = 1.0, S0=Non
     q, k [T, Hk, dk] (head h of v reads head h // (H // Hk)), v [T, H, dv], alpha [H] fp32.  S0 [slots, H, dv, dk]
     with S0_index: the slot that each sequence starts from (-1: zeros; default: its own number).  ckpt_pos: one list of
     1-based positions per sequence.  Returns dict(o, S_final, ckpt_states) as gdn_prefill_ckpt."""
-    cu = _i64(cu_seqlens)
+    cu = _c64(cu_seqlens)
     B = len(cu) - 1
     dev = k.device
     out_dtype = out_dtype or k.dtype
-    pr = _linear_problem(q if readout else None, k, v, alpha, B, cu, scale, out_dtype)
-    T, H, dv, dk = v.shape[0], v.shape[1], v.shape[2], k.shape[2]
-    _expect(B >= 1 and int(cu[-1]) == T, "cu_seqlens must end with the number of tokens")
-    _expect(not readout or q is not None, "a readout needs q")
-    flat, cu_ck = _flatten_ckpts(ckpt_pos, B)
-    n_ck = 0 if cu_ck is None else int(cu_ck[-1])
-    index = None
+    if not readout:
+        q = o = None
+    elif q is None:
+        raise ValueError("a readout needs q")
+    pr = _linear_problem(q, k, v, alpha, B, cu, scale, out_dtype)
+    T, H, dv = v.shape
+    dk = k.shape[2]
+    if B < 1 or cu[B] != T:
+        raise ValueError("cu_seqlens must end with the number of tokens")
+    flat = cu_ck = index = None
+    n_ck = slots = 0
+    if ckpt_pos is not None:
+        if len(ckpt_pos) != B:
+            raise ValueError("ckpt_pos must give one list per sequence")
+        cu_ck, flat = [0], []
+        for lst in ckpt_pos:
+            flat.extend(lst)
+            cu_ck.append(len(flat))
+        n_ck, cu_ck, flat = len(flat), _c64(cu_ck), _c64(flat)
     if S0 is not None:
-        _expect(S0.dim() == 4, "S0 must be [slots, H, d_v, d_k]")
-        _dense(S0, "S0", (S0.shape[0], H, dv, dk), torch.float32, dev)
+        slots = S0.shape[0]
+        _dense(S0, "S0", (slots, H, dv, dk), torch.float32, dev)
         if S0_index is not None:
-            index = np.ascontiguousarray(np.asarray(list(S0_index), dtype=np.int32))
-            _expect(len(index) == B, "S0_index must give one slot per sequence")
-    else:
-        _expect(S0_index is None, "S0_index without S0")
+            index = [int(x) for x in S0_index]
+            if len(index) != B:
+                raise ValueError("S0_index must give one slot per sequence")
+            index = (ctypes.c_int32 * B)(*index)
+    elif S0_index is not None:
+        raise ValueError("S0_index without S0")
+    L = lib()
+    nbytes = L.gdn_linear_scratch_bytes(ctypes.byref(pr))
     with _on(stream, dev):
-        if not readout:
-            o = None
-        elif o is None:
+        if o is not None:
+            _dense(o, "o", (T, H, dv), out_dtype, dev)
+        elif readout:
             o = torch.empty((T, H, dv), dtype=out_dtype, device=dev)
-        if S_final is None:
+        if S_final is not None:
+            _dense(S_final, "S_final", (B, H, dv, dk), torch.float32, dev)
+        else:
             S_final = torch.empty((B, H, dv, dk), dtype=torch.float32, device=dev)
-        if ckpt_states is None and n_ck > 0:
+        if ckpt_states is not None:
+            if n_ck:
+                _dense(ckpt_states, "ckpt_states", (n_ck, H, dv, dk), torch.float32, dev)
+        elif n_ck:
             ckpt_states = torch.empty((n_ck, H, dv, dk), dtype=torch.float32, device=dev)
-        nbytes = int(lib().gdn_linear_scratch_bytes(ctypes.byref(pr)))
         scratch = torch.empty(nbytes, dtype=torch.uint8, device=dev) if nbytes else None
-    if o is not None:
-        _dense(o, "o", (T, H, dv), out_dtype, dev)
-    _dense(S_final, "S_final", (B, H, dv, dk), torch.float32, dev)
-    if n_ck > 0:
-        _dense(ckpt_states, "ckpt_states", (n_ck, H, dv, dk), torch.float32, dev)
-    ws = ws if ws is not None else workspace(dev)
-    rc = lib().gdn_linear_prefill(
-        ctypes.byref(pr), _ptr(q if readout else None), _ptr(k), _ptr(v), _ptr(alpha), _ptr(S0),
-        None if index is None else index.ctypes.data_as(ctypes.POINTER(ctypes.c_int32)),
-        0 if S0 is None else S0.shape[0], _ptr(o), _ptr(S_final), _p64(flat) if n_ck > 0 else None, _p64(cu_ck),
-        _ptr(ckpt_states if n_ck > 0 else None), _ptr(scratch), nbytes, _ptr(ws), ws.numel(), _stream(stream, dev))
-    _check(rc, "gdn_linear_prefill")
+    if ws is None:
+        ws = workspace(dev)
+    rc = L.gdn_linear_prefill(
+        ctypes.byref(pr), None if q is None else q.data_ptr(), k.data_ptr(), v.data_ptr(), alpha.data_ptr(),
+        None if S0 is None else S0.data_ptr(), index, slots, None if o is None else o.data_ptr(), S_final.data_ptr(),
+        flat if n_ck else None, cu_ck, ckpt_states.data_ptr() if n_ck else None,
+        None if scratch is None else scratch.data_ptr(), nbytes, ws.data_ptr(), ws.numel(), _raw_stream(stream, dev))
+    if rc != GDN_OK:
+        raise GdnError(rc, "gdn_linear_prefill")
     return {"o": o, "S_final": S_final, "ckpt_states": ckpt_states}
 
 
@@ -819,20 +845,25 @@ def gdn_prefix_attention(q, k_prefix, v_prefix, k_tail=None, v_tail=None, tail_l
     pr = _PrefixProblem(B, n, Hq, Hkv, D, _dtype_code(dt), P, cap, cap if max_tail is None else max_tail,
                         D ** -0.5 if scale is None else scale, *_strides(q, "q"), *_strides(k_prefix, "k_prefix"),
                         *_strides(v_prefix, "v_prefix"), *kts, *vts)
+    L = lib()
+    nbytes = L.gdn_prefix_scratch_bytes(ctypes.byref(pr))
     with _on(stream, dev):
-        if o is None:
-            o = torch.empty((B, n, Hq, D), dtype=q.dtype, device=dev)
-        if lse is None:
+        if o is not None:
+            _dense(o, "o", (B, n, Hq, D), dt, dev)
+        else:
+            o = torch.empty((B, n, Hq, D), dtype=dt, device=dev)
+        if lse is not None:
+            _dense(lse, "lse", (B, n, Hq), torch.float32, dev)
+        else:
             lse = torch.empty((B, n, Hq), dtype=torch.float32, device=dev)
-        nbytes = int(lib().gdn_prefix_scratch_bytes(ctypes.byref(pr)))
         scratch = torch.empty(nbytes, dtype=torch.uint8, device=dev) if nbytes else None
-    _dense(o, "o", (B, n, Hq, D), q.dtype, dev)
-    _dense(lse, "lse", (B, n, Hq), torch.float32, dev)
-    ws = ws if ws is not None else workspace(dev)
-    rc = lib().gdn_prefix_attention(
+    if ws is None:
+        ws = workspace(dev)
+    rc = L.gdn_prefix_attention(
         ctypes.byref(pr), q.data_ptr(), k_prefix.data_ptr() if P else None, v_prefix.data_ptr() if P else None,
         k_tail.data_ptr() if cap else None, v_tail.data_ptr() if cap else None, tail_len.data_ptr() if cap else None,
-        o.data_ptr(), lse.data_ptr(), _ptr(scratch), nbytes, ws.data_ptr(), ws.numel(),
+        o.data_ptr(), lse.data_ptr(), None if scratch is None else scratch.data_ptr(), nbytes, ws.data_ptr(), ws.numel(),
         _raw_stream(stream, dev))
-    _check(rc, "gdn_prefix_attention")
+    if rc != GDN_OK:
+        raise GdnError(rc, "gdn_prefix_attention")
     return {"o": o, "lse": lse}
