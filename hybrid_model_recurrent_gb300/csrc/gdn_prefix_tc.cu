@@ -246,7 +246,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, NT == 1 ? 2 : 1)
                     const Item x = item_at<NT>(p, item, pre_items, joined);
                     for (int c = 0; c < 2 * x.n_tiles; ++c, ++seq) {
                         const int s = seq % F::ST, j = c >> 1;
-                        ok = !(p.stall_after >= 0 && j >= p.stall_after) &&   // testing hook
+                        ok = !(p.stall_after >= 0 && seq / 2 >= p.stall_after) &&   // testing hook
                              (seq > 0 || wait_bar(q_asked, 0, abort_flag, limit)) &&
                              (seq < F::ST || wait_bar(&empty[s], (uint32_t)((seq / F::ST - 1) & 1), abort_flag, limit));
                         if (!ok) break;
