@@ -283,7 +283,7 @@ gdn_status linear_prefill(const gdn_linear_problem* p, const void* q, const void
 
 struct PrefixPlan {
     bool tc, joined;
-    int pre_rt, tail_rt;   // tensor cores: row tiles of a CTA
+    int row_tiles;         // tensor cores: row tiles of a CTA
     int pre_splits, pre_chunk, tail_splits, pre_tiles, tail_tiles;
     int groups;            // groups of 32 stacked rows of a key/value head
     int64_t rows;          // query rows of all heads
@@ -340,10 +340,9 @@ PrefixPlan plan_prefix(const gdn_prefix_problem& f) {
     const int64_t group = f.num_q_heads / f.num_kv_heads, own = f.num_queries * group, stacked = own * f.batch;
     pl.groups = (int)ceil_div(stacked, 32);
     pl.tc = f.dtype == GDN_BF16 && f.head_dim >= 64;
-    pl.pre_rt = pl.tail_rt = 1;
     const int64_t part_bytes = pl.rows * (f.head_dim * 4 + 8) * 2;
     int64_t unit;   // tokens of a tile
-    int64_t pre_slots, tail_slots;
+    int64_t slots;
     if (pl.tc) {
         unit = gdn::prefix::kTcKeys;
         // A request with a whole row tile of its own needs no stacking: when such tiles fill the GPU, each takes prefix
@@ -351,32 +350,31 @@ PrefixPlan plan_prefix(const gdn_prefix_problem& f) {
         const int64_t pairs = ceil_div(own, 2 * gdn::prefix::kTcRows);
         if (own > gdn::prefix::kTcRows && f.batch * f.num_kv_heads * pairs >= kSms && f.prefix_len + f.max_tail > 0) {
             pl.joined = true;
-            pl.tail_rt = 2;
+            pl.row_tiles = 2;
             pl.tail_tiles = (int)pairs;
             pl.tail_splits = 1;
             return pl;
         }
-        // two row tiles a CTA halve the reads of keys and values; one leaves room for two CTAs
-        pl.pre_rt = stacked > gdn::prefix::kTcRows ? 2 : 1;
-        pl.tail_rt = own > gdn::prefix::kTcRows ? 2 : 1;
-        pl.pre_tiles = (int)ceil_div(stacked, pl.pre_rt * gdn::prefix::kTcRows);
-        pl.tail_tiles = (int)ceil_div(own, pl.tail_rt * gdn::prefix::kTcRows);
-        pre_slots = kSms * (3 - pl.pre_rt), tail_slots = kSms * (3 - pl.tail_rt);
+        // Two row tiles a CTA halve the reads of the prefix when more than one is stacked; one leaves room for two CTAs.
+        pl.row_tiles = std::max(f.prefix_len > 0 ? stacked : 0, own) > gdn::prefix::kTcRows ? 2 : 1;
+        pl.pre_tiles = (int)ceil_div(stacked, pl.row_tiles * gdn::prefix::kTcRows);
+        pl.tail_tiles = (int)ceil_div(own, pl.row_tiles * gdn::prefix::kTcRows);
+        slots = kSms * (3 - pl.row_tiles);
     } else {
         unit = gdn::prefix::kSimtKeys;
         pl.pre_tiles = (int)ceil_div(stacked, gdn::prefix::kSimtRows);
         pl.tail_tiles = (int)ceil_div(own, gdn::prefix::kSimtRows);
-        pre_slots = tail_slots = kSms * 5;   // CTAs that 43 KB of shared memory let run at once
+        slots = kSms * 5;   // CTAs that 43 KB of shared memory let run at once
     }
     if (f.prefix_len > 0) {
         const int64_t tiles = ceil_div(f.prefix_len, unit);
-        const int s = best_splits(tiles, (int64_t)f.num_kv_heads * pl.pre_tiles, pre_slots, part_bytes);
+        const int s = best_splits(tiles, (int64_t)f.num_kv_heads * pl.pre_tiles, slots, part_bytes);
         pl.pre_chunk = (int)(ceil_div(tiles, s) * unit);
         pl.pre_splits = (int)ceil_div(f.prefix_len, pl.pre_chunk);
     }
     if (f.max_tail > 0)
         pl.tail_splits = best_splits(ceil_div(f.max_tail, unit), (int64_t)f.batch * f.num_kv_heads * pl.tail_tiles,
-                                     tail_slots, part_bytes);
+                                     slots, part_bytes);
     const int64_t parts = pl.parts();
     if (parts == 0 || (pl.tc && parts == 1)) return pl;
     pl.ml_off = 0;
@@ -447,16 +445,9 @@ gdn_status prefix_attention(const gdn_prefix_problem* p, const void* q, const vo
                             gdn::prefix::kTcKeys);
         if (!maps) return GDN_ERR_CUDA;
         const bool direct = pl.parts() == 1;
-        cudaError_t e;
-        if (pl.pre_rt == pl.tail_rt || pre_items == 0 || tail_items == 0) {
-            e = gdn::prefix::launch_tc(*prm, f.head_dim, pre_items ? pl.pre_rt : pl.tail_rt, pre_items, tail_items,
-                                       pl.joined, direct, false, stream);
-        } else {
-            e = gdn::prefix::launch_tc(*prm, f.head_dim, pl.pre_rt, pre_items, 0, false, direct, false, stream);
-            if (e == cudaSuccess)
-                e = gdn::prefix::launch_tc(*prm, f.head_dim, pl.tail_rt, 0, tail_items, false, direct, true, stream);
-        }
-        if (e != cudaSuccess) return GDN_ERR_CUDA;
+        if (gdn::prefix::launch_tc(*prm, f.head_dim, pl.row_tiles, pre_items, tail_items, pl.joined, direct, stream) !=
+            cudaSuccess)
+            return GDN_ERR_CUDA;
         if (direct) return GDN_OK;
     } else if (gdn::prefix::launch_simt(*prm, f.head_dim, bf16, stream) != cudaSuccess) {
         return GDN_ERR_CUDA;

@@ -85,10 +85,9 @@ constexpr int kTcKeys = 128;
 
 cudaError_t launch_simt(const Params& p, int D, bool bf16, cudaStream_t stream);
 // `row_tiles` (1 or 2) row tiles a CTA.  joined: an item takes the whole prefix and then the whole tail of one request's
-// rows (pre_items = 0); direct: the items write o and lse themselves (one part in all); beside: may run beside the launch
-// before it on the stream, and ends after it
+// rows (pre_items = 0); direct: the items write o and lse themselves (one part in all)
 cudaError_t launch_tc(const Params& p, int D, int row_tiles, int64_t pre_items, int64_t tail_items, bool joined,
-                      bool direct, bool beside, cudaStream_t stream);
+                      bool direct, cudaStream_t stream);
 // `beside`: launched so that it starts up beside the parts (which let it) and waits for them itself
 cudaError_t launch_join(const Params& p, int D, bool bf16, int parts, bool beside, cudaStream_t stream);
 

@@ -11,7 +11,7 @@
 //
 // Roles: warps 0 .. 4 NT - 1 softmax (one warpgroup a row tile), then one MMA-issuing thread and one copying thread.
 // K and V tiles arrive by TMA in a ring of ST tiles; with NT = 2 both row tiles use each tile, and one tile's softmax
-// runs beside the other's products.  With NT = 1 two CTAs share a multiprocessor and overlap each other instead.  The
+// runs beside the other's products (an item of at most 128 rows uses one).  With NT = 1 two CTAs share a multiprocessor and overlap each other instead.  The
 // grid is one wave and each CTA takes items in turn, the copies running ahead into the next one.
 //
 // A masked token's score is replaced (not multiplied), and value rows past the range are zeroed in shared memory
@@ -88,6 +88,7 @@ __device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* tm, in
 // [lo2, hi2) of request b0, in n_tiles tiles, the first n1 of them the prefix's.
 struct Item {
     bool stacked;   // rows of all requests (prefix only), else one request's
+    int na;         // row tiles that hold rows
     int h, b0, part, len, lo1, hi1, lo2, hi2, rows, row0, n1, n_tiles;
 };
 template <int NT>
@@ -120,6 +121,7 @@ __device__ __forceinline__ Item item_at(const Params& p, int item, int pre_items
         x.part += p.pre_splits;
     }
     x.row0 = tile * (NT * kRows);
+    x.na = NT == 1 || x.rows - x.row0 <= kRows ? 1 : 2;
     x.n1 = (x.hi1 - x.lo1 + kKeys - 1) / kKeys;
     x.n_tiles = x.n1 + (x.hi2 - x.lo2 + kKeys - 1) / kKeys;
     return x;
@@ -137,18 +139,18 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, NT == 1 ? 2 : 1)
     uint64_t* empty = full + F::ST;                                  // [ST] every product that reads it is done
     uint64_t* s_full = empty + F::ST;                                // [NT] S (and every earlier product) done
     uint64_t* p_ready = s_full + NT;                                 // [NT] P written, O rescaled, V's end zeroed
-    uint64_t* q_ready = p_ready + NT;                                // an item's Q tiles written
-    uint64_t* o_full = q_ready + 1;                                  // every product of an item done
-    uint32_t* tslot = reinterpret_cast<uint32_t*>(o_full + 1);
+    uint64_t* q_ready = p_ready + NT;                                // [NT] an item's Q tile written
+    uint64_t* o_full = q_ready + NT;                                 // [NT] every product of an item done
+    uint32_t* tslot = reinterpret_cast<uint32_t*>(o_full + NT);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tslot + 1);
     int* issued = reinterpret_cast<int*>(tslot + 2);                 // tiles whose copy was issued
     uint64_t* end = reinterpret_cast<uint64_t*>(tslot + 4);          // every product done
     uint64_t* q_asked = end + 1;                                     // the first item's Q loads are under way
-    static_assert((2 * F::ST + 2 * NT + 2) * 8 + 32 <= 256, "barrier area");
+    static_assert((2 * F::ST + 4 * NT) * 8 + 32 <= 256, "barrier area");
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const uint64_t limit = p.wait_limit_ns;
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");   // what follows waits for this grid by itself
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");   // the join starts up meanwhile and waits for this grid
 
     if (warp == 0) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(tslot)),
@@ -161,9 +163,10 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, NT == 1 ? 2 : 1)
     }
     if (tid == 0) {
         for (int i = 0; i < F::ST; ++i) mbar_init(&full[i], 1), mbar_init(&empty[i], 1);
-        for (int i = 0; i < NT; ++i) mbar_init(&s_full[i], 1), mbar_init(&p_ready[i], 128);
-        mbar_init(q_ready, NT * 128);
-        mbar_init(o_full, 1);
+        for (int i = 0; i < NT; ++i) {
+            mbar_init(&s_full[i], 1), mbar_init(&p_ready[i], 128);
+            mbar_init(&q_ready[i], 128), mbar_init(&o_full[i], 1);
+        }
         mbar_init(end, 1);
         mbar_init(q_asked, NT * 128);
         *abort_flag = 0;
@@ -190,31 +193,35 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, NT == 1 ? 2 : 1)
             auto done = [&](uint64_t* bar) {
                 if (elect_one()) umma_commit(bar);
             };
-            auto scores = [&](int a, int i) {
-                const uint64_t q = tile_desc(sbase + a * F::kTile, false), k = tile_desc(slot_at(2 * i), false);
-                if (elect_one()) {
-#pragma unroll
-                    for (int s = 0; s < D / 16; ++s)
-                        umma_ss(tbase + a * 128, cols_step(q, s), cols_step(k, s), idesc(kKeys, false, false), s > 0);
-                    umma_commit(&s_full[a]);
-                    if (a == NT - 1) umma_commit(&empty[2 * i % F::ST]);
-                }
-            };
             bool ok = true;
-            int it = 0, nth = 0;
+            int it = 0, tiles[NT] = {}, nth[NT] = {};   // tiles of the ring; tiles and items of each row tile
             for (int item = blockIdx.x; ok && item < items; item += gridDim.x) {
-                const int n = item_at<NT>(p, item, pre_items, joined).n_tiles;
+                const Item x = item_at<NT>(p, item, pre_items, joined);
+                const int n = x.n_tiles, na = x.na;
                 if (n == 0) continue;
-                ok = warp_wait(q_ready, nth) && landed(2 * it);
-                if (!ok) break;
+                auto scores = [&](int a, int i) {
+                    const uint64_t q = tile_desc(sbase + a * F::kTile, false), k = tile_desc(slot_at(2 * i), false);
+                    if (elect_one()) {
 #pragma unroll
-                for (int a = 0; a < NT; ++a) scores(a, it);
+                        for (int s = 0; s < D / 16; ++s)
+                            umma_ss(tbase + a * 128, cols_step(q, s), cols_step(k, s), idesc(kKeys, false, false), s > 0);
+                        umma_commit(&s_full[a]);
+                        if (a == na - 1) umma_commit(&empty[2 * i % F::ST]);
+                    }
+                };
+                ok = landed(2 * it);
+#pragma unroll
+                for (int a = 0; a < NT; ++a) {
+                    if (a < na && ok) ok = warp_wait(&q_ready[a], nth[a]);
+                    if (a < na && ok) scores(a, it);
+                }
                 for (int j = 0; ok && j < n; ++j) {
                     const int i = it + j, vs = 2 * i + 1;
                     ok = landed(vs);
 #pragma unroll
                     for (int a = 0; a < NT; ++a) {
-                        ok = ok && warp_wait(&p_ready[a], i);
+                        if (a >= na) break;
+                        ok = ok && warp_wait(&p_ready[a], tiles[a] + j);
                         if (!ok) break;
                         tc_fence_after();
                         const uint64_t v = tile_desc(slot_at(vs), true);
@@ -223,18 +230,21 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, NT == 1 ? 2 : 1)
                             for (int s = 0; s < kKeys / 16; ++s)
                                 umma_ts(tbase + F::kO + a * D, tbase + a * 128 + 8 * s, rows_step(v, s), idesc(D, false, true),
                                         j > 0 || s > 0);
-                            if (a == NT - 1) umma_commit(&empty[vs % F::ST]);
+                            if (a == na - 1) umma_commit(&empty[vs % F::ST]);
                         }
                         if (j + 1 < n) {
                             if (a == 0) ok = landed(2 * i + 2);
                             if (!ok) break;
                             scores(a, i + 1);
+                        } else {
+                            done(&o_full[a]);
                         }
                     }
                 }
-                if (!ok) break;
-                done(o_full);
-                it += n, ++nth;
+                it += n;
+#pragma unroll
+                for (int a = 0; a < NT; ++a)
+                    if (a < na) tiles[a] += n, ++nth[a];
             }
             done(end);   // also after giving up: the end waits for the products in flight
         } else if (warp == NT * 4 + 1) {
@@ -275,9 +285,14 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, NT == 1 ? 2 : 1)
         const float scale = fmaxf(fabsf(p.scale_log2), 1.17549435e-38f);
         const int nG = (int)p.by_ng.d;
         bool ok = true, first = true;
-        int it = 0, nth = 0;
+        int it = 0, mine = 0, nth = 0;   // tiles of the ring, of this row tile, its items
         for (int item = blockIdx.x; ok && item < items; item += gridDim.x) {
             const Item x = item_at<NT>(p, item, pre_items, joined);
+            if (a >= x.na) {   // no rows for this row tile
+                if (first && x.n_tiles > 0) mbar_arrive(q_asked), first = false;
+                it += x.n_tiles;
+                continue;
+            }
             const int R = x.row0 + a * kRows + r;
             const bool valid = R < x.rows;
             int e, g;
@@ -311,12 +326,12 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, NT == 1 ? 2 : 1)
                         make_uint4(y[i].x ^ flip, y[i].y ^ flip, y[i].z ^ flip, y[i].w ^ flip);
                 }
                 proxy_fence();
-                mbar_arrive(q_ready);
+                mbar_arrive(&q_ready[a]);
             }
             float m = -INFINITY, l = 0.f;
-            for (int j = 0; j < x.n_tiles; ++j, ++it) {
+            for (int j = 0; j < x.n_tiles; ++j, ++it, ++mine) {
                 const int t0 = j < x.n1 ? x.lo1 + j * kKeys : x.lo2 + (j - x.n1) * kKeys;
-                ok = warp_wait(&s_full[a], it);
+                ok = warp_wait(&s_full[a], mine);
                 if (!ok) break;
                 tc_fence_after();
                 if (busy) {
@@ -406,7 +421,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, NT == 1 ? 2 : 1)
             }
             if (!ok) break;
             if (x.n_tiles > 0) {
-                ok = warp_wait(o_full, nth++);
+                ok = warp_wait(&o_full[a], nth++);
                 if (!ok) break;
                 tc_fence_after();
             }
@@ -458,9 +473,6 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, NT == 1 ? 2 : 1)
             tc::drain_phase(end, 0, drain);
             atomicOr(p.status, STATUS_TIMEOUT);
         }
-        // When this grid was started beside the one before it (the other parts of the same call), it ends after that one,
-        // so that the join, which waits for this grid alone, finds both.
-        asm volatile("griddepcontrol.wait;" ::: "memory");
     }
     __syncthreads();
     tc_fence_after();
@@ -469,40 +481,30 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, NT == 1 ? 2 : 1)
 }
 
 template <int D, int NT>
-cudaError_t launch(const Params& p, int64_t pre_items, int64_t tail_items, bool joined, bool direct, bool beside,
-                   cudaStream_t s) {
+cudaError_t launch(const Params& p, int64_t pre_items, int64_t tail_items, bool joined, bool direct, cudaStream_t s) {
     using F = Cfg<D, NT>;
     if (pre_items + tail_items == 0) return cudaSuccess;
     auto kern = prefix_tc_kernel<D, NT>;
     static std::atomic<int> optin[kMaxOptinDevices];
     const cudaError_t e = smem_optin(reinterpret_cast<const void*>(kern), F::kSmem, optin);
     if (e != cudaSuccess) return e;
-    const int items = (int)(pre_items + tail_items);
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((unsigned)std::min(items, kSms * (3 - NT)));
-    cfg.blockDim = dim3(F::kThreads);
-    cfg.dynamicSmemBytes = F::kSmem;
-    cfg.stream = s;
-    cudaLaunchAttribute attr{};
-    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr.val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = &attr;
-    cfg.numAttrs = beside ? 1 : 0;
-    return cudaLaunchKernelEx(&cfg, kern, p, (int)pre_items, items, joined, direct);
+    const int items = (int)(pre_items + tail_items), grid = std::min(items, kSms * (3 - NT));
+    kern<<<grid, F::kThreads, F::kSmem, s>>>(p, (int)pre_items, items, joined, direct);
+    return cudaGetLastError();
 }
 template <int D>
 cudaError_t launch_d(const Params& p, int row_tiles, int64_t pre_items, int64_t tail_items, bool joined, bool direct,
-                     bool beside, cudaStream_t s) {
-    return row_tiles == 2 ? launch<D, 2>(p, pre_items, tail_items, joined, direct, beside, s)
-                          : launch<D, 1>(p, pre_items, tail_items, joined, direct, beside, s);
+                     cudaStream_t s) {
+    return row_tiles == 2 ? launch<D, 2>(p, pre_items, tail_items, joined, direct, s)
+                          : launch<D, 1>(p, pre_items, tail_items, joined, direct, s);
 }
 
 }  // namespace
 
 cudaError_t launch_tc(const Params& p, int D, int row_tiles, int64_t pre_items, int64_t tail_items, bool joined,
-                      bool direct, bool beside, cudaStream_t s) {
-    return D == 64 ? launch_d<64>(p, row_tiles, pre_items, tail_items, joined, direct, beside, s)
-                   : launch_d<128>(p, row_tiles, pre_items, tail_items, joined, direct, beside, s);
+                      bool direct, cudaStream_t s) {
+    return D == 64 ? launch_d<64>(p, row_tiles, pre_items, tail_items, joined, direct, s)
+                   : launch_d<128>(p, row_tiles, pre_items, tail_items, joined, direct, s);
 }
 
 }  // namespace prefix
