@@ -452,7 +452,7 @@ gdn_status prefix_attention(const gdn_prefix_problem* p, const void* q, const vo
     } else if (gdn::prefix::launch_simt(*prm, f.head_dim, bf16, stream) != cudaSuccess) {
         return GDN_ERR_CUDA;
     }
-    return gdn::prefix::launch_join(*prm, f.head_dim, bf16, pl.parts(), pl.tc, stream) == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
+    return gdn::prefix::launch_join(*prm, f.head_dim, bf16, pl.parts(), stream) == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
 }
 
 }  // namespace

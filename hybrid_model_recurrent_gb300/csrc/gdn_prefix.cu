@@ -154,7 +154,6 @@ __global__ void __launch_bounds__(32 * kJoinWarps) prefix_join_kernel(const __gr
     const int nG = p.n * p.G, row = g * 32 + lane;
     const bool valid = row < p.B * nG;
     const int64_t step = (int64_t)p.Hkv * p.groups, first = (int64_t)h * p.groups + g;
-    asm volatile("griddepcontrol.wait;" ::: "memory");   // the parts (nothing to wait for in a plain launch)
     const float2* ml = p.part_ml + first * 32 + lane;
     float m = -INFINITY;
 #pragma unroll 4
@@ -215,17 +214,9 @@ cudaError_t part(const Params& p, cudaStream_t s) {
     return cudaGetLastError();
 }
 template <int D, typename T>
-cudaError_t join(const Params& p, int parts, bool beside, cudaStream_t s) {
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((unsigned)(p.Hkv * p.groups * (D / kJoinCols)));
-    cfg.blockDim = dim3(32 * kJoinWarps);
-    cfg.stream = s;
-    cudaLaunchAttribute attr{};
-    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr.val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = &attr;
-    cfg.numAttrs = beside ? 1 : 0;
-    return cudaLaunchKernelEx(&cfg, prefix_join_kernel<D, T>, p, parts);
+cudaError_t join(const Params& p, int parts, cudaStream_t s) {
+    prefix_join_kernel<D, T><<<(unsigned)(p.Hkv * p.groups * (D / kJoinCols)), 32 * kJoinWarps, 0, s>>>(p, parts);
+    return cudaGetLastError();
 }
 
 }  // namespace
@@ -235,10 +226,10 @@ cudaError_t launch_simt(const Params& p, int D, bool bf16, cudaStream_t s) {
     if (D == 64) return bf16 ? part<64, __nv_bfloat16>(p, s) : part<64, float>(p, s);
     return bf16 ? part<128, __nv_bfloat16>(p, s) : part<128, float>(p, s);
 }
-cudaError_t launch_join(const Params& p, int D, bool bf16, int parts, bool beside, cudaStream_t s) {
-    if (D == 32) return bf16 ? join<32, __nv_bfloat16>(p, parts, beside, s) : join<32, float>(p, parts, beside, s);
-    if (D == 64) return bf16 ? join<64, __nv_bfloat16>(p, parts, beside, s) : join<64, float>(p, parts, beside, s);
-    return bf16 ? join<128, __nv_bfloat16>(p, parts, beside, s) : join<128, float>(p, parts, beside, s);
+cudaError_t launch_join(const Params& p, int D, bool bf16, int parts, cudaStream_t s) {
+    if (D == 32) return bf16 ? join<32, __nv_bfloat16>(p, parts, s) : join<32, float>(p, parts, s);
+    if (D == 64) return bf16 ? join<64, __nv_bfloat16>(p, parts, s) : join<64, float>(p, parts, s);
+    return bf16 ? join<128, __nv_bfloat16>(p, parts, s) : join<128, float>(p, parts, s);
 }
 
 }  // namespace prefix

@@ -88,8 +88,7 @@ cudaError_t launch_simt(const Params& p, int D, bool bf16, cudaStream_t stream);
 // rows (pre_items = 0); direct: the items write o and lse themselves (one part in all)
 cudaError_t launch_tc(const Params& p, int D, int row_tiles, int64_t pre_items, int64_t tail_items, bool joined,
                       bool direct, cudaStream_t stream);
-// `beside`: launched so that it starts up beside the parts (which let it) and waits for them itself
-cudaError_t launch_join(const Params& p, int D, bool bf16, int parts, bool beside, cudaStream_t stream);
+cudaError_t launch_join(const Params& p, int D, bool bf16, int parts, cudaStream_t stream);
 
 }  // namespace prefix
 }  // namespace gdn

@@ -11,8 +11,8 @@
 //
 // Roles: warps 0 .. 4 NT - 1 softmax (one warpgroup a row tile), then one MMA-issuing thread and one copying thread.
 // K and V tiles arrive by TMA in a ring of ST tiles; with NT = 2 both row tiles use each tile, and one tile's softmax
-// runs beside the other's products (an item of at most 128 rows uses one).  With NT = 1 two CTAs share a multiprocessor and overlap each other instead.  The
-// grid is one wave and each CTA takes items in turn, the copies running ahead into the next one.
+// runs beside the other's products (an item of at most 128 rows uses one).  With NT = 1 two CTAs share a multiprocessor and overlap each other instead.  A
+// CTA takes one item after the other, the copies running ahead into the next one.
 //
 // A masked token's score is replaced (not multiplied), and value rows past the range are zeroed in shared memory
 // before the product, so nothing that lies past a tail's end reaches a result.
@@ -63,7 +63,7 @@ struct Cfg {
     static constexpr int ST = NT == 2 ? (D == 128 ? 5 : 8) : (D == 128 ? 2 : 5);
     static constexpr int kRing = NT * kTile;                               // after the Q tiles
     static constexpr int kBar = kRing + ST * kTile;
-    static constexpr int kSmem = kBar + 256 + 1024;
+    static constexpr int kSmem = kBar + 512 + 1024;
     // softmax warpgroups, then a warp that issues products and one that issues copies; with NT = 2 two idle warps fill up
     // their warpgroup, which then hands registers to the others
     static constexpr int kThreads = NT == 2 ? 384 : 192;
@@ -129,8 +129,7 @@ __device__ __forceinline__ Item item_at(const Params& p, int item, int pre_items
 
 template <int D, int NT>
 __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, NT == 1 ? 2 : 1)
-    prefix_tc_kernel(const __grid_constant__ Params p, const int pre_items, const int items, const bool joined,
-                     const bool direct) {
+    prefix_tc_kernel(const __grid_constant__ Params p, const int pre_items, const bool joined, const bool direct) {
     using F = Cfg<D, NT>;
     extern __shared__ unsigned char smem_raw[];
     unsigned char* smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
@@ -143,14 +142,16 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, NT == 1 ? 2 : 1)
     uint64_t* o_full = q_ready + NT;                                 // [NT] every product of an item done
     uint32_t* tslot = reinterpret_cast<uint32_t*>(o_full + NT);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tslot + 1);
-    int* issued = reinterpret_cast<int*>(tslot + 2);                 // tiles whose copy was issued
+    int* issued = reinterpret_cast<int*>(tslot + 2);                 // tiles whose copy was issued; items asked for
     uint64_t* end = reinterpret_cast<uint64_t*>(tslot + 4);          // every product done
     uint64_t* q_asked = end + 1;                                     // the first item's Q loads are under way
-    static_assert((2 * F::ST + 4 * NT) * 8 + 32 <= 256, "barrier area");
+    uint64_t* n_full = q_asked + 1;                                  // [2] the answer to a request for another item
+    uint64_t* n_empty = n_full + 2;                                  // [2] read by every role
+    unsigned char* answer = reinterpret_cast<unsigned char*>(((uintptr_t)(n_empty + 2) + 15) & ~(uintptr_t)15);   // [2][16]
+    static_assert((2 * F::ST + 4 * NT) * 8 + 32 + 80 <= 512, "barrier area");
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const uint64_t limit = p.wait_limit_ns;
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");   // the join starts up meanwhile and waits for this grid
 
     if (warp == 0) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(tslot)),
@@ -169,8 +170,9 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, NT == 1 ? 2 : 1)
         }
         mbar_init(end, 1);
         mbar_init(q_asked, NT * 128);
+        for (int i = 0; i < 2; ++i) mbar_init(&n_full[i], 1), mbar_init(&n_empty[i], 1 + 4 * NT);
         *abort_flag = 0;
-        *issued = 0;
+        issued[0] = issued[1] = 0;
         fence_barrier_init();
     }
     tc_fence_before();
@@ -181,6 +183,30 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, NT == 1 ? 2 : 1)
 
     // 384 threads start with 168 registers each (64512 in all): 256 x 200 + 128 x 96 = 63488
     constexpr bool kKeep = NT == 2;   // a row's 128 scores stay in registers between the maximum and the weights
+
+    // The grid has a CTA an item, and a running CTA takes over items whose CTAs have not started (cluster launch control):
+    // lengths differ, and the items of a fixed share of them summed up to a third more for the unluckiest CTA.  The copying
+    // thread asks for the next item when it begins one, and every role reads the answer.  -1: nothing is left.
+    auto answered = [&](int n) {
+        uint32_t some, x;
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t.reg .b128 r;\n\tld.shared.b128 r, [%2];\n\t"
+            "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, r;\n\tselp.u32 %0, 1, 0, p;\n\tmov.u32 %1, 0;\n\t"
+            "@p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %1, r;\n\t}"
+            : "=r"(some), "=r"(x)
+            : "r"(smem_addr(answer + 16 * (n & 1)))
+            : "memory");
+        return some ? (int)x : -1;
+    };
+    // the item after the CTA's n-th, for a warp; gives up as a wait does
+    auto next_item = [&](int n, bool& ok) {
+        ok = warp_wait(&n_full[n & 1], n >> 1);
+        if (!ok) return -1;
+        const int item = answered(n);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&n_empty[n & 1]);
+        return item;
+    };
 
     // Every role walks the CTA's items; tiles are counted through all of them (it: tiles so far, K of tile i is copy 2 i,
     // V copy 2 i + 1), so the copies of the next item begin while the last one is still computed.
@@ -195,7 +221,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, NT == 1 ? 2 : 1)
             };
             bool ok = true;
             int it = 0, tiles[NT] = {}, nth[NT] = {};   // tiles of the ring; tiles and items of each row tile
-            for (int item = blockIdx.x; ok && item < items; item += gridDim.x) {
+            for (int item = blockIdx.x, nn = 0; ok && item >= 0; item = ok ? next_item(nn++, ok) : -1) {
                 const Item x = item_at<NT>(p, item, pre_items, joined);
                 const int n = x.n_tiles, na = x.na;
                 if (n == 0) continue;
@@ -252,7 +278,24 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, NT == 1 ? 2 : 1)
             if (lane == 0) {
                 bool ok = true;
                 int seq = 0;   // (the copies of a whole wave, asked for first, keep the Q loads waiting for 5 us)
-                for (int item = blockIdx.x; ok && item < items; item += gridDim.x) {
+                for (int item = blockIdx.x, nn = 0; ok && item >= 0; ++nn) {
+                    const int k = nn & 1;
+                    // Asked for once the item's first copy is under way: a CTA that has only just started would take over
+                    // what the next multiprocessor is about to start.
+                    auto ask = [&] {
+                        if (nn >= 2) {
+                            if (!wait_bar(&n_empty[k], (uint32_t)(nn / 2 - 1) & 1u, abort_flag, limit)) return false;
+                            proxy_fence();   // the roles' reads of the answer before it is overwritten
+                        }
+                        mbar_arrive_expect_tx(&n_full[k], 16);
+                        asm volatile(
+                            "clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::
+                                "r"(smem_addr(answer + 16 * k)),
+                            "r"(smem_addr(&n_full[k]))
+                            : "memory");
+                        issued[1] = nn + 1;
+                        return true;
+                    };
                     const Item x = item_at<NT>(p, item, pre_items, joined);
                     for (int c = 0; c < 2 * x.n_tiles; ++c, ++seq) {
                         const int s = seq % F::ST, j = c >> 1;
@@ -264,15 +307,20 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, NT == 1 ? 2 : 1)
                         mbar_arrive_expect_tx(&full[s], F::kTile);
                         const bool v = c & 1;
 #pragma unroll
-                        for (int k = 0; k < D / 64; ++k) {
+                        for (int y = 0; y < D / 64; ++y) {
                             if (j < x.n1)
-                                tma_load_3d(dst + k * 16384, v ? &p.tm_vp : &p.tm_kp, k * 64, x.h, x.lo1 + j * kKeys, &full[s]);
+                                tma_load_3d(dst + y * 16384, v ? &p.tm_vp : &p.tm_kp, y * 64, x.h, x.lo1 + j * kKeys, &full[s]);
                             else
-                                tma_load_4d(dst + k * 16384, v ? &p.tm_vt : &p.tm_kt, k * 64, x.h, x.lo2 + (j - x.n1) * kKeys, x.b0,
+                                tma_load_4d(dst + y * 16384, v ? &p.tm_vt : &p.tm_kt, y * 64, x.h, x.lo2 + (j - x.n1) * kKeys, x.b0,
                                             &full[s]);
                         }
                         *issued = seq + 1;
+                        if (c == 0) ok = ask();
+                        if (!ok) break;
                     }
+                    if (x.n_tiles == 0) ok = ask();
+                    ok = ok && wait_bar(&n_full[k], (uint32_t)(nn >> 1) & 1u, abort_flag, limit);
+                    if (ok) item = answered(nn);
                 }
             }
         }
@@ -286,7 +334,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, NT == 1 ? 2 : 1)
         const int nG = (int)p.by_ng.d;
         bool ok = true, first = true;
         int it = 0, mine = 0, nth = 0;   // tiles of the ring, of this row tile, its items
-        for (int item = blockIdx.x; ok && item < items; item += gridDim.x) {
+        for (int item = blockIdx.x, nn = 0; ok && item >= 0; item = ok ? next_item(nn++, ok) : -1) {
             const Item x = item_at<NT>(p, item, pre_items, joined);
             if (a >= x.na) {   // no rows for this row tile
                 if (first && x.n_tiles > 0) mbar_arrive(q_asked), first = false;
@@ -470,6 +518,8 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, NT == 1 ? 2 : 1)
             const uint64_t drain = limit > kDrainLimitNs ? limit : kDrainLimitNs;
             for (int seq = max(0, *issued - F::ST); seq < *issued; ++seq)
                 tc::drain_phase(&full[seq % F::ST], (uint32_t)((seq / F::ST) & 1), drain);
+            if (issued[1] > 0)
+                tc::drain_phase(&n_full[(issued[1] - 1) & 1], (uint32_t)((issued[1] - 1) >> 1) & 1u, drain);
             tc::drain_phase(end, 0, drain);
             atomicOr(p.status, STATUS_TIMEOUT);
         }
@@ -488,8 +538,7 @@ cudaError_t launch(const Params& p, int64_t pre_items, int64_t tail_items, bool 
     static std::atomic<int> optin[kMaxOptinDevices];
     const cudaError_t e = smem_optin(reinterpret_cast<const void*>(kern), F::kSmem, optin);
     if (e != cudaSuccess) return e;
-    const int items = (int)(pre_items + tail_items), grid = std::min(items, kSms * (3 - NT));
-    kern<<<grid, F::kThreads, F::kSmem, s>>>(p, (int)pre_items, items, joined, direct);
+    kern<<<(unsigned)(pre_items + tail_items), F::kThreads, F::kSmem, s>>>(p, (int)pre_items, joined, direct);
     return cudaGetLastError();
 }
 template <int D>
