@@ -145,10 +145,12 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, NT == 1 ? 2 : 1)
     int* issued = reinterpret_cast<int*>(tslot + 2);                 // tiles whose copy was issued; items asked for
     uint64_t* end = reinterpret_cast<uint64_t*>(tslot + 4);          // every product done
     uint64_t* q_asked = end + 1;                                     // the first item's Q loads are under way
-    uint64_t* n_full = q_asked + 1;                                  // [2] the answer to a request for another item
-    uint64_t* n_empty = n_full + 2;                                  // [2] read by every role
-    unsigned char* answer = reinterpret_cast<unsigned char*>(((uintptr_t)(n_empty + 2) + 15) & ~(uintptr_t)15);   // [2][16]
-    static_assert((2 * F::ST + 4 * NT) * 8 + 32 + 80 <= 512, "barrier area");
+    uint64_t* n_full = q_asked + 1;                                  // [2] an item's description written
+    uint64_t* n_empty = n_full + 2;                                  // [2] and read by every role
+    uint64_t* answered = n_empty + 2;                                // the answer to a request for another item
+    uint4* answer = reinterpret_cast<uint4*>((reinterpret_cast<uintptr_t>(answered + 1) + 15) & ~(uintptr_t)15);
+    Item* described = reinterpret_cast<Item*>(answer + 1);           // [2]
+    static_assert((2 * F::ST + 4 * NT) * 8 + 32 + 5 * 8 + 32 + 2 * sizeof(Item) <= 512, "barrier area");
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const uint64_t limit = p.wait_limit_ns;
@@ -171,6 +173,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, NT == 1 ? 2 : 1)
         mbar_init(end, 1);
         mbar_init(q_asked, NT * 128);
         for (int i = 0; i < 2; ++i) mbar_init(&n_full[i], 1), mbar_init(&n_empty[i], 1 + 4 * NT);
+        mbar_init(answered, 1);
         *abort_flag = 0;
         issued[0] = issued[1] = 0;
         fence_barrier_init();
@@ -186,26 +189,21 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, NT == 1 ? 2 : 1)
 
     // The grid has a CTA an item, and a running CTA takes over items whose CTAs have not started (cluster launch control):
     // lengths differ, and the items of a fixed share of them summed up to a third more for the unluckiest CTA.  The copying
-    // thread asks for the next item when it begins one, and every role reads the answer.  -1: nothing is left.
-    auto answered = [&](int n) {
-        uint32_t some, x;
-        asm volatile(
-            "{\n\t.reg .pred p;\n\t.reg .b128 r;\n\tld.shared.b128 r, [%2];\n\t"
-            "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, r;\n\tselp.u32 %0, 1, 0, p;\n\tmov.u32 %1, 0;\n\t"
-            "@p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %1, r;\n\t}"
-            : "=r"(some), "=r"(x)
-            : "r"(smem_addr(answer + 16 * (n & 1)))
-            : "memory");
-        return some ? (int)x : -1;
-    };
-    // the item after the CTA's n-th, for a warp; gives up as a wait does
-    auto next_item = [&](int n, bool& ok) {
-        ok = warp_wait(&n_full[n & 1], n >> 1);
-        if (!ok) return -1;
-        const int item = answered(n);
+    // thread asks for the next item while it copies one, and describes each item to the other roles ahead of time.
+    auto next_item = [&](int n, Item& x) {   // the CTA's n-th item, for a warp; false: no more, or given up
+        if (!warp_wait(&n_full[n & 1], n >> 1)) return false;
+        x = described[n & 1];
         __syncwarp();
         if (lane == 0) mbar_arrive(&n_empty[n & 1]);
-        return item;
+        return x.n_tiles >= 0;
+    };
+
+    // An item of at most 128 rows takes one row tile; with two, such items take them in turn (every role counts alike), so
+    // that one tile's sums leave and its next Q arrives, 6000 cycles, while the other tile computes.
+    auto takes = [&](const Item& x, int& turn) {
+        const int one = turn;
+        if (NT == 2 && x.na == 1) turn ^= 1;
+        return x.na == 2 ? 3 : 1 << one;   // bit a: row tile a
     };
 
     // Every role walks the CTA's items; tiles are counted through all of them (it: tiles so far, K of tile i is copy 2 i,
@@ -220,10 +218,10 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, NT == 1 ? 2 : 1)
                 if (elect_one()) umma_commit(bar);
             };
             bool ok = true;
-            int it = 0, tiles[NT] = {}, nth[NT] = {};   // tiles of the ring; tiles and items of each row tile
-            for (int item = blockIdx.x, nn = 0; ok && item >= 0; item = ok ? next_item(nn++, ok) : -1) {
-                const Item x = item_at<NT>(p, item, pre_items, joined);
-                const int n = x.n_tiles, na = x.na;
+            int it = 0, turn = 0, tiles[NT] = {}, nth[NT] = {};   // tiles of the ring; tiles and items of each row tile
+            Item x;
+            for (int nn = 0; ok && next_item(nn, x); ++nn) {
+                const int n = x.n_tiles, on = takes(x, turn), last = on >> 1;
                 if (n == 0) continue;
                 auto scores = [&](int a, int i) {
                     const uint64_t q = tile_desc(sbase + a * F::kTile, false), k = tile_desc(slot_at(2 * i), false);
@@ -232,21 +230,22 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, NT == 1 ? 2 : 1)
                         for (int s = 0; s < D / 16; ++s)
                             umma_ss(tbase + a * 128, cols_step(q, s), cols_step(k, s), idesc(kKeys, false, false), s > 0);
                         umma_commit(&s_full[a]);
-                        if (a == na - 1) umma_commit(&empty[2 * i % F::ST]);
+                        if (a == last) umma_commit(&empty[2 * i % F::ST]);
                     }
                 };
                 ok = landed(2 * it);
 #pragma unroll
                 for (int a = 0; a < NT; ++a) {
-                    if (a < na && ok) ok = warp_wait(&q_ready[a], nth[a]);
-                    if (a < na && ok) scores(a, it);
+                    if (!(on >> a & 1)) continue;
+                    ok = ok && warp_wait(&q_ready[a], nth[a]);
+                    if (ok) scores(a, it);
                 }
                 for (int j = 0; ok && j < n; ++j) {
                     const int i = it + j, vs = 2 * i + 1;
                     ok = landed(vs);
 #pragma unroll
                     for (int a = 0; a < NT; ++a) {
-                        if (a >= na) break;
+                        if (!(on >> a & 1)) continue;
                         ok = ok && warp_wait(&p_ready[a], tiles[a] + j);
                         if (!ok) break;
                         tc_fence_after();
@@ -256,10 +255,10 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, NT == 1 ? 2 : 1)
                             for (int s = 0; s < kKeys / 16; ++s)
                                 umma_ts(tbase + F::kO + a * D, tbase + a * 128 + 8 * s, rows_step(v, s), idesc(D, false, true),
                                         j > 0 || s > 0);
-                            if (a == na - 1) umma_commit(&empty[vs % F::ST]);
+                            if (a == last) umma_commit(&empty[vs % F::ST]);
                         }
                         if (j + 1 < n) {
-                            if (a == 0) ok = landed(2 * i + 2);
+                            ok = landed(2 * i + 2);
                             if (!ok) break;
                             scores(a, i + 1);
                         } else {
@@ -270,7 +269,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, NT == 1 ? 2 : 1)
                 it += n;
 #pragma unroll
                 for (int a = 0; a < NT; ++a)
-                    if (a < na) tiles[a] += n, ++nth[a];
+                    if (on >> a & 1) tiles[a] += n, ++nth[a];
             }
             done(end);   // also after giving up: the end waits for the products in flight
         } else if (warp == NT * 4 + 1) {
@@ -278,25 +277,29 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, NT == 1 ? 2 : 1)
             if (lane == 0) {
                 bool ok = true;
                 int seq = 0;   // (the copies of a whole wave, asked for first, keep the Q loads waiting for 5 us)
-                for (int item = blockIdx.x, nn = 0; ok && item >= 0; ++nn) {
+                int item = blockIdx.x;
+                for (int nn = 0; ok; ++nn) {
                     const int k = nn & 1;
+                    if (nn >= 2) ok = wait_bar(&n_empty[k], (uint32_t)(nn / 2 - 1) & 1u, abort_flag, limit);
+                    if (!ok) break;
+                    Item x;
+                    if (item >= 0) x = item_at<NT>(p, item, pre_items, joined);
+                    else x.n_tiles = -1;
+                    described[k] = x;
+                    mbar_arrive(&n_full[k]);
+                    if (item < 0) break;
                     // Asked for once the item's first copy is under way: a CTA that has only just started would take over
                     // what the next multiprocessor is about to start.
                     auto ask = [&] {
-                        if (nn >= 2) {
-                            if (!wait_bar(&n_empty[k], (uint32_t)(nn / 2 - 1) & 1u, abort_flag, limit)) return false;
-                            proxy_fence();   // the roles' reads of the answer before it is overwritten
-                        }
-                        mbar_arrive_expect_tx(&n_full[k], 16);
+                        proxy_fence();   // the last answer has been read
+                        mbar_arrive_expect_tx(answered, 16);
                         asm volatile(
                             "clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::
-                                "r"(smem_addr(answer + 16 * k)),
-                            "r"(smem_addr(&n_full[k]))
+                                "r"(smem_addr(answer)),
+                            "r"(smem_addr(answered))
                             : "memory");
                         issued[1] = nn + 1;
-                        return true;
                     };
-                    const Item x = item_at<NT>(p, item, pre_items, joined);
                     for (int c = 0; c < 2 * x.n_tiles; ++c, ++seq) {
                         const int s = seq % F::ST, j = c >> 1;
                         ok = !(p.stall_after >= 0 && seq / 2 >= p.stall_after) &&   // testing hook
@@ -315,12 +318,21 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, NT == 1 ? 2 : 1)
                                             &full[s]);
                         }
                         *issued = seq + 1;
-                        if (c == 0) ok = ask();
-                        if (!ok) break;
+                        if (c == 0) ask();
                     }
-                    if (x.n_tiles == 0) ok = ask();
-                    ok = ok && wait_bar(&n_full[k], (uint32_t)(nn >> 1) & 1u, abort_flag, limit);
-                    if (ok) item = answered(nn);
+                    if (x.n_tiles == 0) ask();
+                    ok = ok && wait_bar(answered, (uint32_t)nn & 1u, abort_flag, limit);
+                    if (!ok) break;
+                    uint32_t some, first;
+                    asm volatile(
+                        "{\n\t.reg .pred p;\n\t.reg .b128 r;\n\tld.shared.b128 r, [%2];\n\t"
+                        "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, r;\n\tselp.u32 %0, 1, 0, p;\n\t"
+                        "mov.u32 %1, 0;\n\t"
+                        "@p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %1, r;\n\t}"
+                        : "=r"(some), "=r"(first)
+                        : "r"(smem_addr(answer))
+                        : "memory");
+                    item = some ? (int)first : -1;
                 }
             }
         }
@@ -333,15 +345,16 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, NT == 1 ? 2 : 1)
         const float scale = fmaxf(fabsf(p.scale_log2), 1.17549435e-38f);
         const int nG = (int)p.by_ng.d;
         bool ok = true, first = true;
-        int it = 0, mine = 0, nth = 0;   // tiles of the ring, of this row tile, its items
-        for (int item = blockIdx.x, nn = 0; ok && item >= 0; item = ok ? next_item(nn++, ok) : -1) {
-            const Item x = item_at<NT>(p, item, pre_items, joined);
-            if (a >= x.na) {   // no rows for this row tile
+        int it = 0, turn = 0, mine = 0, nth = 0;   // tiles of the ring, of this row tile, its items
+        Item x;
+        for (int nn = 0; ok && next_item(nn, x); ++nn) {
+            const int on = takes(x, turn);
+            if (!(on >> a & 1)) {   // no rows for this row tile
                 if (first && x.n_tiles > 0) mbar_arrive(q_asked), first = false;
                 it += x.n_tiles;
                 continue;
             }
-            const int R = x.row0 + a * kRows + r;
+            const int R = x.row0 + (on == 3 ? a * kRows : 0) + r;
             const bool valid = R < x.rows;
             int e, g;
             const int bs = p.by_ng.divmod(R, &e), b = x.stacked ? bs : x.b0;   // (one request's rows are below n G, or invalid)
@@ -449,7 +462,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, NT == 1 ? 2 : 1)
                     l += (sum0.x + sum0.y) + (sum1.x + sum1.y);
                     tmem_st_wait();
                 }
-                if (a == 0 && j >= x.n1 && t0 + kKeys > x.hi2) {
+                if ((a == 0 || on != 3) && j >= x.n1 && t0 + kKeys > x.hi2) {
                     // the tail's last tile: zero the value rows past the range
                     const int vs = 2 * it + 1;
                     ok = warp_wait(&full[vs % F::ST], vs / F::ST);
@@ -519,7 +532,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, NT == 1 ? 2 : 1)
             for (int seq = max(0, *issued - F::ST); seq < *issued; ++seq)
                 tc::drain_phase(&full[seq % F::ST], (uint32_t)((seq / F::ST) & 1), drain);
             if (issued[1] > 0)
-                tc::drain_phase(&n_full[(issued[1] - 1) & 1], (uint32_t)((issued[1] - 1) >> 1) & 1u, drain);
+                tc::drain_phase(answered, (uint32_t)(issued[1] - 1) & 1u, drain);
             tc::drain_phase(end, 0, drain);
             atomicOr(p.status, STATUS_TIMEOUT);
         }
