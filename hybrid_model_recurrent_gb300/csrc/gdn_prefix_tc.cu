@@ -367,25 +367,30 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, NT == 1 ? 2 : 1)
             if (x.n_tiles > 0) {
                 // a warp loads its own 32 rows, 16 bytes a lane, as many rows at a time as its lanes cover (each lane knows
                 // one row's address)
-                constexpr int kLanes = D / 8, kAtOnce = 32 / kLanes, kLoads = 32 / kAtOnce;
+                constexpr int kLanes = D / 8, kAtOnce = 32 / kLanes;
                 const uint32_t flip = p.scale_log2 < 0.f ? 0x80008000u : 0u;
-                const int64_t own = valid ? b * p.q_sb + qi * p.q_sn + head * p.q_sh : -1;
-                const int c = lane % kLanes;
-                uint4 y[kLoads];
+                // past the rows: the item's first row once more, whose results are not stored (its address is good, and
+                // no load waits for a condition)
+                const int64_t own = valid ? b * p.q_sb + qi * p.q_sn + head * p.q_sh
+                                          : (x.stacked ? 0 : b * p.q_sb) + (int64_t)x.h * p.G * p.q_sh;
+                const int c = lane % kLanes, rows = __popc(__ballot_sync(0xffffffffu, valid));
+                for (int k0 = 0; k0 < rows; k0 += 8 * kAtOnce) {   // (rolled, for the instruction cache)
+                    uint4 y[8];
 #pragma unroll
-                for (int i = 0; i < kLoads; ++i) {
-                    const int64_t off = __shfl_sync(0xffffffffu, own, i * kAtOnce + lane / kLanes);
-                    y[i] = off >= 0 ? *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.q) + off + 8 * c)
-                                    : make_uint4(0, 0, 0, 0);
+                    for (int i = 0; i < 8; ++i) {
+                        const int64_t off = __shfl_sync(0xffffffffu, own, k0 + i * kAtOnce + lane / kLanes);
+                        y[i] = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.q) + off + 8 * c);
+                    }
+                    if (first && k0 + 8 * kAtOnce >= rows) mbar_arrive(q_asked);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const int row = (r & 96) + k0 + i * kAtOnce + lane / kLanes;
+                        *reinterpret_cast<uint4*>(smem + a * F::kTile + (c >> 3) * 16384 + row * 128 + (((c & 7) ^ (row & 7)) << 4)) =
+                            make_uint4(y[i].x ^ flip, y[i].y ^ flip, y[i].z ^ flip, y[i].w ^ flip);
+                    }
                 }
-                if (first) mbar_arrive(q_asked);
+                if (first && rows == 0) mbar_arrive(q_asked);
                 first = false;
-#pragma unroll
-                for (int i = 0; i < kLoads; ++i) {
-                    const int row = (r & 96) + i * kAtOnce + lane / kLanes;
-                    *reinterpret_cast<uint4*>(smem + a * F::kTile + (c >> 3) * 16384 + row * 128 + (((c & 7) ^ (row & 7)) << 4)) =
-                        make_uint4(y[i].x ^ flip, y[i].y ^ flip, y[i].z ^ flip, y[i].w ^ flip);
-                }
                 proxy_fence();
                 mbar_arrive(&q_ready[a]);
             }
@@ -423,7 +428,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, NT == 1 ? 2 : 1)
                         }
                     }
                     const float top = fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3])) * scale;
-                    const bool rise = top > m + kRise || m == -INFINITY;
+                    const bool rise = valid && (top > m + kRise || m == -INFINITY);
                     if (__any_sync(0xffffffffu, rise)) {
                         const float mn = rise ? fmaxf(m, top) : m;
                         const float f = mn == -INFINITY ? 1.f : ex2(m - mn);
