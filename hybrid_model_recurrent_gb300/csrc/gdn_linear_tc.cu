@@ -21,10 +21,11 @@
 // a chunk moved 590 KB through shared memory, now 430 KB, and the room of K' gives every input tile a second buffer.
 //
 // One CTA takes one (job, head) from its first chunk to its last.  Roles:
-//   state  (warps 0-3):  S out of TMEM into its bf16 copy, S scaled by a^n in place; V^T -> V' hi and lo in TMEM;
-//                        checkpoints, initial, final state; key and value rows past a cut chunk zeroed
+//   state  (warps 0-3):  S out of TMEM into its bf16 copy, S scaled by a^n in place; half of V^T -> V' hi and lo in
+//                        TMEM; checkpoints, initial, final state; key and value rows past a cut chunk zeroed
 //   tokens (warps 4-7):  the first half of G's columns -> P in TMEM; a^{t+1} into O
-//   output (warps 8-11): the second half of them; O to memory, staged for TMA
+//   output (warps 8-11): the second half of P; the other half of the next V'; O to memory, staged for TMA
+// (without a readout the last two only form V')
 //   one thread each that issues the products, the copies of K and V, of Q and of staged output
 // They hand over through mbarriers, one phase a chunk, and no barrier completes a phase before everyone who waits for
 // the last one has seen it (a parity tells only two phases apart).  The state's own chain (S and V' converted, Q S^T and
@@ -139,7 +140,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_tc_kernel(const __grid_con
     uint64_t* o_done = st_done + 1;     // O
     uint64_t* s_ready = o_done + 1;     // state: the bf16 copy written, S scaled
     uint64_t* p_ready = s_ready + 1;    // tokens, output: P written, O scaled
-    uint64_t* v_ready = p_ready + 1;    // state: V' written, key and value rows zeroed
+    uint64_t* v_ready = p_ready + 1;    // V' written, key and value rows zeroed
     uint64_t* o_free = v_ready + 1;     // output: O read
     uint64_t* o_staged = o_free + 1;    // output: a chunk's output staged
     uint64_t* o_left = o_staged + 1;    // the staged output has been copied out
@@ -163,8 +164,9 @@ __global__ void __launch_bounds__(kThreads, 1) linear_tc_kernel(const __grid_con
     if (tid == 0) {
         for (int i = 0; i < 2 * NT + 4; ++i) mbar_init(&full[i], 1);
         mbar_init(o_left, 1);
-        for (uint64_t* b : {s_ready, v_ready, o_free, o_staged}) mbar_init(b, 128);
+        for (uint64_t* b : {s_ready, o_free, o_staged}) mbar_init(b, 128);
         mbar_init(p_ready, 256);
+        mbar_init(v_ready, READOUT ? 256 : 384);
         mbar_init(end, 1);
         *abort_flag = 0;
         issued[0] = issued[1] = issued[2] = 0;
@@ -233,6 +235,17 @@ __global__ void __launch_bounds__(kThreads, 1) linear_tc_kernel(const __grid_con
             tmem_st_16x128b_x4(trow + (16u * m << 16) + T_VH + 16 * sb, hi[m]);
             tmem_st_16x128b_x4(trow + (16u * m << 16) + T_VL + 16 * sb, lo[m]);
         }
+    };
+    // Two blocks of chunk j's V', by a role that has not waited for the last update yet.
+    auto form_values = [&](int j, int n, int sb) {
+        if (!warp_wait(&full[bar(1, j)], phase(1, j)) || (j > 0 && !warp_wait(st_done, j - 1))) return false;
+        tc_fence_after();
+#pragma unroll 1
+        for (int i = sb; i < sb + 2; ++i) scale_values(j, n, i);
+        tmem_st_wait();
+        tc_fence_before();
+        mbar_arrive(v_ready);
+        return true;
     };
     // Column block cb of P over G's columns, for this warp's token rows [32 rb, 32 rb + 32), lane a row; diag[i] =
     // a^{lane - i}, the same in every chunk.
@@ -364,13 +377,15 @@ __global__ void __launch_bounds__(kThreads, 1) linear_tc_kernel(const __grid_con
             if (READOUT) proxy_fence();
             tc_fence_before();
             mbar_arrive(s_ready);
-            // then V', on the chain as well
-            ok = warp_wait(&full[bar(1, j)], phase(1, j));
-            if (!ok) break;
+            // then half of V', on the chain as well (without a readout the tokens role has nothing else to do)
+            if (READOUT) {
+                ok = warp_wait(&full[bar(1, j)], phase(1, j));
+                if (!ok) break;
 #pragma unroll 1
-            for (int sb = 0; sb < 4; ++sb) scale_values(j, w.n, sb);
+                for (int sb = 0; sb < 2; ++sb) scale_values(j, w.n, sb);
+            }
             if (w.n < kTok) {
-                ok = warp_wait(&full[bar(0, j)], phase(0, j));
+                ok = warp_wait(&full[bar(0, j)], phase(0, j)) && warp_wait(&full[bar(1, j)], phase(1, j));
                 if (!ok) break;
                 if (row >= w.n) {
 #pragma unroll 1
@@ -403,6 +418,9 @@ __global__ void __launch_bounds__(kThreads, 1) linear_tc_kernel(const __grid_con
         }
     } else if (warp < 8) {
         // ---- tokens: lane = token row, this warp's rows are [32 rb, 32 rb + 32) ----
+        if (!READOUT) {
+            for (int j = 0; w.more() && form_values(j, w.n, 0); w.next()) ++j;
+        }
         if (READOUT) {
             const float rowf = pw[lane], inter = pw[row + 1];
             const float2 inter2 = make_float2(inter, inter);
@@ -434,14 +452,17 @@ __global__ void __launch_bounds__(kThreads, 1) linear_tc_kernel(const __grid_con
         }
     } else if (warp < 12) {
         // ---- output: lane = token row ----
-        if (READOUT) {
+        if (!READOUT) {
+            for (int j = 0; w.more() && form_values(j, w.n, 2); w.next()) ++j;
+        } else if (w.more() && form_values(0, w.n, 2)) {
             const bool wide = (reinterpret_cast<uintptr_t>(p.o) & 31) == 0;
             const float2 scale2 = make_float2(p.scale, p.scale);
             const float rowf = pw[lane];
             float diag[32];
 #pragma unroll
             for (int i = 0; i < 32; ++i) diag[i] = pw[max(lane - i, 0)];
-            for (int j = 0; w.more(); w.next(), ++j) {
+            for (int j = 0; w.more(); ++j) {
+                const int pos = w.pos, n = w.n;
                 if (!warp_wait(g_done, j)) break;
                 tc_fence_after();
 #pragma unroll 1
@@ -449,6 +470,9 @@ __global__ void __launch_bounds__(kThreads, 1) linear_tc_kernel(const __grid_con
                 tmem_st_wait();
                 tc_fence_before();
                 mbar_arrive(p_ready);
+                // the other half of the next chunk's V', for which the update is done before this chunk's O
+                w.next();
+                if (w.more() && !form_values(j + 1, w.n, 2)) break;
                 if (!warp_wait(o_done, j)) break;
                 tc_fence_after();
                 // the whole row into registers first, so that the next chunk's O can begin before the stores are through
@@ -468,16 +492,16 @@ __global__ void __launch_bounds__(kThreads, 1) linear_tc_kernel(const __grid_con
                 // A whole chunk is staged and copied out by TMA: a thread holds a row, and stores of 32 rows at a time,
                 // 32 bytes each, kept the load/store unit from everyone for 1200 cycles.  A cut one is stored like that.
                 if (j > 0 && !warp_wait(o_left, j - 1)) break;
-                if (w.n == kTok) {
+                if (n == kTok) {
 #pragma unroll
                     for (int c = 0; c < DV / 8; ++c)
                         *reinterpret_cast<uint4*>(smem + OFF_O + (c >> 3) * 16384 + sw128(row, (c & 7) * 8)) =
                             make_uint4(u[c >> 1][(c & 1) * 4], u[c >> 1][(c & 1) * 4 + 1], u[c >> 1][(c & 1) * 4 + 2],
                                        u[c >> 1][(c & 1) * 4 + 3]);
                     proxy_fence();
-                } else if (row < w.n) {
+                } else if (row < n) {
                     __nv_bfloat16* dst =
-                        static_cast<__nv_bfloat16*>(p.o) + ((job.tok_begin + w.pos + row) * p.H + h) * (int64_t)DV;
+                        static_cast<__nv_bfloat16*>(p.o) + ((job.tok_begin + pos + row) * p.H + h) * (int64_t)DV;
 #pragma unroll
                     for (int c = 0; c < DV / 16; ++c) store32(dst + 16 * c, u[c], wide);
                 }

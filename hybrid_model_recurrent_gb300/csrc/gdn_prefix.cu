@@ -140,10 +140,10 @@ __global__ void __launch_bounds__(128) prefix_part_kernel(const __grid_constant_
     }
 }
 
-// o = sum_p 2^(m_p - m) o_p / sum_p 2^(m_p - m) l_p.  A CTA joins 8 columns of a group of 32 rows, lane = row, whole lines
+// o = sum_p 2^(m_p - m) o_p / sum_p 2^(m_p - m) l_p.  A CTA joins 16 columns of a group of 32 rows, lane = row, whole lines
 // at a time; its 8 warps share the parts and add up in shared memory, so that few rows of many parts are not read one
 // behind the other.  Bound by reading the parts (from L2).
-constexpr int kJoinCols = 8, kJoinWarps = 8;
+constexpr int kJoinCols = 16, kJoinWarps = 8;
 template <int D, typename T>
 __global__ void __launch_bounds__(32 * kJoinWarps) prefix_join_kernel(const __grid_constant__ Params p, int parts) {
     constexpr int CC = kJoinCols, W = kJoinWarps;
@@ -202,7 +202,10 @@ __global__ void __launch_bounds__(32 * kJoinWarps) prefix_join_kernel(const __gr
     } out;
 #pragma unroll
     for (int j = 0; j < CC; ++j) put(&out.x[j], acc[j] * inv);
-    *reinterpret_cast<Out*>(static_cast<T*>(p.o) + at * D + c0) = out;
+    const uint4* src = reinterpret_cast<const uint4*>(&out);
+    uint4* dst = reinterpret_cast<uint4*>(static_cast<T*>(p.o) + at * D + c0);
+#pragma unroll
+    for (int i = 0; i < (int)(sizeof(Out) / 16); ++i) dst[i] = src[i];
     if (p.lse && c0 == 0) p.lse[at] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
 }
 
