@@ -321,16 +321,14 @@ gdn_status check_prefix(const gdn_prefix_problem* p, gdn_prefix_problem& f) {
 
 // In how many ranges to cut `tiles` tiles of tokens that `items` row tiles take, with `slots` CTAs at once: the fewest
 // tile times, counting whole waves, two tile times for a CTA's start and end, and the join's reading and writing of
-// each range's partial sums (at about 10 TB/s from L2, against a tile time of about 1.2 us; a warp of the join reads
-// every eighth part, one behind the other).
+// each range's partial sums (at about 10 TB/s from L2, against a tile time of about 1.2 us).
 int best_splits(int64_t tiles, int64_t items, int64_t slots, int64_t part_bytes) {
     int64_t best = 1;
     double best_cost = 1e300;
     for (int64_t s = 1; s <= std::min<int64_t>(tiles, 256); ++s) {
         const int64_t per = ceil_div(tiles, s);
         if (ceil_div(tiles, per) != s) continue;   // the same ranges as fewer splits
-        const double cost = (double)ceil_div(items * s, slots) * (double)(per + 2) + (double)(s * part_bytes) / 1.2e7 +
-                            0.05 * (double)s;
+        const double cost = (double)ceil_div(items * s, slots) * (double)(per + 2) + (double)(s * part_bytes) / 1.2e7;
         if (cost < best_cost) best_cost = cost, best = s;
     }
     return (int)best;

@@ -327,8 +327,9 @@ cudaError_t scan_types(const Params& p, bool in_bf16, bool out_bf16, cudaStream_
 
 template <int DK>
 cudaError_t step_types(const StepParams& p, bool in_bf16, bool out_bf16, cudaStream_t s) {
-    // rows of a lane: 2 at d_k = 128 keep twice the warps in flight (64 requests x 32 heads: 48 us against 70 with 4)
-    constexpr int R = DK == 128 ? 2 : 4;
+    // rows of a lane: 2 keep twice the warps in flight (64 requests x 32 heads at d = 128: 48 us against 70 with 4; 256 x 32
+    // at d = 64, fp32: 47 against 53); at d_k = 32 a lane has 16 bytes of a row and takes 4
+    constexpr int R = DK >= 64 ? 2 : 4;
     const int64_t warps = (int64_t)p.B * p.H * (p.dv / (4 * R));
     const int per = 4;
     const int grid = (int)((warps + per - 1) / per), threads = 32 * per;

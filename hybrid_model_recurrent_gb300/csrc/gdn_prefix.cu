@@ -140,13 +140,13 @@ __global__ void __launch_bounds__(128) prefix_part_kernel(const __grid_constant_
     }
 }
 
-// o = sum_p 2^(m_p - m) o_p / sum_p 2^(m_p - m) l_p.  A CTA joins 16 columns of a group of 32 rows, lane = row, whole lines
+// o = sum_p 2^(m_p - m) o_p / sum_p 2^(m_p - m) l_p.  A CTA joins CC columns of a group of 32 rows, lane = row, whole lines
 // at a time; its 8 warps share the parts and add up in shared memory, so that few rows of many parts are not read one
 // behind the other.  Bound by reading the parts (from L2).
-constexpr int kJoinCols = 16, kJoinWarps = 8;
-template <int D, typename T>
+constexpr int kJoinWarps = 8;
+template <int D, int CC, typename T>
 __global__ void __launch_bounds__(32 * kJoinWarps) prefix_join_kernel(const __grid_constant__ Params p, int parts) {
-    constexpr int CC = kJoinCols, W = kJoinWarps;
+    constexpr int W = kJoinWarps;
     __shared__ float top[W][32], sum[W][CC + 1][32];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int c0 = blockIdx.x % (D / CC) * CC;
@@ -169,7 +169,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) prefix_join_kernel(const __gr
     float l = 0.f, acc[CC];
 #pragma unroll
     for (int j = 0; j < CC; ++j) acc[j] = 0.f;
-#pragma unroll 2
+#pragma unroll(32 / CC)
     for (int s = warp; s < parts; s += W) {
         const float2 x = valid ? ml[s * step * 32] : make_float2(0.f, 0.f);
         const float* src = p.part_o + ((s * step + first) * D + c0) * 32 + lane;
@@ -218,7 +218,12 @@ cudaError_t part(const Params& p, cudaStream_t s) {
 }
 template <int D, typename T>
 cudaError_t join(const Params& p, int parts, cudaStream_t s) {
-    prefix_join_kernel<D, T><<<(unsigned)(p.Hkv * p.groups * (D / kJoinCols)), 32 * kJoinWarps, 0, s>>>(p, parts);
+    // 16 columns a CTA read each row's weights half as often as 8; few rows take 8, for twice the CTAs (64 rows: 6 us against 8)
+    const int64_t wide = (int64_t)p.Hkv * p.groups * (D / 16);
+    if (wide >= 2 * kSms)
+        prefix_join_kernel<D, 16, T><<<(unsigned)wide, 32 * kJoinWarps, 0, s>>>(p, parts);
+    else
+        prefix_join_kernel<D, 8, T><<<(unsigned)(2 * wide), 32 * kJoinWarps, 0, s>>>(p, parts);
     return cudaGetLastError();
 }
 
