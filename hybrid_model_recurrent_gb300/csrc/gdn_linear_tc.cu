@@ -11,26 +11,30 @@
 // Every power of a is at most 1, so no decay in [0, 1] leaves the range of fp32.  A chunk ends after 128 tokens, at a
 // checkpoint and at the end of its job.  Products, all M = 128 with fp32 sums in TMEM:
 //     G = Q K^T;  O = Q S^T, its rows scaled by a^{t+1} in place, O += P V with P = G masked and decayed;
-//     S += V'^T K with V' = diag(a^{n-1-s}) V
-// V' is not exact in bf16: it is split into hi + lo halves and both are multiplied, so a state loses 2^-16 of an added
-// term, as the delta rule scan's does.  P and the copy of S that the readout multiplies are rounded to bf16 once (half a
-// step, 2^-8 of each term): the readout itself is rounded to bf16, and its error stays of that order.
+//     V'^T K with V' = diag(a^{n-1-s}) V, added to a^n S in registers
+// V' is not exact in bf16: it is split into hi - mid + lo (mid is formed negated and the product negates it back), 24 bits,
+// all multiplied; and the tensor cores' sums, which are not rounded to nearest, run over one chunk only.  So a state is
+// within 5e-7 of itself against 64 bits, as fp32 sums are; with two parts, and the sums running through all chunks, it was
+// within 2.5e-6 and a pass took 0.87 of the time.  P and the copy of S that the readout multiplies are rounded to bf16 once
+// (half a step, 2^-8 of each term): the readout itself is rounded to bf16, and its error stays of that order.
 //
 // What bounds it: shared memory's 128 bytes a cycle, of which a product with both operands there takes nearly all.  So
 // P and V'^T are operands in TMEM: with K' = diag(.) K split in shared memory instead (written, and read again beside V),
 // a chunk moved 590 KB through shared memory, now 430 KB, and the room of K' gives every input tile a second buffer.
 //
 // One CTA takes one (job, head) from its first chunk to its last.  Roles:
-//   state  (warps 0-3):  S out of TMEM into its bf16 copy, S scaled by a^n in place; half of V^T -> V' hi and lo in
-//                        TMEM; checkpoints, initial, final state; key and value rows past a cut chunk zeroed
-//   tokens (warps 4-7):  the first half of G's columns -> P in TMEM; a^{t+1} into O
-//   output (warps 8-11): the second half of P; the other half of the next V'; O to memory, staged for TMA
+//   state  (warps 0-3):  S, a row a thread, in registers: a^n S + the chunk's products; its bf16 copy; checkpoints,
+//                        initial, final state; rows past a cut chunk zeroed
+//   tokens (warps 4-7):  the first half of G's columns -> P and of V^T -> V', both in TMEM; a^{t+1} into O
+//   output (warps 8-11): the second half of P and V'; O to memory, staged for TMA
 // (without a readout the last two only form V')
 //   one thread each that issues the products, the copies of K and V, of Q and of staged output
 // They hand over through mbarriers, one phase a chunk, and no barrier completes a phase before everyone who waits for
-// the last one has seen it (a parity tells only two phases apart).  The state's own chain (S and V' converted, Q S^T and
-// the update multiplied) is the critical path; G, P and P V of a chunk run beside it.  Each role's chunk is written as
-// short rolled loops: unrolled, the roles' code streamed through the instruction cache once a chunk, 1.5 times as slow.
+// the last one has seen it (a parity tells only two phases apart).  The critical path is the products' own order: V' hi and
+// mid of the next chunk are formed while P V and G are multiplied, lo waits in registers until G's columns are free, and the
+// update starts before Q S^T does.  Each role's chunk is written as short rolled loops, the products' issue among them:
+// unrolled, the roles' code streamed through the instruction cache once a chunk (24 products took 3600 cycles to issue
+// instead of 1400).
 //
 // A sequence's tiles may reach past its end into its neighbour's tokens: P and V' are replaced by zeros there and the
 // key and value rows are zeroed, so a neighbour's values, infinities and NaN included, never reach a result.
@@ -48,7 +52,6 @@ namespace {
 
 using tc::idesc;
 using tc::proxy_fence;
-using tc::split_pair;
 using tc::sw128;
 using tc::tc_fence_after;
 using tc::tc_fence_before;
@@ -77,11 +80,20 @@ constexpr int OFF_POW = 7 * kTile;          // a^0 .. a^128; a^128 .. a^0; a^127
 constexpr int OFF_BAR = OFF_POW + 3 * 528;
 constexpr int kSmem = OFF_BAR + 256 + 1024;
 static_assert(kSmem <= 232448, "227 KB of shared memory per block");
-// P, a block of 32 tokens (16 columns) at a time, goes over columns of G that only the writing role reads: blocks 0 and 1
-// over G's first 32 columns (tokens), 2 and 3 over the third (output)
+// With a readout, P and V' lo go over G, each role's over the 64 columns of its tokens, which only it reads: P's two blocks
+// of 32 tokens (16 columns each) first, then V' lo's.
 __host__ __device__ constexpr uint32_t p_block(int cb) { return 128u + 16u * cb + (cb >= 2 ? 32u : 0u); }
-constexpr uint32_t T_S = 0, T_G = 128, T_O = 256, T_VH = 384, T_VL = 448;
+__host__ __device__ constexpr uint32_t lo_block(bool readout, int cb) { return readout ? p_block(cb) + 32u : 128u + 16u * cb; }
+constexpr uint32_t T_S = 0, T_G = 128, T_O = 256, T_VH = 384, T_VM = 448;
 
+// b - z for two values, b as bf16
+__device__ __forceinline__ float2 less(uint32_t b, float2 z) {
+    float2 r;
+    asm("{.reg .b16 l, h; mov.b32 {l, h}, %2; sub.rn.f32.bf16 %0, l, %3; sub.rn.f32.bf16 %1, h, %4;}"
+        : "=f"(r.x), "=f"(r.y)
+        : "r"(b), "f"(z.x), "f"(z.y));
+    return r;
+}
 __device__ __forceinline__ void tma_store_3d(const void* src, const CUtensorMap* tm, int x, int y, int z) {
     asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(
                      reinterpret_cast<uint64_t>(tm)),
@@ -96,10 +108,12 @@ __device__ __forceinline__ void ldsm_x4_trans(uint32_t addr, uint32_t (&r)[4]) {
                  : "r"(addr)
                  : "memory");
 }
-// 16 TMEM lanes x 16 columns: register 2 g + k of lane l goes to TMEM lane 8 k + l / 4, column 4 g + l % 4
-__device__ __forceinline__ void tmem_st_16x128b_x4(uint32_t taddr, const uint32_t (&r)[8]) {
-    asm volatile("tcgen05.st.sync.aligned.16x128b.x4.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(r[0]), "r"(r[1]),
-                 "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]));
+// 16 TMEM lanes x 32 columns: register 2 g + k of lane l goes to TMEM lane 8 k + l / 4, column 4 g + l % 4
+__device__ __forceinline__ void tmem_st_16x128b_x8(uint32_t taddr, const uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.16x128b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]),
+        "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]));
 }
 
 // the chunks of a job, walked alike by every role
@@ -140,15 +154,16 @@ __global__ void __launch_bounds__(kThreads, 1) linear_tc_kernel(const __grid_con
     uint64_t* o_done = st_done + 1;     // O
     uint64_t* s_ready = o_done + 1;     // state: the bf16 copy written, S scaled
     uint64_t* p_ready = s_ready + 1;    // tokens, output: P written, O scaled
-    uint64_t* v_ready = p_ready + 1;    // V' written, key and value rows zeroed
-    uint64_t* o_free = v_ready + 1;     // output: O read
+    uint64_t* v_ready = p_ready + 1;    // V' hi and mid written, key and value rows zeroed
+    uint64_t* lo_ready = v_ready + 1;   // V' lo written
+    uint64_t* o_free = lo_ready + 1;    // output: O read
     uint64_t* o_staged = o_free + 1;    // output: a chunk's output staged
     uint64_t* o_left = o_staged + 1;    // the staged output has been copied out
     uint64_t* end = o_left + 1;         // every product done
     uint32_t* tslot = reinterpret_cast<uint32_t*>(end + 1);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tslot + 1);
     int* issued = reinterpret_cast<int*>(tslot + 2);   // [3] chunks whose K, V, Q copy was issued
-    static_assert((2 * NT + 11) * 8 + 20 <= 256, "barrier area");
+    static_assert((2 * NT + 12) * 8 + 20 <= 256, "barrier area");
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int h = blockIdx.x % p.H;
@@ -166,7 +181,8 @@ __global__ void __launch_bounds__(kThreads, 1) linear_tc_kernel(const __grid_con
         mbar_init(o_left, 1);
         for (uint64_t* b : {s_ready, o_free, o_staged}) mbar_init(b, 128);
         mbar_init(p_ready, 256);
-        mbar_init(v_ready, READOUT ? 256 : 384);
+        mbar_init(v_ready, 384);
+        mbar_init(lo_ready, 256);
         mbar_init(end, 1);
         *abort_flag = 0;
         issued[0] = issued[1] = issued[2] = 0;
@@ -195,61 +211,61 @@ __global__ void __launch_bounds__(kThreads, 1) linear_tc_kernel(const __grid_con
         return tcu::warp_wait_bar(bar, (uint32_t)parity & 1u, abort_flag, limit);
     };
     Walk w(p, job);
-    // Tokens 32 sb .. of V'^T, this warp's 32 value dimensions (TMEM lanes): transposed on the way from shared memory by
-    // ldmatrix, whose fragment (lane l: dimension l / 4, token pair l % 4 of an 8 x 8 matrix) is the 16x128b form's.
-    auto scale_values = [&](int j, int n, int sb) {
-        const int q4 = warp & 3, pr = lane & 3;
+    // 64 tokens from 32 sb of V'^T, 16 of this warp's 32 value dimensions (TMEM lanes): transposed on the way from shared memory by
+    // ldmatrix, whose fragment (lane l: dimension l / 4, token pair l % 4 of an 8 x 8 matrix) is the 16x128b form's.  hi and
+    // mid are stored, lo is handed back.
+    auto scale_values = [&](int j, int n, int sb, int a, uint32_t (&v)[16]) {
+        const int q4 = warp & 3, s0 = 32 * sb + 2 * (lane & 3);   // this lane's tokens s0 + 8 g and the next
         if (32 * q4 >= DV) return;   // rows past d_v: never read
-        // row addresses: token 8 g + (lane & 7) of the block, dimensions 8 (lane / 8) .. of this warp's 32
-        const uint32_t src = sbase + at(1, j) + (q4 >> 1) * 16384 + (32 * sb + (lane & 7)) * 128 +
-                             ((((q4 & 1) * 4 + (lane >> 3)) ^ (lane & 7)) << 4);
-        uint32_t hi[2][8], lo[2][8];   // [16 dimensions][8-token group g, 8 dimensions of those]
-        // every load first: one at a time, each of the four would wait out its latency and its arithmetic's
-        uint32_t v[4][4];
-        float2 f[4];
+        // row addresses, matrix lane / 8 of a load: token 8 (lane / 16) + (lane & 7), dimensions 16 a + 8 (lane / 8 % 2) ..
+        const uint32_t src = sbase + at(1, j) + (q4 >> 1) * 16384 + (32 * sb + 8 * (lane >> 4) + (lane & 7)) * 128 +
+                             ((((q4 & 1) * 4 + 2 * a + (lane >> 3 & 1)) ^ (lane & 7)) << 4);
+        // v: [8-token group g, 8 dimensions of the 16]
 #pragma unroll
-        for (int g = 0; g < 4; ++g) {
-            ldsm_x4_trans(src + g * 8 * 128, v[g]);
-            f[g] = *reinterpret_cast<const float2*>(vp + 32 * sb + 8 * g + 2 * pr);   // a^{127-s}, a^{126-s}
+        for (int i = 0; i < 4; ++i) {
+            uint32_t x[4];
+            ldsm_x4_trans(src + i * 16 * 128, x);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) v[4 * i + k] = x[k];
         }
+        float2 f[8];   // a^{127-s}, a^{126-s}
+#pragma unroll
+        for (int g = 0; g < 8; ++g) f[g] = *reinterpret_cast<const float2*>(vp + s0 + 8 * g);
         if (n < kTok) {
 #pragma unroll
-            for (int g = 0; g < 4; ++g) {
-                const int s = 32 * sb + 8 * g + 2 * pr;   // this lane's tokens s and s + 1
+            for (int g = 0; g < 8; ++g) {
+                const int s = s0 + 8 * g;
                 f[g].x = pw[max(n - 1 - s, 0)], f[g].y = pw[max(n - 2 - s, 0)];
                 // past the chunk: another chunk's or sequence's values, not taken in
                 const uint32_t in = (s < n ? 0xffffu : 0u) | (s + 1 < n ? 0xffff0000u : 0u);
-#pragma unroll
-                for (int m = 0; m < 4; ++m) v[g][m] &= in;
+                v[2 * g] &= in, v[2 * g + 1] &= in;
             }
         }
+        const uint32_t t = trow + (16u * a << 16);
+        float2 z[16];
 #pragma unroll
-        for (int g = 0; g < 4; ++g)
+        for (int i = 0; i < 16; ++i) {
+            z[i] = __fmul2_rn(bf16x2_to_float2(v[i]), f[i >> 1]);
+            v[i] = pack2(z[i].x, z[i].y);
+        }
+        tmem_st_16x128b_x8(t + T_VH + 16 * sb, v);
 #pragma unroll
-            for (int m = 0; m < 4; ++m) {
-                const float2 z = __fmul2_rn(bf16x2_to_float2(v[g][m]), f[g]);
-                split_pair(z.x, z.y, hi[m >> 1][2 * g + (m & 1)], lo[m >> 1][2 * g + (m & 1)]);
-            }
+        for (int i = 0; i < 16; ++i) {
+            z[i] = less(v[i], z[i]);
+            v[i] = pack2(z[i].x, z[i].y);
+        }
+        tmem_st_16x128b_x8(t + T_VM + 16 * sb, v);
 #pragma unroll
-        for (int m = 0; m < 2; ++m) {
-            tmem_st_16x128b_x4(trow + (16u * m << 16) + T_VH + 16 * sb, hi[m]);
-            tmem_st_16x128b_x4(trow + (16u * m << 16) + T_VL + 16 * sb, lo[m]);
+        for (int i = 0; i < 16; ++i) {
+            z[i] = less(v[i], z[i]);
+            v[i] = pack2(z[i].x, z[i].y);
         }
     };
-    // Two blocks of chunk j's V', by a role that has not waited for the last update yet.
-    auto form_values = [&](int j, int n, int sb) {
-        if (!warp_wait(&full[bar(1, j)], phase(1, j)) || (j > 0 && !warp_wait(st_done, j - 1))) return false;
-        tc_fence_after();
-#pragma unroll 1
-        for (int i = sb; i < sb + 2; ++i) scale_values(j, n, i);
-        tmem_st_wait();
-        tc_fence_before();
-        mbar_arrive(v_ready);
-        return true;
+    auto put_low = [&](int sb, int a, const uint32_t (&lo)[16]) {
+        if (32 * (warp & 3) < DV) tmem_st_16x128b_x8(trow + (16u * a << 16) + lo_block(READOUT, sb), lo);
     };
-    // Column block cb of P over G's columns, for this warp's token rows [32 rb, 32 rb + 32), lane a row; diag[i] =
-    // a^{lane - i}, the same in every chunk.
-    auto decay_scores = [&](int cb, float rowf, const float (&diag)[32]) {
+    // Column block cb of P over G's columns, for this warp's token rows [32 rb, 32 rb + 32), lane a row.
+    auto decay_scores = [&](int cb, float rowf) {
         const int rb = warp & 3;
         uint32_t pk[16];
         if (cb <= rb) {
@@ -273,7 +289,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_tc_kernel(const __grid_con
             } else {
                 tmem_ld32(trow + T_G + 32 * cb, g);
 #pragma unroll
-                for (int i = 0; i < 32; ++i) g[i] = i <= lane ? g[i] * diag[i] : 0.f;
+                for (int i = 0; i < 32; ++i) g[i] = i <= lane ? g[i] * pw[max(lane - i, 0)] : 0.f;
 #pragma unroll
                 for (int i = 0; i < 16; ++i) pk[i] = pack2(g[2 * i], g[2 * i + 1]);
             }
@@ -286,152 +302,201 @@ __global__ void __launch_bounds__(kThreads, 1) linear_tc_kernel(const __grid_con
 
     if (warp < 4) {
         // ---- state ----
-        const bool mine = row < DV;   // whole warps: lanes past d_v hold nothing that is read
-        const size_t warp_off = ((size_t)h * DV + 32 * warp) * DK;
-        // A thread holds a row, and 32 rows' 16 bytes at a time would take the load/store unit 32 lines an instruction, so
-        // 32 x 32 pieces of the state pass through this warp's rows of the S tile, which is free then (two pieces in turn).
-        unsigned char* const piece = smem + OFF_S + 32 * warp * 128;
-        const int pr = lane >> 3, pc = lane & 7;   // by lines: row 4 k + pr, 16-byte column pc
-        auto by_row = [&](int c, int i) {
-            return reinterpret_cast<float4*>(piece + (c & 1) * 16384 + lane * 128 + ((i ^ (lane & 7)) << 4));
-        };
-        auto by_line = [&](int c, int k) {
-            const int r = 4 * k + pr;
-            return reinterpret_cast<float4*>(piece + (c & 1) * 16384 + r * 128 + ((pc ^ (r & 7)) << 4));
-        };
-        auto dump = [&](float* dst) {   // this warp's rows of TMEM to dst
-            if (!mine) return;
-            dst += warp_off + pr * DK + 4 * pc;
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");   // 512 threads start with 128: 208 + 120 + 120 + 64 = 4 x 128
+        auto zero_rows = [&](int j) {   // a cut chunk's key and value rows past it
+            if (w.n == kTok) return true;
+            if (!warp_wait(&full[bar(0, j)], phase(0, j)) || !warp_wait(&full[bar(1, j)], phase(1, j))) return false;
+            if (row >= w.n) {
 #pragma unroll 1
-            for (int c = 0; c < DK / 32; ++c) {
-                float v[32];
-                tmem_ld32(trow + T_S + 32 * c, v);
+                for (int in = 0; in < 2; ++in) {
+                    unsigned char* x = smem + at(in, j) + row * 128;
 #pragma unroll
-                for (int i = 0; i < 8; ++i) *by_row(c, i) = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
-                __syncwarp();
-#pragma unroll
-                for (int k = 0; k < 8; ++k) *reinterpret_cast<float4*>(dst + 4 * k * DK + 32 * c) = *by_line(c, k);
-            }
-            __syncwarp();
-        };
-        if (w.more() && mine) {
-            // the initial state into TMEM, so that the first chunk is like the others
-#pragma unroll 1
-            for (int c0 = 0; c0 < DK / 32; c0 += 2) {
-                if (job.s0) {
-                    const float* src = job.s0 + warp_off + pr * DK + 4 * pc + 32 * c0;
-                    float4 x[16];
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) x[i] = *reinterpret_cast<const float4*>(src + 4 * (i & 7) * DK + 32 * (i >> 3));
-                    __syncwarp();
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) *by_line(i >> 3, i & 7) = x[i];
-                    __syncwarp();
+                    for (int c = 0; c < 16; ++c)
+                        *reinterpret_cast<uint4*>(x + (c >> 3) * 16384 + (c & 7) * 16) = make_uint4(0, 0, 0, 0);
                 }
+            }
+            proxy_fence();
+            return true;
+        };
+        if (32 * warp >= DV) {
+            // lanes past d_v hold nothing that is read: these warps only keep the barriers going (and zero their rows)
+            for (int j = 0; w.more(); w.next(), ++j) {
+                if (j > 0 && !warp_wait(st_done, j - 1)) break;
+                mbar_arrive(s_ready);
+                if (!zero_rows(j)) break;
+                mbar_arrive(v_ready);
+            }
+        } else {
+            const size_t warp_off = ((size_t)h * DV + 32 * warp) * DK;
+            // A thread holds a row, and 32 rows' 16 bytes at a time would take the load/store unit 32 lines an instruction, so
+            // 32 x 32 pieces of the state pass through this warp's rows of the S tile, which is free then (two pieces in turn).
+            unsigned char* const piece = smem + OFF_S + 32 * warp * 128;
+            const int pr = lane >> 3, pc = lane & 7;   // by lines: row 4 k + pr, 16-byte column pc
+            auto by_row = [&](int c, int i) {
+                return reinterpret_cast<float4*>(piece + (c & 1) * 16384 + lane * 128 + ((i ^ (lane & 7)) << 4));
+            };
+            auto by_line = [&](int c, int k) {
+                const int r = 4 * k + pr;
+                return reinterpret_cast<float4*>(piece + (c & 1) * 16384 + r * 128 + ((pc ^ (r & 7)) << 4));
+            };
+            float2 S[DK / 2];   // this thread's row of the state
 #pragma unroll
-                for (int c = 0; c < 2; ++c) {
-                    float v[32];
+            for (int i = 0; i < DK / 2; ++i) S[i] = make_float2(0.f, 0.f);
+            if (job.s0) {
+                const float* src = job.s0 + warp_off + pr * DK + 4 * pc;
+#pragma unroll
+                for (int c = 0; c < DK / 32; ++c) {
+                    float4 x[8];
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) x[k] = *reinterpret_cast<const float4*>(src + 4 * k * DK + 32 * c);
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) *by_line(c, k) = x[k];
+                    __syncwarp();
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
-                        const float4 x = job.s0 ? *by_row(c, i) : make_float4(0.f, 0.f, 0.f, 0.f);
-                        v[4 * i] = x.x, v[4 * i + 1] = x.y, v[4 * i + 2] = x.z, v[4 * i + 3] = x.w;
+                        const float4 y = *by_row(c, i);
+                        S[16 * c + 2 * i] = make_float2(y.x, y.y), S[16 * c + 2 * i + 1] = make_float2(y.z, y.w);
                     }
-                    tmem_st32(trow + T_S + 32 * (c0 + c), v);
                 }
+                __syncwarp();
             }
-            tmem_st_wait();
-            __syncwarp();
-        }
-        bool ok = true;
-        int j = 0, slot = -1;   // slot: where the last chunk's state is dumped
-        for (; w.more(); w.next(), ++j) {
-            if (j > 0) {
-                ok = warp_wait(st_done, j - 1);
-                if (!ok) break;
-                tc_fence_after();
-                if (slot >= 0) dump(p.ckpt_states + (size_t)slot * p.H * DV * DK);
-            }
-            const float2 decay = make_float2(pw[w.n], pw[w.n]);
-#pragma unroll 1
-            for (int c = 0; c < (mine ? DK / 64 : 0); ++c) {
-                float v[2][32];
-                tmem_ld32x2(trow + T_S + 64 * c, trow + T_S + 64 * c + 32, v[0], v[1]);
+            float decay = 1.f;   // a^n of the last chunk
+            bool ok = true;
+            int j = 0, slot = -1;   // slot: where the last chunk's state goes
+            for (;; w.next(), ++j) {
+                if (j > 0) {
+                    ok = warp_wait(st_done, j - 1);
+                    if (!ok) break;
+                    tc_fence_after();
+                    {
+                        // S = a^n S + what the chunk's products added up
+                        const float2 d = make_float2(decay, decay);
 #pragma unroll
+                        for (int c = 0; c < DK / 32; ++c) {
+                            float v[32];
+                            tmem_ld32(trow + T_S + 32 * c, v);
+#pragma unroll
+                            for (int i = 0; i < 16; ++i)
+                                S[16 * c + i] = __ffma2_rn(d, S[16 * c + i], make_float2(v[2 * i], v[2 * i + 1]));
+                        }
+                    }
+                }
+                // the states wanted here: a checkpoint's, the final one (S stays in registers only while it is used in one place)
+#pragma unroll 1
                 for (int k = 0; k < 2; ++k) {
+                    float* dst = k == 0 ? (slot >= 0 ? p.ckpt_states + (size_t)slot * p.H * DV * DK : nullptr)
+                                        : (w.more() ? nullptr : job.s_final);
+                    if (!dst) continue;
+                    dst += warp_off + pr * DK + 4 * pc;
+#pragma unroll
+                    for (int c = 0; c < DK / 32; ++c) {
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            const float2 x = S[16 * c + 2 * i], y = S[16 * c + 2 * i + 1];
+                            *by_row(c, i) = make_float4(x.x, x.y, y.x, y.y);
+                        }
+                        __syncwarp();
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) *reinterpret_cast<float4*>(dst + 4 * i * DK + 32 * c) = *by_line(c, i);
+                    }
+                    __syncwarp();
+                }
+                if (!w.more()) break;
+                decay = pw[w.n];
+                if (READOUT) {
+#pragma unroll
+                    for (int c = 0; c < DK / 8; ++c)
+                        *reinterpret_cast<uint4*>(smem + OFF_S + (c >> 3) * 16384 + sw128(row, (c & 7) * 8)) =
+                            make_uint4(pack2(S[4 * c].x, S[4 * c].y), pack2(S[4 * c + 1].x, S[4 * c + 1].y),
+                                       pack2(S[4 * c + 2].x, S[4 * c + 2].y), pack2(S[4 * c + 3].x, S[4 * c + 3].y));
+                }
+                if (READOUT) proxy_fence();
+                tc_fence_before();
+                mbar_arrive(s_ready);
+                ok = zero_rows(j);
+                if (!ok) break;
+                mbar_arrive(v_ready);
+                slot = w.dump() ? p.ckpts[w.ck].slot : -1;
+            }
+        }
+    } else if (warp < 12) {
+        // ---- tokens, output: lane = token row, this warp's rows are [32 rb, 32 rb + 32) ----
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 120;");
+        const bool tokens = warp < 8;
+        const bool wide = (reinterpret_cast<uintptr_t>(p.o) & 31) == 0;
+        const float rowf = pw[lane], inter = tokens ? pw[row + 1] : p.scale;
+        const float2 inter2 = make_float2(inter, inter);
+        const int b0 = tokens ? 0 : 2;   // the blocks of 32 tokens of this role
+        int pos = 0, n = 0;              // the chunk before j, whose O is still to be taken
+        for (int j = 0;; w.next(), ++j) {
+            const bool more = w.more();
+            // V' hi and mid as soon as the last update is done with theirs, while PV and G are made; lo stays here until G is
+            // read
+            uint32_t lo[2][16];
+            if (more) {
+                if (!warp_wait(&full[bar(1, j)], phase(1, j)) || (j > 0 && !warp_wait(st_done, j - 1))) break;
+                tc_fence_after();
+#pragma unroll 1
+                for (int a = 0; a < 2; ++a) {
+                    uint32_t v[16];
+                    scale_values(j, w.n, b0, a, v);
                     if (READOUT) {
 #pragma unroll
-                        for (int i = 0; i < 32; i += 8)
-                            *reinterpret_cast<uint4*>(smem + OFF_S + c * 16384 + sw128(row, k * 32 + i)) =
-                                make_uint4(pack2(v[k][i], v[k][i + 1]), pack2(v[k][i + 2], v[k][i + 3]),
-                                           pack2(v[k][i + 4], v[k][i + 5]), pack2(v[k][i + 6], v[k][i + 7]));
-                    }
-#pragma unroll
-                    for (int i = 0; i < 32; i += 2) {
-                        const float2 x = __fmul2_rn(make_float2(v[k][i], v[k][i + 1]), decay);
-                        v[k][i] = x.x, v[k][i + 1] = x.y;
-                    }
-                    tmem_st32(trow + T_S + 64 * c + 32 * k, v[k]);
-                }
-            }
-            tmem_st_wait();
-            if (READOUT) proxy_fence();
-            tc_fence_before();
-            mbar_arrive(s_ready);
-            // then half of V', on the chain as well (without a readout the tokens role has nothing else to do)
-            if (READOUT) {
-                ok = warp_wait(&full[bar(1, j)], phase(1, j));
-                if (!ok) break;
-#pragma unroll 1
-                for (int sb = 0; sb < 2; ++sb) scale_values(j, w.n, sb);
-            }
-            if (w.n < kTok) {
-                ok = warp_wait(&full[bar(0, j)], phase(0, j)) && warp_wait(&full[bar(1, j)], phase(1, j));
-                if (!ok) break;
-                if (row >= w.n) {
-#pragma unroll 1
-                    for (int in = 0; in < 2; ++in) {
-                        unsigned char* x = smem + at(in, j) + row * 128;
-#pragma unroll
-                        for (int c = 0; c < 16; ++c)
-                            *reinterpret_cast<uint4*>(x + (c >> 3) * 16384 + (c & 7) * 16) = make_uint4(0, 0, 0, 0);
+                        for (int i = 0; i < 16; ++i) lo[0][i] = a == 0 ? v[i] : lo[0][i], lo[1][i] = v[i];
+                    } else {
+                        put_low(b0, a, v);
                     }
                 }
+                tmem_st_wait();
+                tc_fence_before();
+                mbar_arrive(v_ready);
+            }
+            if (READOUT && !tokens && j > 0) {
+                if (!warp_wait(o_done, j - 1) || (j > 1 && !warp_wait(o_left, j - 2))) break;
+                tc_fence_after();
+                // A whole chunk is staged and copied out by TMA: a thread holds a row, and stores of 32 rows at a time,
+                // 32 bytes each, kept the load/store unit from everyone for 1200 cycles.  A cut one is stored like that.
+                __nv_bfloat16* const dst =
+                    static_cast<__nv_bfloat16*>(p.o) + ((job.tok_begin + pos + row) * p.H + h) * (int64_t)DV;
+#pragma unroll 1
+                for (int c = 0; c < DV / 32; ++c) {
+                    float x[32];
+                    tmem_ld32(trow + T_O + 32 * c, x);
+                    uint32_t u[2][8];
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        const float2 z = __fmul2_rn(inter2, make_float2(x[2 * i], x[2 * i + 1]));
+                        u[i >> 3][i & 7] = pack2(z.x, z.y);
+                    }
+                    if (n == kTok) {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            *reinterpret_cast<uint4*>(smem + OFF_O + (c >> 1) * 16384 + sw128(row, ((c & 1) * 4 + i) * 8)) =
+                                make_uint4(u[i >> 1][(i & 1) * 4], u[i >> 1][(i & 1) * 4 + 1], u[i >> 1][(i & 1) * 4 + 2],
+                                           u[i >> 1][(i & 1) * 4 + 3]);
+                    } else if (row < n) {
+                        store32(dst + 32 * c, u[0], wide);
+                        store32(dst + 32 * c + 16, u[1], wide);
+                    }
+                }
+                tc_fence_before();
+                mbar_arrive(o_free);
                 proxy_fence();
+                mbar_arrive(o_staged);
             }
+            if (!more) break;
+            pos = w.pos, n = w.n;
+            if (!READOUT) continue;
+            if (!warp_wait(g_done, j)) break;
+            tc_fence_after();
+#pragma unroll 1
+            for (int b = b0; b < b0 + 2; ++b) decay_scores(b, rowf);
+            put_low(b0, 0, lo[0]);
+            put_low(b0, 1, lo[1]);
             tmem_st_wait();
             tc_fence_before();
-            mbar_arrive(v_ready);
-            slot = w.dump() ? p.ckpts[w.ck].slot : -1;
-        }
-        if (ok && j > 0) {
-            ok = warp_wait(st_done, j - 1);
-            if (ok) {
-                tc_fence_after();
-                if (slot >= 0) dump(p.ckpt_states + (size_t)slot * p.H * DV * DK);
-                if (job.s_final) dump(job.s_final);
-            }
-        } else if (ok && job.s_final && mine) {
-            // no tokens: the final state is the initial one
-            for (int i = lane; i < 32 * DK / 4; i += 32)
-                reinterpret_cast<float4*>(job.s_final + warp_off)[i] =
-                    job.s0 ? reinterpret_cast<const float4*>(job.s0 + warp_off)[i] : make_float4(0.f, 0.f, 0.f, 0.f);
-        }
-    } else if (warp < 8) {
-        // ---- tokens: lane = token row, this warp's rows are [32 rb, 32 rb + 32) ----
-        if (!READOUT) {
-            for (int j = 0; w.more() && form_values(j, w.n, 0); w.next()) ++j;
-        }
-        if (READOUT) {
-            const float rowf = pw[lane], inter = pw[row + 1];
-            const float2 inter2 = make_float2(inter, inter);
-            float diag[32];
-#pragma unroll
-            for (int i = 0; i < 32; ++i) diag[i] = pw[max(lane - i, 0)];
-            for (int j = 0; w.more(); w.next(), ++j) {
-                if (!warp_wait(g_done, j)) break;
-                tc_fence_after();
-#pragma unroll 1
-                for (int cb = 0; cb < 2; ++cb) decay_scores(cb, rowf, diag);
+            mbar_arrive(lo_ready);
+            if (tokens) {
                 if (!warp_wait(q_done, j)) break;
                 tc_fence_after();
 #pragma unroll 1
@@ -447,164 +512,115 @@ __global__ void __launch_bounds__(kThreads, 1) linear_tc_kernel(const __grid_con
                 }
                 tmem_st_wait();
                 tc_fence_before();
-                mbar_arrive(p_ready);
             }
+            mbar_arrive(p_ready);
         }
-    } else if (warp < 12) {
-        // ---- output: lane = token row ----
-        if (!READOUT) {
-            for (int j = 0; w.more() && form_values(j, w.n, 2); w.next()) ++j;
-        } else if (w.more() && form_values(0, w.n, 2)) {
-            const bool wide = (reinterpret_cast<uintptr_t>(p.o) & 31) == 0;
-            const float2 scale2 = make_float2(p.scale, p.scale);
-            const float rowf = pw[lane];
-            float diag[32];
-#pragma unroll
-            for (int i = 0; i < 32; ++i) diag[i] = pw[max(lane - i, 0)];
-            for (int j = 0; w.more(); ++j) {
-                const int pos = w.pos, n = w.n;
-                if (!warp_wait(g_done, j)) break;
-                tc_fence_after();
+    } else {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
+        if (warp == 12) {
+            // ---- products (the whole warp walks along, one elected lane issues) ----
+            const uint32_t id_g = idesc(kTok, false, false), id_q = idesc(DV, false, false), id_o = idesc(DV, false, true),
+                           id_s = idesc(DK, false, true);
+            const uint64_t s_desc = tile_desc(sbase + OFF_S, false);
+            auto scores = [&](int j) {   // G of chunk j
+                if (!warp_wait(&full[bar(0, j)], phase(0, j)) || !warp_wait(&full[bar(2, j)], phase(2, j))) return false;
+                const uint64_t q = tile_desc(sbase + at(2, j), false), k = tile_desc(sbase + at(0, j), false);
+                if (elect_one()) {
 #pragma unroll 1
-                for (int cb = 2; cb < 4; ++cb) decay_scores(cb, rowf, diag);
-                tmem_st_wait();
-                tc_fence_before();
-                mbar_arrive(p_ready);
-                // the other half of the next chunk's V', for which the update is done before this chunk's O
+                    for (int i = 0; i < DK / 16; ++i) umma_ss(tbase + T_G, cols_step(q, i), cols_step(k, i), id_g, i > 0);
+                    umma_commit(g_done);
+                }
+                return true;
+            };
+            bool ok = !READOUT || !w.more() || scores(0);
+            for (int j = 0; ok && w.more(); ++j) {
                 w.next();
-                if (w.more() && !form_values(j + 1, w.n, 2)) break;
-                if (!warp_wait(o_done, j)) break;
+                ok = warp_wait(s_ready, j) && warp_wait(v_ready, j) && warp_wait(&full[bar(0, j)], phase(0, j));
+                if (!ok) break;
                 tc_fence_after();
-                // the whole row into registers first, so that the next chunk's O can begin before the stores are through
-                uint32_t u[DV / 16][8];
-#pragma unroll
-                for (int c = 0; c < DV / 32; ++c) {
-                    float x[32];
-                    tmem_ld32(trow + T_O + 32 * c, x);
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        const float2 z = __fmul2_rn(scale2, make_float2(x[2 * i], x[2 * i + 1]));
-                        u[2 * c + (i >> 3)][i & 7] = pack2(z.x, z.y);
+                const uint64_t k = tile_desc(sbase + at(0, j), true), v = tile_desc(sbase + at(1, j), true);
+                if (elect_one()) {
+#pragma unroll 1
+                    for (int i = 0; i < 8; ++i) {   // the key rows of 16 tokens
+                        umma_ts(tbase + T_S, tbase + T_VH + 8 * i, rows_step(k, i), id_s, i > 0);
+                        umma_ts(tbase + T_S, tbase + T_VM + 8 * i, rows_step(k, i), id_s | 1u << 13, 1);   // A negated
                     }
                 }
-                tc_fence_before();
-                mbar_arrive(o_free);
-                // A whole chunk is staged and copied out by TMA: a thread holds a row, and stores of 32 rows at a time,
-                // 32 bytes each, kept the load/store unit from everyone for 1200 cycles.  A cut one is stored like that.
-                if (j > 0 && !warp_wait(o_left, j - 1)) break;
-                if (n == kTok) {
-#pragma unroll
-                    for (int c = 0; c < DV / 8; ++c)
-                        *reinterpret_cast<uint4*>(smem + OFF_O + (c >> 3) * 16384 + sw128(row, (c & 7) * 8)) =
-                            make_uint4(u[c >> 1][(c & 1) * 4], u[c >> 1][(c & 1) * 4 + 1], u[c >> 1][(c & 1) * 4 + 2],
-                                       u[c >> 1][(c & 1) * 4 + 3]);
-                    proxy_fence();
-                } else if (row < n) {
-                    __nv_bfloat16* dst =
-                        static_cast<__nv_bfloat16*>(p.o) + ((job.tok_begin + pos + row) * p.H + h) * (int64_t)DV;
-#pragma unroll
-                    for (int c = 0; c < DV / 16; ++c) store32(dst + 16 * c, u[c], wide);
-                }
-                mbar_arrive(o_staged);
-            }
-        }
-    } else if (warp == 12) {
-        // ---- products (the whole warp walks along, one elected lane issues) ----
-        const uint32_t id_g = idesc(kTok, false, false), id_q = idesc(DV, false, false), id_o = idesc(DV, false, true),
-                       id_s = idesc(DK, false, true);
-        const uint64_t s_desc = tile_desc(sbase + OFF_S, false);
-        auto scores = [&](int j) {   // G of chunk j
-            if (!warp_wait(&full[bar(0, j)], phase(0, j)) || !warp_wait(&full[bar(2, j)], phase(2, j))) return false;
-            const uint64_t q = tile_desc(sbase + at(2, j), false), k = tile_desc(sbase + at(0, j), false);
-            if (elect_one()) {
-#pragma unroll
-                for (int i = 0; i < DK / 16; ++i) umma_ss(tbase + T_G, cols_step(q, i), cols_step(k, i), id_g, i > 0);
-                umma_commit(g_done);
-            }
-            return true;
-        };
-        bool ok = !READOUT || !w.more() || scores(0);
-        for (int j = 0; ok && w.more(); ++j) {
-            w.next();
-            ok = warp_wait(s_ready, j);
-            if (!ok) break;
-            if (READOUT) {
-                ok = j == 0 || warp_wait(o_free, j - 1);
-                if (!ok) break;
-                tc_fence_after();
-                const uint64_t q = tile_desc(sbase + at(2, j), false);
-                if (elect_one()) {
-#pragma unroll
-                    for (int i = 0; i < DK / 16; ++i)
-                        umma_ss(tbase + T_O, cols_step(q, i), cols_step(s_desc, i), id_q, i > 0);
-                    umma_commit(q_done);
-                    umma_commit(&empty[bar(2, j)]);
-                }
-            }
-            ok = warp_wait(v_ready, j) && warp_wait(&full[bar(0, j)], phase(0, j));
-            if (!ok) break;
-            tc_fence_after();
-            const uint64_t k = tile_desc(sbase + at(0, j), true), v = tile_desc(sbase + at(1, j), true);
-            if (elect_one()) {
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    umma_ts(tbase + T_S, tbase + T_VH + 8 * i, rows_step(k, i), id_s, 1);
-                    umma_ts(tbase + T_S, tbase + T_VL + 8 * i, rows_step(k, i), id_s, 1);
-                }
-                umma_commit(st_done);
-                umma_commit(&empty[bar(0, j)]);
-            }
-            if (READOUT) {
-                ok = warp_wait(p_ready, j) && warp_wait(&full[bar(1, j)], phase(1, j));
-                if (!ok) break;
-                tc_fence_after();
-            }
-            if (elect_one()) {
                 if (READOUT) {
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) umma_ts(tbase + T_O, tbase + p_block(i >> 1) + 8 * (i & 1), rows_step(v, i), id_o, 1);
-                    umma_commit(o_done);
+                    ok = j == 0 || warp_wait(o_free, j - 1);
+                    if (!ok) break;
+                    tc_fence_after();
+                    const uint64_t q = tile_desc(sbase + at(2, j), false);
+                    if (elect_one()) {
+#pragma unroll 1
+                        for (int i = 0; i < DK / 16; ++i)
+                            umma_ss(tbase + T_O, cols_step(q, i), cols_step(s_desc, i), id_q, i > 0);
+                        umma_commit(q_done);
+                        umma_commit(&empty[bar(2, j)]);
+                    }
+                    ok = warp_wait(lo_ready, j);
+                    if (!ok) break;
+                    tc_fence_after();
                 }
-                umma_commit(&empty[bar(1, j)]);
+                if (elect_one()) {
+#pragma unroll 1
+                    for (int i = 0; i < 8; ++i)
+                        umma_ts(tbase + T_S, tbase + lo_block(READOUT, i >> 1) + 8 * (i & 1), rows_step(k, i), id_s, 1);
+                    umma_commit(st_done);
+                    umma_commit(&empty[bar(0, j)]);
+                }
+                if (READOUT) {
+                    ok = warp_wait(p_ready, j) && warp_wait(&full[bar(1, j)], phase(1, j));
+                    if (!ok) break;
+                    tc_fence_after();
+                }
+                if (elect_one()) {
+                    if (READOUT) {
+#pragma unroll 1
+                        for (int i = 0; i < 8; ++i) umma_ts(tbase + T_O, tbase + p_block(i >> 1) + 8 * (i & 1), rows_step(v, i), id_o, 1);
+                        umma_commit(o_done);
+                    }
+                    umma_commit(&empty[bar(1, j)]);
+                }
+                if (READOUT) ok = !w.more() || scores(j + 1);
             }
-            if (READOUT) ok = !w.more() || scores(j + 1);
-        }
-        if (elect_one()) umma_commit(end);   // also after giving up: the end waits for the products in flight
-    } else if (warp == 14) {
-        // ---- staged output to memory ----
-        if (READOUT && lane == 0) {
-            for (int j = 0; w.more(); w.next(), ++j) {
-                if (!wait_bar(o_staged, (uint32_t)j & 1u, abort_flag, limit)) break;
-                if (w.n == kTok) {
-                    const int t0 = (int)(job.tok_begin + w.pos);
+            if (elect_one()) umma_commit(end);   // also after giving up: the end waits for the products in flight
+        } else if (warp == 14) {
+            // ---- staged output to memory ----
+            if (READOUT && lane == 0) {
+                for (int j = 0; w.more(); w.next(), ++j) {
+                    if (!wait_bar(o_staged, (uint32_t)j & 1u, abort_flag, limit)) break;
+                    if (w.n == kTok) {
+                        const int t0 = (int)(job.tok_begin + w.pos);
 #pragma unroll
-                    for (int x = 0; x < DV / 64; ++x) tma_store_3d(smem + OFF_O + x * 16384, &p.tm_o, 64 * x, h, t0);
-                    asm volatile("cp.async.bulk.commit_group;" ::: "memory");
-                    asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+                        for (int x = 0; x < DV / 64; ++x) tma_store_3d(smem + OFF_O + x * 16384, &p.tm_o, 64 * x, h, t0);
+                        asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+                        asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+                    }
+                    mbar_arrive(o_left);
                 }
-                mbar_arrive(o_left);
             }
-        }
-    } else if (lane == 0 && (warp == 13 || READOUT)) {
-        // ---- copies: warp 13 K and V, warp 15 Q, whose buffer comes free at another time of the chunk ----
-        const int first = warp == 13 ? 0 : 2, last = warp == 13 ? 1 : 2;
-        bool ok = true;
-        for (int j = 0; ok && w.more(); w.next(), ++j) {
-            if (p.stall_after >= 0 && j >= p.stall_after) break;   // testing hook
-            const int t0 = (int)(job.tok_begin + w.pos);
-            for (int in = first; in <= last; ++in) {
-                if (phase(in, j) > 0 &&
-                    !wait_bar(&empty[bar(in, j)], (uint32_t)(phase(in, j) - 1) & 1u, abort_flag, limit)) {
-                    ok = false;
-                    break;
+        } else if (lane == 0 && (warp == 13 || READOUT)) {
+            // ---- copies: warp 13 K and V, warp 15 Q, whose buffer comes free at another time of the chunk ----
+            const int first = warp == 13 ? 0 : 2, last = warp == 13 ? 1 : 2;
+            bool ok = true;
+            for (int j = 0; ok && w.more(); w.next(), ++j) {
+                if (p.stall_after >= 0 && j >= p.stall_after) break;   // testing hook
+                const int t0 = (int)(job.tok_begin + w.pos);
+                for (int in = first; in <= last; ++in) {
+                    if (phase(in, j) > 0 &&
+                        !wait_bar(&empty[bar(in, j)], (uint32_t)(phase(in, j) - 1) & 1u, abort_flag, limit)) {
+                        ok = false;
+                        break;
+                    }
+                    const CUtensorMap* tm = in == 0 ? &p.tm_k : in == 1 ? &p.tm_v : &p.tm_q;
+                    const int head = in == 1 ? h : hk;
+                    uint64_t* b = &full[bar(in, j)];
+                    const int blocks = (in == 1 ? DV : DK) / 64;
+                    mbar_arrive_expect_tx(b, blocks * 16384);
+                    for (int x = 0; x < blocks; ++x) tma_load_3d(smem + at(in, j) + x * 16384, tm, 64 * x, head, t0, b);
+                    issued[in] = j + 1;
                 }
-                const CUtensorMap* tm = in == 0 ? &p.tm_k : in == 1 ? &p.tm_v : &p.tm_q;
-                const int head = in == 1 ? h : hk;
-                uint64_t* b = &full[bar(in, j)];
-                const int blocks = (in == 1 ? DV : DK) / 64;
-                mbar_arrive_expect_tx(b, blocks * 16384);
-                for (int x = 0; x < blocks; ++x) tma_load_3d(smem + at(in, j) + x * 16384, tm, 64 * x, head, t0, b);
-                issued[in] = j + 1;
             }
         }
     }
