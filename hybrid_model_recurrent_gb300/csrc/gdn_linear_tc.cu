@@ -152,9 +152,9 @@ __global__ void __launch_bounds__(kThreads, 1) linear_tc_kernel(const __grid_con
     uint64_t* q_done = g_done + 1;      // Q S^T
     uint64_t* st_done = q_done + 1;     // the state's update (and Q S^T before it)
     uint64_t* o_done = st_done + 1;     // O
-    uint64_t* s_ready = o_done + 1;     // state: the bf16 copy written, S scaled
+    uint64_t* s_ready = o_done + 1;     // state: the bf16 copy written
     uint64_t* p_ready = s_ready + 1;    // tokens, output: P written, O scaled
-    uint64_t* v_ready = p_ready + 1;    // V' hi and mid written, key and value rows zeroed
+    uint64_t* v_ready = p_ready + 1;    // the last products read, V' hi and mid written, key and value rows zeroed
     uint64_t* lo_ready = v_ready + 1;   // V' lo written
     uint64_t* o_free = lo_ready + 1;    // output: O read
     uint64_t* o_staged = o_free + 1;    // output: a chunk's output staged
@@ -381,6 +381,12 @@ __global__ void __launch_bounds__(kThreads, 1) linear_tc_kernel(const __grid_con
                         }
                     }
                 }
+                if (w.more()) {   // the update may begin; only Q S^T waits for what follows
+                    ok = zero_rows(j);
+                    if (!ok) break;
+                    tc_fence_before();
+                    mbar_arrive(v_ready);
+                }
                 // the states wanted here: a checkpoint's, the final one (S stays in registers only while it is used in one place)
 #pragma unroll 1
                 for (int k = 0; k < 2; ++k) {
@@ -411,11 +417,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_tc_kernel(const __grid_con
                                        pack2(S[4 * c + 2].x, S[4 * c + 2].y), pack2(S[4 * c + 3].x, S[4 * c + 3].y));
                 }
                 if (READOUT) proxy_fence();
-                tc_fence_before();
                 mbar_arrive(s_ready);
-                ok = zero_rows(j);
-                if (!ok) break;
-                mbar_arrive(v_ready);
                 slot = w.dump() ? p.ckpts[w.ck].slot : -1;
             }
         }
@@ -535,7 +537,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_tc_kernel(const __grid_con
             bool ok = !READOUT || !w.more() || scores(0);
             for (int j = 0; ok && w.more(); ++j) {
                 w.next();
-                ok = warp_wait(s_ready, j) && warp_wait(v_ready, j) && warp_wait(&full[bar(0, j)], phase(0, j));
+                ok = warp_wait(v_ready, j) && warp_wait(&full[bar(0, j)], phase(0, j));
                 if (!ok) break;
                 tc_fence_after();
                 const uint64_t k = tile_desc(sbase + at(0, j), true), v = tile_desc(sbase + at(1, j), true);
@@ -547,7 +549,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_tc_kernel(const __grid_con
                     }
                 }
                 if (READOUT) {
-                    ok = j == 0 || warp_wait(o_free, j - 1);
+                    ok = warp_wait(s_ready, j) && (j == 0 || warp_wait(o_free, j - 1));
                     if (!ok) break;
                     tc_fence_after();
                     const uint64_t q = tile_desc(sbase + at(2, j), false);
