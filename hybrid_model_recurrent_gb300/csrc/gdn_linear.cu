@@ -4,9 +4,17 @@
 // The scan.  Row i of S evolves only from v_{t,i}, so the rows of a head split over warps and CTAs with no
 // exchange.  A warp holds 16 rows: 4 row groups of 8 column lanes, a lane 4 rows x d_k/8 columns in registers.
 // A token costs three FP32 operations per state element (decay, update, readout) and one reduction of the
-// readout over the 8 column lanes: 4 shuffles for 16 rows.  The recurrence itself is one multiply and one FMA
-// deep, so the reductions of successive tokens overlap.  q, k and v arrive by cp.async in tiles of 16
-// (fp32) or 32 (bf16) tokens, double buffered.
+// readout over the 8 column lanes.  The recurrence itself is one multiply and one FMA deep; loads and reductions of
+// 4 or 8 tokens go together, round by round.  q, k and v arrive by cp.async in tiles of 16 (fp32) or 32 (bf16) tokens,
+// 2 to 6 of them at a time.
+//
+// What bounds it: a few scans, the latency of a token's steps (2 heads of 32 x 32, 256 tokens, fp32: 21 us, 38 with each
+// token's reduction by itself and two tiles; 4 heads of 64 x 64, 512 tokens: 58 us, 87); many, the issue of its FP32
+// instructions (8 x 16 x 2048, 128 x 128, fp32: 637 us, 20 of the
+// pipes' 37 T instructions a second).
+//
+// The step.  A warp holds 16 or 8 rows of one head's state, read and written once: 268 MB in 46 us (64 requests x 32 heads
+// at d = 128, or 256 x 32 at d = 64) are 5.9 of the 6.7 TB/s that a copy reaches.
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -96,15 +104,28 @@ struct Cols {
     }
 };
 
-// Sums of four rows' partial values over the 8 column lanes: each round keeps half of the rows and sends the
-// other half, so lane c ends with row (c >> 1)'s sum (lanes c and c ^ 1 the same one).
-__device__ __forceinline__ float reduce_rows(const float (&p)[4], int c) {
-    const bool u4 = c & 4, u2 = c & 2;
-    float a = u4 ? p[2] : p[0], b = u4 ? p[3] : p[1];
-    a += __shfl_xor_sync(0xffffffffu, u4 ? p[0] : p[2], 4);
-    b += __shfl_xor_sync(0xffffffffu, u4 ? p[1] : p[3], 4);
-    float x = (u2 ? b : a) + __shfl_xor_sync(0xffffffffu, u2 ? a : b, 2);
-    return x + __shfl_xor_sync(0xffffffffu, x, 1);
+// Sums of four rows' partial values of U tokens over the 8 column lanes: each round keeps half of the values and sends the
+// other half.  Lane c ends with row c >> 1, of every token for U = 1 (lanes c and c ^ 1 the same sum) and of token 2 i +
+// (c & 1) in x[i] otherwise.  All tokens go through a round together: one after the other, each would wait out its three
+// shuffles.
+template <int U>
+__device__ __forceinline__ void reduce_rows(const float (&p)[U][4], int c, float (&x)[(U + 1) / 2]) {
+    const bool u4 = c & 4, u2 = c & 2, u1 = c & 1;
+    float a[U], b[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        a[u] = (u4 ? p[u][2] : p[u][0]) + __shfl_xor_sync(0xffffffffu, u4 ? p[u][0] : p[u][2], 4);
+        b[u] = (u4 ? p[u][3] : p[u][1]) + __shfl_xor_sync(0xffffffffu, u4 ? p[u][1] : p[u][3], 4);
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) a[u] = (u2 ? b[u] : a[u]) + __shfl_xor_sync(0xffffffffu, u2 ? a[u] : b[u], 2);
+    if constexpr (U == 1) {
+        x[0] = a[0] + __shfl_xor_sync(0xffffffffu, a[0], 1);
+    } else {
+#pragma unroll
+        for (int u = 0; u < U; u += 2)
+            x[u / 2] = (u1 ? a[u + 1] : a[u]) + __shfl_xor_sync(0xffffffffu, u1 ? a[u] : a[u + 1], 1);
+    }
 }
 
 template <int DK, bool READOUT, typename T, typename OutT>
@@ -112,10 +133,13 @@ __global__ void __launch_bounds__(128) linear_scan_kernel(const __grid_constant_
     using CM = Cols<DK, T>;
     constexpr int CT = CM::CT;
     constexpr int kPiece = 16 / (int)sizeof(T);         // elements of a 16-byte copy
-    constexpr int kTile = sizeof(T) == 4 ? 16 : 32;     // tokens of a staged tile (within 48 KB of static memory)
-    __shared__ __align__(16) T sk[2][kTile][DK];
-    __shared__ __align__(16) T sq[2][kTile][DK];
-    __shared__ __align__(16) T sv[2][kTile][64];
+    constexpr int kTile = sizeof(T) == 4 ? 16 : 32;     // tokens of a staged tile
+    // As many tiles as 48 KB of static memory hold: a narrow one's tokens take less time than its copy from memory.
+    constexpr int NB = 49152 / (kTile * (2 * DK + 64) * (int)sizeof(T));
+    static_assert(NB >= 2, "a tile being read and one on its way");
+    __shared__ __align__(16) T sk[NB][kTile][DK];
+    __shared__ __align__(16) T sq[NB][kTile][DK];
+    __shared__ __align__(16) T sv[NB][kTile][64];
 
     const int RB = p.rows_per_cta;
     const int blocks = p.dv / RB;
@@ -146,16 +170,17 @@ __global__ void __launch_bounds__(128) linear_scan_kernel(const __grid_constant_
     const T* gv = static_cast<const T*>(p.v) + job.tok_begin * p.v_stride + (int64_t)h * p.dv + rb * RB;
     OutT* go = READOUT ? static_cast<OutT*>(p.o) + (job.tok_begin * p.H + h) * (int64_t)p.dv + row0 : nullptr;
 
-    auto stage = [&](int tile) {
-        const int t0 = tile * kTile, buf = tile & 1;
-        for (int i = tid; i < kTile * (DK / kPiece); i += blockDim.x) {
+    const int tiles = (len + kTile - 1) / kTile;
+    auto stage = [&](int tile) {   // one group of copies, empty past the end
+        const int t0 = tile * kTile, buf = tile % NB;
+        for (int i = tid; tile < tiles && i < kTile * (DK / kPiece); i += blockDim.x) {
             const int t = i / (DK / kPiece), x = (i % (DK / kPiece)) * kPiece;
             const int ts = min(t0 + t, len - 1);   // past the end: a valid address, nothing copied
             const int n = t0 + t < len ? 16 : 0;
             cp_async<16>(&sk[buf][t][x], gk + (int64_t)ts * p.k_stride + x, n);
             if (READOUT) cp_async<16>(&sq[buf][t][x], gq + (int64_t)ts * p.q_stride + x, n);
         }
-        for (int i = tid; i < kTile * (RB / kPiece); i += blockDim.x) {
+        for (int i = tid; tile < tiles && i < kTile * (RB / kPiece); i += blockDim.x) {
             const int t = i / (RB / kPiece), x = (i % (RB / kPiece)) * kPiece;
             const int ts = min(t0 + t, len - 1);
             cp_async<16>(&sv[buf][t][x], gv + (int64_t)ts * p.v_stride + x, t0 + t < len ? 16 : 0);
@@ -163,52 +188,57 @@ __global__ void __launch_bounds__(128) linear_scan_kernel(const __grid_constant_
         cp_commit();
     };
 
-    const int tiles = (len + kTile - 1) / kTile;
     int ck = job.ck_begin;
     const int ck_end = job.ck_begin + job.ck_count;
     int next_ck = ck < ck_end ? p.ckpts[ck].pos : INT32_MAX;
-    if (tiles > 0) stage(0);
+#pragma unroll 1
+    for (int i = 0; i < NB - 1; ++i) stage(i);
     for (int tile = 0; tile < tiles; ++tile) {
-        if (tile + 1 < tiles) {
-            stage(tile + 1);
-            cp_wait<1>();
-        } else {
-            cp_wait<0>();
-        }
+        stage(tile + NB - 1);
+        cp_wait<NB - 1>();
         __syncthreads();
-        const int buf = tile & 1, n = min(kTile, len - tile * kTile);
-        auto token = [&](int t) {
-            float kk[CT], vv[4];
-            CM::load(sk[buf][t], c, kk);
-            load_vec<4>(&sv[buf][t][warp * kWarpRows + rg * 4], vv);
+        const int buf = tile % NB, n = min(kTile, len - tile * kTile);
+        auto tokens = [&](int t, auto count) {
+            constexpr int U = decltype(count)::value;
+            [[maybe_unused]] float part[U][4];
 #pragma unroll
-            for (int r = 0; r < 4; ++r)
+            for (int u = 0; u < U; ++u) {
+                float kk[CT], vv[4];
+                CM::load(sk[buf][t + u], c, kk);
+                load_vec<4>(&sv[buf][t + u][warp * kWarpRows + rg * 4], vv);
 #pragma unroll
-                for (int j = 0; j < CT; ++j) S[r][j] = fmaf(vv[r], kk[j], a * S[r][j]);
-            if constexpr (READOUT) {
-                float qq[CT], part[4];
-                CM::load(sq[buf][t], c, qq);
+                for (int r = 0; r < 4; ++r)
 #pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    float x = 0.f;
+                    for (int j = 0; j < CT; ++j) S[r][j] = fmaf(vv[r], kk[j], a * S[r][j]);
+                if constexpr (READOUT) {
+                    float qq[CT];
+                    CM::load(sq[buf][t + u], c, qq);
 #pragma unroll
-                    for (int j = 0; j < CT; ++j) x = fmaf(S[r][j], qq[j], x);
-                    part[r] = x;
+                    for (int r = 0; r < 4; ++r) {
+                        float x = 0.f;
+#pragma unroll
+                        for (int j = 0; j < CT; ++j) x = fmaf(S[r][j], qq[j], x);
+                        part[u][r] = x;
+                    }
                 }
-                const float x = reduce_rows(part, c);
-                if ((c & 1) == 0) store_out(go + (int64_t)(tile * kTile + t) * p.H * p.dv + (c >> 1), x * p.scale);
+            }
+            if constexpr (READOUT) {
+                float x[(U + 1) / 2];
+                reduce_rows<U>(part, c, x);
+                const int own = U > 1 ? c & 1 : 0;   // the token of a pair that this lane has
+#pragma unroll
+                for (int u = 0; u < U; u += 2)
+                    if (U > 1 || (c & 1) == 0)
+                        store_out(go + (int64_t)(tile * kTile + t + u + own) * p.H * p.dv + (c >> 1), x[u / 2] * p.scale);
             }
         };
         for (int t = 0; t < n;) {
             // up to the next checkpoint without a branch, several tokens at a time: a token's loads, its reduction and its
             // store have no part in the recurrence and overlap the next token's
             const int stop = min(n, next_ck - tile * kTile);
-            constexpr int U = CT >= 16 ? 2 : 4;
-            for (; t + U <= stop; t += U) {
-#pragma unroll
-                for (int u = 0; u < U; ++u) token(t + u);
-            }
-            for (; t < stop; ++t) token(t);
+            constexpr int U = CT >= 16 ? 4 : 8;
+            for (; t + U <= stop; t += U) tokens(t, std::integral_constant<int, U>{});
+            for (; t < stop; ++t) tokens(t, std::integral_constant<int, 1>{});
             if (tile * kTile + t == next_ck) {
                 float* dst = p.ckpt_states + (size_t)p.ckpts[ck].slot * p.H * p.dv * DK + head;
 #pragma unroll
@@ -288,7 +318,7 @@ __global__ void __launch_bounds__(128) linear_step_kernel(const __grid_constant_
 #pragma unroll
     for (int r = 0; r < R; ++r) vv[r] = (float)v[r];
     const float a = p.alpha[h];
-    float part[R];
+    float part[1][R];
 #pragma unroll
     for (int r = 0; r < R; ++r) {
         float x = 0.f;
@@ -297,20 +327,20 @@ __global__ void __launch_bounds__(128) linear_step_kernel(const __grid_constant_
             S[r][j] = fmaf(vv[r], kk[j], a * S[r][j]);
             x = fmaf(S[r][j], qq[j], x);
         }
-        part[r] = x;
+        part[0][r] = x;
         CM::store_state(st + r * DK, c, S[r]);
     }
-    float x;
+    float sum[1];
     if constexpr (R == 4) {
-        x = reduce_rows(part, c);
+        reduce_rows<1>(part, c, sum);
     } else {
         static_assert(R == 2, "rows of a lane");
         const bool up = c & 4;
-        x = (up ? part[1] : part[0]) + __shfl_xor_sync(0xffffffffu, up ? part[0] : part[1], 4);
+        float x = (up ? part[0][1] : part[0][0]) + __shfl_xor_sync(0xffffffffu, up ? part[0][0] : part[0][1], 4);
         x += __shfl_xor_sync(0xffffffffu, x, 2);
-        x += __shfl_xor_sync(0xffffffffu, x, 1);
+        sum[0] = x + __shfl_xor_sync(0xffffffffu, x, 1);
     }
-    if (writes) store_out(o + c / (8 / R), x * p.scale);
+    if (writes) store_out(o + c / (8 / R), sum[0] * p.scale);
 }
 
 template <int DK>
