@@ -23,7 +23,7 @@
 // a chunk moved 590 KB through shared memory, now 430 KB, and the room of K' gives every input tile a second buffer.
 //
 // What it measured (d = 128): 8 x 16 scans of 8192 tokens with 16 checkpoints each, 1.22 GB in 235 us, 5.2 of the 6.7 TB/s
-// that a copy reaches (128 of 152 multiprocessors have a scan); 3.2 us a chunk of one CTA, where the products alone need
+// that a copy reaches (128 of 152 multiprocessors have a scan); 3.2 us a chunk without a checkpoint, where the products need
 // 1.6.  32 scans of 131072, cut into segments and read twice: 1.21 ms.
 //
 // One CTA takes one (job, head) from its first chunk to its last.  Roles:
