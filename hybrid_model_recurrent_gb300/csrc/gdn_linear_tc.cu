@@ -24,14 +24,14 @@
 //
 // What it measured (d = 128): 8 x 16 scans of 8192 tokens with 16 checkpoints each, 1.22 GB in 235 us, 5.2 of the 6.7 TB/s
 // that a copy reaches (128 of 152 multiprocessors have a scan); 3.2 us a chunk without a checkpoint, where the products need
-// 1.6.  32 scans of 131072, cut into segments and read twice: 1.21 ms.
+// 1.6.  32 scans of 131072, cut into segments and read twice: 1.09 ms.
 //
 // One CTA takes one (job, head) from its first chunk to its last.  Roles:
 //   state  (warps 0-3):  S, a row a thread, in registers: a^n S + the chunk's products; its bf16 copy; checkpoints,
 //                        initial, final state; rows past a cut chunk zeroed
 //   tokens (warps 4-7):  the first half of G's columns -> P and of V^T -> V', both in TMEM; a^{t+1} into O
 //   output (warps 8-11): the second half of P and V'; O to memory, staged for TMA
-// (without a readout the last two only form V')
+// (without a readout the last two only form V', into two buffers in turn, so the next chunk's while this one's is multiplied)
 //   one thread each that issues the products, the copies of K and V, of Q and of staged output
 // They hand over through mbarriers, one phase a chunk, and no barrier completes a phase before everyone who waits for
 // the last one has seen it (a parity tells only two phases apart).  The critical path is the products' own order: V' hi and
@@ -87,8 +87,12 @@ static_assert(kSmem <= 232448, "227 KB of shared memory per block");
 // With a readout, P and V' lo go over G, each role's over the 64 columns of its tokens, which only it reads: P's two blocks
 // of 32 tokens (16 columns each) first, then V' lo's.
 __host__ __device__ constexpr uint32_t p_block(int cb) { return 128u + 16u * cb + (cb >= 2 ? 32u : 0u); }
-__host__ __device__ constexpr uint32_t lo_block(bool readout, int cb) { return readout ? p_block(cb) + 32u : 128u + 16u * cb; }
-constexpr uint32_t T_S = 0, T_G = 128, T_O = 256, T_VH = 384, T_VM = 448;
+constexpr uint32_t T_S = 0, T_G = 128, T_O = 256;
+// V' hi, then mid; without a readout the columns of G and O give room to two whole V', and the next one is formed during an update
+__host__ __device__ constexpr uint32_t t_hi(bool readout, int buf) { return readout ? 384u : 128u + 192u * buf; }
+__host__ __device__ constexpr uint32_t lo_block(bool readout, int buf, int cb) {
+    return readout ? p_block(cb) + 32u : t_hi(false, buf) + 128u + 16u * cb;
+}
 
 // b - z for two values, b as bf16
 __device__ __forceinline__ float2 less(uint32_t b, float2 z) {
@@ -143,6 +147,7 @@ struct Walk {
 template <int DK, int DV, bool READOUT>
 __global__ void __launch_bounds__(kThreads, 1) linear_tc_kernel(const __grid_constant__ Params p) {
     constexpr int NB = READOUT ? 2 : 3;               // buffers of K and of V (Q is spent early in its chunk: one)
+    constexpr int NV = READOUT ? 1 : 2;               // V'
     constexpr int NT = READOUT ? 2 * NB + 1 : 2 * NB; // input tiles
     extern __shared__ unsigned char smem_raw[];
     unsigned char* smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
@@ -154,12 +159,12 @@ __global__ void __launch_bounds__(kThreads, 1) linear_tc_kernel(const __grid_con
     uint64_t* empty = full + NT;        // [NT] everything that reads it is done
     uint64_t* g_done = empty + NT;      // G
     uint64_t* q_done = g_done + 1;      // Q S^T
-    uint64_t* st_done = q_done + 1;     // the state's update (and Q S^T before it)
-    uint64_t* o_done = st_done + 1;     // O
+    uint64_t* st_done = q_done + 1;     // [NV] the state's update (and Q S^T before it)
+    uint64_t* o_done = st_done + NV;    // O
     uint64_t* s_ready = o_done + 1;     // state: the bf16 copy written
     uint64_t* p_ready = s_ready + 1;    // tokens, output: P written, O scaled
-    uint64_t* v_ready = p_ready + 1;    // the last products read, V' hi and mid written, key and value rows zeroed
-    uint64_t* lo_ready = v_ready + 1;   // V' lo written
+    uint64_t* v_ready = p_ready + 1;    // [NV] the last products read, V' hi and mid written, key and value rows zeroed
+    uint64_t* lo_ready = v_ready + NV;  // V' lo written
     uint64_t* o_free = lo_ready + 1;    // output: O read
     uint64_t* o_staged = o_free + 1;    // output: a chunk's output staged
     uint64_t* o_left = o_staged + 1;    // the staged output has been copied out
@@ -167,7 +172,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_tc_kernel(const __grid_con
     uint32_t* tslot = reinterpret_cast<uint32_t*>(end + 1);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tslot + 1);
     int* issued = reinterpret_cast<int*>(tslot + 2);   // [3] chunks whose K, V, Q copy was issued
-    static_assert((2 * NT + 12) * 8 + 20 <= 256, "barrier area");
+    static_assert((2 * NT + 10 + 2 * NV) * 8 + 20 <= 256, "barrier area");
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int h = blockIdx.x % p.H;
@@ -181,11 +186,11 @@ __global__ void __launch_bounds__(kThreads, 1) linear_tc_kernel(const __grid_con
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
     }
     if (tid == 0) {
-        for (int i = 0; i < 2 * NT + 4; ++i) mbar_init(&full[i], 1);
+        for (int i = 0; i < 2 * NT + 3 + NV; ++i) mbar_init(&full[i], 1);
         mbar_init(o_left, 1);
         for (uint64_t* b : {s_ready, o_free, o_staged}) mbar_init(b, 128);
         mbar_init(p_ready, 256);
-        mbar_init(v_ready, 384);
+        for (int i = 0; i < NV; ++i) mbar_init(&v_ready[i], 384);
         mbar_init(lo_ready, 256);
         mbar_init(end, 1);
         *abort_flag = 0;
@@ -214,6 +219,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_tc_kernel(const __grid_con
     auto warp_wait = [&](uint64_t* bar, int parity) {
         return tcu::warp_wait_bar(bar, (uint32_t)parity & 1u, abort_flag, limit);
     };
+    auto update_wait = [&](int j) { return warp_wait(&st_done[j % NV], j / NV); };   // chunk j's update is done
     Walk w(p, job);
     // 64 tokens from 32 sb of V'^T, 16 of this warp's 32 value dimensions (TMEM lanes): transposed on the way from shared memory by
     // ldmatrix, whose fragment (lane l: dimension l / 4, token pair l % 4 of an 8 x 8 matrix) is the 16x128b form's.  hi and
@@ -252,21 +258,21 @@ __global__ void __launch_bounds__(kThreads, 1) linear_tc_kernel(const __grid_con
             z[i] = __fmul2_rn(bf16x2_to_float2(v[i]), f[i >> 1]);
             v[i] = pack2(z[i].x, z[i].y);
         }
-        tmem_st_16x128b_x8(t + T_VH + 16 * sb, v);
+        tmem_st_16x128b_x8(t + t_hi(READOUT, j % NV) + 16 * sb, v);
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
             z[i] = less(v[i], z[i]);
             v[i] = pack2(z[i].x, z[i].y);
         }
-        tmem_st_16x128b_x8(t + T_VM + 16 * sb, v);
+        tmem_st_16x128b_x8(t + t_hi(READOUT, j % NV) + 64 + 16 * sb, v);
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
             z[i] = less(v[i], z[i]);
             v[i] = pack2(z[i].x, z[i].y);
         }
     };
-    auto put_low = [&](int sb, int a, const uint32_t (&lo)[16]) {
-        if (32 * (warp & 3) < DV) tmem_st_16x128b_x8(trow + (16u * a << 16) + lo_block(READOUT, sb), lo);
+    auto put_low = [&](int j, int sb, int a, const uint32_t (&lo)[16]) {
+        if (32 * (warp & 3) < DV) tmem_st_16x128b_x8(trow + (16u * a << 16) + lo_block(READOUT, j % NV, sb), lo);
     };
     // Column block cb of P over G's columns, for this warp's token rows [32 rb, 32 rb + 32), lane a row.
     auto decay_scores = [&](int cb, float rowf) {
@@ -325,10 +331,10 @@ __global__ void __launch_bounds__(kThreads, 1) linear_tc_kernel(const __grid_con
         if (32 * warp >= DV) {
             // lanes past d_v hold nothing that is read: these warps only keep the barriers going (and zero their rows)
             for (int j = 0; w.more(); w.next(), ++j) {
-                if (j > 0 && !warp_wait(st_done, j - 1)) break;
+                if (j > 0 && !update_wait(j - 1)) break;
                 mbar_arrive(s_ready);
                 if (!zero_rows(j)) break;
-                mbar_arrive(v_ready);
+                mbar_arrive(&v_ready[j % NV]);
             }
         } else {
             const size_t warp_off = ((size_t)h * DV + 32 * warp) * DK;
@@ -369,7 +375,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_tc_kernel(const __grid_con
             int j = 0, slot = -1;   // slot: where the last chunk's state goes
             for (;; w.next(), ++j) {
                 if (j > 0) {
-                    ok = warp_wait(st_done, j - 1);
+                    ok = update_wait(j - 1);
                     if (!ok) break;
                     tc_fence_after();
                     {
@@ -389,7 +395,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_tc_kernel(const __grid_con
                     ok = zero_rows(j);
                     if (!ok) break;
                     tc_fence_before();
-                    mbar_arrive(v_ready);
+                    mbar_arrive(&v_ready[j % NV]);
                 }
                 // the states wanted here: a checkpoint's, the final one (S stays in registers only while it is used in one place)
 #pragma unroll 1
@@ -440,7 +446,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_tc_kernel(const __grid_con
             // read
             uint32_t lo[2][16];
             if (more) {
-                if (!warp_wait(&full[bar(1, j)], phase(1, j)) || (j > 0 && !warp_wait(st_done, j - 1))) break;
+                if (!warp_wait(&full[bar(1, j)], phase(1, j)) || (j >= NV && !update_wait(j - NV))) break;
                 tc_fence_after();
 #pragma unroll 1
                 for (int a = 0; a < 2; ++a) {
@@ -450,12 +456,12 @@ __global__ void __launch_bounds__(kThreads, 1) linear_tc_kernel(const __grid_con
 #pragma unroll
                         for (int i = 0; i < 16; ++i) lo[0][i] = a == 0 ? v[i] : lo[0][i], lo[1][i] = v[i];
                     } else {
-                        put_low(b0, a, v);
+                        put_low(j, b0, a, v);
                     }
                 }
                 tmem_st_wait();
                 tc_fence_before();
-                mbar_arrive(v_ready);
+                mbar_arrive(&v_ready[j % NV]);
             }
             if (READOUT && !tokens && j > 0) {
                 if (!warp_wait(o_done, j - 1) || (j > 1 && !warp_wait(o_left, j - 2))) break;
@@ -497,8 +503,8 @@ __global__ void __launch_bounds__(kThreads, 1) linear_tc_kernel(const __grid_con
             tc_fence_after();
 #pragma unroll 1
             for (int b = b0; b < b0 + 2; ++b) decay_scores(b, rowf);
-            put_low(b0, 0, lo[0]);
-            put_low(b0, 1, lo[1]);
+            put_low(j, b0, 0, lo[0]);
+            put_low(j, b0, 1, lo[1]);
             tmem_st_wait();
             tc_fence_before();
             mbar_arrive(lo_ready);
@@ -541,15 +547,16 @@ __global__ void __launch_bounds__(kThreads, 1) linear_tc_kernel(const __grid_con
             bool ok = !READOUT || !w.more() || scores(0);
             for (int j = 0; ok && w.more(); ++j) {
                 w.next();
-                ok = warp_wait(v_ready, j) && warp_wait(&full[bar(0, j)], phase(0, j));
+                ok = warp_wait(&v_ready[j % NV], j / NV) && warp_wait(&full[bar(0, j)], phase(0, j));
                 if (!ok) break;
                 tc_fence_after();
                 const uint64_t k = tile_desc(sbase + at(0, j), true), v = tile_desc(sbase + at(1, j), true);
+                const uint32_t vh = tbase + t_hi(READOUT, j % NV);
                 if (elect_one()) {
 #pragma unroll 1
                     for (int i = 0; i < 8; ++i) {   // the key rows of 16 tokens
-                        umma_ts(tbase + T_S, tbase + T_VH + 8 * i, rows_step(k, i), id_s, i > 0);
-                        umma_ts(tbase + T_S, tbase + T_VM + 8 * i, rows_step(k, i), id_s | 1u << 13, 1);   // A negated
+                        umma_ts(tbase + T_S, vh + 8 * i, rows_step(k, i), id_s, i > 0);
+                        umma_ts(tbase + T_S, vh + 64 + 8 * i, rows_step(k, i), id_s | 1u << 13, 1);   // A negated
                     }
                 }
                 if (READOUT) {
@@ -571,8 +578,8 @@ __global__ void __launch_bounds__(kThreads, 1) linear_tc_kernel(const __grid_con
                 if (elect_one()) {
 #pragma unroll 1
                     for (int i = 0; i < 8; ++i)
-                        umma_ts(tbase + T_S, tbase + lo_block(READOUT, i >> 1) + 8 * (i & 1), rows_step(k, i), id_s, 1);
-                    umma_commit(st_done);
+                        umma_ts(tbase + T_S, tbase + lo_block(READOUT, j % NV, i >> 1) + 8 * (i & 1), rows_step(k, i), id_s, 1);
+                    umma_commit(&st_done[j % NV]);
                     umma_commit(&empty[bar(0, j)]);
                 }
                 if (READOUT) {
