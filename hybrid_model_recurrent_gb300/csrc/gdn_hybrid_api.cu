@@ -95,13 +95,34 @@ LinPlan plan_linear(const gdn_linear_problem* p) {
     pl.rows_per_cta = pl.tc ? p->d_v : std::min(64, p->d_v);
     while (!pl.tc && pl.rows_per_cta > 16 && (int64_t)B * p->num_heads * (p->d_v / pl.rows_per_cta) < 2 * kSms) pl.rows_per_cta /= 2;
     const int64_t per_seq = (int64_t)p->num_heads * (p->d_v / pl.rows_per_cta);
-    // A scan is sequential, so a call with few long ones leaves multiprocessors idle.  Its scans are then cut into
+    // A scan is sequential, so a call with few long ones leaves multiprocessors idle.  Its scans may then be cut into
     // segments: each segment's own state from zero (keys and values read once more), the chain of the states, and all
-    // segments side by side.  That is about twice the work, so it pays when the longest scan is more than twice an
-    // even share of all the work.
-    const int64_t share = ceil_div(T * per_seq, kSms);
-    if (longest > 2 * share && longest >= 1024) {
-        pl.seg_len = ceil_div(std::max<int64_t>(512, share / 4), 128) * 128;
+    // segments side by side.  Both ways are estimated, in us, from what was measured: a token's time in a CTA with a readout
+    // and without, a CTA's start, the chain's time a segment, two more launches, five passes of memory over the segments'
+    // states; the FP32 pipes' CTAs are small and run four to a multiprocessor.  At d = 128 in bf16, 8192 tokens, 16 / 32 / 48
+    // / 64 heads took 55 / 92 / 121 / 162 us cut and 190 whole, 1024 tokens of 16 heads 34 cut and 30 whole; in fp32, 4096
+    // tokens of 32 heads of 64 x 64 205 us cut and 456 whole.
+    const double read = pl.tc ? 0.026 : 0.1, update = pl.tc ? 0.014 : 0.06, start = 6, link = 0.8;
+    const int64_t slots = kSms * (pl.tc ? 1 : 4), share = ceil_div(T * per_seq, slots);
+    double best = (double)std::max(longest, share) * read + start;
+    auto segments = [&](int64_t len) {   // of all scans
+        int64_t n = 0;
+        for (int b = 0; b < B; ++b) n += ceil_div(p->cu_seqlens[b + 1] - p->cu_seqlens[b], len);
+        return n;
+    };
+    for (int waves = 1; waves <= 4 && (double)share * (read + update) < best; ++waves) {
+        // the shortest segments that all run in `waves` waves, if about the even share's length will do
+        const int64_t even = ceil_div(std::max<int64_t>(256, ceil_div(share, waves)), 128) * 128;
+        int64_t len = even, n = segments(len);
+        for (int i = 0; i < 10 && n * per_seq > waves * slots; ++i) len += ceil_div(len, 2048) * 128, n = segments(len);
+        if (n * per_seq > waves * slots) len = even, n = segments(len);
+        if (len >= longest) continue;
+        const int64_t tokens = std::min(ceil_div(n * per_seq, slots) * len, share + len);   // of the busiest CTA slot
+        const double cost = (double)tokens * (read + update) + 2 * start * waves + link * (double)ceil_div(longest, len) + 6 +
+                            (double)(n * p->num_heads) * p->d_v * p->d_k * 20 / 6e6;
+        if (cost < 0.95 * best) best = cost, pl.seg_len = len;
+    }
+    if (pl.seg_len) {
         for (int b = 0; b < B; ++b) {
             const int64_t n = p->cu_seqlens[b + 1] - p->cu_seqlens[b];
             if (n > 0) pl.slots += ceil_div(n, pl.seg_len) - 1;
