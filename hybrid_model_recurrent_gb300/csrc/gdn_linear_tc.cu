@@ -15,21 +15,21 @@
 // V' is not exact in bf16: it is split into hi - mid + lo (mid is formed negated and the product negates it back), 24 bits,
 // all multiplied; and the tensor cores' sums, which are not rounded to nearest, run over one chunk only.  So a state is
 // within 5e-7 of itself against 64 bits, as fp32 sums are; with two parts, and the sums running through all chunks, it was
-// within 2.5e-6 and a pass took 0.87 of the time.  P and the copy of S that the readout multiplies are rounded to bf16 once
+// within 2.5e-6.  P and the copy of S that the readout multiplies are rounded to bf16 once
 // (half a step, 2^-8 of each term): the readout itself is rounded to bf16, and its error stays of that order.
 //
 // What bounds it: shared memory's 128 bytes a cycle, of which a product with both operands there takes nearly all.  So
 // P and V'^T are operands in TMEM: with K' = diag(.) K split in shared memory instead (written, and read again beside V),
 // a chunk moved 590 KB through shared memory, now 430 KB, and the room of K' gives every input tile a second buffer.
 //
-// What it measured (d = 128): 8 x 16 scans of 8192 tokens with 16 checkpoints each, 1.22 GB in 235 us, 5.2 of the 6.7 TB/s
-// that a copy reaches (128 of 152 multiprocessors have a scan); 3.2 us a chunk without a checkpoint, where the products need
-// 1.6.  32 scans of 131072, cut into segments and read twice: 1.09 ms.
+// What it measured (d = 128): 8 x 16 scans of 8192 tokens with 16 checkpoints each, 1.22 GB in 213 us, 5.7 of the 6.7 TB/s
+// that a copy reaches (128 of 152 multiprocessors have a scan); 2.9 us a chunk without a checkpoint, where the products need
+// 1.6.  32 scans of 131072, cut into segments and read twice: 1.05 ms.
 //
 // One CTA takes one (job, head) from its first chunk to its last.  Roles:
 //   state  (warps 0-3):  S, a row a thread, in registers: a^n S + the chunk's products; its bf16 copy; checkpoints,
-//                        initial, final state; rows past a cut chunk zeroed
-//   tokens (warps 4-7):  the first half of G's columns -> P and of V^T -> V', both in TMEM; a^{t+1} into O
+//                        initial, final state; a^{t+1} into O; rows past a cut chunk zeroed
+//   tokens (warps 4-7):  the first half of G's columns -> P and of V^T -> V', both in TMEM
 //   output (warps 8-11): the second half of P and V'; O to memory, staged for TMA
 // (without a readout the last two only form V', into two buffers in turn, so the next chunk's while this one's is multiplied)
 //   one thread each that issues the products, the copies of K and V, of Q and of staged output
@@ -109,6 +109,11 @@ __device__ __forceinline__ void tma_store_3d(const void* src, const CUtensorMap*
                  : "memory");
 }
 
+__device__ __forceinline__ void tma_prefetch_3d(const CUtensorMap* tm, int x, int y, int z) {
+    asm volatile("cp.async.bulk.prefetch.tensor.3d.L2.global.tile [%0, {%1, %2, %3}];" ::"l"(reinterpret_cast<uint64_t>(tm)),
+                 "r"(x), "r"(y), "r"(z)
+                 : "memory");
+}
 // four 8 x 8 matrices of 16-bit elements, transposed: register m of lane l holds rows 2 (l % 4), + 1 of column l / 4
 __device__ __forceinline__ void ldsm_x4_trans(uint32_t addr, uint32_t (&r)[4]) {
     asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
@@ -162,7 +167,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_tc_kernel(const __grid_con
     uint64_t* st_done = q_done + 1;     // [NV] the state's update (and Q S^T before it)
     uint64_t* o_done = st_done + NV;    // O
     uint64_t* s_ready = o_done + 1;     // state: the bf16 copy written
-    uint64_t* p_ready = s_ready + 1;    // tokens, output: P written, O scaled
+    uint64_t* p_ready = s_ready + 1;    // tokens, output: P written; state: O scaled
     uint64_t* v_ready = p_ready + 1;    // [NV] the last products read, V' hi and mid written, key and value rows zeroed
     uint64_t* lo_ready = v_ready + NV;  // V' lo written
     uint64_t* o_free = lo_ready + 1;    // output: O read
@@ -189,7 +194,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_tc_kernel(const __grid_con
         for (int i = 0; i < 2 * NT + 3 + NV; ++i) mbar_init(&full[i], 1);
         mbar_init(o_left, 1);
         for (uint64_t* b : {s_ready, o_free, o_staged}) mbar_init(b, 128);
-        mbar_init(p_ready, 256);
+        mbar_init(p_ready, 384);
         for (int i = 0; i < NV; ++i) mbar_init(&v_ready[i], 384);
         mbar_init(lo_ready, 256);
         mbar_init(end, 1);
@@ -328,13 +333,35 @@ __global__ void __launch_bounds__(kThreads, 1) linear_tc_kernel(const __grid_con
             proxy_fence();
             return true;
         };
-        if (32 * warp >= DV) {
+        const float2 inter2 = make_float2(pw[row + 1], pw[row + 1]);
+        auto scale_out = [&](int j) {   // O = Q S^T's rows, one a thread, by a^{t+1}
+            if (!READOUT) return true;
+            if (!warp_wait(q_done, j)) return false;
+            tc_fence_after();
+#pragma unroll 1
+            for (int c = 0; c < DV / 32; ++c) {
+                float x[32];
+                tmem_ld32(trow + T_O + 32 * c, x);
+#pragma unroll
+                for (int i = 0; i < 32; i += 2) {
+                    const float2 z = __fmul2_rn(inter2, make_float2(x[i], x[i + 1]));
+                    x[i] = z.x, x[i + 1] = z.y;
+                }
+                tmem_st32(trow + T_O + 32 * c, x);
+            }
+            tmem_st_wait();
+            tc_fence_before();
+            mbar_arrive(p_ready);
+            return true;
+        };
+        if (DV < 128 && 32 * warp >= DV) {
             // lanes past d_v hold nothing that is read: these warps only keep the barriers going (and zero their rows)
             for (int j = 0; w.more(); w.next(), ++j) {
                 if (j > 0 && !update_wait(j - 1)) break;
                 mbar_arrive(s_ready);
                 if (!zero_rows(j)) break;
                 mbar_arrive(&v_ready[j % NV]);
+                if (!scale_out(j)) break;
             }
         } else {
             const size_t warp_off = ((size_t)h * DV + 32 * warp) * DK;
@@ -429,6 +456,8 @@ __global__ void __launch_bounds__(kThreads, 1) linear_tc_kernel(const __grid_con
                 if (READOUT) proxy_fence();
                 mbar_arrive(s_ready);
                 slot = w.dump() ? p.ckpts[w.ck].slot : -1;
+                ok = scale_out(j);
+                if (!ok) break;
             }
         }
     } else if (warp < 12) {
@@ -436,8 +465,8 @@ __global__ void __launch_bounds__(kThreads, 1) linear_tc_kernel(const __grid_con
         asm volatile("setmaxnreg.dec.sync.aligned.u32 120;");
         const bool tokens = warp < 8;
         const bool wide = (reinterpret_cast<uintptr_t>(p.o) & 31) == 0;
-        const float rowf = pw[lane], inter = tokens ? pw[row + 1] : p.scale;
-        const float2 inter2 = make_float2(inter, inter);
+        const float rowf = pw[lane];
+        const float2 scale2 = make_float2(p.scale, p.scale);
         const int b0 = tokens ? 0 : 2;   // the blocks of 32 tokens of this role
         int pos = 0, n = 0;              // the chunk before j, whose O is still to be taken
         for (int j = 0;; w.next(), ++j) {
@@ -477,7 +506,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_tc_kernel(const __grid_con
                     uint32_t u[2][8];
 #pragma unroll
                     for (int i = 0; i < 16; ++i) {
-                        const float2 z = __fmul2_rn(inter2, make_float2(x[2 * i], x[2 * i + 1]));
+                        const float2 z = __fmul2_rn(scale2, make_float2(x[2 * i], x[2 * i + 1]));
                         u[i >> 3][i & 7] = pack2(z.x, z.y);
                     }
                     if (n == kTok) {
@@ -508,23 +537,6 @@ __global__ void __launch_bounds__(kThreads, 1) linear_tc_kernel(const __grid_con
             tmem_st_wait();
             tc_fence_before();
             mbar_arrive(lo_ready);
-            if (tokens) {
-                if (!warp_wait(q_done, j)) break;
-                tc_fence_after();
-#pragma unroll 1
-                for (int c = 0; c < DV / 32; ++c) {
-                    float x[32];
-                    tmem_ld32(trow + T_O + 32 * c, x);
-#pragma unroll
-                    for (int i = 0; i < 32; i += 2) {
-                        const float2 z = __fmul2_rn(inter2, make_float2(x[i], x[i + 1]));
-                        x[i] = z.x, x[i + 1] = z.y;
-                    }
-                    tmem_st32(trow + T_O + 32 * c, x);
-                }
-                tmem_st_wait();
-                tc_fence_before();
-            }
             mbar_arrive(p_ready);
         }
     } else {
@@ -538,7 +550,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_tc_kernel(const __grid_con
                 if (!warp_wait(&full[bar(0, j)], phase(0, j)) || !warp_wait(&full[bar(2, j)], phase(2, j))) return false;
                 const uint64_t q = tile_desc(sbase + at(2, j), false), k = tile_desc(sbase + at(0, j), false);
                 if (elect_one()) {
-#pragma unroll 1
+#pragma unroll 2
                     for (int i = 0; i < DK / 16; ++i) umma_ss(tbase + T_G, cols_step(q, i), cols_step(k, i), id_g, i > 0);
                     umma_commit(g_done);
                 }
@@ -553,7 +565,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_tc_kernel(const __grid_con
                 const uint64_t k = tile_desc(sbase + at(0, j), true), v = tile_desc(sbase + at(1, j), true);
                 const uint32_t vh = tbase + t_hi(READOUT, j % NV);
                 if (elect_one()) {
-#pragma unroll 1
+#pragma unroll 2
                     for (int i = 0; i < 8; ++i) {   // the key rows of 16 tokens
                         umma_ts(tbase + T_S, vh + 8 * i, rows_step(k, i), id_s, i > 0);
                         umma_ts(tbase + T_S, vh + 64 + 8 * i, rows_step(k, i), id_s | 1u << 13, 1);   // A negated
@@ -565,7 +577,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_tc_kernel(const __grid_con
                     tc_fence_after();
                     const uint64_t q = tile_desc(sbase + at(2, j), false);
                     if (elect_one()) {
-#pragma unroll 1
+#pragma unroll 2
                         for (int i = 0; i < DK / 16; ++i)
                             umma_ss(tbase + T_O, cols_step(q, i), cols_step(s_desc, i), id_q, i > 0);
                         umma_commit(q_done);
@@ -576,7 +588,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_tc_kernel(const __grid_con
                     tc_fence_after();
                 }
                 if (elect_one()) {
-#pragma unroll 1
+#pragma unroll 2
                     for (int i = 0; i < 8; ++i)
                         umma_ts(tbase + T_S, tbase + lo_block(READOUT, j % NV, i >> 1) + 8 * (i & 1), rows_step(k, i), id_s, 1);
                     umma_commit(&st_done[j % NV]);
@@ -589,7 +601,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_tc_kernel(const __grid_con
                 }
                 if (elect_one()) {
                     if (READOUT) {
-#pragma unroll 1
+#pragma unroll 2
                         for (int i = 0; i < 8; ++i) umma_ts(tbase + T_O, tbase + p_block(i >> 1) + 8 * (i & 1), rows_step(v, i), id_o, 1);
                         umma_commit(o_done);
                     }
@@ -633,6 +645,9 @@ __global__ void __launch_bounds__(kThreads, 1) linear_tc_kernel(const __grid_con
                     mbar_arrive_expect_tx(b, blocks * 16384);
                     for (int x = 0; x < blocks; ++x) tma_load_3d(smem + at(in, j) + x * 16384, tm, 64 * x, head, t0, b);
                     issued[in] = j + 1;
+                    // Q has one buffer, and the next chunk's scores wait for it: on its way into the L2 cache before there is room
+                    if (in == 2 && w.pos + w.n < w.len)
+                        for (int x = 0; x < blocks; ++x) tma_prefetch_3d(tm, 64 * x, head, t0 + w.n);
                 }
             }
         }
