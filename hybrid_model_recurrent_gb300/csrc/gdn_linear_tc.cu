@@ -14,7 +14,7 @@
 //     V'^T K with V' = diag(a^{n-1-s}) V, added to a^n S in registers
 // V' is not exact in bf16: it is split into hi - mid + lo (mid is formed negated and the product negates it back), 24 bits,
 // all multiplied; and the tensor cores' sums, which are not rounded to nearest, run over one chunk only.  So a state is
-// within 5e-7 of itself against 64 bits, as fp32 sums are; with two parts, and the sums running through all chunks, it was
+// within 6e-7 of itself against 64 bits, as fp32 sums are; with two parts, and the sums running through all chunks, it was
 // within 2.5e-6.  P and the copy of S that the readout multiplies are rounded to bf16 once
 // (half a step, 2^-8 of each term): the readout itself is rounded to bf16, and its error stays of that order.
 //
@@ -22,9 +22,9 @@
 // P and V'^T are operands in TMEM: with K' = diag(.) K split in shared memory instead (written, and read again beside V),
 // a chunk moved 590 KB through shared memory, now 430 KB, and the room of K' gives every input tile a second buffer.
 //
-// What it measured (d = 128): 8 x 16 scans of 8192 tokens with 16 checkpoints each, 1.22 GB in 213 us, 5.7 of the 6.7 TB/s
+// What it measured (d = 128): 8 x 16 scans of 8192 tokens with 16 checkpoints each, 1.22 GB in 211 us, 5.8 of the 6.7 TB/s
 // that a copy reaches (128 of 152 multiprocessors have a scan); 2.9 us a chunk without a checkpoint, where the products need
-// 1.6.  32 scans of 131072, cut into segments and read twice: 1.05 ms.
+// 1.6.  32 scans of 131072, cut into segments and read twice: 1.04 ms.
 //
 // One CTA takes one (job, head) from its first chunk to its last.  Roles:
 //   state  (warps 0-3):  S, a row a thread, in registers: a^n S + the chunk's products; its bf16 copy; checkpoints,
