@@ -654,7 +654,10 @@ def _expect(ok: bool, message: str) -> None:
 
 
 def _raw_stream(stream, dev) -> int:
-    """cudaStream_t of `stream`, or of the current stream of `dev` (without building a Stream object)."""
+    """cudaStream_t of `stream`, or of the current stream of `dev` (without building a Stream object).  Every call takes its
+    stream here, so this is where one whose tensors, all on `dev`, lie in host memory is refused."""
+    if dev.type != "cuda":
+        raise ValueError(f"the tensors must be on a GPU, not on {dev}")
     if stream is not None:
         return stream.cuda_stream
     return torch._C._cuda_getCurrentRawStream(dev.index if dev.index is not None else torch.cuda.current_device())
@@ -756,13 +759,14 @@ def gdn_linear_prefill(q, k, v, alpha, cu_seqlens, *, scale: float = 1.0, S0=Non
         elif n_ck:
             ckpt_states = torch.empty((n_ck, H, dv, dk), dtype=torch.float32, device=dev)
         scratch = torch.empty(nbytes, dtype=torch.uint8, device=dev) if nbytes else None
+    raw = _raw_stream(stream, dev)
     if ws is None:
         ws = workspace(dev)
     rc = L.gdn_linear_prefill(
         ctypes.byref(pr), None if q is None else q.data_ptr(), k.data_ptr(), v.data_ptr(), alpha.data_ptr(),
         None if S0 is None else S0.data_ptr(), index, slots, None if o is None else o.data_ptr(), S_final.data_ptr(),
         flat if n_ck else None, cu_ck, ckpt_states.data_ptr() if n_ck else None,
-        None if scratch is None else scratch.data_ptr(), nbytes, ws.data_ptr(), ws.numel(), _raw_stream(stream, dev))
+        None if scratch is None else scratch.data_ptr(), nbytes, ws.data_ptr(), ws.numel(), raw)
     if rc != GDN_OK:
         raise GdnError(rc, "gdn_linear_prefill")
     return {"o": o, "S_final": S_final, "ckpt_states": ckpt_states}
@@ -857,13 +861,13 @@ def gdn_prefix_attention(q, k_prefix, v_prefix, k_tail=None, v_tail=None, tail_l
         else:
             lse = torch.empty((B, n, Hq), dtype=torch.float32, device=dev)
         scratch = torch.empty(nbytes, dtype=torch.uint8, device=dev) if nbytes else None
+    raw = _raw_stream(stream, dev)
     if ws is None:
         ws = workspace(dev)
     rc = L.gdn_prefix_attention(
         ctypes.byref(pr), q.data_ptr(), k_prefix.data_ptr() if P else None, v_prefix.data_ptr() if P else None,
         k_tail.data_ptr() if cap else None, v_tail.data_ptr() if cap else None, tail_len.data_ptr() if cap else None,
-        o.data_ptr(), lse.data_ptr(), None if scratch is None else scratch.data_ptr(), nbytes, ws.data_ptr(), ws.numel(),
-        _raw_stream(stream, dev))
+        o.data_ptr(), lse.data_ptr(), None if scratch is None else scratch.data_ptr(), nbytes, ws.data_ptr(), ws.numel(), raw)
     if rc != GDN_OK:
         raise GdnError(rc, "gdn_prefix_attention")
     return {"o": o, "lse": lse}

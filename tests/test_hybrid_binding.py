@@ -1,0 +1,36 @@
+"""The binding of include/gdn_hybrid.h on the host (no GPU): arguments that no status code of the library can catch."""
+import types
+
+import pytest
+import torch
+
+import hybrid_model_recurrent_gb300 as gdn
+
+BF = torch.bfloat16
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    gdn.build()
+
+
+def linear(T=5):
+    """q, k, v and alpha of 2 key and 4 value heads, in host memory."""
+    return torch.zeros(T, 2, 64, dtype=BF), torch.zeros(T, 2, 64, dtype=BF), torch.zeros(T, 4, 64, dtype=BF), torch.ones(4)
+
+
+def test_host_tensors_are_refused():
+    """A kernel must never get a host address: tensors that agree in everything but lie in host memory are refused, with the
+    caller's stream as well."""
+    q, k, v, a = linear()
+    ws = torch.zeros(256, dtype=torch.uint8)
+    with pytest.raises(ValueError, match="GPU"):
+        gdn.gdn_linear_prefill(q, k, v, a, [0, 5], ws=ws)
+    states, o = torch.zeros(5, 4, 64, 64), torch.zeros(5, 4, 64, dtype=BF)
+    with pytest.raises(ValueError, match="GPU"):
+        gdn.gdn_linear_step(q, k, v, a, states)
+    with pytest.raises(ValueError, match="GPU"):
+        gdn.gdn_linear_step(q, k, v, a, states, o=o, stream=types.SimpleNamespace(cuda_stream=0))
+    pq, pk = torch.zeros(2, 1, 8, 64, dtype=BF), torch.zeros(10, 2, 64, dtype=BF)
+    with pytest.raises(ValueError, match="GPU"):
+        gdn.gdn_prefix_attention(pq, pk, pk, ws=ws)
