@@ -739,6 +739,8 @@ def gdn_linear_prefill(q, k, v, alpha, cu_seqlens, *, scale: float = 1.0, S0=Non
             index = [int(x) for x in S0_index]
             if len(index) != B:
                 raise ValueError("S0_index must give one slot per sequence")
+            if not all(-2 ** 31 <= x < 2 ** 31 for x in index):   # (ctypes would keep the low 32 bits)
+                raise ValueError("S0_index: a slot does not fit 32 bits")
             index = (ctypes.c_int32 * B)(*index)
     elif S0_index is not None:
         raise ValueError("S0_index without S0")

@@ -34,3 +34,12 @@ def test_host_tensors_are_refused():
     pq, pk = torch.zeros(2, 1, 8, 64, dtype=BF), torch.zeros(10, 2, 64, dtype=BF)
     with pytest.raises(ValueError, match="GPU"):
         gdn.gdn_prefix_attention(pq, pk, pk, ws=ws)
+
+
+@pytest.mark.parametrize("slot", [2 ** 32, 2 ** 32 + 1, -2 ** 32 - 1, 2 ** 31, -2 ** 31 - 1])
+def test_initial_slots_past_32_bits_are_refused(slot):
+    """A slot that 32 bits do not hold must not come out as another one (2^32 as slot 0)."""
+    q, k, v, a = linear()
+    with pytest.raises(ValueError, match="S0_index"):
+        gdn.gdn_linear_prefill(q, k, v, a, [0, 3, 5], S0=torch.zeros(3, 4, 64, 64), S0_index=[0, slot],
+                               ws=torch.zeros(256, dtype=torch.uint8))
