@@ -780,6 +780,8 @@ def gdn_linear_step(q, k, v, alpha, states, *, slots=None, scale: float = 1.0, o
 
     q, k [B, Hk, dk], v [B, H, dv]; states [num_slots, H, dv, dk] fp32; slots int32 [B] on the GPU (default: request b's
     slot is b), distinct but for negative ones, which mark padding rows (output 0).  Returns o [B, H, dv]."""
+    if q is None:
+        raise ValueError("a step needs q")
     dev = k.device
     out_dtype = out_dtype or k.dtype
     pr = _linear_problem(q, k, v, alpha, k.shape[0], None, scale, out_dtype)

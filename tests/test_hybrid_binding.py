@@ -43,3 +43,10 @@ def test_initial_slots_past_32_bits_are_refused(slot):
     with pytest.raises(ValueError, match="S0_index"):
         gdn.gdn_linear_prefill(q, k, v, a, [0, 3, 5], S0=torch.zeros(3, 4, 64, 64), S0_index=[0, slot],
                                ws=torch.zeros(256, dtype=torch.uint8))
+
+
+def test_step_without_queries_is_refused():
+    """A step always reads out."""
+    _, k, v, a = linear()
+    with pytest.raises(ValueError, match="q"):
+        gdn.gdn_linear_step(None, k, v, a, torch.zeros(5, 4, 64, 64))
