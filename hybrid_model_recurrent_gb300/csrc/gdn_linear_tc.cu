@@ -202,7 +202,8 @@ __global__ void __launch_bounds__(kThreads, 1) linear_tc_kernel(const __grid_con
         issued[0] = issued[1] = issued[2] = 0;
         fence_barrier_init();
     }
-    if (tid == 13 * 32) {   // the copies' descriptors, on their way while the barriers are made
+    if (tid == 13 * 32 && job.len > 0) {   // the copies' descriptors, on their way while the barriers are made (a call without
+                                           // tokens has none)
         for (const CUtensorMap* tm : {&p.tm_k, &p.tm_v, &p.tm_q})
             if (READOUT || tm != &p.tm_q)
                 asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(tm)) : "memory");

@@ -164,9 +164,10 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, NT == 1 ? 2 : 1)
                      "r"(F::kTmem));
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
     }
-    if (warp == NT * 4 + 1 && lane == 0) {
+    if (warp == NT * 4 + 1 && lane == 0) {   // the descriptors that there are: none without a prefix, none without tails
         for (const CUtensorMap* tm : {&p.tm_kp, &p.tm_vp, &p.tm_kt, &p.tm_vt})
-            asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(tm)) : "memory");
+            if (tm == &p.tm_kp || tm == &p.tm_vp ? p.prefix_len > 0 : p.max_tail > 0)
+                asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(tm)) : "memory");
     }
     if (tid == 0) {
         for (int i = 0; i < F::ST; ++i) mbar_init(&full[i], 1), mbar_init(&empty[i], 1);
