@@ -131,9 +131,14 @@ LinPlan plan_linear(const gdn_linear_problem* p) {
     return pl;
 }
 
+// A sequence with more checkpoints than a job holds takes several launches in a row, in a call of at most this many sequences.
+// The limit is one of the call, not of the plan: how the scans are cut does not decide what is accepted.
+constexpr int kLongListSeqs = 256;
+
 struct LinHostJob {
     gdn::lin::Job job;
     std::vector<gdn::lin::Ckpt> ckpts;
+    int round = 0;   // jobs of a round start from checkpoints of the round before
 };
 
 using EncodeFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
@@ -154,15 +159,16 @@ bool bf16_map(CUtensorMap* m, const void* base, int rank, const int64_t (&dim)[4
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// Batch jobs into parameter blocks, longest first.
+// Batch jobs into parameter blocks, a round after the other, longest first.
 template <class F>
 gdn_status launch_jobs(gdn::lin::Params& prm, std::vector<LinHostJob>& jobs, F&& launch) {
-    std::stable_sort(jobs.begin(), jobs.end(),
-                     [](const LinHostJob& a, const LinHostJob& b) { return a.job.len > b.job.len; });
+    std::stable_sort(jobs.begin(), jobs.end(), [](const LinHostJob& a, const LinHostJob& b) {
+        return a.round != b.round ? a.round < b.round : a.job.len > b.job.len;
+    });
     size_t i = 0;
     while (i < jobs.size()) {
         int nj = 0, nc = 0;
-        while (i + nj < jobs.size() && nj < gdn::lin::kMaxJobs &&
+        while (i + nj < jobs.size() && nj < gdn::lin::kMaxJobs && jobs[i + nj].round == jobs[i].round &&
                nc + (int)jobs[i + nj].ckpts.size() <= gdn::lin::kMaxCkpts) {
             gdn::lin::Job j = jobs[i + nj].job;
             j.ck_begin = nc;
@@ -213,6 +219,8 @@ gdn_status linear_prefill(const gdn_linear_problem* p, const void* q, const void
                     return GDN_ERR_INVALID_ARG;
         }
         if (n_ck >= (1ll << 23)) return GDN_ERR_UNSUPPORTED;
+        for (int b = 0; b < B; ++b)
+            if (cu_ckpt[b + 1] - cu_ckpt[b] > gdn::lin::kMaxCkpts && B > kLongListSeqs) return GDN_ERR_UNSUPPORTED;
     }
     const LinPlan pl = plan_linear(p);
     const size_t state = (size_t)H * p->d_v * p->d_k;
@@ -240,15 +248,32 @@ gdn_status linear_prefill(const gdn_linear_problem* p, const void* q, const void
             w.job.len = (int32_t)std::min(L, n - j * L);
             w.job.s0 = j == 0 ? s0 : seg_states + (size_t)(slot + j - 1) * state;
             w.job.s_final = j == segs - 1 ? S_final + (size_t)b * state : nullptr;
-            for (; ck < ck_end && ckpt_pos[ck] <= j * L + w.job.len; ++ck)
-                w.ckpts.push_back({(int32_t)(ckpt_pos[ck] - j * L), (int32_t)ck});
-            if (w.ckpts.size() > (size_t)gdn::lin::kMaxCkpts) return GDN_ERR_UNSUPPORTED;
             if (j < segs - 1) {
                 LinHostJob z{};
                 z.job = w.job;
                 z.job.s0 = nullptr;
                 z.job.s_final = seg_states + (size_t)(slot + j) * state;
                 own.push_back(std::move(z));
+            }
+            const int64_t end = j * L + w.job.len;
+            int64_t from_pos = j * L;
+            for (; ck < ck_end && ckpt_pos[ck] <= end; ++ck) {
+                if (w.ckpts.size() == (size_t)gdn::lin::kMaxCkpts) {
+                    // a full list: the job ends at its last checkpoint, and the next round's takes that state up
+                    const int64_t cut = ckpt_pos[ck - 1];
+                    LinHostJob rest{};
+                    rest.job = w.job;
+                    rest.job.tok_begin = beg + cut;
+                    rest.job.len = (int32_t)(end - cut);
+                    rest.job.s0 = ckpt_states + (size_t)(ck - 1) * state;
+                    rest.round = w.round + 1;
+                    w.job.len = (int32_t)(cut - from_pos);
+                    w.job.s_final = nullptr;
+                    jobs.push_back(std::move(w));
+                    w = std::move(rest);
+                    from_pos = cut;
+                }
+                w.ckpts.push_back({(int32_t)(ckpt_pos[ck] - from_pos), (int32_t)ck});
             }
             // without a readout a segment that ends in no wanted state has nothing to do
             if (o || w.job.s_final || !w.ckpts.empty()) jobs.push_back(std::move(w));

@@ -64,7 +64,9 @@ typedef struct gdn_linear_problem {
  *  s0_slots     slots of S0 (bound of s0_index; with s0_index NULL at least B)
  *  o            device [T, H, d_v] out_dtype, packed, or NULL
  *  S_final      device [B, H, d_v, d_k] fp32
- *  ckpt_pos, cu_ckpt, ckpt_states   as gdn_prefill_ckpt
+ *  ckpt_pos, cu_ckpt, ckpt_states   as gdn_prefill_ckpt; fewer than 2^23 in all.  A sequence
+ *               with more than 1536 takes several launches in a row, and is taken in a call of
+ *               at most 256 sequences (else GDN_ERR_UNSUPPORTED: give it a call of its own)
  *  scratch      device, 16-byte aligned, at least gdn_linear_scratch_bytes(p) bytes
  *               (may be NULL when that is 0): partial states of a call whose few long
  *               scans are split along the tokens
