@@ -60,6 +60,10 @@ using tcu::warp_wait_bar;
 constexpr int kRows = 128;   // rows of a tile
 constexpr int kKeys = 128;   // tokens of a tile
 constexpr float kRise = 8.f; // O is rescaled when a maximum has risen by more than this (log2)
+// A weight's exponent is score * scale - m in one rounding, but m is a product already rounded: for the largest score its
+// rounding error is left, half a step of m, 16 at 2^28 and past what an exponential holds from 2^31 on.  Rows further from zero
+// than this round the product by itself first.
+constexpr float kFar = 268435456.f;
 
 template <int D, int NT>
 struct Cfg {
@@ -129,6 +133,28 @@ __device__ __forceinline__ Item item_at(const Params& p, int item, int pre_items
     x.n1 = (x.hi1 - x.lo1 + kKeys - 1) / kKeys;
     x.n_tiles = x.n1 + (x.hi2 - x.lo2 + kKeys - 1) / kKeys;
     return x;
+}
+
+// The weights of a tile's row, over its own scores in TMEM, for rows far from zero; returns their sum.  A function by itself:
+// inlined, it made the kernel 4 % slower where no row is far (turns of 16 x 256 tokens: 806 us against 778), a call 1 % (787).
+__device__ __noinline__ float far_weights(uint32_t taddr, int seen, float scale, float base) {
+    float sum = 0.f;
+#pragma unroll 1
+    for (int c = 0; c < kKeys / 32; ++c) {
+        float x[32];
+        uint32_t w[16];
+        tmem_ld32(taddr + 32 * c, x);
+#pragma unroll
+        for (int i = 0; i < 32; ++i) {
+            const float y = __fsub_rn(__fmul_rn(x[i], scale), base);
+            x[i] = 32 * c + i < seen ? ex2(y) : 0.f;
+            sum += x[i];
+        }
+#pragma unroll
+        for (int i = 0; i < 16; ++i) w[i] = pack2(x[2 * i], x[2 * i + 1]);
+        tmem_st16(taddr + 16 * c, w);
+    }
+    return sum;
 }
 
 template <int D, int NT>
@@ -453,21 +479,25 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, NT == 1 ? 2 : 1)
                     const float base = m == -INFINITY ? 0.f : m;
                     const float2 scale2 = make_float2(scale, scale), base2 = make_float2(-base, -base);
                     float2 sum0 = make_float2(0.f, 0.f), sum1 = sum0;
+                    if (__any_sync(0xffffffffu, fabsf(base) > kFar)) {
+                        sum0.x = far_weights(trow + a * 128, seen, scale, base);
+                    } else {
 #pragma unroll
-                    for (int half = 0; half < 2; ++half) {
-                        float(&s0)[32] = s[kKeep ? 2 * half : 0], (&s1)[32] = s[kKeep ? 2 * half + 1 : 1];
-                        if (!kKeep) load(half, s0, s1);
-                        uint32_t w0[16], w1[16];
+                        for (int half = 0; half < 2; ++half) {
+                            float(&s0)[32] = s[kKeep ? 2 * half : 0], (&s1)[32] = s[kKeep ? 2 * half + 1 : 1];
+                            if (!kKeep) load(half, s0, s1);
+                            uint32_t w0[16], w1[16];
 #pragma unroll
-                        for (int i = 0; i < 16; ++i) {
-                            float2 e = __ffma2_rn(make_float2(s0[2 * i], s0[2 * i + 1]), scale2, base2);
-                            float2 g = __ffma2_rn(make_float2(s1[2 * i], s1[2 * i + 1]), scale2, base2);
-                            e = make_float2(ex2(e.x), ex2(e.y)), g = make_float2(ex2(g.x), ex2(g.y));
-                            sum0 = __fadd2_rn(sum0, e), sum1 = __fadd2_rn(sum1, g);
-                            w0[i] = pack2(e.x, e.y), w1[i] = pack2(g.x, g.y);
+                            for (int i = 0; i < 16; ++i) {
+                                float2 e = __ffma2_rn(make_float2(s0[2 * i], s0[2 * i + 1]), scale2, base2);
+                                float2 g = __ffma2_rn(make_float2(s1[2 * i], s1[2 * i + 1]), scale2, base2);
+                                e = make_float2(ex2(e.x), ex2(e.y)), g = make_float2(ex2(g.x), ex2(g.y));
+                                sum0 = __fadd2_rn(sum0, e), sum1 = __fadd2_rn(sum1, g);
+                                w0[i] = pack2(e.x, e.y), w1[i] = pack2(g.x, g.y);
+                            }
+                            tmem_st16(trow + a * 128 + 32 * half, w0);
+                            tmem_st16(trow + a * 128 + 32 * half + 16, w1);
                         }
-                        tmem_st16(trow + a * 128 + 32 * half, w0);
-                        tmem_st16(trow + a * 128 + 32 * half + 16, w1);
                     }
                     l += (sum0.x + sum0.y) + (sum1.x + sum1.y);
                     tmem_st_wait();
