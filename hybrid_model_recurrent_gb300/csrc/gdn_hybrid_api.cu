@@ -337,12 +337,15 @@ struct PrefixPlan {
     int parts() const { return pre_splits + tail_splits; }
 };
 
+// what the kernels multiply scores by: exponentials of base 2
+float scale_log2(const gdn_prefix_problem& f) { return (float)((double)f.softmax_scale * 1.4426950408889634); }
+
 gdn_status check_prefix(const gdn_prefix_problem* p, gdn_prefix_problem& f) {
     if (!p) return GDN_ERR_INVALID_ARG;
     f = *p;
     if (f.batch < 1 || f.num_queries < 1 || f.num_q_heads < 1 || f.num_kv_heads < 1 || f.head_dim < 1)
         return GDN_ERR_INVALID_ARG;
-    if (f.num_q_heads % f.num_kv_heads || !known_dtype(f.dtype) || !std::isfinite(f.softmax_scale))
+    if (f.num_q_heads % f.num_kv_heads || !known_dtype(f.dtype) || !std::isfinite(scale_log2(f)))
         return GDN_ERR_INVALID_ARG;
     if (f.prefix_len < 0 || f.tail_cap < 0 || f.max_tail < 0 || f.max_tail > f.tail_cap) return GDN_ERR_INVALID_ARG;
     if (!supported_d(f.head_dim)) return GDN_ERR_UNSUPPORTED;
@@ -465,7 +468,7 @@ gdn_status prefix_attention(const gdn_prefix_problem* p, const void* q, const vo
     prm->wait_limit_ns = gdn::wait_limit_ns();
     prm->stall_after = gdn::stall_after();
     prm->prefix_len = f.prefix_len, prm->max_tail = f.max_tail;
-    prm->scale_log2 = (float)((double)f.softmax_scale * 1.4426950408889634);
+    prm->scale_log2 = scale_log2(f);
     prm->B = f.batch, prm->n = f.num_queries, prm->Hq = f.num_q_heads, prm->Hkv = f.num_kv_heads;
     prm->G = f.num_q_heads / f.num_kv_heads;
     prm->pre_splits = pl.pre_splits, prm->pre_chunk = pl.pre_chunk, prm->tail_splits = pl.tail_splits;

@@ -114,6 +114,7 @@ gdn_status gdn_linear_step(const gdn_linear_problem* p, const void* q, const voi
  *  num_q_heads, num_kv_heads   num_kv_heads divides num_q_heads; head h reads key/value
  *               head h / (num_q_heads / num_kv_heads)
  *  head_dim     32, 64 or 128
+ *  softmax_scale  any sign; softmax_scale * log2 e finite in fp32
  *  prefix_len   P >= 0;  tail_cap  tokens a request's tail buffer holds, >= 0
  *  max_tail     host bound of tail_len (0 .. tail_cap); tail_len values above it are
  *               taken as max_tail, negative ones as 0
