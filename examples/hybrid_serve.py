@@ -53,7 +53,8 @@ class Server:
         self.w, self.B, self.cap = w, requests, capacity
         self.dtype = w["embed"].dtype
         dev = w["embed"].device
-        self.lens = torch.zeros(requests, dtype=torch.int32, device=dev)
+        self.lens = torch.zeros(requests, dtype=torch.int32, device=dev)   # tokens in each request's tail
+        self.forks = [0] * requests   # the state that each request's linear layers go on from: at first the prefix's
         self.state = []
         x = w["embed"][prefix].float()
         P = len(prefix)
@@ -72,23 +73,25 @@ class Server:
             x = x + (y.flatten(-2) @ ly["o"].T).float()
 
     def turn(self, prompts):
-        """Prefill one ragged turn (a list of token tensors); returns the logits of each request's last token."""
+        """Prefill a ragged turn (a list of token tensors, one a request) after what each request has; returns the logits of each
+        request's last token."""
         n = [len(p) for p in prompts]
         top, cu = max(n), [0]
         for m in n:
             cu.append(cu[-1] + m)
         dev = self.lens.device
+        had = self.lens.long()
         self.lens += torch.tensor(n, dtype=torch.int32, device=dev)
         x = self.w["embed"][torch.cat(prompts)].float()
         # attention takes the last `top` tokens of every tail: rows of shorter turns are padded in front
         row = torch.cat([torch.arange(m, device=dev) + b * top + top - m for b, m in enumerate(n)])
-        pos = torch.cat([torch.arange(m, device=dev) for m in n])
         req = torch.repeat_interleave(torch.arange(self.B, device=dev), torch.tensor(n, device=dev))
+        pos = torch.cat([torch.arange(m, device=dev) for m in n]) + had[req]
         for i, ly in enumerate(self.w["layers"]):
             q, k, v = (heads(x, ly[c], self.dtype) for c in "qkv")
             if ly["kind"] == "linear":
                 r = gdn.gdn_linear_prefill(q, k, v, self.w["alpha"], cu, scale=D_HEAD ** -0.5, S0=self.state[i],
-                                           S0_index=[0] * self.B)
+                                           S0_index=self.forks)
                 self.state[i], y = r["S_final"], r["o"]
             else:
                 kp, vp, kt, vt = self.state[i]
@@ -97,6 +100,7 @@ class Server:
                 qp[row] = q
                 y = gdn.gdn_prefix_attention(qp.unflatten(0, (self.B, top)), kp, vp, kt, vt, self.lens)["o"].flatten(0, 1)[row]
             x = x + (y.flatten(-2) @ ly["o"].T).float()
+        self.forks = list(range(self.B))   # from now on its own
         return self.logits(x[torch.tensor(cu[1:], device=dev) - 1])
 
     def step(self, tokens):
