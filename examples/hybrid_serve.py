@@ -54,6 +54,7 @@ class Server:
         self.dtype = w["embed"].dtype
         dev = w["embed"].device
         self.lens = torch.zeros(requests, dtype=torch.int32, device=dev)   # tokens in each request's tail
+        self.used = [0] * requests    # the same, for checks on the host
         self.forks = [0] * requests   # the state that each request's linear layers go on from: at first the prefix's
         self.state = []
         x = w["embed"][prefix].float()
@@ -72,10 +73,18 @@ class Server:
                 self.state.append((k, v, *tails))
             x = x + (y.flatten(-2) @ ly["o"].T).float()
 
+    def grow(self, n):
+        """Room for n[b] more tokens in request b's tail."""
+        used = [u + m for u, m in zip(self.used, n)]
+        if max(used) > self.cap:
+            raise ValueError(f"a tail of {max(used)} tokens is past the capacity of {self.cap}")
+        self.used = used
+
     def turn(self, prompts):
         """Prefill a ragged turn (a list of token tensors, one a request) after what each request has; returns the logits of each
         request's last token."""
         n = [len(p) for p in prompts]
+        self.grow(n)
         top, cu = max(n), [0]
         for m in n:
             cu.append(cu[-1] + m)
@@ -105,6 +114,7 @@ class Server:
 
     def step(self, tokens):
         """One token a request; returns its logits."""
+        self.grow([1] * self.B)
         x = self.w["embed"][tokens].float()
         at = self.lens.long()
         every = torch.arange(self.B, device=tokens.device)

@@ -99,3 +99,22 @@ def test_turns_and_steps_follow_one_another(server):
         new = [tokens(n) for n in (lens or (1, 1, 1))]
         seqs = [torch.cat(x) for x in zip(seqs, new)]
         check(w, s.turn(new) if lens else s.step(torch.cat(new)), seqs)
+
+
+def test_tails_past_their_capacity_are_refused(server):
+    """On the host and before anything changes: an index past a buffer would reach the GPU otherwise."""
+    w, prefix, tokens, make = server
+    s, first = make(8), [tokens(6), tokens(1), tokens(3)]
+    with pytest.raises(ValueError, match="capacity"):
+        s.turn([tokens(1), tokens(9), tokens(1)])
+    check(w, s.turn(first), [torch.cat([prefix, t]) for t in first])
+    with pytest.raises(ValueError, match="capacity"):
+        s.turn([tokens(3), tokens(1), tokens(1)])
+    seqs = [torch.cat([prefix, t]) for t in first]
+    for _ in range(2):
+        new = tokens(3)
+        seqs = [torch.cat([q, new[b:b + 1]]) for b, q in enumerate(seqs)]
+        check(w, s.step(new), seqs)
+    with pytest.raises(ValueError, match="capacity"):
+        s.step(tokens(3))
+    assert s.lens.tolist() == [8, 3, 5]
