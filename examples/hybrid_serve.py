@@ -84,6 +84,8 @@ class Server:
         """Prefill a ragged turn (a list of token tensors, one a request) after what each request has; returns the logits of each
         request's last token."""
         n = [len(p) for p in prompts]
+        if len(n) != self.B or min(n) < 1:
+            raise ValueError("a turn takes a prompt of at least one token for each request")
         self.grow(n)
         top, cu = max(n), [0]
         for m in n:

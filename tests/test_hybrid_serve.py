@@ -118,3 +118,13 @@ def test_tails_past_their_capacity_are_refused(server):
     with pytest.raises(ValueError, match="capacity"):
         s.step(tokens(3))
     assert s.lens.tolist() == [8, 3, 5]
+
+
+@pytest.mark.parametrize("lens", [(0, 2, 3), (2, 0, 3), (2, 3, 0), (0, 0, 0), (2, 3), (2, 3, 1, 1)])
+def test_turns_without_a_token_for_each_request_are_refused(server, lens):
+    """A request without a token has no last token whose logits the turn could return (it would get another's)."""
+    w, _, tokens, make = server
+    s = make(8)
+    with pytest.raises(ValueError, match="prompt"):
+        s.turn([tokens(n) for n in lens])
+    assert s.lens.tolist() == [0, 0, 0]
