@@ -60,7 +60,6 @@ using tc::sw128;
 using tc::tc_fence_after;
 using tc::tc_fence_before;
 using tc::tmem_ld32;
-using tc::tmem_ld32x2;
 using tc::tmem_st16;
 using tc::tmem_st32;
 using tc::tmem_st_wait;

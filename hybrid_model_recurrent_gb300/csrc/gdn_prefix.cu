@@ -246,8 +246,7 @@ cudaError_t join(const Params& p, int parts, cudaStream_t s) {
 
 cudaError_t launch_simt(const Params& p, int D, bool bf16, cudaStream_t s) {
     if (D == 32) return bf16 ? part<32, __nv_bfloat16>(p, s) : part<32, float>(p, s);
-    if (D == 64) return bf16 ? part<64, __nv_bfloat16>(p, s) : part<64, float>(p, s);
-    return bf16 ? part<128, __nv_bfloat16>(p, s) : part<128, float>(p, s);
+    return D == 64 ? part<64, float>(p, s) : part<128, float>(p, s);   // (wider bf16: launch_tc)
 }
 cudaError_t launch_join(const Params& p, int D, bool bf16, int parts, cudaStream_t s) {
     if (D == 32) return bf16 ? join<32, __nv_bfloat16>(p, parts, s) : join<32, float>(p, parts, s);
