@@ -14,7 +14,7 @@
 // pipes' 37 T instructions a second).
 //
 // The step.  A warp holds 16 or 8 rows of one head's state, read and written once: 268 MB in 46 us (64 requests x 32 heads
-// at d = 128, or 256 x 32 at d = 64) are 5.9 of the 6.7 TB/s that a copy reaches.
+// at d = 128, or 256 x 32 at d = 64), a call among others, are 5.9 of the 6.7 TB/s that a copy reaches.
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -27,11 +27,9 @@ namespace lin {
 namespace {
 
 __device__ __forceinline__ uint32_t saddr(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
-// 16-byte (or 8-byte) asynchronous copy; bytes = 0 fills with zeros
-template <int BYTES>
+// 16-byte asynchronous copy; bytes = 0 fills with zeros
 __device__ __forceinline__ void cp_async(void* dst, const void* src, int bytes) {
-    asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(saddr(dst)), "l"(src), "n"(BYTES), "r"(bytes)
-                 : "memory");
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 16, %2;" ::"r"(saddr(dst)), "l"(src), "r"(bytes) : "memory");
 }
 __device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
@@ -177,13 +175,13 @@ __global__ void __launch_bounds__(128) linear_scan_kernel(const __grid_constant_
             const int t = i / (DK / kPiece), x = (i % (DK / kPiece)) * kPiece;
             const int ts = min(t0 + t, len - 1);   // past the end: a valid address, nothing copied
             const int n = t0 + t < len ? 16 : 0;
-            cp_async<16>(&sk[buf][t][x], gk + (int64_t)ts * p.k_stride + x, n);
-            if (READOUT) cp_async<16>(&sq[buf][t][x], gq + (int64_t)ts * p.q_stride + x, n);
+            cp_async(&sk[buf][t][x], gk + (int64_t)ts * p.k_stride + x, n);
+            if (READOUT) cp_async(&sq[buf][t][x], gq + (int64_t)ts * p.q_stride + x, n);
         }
         for (int i = tid; tile < tiles && i < kTile * (RB / kPiece); i += blockDim.x) {
             const int t = i / (RB / kPiece), x = (i % (RB / kPiece)) * kPiece;
             const int ts = min(t0 + t, len - 1);
-            cp_async<16>(&sv[buf][t][x], gv + (int64_t)ts * p.v_stride + x, t0 + t < len ? 16 : 0);
+            cp_async(&sv[buf][t][x], gv + (int64_t)ts * p.v_stride + x, t0 + t < len ? 16 : 0);
         }
         cp_commit();
     };
@@ -357,8 +355,8 @@ cudaError_t scan_types(const Params& p, bool in_bf16, bool out_bf16, cudaStream_
 
 template <int DK>
 cudaError_t step_types(const StepParams& p, bool in_bf16, bool out_bf16, cudaStream_t s) {
-    // rows of a lane: 2 keep twice the warps in flight (64 requests x 32 heads at d = 128: 48 us against 70 with 4; 256 x 32
-    // at d = 64, fp32: 47 against 53); at d_k = 32 a lane has 16 bytes of a row and takes 4
+    // rows of a lane: 2 keep twice the warps in flight (GPU time, 64 requests x 32 heads at d = 128: 43 us against 57 with 4;
+    // 256 x 32 at d = 64, fp32: 44 against 51); at d_k = 32 a lane has 16 bytes of a row and takes 4
     constexpr int R = DK >= 64 ? 2 : 4;
     const int64_t warps = (int64_t)p.B * p.H * (p.dv / (4 * R));
     const int per = 4;

@@ -22,7 +22,7 @@
 // P and V'^T are operands in TMEM: with K' = diag(.) K split in shared memory instead (written, and read again beside V),
 // a chunk moved 590 KB through shared memory, now 430 KB, and the room of K' gives every input tile a second buffer.
 //
-// What it measured (d = 128): 8 x 16 scans of 8192 tokens with 16 checkpoints each, 1.22 GB in 211 us, 5.8 of the 6.7 TB/s
+// What it measured (d = 128): 8 x 16 scans of 8192 tokens with 16 checkpoints each, 1.22 GB in 207 us, 5.9 of the 6.7 TB/s
 // that a copy reaches (128 of 152 multiprocessors have a scan); 2.9 us a chunk without a checkpoint, where the products need
 // 1.6.  32 scans of 131072, cut into segments and read twice: 1.04 ms.
 //
@@ -148,6 +148,9 @@ struct Walk {
     }
 };
 
+// 512 threads leave 128 registers a thread, by which the compiler spills although the state role has 208 later: with a readout
+// 236 bytes of stores and 256 of loads a thread (128 x 128), 200 and 240 (128 x 64), 100 or less otherwise; without one 172 and
+// 140 (128 x 64), else 80 or less.  What that costs has not been measured by itself.
 template <int DK, int DV, bool READOUT>
 __global__ void __launch_bounds__(kThreads, 1) linear_tc_kernel(const __grid_constant__ Params p) {
     constexpr int NB = READOUT ? 2 : 3;               // buffers of K and of V (Q is spent early in its chunk: one)

@@ -1,11 +1,11 @@
-// gdn_prefix.cu - attention for a batch that shares a long prefix, on the FP32 pipes (every size and type), and the
+// gdn_prefix.cu - attention for a batch that shares a long prefix, on the FP32 pipes (fp32, and bf16 of width 32), and the
 // join of the parts.
 //
 // A CTA takes 16 query rows against one range of tokens, in tiles of 32: a lane scores one token for its warp's 4
 // rows, the warp keeps each row's running maximum and sum, and the value product runs with a lane holding D/32
 // columns of the 4 rows.  One pass over the keys and values; scores, statistics and sums in fp32.
 //
-// What bounds it: few rows, latency (7 requests x 8 heads on 2047 + 77 tokens, d = 64, fp32: 20 us for 9.5 MB, join and
+// What bounds it: few rows, latency (7 requests x 8 heads on 2047 + 77 tokens, d = 64, fp32: 17 us for 9.5 MB, join and
 // all); many, the FP32 pipes.  The join reads each part's sums once, from the L2 cache.
 #include <cuda_bf16.h>
 
@@ -172,7 +172,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) prefix_join_kernel(const __gr
     float l = 0.f, acc[CC];
 #pragma unroll
     for (int j = 0; j < CC; ++j) acc[j] = 0.f;
-    // parts at a time: few rows have few warps to hide their loads behind (56 rows in 85 parts: 17 us with the FP32-pipe
+    // parts at a time: few rows have few warps to hide their loads behind (7 rows a head in 67 parts: 17 us with the FP32-pipe
     // kernel against 19 with 1; 16 columns have as many loads in one part)
     constexpr int U = CC == 8 ? 2 : 1;
 #pragma unroll 1

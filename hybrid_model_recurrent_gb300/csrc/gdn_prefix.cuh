@@ -1,6 +1,6 @@
 // gdn_prefix.cuh - attention for a batch that shares a long prefix: the parameter block and launchers shared by
-// the kernels (gdn_prefix.cu: every size and type, and the join; gdn_prefix_tc.cu: tensor cores) and the host
-// side (gdn_hybrid_api.cu).
+// the kernels (gdn_prefix_tc.cu: tensor cores, bf16 of width 64 and 128; gdn_prefix.cu: every other size and type, and
+// the join) and the host side (gdn_hybrid_api.cu).
 //
 // The work falls into parts: `pre_splits` ranges of the prefix, taken by the stacked query rows of all requests,
 // and `tail_splits` ranges of each request's own tail, taken by its own rows.  A part leaves, for every query row,
@@ -17,7 +17,8 @@
 namespace gdn {
 namespace prefix {
 
-// Division of 0 <= x < 2^31 by a fixed d >= 1 as a multiplication (m = floor(2^32 (2^s - d) / d) + 1, s = ceil(log2 d):
+// Division of 0 <= x < 2^31 by a fixed d >= 1 as a multiplication, by Granlund and Montgomery's method ("Division by invariant
+// integers using multiplication", 1994: m = floor(2^32 (2^s - d) / d) + 1, s = ceil(log2 d):
 // x / d = (mulhi(x, m) + x) >> s).  A CTA finds its item with half a dozen of them, and starts on a cold instruction
 // cache, where the divisions' code took longer than their arithmetic.
 struct Div {
@@ -79,7 +80,7 @@ __device__ __forceinline__ void tail_range(const Params& p, int len, int tile, i
 constexpr int kSimtRows = 16;    // query rows of a tile of the FP32-pipe kernel
 constexpr int kSimtKeys = 32;    // tokens of a staged tile
 
-constexpr int kSms = 152;        // multiprocessors of a GB300: the wave that a persistent grid fills
+constexpr int kSms = 152;        // multiprocessors of a GB300, by which the host estimates how many CTAs run at once
 constexpr int kTcRows = 128;     // query rows of a row tile, and tokens of a tile, of the tensor-core kernel
 constexpr int kTcKeys = 128;
 

@@ -9,14 +9,14 @@
 // weights are at most 2^8 and only their common scale differs.  Scores, statistics and sums are fp32; the weights are
 // rounded to bf16 for the product (half a step, 2^-8 of each weight), as the tensor cores take them.
 //
-// Roles: warps 0 .. 4 NT - 1 softmax (one warpgroup a row tile), then one MMA-issuing thread and one copying thread.
+// Roles: warps 0 .. 4 NT - 1 softmax (one warpgroup a row tile), then a warp that issues products and one copying thread.
 // K and V tiles arrive by TMA in a ring of ST tiles; with NT = 2 both row tiles use each tile, and one tile's softmax
 // runs beside the other's products (an item of at most 128 rows uses one).  With NT = 1 two CTAs share a multiprocessor and
 // overlap each other instead.  A CTA takes one item after the other, the copies running ahead into the next one.
 //
 // What bounds it: where queries are many, a tile's chain of product, softmax and product (16 requests x 256 tokens x 32
-// heads on 16384 + 700 tokens, d = 128: 797 us, 1418 TFLOP/s, 0.75 of a library product's rate); where they are few, the
-// reading of the prefix and the start and end of each CTA (64 x 32 heads on 32768 + 1024 tokens: 73 us, 3.7 TB/s).
+// heads on 16384 + 700 tokens, d = 128: 784 us, 1440 TFLOP/s, 0.76 of a library product's rate); where they are few, the
+// reading of the prefix and the start and end of each CTA (64 x 32 heads on 32768 + 1024 tokens: 74 us, 3.6 TB/s).
 //
 // A masked token's score is replaced (not multiplied), and value rows past the range are zeroed in shared memory
 // before the product, so nothing that lies past a tail's end reaches a result.

@@ -13,9 +13,11 @@
  * rule, without defining them.)
  *
  * All values are expected to be finite.  An infinity or NaN spreads to what it takes part
- * in, and with d_k, d_v in {64, 128} and bf16 inputs (products of whole tiles) also to
- * the other tokens of its own sequence within the same 128-token tile.  Nothing outside a
- * sequence's own tokens, or past a request's tail length, is ever taken into a result.
+ * in, and, in the linear prefill with d_k, d_v in {64, 128} and bf16 inputs (products of
+ * whole tiles), also to the other tokens of its own sequence within the same 128-token
+ * tile; in the attention, from a value of a request's tail also to that request's queries
+ * that come before it.  Nothing outside a sequence's own tokens, or past a request's tail
+ * length, is ever taken into a result.
  */
 #ifndef GDN_HYBRID_H
 #define GDN_HYBRID_H
