@@ -17,6 +17,14 @@ and in ``include/gdn_hybrid.h`` (the other layers of a hybrid model):
 * ``gdn_linear_step``       the same, one token a request, states in place
 * ``gdn_prefix_attention``  attention of a batch that shares a long prefix
 
+and in ``include/gdn_cache.h`` (a paged key/value cache in 8 bits: ``PagedCache``):
+
+* ``gdn_qk_norm_rope``      norm of each head of queries and keys, and their rotation
+* ``gdn_cache_append``      new keys and values into the pages
+* ``gdn_paged_attention``   attention of each request's new tokens over its pages
+* ``gdn_cache_update``      rows freed, forked and grown
+* ``gdn_cache_compact``     pages in use moved together
+
 There is no fallback: if the compiled library is missing the import of a
 compute entry point raises.
 """
@@ -98,6 +106,25 @@ class _PrefixProblem(ctypes.Structure):
                                       "vt_stride_b", "vt_stride_t", "vt_stride_h")]
 
 
+class _Rope(ctypes.Structure):
+    _fields_ = [("num_tokens", ctypes.c_int64), ("num_q_heads", ctypes.c_int32), ("num_k_heads", ctypes.c_int32),
+                ("head_dim", ctypes.c_int32), ("rotary_dim", ctypes.c_int32), ("dtype", ctypes.c_int),
+                ("layout", ctypes.c_int), ("normalize", ctypes.c_int32), ("eps", ctypes.c_float),
+                ("mscale", ctypes.c_float)] + [(n, ctypes.c_int64) for n in ("q_stride", "k_stride", "q_out_stride",
+                                                                             "k_out_stride")]
+
+
+class _Cache(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("num_layers", "num_pages", "page_size", "num_kv_heads", "head_dim",
+                                              "num_rows", "row_pages")] + [
+        (n, ctypes.c_void_p) for n in ("pages", "scales", "table", "lens", "refs")]
+
+
+class _Batch(ctypes.Structure):
+    _fields_ = [("num_requests", ctypes.c_int32), ("max_new", ctypes.c_int32), ("num_tokens", ctypes.c_int64),
+                ("max_len", ctypes.c_int64), ("cu_new", ctypes.c_void_p), ("rows", ctypes.c_void_p)]
+
+
 def build(force: bool = False) -> str:
     from . import _build
     return _build.build(force=force)
@@ -157,7 +184,19 @@ def lib():
             L.gdn_prefix_scratch_bytes.argtypes = [PP]
             L.gdn_prefix_scratch_bytes.restype = sz
             L.gdn_prefix_attention.argtypes = [PP, vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp, sz, vp]
-            for f in ("gdn_linear_prefill", "gdn_linear_step", "gdn_prefix_attention"):
+            RP, CP, BP = ctypes.POINTER(_Rope), ctypes.POINTER(_Cache), ctypes.POINTER(_Batch)
+            L.gdn_qk_norm_rope.argtypes = [RP] + [vp] * 9
+            L.gdn_cache_append.argtypes = [CP, i32, BP, vp, vp, ctypes.c_int, i64, i64, vp, sz, vp]
+            L.gdn_paged_scratch_bytes.argtypes = [CP, BP, ctypes.c_int, i32]
+            L.gdn_paged_scratch_bytes.restype = sz
+            L.gdn_paged_attention.argtypes = [CP, i32, BP, vp, ctypes.c_int, i32, i64, ctypes.c_float, vp, vp, vp, sz, vp,
+                                              sz, vp]
+            L.gdn_cache_scratch_bytes.argtypes = [CP]
+            L.gdn_cache_scratch_bytes.restype = sz
+            L.gdn_cache_update.argtypes = [CP, i32, vp, i32, vp, vp, vp, vp, vp, sz, vp, sz, vp]
+            L.gdn_cache_compact.argtypes = [CP, vp, vp, sz, vp, sz, vp]
+            for f in ("gdn_linear_prefill", "gdn_linear_step", "gdn_prefix_attention", "gdn_qk_norm_rope",
+                      "gdn_cache_append", "gdn_paged_attention", "gdn_cache_update", "gdn_cache_compact"):
                 getattr(L, f).restype = ctypes.c_int
             for f in ("gdn_prefill_ckpt", "gdn_resume_from_ckpt", "gdn_tail_replay", "gdn_step", "gdn_replay_plan",
                       "gdn_select_ckpt", "gdn_clear_status", "gdn_read_status"):
@@ -875,3 +914,278 @@ def gdn_prefix_attention(q, k_prefix, v_prefix, k_tail=None, v_tail=None, tail_l
     if rc != GDN_OK:
         raise GdnError(rc, "gdn_prefix_attention")
     return {"o": o, "lse": lse}
+
+
+# ---- a paged key/value cache in 8 bits (include/gdn_cache.h) ------------------------------------------
+
+
+def gdn_rope_frequencies(rotary_dim: int, *, base: float = 10000.0, scaling: str = "none", factor: float = 1.0,
+                         original_len: int = 4096, fast_turns: float = 32.0, slow_turns: float = 1.0, device="cuda"):
+    """Frequencies (radians a token, float64 [rotary_dim / 2]) for ``gdn_qk_norm_rope``.
+
+    scaling for contexts `factor` times as long as the `original_len` a model was trained on: "linear" (every position
+    divided by factor), "base" (the base raised so that the slowest pair is stretched by factor), or "parts" (pairs that
+    turn at least fast_turns times within original_len are left, those below slow_turns stretched, those between in
+    part, linearly in their turns)."""
+    _expect(rotary_dim >= 0 and rotary_dim % 16 == 0, "rotary_dim must be a multiple of 16")
+    if not (base > 0 and factor >= 1 and original_len > 0 and fast_turns > slow_turns >= 0):
+        raise ValueError("base and original_len must be positive, factor at least 1, fast_turns above slow_turns")
+    i = np.arange(0, rotary_dim, 2, dtype=np.float64) / max(rotary_dim, 1)
+    if scaling == "base" and rotary_dim > 2:
+        base = base * factor ** (rotary_dim / (rotary_dim - 2))
+    f = float(base) ** -i
+    if scaling == "linear":
+        f = f / factor
+    elif scaling == "parts":
+        keep = np.clip((original_len * f / (2 * np.pi) - slow_turns) / (fast_turns - slow_turns), 0.0, 1.0)
+        f = f * keep + f / factor * (1 - keep)
+    elif scaling not in ("none", "base"):
+        raise ValueError(f"unknown scaling {scaling!r}")
+    return torch.from_numpy(f).to(device)
+
+
+class _device:
+    """The launches of a call go to the device of its tensors."""
+
+    def __init__(self, dev):
+        at = torch.cuda.current_device()
+        self.guard = None if dev.index is None or dev.index == at else torch.cuda.device(dev)
+
+    def __enter__(self):
+        if self.guard:
+            self.guard.__enter__()
+
+    def __exit__(self, *e):
+        if self.guard:
+            self.guard.__exit__(*e)
+
+
+def _same(x, like, name: str, shape) -> None:
+    if x.shape != shape or x.dtype != like.dtype or x.device != like.device:
+        raise ValueError(f"{name} must be a {like.dtype} tensor of shape {tuple(shape)} on {like.device}")
+
+
+def gdn_qk_norm_rope(q, k, positions, inv_freq, *, layout: str = "half", q_weight=None, k_weight=None,
+                     eps: Optional[float] = None, mscale: float = 1.0, q_out=None, k_out=None, stream=None):
+    """Norm of each head of queries and keys, and the rotation by their positions, in one pass (see the header).
+
+    q [T, Hq, D], k [T, Hk, D] or None, rows at any stride (slices of one projection's output); positions int32 [T];
+    inv_freq float64 [rotary_dim / 2] (``gdn_rope_frequencies``), radians a token, or None for no rotation.  layout: "half"
+    (pairs i, i + rotary_dim / 2) or "interleaved" (2 i, 2 i + 1).  eps None: no norm.  q_out, k_out may be q and k.
+    Returns (q_out, k_out)."""
+    dev, dt = q.device, q.dtype
+    raw = _raw_stream(stream, dev)
+    _expect(q.dim() == 3, "q must be [T, Hq, D]")
+    T, Hq, D = q.shape
+    Hk = 0
+    if k is not None:
+        _expect(k.dim() == 3, "k must be [T, Hk, D]")
+        Hk = k.shape[1]
+        _same(k, q, "k", (T, Hk, D))
+    _expect(layout in ("half", "interleaved"), f"unknown layout {layout!r}")
+    rd = 0
+    if inv_freq is not None:
+        rd = 2 * inv_freq.shape[0]
+        _dense(inv_freq, "inv_freq", (rd // 2,), torch.float64, dev)
+        if rd:
+            _expect(positions is not None, "a rotation needs positions")
+            _dense(positions, "positions", (T,), torch.int32, dev)
+    for w, name in ((q_weight, "q_weight"), (k_weight, "k_weight")):
+        if w is not None:
+            _expect(eps is not None, "weights of a norm need eps")
+            _dense(w, name, (D,), dt, dev)
+    with _on(stream, dev):
+        if q_out is None:
+            q_out = torch.empty((T, Hq, D), dtype=dt, device=dev)
+        else:
+            _same(q_out, q, "q_out", q.shape)
+        if k is None:
+            k_out = None
+        elif k_out is None:
+            k_out = torch.empty((T, Hk, D), dtype=dt, device=dev)
+        else:
+            _same(k_out, k, "k_out", k.shape)
+    pr = _Rope(T, Hq, Hk, D, rd, _dtype_code(dt), 0 if layout == "half" else 1, eps is not None, eps or 0.0, mscale,
+               _row_stride(q, "q"), _row_stride(k, "k") if Hk else 0, _row_stride(q_out, "q_out"),
+               _row_stride(k_out, "k_out") if Hk else 0)
+    with _device(dev):
+        rc = lib().gdn_qk_norm_rope(
+            ctypes.byref(pr), q.data_ptr(), k.data_ptr() if Hk else None, positions.data_ptr() if rd else None,
+            inv_freq.data_ptr() if rd else None, None if q_weight is None else q_weight.data_ptr(),
+            None if k_weight is None else k_weight.data_ptr(), q_out.data_ptr(), k_out.data_ptr() if Hk else None, raw)
+    if rc != GDN_OK:
+        raise GdnError(rc, "gdn_qk_norm_rope")
+    return q_out, k_out
+
+
+class PagedCache:
+    """A paged key/value cache in 8 bits (see the header): pages [L, N, 2, Hkv, page, D] float8_e4m3fn, scales
+    [L, N, 2, Hkv] fp32, table [R, W] int32, lens [R] int32, refs [N] int32, all on one GPU.  The operators change them
+    in place."""
+
+    def __init__(self, pages, scales, table, lens, refs):
+        _expect(pages.dim() == 6 and pages.shape[2] == 2 and table.dim() == 2,
+                "pages must be [L, N, 2, Hkv, page, D] and table [R, W]")
+        L, N, _, H, page, D = pages.shape
+        R, W = table.shape
+        dev = pages.device
+        _dense(pages, "pages", pages.shape, torch.float8_e4m3fn, dev)
+        _dense(scales, "scales", (L, N, 2, H), torch.float32, dev)
+        _dense(table, "table", (R, W), torch.int32, dev)
+        _dense(lens, "lens", (R,), torch.int32, dev)
+        _dense(refs, "refs", (N,), torch.int32, dev)
+        self.pages, self.scales, self.table, self.lens, self.refs = pages, scales, table, lens, refs
+        self.device, self.page_size = dev, page
+        self._c = _Cache(L, N, page, H, D, R, W, pages.data_ptr(), scales.data_ptr(), table.data_ptr(), lens.data_ptr(),
+                         refs.data_ptr())
+
+    @classmethod
+    def empty(cls, layers: int, num_pages: int, kv_heads: int, head_dim: int, rows: int, row_pages: int, *,
+              page_size: int = 64, device="cuda"):
+        """A cache whose rows hold nothing."""
+        z = dict(device=device)
+        return cls(torch.zeros((layers, num_pages, 2, kv_heads, page_size, head_dim), dtype=torch.uint8,
+                               **z).view(torch.float8_e4m3fn),
+                   torch.zeros((layers, num_pages, 2, kv_heads), **z), torch.zeros((rows, row_pages), dtype=torch.int32, **z),
+                   torch.zeros(rows, dtype=torch.int32, **z), torch.zeros(num_pages, dtype=torch.int32, **z))
+
+
+def _batch(cache, T: int, cu_new, rows, max_new, max_len):
+    B = cu_new.shape[0] - 1
+    _expect(B >= 1, "cu_new must be [B + 1]")
+    _dense(cu_new, "cu_new", (B + 1,), torch.int32, cache.device)
+    if rows is not None:
+        _dense(rows, "rows", (B,), torch.int32, cache.device)
+    return _Batch(B, max(T, 1) if max_new is None else max_new, T, max_len or 0, cu_new.data_ptr(),
+                  None if rows is None else rows.data_ptr())
+
+
+def gdn_cache_append(k, v, cache: PagedCache, cu_new, *, layer: int = 0, rows=None, max_new: Optional[int] = None,
+                     stream=None, ws: Optional[torch.Tensor] = None) -> None:
+    """Append new keys and values to rows of the cache (see the header).
+
+    k, v [T, Hkv, D], rows at any stride; cu_new int32 [B + 1] on the GPU: request b's tokens, the last ones of row
+    rows[b] (default b), whose lens counts them already.  max_new bounds a request's new tokens (default: T)."""
+    dev = cache.device
+    raw = _raw_stream(stream, dev)
+    c = cache._c
+    _expect(k.dim() == 3, "k must be [T, Hkv, D]")
+    T = k.shape[0]
+    if k.device != dev or k.shape != (T, c.num_kv_heads, c.head_dim):
+        raise ValueError(f"k must be [T, {c.num_kv_heads}, {c.head_dim}] on {dev}")
+    _same(v, k, "v", k.shape)
+    b = _batch(cache, T, cu_new, rows, max_new, None)
+    if ws is None:
+        ws = workspace(dev)
+    with _device(dev):
+        rc = lib().gdn_cache_append(ctypes.byref(c), layer, ctypes.byref(b), k.data_ptr(), v.data_ptr(),
+                                    _dtype_code(k.dtype), _row_stride(k, "k"), _row_stride(v, "v"), ws.data_ptr(), ws.numel(),
+                                    raw)
+    if rc != GDN_OK:
+        raise GdnError(rc, "gdn_cache_append")
+
+
+def gdn_paged_attention(q, cache: PagedCache, cu_new, *, layer: int = 0, rows=None, max_new: Optional[int] = None,
+                        max_len: Optional[int] = None, scale: Optional[float] = None, o=None, lse=None, stream=None,
+                        ws: Optional[torch.Tensor] = None):
+    """Causal attention of each request's new tokens over its row of the cache, their own keys and values included (see
+    the header).
+
+    q [T, Hq, D], rows at any stride; cu_new, rows, max_new as gdn_cache_append; max_len bounds the rows' lens (default:
+    what the table holds).  scale defaults to D ** -0.5.  Returns dict(o [T, Hq, D], lse [T, Hq] fp32); rows of o and lse
+    behind the last request are left as they are."""
+    dev = cache.device
+    raw = _raw_stream(stream, dev)
+    c = cache._c
+    _expect(q.dim() == 3, "q must be [T, Hq, D]")
+    T, Hq, D = q.shape
+    if q.device != dev or D != c.head_dim:
+        raise ValueError(f"q must be [T, Hq, {c.head_dim}] on {dev}")
+    code = _dtype_code(q.dtype)
+    b = _batch(cache, T, cu_new, rows, max_new, max_len)
+    L = lib()
+    nbytes = L.gdn_paged_scratch_bytes(ctypes.byref(c), ctypes.byref(b), code, Hq)
+    with _on(stream, dev):
+        if o is not None:
+            _dense(o, "o", (T, Hq, D), q.dtype, dev)
+        else:
+            o = torch.empty((T, Hq, D), dtype=q.dtype, device=dev)
+        if lse is not None:
+            _dense(lse, "lse", (T, Hq), torch.float32, dev)
+        else:
+            lse = torch.empty((T, Hq), dtype=torch.float32, device=dev)
+        scratch = torch.empty(max(nbytes, 32), dtype=torch.uint8, device=dev)
+    if ws is None:
+        ws = workspace(dev)
+    with _device(dev):
+        rc = L.gdn_paged_attention(ctypes.byref(c), layer, ctypes.byref(b), q.data_ptr(), code, Hq, _row_stride(q, "q"),
+                                   D ** -0.5 if scale is None else scale, o.data_ptr(), lse.data_ptr(), scratch.data_ptr(),
+                                   nbytes, ws.data_ptr(), ws.numel(), raw)
+    if rc != GDN_OK:
+        raise GdnError(rc, "gdn_paged_attention")
+    return {"o": o, "lse": lse}
+
+
+def gdn_cache_update(cache: PagedCache, *, drop=None, fork_from=None, fork_to=None, grow=None, granted=None, stream=None,
+                     ws: Optional[torch.Tensor] = None):
+    """One turn of upkeep of the cache's rows (see the header): the rows `drop` and `fork_to` are freed, fork_to[i] becomes
+    a fork of fork_from[i], and row r gets room for grow[r] more tokens (its lens grows; a shared last page is copied).
+
+    drop, fork_from, fork_to int32 on the GPU; grow int32 [R].  Returns granted int32 [R]: grow[r], or -1 where there were
+    too few pages for row r; None without grow."""
+    dev = cache.device
+    raw = _raw_stream(stream, dev)
+    c = cache._c
+    n_drop = n_fork = 0
+    if drop is not None:
+        n_drop = drop.numel()
+        _dense(drop, "drop", (n_drop,), torch.int32, dev)
+    if fork_to is not None or fork_from is not None:
+        _expect(fork_to is not None and fork_from is not None, "a fork needs fork_from and fork_to")
+        n_fork = fork_to.numel()
+        _dense(fork_to, "fork_to", (n_fork,), torch.int32, dev)
+        _dense(fork_from, "fork_from", (n_fork,), torch.int32, dev)
+    L = lib()
+    nbytes = L.gdn_cache_scratch_bytes(ctypes.byref(c))
+    with _on(stream, dev):
+        if grow is not None:
+            _dense(grow, "grow", (c.num_rows,), torch.int32, dev)
+            if granted is not None:
+                _dense(granted, "granted", (c.num_rows,), torch.int32, dev)
+            else:
+                granted = torch.empty(c.num_rows, dtype=torch.int32, device=dev)
+        else:
+            granted = None
+        scratch = torch.empty(max(nbytes, 16), dtype=torch.uint8, device=dev)
+    if ws is None:
+        ws = workspace(dev)
+    with _device(dev):
+        rc = L.gdn_cache_update(ctypes.byref(c), n_drop, drop.data_ptr() if n_drop else None, n_fork,
+                                fork_from.data_ptr() if n_fork else None, fork_to.data_ptr() if n_fork else None,
+                                None if grow is None else grow.data_ptr(), None if granted is None else granted.data_ptr(),
+                                scratch.data_ptr(), nbytes, ws.data_ptr(), ws.numel(), raw)
+    if rc != GDN_OK:
+        raise GdnError(rc, "gdn_cache_update")
+    return granted
+
+
+def gdn_cache_compact(cache: PagedCache, *, live=None, stream=None, ws: Optional[torch.Tensor] = None):
+    """Move the cache's pages in use together (see the header).  Returns live int32 [1]: their number, on the GPU."""
+    dev = cache.device
+    raw = _raw_stream(stream, dev)
+    c = cache._c
+    L = lib()
+    nbytes = L.gdn_cache_scratch_bytes(ctypes.byref(c))
+    with _on(stream, dev):
+        if live is not None:
+            _dense(live, "live", (1,), torch.int32, dev)
+        else:
+            live = torch.empty(1, dtype=torch.int32, device=dev)
+        scratch = torch.empty(max(nbytes, 16), dtype=torch.uint8, device=dev)
+    if ws is None:
+        ws = workspace(dev)
+    with _device(dev):
+        rc = L.gdn_cache_compact(ctypes.byref(c), live.data_ptr(), scratch.data_ptr(), nbytes, ws.data_ptr(), ws.numel(), raw)
+    if rc != GDN_OK:
+        raise GdnError(rc, "gdn_cache_compact")
+    return live

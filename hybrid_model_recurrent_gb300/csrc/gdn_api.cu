@@ -429,7 +429,8 @@ GDN_EXPORT gdn_status gdn_read_status(const void* workspace, size_t ws_bytes, gd
     if (cudaMemcpyAsync(&word, workspace, sizeof(word), cudaMemcpyDeviceToHost, (cudaStream_t)stream) != cudaSuccess)
         return GDN_ERR_CUDA;
     if (cudaStreamSynchronize((cudaStream_t)stream) != cudaSuccess) return GDN_ERR_CUDA;
-    return (word & gdn::STATUS_TIMEOUT) ? GDN_ERR_DEVICE_TIMEOUT : GDN_OK;
+    if (word & gdn::STATUS_TIMEOUT) return GDN_ERR_DEVICE_TIMEOUT;
+    return (word & gdn::STATUS_BAD_INDEX) ? GDN_ERR_INVALID_ARG : GDN_OK;
 }
 
 // ---------------------------------------------------------------------------------------

@@ -71,7 +71,7 @@ constexpr float kRenormFloor = 0x1p-32f;
 constexpr uint64_t kDrainLimitNs = 1000000000ull;
 
 enum : uint32_t { FLAG_RENORM = 1u, FLAG_DUMP = 2u, FLAG_INDEX_SHIFT = 8u };
-enum : unsigned { STATUS_TIMEOUT = 1u };
+enum : unsigned { STATUS_TIMEOUT = 1u, STATUS_BAD_INDEX = 2u };
 
 // One scan over a contiguous token range, the same for all heads.
 struct Job {

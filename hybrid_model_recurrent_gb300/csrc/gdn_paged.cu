@@ -1,0 +1,567 @@
+// gdn_paged.cu - attention over a paged 8-bit cache for few query rows a key/value head (decode, drafts) and for fp32
+// queries, and the join of the parts.
+//
+// Bound by memory, so the keys and values go from global memory straight into the registers that warp-level products take
+// them from: nothing is staged.  A product's contraction index and its columns may be numbered at will as long as both
+// sides agree, which lets a lane's operand be whole 16-byte pieces: of the keys the pieces c and c + 4 of a token's row
+// (lane 4 t + c of token t, 8 tokens a load), of the values the piece t of the tokens 2 c, 2 c + 1 (+ 8).  e4m3 becomes f16
+// exactly, two values an instruction; values of two tokens are interleaved by byte permutes first.
+//
+// Per 16 tokens of a warp:  S = Q K^T (rows x 16),  x = S * scale of the keys' block,  p = 2^(x - m),  O += P V.
+// Queries are brought to [2^14, 2^15) by a power of two for each row and held as one f16 (bf16 queries: exact) or the sum of two
+// (fp32: 22 bits); the weights likewise, times 2^11 and the block's scale over the largest scale met (a power of two).
+// m is raised only when a score is more than 2^4 above it, so the weights stay below 2^15.  Statistics and sums are fp32.
+//
+// The units of all items are dealt out evenly (gdn_cache.cuh), so lengths may differ at will; a CTA's four warps take
+// 16-token steps in turn and add their sums up in shared memory at the end of an item.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include <algorithm>
+#include <cmath>
+
+#include "gdn_cache.cuh"
+#include "gdn_kernel.cuh"
+
+namespace gdn {
+namespace cache {
+namespace {
+
+constexpr int kWarps = 4;
+constexpr float kRise = 4.f;       // log2: how far a score may be above m
+constexpr float kLift = 2048.f;    // weights are held times this: 2^11 2^4 = 2^15 in f16
+
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+// four e4m3 as two pairs of f16
+__device__ __forceinline__ void widen4(uint32_t w, uint32_t& lo, uint32_t& hi) {
+    asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+        : "=r"(lo), "=r"(hi)
+        : "r"(w));
+}
+__device__ __forceinline__ void mma(float (&d)[4], const uint4& a, uint32_t b0, uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t half2(float a, float b) {
+    const __half2 h = __floats2half2_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+// x minus its f16 rounding, in f16
+__device__ __forceinline__ uint32_t half2_rest(float a, float b, uint32_t h) {
+    const float2 r = __half22float2(*reinterpret_cast<const __half2*>(&h));
+    return half2(a - r.x, b - r.y);
+}
+template <int BYTES>
+__device__ __forceinline__ void load_bytes(uint32_t* to, const unsigned char* p) {   // read once: not kept in L1
+    if constexpr (BYTES == 16)
+        asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
+                     : "=r"(to[0]), "=r"(to[1]), "=r"(to[2]), "=r"(to[3]) : "l"(p));
+    else if constexpr (BYTES == 8)
+        asm volatile("ld.global.nc.L1::no_allocate.v2.u32 {%0,%1}, [%2];" : "=r"(to[0]), "=r"(to[1]) : "l"(p));
+    else
+        asm volatile("ld.global.nc.L1::no_allocate.u32 %0, [%1];" : "=r"(to[0]) : "l"(p));
+}
+__device__ __forceinline__ float to_f(float x) { return x; }
+__device__ __forceinline__ float to_f(__nv_bfloat16 x) { return __bfloat162float(x); }
+__device__ __forceinline__ void put(float* p, float x) { *p = x; }
+__device__ __forceinline__ void put(__nv_bfloat16* p, float x) { *p = __float2bfloat16_rn(x); }
+
+__device__ __forceinline__ int units_of(const Request& q) { return q.len > 0 ? (q.len + kUnit - 1) / kUnit : 1; }
+// units of all items of a request
+__device__ __forceinline__ int request_units(const PagedParams& p, const Request& q, int tile_rows) {
+    return q.n == 0 ? 0 : (q.n * p.G + tile_rows - 1) / tile_rows * units_of(q) * p.c.Hkv;
+}
+
+template <int D, typename T, int MT>
+struct Cfg {
+    static constexpr int PARTS = sizeof(T) == 2 ? 1 : 2;
+    static constexpr int RT = 16 * MT;        // rows of a tile
+    static constexpr int U = 128 / D;         // 16-token pieces of a step: the same bytes in flight at every width
+    static constexpr int KW = D / 16;         // words of a key that a lane holds
+    static constexpr int VW = D / 32;         // and of a value
+    static constexpr int NT = D / 8;          // column tiles of the output
+    static constexpr int kQ = 0;              // queries: [PARTS][MT][KW][32] uint4
+    static constexpr int kO = kQ + PARTS * MT * KW * 512;            // sums: [warps][MT][NT][4][32] fp32
+    static constexpr int kMl = kO + kWarps * MT * NT * 512;          // m, l: [warps][RT] float2
+    static constexpr int kQe = kMl + kWarps * RT * 8;                // factors of the rows [RT]
+    static constexpr int kCum = kQe + RT * 4 + 64;                   // units before each request [B + 1]
+    static constexpr int bytes(int B) { return kCum + (B + 1) * 4; }
+};
+
+template <int D, typename T, int MT>
+__global__ void __launch_bounds__(kWarps * 32, MT == 1 ? 3 : 2) paged_kernel(const __grid_constant__ PagedParams p) {
+    using F = Cfg<D, T, MT>;
+    constexpr int PARTS = F::PARTS, U = F::U, KW = F::KW, VW = F::VW, NT = F::NT, RT = F::RT;
+    extern __shared__ __align__(16) unsigned char smem[];
+    uint4* s_q = reinterpret_cast<uint4*>(smem + F::kQ);
+    float* s_o = reinterpret_cast<float*>(smem + F::kO);
+    float2* s_ml = reinterpret_cast<float2*>(smem + F::kMl);
+    float* s_f = reinterpret_cast<float*>(smem + F::kQe);
+    int* s_scan = reinterpret_cast<int*>(smem + F::kQe + RT * 4);
+    int* s_cum = reinterpret_cast<int*>(smem + F::kCum);
+    const Cache& c = p.c;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, q4 = lane & 3;
+    const int B = p.t.B;
+
+    // ---- units before each request ----
+    {
+        const int per = (B + kWarps * 32 - 1) / (kWarps * 32);
+        int sum = 0;
+        for (int i = 0; i < per; ++i) {
+            const int b = tid * per + i;
+            if (b < B) {
+                const Request q = request_at(c, p.t, b);
+                if (q.bad && blockIdx.x == 0) atomicOr(p.status, STATUS_BAD_INDEX);
+                const int u = request_units(p, q, RT);
+                s_cum[b] = sum;
+                sum += u;
+            }
+        }
+        int y = sum;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int z = __shfl_up_sync(0xffffffffu, y, o);
+            if (lane >= o) y += z;
+        }
+        if (lane == 31) s_scan[warp] = y;
+        __syncthreads();
+        int before = y - sum;
+        for (int w = 0; w < warp; ++w) before += s_scan[w];
+        for (int i = 0; i < per; ++i)
+            if (tid * per + i < B) s_cum[tid * per + i] += before;
+        if (tid == kWarps * 32 - 1) s_cum[B] = before + sum;
+        __syncthreads();
+        if (blockIdx.x == 0 && p.starts)
+            for (int i = tid; i <= B; i += kWarps * 32) p.starts[i] = s_cum[i];
+    }
+    const int total = s_cum[B], share = (total + gridDim.x - 1) / gridDim.x;
+    int x = (int)min((int64_t)blockIdx.x * share, (int64_t)total);
+    const int end = min(x + share, total);
+
+    while (x < end) {
+        // ---- the item ----
+        int b = 0, top = B;   // cum[b] <= x < cum[top]
+        while (top - b > 1) {
+            const int mid = (b + top) >> 1;
+            if (s_cum[mid] <= x) b = mid;
+            else top = mid;
+        }
+        const Request rq = request_at(c, p.t, b);
+        const int units = units_of(rq), tiles = (rq.n * p.G + RT - 1) / RT;
+        int rest = x - s_cum[b];
+        const int item = rest / units, u0 = rest - item * units;
+        const int u1 = min(units, u0 + end - x);
+        const int h = item / tiles, tile = item - h * tiles;
+        const int row0 = tile * RT, rows = min(rq.n * p.G - row0, RT);
+        x += u1 - u0;
+        const int shift = rq.len - rq.n;   // query i sees the tokens below shift + i + 1
+        const int lo = u0 * kUnit;
+        const int hi = min(u1 * kUnit, max(0, shift + (row0 + rows - 1) / p.G + 1));
+        const int all_see = shift + row0 / p.G + 1;   // tokens that every row sees end here
+        const int32_t* table = c.table + (int64_t)max(rq.row, 0) * c.W;
+
+        // ---- loads of a step: pages one step ahead of the data ----
+        struct Data {
+            uint32_t k[U][2][KW], v[U][4][VW];
+            float ks[U], vs[U];
+        };
+        const unsigned char* pages = c.pages + (int64_t)h * c.page * D;
+        const int64_t kv_bytes = (int64_t)c.Hkv * c.page * D;
+        auto ids = [&](int t0, int (&id)[U]) {
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int t = t0 + 16 * u;
+                id[u] = t < hi ? __ldg(table + (t >> c.page_log2)) : 0;
+            }
+        };
+        auto fetch = [&](int t0, int (&id)[U], Data& d) {
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int t = t0 + 16 * u;
+                if (t < hi) {
+                    if ((unsigned)id[u] >= (unsigned)c.N) {
+                        if (lane == 0) atomicOr(p.status, STATUS_BAD_INDEX);
+                        id[u] = 0;
+                    }
+                    const unsigned char* a = pages + (int64_t)id[u] * 2 * kv_bytes + (int64_t)(t & (c.page - 1)) * D;
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        const unsigned char* row = a + (8 * j + g) * D;
+                        if constexpr (D == 128) {
+                            load_bytes<16>(&d.k[u][j][0], row + 16 * q4);
+                            load_bytes<16>(&d.k[u][j][4], row + 64 + 16 * q4);
+                        } else {
+                            load_bytes<D / 4>(&d.k[u][j][0], row + D / 4 * q4);
+                        }
+                    }
+                    a += kv_bytes;
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        load_bytes<D / 8>(&d.v[u][j][0], a + (8 * (j >> 1) + 2 * q4 + (j & 1)) * D + D / 8 * g);
+                    const float* sc = c.scales + (int64_t)id[u] * 2 * c.Hkv + h;
+                    d.ks[u] = __ldg(sc), d.vs[u] = __ldg(sc + c.Hkv);
+                } else {
+                    d.ks[u] = d.vs[u] = 0.f;
+                }
+            }
+        };
+        constexpr int STEP = 16 * U;
+        int id[U];
+        Data d;
+        int t0 = lo + warp * STEP;
+        ids(t0, id);
+
+        // ---- queries: a power of two for each row, then the products' operands ----
+        const T* q = static_cast<const T*>(p.q);
+        for (int r = warp; r < RT; r += kWarps) {
+            float most = 0.f;
+            if (r < rows) {
+                const int R = row0 + r;
+                const T* a = q + (int64_t)(rq.first + R / p.G) * p.q_stride + (int64_t)(h * p.G + R % p.G) * D;
+#pragma unroll
+                for (int i = 0; i < D / 32; ++i) most = fmaxf(most, fabsf(to_f(a[lane + 32 * i])));
+            }
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
+            const int e = max((int)(__float_as_uint(most) >> 23) - 127, -100);
+            if (lane == 0) s_f[r] = __uint_as_float((uint32_t)(14 - min(e, 127) + 127) << 23);
+        }
+        fetch(t0, id, d);
+        ids(t0 + kWarps * STEP, id);
+        __syncthreads();
+        for (int i = tid; i < MT * KW * 32; i += kWarps * 32) {
+            const int l = i & 31, w = (i >> 5) % KW, mt = i / (32 * KW);
+            const int col = (D == 128 ? 64 * (w >> 2) + 16 * (l & 3) + 4 * (w & 3) : D / 4 * (l & 3) + 4 * w);
+            float y[2][4];
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+                const int r = mt * 16 + half * 8 + (l >> 2), R = row0 + r;
+                const float f = s_f[r];
+                const T* a = q + (int64_t)(rq.first + R / p.G) * p.q_stride + (int64_t)(h * p.G + R % p.G) * D + col;
+#pragma unroll
+                for (int k = 0; k < 4; ++k) y[half][k] = r < rows ? to_f(a[k]) * f : 0.f;
+            }
+            uint4 hi4 = make_uint4(half2(y[0][0], y[0][1]), half2(y[1][0], y[1][1]), half2(y[0][2], y[0][3]), half2(y[1][2], y[1][3]));
+            s_q[i] = hi4;
+            if constexpr (PARTS == 2)
+                s_q[MT * KW * 32 + i] = make_uint4(half2_rest(y[0][0], y[0][1], hi4.x), half2_rest(y[1][0], y[1][1], hi4.y),
+                                                   half2_rest(y[0][2], y[0][3], hi4.z), half2_rest(y[1][2], y[1][3], hi4.w));
+        }
+        float fr[MT][2];
+        int sees[MT][2];
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+                const int r = mt * 16 + half * 8 + g;
+                fr[mt][half] = p.scale_log2 / s_f[r];
+                sees[mt][half] = r < rows ? min(rq.len, shift + (row0 + r) / p.G + 1) : 0;
+            }
+        __syncthreads();
+
+        // ---- the tokens ----
+        float m[MT][2], l[MT][2], o[MT][NT][4], vref = 0.f;
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) {
+            m[mt][0] = m[mt][1] = -INFINITY, l[mt][0] = l[mt][1] = 0.f;
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) o[mt][n][i] = 0.f;
+        }
+        for (; t0 < hi; t0 += kWarps * STEP) {
+            Data e = d;
+            fetch(t0 + kWarps * STEP, id, d);
+            ids(t0 + 2 * kWarps * STEP, id);
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int t = t0 + 16 * u;
+                if (t >= hi) break;
+                float s[MT][2][4];
+#pragma unroll
+                for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                    for (int j = 0; j < 2; ++j)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) s[mt][j][i] = 0.f;
+#pragma unroll
+                for (int w = 0; w < KW; ++w) {
+                    uint32_t b0, b1, b2, b3;
+                    widen4(e.k[u][0][w], b0, b1);
+                    widen4(e.k[u][1][w], b2, b3);
+#pragma unroll
+                    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                        for (int part = 0; part < PARTS; ++part) {
+                            const uint4 a = s_q[(part * MT + mt) * KW * 32 + w * 32 + lane];
+                            mma(s[mt][0], a, b0, b1);
+                            mma(s[mt][1], a, b2, b3);
+                        }
+                }
+                bool rise = false;
+#pragma unroll
+                for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                    for (int half = 0; half < 2; ++half) {
+                        const float f = fr[mt][half] * e.ks[u];
+#pragma unroll
+                        for (int j = 0; j < 2; ++j)
+#pragma unroll
+                            for (int i = 0; i < 2; ++i) s[mt][j][2 * half + i] *= f;
+                    }
+                if (t + 16 > all_see) {
+#pragma unroll
+                    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                        for (int j = 0; j < 2; ++j)
+#pragma unroll
+                            for (int i = 0; i < 4; ++i)
+                                if (t + 8 * j + 2 * q4 + (i & 1) >= sees[mt][i >> 1]) s[mt][j][i] = -INFINITY;
+                }
+#pragma unroll
+                for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                    for (int half = 0; half < 2; ++half) {
+                        const float t4 = fmaxf(fmaxf(s[mt][0][2 * half], s[mt][0][2 * half + 1]),
+                                               fmaxf(s[mt][1][2 * half], s[mt][1][2 * half + 1]));
+                        rise |= t4 > m[mt][half] + kRise;   // (m = -infinity: any score)
+                    }
+                if (__any_sync(0xffffffffu, rise)) {
+#pragma unroll
+                    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                        for (int half = 0; half < 2; ++half) {
+                            float t4 = fmaxf(fmaxf(s[mt][0][2 * half], s[mt][0][2 * half + 1]),
+                                             fmaxf(s[mt][1][2 * half], s[mt][1][2 * half + 1]));
+                            t4 = fmaxf(t4, __shfl_xor_sync(0xffffffffu, t4, 1));
+                            t4 = fmaxf(t4, __shfl_xor_sync(0xffffffffu, t4, 2));
+                            const float mn = fmaxf(m[mt][half], t4);
+                            const float f = mn == -INFINITY ? 1.f : ex2(m[mt][half] - mn);
+                            m[mt][half] = mn;
+                            l[mt][half] *= f;
+#pragma unroll
+                            for (int n = 0; n < NT; ++n) o[mt][n][2 * half] *= f, o[mt][n][2 * half + 1] *= f;
+                        }
+                }
+                if (e.vs[u] > vref) {   // (the same for the whole warp)
+                    const float f = vref / e.vs[u];
+                    vref = e.vs[u];
+#pragma unroll
+                    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                        for (int n = 0; n < NT; ++n)
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) o[mt][n][i] *= f;
+                }
+                const float lift = vref > 0.f ? e.vs[u] / vref * kLift : 0.f;
+                uint4 a[PARTS][MT];
+#pragma unroll
+                for (int mt = 0; mt < MT; ++mt) {
+                    uint32_t w[4], w2[4];
+#pragma unroll
+                    for (int half = 0; half < 2; ++half) {
+                        const float base = m[mt][half] == -INFINITY ? 0.f : m[mt][half];
+#pragma unroll
+                        for (int j = 0; j < 2; ++j) {
+                            const float p0 = ex2(s[mt][j][2 * half] - base), p1 = ex2(s[mt][j][2 * half + 1] - base);
+                            l[mt][half] += p0 + p1;
+                            w[2 * j + half] = half2(p0 * lift, p1 * lift);
+                            if constexpr (PARTS == 2) w2[2 * j + half] = half2_rest(p0 * lift, p1 * lift, w[2 * j + half]);
+                        }
+                    }
+                    a[0][mt] = make_uint4(w[0], w[1], w[2], w[3]);
+                    if constexpr (PARTS == 2) a[1][mt] = make_uint4(w2[0], w2[1], w2[2], w2[3]);
+                }
+                if (t + 16 > hi) {   // what lies behind the row's tokens
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        if (t + 8 * (j >> 1) + 2 * q4 + (j & 1) >= hi)
+#pragma unroll
+                            for (int w = 0; w < VW; ++w) e.v[u][j][w] = 0;
+                }
+#pragma unroll
+                for (int w = 0; w < VW; ++w) {
+                    const uint32_t l01 = __byte_perm(e.v[u][0][w], e.v[u][1][w], 0x5140), h01 = __byte_perm(e.v[u][0][w], e.v[u][1][w], 0x7362);
+                    const uint32_t l23 = __byte_perm(e.v[u][2][w], e.v[u][3][w], 0x5140), h23 = __byte_perm(e.v[u][2][w], e.v[u][3][w], 0x7362);
+                    uint32_t b0[4], b1[4];
+                    widen4(l01, b0[0], b0[1]), widen4(h01, b0[2], b0[3]);
+                    widen4(l23, b1[0], b1[1]), widen4(h23, b1[2], b1[3]);
+#pragma unroll
+                    for (int n = 0; n < 4; ++n)
+#pragma unroll
+                        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                            for (int part = 0; part < PARTS; ++part) mma(o[mt][4 * w + n], a[part][mt], b0[n], b1[n]);
+                }
+            }
+        }
+
+        // ---- the warps' sums ----
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+                float y = l[mt][half];
+                y += __shfl_xor_sync(0xffffffffu, y, 1);
+                y += __shfl_xor_sync(0xffffffffu, y, 2);
+                if (q4 == 0) s_ml[warp * RT + mt * 16 + half * 8 + g] = make_float2(m[mt][half], y);
+            }
+        __syncthreads();
+        float M[MT][2], Ls[MT][2];
+        vref *= 1.f / kLift;
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+                const int r = mt * 16 + half * 8 + g;
+                float2 y[kWarps];
+                float mm = -INFINITY, ll = 0.f;
+#pragma unroll
+                for (int w = 0; w < kWarps; ++w) y[w] = s_ml[w * RT + r], mm = fmaxf(mm, y[w].x);
+#pragma unroll
+                for (int w = 0; w < kWarps; ++w) ll += mm == -INFINITY ? 0.f : y[w].y * ex2(y[w].x - mm);
+                M[mt][half] = mm, Ls[mt][half] = ll;
+                const float f = mm == -INFINITY ? 0.f : ex2(m[mt][half] - mm) * vref;
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i)
+                        s_o[(((warp * MT + mt) * NT + n) * 4 + 2 * half + i) * 32 + lane] = o[mt][n][2 * half + i] * f;
+            }
+        __syncthreads();
+        // each warp has a quarter of the column tiles: NT / 4 neighbouring columns of the output
+        const bool whole = u0 == 0 && u1 == units;
+        const int64_t slot = 2 * (int64_t)blockIdx.x + (u0 == 0);
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+                const int r = mt * 16 + half * 8 + g;
+                if (r >= rows) continue;
+                const int R = row0 + r;
+                const int64_t at = (int64_t)(rq.first + R / p.G) * p.Hq + h * p.G + R % p.G;
+                const float inv = Ls[mt][half] > 0.f ? 1.f / Ls[mt][half] : Ls[mt][half] == 0.f ? 0.f : NAN;
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    float y[NT / 4];
+#pragma unroll
+                    for (int n = 0; n < NT / 4; ++n) {
+                        y[n] = 0.f;
+#pragma unroll
+                        for (int w = 0; w < kWarps; ++w)
+                            y[n] += s_o[(((w * MT + mt) * NT + warp * (NT / 4) + n) * 4 + 2 * half + i) * 32 + lane];
+                    }
+                    const int col = D / 8 * (2 * q4 + i) + warp * (NT / 4);
+                    if (whole) {
+                        T* to = static_cast<T*>(p.o) + at * D + col;
+                        if constexpr (sizeof(T) == 2 && NT / 4 >= 2) {
+#pragma unroll
+                            for (int n = 0; n < NT / 4; n += 2)
+                                *reinterpret_cast<__nv_bfloat162*>(to + n) = __floats2bfloat162_rn(y[n] * inv, y[n + 1] * inv);
+                        } else {
+#pragma unroll
+                            for (int n = 0; n < NT / 4; ++n) put(to + n, y[n] * inv);
+                        }
+                    } else {
+                        float* to = p.part_o + (slot * RT + r) * D + col;
+#pragma unroll
+                        for (int n = 0; n < NT / 4; ++n) to[n] = y[n];
+                    }
+                }
+                if (warp == 0 && q4 == 0) {
+                    if (!whole) p.part_ml[slot * RT + r] = make_float2(M[mt][half], Ls[mt][half]);
+                    else if (p.lse)
+                        p.lse[at] = Ls[mt][half] == 0.f ? -INFINITY : (M[mt][half] + log2f(Ls[mt][half])) * 0.6931471805599453f;
+                }
+            }
+        __syncthreads();
+    }
+}
+
+// A warp adds up the parts of one query row.
+template <int D, typename T>
+__global__ void __launch_bounds__(128) paged_join_kernel(const __grid_constant__ PagedParams p, const int RT) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int b = blockIdx.y, h = blockIdx.z;
+    const Request rq = request_at(p.c, p.t, b);
+    const int rows = rq.n * p.G;
+    const int R = blockIdx.x * 4 + warp;
+    if (R >= rows) return;
+    const int total = p.starts[p.t.B], share = (total + p.ctas - 1) / p.ctas;
+    const int tiles = (rows + RT - 1) / RT, units = units_of(rq), tile = R / RT, r = R - tile * RT;
+    const int first = p.starts[b] + (h * tiles + tile) * units;
+    const int c0 = first / share, c1 = (first + units - 1) / share;
+    if (c0 == c1) return;
+    auto slot = [&](int c) { return (int64_t)2 * c + (c == c0); };
+    float m = -INFINITY;
+    for (int c = c0 + lane; c <= c1; c += 32) m = fmaxf(m, p.part_ml[slot(c) * RT + r].x);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    constexpr int N = D / 32;
+    float acc[N] = {}, l = 0.f;
+    for (int cb = c0; cb <= c1; cb += 32) {
+        float f = 0.f, fl = 0.f;
+        if (cb + lane <= c1) {
+            const float2 ml = p.part_ml[slot(cb + lane) * RT + r];
+            f = m == -INFINITY ? 0.f : ex2(ml.x - m);
+            fl = m == -INFINITY ? 0.f : ml.y * f;
+        }
+        const int n = min(32, c1 - cb + 1);
+#pragma unroll 4
+        for (int i = 0; i < n; ++i) {
+            const float w = __shfl_sync(0xffffffffu, f, i);
+            l += __shfl_sync(0xffffffffu, fl, i);
+            const float* a = p.part_o + (slot(cb + i) * RT + r) * D + lane * N;
+            float y[N];
+#pragma unroll
+            for (int k = 0; k < N; ++k) y[k] = a[k];
+#pragma unroll
+            for (int k = 0; k < N; ++k) acc[k] += w * y[k];
+        }
+    }
+    const int64_t at = (int64_t)(rq.first + R / p.G) * p.Hq + h * p.G + R % p.G;
+    const float inv = l > 0.f ? 1.f / l : l == 0.f ? 0.f : NAN;
+    T* to = static_cast<T*>(p.o) + at * D + lane * N;
+#pragma unroll
+    for (int k = 0; k < N; ++k) put(to + k, acc[k] * inv);
+    if (lane == 0 && p.lse) p.lse[at] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
+}
+
+template <int D, typename T, int MT>
+cudaError_t launch(const PagedParams& p, bool join, cudaStream_t s) {
+    using F = Cfg<D, T, MT>;
+    static std::atomic<int> optin[kMaxOptinDevices];
+    const cudaError_t e = smem_optin(reinterpret_cast<const void*>(paged_kernel<D, T, MT>), F::bytes(kMaxBatch), optin);
+    if (e != cudaSuccess) return e;
+    paged_kernel<D, T, MT><<<p.ctas, kWarps * 32, F::bytes(p.t.B), s>>>(p);
+    cudaError_t r = cudaGetLastError();
+    if (r != cudaSuccess || !join) return r;
+    const int blocks = (int)(((int64_t)p.t.max_new * p.G + 3) / 4);
+    paged_join_kernel<D, T><<<dim3(blocks, p.t.B, p.c.Hkv), 128, 0, s>>>(p, F::RT);
+    return cudaGetLastError();
+}
+template <int D, typename T>
+cudaError_t launch_t(const PagedParams& p, int tiles, bool join, cudaStream_t s) {
+    return tiles == 1 ? launch<D, T, 1>(p, join, s) : launch<D, T, 2>(p, join, s);
+}
+
+}  // namespace
+
+cudaError_t launch_paged(const PagedParams& p, int D, bool bf16, int tiles, bool join, cudaStream_t s) {
+    switch (D * 2 + bf16) {
+        case 64: return launch_t<32, float>(p, tiles, join, s);
+        case 65: return launch_t<32, __nv_bfloat16>(p, tiles, join, s);
+        case 128: return launch_t<64, float>(p, tiles, join, s);
+        case 129: return launch_t<64, __nv_bfloat16>(p, tiles, join, s);
+        case 256: return launch_t<128, float>(p, tiles, join, s);
+        default: return launch_t<128, __nv_bfloat16>(p, tiles, join, s);
+    }
+}
+
+}  // namespace cache
+}  // namespace gdn

@@ -465,7 +465,9 @@ size_t gdn_workspace_size_two_pass(int64_t tokens, int32_t num_heads, int32_t nu
 gdn_status gdn_clear_status(void* workspace, size_t ws_bytes, gdn_stream_t stream);
 
 /* Synchronise `stream` and report the workspace's sticky device status:
- * GDN_OK, or GDN_ERR_DEVICE_TIMEOUT if any kernel that used it gave up on a wait. */
+ * GDN_OK, GDN_ERR_DEVICE_TIMEOUT if any kernel that used it gave up on a wait, or
+ * GDN_ERR_INVALID_ARG if one met a page number or a count on the device that its call
+ * does not allow (gdn_cache.h). */
 gdn_status gdn_read_status(const void* workspace, size_t ws_bytes, gdn_stream_t stream);
 
 /* Time limit, in nanoseconds, of every device-side wait of later launches
