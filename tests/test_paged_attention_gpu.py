@@ -1,0 +1,224 @@
+"""Attention over a paged 8-bit cache on the GPU, against the definition in 64 bits (tolerances: tests/cache_util.py)."""
+import math
+
+import pytest
+import torch
+
+import hybrid_model_recurrent_gb300 as gdn
+from cache_util import E4M3, NAN_BYTE, check_attention, make_cache
+
+pytestmark = pytest.mark.gpu
+BF, F32 = torch.bfloat16, torch.float32
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    gdn.build()
+
+
+def ints(*x):
+    return torch.tensor(x, dtype=torch.int32, device="cuda")
+
+
+def cu_of(new):
+    out = [0]
+    for n in new:
+        out.append(out[-1] + n)
+    return ints(*out)
+
+
+def queries(T, Hq, D, dtype, seed=1, gain=1.0):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    return (torch.randn(T, Hq, D, generator=g, device="cuda") * gain).to(dtype)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("D", [32, 64, 128])
+@pytest.mark.parametrize("page", [16, 32, 64, 128])
+def test_decode(dtype, D, page):
+    """One token a request: lengths from one token on, page ends, a length that leaves one token in its last page."""
+    lens = [1, 2, 15, 16, 17, 63, 64, 65, 129, 400, 1000, 2049]
+    c = make_cache(lens, page=page, H=2, D=D, seed=D + page)
+    q = queries(len(lens), 8, D, dtype)
+    check_attention(c, q, cu_of([1] * len(lens)), max_new=1)
+    check_attention(c, q, cu_of([1] * len(lens)), max_new=1, max_len=2049)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("H, G", [(1, 1), (3, 3), (2, 5), (1, 16), (1, 17), (2, 40), (1, 128)])
+def test_head_groups(dtype, H, G):
+    c = make_cache([5, 333, 70], page=32, H=H, D=64, seed=G)
+    check_attention(c, queries(3, H * G, 64, dtype), cu_of([1, 1, 1]), max_new=1)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("D", [32, 64, 128])
+@pytest.mark.parametrize("G", [1, 4, 7])
+def test_several_queries(dtype, D, G):
+    """Drafts and turns: ragged numbers of queries, none, more than the row has tokens (which see nothing), whole prompts."""
+    lens, new = [100, 40, 7, 300, 64, 33, 0, 1], [4, 0, 9, 33, 64, 33, 2, 1]
+    c = make_cache(lens, page=16, H=2, D=D, seed=G)
+    check_attention(c, queries(sum(new), 2 * G, D, dtype), cu_of(new), max_new=64)
+    check_attention(c, queries(sum(new), 2 * G, D, dtype), cu_of(new))
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_rows_of_the_table(dtype):
+    """A batch is some of the rows, in any order; padding rows give zeros; a row may be attended twice."""
+    c = make_cache([10, 200, 31, 90], page=16, H=2, D=64)
+    rows = ints(3, -1, 1, 4, 0, 1, 2 ** 31 - 1, -2 ** 31)
+    new = [1, 1, 3, 2, 1, 1, 1, 1]
+    check_attention(c, queries(sum(new), 4, 64, dtype), cu_of(new), rows=rows, max_new=3)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_strided_queries_and_own_outputs(dtype):
+    """q as a slice of one projection's output; rows of o and lse behind the last request are left as they were."""
+    c = make_cache([50, 77], page=16, H=2, D=64)
+    qkv = queries(9, 12, 64, dtype)
+    q = qkv[:, 2:10]
+    o, lse = torch.full((9, 8, 64), 7.0, dtype=dtype, device="cuda"), torch.full((9, 8), 7.0, device="cuda")
+    check_attention(c, q, ints(0, 2, 5), max_new=3, o=o, lse=lse)
+    assert (o[5:] == 7).all() and (lse[5:] == 7).all()
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("gain", [1e-30, 1e-3, 30.0, 1e4, -1.0])
+def test_sizes_of_queries_and_scales(dtype, gain):
+    """Queries far from one and a negative scale: the rows' powers of two."""
+    c = make_cache([300, 41], page=16, H=2, D=64)
+    q = queries(2, 4, 64, dtype, gain=abs(gain))
+    check_attention(c, q, ints(0, 1, 2), scale=0.1 / abs(gain) * math.copysign(1, gain))
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_blocks_of_very_different_sizes(dtype):
+    """Blocks whose values differ by 2^24: a query that attends to the small ones alone keeps their precision."""
+    c = make_cache([256], page=16, H=1, D=64, poison=False, spread=1)
+    big = c.table[0, ::2].long()
+    c.scales[0, big, 1] *= 2.0 ** 12
+    c.scales[0, c.table[0, 1::2].long(), 1] *= 2.0 ** -12
+    c.scales[0, big, 0] = 2.0 ** -9
+    q = queries(3, 2, 64, dtype, gain=2.0)
+    check_attention(c, q, ints(0, 3))
+    # keys of the large blocks pushed far down: the row's own scale of values decides, not the largest block's
+    kb = c.pages.view(torch.uint8)
+    kb[0, big, 0] = 0x80 | 0x78   # -256
+    c.scales[0, big, 0] = 2.0 ** -2
+    q = queries(1, 2, 64, dtype).abs() + 0.5
+    check_attention(c, q.to(dtype), ints(0, 1))
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_scores_that_rise_late(dtype):
+    """The maximum rises by little, by much and at the last token: weights are rescaled."""
+    for step in (0.5, 3.0, 100.0):
+        c = make_cache([700], page=16, H=1, D=32, poison=False, spread=1)
+        kb = c.pages.view(torch.uint8)
+        w = torch.arange(44, device="cuda")
+        kb[0, c.table[0, :44].long(), 0] = 0x38                       # every key element 1 ..
+        c.scales[0, c.table[0, :44].long(), 0, 0] = (w + 1).float() * step / 44   # .. times a rising scale
+        q = torch.full((1, 2, 32), 0.25, device="cuda", dtype=dtype)
+        check_attention(c, q, ints(0, 1), scale=1.0)
+
+
+def test_zero_values_and_zero_queries():
+    c = make_cache([40], page=16, H=1, D=64, poison=False)
+    c.pages.view(torch.uint8)[:, :, 1] = 0
+    c.scales[:, :, 1] = 2.0 ** -126
+    r = check_attention(c, queries(2, 4, 64, BF), ints(0, 2))
+    assert not r["o"].any()
+    check_attention(make_cache([40], page=16, H=1, D=64), torch.zeros(2, 4, 64, dtype=BF, device="cuda"), ints(0, 2))
+
+
+def test_a_nan_stays_within_its_request():
+    c = make_cache([40, 50], page=16, H=2, D=64)
+    c.pages.view(torch.uint8)[0, c.table[0, 1], 0, 1, 3] = NAN_BYTE
+    q = queries(2, 4, 64, BF)
+    r = gdn.gdn_paged_attention(q, c, ints(0, 1, 2))
+    assert torch.isnan(r["o"][0, 2:]).all() and torch.isfinite(r["o"][0, :2]).all() and torch.isfinite(r["o"][1]).all()
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_many_requests_few_units(dtype):
+    """More requests than threads look through at once, many of them without tokens or queries."""
+    lens = [(7 * i) % 90 if i % 3 else 0 for i in range(700)]
+    new = [i % 3 for i in range(700)]
+    c = make_cache(lens, page=16, H=1, D=32)
+    check_attention(c, queries(sum(new), 2, 32, dtype), cu_of(new), max_new=2)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_one_long_row(dtype):
+    """A single long row is cut over the whole GPU: parts of many CTAs are joined."""
+    c = make_cache([50003], page=64, H=2, D=128)
+    check_attention(c, queries(3, 8, 128, dtype), ints(0, 3), max_new=3)
+    check_attention(c, queries(1, 2, 128, dtype), ints(0, 1), max_new=1)
+
+
+def test_layers_and_pages_past_32_bits():
+    """Pages behind the first 2^32 bytes of the pool, and a layer behind the first."""
+    H, page, D, N = 8, 128, 128, 9000
+    c = gdn.PagedCache.empty(2, N, H, D, 1, 4, page_size=page)   # 2.4 GB a layer
+    g = torch.Generator(device="cuda").manual_seed(3)
+    c.table[0, :2] = ints(N - 1, N - 2)
+    c.lens[0] = 200
+    c.pages.view(torch.uint8)[1, N - 2:] = (torch.randn(2, 2, H, page, D, generator=g, device="cuda") * 60).clamp(-448, 448).to(
+        E4M3).view(torch.uint8)
+    c.scales[1, N - 2:] = 2.0 ** -6
+    check_attention(c, queries(1, 16, D, BF), ints(0, 1), layer=1)
+    assert not gdn.gdn_paged_attention(queries(1, 16, D, BF), c, ints(0, 1), layer=0)["o"].any()
+
+
+def test_bad_pages_and_counts_are_reported():
+    """A page number outside the pool, and a request with more new tokens than the bound, are reported and followed nowhere."""
+    for bad in (-1, 10 ** 6, 2 ** 31 - 1):
+        c = make_cache([40, 50], page=16, H=2, D=64)
+        want = gdn.gdn_paged_attention(queries(2, 4, 64, BF), c, ints(0, 1, 2))["o"]
+        c.table[0, 1] = bad
+        ws = torch.zeros(256, dtype=torch.uint8, device="cuda")
+        r = gdn.gdn_paged_attention(queries(2, 4, 64, BF), c, ints(0, 1, 2), ws=ws)
+        assert gdn.read_status(ws=ws) == gdn.GDN_ERR_INVALID_ARG
+        assert torch.equal(r["o"][1], want[1])
+    ws = torch.zeros(256, dtype=torch.uint8, device="cuda")
+    gdn.gdn_paged_attention(queries(9, 4, 64, BF), make_cache([40, 50], page=16, H=2, D=64), ints(0, 7, 9), max_new=3, ws=ws)
+    assert gdn.read_status(ws=ws) == gdn.GDN_ERR_INVALID_ARG
+    gdn.clear_status(ws=ws)
+    assert gdn.read_status(ws=ws) == gdn.GDN_OK
+
+
+@pytest.mark.parametrize("dtype, G, new", [(BF, 4, 1), (BF, 16, 20), (F32, 4, 2)])
+def test_captured_and_on_another_stream(dtype, G, new):
+    """A captured call follows lengths, tables and counts that change between replays; two calls on two streams at once."""
+    lens = [120, 500, 64]
+    c = make_cache(lens, page=16, H=2, D=64, poison=False)
+    q, cu = queries(3 * new, 2 * G, 64, dtype), cu_of([new] * 3)
+    want = gdn.gdn_paged_attention(q, c, cu, max_new=new)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    a, b = (gdn.gdn_paged_attention(q, c, cu, max_new=new, stream=x) for x in (s, None))
+    torch.cuda.synchronize()
+    assert torch.equal(a["o"], want["o"]) and torch.equal(b["o"], want["o"]) and torch.equal(a["lse"], want["lse"])
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        r = gdn.gdn_paged_attention(q, c, cu, max_new=new)
+    for again in ([30, 499, 64], [500, 120, 1]):
+        c.lens.copy_(ints(*again))
+        rows = c.table.clone()
+        if again[0] == 500:
+            c.table.copy_(rows[[1, 0, 2]])
+        graph.replay()
+        torch.cuda.synchronize()
+        eager = check_attention(c, q, cu, max_new=new)
+        assert torch.equal(r["o"], eager["o"]) and torch.equal(r["lse"], eager["lse"])
+        c.table.copy_(rows)
+
+
+def test_results_do_not_change():
+    """The same call gives the same bits, every time."""
+    c = make_cache([5000, 333, 1200], page=64, H=2, D=128)
+    q = queries(30, 8, 128, BF)
+    first = gdn.gdn_paged_attention(q, c, ints(0, 10, 20, 30))
+    for _ in range(5):
+        r = gdn.gdn_paged_attention(q, c, ints(0, 10, 20, 30))
+        assert torch.equal(r["o"], first["o"]) and torch.equal(r["lse"], first["lse"])
