@@ -13,7 +13,7 @@ LIB = os.path.join(PKG, "libgdn_scan.so")
 SOURCES = ["gdn_api.cu", "gdn_noalloc.cu", "gdn_placement.cpp", "gdn_group.cu", "gdn_tprep.cu", "inst_chunk_tc.cu",
            "inst_chunk_tc_pre.cu", "inst_dk32.cu", "inst_dk64.cu", "inst_dk128.cu", "gdn_hybrid_api.cu",
            "gdn_linear.cu", "gdn_linear_tc.cu", "gdn_prefix.cu",
-           "gdn_prefix_tc.cu", "gdn_cache_api.cu", "gdn_cache.cu", "gdn_paged.cu"]
+           "gdn_prefix_tc.cu", "gdn_cache_api.cu", "gdn_cache.cu", "gdn_paged.cu", "gdn_paged_tc.cu"]
 HEADERS = [os.path.join(CSRC, f) for f in ("gdn_kernel.cuh", "gdn_chunk.cuh", "gdn_chunk_tc.cuh", "gdn_group.cuh",
                                            "gdn_linear.cuh", "gdn_prefix.cuh", "gdn_tc_util.cuh",
                                            "gdn_cache.cuh")] + [

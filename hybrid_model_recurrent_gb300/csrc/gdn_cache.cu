@@ -8,7 +8,6 @@
 #include <cfloat>
 
 #include "gdn_cache.cuh"
-#include "gdn_kernel.cuh"
 
 namespace gdn {
 namespace cache {

@@ -7,6 +7,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include "gdn_kernel.cuh"
+
 namespace gdn {
 namespace cache {
 
@@ -107,10 +109,11 @@ cudaError_t launch_compact(const UpkeepParams& p, cudaStream_t s);
 
 // ---- attention ----------------------------------------------------------------------------------------------------
 //
-// The work is cut evenly over the CTAs: an item is a tile of the query rows of one request and key/value head, a unit is
-// `kUnit` tokens of an item, and CTA c takes the units [c share, (c + 1) share) of them all, in the order of requests,
-// heads, row tiles and tokens.  A CTA has so at most one item that it begins in the middle (its part goes to slot 2 c) and one that
-// it begins and leaves unfinished (slot 2 c + 1); a join adds the parts up.
+// The work is cut evenly over the CTAs: an item is a tile of RT query rows of one request and key/value head (rows in the
+// order of tokens and of the heads of the group), a unit is a number of tokens that an item's rows see, and CTA c takes the
+// units [c share, (c + 1) share) of them all, in the order of requests, heads, row tiles and tokens.  So a CTA has at most one
+// item that it begins in the middle (its part goes to slot 2 c) and one that it begins and leaves unfinished (slot 2 c + 1); a
+// join adds the parts up.  Lengths are read on the device only, and differ at will.
 struct PagedParams {
     Cache c;
     Batch t;
@@ -118,17 +121,111 @@ struct PagedParams {
     int64_t q_stride;
     void* o;             // [T, Hq, D]
     float* lse;          // [T, Hq] or nullptr
-    float* part_o;       // [2 CTAs][rows of a tile][D]
-    float2* part_ml;     // [2 CTAs][rows of a tile]: m, l
+    float* part_o;       // [2 CTAs][RT][D]: sums of 2^(x - m) v
+    float2* part_ml;     // [2 CTAs][RT]: m, l
     int32_t* starts;     // [B + 1] units before each request, written by the first CTA for the join
     unsigned int* status;
     float scale_log2;
     int32_t Hq, G, ctas;
+    unsigned long long wait_limit_ns;   // (tensor-core kernel)
+    int32_t stall_after;
 };
-constexpr int kUnit = 64;
+
+// Tokens that a row tile's last row sees, and the tile's units (one at least: rows that see nothing are written too).
+__device__ __forceinline__ int tile_sees(const Request& q, int G, int RT, int tile) {
+    const int last = (min((tile + 1) * RT, q.n * G) - 1) / G;
+    return max(0, min(q.len, q.len - q.n + last + 1));
+}
+template <int RT, int UNIT>
+__device__ __forceinline__ int tile_units(const Request& q, int G, int tile) {
+    return max(1, (tile_sees(q, G, RT, tile) + UNIT - 1) / UNIT);
+}
+// units of a request for one head
+template <int RT, int UNIT>
+__device__ __forceinline__ int head_units(const Request& q, int G) {
+    int n = 0;
+    const int tiles = (q.n * G + RT - 1) / RT;
+    for (int t = 0; t < tiles; ++t) n += tile_units<RT, UNIT>(q, G, t);
+    return n;
+}
+
+// Units before each request into s_cum[0 .. B], by all THREADS threads of a CTA; s_scan: THREADS / 32 ints.
+template <int THREADS, int RT, int UNIT>
+__device__ __forceinline__ void count_units(const PagedParams& p, int* s_cum, int* s_scan) {
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, B = p.t.B;
+    const int per = (B + THREADS - 1) / THREADS;
+    int sum = 0;
+    for (int i = 0; i < per; ++i) {
+        const int b = tid * per + i;
+        if (b < B) {
+            const Request q = request_at(p.c, p.t, b);
+            if (q.bad && blockIdx.x == 0) atomicOr(p.status, STATUS_BAD_INDEX);
+            s_cum[b] = sum;
+            sum += head_units<RT, UNIT>(q, p.G) * p.c.Hkv;
+        }
+    }
+    int y = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int z = __shfl_up_sync(0xffffffffu, y, o);
+        if (lane >= o) y += z;
+    }
+    if (lane == 31) s_scan[warp] = y;
+    __syncthreads();
+    int before = y - sum;
+    for (int w = 0; w < warp; ++w) before += s_scan[w];
+    for (int i = 0; i < per; ++i)
+        if (tid * per + i < B) s_cum[tid * per + i] += before;
+    if (tid == THREADS - 1) s_cum[B] = before + sum;
+    __syncthreads();
+    if (blockIdx.x == 0)
+        for (int i = tid; i <= B; i += THREADS) p.starts[i] = s_cum[i];
+}
+
+// What a CTA does of one item, from unit x on: rows row0 .. of `rows` of the request, tokens lo .. hi.
+struct Segment {
+    Request rq;
+    int b, h, row0, rows, lo, hi, u0, u1, units;
+    __device__ __forceinline__ bool whole() const { return u0 == 0 && u1 == units; }
+    __device__ __forceinline__ int64_t slot() const { return 2 * (int64_t)blockIdx.x + (u0 == 0); }
+};
+template <int RT, int UNIT>
+__device__ __forceinline__ Segment segment_at(const PagedParams& p, const int* s_cum, int x, int end) {
+    Segment s;
+    int b = 0, top = p.t.B;   // cum[b] <= x < cum[top]
+    while (top - b > 1) {
+        const int mid = (b + top) >> 1;
+        if (s_cum[mid] <= x) b = mid;
+        else top = mid;
+    }
+    s.b = b;
+    s.rq = request_at(p.c, p.t, b);
+    const int per_head = (s_cum[b + 1] - s_cum[b]) / p.c.Hkv, rest = x - s_cum[b];
+    s.h = rest / per_head;
+    s.u0 = rest - s.h * per_head;
+    int tile = 0;
+    for (;;) {
+        s.units = tile_units<RT, UNIT>(s.rq, p.G, tile);
+        if (s.u0 < s.units) break;
+        s.u0 -= s.units;
+        ++tile;
+    }
+    s.u1 = min(s.units, s.u0 + end - x);
+    s.row0 = tile * RT;
+    s.rows = min(s.rq.n * p.G - s.row0, RT);
+    s.lo = s.u0 * UNIT;
+    s.hi = min(s.u1 * UNIT, tile_sees(s.rq, p.G, RT, tile));
+    return s;
+}
+
+constexpr int kUnit = 64;       // tokens of a unit: warp-level products
+constexpr int kTcUnit = 128;    // 5th-generation tensor cores
+constexpr int kTcRows = 256;
 
 // `tiles`: row tiles of 16 that a CTA takes at once (1 or 2)
-cudaError_t launch_paged(const PagedParams& p, int D, bool bf16, int tiles, bool join, cudaStream_t s);
+cudaError_t launch_paged(const PagedParams& p, int D, bool bf16, int tiles, cudaStream_t s);
+cudaError_t launch_paged_tc(const PagedParams& p, int D, cudaStream_t s);
+cudaError_t launch_paged_join(const PagedParams& p, int D, bool bf16, int tile_rows, cudaStream_t s);
 
 }  // namespace cache
 }  // namespace gdn

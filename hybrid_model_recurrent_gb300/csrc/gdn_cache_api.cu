@@ -11,6 +11,12 @@
 
 #define GDN_EXPORT extern "C" __attribute__((visibility("default")))
 
+namespace gdn {
+// gdn_api.cu
+uint64_t wait_limit_ns();
+int32_t stall_after();
+}  // namespace gdn
+
 namespace {
 
 using namespace gdn::cache;
@@ -78,24 +84,28 @@ gdn_status check_batch(const gdn_cache* c, const gdn_batch* b, Batch& t) {
 // ---- attention ----------------------------------------------------------------------------------------------------
 
 struct PagedPlan {
-    int tiles, ctas;   // row tiles of 16 a CTA; CTAs
-    bool join;
+    bool tc, join;
+    int tiles, ctas;   // row tiles of 16 a CTA (without tensor cores of the 5th generation); CTAs
+    int tile_rows;
     size_t ml_off, o_off, total;
 };
 
 gdn_status plan_paged(const gdn_cache* c, const Batch& t, gdn_dtype dtype, int Hq, PagedPlan& pl) {
     const int64_t G = Hq / c->num_kv_heads, rows = t.max_new * G;
+    pl.tc = dtype == GDN_BF16 && c->head_dim >= 64 && rows > 32;
     // Rows beyond 16 take tiles of 32, which halve the reads; the second tile costs a third of the warps at once.
     pl.tiles = rows > 16 ? 2 : 1;
-    const int RT = 16 * pl.tiles;
-    const int64_t per_item = std::max<int64_t>(ceil_div(t.max_len, kUnit), 1);
-    const int64_t items = std::min(t.B * ceil_div(rows, RT), ceil_div((int64_t)t.T * G, RT) + t.B) * c->num_kv_heads;
+    pl.tile_rows = pl.tc ? kTcRows : 16 * pl.tiles;
+    const int64_t per_item = std::max<int64_t>(ceil_div(t.max_len, pl.tc ? kTcUnit : kUnit), 1);
+    const int64_t items =
+        std::min(t.B * ceil_div(rows, pl.tile_rows), ceil_div((int64_t)t.T * G, pl.tile_rows) + t.B) * c->num_kv_heads;
     if (items >= (1ll << 31) / per_item - (1 << 16)) return GDN_ERR_UNSUPPORTED;
-    pl.ctas = (int)std::max<int64_t>(1, std::min<int64_t>(items * per_item, (int64_t)kSms * (pl.tiles == 1 ? 3 : 2)));
+    const int per_sm = pl.tc ? 1 : pl.tiles == 1 ? 3 : 2;
+    pl.ctas = (int)std::max<int64_t>(1, std::min<int64_t>(items * per_item, (int64_t)kSms * per_sm));
     pl.join = per_item > 1;
     pl.ml_off = ((size_t)(t.B + 1) * 4 + 31) / 32 * 32;
-    pl.o_off = pl.ml_off + (size_t)2 * pl.ctas * RT * 8;
-    pl.total = pl.o_off + (size_t)2 * pl.ctas * RT * c->head_dim * 4;
+    pl.o_off = pl.ml_off + (size_t)2 * pl.ctas * pl.tile_rows * 8;
+    pl.total = pl.o_off + (size_t)2 * pl.ctas * pl.tile_rows * c->head_dim * 4;
     return GDN_OK;
 }
 
@@ -231,7 +241,12 @@ GDN_EXPORT gdn_status gdn_paged_attention(const gdn_cache* c, int32_t layer, con
     p.part_o = reinterpret_cast<float*>(sc + pl.o_off);
     p.status = static_cast<unsigned int*>(workspace);
     p.Hq = num_q_heads, p.G = num_q_heads / c->num_kv_heads, p.ctas = pl.ctas;
-    return launched(launch_paged(p, c->head_dim, dtype == GDN_BF16, pl.tiles, pl.join, (cudaStream_t)stream));
+    p.wait_limit_ns = gdn::wait_limit_ns();
+    p.stall_after = gdn::stall_after();
+    const bool bf16 = dtype == GDN_BF16;
+    const cudaStream_t s = (cudaStream_t)stream;
+    st = launched(pl.tc ? launch_paged_tc(p, c->head_dim, s) : launch_paged(p, c->head_dim, bf16, pl.tiles, s));
+    return st == GDN_OK && pl.join ? launched(launch_paged_join(p, c->head_dim, bf16, pl.tile_rows, s)) : st;
 }
 
 GDN_EXPORT size_t gdn_cache_scratch_bytes(const gdn_cache* c) { return check_cache(c, true) == GDN_OK ? upkeep_bytes(c) : 0; }

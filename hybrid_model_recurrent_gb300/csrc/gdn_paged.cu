@@ -19,9 +19,9 @@
 
 #include <algorithm>
 #include <cmath>
+#include <type_traits>
 
 #include "gdn_cache.cuh"
-#include "gdn_kernel.cuh"
 
 namespace gdn {
 namespace cache {
@@ -71,12 +71,6 @@ __device__ __forceinline__ float to_f(__nv_bfloat16 x) { return __bfloat162float
 __device__ __forceinline__ void put(float* p, float x) { *p = x; }
 __device__ __forceinline__ void put(__nv_bfloat16* p, float x) { *p = __float2bfloat16_rn(x); }
 
-__device__ __forceinline__ int units_of(const Request& q) { return q.len > 0 ? (q.len + kUnit - 1) / kUnit : 1; }
-// units of all items of a request
-__device__ __forceinline__ int request_units(const PagedParams& p, const Request& q, int tile_rows) {
-    return q.n == 0 ? 0 : (q.n * p.G + tile_rows - 1) / tile_rows * units_of(q) * p.c.Hkv;
-}
-
 template <int D, typename T, int MT>
 struct Cfg {
     static constexpr int PARTS = sizeof(T) == 2 ? 1 : 2;
@@ -106,62 +100,18 @@ __global__ void __launch_bounds__(kWarps * 32, MT == 1 ? 3 : 2) paged_kernel(con
     int* s_cum = reinterpret_cast<int*>(smem + F::kCum);
     const Cache& c = p.c;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, q4 = lane & 3;
-    const int B = p.t.B;
 
-    // ---- units before each request ----
-    {
-        const int per = (B + kWarps * 32 - 1) / (kWarps * 32);
-        int sum = 0;
-        for (int i = 0; i < per; ++i) {
-            const int b = tid * per + i;
-            if (b < B) {
-                const Request q = request_at(c, p.t, b);
-                if (q.bad && blockIdx.x == 0) atomicOr(p.status, STATUS_BAD_INDEX);
-                const int u = request_units(p, q, RT);
-                s_cum[b] = sum;
-                sum += u;
-            }
-        }
-        int y = sum;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int z = __shfl_up_sync(0xffffffffu, y, o);
-            if (lane >= o) y += z;
-        }
-        if (lane == 31) s_scan[warp] = y;
-        __syncthreads();
-        int before = y - sum;
-        for (int w = 0; w < warp; ++w) before += s_scan[w];
-        for (int i = 0; i < per; ++i)
-            if (tid * per + i < B) s_cum[tid * per + i] += before;
-        if (tid == kWarps * 32 - 1) s_cum[B] = before + sum;
-        __syncthreads();
-        if (blockIdx.x == 0 && p.starts)
-            for (int i = tid; i <= B; i += kWarps * 32) p.starts[i] = s_cum[i];
-    }
-    const int total = s_cum[B], share = (total + gridDim.x - 1) / gridDim.x;
+    count_units<kWarps * 32, RT, kUnit>(p, s_cum, s_scan);
+    const int total = s_cum[p.t.B], share = (total + gridDim.x - 1) / gridDim.x;
     int x = (int)min((int64_t)blockIdx.x * share, (int64_t)total);
     const int end = min(x + share, total);
 
     while (x < end) {
-        // ---- the item ----
-        int b = 0, top = B;   // cum[b] <= x < cum[top]
-        while (top - b > 1) {
-            const int mid = (b + top) >> 1;
-            if (s_cum[mid] <= x) b = mid;
-            else top = mid;
-        }
-        const Request rq = request_at(c, p.t, b);
-        const int units = units_of(rq), tiles = (rq.n * p.G + RT - 1) / RT;
-        int rest = x - s_cum[b];
-        const int item = rest / units, u0 = rest - item * units;
-        const int u1 = min(units, u0 + end - x);
-        const int h = item / tiles, tile = item - h * tiles;
-        const int row0 = tile * RT, rows = min(rq.n * p.G - row0, RT);
-        x += u1 - u0;
-        const int shift = rq.len - rq.n;   // query i sees the tokens below shift + i + 1
-        const int lo = u0 * kUnit;
-        const int hi = min(u1 * kUnit, max(0, shift + (row0 + rows - 1) / p.G + 1));
+        const Segment sg = segment_at<RT, kUnit>(p, s_cum, x, end);
+        const Request& rq = sg.rq;
+        const int h = sg.h, row0 = sg.row0, rows = sg.rows, lo = sg.lo, hi = sg.hi;
+        x += sg.u1 - sg.u0;
+        const int shift = rq.len - rq.n;              // query i sees the tokens below shift + i + 1
         const int all_see = shift + row0 / p.G + 1;   // tokens that every row sees end here
         const int32_t* table = c.table + (int64_t)max(rq.row, 0) * c.W;
 
@@ -435,8 +385,8 @@ __global__ void __launch_bounds__(kWarps * 32, MT == 1 ? 3 : 2) paged_kernel(con
             }
         __syncthreads();
         // each warp has a quarter of the column tiles: NT / 4 neighbouring columns of the output
-        const bool whole = u0 == 0 && u1 == units;
-        const int64_t slot = 2 * (int64_t)blockIdx.x + (u0 == 0);
+        const bool whole = sg.whole();
+        const int64_t slot = sg.slot();
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
@@ -484,8 +434,8 @@ __global__ void __launch_bounds__(kWarps * 32, MT == 1 ? 3 : 2) paged_kernel(con
 }
 
 // A warp adds up the parts of one query row.
-template <int D, typename T>
-__global__ void __launch_bounds__(128) paged_join_kernel(const __grid_constant__ PagedParams p, const int RT) {
+template <int D, typename T, int RT, int UNIT>
+__global__ void __launch_bounds__(128) paged_join_kernel(const __grid_constant__ PagedParams p) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int b = blockIdx.y, h = blockIdx.z;
     const Request rq = request_at(p.c, p.t, b);
@@ -493,8 +443,12 @@ __global__ void __launch_bounds__(128) paged_join_kernel(const __grid_constant__
     const int R = blockIdx.x * 4 + warp;
     if (R >= rows) return;
     const int total = p.starts[p.t.B], share = (total + p.ctas - 1) / p.ctas;
-    const int tiles = (rows + RT - 1) / RT, units = units_of(rq), tile = R / RT, r = R - tile * RT;
-    const int first = p.starts[b] + (h * tiles + tile) * units;
+    const int tile = R / RT, r = R - tile * RT, units = tile_units<RT, UNIT>(rq, p.G, tile);
+    int first = 0;
+    for (int t = lane; t < tile; t += 32) first += tile_units<RT, UNIT>(rq, p.G, t);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) first += __shfl_xor_sync(0xffffffffu, first, o);
+    first += p.starts[b] + h * ((p.starts[b + 1] - p.starts[b]) / p.c.Hkv);
     const int c0 = first / share, c1 = (first + units - 1) / share;
     if (c0 == c1) return;
     auto slot = [&](int c) { return (int64_t)2 * c + (c == c0); };
@@ -533,34 +487,44 @@ __global__ void __launch_bounds__(128) paged_join_kernel(const __grid_constant__
 }
 
 template <int D, typename T, int MT>
-cudaError_t launch(const PagedParams& p, bool join, cudaStream_t s) {
+cudaError_t launch(const PagedParams& p, cudaStream_t s) {
     using F = Cfg<D, T, MT>;
     static std::atomic<int> optin[kMaxOptinDevices];
     const cudaError_t e = smem_optin(reinterpret_cast<const void*>(paged_kernel<D, T, MT>), F::bytes(kMaxBatch), optin);
     if (e != cudaSuccess) return e;
     paged_kernel<D, T, MT><<<p.ctas, kWarps * 32, F::bytes(p.t.B), s>>>(p);
-    cudaError_t r = cudaGetLastError();
-    if (r != cudaSuccess || !join) return r;
-    const int blocks = (int)(((int64_t)p.t.max_new * p.G + 3) / 4);
-    paged_join_kernel<D, T><<<dim3(blocks, p.t.B, p.c.Hkv), 128, 0, s>>>(p, F::RT);
     return cudaGetLastError();
 }
 template <int D, typename T>
-cudaError_t launch_t(const PagedParams& p, int tiles, bool join, cudaStream_t s) {
-    return tiles == 1 ? launch<D, T, 1>(p, join, s) : launch<D, T, 2>(p, join, s);
+cudaError_t join(const PagedParams& p, int tile_rows, cudaStream_t s) {
+    const dim3 grid((unsigned)(((int64_t)p.t.max_new * p.G + 3) / 4), p.t.B, p.c.Hkv);
+    if (tile_rows == 16) paged_join_kernel<D, T, 16, kUnit><<<grid, 128, 0, s>>>(p);
+    else if (tile_rows == 32) paged_join_kernel<D, T, 32, kUnit><<<grid, 128, 0, s>>>(p);
+    else if constexpr (sizeof(T) == 2 && D >= 64) paged_join_kernel<D, T, kTcRows, kTcUnit><<<grid, 128, 0, s>>>(p);
+    return cudaGetLastError();
+}
+template <typename F>
+cudaError_t by_type(int D, bool bf16, F&& f) {
+    switch (D * 2 + bf16) {
+        case 64: return f(std::integral_constant<int, 32>(), 0.f);
+        case 65: return f(std::integral_constant<int, 32>(), __nv_bfloat16());
+        case 128: return f(std::integral_constant<int, 64>(), 0.f);
+        case 129: return f(std::integral_constant<int, 64>(), __nv_bfloat16());
+        case 256: return f(std::integral_constant<int, 128>(), 0.f);
+        default: return f(std::integral_constant<int, 128>(), __nv_bfloat16());
+    }
 }
 
 }  // namespace
 
-cudaError_t launch_paged(const PagedParams& p, int D, bool bf16, int tiles, bool join, cudaStream_t s) {
-    switch (D * 2 + bf16) {
-        case 64: return launch_t<32, float>(p, tiles, join, s);
-        case 65: return launch_t<32, __nv_bfloat16>(p, tiles, join, s);
-        case 128: return launch_t<64, float>(p, tiles, join, s);
-        case 129: return launch_t<64, __nv_bfloat16>(p, tiles, join, s);
-        case 256: return launch_t<128, float>(p, tiles, join, s);
-        default: return launch_t<128, __nv_bfloat16>(p, tiles, join, s);
-    }
+cudaError_t launch_paged(const PagedParams& p, int D, bool bf16, int tiles, cudaStream_t s) {
+    return by_type(D, bf16, [&](auto d, auto t) {
+        return tiles == 1 ? launch<d(), decltype(t), 1>(p, s) : launch<d(), decltype(t), 2>(p, s);
+    });
+}
+
+cudaError_t launch_paged_join(const PagedParams& p, int D, bool bf16, int tile_rows, cudaStream_t s) {
+    return by_type(D, bf16, [&](auto d, auto t) { return join<d(), decltype(t)>(p, tile_rows, s); });
 }
 
 }  // namespace cache

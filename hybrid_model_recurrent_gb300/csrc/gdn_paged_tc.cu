@@ -1,0 +1,496 @@
+// gdn_paged_tc.cu - attention over a paged 8-bit cache for many query rows a key/value head (turns and prompts, bf16,
+// head_dim 64 or 128), on the 5th-generation tensor cores.
+//
+// A CTA takes two tiles of 128 query rows of one request and key/value head against tiles of 128 tokens:
+//     S = Q K^T  (TMEM, fp32)  ->  P = 2^(x - m) (bf16, over S's own columns)  ->  O += P V  (TMEM, fp32)
+// with each row's running maximum m and sum l in the thread that owns the row, and O rescaled only when m has risen by more
+// than 2^8.  Scores, statistics and sums are fp32; the weights are rounded to bf16 for the product (half a step, 2^-8 of each).
+//
+// Keys and values reach the products as bf16: three warps load the pages' bytes into registers, a whole tile ahead,
+// multiply by the block's scale (a power of two: e4m3 times it is exact in bf16), and write the swizzled tiles that the
+// products read.  Tokens behind what the rows see are written as zeros, whatever the page holds there.
+// The e4m3 operand itself would need Q and P in 8 bits too: two products with each in two parts, and weights cut at
+// 2^-18 of the largest; and a copy of the cache in bf16 would be read and written once more.
+//
+// The units (128 tokens of an item) are dealt out evenly over the CTAs, one a multiprocessor (gdn_cache.cuh).
+// Roles: warps 0 .. 7 softmax (one warpgroup a row tile), warp 8 issues products, warps 9 .. 11 convert.  One row tile's softmax
+// runs beside the other's products; an item of at most 128 rows takes one tile, in turn.
+//
+// Every wait is bounded: a role that gives up sets the CTA's abort flag and the sticky status, every role leaves its
+// loop, products in flight are waited for, and TMEM is freed.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include <algorithm>
+#include <cmath>
+
+#include "gdn_cache.cuh"
+#include "gdn_tc_util.cuh"
+
+namespace gdn {
+namespace cache {
+namespace {
+
+using tc::idesc;
+using tc::proxy_fence;
+using tc::tc_fence_after;
+using tc::tc_fence_before;
+using tc::tmem_ld32;
+using tc::tmem_ld32x2;
+using tc::tmem_st16;
+using tc::tmem_st32;
+using tc::tmem_st_wait;
+using tc::umma_commit;
+using tc::umma_ss;
+using tc::umma_ts;
+using tcu::cols_step;
+using tcu::elect_one;
+using tcu::ex2;
+using tcu::far_weights;
+using tcu::kFar;
+using tcu::pack2;
+using tcu::rows_step;
+using tcu::store32;
+using tcu::tile_desc;
+using tcu::warp_wait_bar;
+
+constexpr int kRows = 128;    // rows of a tile
+constexpr int kKeys = kTcUnit;
+constexpr float kRise = 8.f;  // O is rescaled when a maximum has risen by more than this (log2)
+constexpr int kConv = 3;      // converting warps
+constexpr int kThreads = 384;
+
+template <int D>
+struct Cfg {
+    static constexpr int kTile = kKeys * D * 2;               // bytes of a K, V or Q tile
+    static constexpr int ST = D == 128 ? 4 : 8;               // K and V tiles in turn
+    static constexpr int kRing = 2 * kTile;                   // after the Q tiles
+    static constexpr int kBar = kRing + ST * kTile;
+    static constexpr int kCum = kBar + 512;                   // units before each request [B + 1]
+    static constexpr int bytes(int B) { return kCum + (B + 1) * 4 + 1024; }
+    static constexpr uint32_t kO = 256;                       // TMEM: S of each row tile, then O of each
+    // pieces of 8 tokens x 64 bytes, 16 bytes a lane
+    static constexpr int kPieces = 16 * D / 64, kOwn = (kPieces + kConv - 1) / kConv;
+    static_assert(bytes(kMaxBatch) <= 232448, "shared memory");
+};
+
+// 16 e4m3 times a scale, as bf16
+__device__ __forceinline__ void widen16(const uint4& u, float scale, uint4& lo, uint4& hi) {
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+    uint32_t y[8];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        uint32_t h0, h1;
+        asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+            : "=r"(h0), "=r"(h1)
+            : "r"(w[i]));
+        const float2 s2 = make_float2(scale, scale);
+        const float2 a = __fmul2_rn(__half22float2(*reinterpret_cast<const __half2*>(&h0)), s2);
+        const float2 b = __fmul2_rn(__half22float2(*reinterpret_cast<const __half2*>(&h1)), s2);
+        y[2 * i] = pack2(a.x, a.y), y[2 * i + 1] = pack2(b.x, b.y);
+    }
+    lo = make_uint4(y[0], y[1], y[2], y[3]), hi = make_uint4(y[4], y[5], y[6], y[7]);
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_constant__ PagedParams p) {
+    using F = Cfg<D>;
+    extern __shared__ unsigned char smem_raw[];
+    unsigned char* smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
+    const uint32_t sbase = smem_addr(smem);
+    uint64_t* full = reinterpret_cast<uint64_t*>(smem + F::kBar);   // [ST] a K or V tile written
+    uint64_t* empty = full + F::ST;                                  // [ST] every product that reads it is done
+    uint64_t* s_full = empty + F::ST;                                // [2] S (and every earlier product) done
+    uint64_t* p_ready = s_full + 2;                                  // [2] P written, O rescaled
+    uint64_t* q_ready = p_ready + 2;                                 // [2] an item's Q tile written
+    uint64_t* o_full = q_ready + 2;                                  // [2] every product of an item done
+    uint64_t* end_bar = o_full + 2;                                  // every product done
+    uint32_t* tslot = reinterpret_cast<uint32_t*>(end_bar + 1);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(tslot + 1);
+    int* s_scan = reinterpret_cast<int*>(tslot + 2);
+    static_assert((2 * F::ST + 9) * 8 + 8 + kThreads / 32 * 4 <= 512, "barrier area");
+    int* s_cum = reinterpret_cast<int*>(smem + F::kCum);
+
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const uint64_t limit = p.wait_limit_ns;
+
+    if (warp == 0) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(tslot)), "r"(512));
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+    }
+    if (tid == 0) {
+        for (int i = 0; i < F::ST; ++i) mbar_init(&full[i], kConv), mbar_init(&empty[i], 1);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&s_full[i], 1), mbar_init(&p_ready[i], 128);
+            mbar_init(&q_ready[i], 128), mbar_init(&o_full[i], 1);
+        }
+        mbar_init(end_bar, 1);
+        *abort_flag = 0;
+        fence_barrier_init();
+    }
+    count_units<kThreads, kTcRows, kTcUnit>(p, s_cum, s_scan);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tbase = *tslot;
+    auto warp_wait = [&](uint64_t* bar, int parity) { return warp_wait_bar(bar, (uint32_t)parity & 1u, abort_flag, limit); };
+
+    const int total = s_cum[p.t.B], share = (total + (int)gridDim.x - 1) / (int)gridDim.x;
+    const int begin = (int)min((int64_t)blockIdx.x * share, (int64_t)total), end = min(begin + share, total);
+
+    // Every role walks the CTA's items; an item of at most 128 rows takes one row tile, the two in turn, so that one tile's sums
+    // leave and its next Q arrives while the other computes.
+    auto takes = [&](const Segment& x, int& turn) {
+        const int one = turn;
+        if (x.rows <= kRows) turn ^= 1;
+        return x.rows > kRows ? 3 : 1 << one;   // bit a: row tile a
+    };
+    auto tiles_of = [&](const Segment& x) { return max(0, (x.hi - x.lo + kKeys - 1) / kKeys); };
+
+    // 384 threads start with 168 registers each (64512 in all): 256 x 200 + 128 x 96 = 63488
+    if (warp >= 8) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 96;");
+        if (warp == 8) {
+            // ---- products (the whole warp walks along, one elected lane issues); K of tile i is ring entry 2 i, V 2 i + 1 ----
+            auto slot_at = [&](int seq) { return sbase + F::kRing + (uint32_t)(seq % F::ST) * F::kTile; };
+            auto landed = [&](int seq) { return warp_wait(&full[seq % F::ST], seq / F::ST); };
+            bool ok = true;
+            int it = 0, turn = 0, tiles[2] = {}, nth[2] = {};   // tiles of the ring; tiles and items of each row tile
+            for (int at = begin; ok && at < end;) {
+                const Segment x = segment_at<kTcRows, kTcUnit>(p, s_cum, at, end);
+                at += x.u1 - x.u0;
+                const int n = tiles_of(x), on = takes(x, turn), last = on >> 1;
+                if (n == 0) continue;
+                auto scores = [&](int a, int i) {
+                    tc_fence_after();
+                    const uint64_t q = tile_desc(sbase + a * F::kTile, false), k = tile_desc(slot_at(2 * i), false);
+                    if (elect_one()) {
+#pragma unroll
+                        for (int s = 0; s < D / 16; ++s)
+                            umma_ss(tbase + a * 128, cols_step(q, s), cols_step(k, s), idesc(kKeys, false, false), s > 0);
+                        umma_commit(&s_full[a]);
+                        if (a == last) umma_commit(&empty[2 * i % F::ST]);
+                    }
+                };
+                ok = landed(2 * it);
+#pragma unroll
+                for (int a = 0; a < 2; ++a) {
+                    if (!(on >> a & 1)) continue;
+                    ok = ok && warp_wait(&q_ready[a], nth[a]);
+                    if (ok) scores(a, it);
+                }
+                for (int j = 0; ok && j < n; ++j) {
+                    const int i = it + j, vs = 2 * i + 1;
+                    ok = landed(vs);
+#pragma unroll
+                    for (int a = 0; a < 2; ++a) {
+                        if (!(on >> a & 1)) continue;
+                        ok = ok && warp_wait(&p_ready[a], tiles[a] + j);
+                        if (!ok) break;
+                        tc_fence_after();
+                        const uint64_t v = tile_desc(slot_at(vs), true);
+                        if (elect_one()) {
+#pragma unroll
+                            for (int s = 0; s < kKeys / 16; ++s)
+                                umma_ts(tbase + F::kO + a * D, tbase + a * 128 + 8 * s, rows_step(v, s), idesc(D, false, true),
+                                        j > 0 || s > 0);
+                            if (a == last) umma_commit(&empty[vs % F::ST]);
+                        }
+                        if (j + 1 < n) {
+                            ok = landed(2 * i + 2);
+                            if (!ok) break;
+                            scores(a, i + 1);
+                        } else if (elect_one()) {
+                            umma_commit(&o_full[a]);
+                        }
+                    }
+                }
+                it += n;
+#pragma unroll
+                for (int a = 0; a < 2; ++a)
+                    if (on >> a & 1) tiles[a] += n, ++nth[a];
+            }
+            if (elect_one()) umma_commit(end_bar);   // also after giving up: the end waits for the products in flight
+        } else {
+            // ---- keys and values, converted ----
+            const int mine = warp - 9, sub = lane >> 2, c16 = (lane & 3) * 16;
+            const int64_t kv_bytes = (int64_t)p.c.Hkv * p.c.page * D;
+            bool ok = true;
+            int seq = 0;
+            for (int at = begin; ok && at < end;) {
+                const Segment x = segment_at<kTcRows, kTcUnit>(p, s_cum, at, end);
+                at += x.u1 - x.u0;
+                const int n = tiles_of(x);
+                if (n == 0) continue;
+                const int32_t* table = p.c.table + (int64_t)x.rq.row * p.c.W;   // (a row without tokens has no tiles)
+                const unsigned char* pages = p.c.pages + (int64_t)x.h * p.c.page * D;
+                // lane l < 16: the page of the tile's tokens 8 l .. 8 l + 7, and its scales (-1 and 0 where there are none)
+                auto page_of = [&](int j) {
+                    const int t = x.lo + j * kKeys + 8 * lane;
+                    if (lane >= 16 || t >= x.hi) return -1;
+                    const int id = __ldg(table + (t >> p.c.page_log2));
+                    if ((unsigned)id < (unsigned)p.c.N) return id;
+                    atomicOr(p.status, STATUS_BAD_INDEX);
+                    return 0;
+                };
+                auto scale_of = [&](int id, int kv) {
+                    return id >= 0 ? __ldg(p.c.scales + ((int64_t)id * 2 + kv) * p.c.Hkv + x.h) : 0.f;
+                };
+                uint4 raw[F::kOwn];
+                auto fetch = [&](int i, int j, int id, int kv) {
+                    const int piece = mine + kConv * i;
+                    if (piece >= F::kPieces) return;
+                    const int group = D == 128 ? piece >> 1 : piece, half = D == 128 ? piece & 1 : 0;
+                    const int pg = __shfl_sync(0xffffffffu, id, group);
+                    const int t = x.lo + j * kKeys + 8 * group + sub;
+                    raw[i] = make_uint4(0, 0, 0, 0);
+                    if (t < x.hi) {
+                        const unsigned char* a = pages + ((int64_t)pg * 2 + kv) * kv_bytes + (int64_t)(t & (p.c.page - 1)) * D + half * 64 + c16;
+                        asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
+                                     : "=r"(raw[i].x), "=r"(raw[i].y), "=r"(raw[i].z), "=r"(raw[i].w)
+                                     : "l"(a));
+                    }
+                };
+                auto write = [&](int i, float scale, unsigned char* tile) {
+                    const int piece = mine + kConv * i;
+                    if (piece >= F::kPieces) return;
+                    const int group = D == 128 ? piece >> 1 : piece, half = D == 128 ? piece & 1 : 0;
+                    uint4 lo, hi;
+                    widen16(raw[i], __shfl_sync(0xffffffffu, scale, group), lo, hi);
+                    unsigned char* row = tile + half * 16384 + (8 * group + sub) * 128;   // (row & 7 = sub)
+                    const int ch = 2 * (lane & 3);
+                    *reinterpret_cast<uint4*>(row + ((ch ^ sub) << 4)) = lo;
+                    *reinterpret_cast<uint4*>(row + (((ch + 1) ^ sub) << 4)) = hi;
+                };
+                auto ready = [&](int s) {   // ring entry s may be written
+                    return !(p.stall_after >= 0 && s / 2 >= p.stall_after) &&   // testing hook
+                           (s < F::ST || warp_wait(&empty[s % F::ST], s / F::ST - 1));
+                };
+                auto written = [&](int s) {
+                    proxy_fence();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&full[s % F::ST]);
+                };
+                int id = page_of(0), id1 = n > 1 ? page_of(1) : -1;
+                float ks = scale_of(id, 0), vs = scale_of(id, 1);
+#pragma unroll
+                for (int i = 0; i < F::kOwn; ++i) fetch(i, 0, id, 0);
+                for (int j = 0; j < n; ++j, seq += 2) {
+                    const int id2 = j + 2 < n ? page_of(j + 2) : -1;
+                    const float ks1 = scale_of(id1, 0), vs1 = scale_of(id1, 1);
+                    if (!(ok = ready(seq))) break;
+                    unsigned char* tile = smem + F::kRing + (seq % F::ST) * F::kTile;
+#pragma unroll
+                    for (int i = 0; i < F::kOwn; ++i) {
+                        write(i, ks, tile);
+                        fetch(i, j, id, 1);
+                    }
+                    written(seq);
+                    if (!(ok = ready(seq + 1))) break;
+                    tile = smem + F::kRing + ((seq + 1) % F::ST) * F::kTile;
+#pragma unroll
+                    for (int i = 0; i < F::kOwn; ++i) {
+                        write(i, vs, tile);
+                        if (j + 1 < n) fetch(i, j + 1, id1, 0);
+                    }
+                    written(seq + 1);
+                    id = id1, id1 = id2, ks = ks1, vs = vs1;
+                }
+            }
+        }
+    } else {
+        // ---- softmax of row tile a; this thread's row ----
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
+        const int a = warp >> 2, r = tid & 127;
+        const uint32_t trow = tbase + ((uint32_t)(32 * (warp & 3)) << 16);
+        // (a scale of 0 as the smallest normal number: every weight is 1, and a hidden token's -infinity stays that)
+        const float scale = fmaxf(fabsf(p.scale_log2), 1.17549435e-38f);
+        bool ok = true;
+        int turn = 0, mine = 0, nth = 0;   // tiles and items of this row tile
+        for (int at = begin; ok && at < end;) {
+            const Segment x = segment_at<kTcRows, kTcUnit>(p, s_cum, at, end);
+            at += x.u1 - x.u0;
+            const int on = takes(x, turn), n = tiles_of(x);
+            if (!(on >> a & 1)) continue;
+            const int rr = (on == 3 ? a * kRows : 0) + r;   // row of the item
+            const bool valid = rr < x.rows;
+            const int R = x.row0 + (valid ? rr : 0), qi = R / p.G;
+            const int vis = min(x.rq.len, x.rq.len - x.rq.n + qi + 1);   // tokens that this row sees end here
+            const int64_t at_o = (int64_t)(x.rq.first + qi) * p.Hq + x.h * p.G + (R - qi * p.G);
+            const bool busy = __any_sync(0xffffffffu, valid);   // a warp without rows only keeps the barriers going
+            // Q, its tile free since the last item's last scores; negated where the scale is negative, so that a maximum of
+            // scores is one of products
+            if (n > 0) {
+                // a warp loads its own 32 rows, 16 bytes a lane, as many rows at a time as its lanes cover (each lane knows
+                // one row's address)
+                constexpr int kLanes = D / 8, kAtOnce = 32 / kLanes;
+                const uint32_t flip = p.scale_log2 < 0.f ? 0x80008000u : 0u;
+                // (past the rows: the item's first row once more, whose results are not stored)
+                const int64_t own = (int64_t)(x.rq.first + qi) * p.q_stride + (int64_t)(x.h * p.G + (R - qi * p.G)) * D;
+                const int c = lane % kLanes, rows = __popc(__ballot_sync(0xffffffffu, valid));
+                for (int k0 = 0; k0 < rows; k0 += 8 * kAtOnce) {   // (rolled, for the instruction cache)
+                    uint4 y[8];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const int64_t off = __shfl_sync(0xffffffffu, own, k0 + i * kAtOnce + lane / kLanes);
+                        y[i] = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.q) + off + 8 * c);
+                    }
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const int row = (r & 96) + k0 + i * kAtOnce + lane / kLanes;
+                        *reinterpret_cast<uint4*>(smem + a * F::kTile + (c >> 3) * 16384 + row * 128 + (((c & 7) ^ (row & 7)) << 4)) =
+                            make_uint4(y[i].x ^ flip, y[i].y ^ flip, y[i].z ^ flip, y[i].w ^ flip);
+                    }
+                }
+                proxy_fence();
+                mbar_arrive(&q_ready[a]);
+            }
+            float m = -INFINITY, l = 0.f;
+            for (int j = 0; j < n; ++j, ++mine) {
+                const int t0 = x.lo + j * kKeys;
+                ok = warp_wait(&s_full[a], mine);
+                if (!ok) break;
+                tc_fence_after();
+                if (busy) {
+                    const int seen = valid ? vis - t0 : kKeys;
+                    const bool hide = __any_sync(0xffffffffu, seen < kKeys);
+                    float s[4][32];
+                    float t[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                    for (int half = 0; half < 2; ++half) {
+                        float(&s0)[32] = s[2 * half], (&s1)[32] = s[2 * half + 1];
+                        tmem_ld32x2(trow + a * 128 + 64 * half, trow + a * 128 + 64 * half + 32, s0, s1);
+                        if (hide) {
+#pragma unroll
+                            for (int i = 0; i < 32; ++i) {
+                                if (64 * half + i >= seen) s0[i] = -INFINITY;
+                                if (64 * half + 32 + i >= seen) s1[i] = -INFINITY;
+                            }
+                        }
+#pragma unroll
+                        for (int i = 0; i < 32; i += 2) {
+                            t[0] = fmaxf(fmaxf(t[0], s0[i]), s0[i + 1]);
+                            t[1 + (i & 2)] = fmaxf(fmaxf(t[1 + (i & 2)], s1[i]), s1[i + 1]);
+                        }
+                    }
+                    const float top = fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3])) * scale;
+                    const bool rise = valid && (top > m + kRise || m == -INFINITY);
+                    if (__any_sync(0xffffffffu, rise)) {
+                        const float mn = rise ? fmaxf(m, top) : m;
+                        const float f = mn == -INFINITY ? 1.f : ex2(m - mn);
+                        m = mn;
+                        l *= f;
+                        if (j > 0) {   // every earlier product into O is done: s_full came after them
+#pragma unroll 1
+                            for (int c = 0; c < D / 32; ++c) {
+                                float o[32];
+                                tmem_ld32(trow + F::kO + a * D + 32 * c, o);
+#pragma unroll
+                                for (int i = 0; i < 32; ++i) o[i] *= f;
+                                tmem_st32(trow + F::kO + a * D + 32 * c, o);
+                            }
+                        }
+                    }
+                    const float base = m == -INFINITY ? 0.f : m;
+                    const float2 scale2 = make_float2(scale, scale), base2 = make_float2(-base, -base);
+                    float2 sum0 = make_float2(0.f, 0.f), sum1 = sum0;
+                    if (__any_sync(0xffffffffu, fabsf(base) > kFar)) {
+                        sum0.x = far_weights(trow + a * 128, seen, scale, base);
+                    } else {
+#pragma unroll
+                        for (int half = 0; half < 2; ++half) {
+                            float(&s0)[32] = s[2 * half], (&s1)[32] = s[2 * half + 1];
+                            uint32_t w0[16], w1[16];
+#pragma unroll
+                            for (int i = 0; i < 16; ++i) {
+                                float2 e = __ffma2_rn(make_float2(s0[2 * i], s0[2 * i + 1]), scale2, base2);
+                                float2 g = __ffma2_rn(make_float2(s1[2 * i], s1[2 * i + 1]), scale2, base2);
+                                e = make_float2(ex2(e.x), ex2(e.y)), g = make_float2(ex2(g.x), ex2(g.y));
+                                sum0 = __fadd2_rn(sum0, e), sum1 = __fadd2_rn(sum1, g);
+                                w0[i] = pack2(e.x, e.y), w1[i] = pack2(g.x, g.y);
+                            }
+                            tmem_st16(trow + a * 128 + 32 * half, w0);
+                            tmem_st16(trow + a * 128 + 32 * half + 16, w1);
+                        }
+                    }
+                    l += (sum0.x + sum0.y) + (sum1.x + sum1.y);
+                    tmem_st_wait();
+                }
+                tc_fence_before();
+                mbar_arrive(&p_ready[a]);
+            }
+            if (!ok) break;
+            if (n > 0) {
+                ok = warp_wait(&o_full[a], nth++);
+                if (!ok) break;
+                tc_fence_after();
+            }
+            if (!busy) continue;
+            const bool some = l != 0.f, whole = x.whole();
+            const float inv = some ? 1.f / l : 0.f;
+            const int64_t part = x.slot() * kTcRows + rr;
+            if (valid && !whole) p.part_ml[part] = make_float2(m, l);
+            if (valid && whole && p.lse) p.lse[at_o] = some ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
+            const bool wide = (reinterpret_cast<uintptr_t>(p.o) & 31) == 0;
+#pragma unroll 1
+            for (int c = 0; c < D / 32; ++c) {
+                float o[32];
+                if (n > 0) {
+                    tmem_ld32(trow + F::kO + a * D + 32 * c, o);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) o[i] = 0.f;
+                }
+                if (valid && whole) {
+                    __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.o) + at_o * D + 32 * c;
+#pragma unroll
+                    for (int i = 0; i < 32; i += 16) {
+                        uint32_t u[8];
+#pragma unroll
+                        for (int k = 0; k < 8; ++k)
+                            u[k] = some ? pack2(o[i + 2 * k] * inv, o[i + 2 * k + 1] * inv) : 0u;
+                        store32(dst + i, u, wide);
+                    }
+                } else if (valid) {
+                    float* dst = p.part_o + part * D + 32 * c;
+#pragma unroll
+                    for (int i = 0; i < 32; i += 8) {
+                        uint32_t u[8];
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) u[k] = __float_as_uint(o[i + k]);
+                        store32(dst + i, u, true);
+                    }
+                }
+            }
+        }
+    }
+
+    // ---- leave only with no product still writing into this CTA's TMEM ----
+    tc_fence_before();
+    __syncthreads();
+    if (tid == 0 && *abort_flag) {
+        tc::drain_phase(end_bar, 0, limit > kDrainLimitNs ? limit : kDrainLimitNs);
+        atomicOr(p.status, STATUS_TIMEOUT);
+    }
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 0)
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tbase), "r"(512));
+}
+
+template <int D>
+cudaError_t launch(const PagedParams& p, cudaStream_t s) {
+    using F = Cfg<D>;
+    static std::atomic<int> optin[kMaxOptinDevices];
+    const cudaError_t e = smem_optin(reinterpret_cast<const void*>(paged_tc_kernel<D>), F::bytes(kMaxBatch), optin);
+    if (e != cudaSuccess) return e;
+    paged_tc_kernel<D><<<p.ctas, kThreads, F::bytes(p.t.B), s>>>(p);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_paged_tc(const PagedParams& p, int D, cudaStream_t s) { return D == 64 ? launch<64>(p, s) : launch<128>(p, s); }
+
+}  // namespace cache
+}  // namespace gdn

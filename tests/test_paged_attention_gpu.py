@@ -27,6 +27,11 @@ def cu_of(new):
     return ints(*out)
 
 
+def step_of(dtype, D, rows):
+    """The rounding step of the weights: bf16 on the tensor cores, which take many rows of bf16."""
+    return dict(weight_step=2.0 ** -8) if dtype == BF and D >= 64 and rows > 32 else {}
+
+
 def queries(T, Hq, D, dtype, seed=1, gain=1.0):
     g = torch.Generator(device="cuda").manual_seed(seed)
     return (torch.randn(T, Hq, D, generator=g, device="cuda") * gain).to(dtype)
@@ -48,7 +53,7 @@ def test_decode(dtype, D, page):
 @pytest.mark.parametrize("H, G", [(1, 1), (3, 3), (2, 5), (1, 16), (1, 17), (2, 40), (1, 128)])
 def test_head_groups(dtype, H, G):
     c = make_cache([5, 333, 70], page=32, H=H, D=64, seed=G)
-    check_attention(c, queries(3, H * G, 64, dtype), cu_of([1, 1, 1]), max_new=1)
+    check_attention(c, queries(3, H * G, 64, dtype), cu_of([1, 1, 1]), max_new=1, **step_of(dtype, 64, G))
 
 
 @pytest.mark.parametrize("dtype", [BF, F32])
@@ -58,8 +63,8 @@ def test_several_queries(dtype, D, G):
     """Drafts and turns: ragged numbers of queries, none, more than the row has tokens (which see nothing), whole prompts."""
     lens, new = [100, 40, 7, 300, 64, 33, 0, 1], [4, 0, 9, 33, 64, 33, 2, 1]
     c = make_cache(lens, page=16, H=2, D=D, seed=G)
-    check_attention(c, queries(sum(new), 2 * G, D, dtype), cu_of(new), max_new=64)
-    check_attention(c, queries(sum(new), 2 * G, D, dtype), cu_of(new))
+    check_attention(c, queries(sum(new), 2 * G, D, dtype), cu_of(new), max_new=64, **step_of(dtype, D, 64 * G))
+    check_attention(c, queries(sum(new), 2 * G, D, dtype), cu_of(new), **step_of(dtype, D, 64 * G))
 
 
 @pytest.mark.parametrize("dtype", [BF, F32])
@@ -209,7 +214,7 @@ def test_captured_and_on_another_stream(dtype, G, new):
             c.table.copy_(rows[[1, 0, 2]])
         graph.replay()
         torch.cuda.synchronize()
-        eager = check_attention(c, q, cu, max_new=new)
+        eager = check_attention(c, q, cu, max_new=new, **step_of(dtype, 64, new * G))
         assert torch.equal(r["o"], eager["o"]) and torch.equal(r["lse"], eager["lse"])
         c.table.copy_(rows)
 
@@ -222,3 +227,96 @@ def test_results_do_not_change():
     for _ in range(5):
         r = gdn.gdn_paged_attention(q, c, ints(0, 10, 20, 30))
         assert torch.equal(r["o"], first["o"]) and torch.equal(r["lse"], first["lse"])
+
+
+TC = dict(weight_step=2.0 ** -8)   # rows of many queries in bf16: weights rounded to bf16
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("page", [16, 64, 128])
+@pytest.mark.parametrize("G", [1, 3, 8])
+def test_many_queries(D, page, G):
+    """Turns and whole prompts on the tensor cores: ragged counts around the tiles' rows, lengths around their tokens, queries
+    that see nothing, requests without any."""
+    lens, new = [300, 129, 128, 700, 64, 1, 0, 90, 1500, 257], [130, 129, 1, 33, 64, 1, 3, 100, 0, 256]
+    c = make_cache(lens, page=page, H=2, D=D, seed=G)
+    check_attention(c, queries(sum(new), 2 * G, D, BF), cu_of(new), max_new=256, **TC)
+    check_attention(c, queries(sum(new), 2 * G, D, BF), cu_of(new), **TC)
+
+
+def test_many_queries_of_rows_padding_and_strides():
+    c = make_cache([300, 129, 515], page=16, H=2, D=64, L=2)
+    qkv = queries(520, 12, 64, BF)
+    new = [100, 17, 300, 90]
+    o, lse = torch.full((520, 8, 64), 7.0, dtype=BF, device="cuda"), torch.full((520, 8), 7.0, device="cuda")
+    check_attention(c, qkv[:, 4:], cu_of(new), rows=ints(2, -1, 0, 9), max_new=300, o=o, lse=lse, layer=1, **TC)
+    assert (o[507:] == 7).all() and (lse[507:] == 7).all()
+
+
+@pytest.mark.parametrize("scale", [0.0, -0.2, 3.0, 1e7, 1e9])
+def test_many_queries_and_scales(scale):
+    """A negative scale, one of zero, and scores so far from zero that a maximum's rounding error matters."""
+    c = make_cache([400], page=64, H=1, D=64)
+    q = queries(60, 4, 64, BF)
+    r = gdn.gdn_paged_attention(q, c, ints(0, 60), scale=scale)
+    assert torch.isfinite(r["o"]).all()
+    if abs(scale) < 10:
+        check_attention(c, q, ints(0, 60), scale=scale, **TC)
+
+
+def test_many_queries_long_and_few():
+    """Few items of many tokens: cut inside an item, by several CTAs; and items of one row tile in turn."""
+    c = make_cache([20011], page=64, H=1, D=128)
+    check_attention(c, queries(130, 2, 128, BF), ints(0, 130), **TC)
+    check_attention(c, queries(40, 2, 128, BF), ints(0, 40), **TC)
+    c = make_cache([777 + 50 * i for i in range(12)], page=32, H=2, D=64)
+    check_attention(c, queries(12 * 40, 4, 64, BF), cu_of([40] * 12), max_new=40, **TC)
+
+
+def test_many_queries_many_requests():
+    lens = [(37 * i) % 300 for i in range(400)]
+    new = [(5 * i) % 23 for i in range(400)]
+    c = make_cache(lens, page=16, H=1, D=64)
+    check_attention(c, queries(sum(new), 2, 64, BF), cu_of(new), max_new=22, **TC)
+
+
+def test_many_queries_blocks_of_different_sizes():
+    c = make_cache([700], page=16, H=1, D=128, spread=12)
+    check_attention(c, queries(80, 2, 128, BF, gain=0.1), ints(0, 80), **TC)
+
+
+def test_many_queries_bad_pages():
+    for bad in (-1, 10 ** 6, 2 ** 31 - 1):
+        c = make_cache([400, 50], page=16, H=2, D=64)
+        want = gdn.gdn_paged_attention(queries(90, 4, 64, BF), c, ints(0, 60, 90))["o"]
+        c.table[0, 3] = bad
+        ws = torch.zeros(256, dtype=torch.uint8, device="cuda")
+        r = gdn.gdn_paged_attention(queries(90, 4, 64, BF), c, ints(0, 60, 90), ws=ws)
+        assert gdn.read_status(ws=ws) == gdn.GDN_ERR_INVALID_ARG
+        assert torch.equal(r["o"][60:], want[60:])
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_many_queries_wait_limit(D):
+    """With the testing hook the converting warps stop; the waits run out, are reported, and the next call is right again."""
+    c = make_cache([900, 800], page=16, H=2, D=D)
+    q, cu = queries(300, 4, D, BF), ints(0, 200, 300)
+    ws = torch.zeros(int(gdn.lib().gdn_workspace_size()), dtype=torch.uint8, device="cuda")
+    want = gdn.gdn_paged_attention(q, c, cu, ws=ws)["o"]
+    torch.cuda.synchronize()
+    assert gdn.read_status(ws=ws) == gdn.GDN_OK
+    try:
+        gdn.set_wait_limit_ns(20_000_000)   # 20 ms
+        for stall in (0, 1):
+            gdn.debug_stall_after(stall)
+            gdn.gdn_paged_attention(q, c, cu, ws=ws)
+            torch.cuda.synchronize()
+            if stall == 0:
+                assert gdn.read_status(ws=ws) == gdn.GDN_ERR_DEVICE_TIMEOUT
+    finally:
+        gdn.debug_stall_after(-1)
+        gdn.set_wait_limit_ns(0)
+    gdn.clear_status(ws=ws)
+    again = gdn.gdn_paged_attention(q, c, cu, ws=ws)["o"]
+    torch.cuda.synchronize()
+    assert gdn.read_status(ws=ws) == gdn.GDN_OK and torch.equal(again, want)
