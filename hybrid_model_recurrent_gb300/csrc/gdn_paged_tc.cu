@@ -6,9 +6,11 @@
 // with each row's running maximum m and sum l in the thread that owns the row, and O rescaled only when m has risen by more
 // than 2^8.  Scores, statistics and sums are fp32; the weights are rounded to bf16 for the product (half a step, 2^-8 of each).
 //
-// Keys and values reach the products as bf16: three warps load the pages' bytes into registers, a whole tile ahead,
-// multiply by the block's scale (a power of two: e4m3 times it is exact in bf16), and write the swizzled tiles that the
-// products read.  Tokens behind what the rows see are written as zeros, whatever the page holds there.
+// Keys and values reach the products as bf16: bulk copies bring the pages' bytes (a block is contiguous) into a ring of
+// their own, three warps multiply them by the block's scale (a power of two: e4m3 times it is exact in bf16) and write
+// the swizzled tiles that the products read.  Tokens behind what the rows see are written as zeros, whatever the page holds
+// there.  (Loaded into registers a tile ahead instead, 11 loads in flight a lane share the few scoreboards, each use waited for
+// the newest of them, and a tile took 11.7 k cycles.)
 // The e4m3 operand itself would need Q and P in 8 bits too: two products with each in two parts, and weights cut at
 // 2^-18 of the largest; and a copy of the cache in bf16 would be read and written once more.
 //
@@ -17,7 +19,7 @@
 // runs beside the other's products; an item of at most 128 rows takes one tile, in turn.
 //
 // Every wait is bounded: a role that gives up sets the CTA's abort flag and the sticky status, every role leaves its
-// loop, products in flight are waited for, and TMEM is freed.
+// loop, copies and products in flight are waited for, and TMEM is freed.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -63,9 +65,11 @@ constexpr int kThreads = 384;
 template <int D>
 struct Cfg {
     static constexpr int kTile = kKeys * D * 2;               // bytes of a K, V or Q tile
-    static constexpr int ST = D == 128 ? 4 : 8;               // K and V tiles in turn
+    static constexpr int ST = D == 128 ? 3 : 6;               // K and V tiles in turn
+    static constexpr int RS = D == 128 ? 3 : 4;               // the same as bytes of the pages
     static constexpr int kRing = 2 * kTile;                   // after the Q tiles
-    static constexpr int kBar = kRing + ST * kTile;
+    static constexpr int kRaw = kRing + ST * kTile;
+    static constexpr int kBar = kRaw + RS * kTile / 2;
     static constexpr int kCum = kBar + 512;                   // units before each request [B + 1]
     static constexpr int bytes(int B) { return kCum + (B + 1) * 4 + 1024; }
     static constexpr uint32_t kO = 256;                       // TMEM: S of each row tile, then O of each
@@ -105,10 +109,13 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_cons
     uint64_t* q_ready = p_ready + 2;                                 // [2] an item's Q tile written
     uint64_t* o_full = q_ready + 2;                                  // [2] every product of an item done
     uint64_t* end_bar = o_full + 2;                                  // every product done
-    uint32_t* tslot = reinterpret_cast<uint32_t*>(end_bar + 1);
+    uint64_t* raw_full = end_bar + 1;                                // [RS] a tile's bytes landed
+    uint64_t* raw_empty = raw_full + F::RS;                          // [RS] and read by the converting warps
+    uint32_t* tslot = reinterpret_cast<uint32_t*>(raw_empty + F::RS);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tslot + 1);
     int* s_scan = reinterpret_cast<int*>(tslot + 2);
-    static_assert((2 * F::ST + 9) * 8 + 8 + kThreads / 32 * 4 <= 512, "barrier area");
+    int* issued = s_scan + kThreads / 32;                            // tiles whose copies were issued
+    static_assert((2 * F::ST + 2 * F::RS + 9) * 8 + 8 + kThreads / 32 * 4 + 4 <= 512, "barrier area");
     int* s_cum = reinterpret_cast<int*>(smem + F::kCum);
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -125,7 +132,9 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_cons
             mbar_init(&q_ready[i], 128), mbar_init(&o_full[i], 1);
         }
         mbar_init(end_bar, 1);
+        for (int i = 0; i < F::RS; ++i) mbar_init(&raw_full[i], 1), mbar_init(&raw_empty[i], kConv);
         *abort_flag = 0;
+        *issued = 0;
         fence_barrier_init();
     }
     count_units<kThreads, kTcRows, kTcUnit>(p, s_cum, s_scan);
@@ -212,9 +221,16 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_cons
             }
             if (elect_one()) umma_commit(end_bar);   // also after giving up: the end waits for the products in flight
         } else {
-            // ---- keys and values, converted ----
-            const int mine = warp - 9, sub = lane >> 2, c16 = (lane & 3) * 16;
-            const int64_t kv_bytes = (int64_t)p.c.Hkv * p.c.page * D;
+            // ---- keys and values: copied (the first of the three warps, a lane a page) and converted ----
+            const int mine = warp - 9, sub = lane >> 2, quad = lane & 3;
+            const int64_t block = (int64_t)p.c.page * D;
+            const int per_tile = kKeys >> p.c.page_log2;   // pages of a tile
+            auto page_id = [&](const int32_t* table, int t) {
+                const int id = __ldg(table + (t >> p.c.page_log2));
+                if ((unsigned)id < (unsigned)p.c.N) return id;
+                atomicOr(p.status, STATUS_BAD_INDEX);
+                return 0;
+            };
             bool ok = true;
             int seq = 0;
             for (int at = begin; ok && at < end;) {
@@ -223,79 +239,84 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_cons
                 const int n = tiles_of(x);
                 if (n == 0) continue;
                 const int32_t* table = p.c.table + (int64_t)x.rq.row * p.c.W;   // (a row without tokens has no tiles)
-                const unsigned char* pages = p.c.pages + (int64_t)x.h * p.c.page * D;
-                // lane l < 16: the page of the tile's tokens 8 l .. 8 l + 7, and its scales (-1 and 0 where there are none)
-                auto page_of = [&](int j) {
+                // the page of tile j that this lane copies, and the one of its tokens 8 l .. 8 l + 7 for the scales; -1: none
+                auto copied = [&](int j) {
+                    const int t = x.lo + j * kKeys + (lane << p.c.page_log2);
+                    return lane < per_tile && j < n && t < x.hi ? page_id(table, t) : -1;
+                };
+                auto scaled = [&](int j) {
                     const int t = x.lo + j * kKeys + 8 * lane;
-                    if (lane >= 16 || t >= x.hi) return -1;
-                    const int id = __ldg(table + (t >> p.c.page_log2));
-                    if ((unsigned)id < (unsigned)p.c.N) return id;
-                    atomicOr(p.status, STATUS_BAD_INDEX);
-                    return 0;
+                    return lane < 16 && j < n && t < x.hi ? page_id(table, t) : -1;
                 };
                 auto scale_of = [&](int id, int kv) {
                     return id >= 0 ? __ldg(p.c.scales + ((int64_t)id * 2 + kv) * p.c.Hkv + x.h) : 0.f;
                 };
-                uint4 raw[F::kOwn];
-                auto fetch = [&](int i, int j, int id, int kv) {
-                    const int piece = mine + kConv * i;
-                    if (piece >= F::kPieces) return;
-                    const int group = D == 128 ? piece >> 1 : piece, half = D == 128 ? piece & 1 : 0;
-                    const int pg = __shfl_sync(0xffffffffu, id, group);
-                    const int t = x.lo + j * kKeys + 8 * group + sub;
-                    raw[i] = make_uint4(0, 0, 0, 0);
-                    if (t < x.hi) {
-                        const unsigned char* a = pages + ((int64_t)pg * 2 + kv) * kv_bytes + (int64_t)(t & (p.c.page - 1)) * D + half * 64 + c16;
-                        asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
-                                     : "=r"(raw[i].x), "=r"(raw[i].y), "=r"(raw[i].z), "=r"(raw[i].w)
-                                     : "l"(a));
+                // ring entry `e` of all: keys or values of a tile of this item, whose pages the lanes hold
+                auto copy = [&](int e, int id, int kv) {
+                    if (p.stall_after >= 0 && e / 2 >= p.stall_after) return false;   // testing hook
+                    if (e >= F::RS && !warp_wait(&raw_empty[e % F::RS], e / F::RS - 1)) return false;
+                    const int pages = __popc(__ballot_sync(0xffffffffu, id >= 0));
+                    if (lane == 0) {
+                        mbar_arrive_expect_tx(&raw_full[e % F::RS], (uint32_t)(pages * block));
+                        *issued = e + 1;
                     }
+                    __syncwarp();
+                    if (id >= 0)
+                        asm volatile(
+                            "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                                sbase + F::kRaw + (uint32_t)(e % F::RS) * (F::kTile / 2) + (uint32_t)(lane * block)),
+                            "l"(p.c.pages + (((int64_t)id * 2 + kv) * p.c.Hkv + x.h) * block), "r"((uint32_t)block),
+                            "r"(smem_addr(&raw_full[e % F::RS]))
+                            : "memory");
+                    return true;
                 };
-                auto write = [&](int i, float scale, unsigned char* tile) {
-                    const int piece = mine + kConv * i;
-                    if (piece >= F::kPieces) return;
-                    const int group = D == 128 ? piece >> 1 : piece, half = D == 128 ? piece & 1 : 0;
-                    uint4 lo, hi;
-                    widen16(raw[i], __shfl_sync(0xffffffffu, scale, group), lo, hi);
-                    unsigned char* row = tile + half * 16384 + (8 * group + sub) * 128;   // (row & 7 = sub)
-                    const int ch = 2 * (lane & 3);
-                    *reinterpret_cast<uint4*>(row + ((ch ^ sub) << 4)) = lo;
-                    *reinterpret_cast<uint4*>(row + (((ch + 1) ^ sub) << 4)) = hi;
-                };
-                auto ready = [&](int s) {   // ring entry s may be written
-                    return !(p.stall_after >= 0 && s / 2 >= p.stall_after) &&   // testing hook
-                           (s < F::ST || warp_wait(&empty[s % F::ST], s / F::ST - 1));
-                };
-                auto written = [&](int s) {
+                auto convert = [&](int e, float scale, int t0) {
+                    if (!warp_wait(&raw_full[e % F::RS], e / F::RS)) return false;
+                    if (e >= F::ST && !warp_wait(&empty[e % F::ST], e / F::ST - 1)) return false;
+                    const unsigned char* raw = smem + F::kRaw + (e % F::RS) * (F::kTile / 2);
+                    unsigned char* tile = smem + F::kRing + (e % F::ST) * F::kTile;
+                    const bool part = x.hi - t0 < kKeys;
+#pragma unroll
+                    for (int i = 0; i < F::kOwn; ++i) {
+                        const int piece = mine + kConv * i;
+                        if (piece >= F::kPieces) break;
+                        // 8 tokens x 64 bytes; at width 128 odd tokens take the other half, for the banks
+                        const int group = D == 128 ? piece >> 1 : piece, half = D == 128 ? (piece ^ sub) & 1 : 0;
+                        const int row = 8 * group + sub;
+                        uint4 y = *reinterpret_cast<const uint4*>(raw + row * D + half * 64 + quad * 16), lo, hi;
+                        if (part && t0 + row >= x.hi) y = make_uint4(0, 0, 0, 0);
+                        widen16(y, __shfl_sync(0xffffffffu, scale, group), lo, hi);
+                        unsigned char* to = tile + half * 16384 + row * 128;   // (row & 7 = sub)
+                        *reinterpret_cast<uint4*>(to + (((2 * quad) ^ sub) << 4)) = lo;
+                        *reinterpret_cast<uint4*>(to + (((2 * quad + 1) ^ sub) << 4)) = hi;
+                    }
                     proxy_fence();
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(&full[s % F::ST]);
+                    if (lane == 0) mbar_arrive(&raw_empty[e % F::RS]), mbar_arrive(&full[e % F::ST]);
+                    return true;
                 };
-                int id = page_of(0), id1 = n > 1 ? page_of(1) : -1;
-                float ks = scale_of(id, 0), vs = scale_of(id, 1);
-#pragma unroll
-                for (int i = 0; i < F::kOwn; ++i) fetch(i, 0, id, 0);
-                for (int j = 0; j < n; ++j, seq += 2) {
-                    const int id2 = j + 2 < n ? page_of(j + 2) : -1;
+                // the copies run RS - 1 entries ahead of the conversion
+                int idc = mine == 0 ? copied(0) : -1, idc1 = mine == 0 ? copied(1) : -1;   // of tile `ahead` / 2 and the next
+                int ahead = 0;
+                auto advance = [&] {
+                    if (mine != 0 || ahead >= 2 * n) return true;
+                    const bool good = copy(seq + ahead, idc, ahead & 1);
+                    if (ahead & 1) idc = idc1, idc1 = copied(ahead / 2 + 2);
+                    ++ahead;
+                    return good;
+                };
+                const int id0 = scaled(0);
+                int id1 = scaled(1);
+                float ks = scale_of(id0, 0), vs = scale_of(id0, 1);
+                for (int i = 0; ok && i < F::RS - 1; ++i) ok = advance();
+                for (int j = 0; ok && j < n; ++j) {
+                    const int id2 = scaled(j + 2);
                     const float ks1 = scale_of(id1, 0), vs1 = scale_of(id1, 1);
-                    if (!(ok = ready(seq))) break;
-                    unsigned char* tile = smem + F::kRing + (seq % F::ST) * F::kTile;
-#pragma unroll
-                    for (int i = 0; i < F::kOwn; ++i) {
-                        write(i, ks, tile);
-                        fetch(i, j, id, 1);
-                    }
-                    written(seq);
-                    if (!(ok = ready(seq + 1))) break;
-                    tile = smem + F::kRing + ((seq + 1) % F::ST) * F::kTile;
-#pragma unroll
-                    for (int i = 0; i < F::kOwn; ++i) {
-                        write(i, vs, tile);
-                        if (j + 1 < n) fetch(i, j + 1, id1, 0);
-                    }
-                    written(seq + 1);
-                    id = id1, id1 = id2, ks = ks1, vs = vs1;
+                    const int t0 = x.lo + j * kKeys;
+                    ok = advance() && convert(seq + 2 * j, ks, t0) && advance() && convert(seq + 2 * j + 1, vs, t0);
+                    id1 = id2, ks = ks1, vs = vs1;
                 }
+                seq += 2 * n;
             }
         }
     } else {
@@ -465,11 +486,14 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_cons
         }
     }
 
-    // ---- leave only with no product still writing into this CTA's TMEM ----
+    // ---- leave only with no copy and no product still writing into this CTA's shared memory or TMEM ----
     tc_fence_before();
     __syncthreads();
     if (tid == 0 && *abort_flag) {
-        tc::drain_phase(end_bar, 0, limit > kDrainLimitNs ? limit : kDrainLimitNs);
+        const uint64_t drain = limit > kDrainLimitNs ? limit : kDrainLimitNs;
+        for (int e = max(0, *issued - F::RS); e < *issued; ++e)
+            tc::drain_phase(&raw_full[e % F::RS], (uint32_t)((e / F::RS) & 1), drain);
+        tc::drain_phase(end_bar, 0, drain);
         atomicOr(p.status, STATUS_TIMEOUT);
     }
     __syncthreads();
