@@ -2,17 +2,22 @@
 // head_dim 64 or 128), on the 5th-generation tensor cores.
 //
 // A CTA takes two tiles of 128 query rows of one request and key/value head against tiles of 128 tokens:
-//     S = Q K^T  (TMEM, fp32)  ->  P = 2^(x - m) (bf16, over S's own columns)  ->  O += P V  (TMEM, fp32)
+//     S = Q K^T  (TMEM, fp32)  ->  P = 2^(x - m) (f16, over S's own columns)  ->  O += P V  (TMEM, fp32)
 // with each row's running maximum m and sum l in the thread that owns the row, and O rescaled only when m has risen by more
-// than 2^8.  Scores, statistics and sums are fp32; the weights are rounded to bf16 for the product (half a step, 2^-8 of each).
+// than 2^8.  Scores, statistics and sums are fp32; the weights are rounded to f16 for the product (half a step, 2^-11 of each).
 //
-// Keys and values reach the products as bf16: bulk copies bring the pages' bytes (a block is contiguous) into a ring of
-// their own, three warps multiply them by the block's scale (a power of two: e4m3 times it is exact in bf16) and write
+// All operands are f16, which holds e4m3 exactly and takes one conversion for two values.  What f16 lacks in range is carried
+// beside it, by powers of two that cost nothing a value: a row of Q is brought to [2^14, 2^15), a tile's keys and values
+// are taken relative to the largest scale of their blocks (the blocks of a tile that differ are multiplied by the ratio;
+// below 2^-24 a block counts as zeros).  The keys' scale joins the row's in the exponent; the values' goes into it too,
+// relative to the largest of the item so far (16 powers of two at most: l is summed from the same weights), and raising
+// that one rescales O as a risen maximum does.
+// (With bf16 operands, which take the blocks' scales as they are, the three warps below made two conversions and a product
+// for each value, 40 instructions for 16 of them, and a tile took 10 k cycles; without that arithmetic 5.7 k.)
+//
+// Bulk copies bring the pages' bytes (a block is contiguous) into a ring of their own, three warps convert them and write
 // the swizzled tiles that the products read.  Tokens behind what the rows see are written as zeros, whatever the page holds
-// there.  (Loaded into registers a tile ahead instead, 11 loads in flight a lane share the few scoreboards, each use waited for
-// the newest of them, and a tile took 11.7 k cycles.)
-// The e4m3 operand itself would need Q and P in 8 bits too: two products with each in two parts, and weights cut at
-// 2^-18 of the largest; and a copy of the cache in bf16 would be read and written once more.
+// there.
 //
 // The units (128 tokens of an item) are dealt out evenly over the CTAs, one a multiprocessor (gdn_cache.cuh).
 // Roles: warps 0 .. 7 softmax (one warpgroup a row tile), warp 8 issues products, warps 9 .. 11 convert.  One row tile's softmax
@@ -47,9 +52,6 @@ using tc::umma_ss;
 using tc::umma_ts;
 using tcu::cols_step;
 using tcu::elect_one;
-using tcu::ex2;
-using tcu::far_weights;
-using tcu::kFar;
 using tcu::pack2;
 using tcu::rows_step;
 using tcu::store32;
@@ -59,7 +61,14 @@ using tcu::warp_wait_bar;
 constexpr int kRows = 128;    // rows of a tile
 constexpr int kKeys = kTcUnit;
 constexpr float kRise = 8.f;  // O is rescaled when a maximum has risen by more than this (log2)
+constexpr float kLift = 7.f;  // log2 of a weight at the maximum: with the rise 2^15 in f16
+constexpr int kLow = 16;      // powers of two that a tile's values may lie below the item's largest before they are cut
 constexpr int kConv = 3;      // converting warps
+constexpr int kInfos = 8;     // tiles whose scales are kept: more than the converting warps can run ahead
+// A weight's exponent is score * scale - m in one rounding, but m is a product already rounded: for the largest score its
+// rounding error is left, half a step of m, 16 at 2^28 and past what an exponential holds from 2^31 on.  Rows further from zero
+// than this round the product by itself first.
+constexpr float kFar = 268435456.f;
 constexpr int kThreads = 384;
 
 template <int D>
@@ -78,22 +87,54 @@ struct Cfg {
     static_assert(bytes(kMaxBatch) <= 232448, "shared memory");
 };
 
-// 16 e4m3 times a scale, as bf16
-__device__ __forceinline__ void widen16(const uint4& u, float scale, uint4& lo, uint4& hi) {
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ uint32_t half2(float a, float b) {
+    const __half2 h = __floats2half2_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+// instruction descriptor of kind::f16: D fp32, A and B f16, M = 128
+__host__ __device__ constexpr uint32_t idesc_f16(int N, bool b_mn) { return idesc(N, false, b_mn) & ~((1u << 7) | (1u << 10)); }
+
+// 16 e4m3 as f16
+__device__ __forceinline__ void widen16(const uint4& u, uint32_t (&y)[8]) {
     const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-    uint32_t y[8];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        uint32_t h0, h1;
+    for (int i = 0; i < 4; ++i)
         asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
-            : "=r"(h0), "=r"(h1)
+            : "=r"(y[2 * i]), "=r"(y[2 * i + 1])
             : "r"(w[i]));
-        const float2 s2 = make_float2(scale, scale);
-        const float2 a = __fmul2_rn(__half22float2(*reinterpret_cast<const __half2*>(&h0)), s2);
-        const float2 b = __fmul2_rn(__half22float2(*reinterpret_cast<const __half2*>(&h1)), s2);
-        y[2 * i] = pack2(a.x, a.y), y[2 * i + 1] = pack2(b.x, b.y);
+}
+
+// What the rows need to know of a tile: the largest scale of its keys' blocks, the item's largest of the values so far (a power of
+// two), the log2 of a weight at the maximum, and the weight's inverse.
+struct TileInfo {
+    float k, v, lift, drop;
+};
+
+// The weights of a tile's row, over its own scores in TMEM, for rows far from zero; returns their sum.  A function by itself, so
+// that the loop of every other row stays small.
+__device__ __noinline__ float far_weights(uint32_t taddr, int seen, float scale, float base, float lift) {
+    float sum = 0.f;
+#pragma unroll 1
+    for (int c = 0; c < kKeys / 32; ++c) {
+        float x[32];
+        uint32_t w[16];
+        tmem_ld32(taddr + 32 * c, x);
+#pragma unroll
+        for (int i = 0; i < 32; ++i) {
+            const float y = __fsub_rn(__fmul_rn(x[i], scale), base);
+            x[i] = 32 * c + i < seen ? ex2(y + lift) : 0.f;
+            sum += x[i];
+        }
+#pragma unroll
+        for (int i = 0; i < 16; ++i) w[i] = half2(x[2 * i], x[2 * i + 1]);
+        tmem_st16(taddr + 16 * c, w);
     }
-    lo = make_uint4(y[0], y[1], y[2], y[3]), hi = make_uint4(y[4], y[5], y[6], y[7]);
+    return sum;
 }
 
 template <int D>
@@ -115,7 +156,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_cons
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tslot + 1);
     int* s_scan = reinterpret_cast<int*>(tslot + 2);
     int* issued = s_scan + kThreads / 32;                            // tiles whose copies were issued
-    static_assert((2 * F::ST + 2 * F::RS + 9) * 8 + 8 + kThreads / 32 * 4 + 4 <= 512, "barrier area");
+    TileInfo* info = reinterpret_cast<TileInfo*>(smem + F::kBar + 512 - sizeof(TileInfo) * kInfos);
+    static_assert((2 * F::ST + 2 * F::RS + 9) * 8 + 8 + kThreads / 32 * 4 + 4 + sizeof(TileInfo) * kInfos <= 512, "barrier area");
     int* s_cum = reinterpret_cast<int*>(smem + F::kCum);
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -176,7 +218,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_cons
                     if (elect_one()) {
 #pragma unroll
                         for (int s = 0; s < D / 16; ++s)
-                            umma_ss(tbase + a * 128, cols_step(q, s), cols_step(k, s), idesc(kKeys, false, false), s > 0);
+                            umma_ss(tbase + a * 128, cols_step(q, s), cols_step(k, s), idesc_f16(kKeys, false), s > 0);
                         umma_commit(&s_full[a]);
                         if (a == last) umma_commit(&empty[2 * i % F::ST]);
                     }
@@ -201,7 +243,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_cons
                         if (elect_one()) {
 #pragma unroll
                             for (int s = 0; s < kKeys / 16; ++s)
-                                umma_ts(tbase + F::kO + a * D, tbase + a * 128 + 8 * s, rows_step(v, s), idesc(D, false, true),
+                                umma_ts(tbase + F::kO + a * D, tbase + a * 128 + 8 * s, rows_step(v, s), idesc_f16(D, true),
                                         j > 0 || s > 0);
                             if (a == last) umma_commit(&empty[vs % F::ST]);
                         }
@@ -270,12 +312,14 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_cons
                             : "memory");
                     return true;
                 };
-                auto convert = [&](int e, float scale, int t0) {
+                auto convert = [&](int e, float ratio, int t0) {   // (a lane's ratio is that of its 8 tokens' block)
                     if (!warp_wait(&raw_full[e % F::RS], e / F::RS)) return false;
                     if (e >= F::ST && !warp_wait(&empty[e % F::ST], e / F::ST - 1)) return false;
                     const unsigned char* raw = smem + F::kRaw + (e % F::RS) * (F::kTile / 2);
                     unsigned char* tile = smem + F::kRing + (e % F::ST) * F::kTile;
                     const bool part = x.hi - t0 < kKeys;
+                    const uint32_t ratio2 = half2(ratio, ratio);
+                    const bool same = __all_sync(0xffffffffu, ratio == 1.f || lane >= 16);
 #pragma unroll
                     for (int i = 0; i < F::kOwn; ++i) {
                         const int piece = mine + kConv * i;
@@ -283,12 +327,18 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_cons
                         // 8 tokens x 64 bytes; at width 128 odd tokens take the other half, for the banks
                         const int group = D == 128 ? piece >> 1 : piece, half = D == 128 ? (piece ^ sub) & 1 : 0;
                         const int row = 8 * group + sub;
-                        uint4 y = *reinterpret_cast<const uint4*>(raw + row * D + half * 64 + quad * 16), lo, hi;
-                        if (part && t0 + row >= x.hi) y = make_uint4(0, 0, 0, 0);
-                        widen16(y, __shfl_sync(0xffffffffu, scale, group), lo, hi);
+                        uint4 u = *reinterpret_cast<const uint4*>(raw + row * D + half * 64 + quad * 16);
+                        if (part && t0 + row >= x.hi) u = make_uint4(0, 0, 0, 0);
+                        uint32_t y[8];
+                        widen16(u, y);
+                        if (!same) {
+                            const uint32_t f = __shfl_sync(0xffffffffu, ratio2, group);
+#pragma unroll
+                            for (int k = 0; k < 8; ++k) asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(y[k]) : "r"(y[k]), "r"(f));
+                        }
                         unsigned char* to = tile + half * 16384 + row * 128;   // (row & 7 = sub)
-                        *reinterpret_cast<uint4*>(to + (((2 * quad) ^ sub) << 4)) = lo;
-                        *reinterpret_cast<uint4*>(to + (((2 * quad + 1) ^ sub) << 4)) = hi;
+                        *reinterpret_cast<uint4*>(to + (((2 * quad) ^ sub) << 4)) = make_uint4(y[0], y[1], y[2], y[3]);
+                        *reinterpret_cast<uint4*>(to + (((2 * quad + 1) ^ sub) << 4)) = make_uint4(y[4], y[5], y[6], y[7]);
                     }
                     proxy_fence();
                     __syncwarp();
@@ -309,11 +359,21 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_cons
                 int id1 = scaled(1);
                 float ks = scale_of(id0, 0), vs = scale_of(id0, 1);
                 for (int i = 0; ok && i < F::RS - 1; ++i) ok = advance();
+                auto largest = [](float y) { return __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(y))); };
+                float item_v = 0.f;   // the largest scale of the item's values so far, as a power of two
                 for (int j = 0; ok && j < n; ++j) {
                     const int id2 = scaled(j + 2);
                     const float ks1 = scale_of(id1, 0), vs1 = scale_of(id1, 1);
                     const int t0 = x.lo + j * kKeys;
-                    ok = advance() && convert(seq + 2 * j, ks, t0) && advance() && convert(seq + 2 * j + 1, vs, t0);
+                    const float tk = largest(ks), tv = largest(vs);
+                    item_v = fmaxf(item_v, __uint_as_float(__float_as_uint(tv) & 0x7f800000u));
+                    // the tile's values relative to a power of two, kLow below the item's at least
+                    const int low = min((int)(__float_as_uint(item_v) >> 23) - (int)(__float_as_uint(tv) >> 23), kLow);
+                    const float ref = item_v * __uint_as_float((uint32_t)(127 - low) << 23);
+                    if (mine == 0 && lane == 0) info[(seq / 2 + j) % kInfos] =
+                            {tk, item_v, kLift - (float)low, __uint_as_float((uint32_t)(127 - (int)kLift + low) << 23)};
+                    ok = advance() && convert(seq + 2 * j, tk > 0.f ? ks / tk : 0.f, t0) && advance() &&
+                         convert(seq + 2 * j + 1, ref > 0.f ? vs / ref : 0.f, t0);
                     id1 = id2, ks = ks1, vs = vs1;
                 }
                 seq += 2 * n;
@@ -324,14 +384,13 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_cons
         asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
         const int a = warp >> 2, r = tid & 127;
         const uint32_t trow = tbase + ((uint32_t)(32 * (warp & 3)) << 16);
-        // (a scale of 0 as the smallest normal number: every weight is 1, and a hidden token's -infinity stays that)
-        const float scale = fmaxf(fabsf(p.scale_log2), 1.17549435e-38f);
         bool ok = true;
-        int turn = 0, mine = 0, nth = 0;   // tiles and items of this row tile
+        int turn = 0, it = 0, mine = 0, nth = 0;   // tiles of all items; tiles and items of this row tile
         for (int at = begin; ok && at < end;) {
             const Segment x = segment_at<kTcRows, kTcUnit>(p, s_cum, at, end);
             at += x.u1 - x.u0;
-            const int on = takes(x, turn), n = tiles_of(x);
+            const int on = takes(x, turn), n = tiles_of(x), it0 = it;
+            it += n;
             if (!(on >> a & 1)) continue;
             const int rr = (on == 3 ? a * kRows : 0) + r;   // row of the item
             const bool valid = rr < x.rows;
@@ -339,13 +398,13 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_cons
             const int vis = min(x.rq.len, x.rq.len - x.rq.n + qi + 1);   // tokens that this row sees end here
             const int64_t at_o = (int64_t)(x.rq.first + qi) * p.Hq + x.h * p.G + (R - qi * p.G);
             const bool busy = __any_sync(0xffffffffu, valid);   // a warp without rows only keeps the barriers going
-            // Q, its tile free since the last item's last scores; negated where the scale is negative, so that a maximum of
-            // scores is one of products
+            // Q, its tile free since the last item's last scores: a power of two times the row, negated where the scale is
+            // negative, so that a maximum of scores is one of products
+            float row_scale = 0.f;
             if (n > 0) {
                 // a warp loads its own 32 rows, 16 bytes a lane, as many rows at a time as its lanes cover (each lane knows
                 // one row's address)
                 constexpr int kLanes = D / 8, kAtOnce = 32 / kLanes;
-                const uint32_t flip = p.scale_log2 < 0.f ? 0x80008000u : 0u;
                 // (past the rows: the item's first row once more, whose results are not stored)
                 const int64_t own = (int64_t)(x.rq.first + qi) * p.q_stride + (int64_t)(x.h * p.G + (R - qi * p.G)) * D;
                 const int c = lane % kLanes, rows = __popc(__ballot_sync(0xffffffffu, valid));
@@ -358,15 +417,31 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_cons
                     }
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
-                        const int row = (r & 96) + k0 + i * kAtOnce + lane / kLanes;
+                        uint32_t top = __vmaxu2(__vmaxu2(y[i].x & 0x7fff7fffu, y[i].y & 0x7fff7fffu),
+                                                __vmaxu2(y[i].z & 0x7fff7fffu, y[i].w & 0x7fff7fffu));
+#pragma unroll
+                        for (int o = kLanes / 2; o > 0; o >>= 1) top = __vmaxu2(top, __shfl_xor_sync(0xffffffffu, top, o));
+                        const int e = max((int)(max(top & 0xffffu, top >> 16) >> 7) - 127, -100);
+                        const float f = __uint_as_float((uint32_t)(14 - min(e, 127) + 127) << 23);
+                        const int first = k0 + i * kAtOnce;
+                        const float fr = __shfl_sync(0xffffffffu, f, ((lane - first) & (kAtOnce - 1)) * kLanes);
+                        if (lane >= first && lane < first + kAtOnce) row_scale = fr;
+                        const float g = p.scale_log2 < 0.f ? -f : f;
+                        const uint32_t w[4] = {y[i].x, y[i].y, y[i].z, y[i].w};
+                        uint32_t z[4];
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            z[k] = half2(__uint_as_float(w[k] << 16) * g, __uint_as_float(w[k] & 0xffff0000u) * g);
+                        const int row = (r & 96) + first + lane / kLanes;
                         *reinterpret_cast<uint4*>(smem + a * F::kTile + (c >> 3) * 16384 + row * 128 + (((c & 7) ^ (row & 7)) << 4)) =
-                            make_uint4(y[i].x ^ flip, y[i].y ^ flip, y[i].z ^ flip, y[i].w ^ flip);
+                            make_uint4(z[0], z[1], z[2], z[3]);
                     }
                 }
+                row_scale = valid ? fabsf(p.scale_log2) / row_scale : 0.f;
                 proxy_fence();
                 mbar_arrive(&q_ready[a]);
             }
-            float m = -INFINITY, l = 0.f;
+            float m = -INFINITY, l = 0.f, item_v = 0.f;
             for (int j = 0; j < n; ++j, ++mine) {
                 const int t0 = x.lo + j * kKeys;
                 ok = warp_wait(&s_full[a], mine);
@@ -394,13 +469,17 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_cons
                             t[1 + (i & 2)] = fmaxf(fmaxf(t[1 + (i & 2)], s1[i]), s1[i + 1]);
                         }
                     }
+                    const TileInfo ti = info[(it0 + j) % kInfos];
+                    // (never below the smallest normal number: a hidden token's -infinity stays that)
+                    const float scale = fmaxf(row_scale * ti.k, 1.17549435e-38f);
                     const float top = fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3])) * scale;
                     const bool rise = valid && (top > m + kRise || m == -INFINITY);
-                    if (__any_sync(0xffffffffu, rise)) {
+                    if (__any_sync(0xffffffffu, rise || ti.v > item_v)) {
                         const float mn = rise ? fmaxf(m, top) : m;
-                        const float f = mn == -INFINITY ? 1.f : ex2(m - mn);
+                        float f = mn == -INFINITY ? 1.f : ex2(m - mn);
                         m = mn;
                         l *= f;
+                        if (ti.v > item_v) f *= item_v / ti.v, item_v = ti.v;
                         if (j > 0) {   // every earlier product into O is done: s_full came after them
 #pragma unroll 1
                             for (int c = 0; c < D / 32; ++c) {
@@ -413,10 +492,10 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_cons
                         }
                     }
                     const float base = m == -INFINITY ? 0.f : m;
-                    const float2 scale2 = make_float2(scale, scale), base2 = make_float2(-base, -base);
+                    const float2 scale2 = make_float2(scale, scale), base2 = make_float2(ti.lift - base, ti.lift - base);
                     float2 sum0 = make_float2(0.f, 0.f), sum1 = sum0;
                     if (__any_sync(0xffffffffu, fabsf(base) > kFar)) {
-                        sum0.x = far_weights(trow + a * 128, seen, scale, base);
+                        sum0.x = far_weights(trow + a * 128, seen, scale, base, ti.lift);
                     } else {
 #pragma unroll
                         for (int half = 0; half < 2; ++half) {
@@ -428,13 +507,13 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_cons
                                 float2 g = __ffma2_rn(make_float2(s1[2 * i], s1[2 * i + 1]), scale2, base2);
                                 e = make_float2(ex2(e.x), ex2(e.y)), g = make_float2(ex2(g.x), ex2(g.y));
                                 sum0 = __fadd2_rn(sum0, e), sum1 = __fadd2_rn(sum1, g);
-                                w0[i] = pack2(e.x, e.y), w1[i] = pack2(g.x, g.y);
+                                w0[i] = half2(e.x, e.y), w1[i] = half2(g.x, g.y);
                             }
                             tmem_st16(trow + a * 128 + 32 * half, w0);
                             tmem_st16(trow + a * 128 + 32 * half + 16, w1);
                         }
                     }
-                    l += (sum0.x + sum0.y) + (sum1.x + sum1.y);
+                    l += ((sum0.x + sum0.y) + (sum1.x + sum1.y)) * ti.drop;
                     tmem_st_wait();
                 }
                 tc_fence_before();
@@ -448,7 +527,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_cons
             }
             if (!busy) continue;
             const bool some = l != 0.f, whole = x.whole();
-            const float inv = some ? 1.f / l : 0.f;
+            const float unit = item_v * 0.0078125f;   // of O: 2^-kLift
+            const float inv = some ? unit / l : 0.f;
             const int64_t part = x.slot() * kTcRows + rr;
             if (valid && !whole) p.part_ml[part] = make_float2(m, l);
             if (valid && whole && p.lse) p.lse[at_o] = some ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
@@ -478,7 +558,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_cons
                     for (int i = 0; i < 32; i += 8) {
                         uint32_t u[8];
 #pragma unroll
-                        for (int k = 0; k < 8; ++k) u[k] = __float_as_uint(o[i + k]);
+                        for (int k = 0; k < 8; ++k) u[k] = __float_as_uint(o[i + k] * unit);
                         store32(dst + i, u, true);
                     }
                 }

@@ -50,9 +50,6 @@ using tc::umma_ss;
 using tc::umma_ts;
 using tcu::cols_step;
 using tcu::elect_one;
-using tcu::ex2;
-using tcu::far_weights;
-using tcu::kFar;
 using tcu::pack2;
 using tcu::rows_step;
 using tcu::store32;
@@ -63,6 +60,11 @@ using tcu::warp_wait_bar;
 constexpr int kRows = 128;   // rows of a tile
 constexpr int kKeys = 128;   // tokens of a tile
 constexpr float kRise = 8.f; // O is rescaled when a maximum has risen by more than this (log2)
+// A weight's exponent is score * scale - m in one rounding, but m is a product already rounded: for the largest score its
+// rounding error is left, half a step of m, 16 at 2^28 and past what an exponential holds from 2^31 on.  Rows further from zero
+// than this round the product by itself first.
+constexpr float kFar = 268435456.f;
+
 template <int D, int NT>
 struct Cfg {
     static constexpr int kTile = kKeys * D * 2;                            // bytes of a K, V or Q tile
@@ -78,6 +80,11 @@ struct Cfg {
     static_assert(kSmem <= 232448 / (NT == 1 ? 2 : 1) - (NT == 1 ? 1024 : 0), "shared memory");
 };
 
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
 __device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* tm, int x, int y, int z, int w, uint64_t* bar) {
     asm volatile(
         "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], "
@@ -126,6 +133,28 @@ __device__ __forceinline__ Item item_at(const Params& p, int item, int pre_items
     x.n1 = (x.hi1 - x.lo1 + kKeys - 1) / kKeys;
     x.n_tiles = x.n1 + (x.hi2 - x.lo2 + kKeys - 1) / kKeys;
     return x;
+}
+
+// The weights of a tile's row, over its own scores in TMEM, for rows far from zero; returns their sum.  A function by itself:
+// inlined, it made the kernel 4 % slower where no row is far (turns of 16 x 256 tokens: 806 us against 778), a call 1 % (787).
+__device__ __noinline__ float far_weights(uint32_t taddr, int seen, float scale, float base) {
+    float sum = 0.f;
+#pragma unroll 1
+    for (int c = 0; c < kKeys / 32; ++c) {
+        float x[32];
+        uint32_t w[16];
+        tmem_ld32(taddr + 32 * c, x);
+#pragma unroll
+        for (int i = 0; i < 32; ++i) {
+            const float y = __fsub_rn(__fmul_rn(x[i], scale), base);
+            x[i] = 32 * c + i < seen ? ex2(y) : 0.f;
+            sum += x[i];
+        }
+#pragma unroll
+        for (int i = 0; i < 16; ++i) w[i] = pack2(x[2 * i], x[2 * i + 1]);
+        tmem_st16(taddr + 16 * c, w);
+    }
+    return sum;
 }
 
 template <int D, int NT>

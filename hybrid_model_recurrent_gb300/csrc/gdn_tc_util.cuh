@@ -64,40 +64,5 @@ __device__ __forceinline__ void store32(void* p, const uint32_t (&x)[8], bool wi
     }
 }
 
-__device__ __forceinline__ float ex2(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-
-// ---- softmax of a tile's row ----
-
-// A weight's exponent is score * scale - m in one rounding, but m is a product already rounded: for the largest score its
-// rounding error is left, half a step of m, 16 at 2^28 and past what an exponential holds from 2^31 on.  Rows further from zero
-// than this round the product by itself first.
-constexpr float kFar = 268435456.f;
-
-// The weights of a tile's row (128 tokens), over its own scores in TMEM, for rows far from zero; returns their sum.  A function by
-// itself: inlined, it made the prefix kernel 4 % slower where no row is far (turns of 16 x 256 tokens: 806 us against 778), a call 1 % (787).
-static __device__ __noinline__ float far_weights(uint32_t taddr, int seen, float scale, float base) {
-    float sum = 0.f;
-#pragma unroll 1
-    for (int c = 0; c < 128 / 32; ++c) {
-        float x[32];
-        uint32_t w[16];
-        tc::tmem_ld32(taddr + 32 * c, x);
-#pragma unroll
-        for (int i = 0; i < 32; ++i) {
-            const float y = __fsub_rn(__fmul_rn(x[i], scale), base);
-            x[i] = 32 * c + i < seen ? ex2(y) : 0.f;
-            sum += x[i];
-        }
-#pragma unroll
-        for (int i = 0; i < 16; ++i) w[i] = pack2(x[2 * i], x[2 * i + 1]);
-        tc::tmem_st16(taddr + 16 * c, w);
-    }
-    return sum;
-}
-
 }  // namespace tcu
 }  // namespace gdn

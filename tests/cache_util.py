@@ -57,11 +57,12 @@ def row_values(c, r, n, layer=0):
     return [x[:, kv].permute(0, 2, 1, 3).reshape(-1, x.shape[2], x.shape[4])[:n] for kv in (0, 1)]   # x [pages, 2, H, page, D]
 
 
-def check_attention(c, q, cu, *, rows=None, layer=0, scale=None, weight_step=None, lens=None, **kw):
+def check_attention(c, q, cu, *, rows=None, layer=0, scale=None, cut=0.0, lens=None, **kw):
     """The call's outputs against the definition in 64 bits.  Tolerances (u = 2^-24): a score (times log2 e) is a sum of D
     products and three scalings, off by e = (D + 6) u scale sum |q||k| + 6 u |x|, and fp32 queries by 2^-22 of sum |q||k| more;
-    a weight by 2 e + 2^-21 and its rounding (half a step: 2^-11 in f16, 2^-22 in two, 2^-8 in bf16; below 2^-25 of the
-    largest lifted one, 2^-36 of it, in f16); numerator and denominator add N terms; the output is rounded once."""
+    a weight by 2 e + 2^-21 and its rounding (half a step: 2^-11 in f16, 2^-22 in two; at least 2^-32 of the largest: half
+    of f16's last step where that one is held as 2^7); numerator and denominator add N terms; the output is rounded once.
+    `cut`: what blocks far below the largest of their tile may lose, relative to the largest value (tensor cores: 2^-24)."""
     T, Hq, D = q.shape
     H = c.pages.shape[3]
     G = Hq // H
@@ -71,7 +72,7 @@ def check_attention(c, q, cu, *, rows=None, layer=0, scale=None, weight_step=Non
     scale = D ** -0.5 if scale is None else scale
     bf = q.dtype == torch.bfloat16
     out_step = 2.0 ** -8 if bf else U
-    weight_step = weight_step or (2.0 ** -11 if bf else 2.0 ** -22)
+    weight_step = 2.0 ** -11 if bf else 2.0 ** -22
     ends = cu.tolist()
     lens = c.lens.tolist() if lens is None else lens
     at = list(range(len(ends) - 1)) if rows is None else rows.tolist()
@@ -99,7 +100,7 @@ def check_attention(c, q, cu, *, rows=None, layer=0, scale=None, weight_step=Non
         rel = 2 * (2 * e + 2.0 ** -21 + N * U) + weight_step
         vmax = v.abs().amax((0, 2))[None, :, None]
         want = torch.einsum("ihgk,khd->ihgd", p, v)
-        tol = rel[..., None] * torch.einsum("ihgk,khd->ihgd", p, v.abs()) + (N * 2.0 ** -36 * vmax)[..., None]
+        tol = rel[..., None] * torch.einsum("ihgk,khd->ihgd", p, v.abs()) + ((N * 2.0 ** -32 + cut) * vmax)[..., None]
         tol = tol + out_step * (want.abs() + tol) + 1e-37
         off = (o[live] - want).abs()
         assert torch.isfinite(o[live]).all(), b

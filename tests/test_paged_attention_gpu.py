@@ -27,9 +27,12 @@ def cu_of(new):
     return ints(*out)
 
 
+TC = dict(cut=2.0 ** -24)
+
+
 def step_of(dtype, D, rows):
-    """The rounding step of the weights: bf16 on the tensor cores, which take many rows of bf16."""
-    return dict(weight_step=2.0 ** -8) if dtype == BF and D >= 64 and rows > 32 else {}
+    """The tensor cores take many rows of bf16."""
+    return TC if dtype == BF and D >= 64 and rows > 32 else {}
 
 
 def queries(T, Hq, D, dtype, seed=1, gain=1.0):
@@ -227,9 +230,6 @@ def test_results_do_not_change():
     for _ in range(5):
         r = gdn.gdn_paged_attention(q, c, ints(0, 10, 20, 30))
         assert torch.equal(r["o"], first["o"]) and torch.equal(r["lse"], first["lse"])
-
-
-TC = dict(weight_step=2.0 ** -8)   # rows of many queries in bf16: weights rounded to bf16
 
 
 @pytest.mark.parametrize("D", [64, 128])
