@@ -7,13 +7,11 @@
 // than 2^8.  Scores, statistics and sums are fp32; the weights are rounded to f16 for the product (half a step, 2^-11 of each).
 //
 // All operands are f16, which holds e4m3 exactly and takes one conversion for two values.  What f16 lacks in range is carried
-// beside it, by powers of two that cost nothing a value: a row of Q is brought to [2^14, 2^15), a tile's keys and values
-// are taken relative to the largest scale of their blocks (the blocks of a tile that differ are multiplied by the ratio;
-// below 2^-24 a block counts as zeros).  The keys' scale joins the row's in the exponent; the values' goes into it too,
-// relative to the largest of the item so far (16 powers of two at most: l is summed from the same weights), and raising
-// that one rescales O as a risen maximum does.
-// (With bf16 operands, which take the blocks' scales as they are, the three warps below made two conversions and a product
-// for each value, 40 instructions for 16 of them, and a tile took 10 k cycles; without that arithmetic 5.7 k.)
+// beside it, by factors that cost nothing a value: a row of Q is brought to [2^14, 2^15) by a power of two, the scale of
+// the keys' block joins that of the row in the exponent, the scale of the values' block goes into it too, relative to the
+// largest of the item so far (and is taken out again where l is summed); raising that one rescales O as a risen maximum does.
+// (With bf16 operands the three warps below made two conversions and a product for each value, and a tile took 10 k cycles; a product
+// of f16 pairs for blocks that differ within a tile took as long as conversion and copies together.)
 //
 // Bulk copies bring the pages' bytes (a block is contiguous) into a ring of their own, three warps convert them and write
 // the swizzled tiles that the products read.  Tokens behind what the rows see are written as zeros, whatever the page holds
@@ -62,13 +60,14 @@ constexpr int kRows = 128;    // rows of a tile
 constexpr int kKeys = kTcUnit;
 constexpr float kRise = 8.f;  // O is rescaled when a maximum has risen by more than this (log2)
 constexpr float kLift = 7.f;  // log2 of a weight at the maximum: with the rise 2^15 in f16
-constexpr int kLow = 16;      // powers of two that a tile's values may lie below the item's largest before they are cut
 constexpr int kConv = 3;      // converting warps
-constexpr int kInfos = 8;     // tiles whose scales are kept: more than the converting warps can run ahead
+constexpr int kInfos = 4;     // tiles whose scales are kept: the converting warps are at most 3 ahead of the rows' reading
 // A weight's exponent is score * scale - m in one rounding, but m is a product already rounded: for the largest score its
 // rounding error is left, half a step of m, 16 at 2^28 and past what an exponential holds from 2^31 on.  Rows further from zero
 // than this round the product by itself first.
 constexpr float kFar = 268435456.f;
+// Factors of scores are not below the smallest normal number: a hidden token's -infinity stays that.
+constexpr float kTiny = 1.17549435e-38f;
 constexpr int kThreads = 384;
 
 template <int D>
@@ -79,11 +78,10 @@ struct Cfg {
     static constexpr int kRing = 2 * kTile;                   // after the Q tiles
     static constexpr int kRaw = kRing + ST * kTile;
     static constexpr int kBar = kRaw + RS * kTile / 2;
-    static constexpr int kCum = kBar + 512;                   // units before each request [B + 1]
+    static constexpr int kCum = kBar + 1024;                  // units before each request [B + 1]
     static constexpr int bytes(int B) { return kCum + (B + 1) * 4 + 1024; }
     static constexpr uint32_t kO = 256;                       // TMEM: S of each row tile, then O of each
-    // pieces of 8 tokens x 64 bytes, 16 bytes a lane
-    static constexpr int kPieces = 16 * D / 64, kOwn = (kPieces + kConv - 1) / kConv;
+    static constexpr int kOwn = (kKeys / 8 + kConv - 1) / kConv;   // groups of 8 tokens that a warp converts
     static_assert(bytes(kMaxBatch) <= 232448, "shared memory");
 };
 
@@ -99,6 +97,12 @@ __device__ __forceinline__ uint32_t half2(float a, float b) {
 // instruction descriptor of kind::f16: D fp32, A and B f16, M = 128
 __host__ __device__ constexpr uint32_t idesc_f16(int N, bool b_mn) { return idesc(N, false, b_mn) & ~((1u << 7) | (1u << 10)); }
 
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8]) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(r[0]), "r"(r[1]),
+                 "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+                 : "memory");
+}
+
 // 16 e4m3 as f16
 __device__ __forceinline__ void widen16(const uint4& u, uint32_t (&y)[8]) {
     const uint32_t w[4] = {u.x, u.y, u.z, u.w};
@@ -109,15 +113,16 @@ __device__ __forceinline__ void widen16(const uint4& u, uint32_t (&y)[8]) {
             : "r"(w[i]));
 }
 
-// What the rows need to know of a tile: the largest scale of its keys' blocks, the item's largest of the values so far (a power of
-// two), the log2 of a weight at the maximum, and the weight's inverse.
+// What the rows need to know of a tile: for each 16 of its tokens (a page has as many at least) the scale of the keys, the log2
+// of a weight at the maximum, and that weight's inverse; the largest scale of the item's values so far (a power of two).
 struct TileInfo {
-    float k, v, lift, drop;
+    float4 part[kKeys / 16];
+    float v, unused[3];
 };
 
 // The weights of a tile's row, over its own scores in TMEM, for rows far from zero; returns their sum.  A function by itself, so
 // that the loop of every other row stays small.
-__device__ __noinline__ float far_weights(uint32_t taddr, int seen, float scale, float base, float lift) {
+__device__ __noinline__ float far_weights(uint32_t taddr, int seen, float row_scale, float base, const TileInfo& ti) {
     float sum = 0.f;
 #pragma unroll 1
     for (int c = 0; c < kKeys / 32; ++c) {
@@ -126,9 +131,10 @@ __device__ __noinline__ float far_weights(uint32_t taddr, int seen, float scale,
         tmem_ld32(taddr + 32 * c, x);
 #pragma unroll
         for (int i = 0; i < 32; ++i) {
-            const float y = __fsub_rn(__fmul_rn(x[i], scale), base);
-            x[i] = 32 * c + i < seen ? ex2(y + lift) : 0.f;
-            sum += x[i];
+            const float4 f = ti.part[2 * c + i / 16];
+            const float y = __fsub_rn(__fmul_rn(x[i], fmaxf(row_scale * f.x, kTiny)), base);
+            x[i] = 32 * c + i < seen ? ex2(y + f.y) : 0.f;
+            sum += x[i] * f.z;
         }
 #pragma unroll
         for (int i = 0; i < 16; ++i) w[i] = half2(x[2 * i], x[2 * i + 1]);
@@ -156,8 +162,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_cons
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tslot + 1);
     int* s_scan = reinterpret_cast<int*>(tslot + 2);
     int* issued = s_scan + kThreads / 32;                            // tiles whose copies were issued
-    TileInfo* info = reinterpret_cast<TileInfo*>(smem + F::kBar + 512 - sizeof(TileInfo) * kInfos);
-    static_assert((2 * F::ST + 2 * F::RS + 9) * 8 + 8 + kThreads / 32 * 4 + 4 + sizeof(TileInfo) * kInfos <= 512, "barrier area");
+    TileInfo* info = reinterpret_cast<TileInfo*>(smem + F::kBar + 1024 - sizeof(TileInfo) * kInfos);
+    static_assert((2 * F::ST + 2 * F::RS + 9) * 8 + 8 + kThreads / 32 * 4 + 4 + sizeof(TileInfo) * kInfos <= 1024, "barrier area");
     int* s_cum = reinterpret_cast<int*>(smem + F::kCum);
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -267,11 +273,18 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_cons
             const int mine = warp - 9, sub = lane >> 2, quad = lane & 3;
             const int64_t block = (int64_t)p.c.page * D;
             const int per_tile = kKeys >> p.c.page_log2;   // pages of a tile
-            auto page_id = [&](const int32_t* table, int t) {
-                const int id = __ldg(table + (t >> p.c.page_log2));
-                if ((unsigned)id < (unsigned)p.c.N) return id;
-                atomicOr(p.status, STATUS_BAD_INDEX);
-                return 0;
+            // A warp converts the tokens 8 g .. 8 g + 7 for every third g, 64 bytes of a token by four lanes.  At width 128 odd
+            // tokens take their halves the other way round: a quarter of a warp then meets every bank once, reading and writing.
+            constexpr int kHalves = D / 64;
+            const int turned = kHalves == 2 ? sub & 1 : 0;
+            const int from = (8 * mine + sub) * D + quad * 16, to = (8 * mine + sub) * 128;
+            const int chunk0 = ((2 * quad) ^ sub) << 4, chunk1 = ((2 * quad + 1) ^ sub) << 4;   // (token & 7 = sub)
+            auto checked = [&](int id) {   // a table's entry, where it is used
+                if ((unsigned)id >= (unsigned)p.c.N) {
+                    atomicOr(p.status, STATUS_BAD_INDEX);
+                    id = 0;
+                }
+                return id;
             };
             bool ok = true;
             int seq = 0;
@@ -281,64 +294,69 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_cons
                 const int n = tiles_of(x);
                 if (n == 0) continue;
                 const int32_t* table = p.c.table + (int64_t)x.rq.row * p.c.W;   // (a row without tokens has no tiles)
-                // the page of tile j that this lane copies, and the one of its tokens 8 l .. 8 l + 7 for the scales; -1: none
-                auto copied = [&](int j) {
-                    const int t = x.lo + j * kKeys + (lane << p.c.page_log2);
-                    return lane < per_tile && j < n && t < x.hi ? page_id(table, t) : -1;
+                // this lane's page of tile j to copy, and the one of its tokens 16 l .. 16 l + 15 for their scales
+                auto copies = [&](int j) { return lane < per_tile && j < n && x.lo + j * kKeys + (lane << p.c.page_log2) < x.hi; };
+                auto holds = [&](int j) { return lane < 8 && j < n && x.lo + j * kKeys + 16 * lane < x.hi; };
+                // (asked for by name where they stand, a tile before their use: the compiler moved plain loads down to it)
+                auto load = [](const void* a) {
+                    uint32_t y;
+                    asm volatile("ld.global.nc.u32 %0, [%1];" : "=r"(y) : "l"(a));
+                    return y;
                 };
-                auto scaled = [&](int j) {
-                    const int t = x.lo + j * kKeys + 8 * lane;
-                    return lane < 16 && j < n && t < x.hi ? page_id(table, t) : -1;
+                auto copied = [&](int j) { return copies(j) ? (int)load(table + ((x.lo + j * kKeys) >> p.c.page_log2) + lane) : 0; };
+                auto held = [&](int j) { return holds(j) ? (int)load(table + ((x.lo + j * kKeys + 16 * lane) >> p.c.page_log2)) : 0; };
+                auto scale_of = [&](int j, int id, int kv) {
+                    return holds(j) ? __uint_as_float(load(p.c.scales + ((int64_t)checked(id) * 2 + kv) * p.c.Hkv + x.h)) : 0.f;
                 };
-                auto scale_of = [&](int id, int kv) {
-                    return id >= 0 ? __ldg(p.c.scales + ((int64_t)id * 2 + kv) * p.c.Hkv + x.h) : 0.f;
-                };
-                // ring entry `e` of all: keys or values of a tile of this item, whose pages the lanes hold
-                auto copy = [&](int e, int id, int kv) {
+                // ring entry `e` of all: keys or values of tile j, whose pages the lanes hold
+                auto copy = [&](int e, int j, int id, int kv) {
                     if (p.stall_after >= 0 && e / 2 >= p.stall_after) return false;   // testing hook
                     if (e >= F::RS && !warp_wait(&raw_empty[e % F::RS], e / F::RS - 1)) return false;
-                    const int pages = __popc(__ballot_sync(0xffffffffu, id >= 0));
+                    const int pages = __popc(__ballot_sync(0xffffffffu, copies(j)));
                     if (lane == 0) {
                         mbar_arrive_expect_tx(&raw_full[e % F::RS], (uint32_t)(pages * block));
                         *issued = e + 1;
                     }
                     __syncwarp();
-                    if (id >= 0)
+                    if (copies(j))
                         asm volatile(
                             "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
                                 sbase + F::kRaw + (uint32_t)(e % F::RS) * (F::kTile / 2) + (uint32_t)(lane * block)),
-                            "l"(p.c.pages + (((int64_t)id * 2 + kv) * p.c.Hkv + x.h) * block), "r"((uint32_t)block),
+                            "l"(p.c.pages + (((int64_t)checked(id) * 2 + kv) * p.c.Hkv + x.h) * block), "r"((uint32_t)block),
                             "r"(smem_addr(&raw_full[e % F::RS]))
                             : "memory");
                     return true;
                 };
-                auto convert = [&](int e, float ratio, int t0) {   // (a lane's ratio is that of its 8 tokens' block)
+                auto convert = [&](int e, int t0) {
                     if (!warp_wait(&raw_full[e % F::RS], e / F::RS)) return false;
                     if (e >= F::ST && !warp_wait(&empty[e % F::ST], e / F::ST - 1)) return false;
-                    const unsigned char* raw = smem + F::kRaw + (e % F::RS) * (F::kTile / 2);
-                    unsigned char* tile = smem + F::kRing + (e % F::ST) * F::kTile;
-                    const bool part = x.hi - t0 < kKeys;
-                    const uint32_t ratio2 = half2(ratio, ratio);
-                    const bool same = __all_sync(0xffffffffu, ratio == 1.f || lane >= 16);
+                    const unsigned char* raw = smem + F::kRaw + (e % F::RS) * (F::kTile / 2) + from;
+                    unsigned char* tile = smem + F::kRing + (e % F::ST) * F::kTile + to;
+                    const int left = x.hi - t0 - 8 * mine - sub;   // tokens that are seen from this lane's first on
+                    auto read = [&](int i, uint4 (&u)[kHalves]) {
+#pragma unroll
+                        for (int h = 0; h < kHalves; ++h)
+                            u[h] = *reinterpret_cast<const uint4*>(raw + i * (8 * kConv) * D + (h ^ turned) * 64);
+                    };
+                    uint4 u[kHalves], next[kHalves];
+                    read(0, u);
 #pragma unroll
                     for (int i = 0; i < F::kOwn; ++i) {
-                        const int piece = mine + kConv * i;
-                        if (piece >= F::kPieces) break;
-                        // 8 tokens x 64 bytes; at width 128 odd tokens take the other half, for the banks
-                        const int group = D == 128 ? piece >> 1 : piece, half = D == 128 ? (piece ^ sub) & 1 : 0;
-                        const int row = 8 * group + sub;
-                        uint4 u = *reinterpret_cast<const uint4*>(raw + row * D + half * 64 + quad * 16);
-                        if (part && t0 + row >= x.hi) u = make_uint4(0, 0, 0, 0);
-                        uint32_t y[8];
-                        widen16(u, y);
-                        if (!same) {
-                            const uint32_t f = __shfl_sync(0xffffffffu, ratio2, group);
+                        if (mine + kConv * i >= 16) break;
+                        if (i + 1 < F::kOwn && mine + kConv * (i + 1) < 16) read(i + 1, next);
 #pragma unroll
-                            for (int k = 0; k < 8; ++k) asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(y[k]) : "r"(y[k]), "r"(f));
+                        for (int h = 0; h < kHalves; ++h) {
+                            uint32_t y[8];
+                            widen16(u[h], y);
+                            if (8 * kConv * i >= left) {
+#pragma unroll
+                                for (int k = 0; k < 8; ++k) y[k] = 0;
+                            }
+                            unsigned char* row = tile + i * (8 * kConv) * 128 + (h ^ turned) * 16384;
+                            *reinterpret_cast<uint4*>(row + chunk0) = make_uint4(y[0], y[1], y[2], y[3]);
+                            *reinterpret_cast<uint4*>(row + chunk1) = make_uint4(y[4], y[5], y[6], y[7]);
+                            u[h] = next[h];
                         }
-                        unsigned char* to = tile + half * 16384 + row * 128;   // (row & 7 = sub)
-                        *reinterpret_cast<uint4*>(to + (((2 * quad) ^ sub) << 4)) = make_uint4(y[0], y[1], y[2], y[3]);
-                        *reinterpret_cast<uint4*>(to + (((2 * quad + 1) ^ sub) << 4)) = make_uint4(y[4], y[5], y[6], y[7]);
                     }
                     proxy_fence();
                     __syncwarp();
@@ -346,34 +364,35 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_cons
                     return true;
                 };
                 // the copies run RS - 1 entries ahead of the conversion
-                int idc = mine == 0 ? copied(0) : -1, idc1 = mine == 0 ? copied(1) : -1;   // of tile `ahead` / 2 and the next
+                int idc = mine == 0 ? copied(0) : 0, idc1 = mine == 0 ? copied(1) : 0;   // of tile `ahead` / 2 and the next
                 int ahead = 0;
                 auto advance = [&] {
                     if (mine != 0 || ahead >= 2 * n) return true;
-                    const bool good = copy(seq + ahead, idc, ahead & 1);
+                    const bool good = copy(seq + ahead, ahead / 2, idc, ahead & 1);
                     if (ahead & 1) idc = idc1, idc1 = copied(ahead / 2 + 2);
                     ++ahead;
                     return good;
                 };
-                const int id0 = scaled(0);
-                int id1 = scaled(1);
-                float ks = scale_of(id0, 0), vs = scale_of(id0, 1);
+                const int id0 = held(0);
+                int id1 = held(1);
+                float ks = scale_of(0, id0, 0), vs = scale_of(0, id0, 1);
                 for (int i = 0; ok && i < F::RS - 1; ++i) ok = advance();
-                auto largest = [](float y) { return __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(y))); };
                 float item_v = 0.f;   // the largest scale of the item's values so far, as a power of two
                 for (int j = 0; ok && j < n; ++j) {
-                    const int id2 = scaled(j + 2);
-                    const float ks1 = scale_of(id1, 0), vs1 = scale_of(id1, 1);
+                    const int id2 = held(j + 2);
+                    const float ks1 = scale_of(j + 1, id1, 0), vs1 = scale_of(j + 1, id1, 1);
                     const int t0 = x.lo + j * kKeys;
-                    const float tk = largest(ks), tv = largest(vs);
-                    item_v = fmaxf(item_v, __uint_as_float(__float_as_uint(tv) & 0x7f800000u));
-                    // the tile's values relative to a power of two, kLow below the item's at least
-                    const int low = min((int)(__float_as_uint(item_v) >> 23) - (int)(__float_as_uint(tv) >> 23), kLow);
-                    const float ref = item_v * __uint_as_float((uint32_t)(127 - low) << 23);
-                    if (mine == 0 && lane == 0) info[(seq / 2 + j) % kInfos] =
-                            {tk, item_v, kLift - (float)low, __uint_as_float((uint32_t)(127 - (int)kLift + low) << 23)};
-                    ok = advance() && convert(seq + 2 * j, tk > 0.f ? ks / tk : 0.f, t0) && advance() &&
-                         convert(seq + 2 * j + 1, ref > 0.f ? vs / ref : 0.f, t0);
+                    if (mine == 0) {
+                        const uint32_t top = __reduce_max_sync(0xffffffffu, __float_as_uint(vs));
+                        item_v = fmaxf(item_v, __uint_as_float(top & 0x7f800000u));
+                        // (far below the largest, where f16 holds nothing of it, the weight is still one for the sum)
+                        const float lift = kLift + (item_v > 0.f ? fmaxf(log2f(vs / item_v), -80.f) : 0.f);
+                        TileInfo& ti = info[(seq / 2 + j) % kInfos];
+                        if (lane < 8) ti.part[lane] = make_float4(ks, lift, exp2f(-lift), 0.f);
+                        if (lane == 0) ti.v = item_v;
+                        __syncwarp();
+                    }
+                    ok = advance() && convert(seq + 2 * j, t0) && advance() && convert(seq + 2 * j + 1, t0);
                     id1 = id2, ks = ks1, vs = vs1;
                 }
                 seq += 2 * n;
@@ -451,7 +470,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_cons
                     const int seen = valid ? vis - t0 : kKeys;
                     const bool hide = __any_sync(0xffffffffu, seen < kKeys);
                     float s[4][32];
-                    float t[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+                    const TileInfo& ti = info[(it0 + j) % kInfos];
+                    float top = -INFINITY;
 #pragma unroll
                     for (int half = 0; half < 2; ++half) {
                         float(&s0)[32] = s[2 * half], (&s1)[32] = s[2 * half + 1];
@@ -464,15 +484,14 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_cons
                             }
                         }
 #pragma unroll
-                        for (int i = 0; i < 32; i += 2) {
-                            t[0] = fmaxf(fmaxf(t[0], s0[i]), s0[i + 1]);
-                            t[1 + (i & 2)] = fmaxf(fmaxf(t[1 + (i & 2)], s1[i]), s1[i + 1]);
+                        for (int c = 0; c < 4; ++c) {   // 16 tokens each
+                            const float* y = s[2 * half + c / 2] + 16 * (c & 1);
+                            float t = fmaxf(y[0], y[1]);
+#pragma unroll
+                            for (int i = 2; i < 16; i += 2) t = fmaxf(fmaxf(t, y[i]), y[i + 1]);
+                            top = fmaxf(top, t * fmaxf(row_scale * ti.part[4 * half + c].x, kTiny));
                         }
                     }
-                    const TileInfo ti = info[(it0 + j) % kInfos];
-                    // (never below the smallest normal number: a hidden token's -infinity stays that)
-                    const float scale = fmaxf(row_scale * ti.k, 1.17549435e-38f);
-                    const float top = fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3])) * scale;
                     const bool rise = valid && (top > m + kRise || m == -INFINITY);
                     if (__any_sync(0xffffffffu, rise || ti.v > item_v)) {
                         const float mn = rise ? fmaxf(m, top) : m;
@@ -492,28 +511,29 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_cons
                         }
                     }
                     const float base = m == -INFINITY ? 0.f : m;
-                    const float2 scale2 = make_float2(scale, scale), base2 = make_float2(ti.lift - base, ti.lift - base);
                     float2 sum0 = make_float2(0.f, 0.f), sum1 = sum0;
                     if (__any_sync(0xffffffffu, fabsf(base) > kFar)) {
-                        sum0.x = far_weights(trow + a * 128, seen, scale, base, ti.lift);
+                        sum0.x = far_weights(trow + a * 128, seen, row_scale, base, ti);
                     } else {
 #pragma unroll
-                        for (int half = 0; half < 2; ++half) {
-                            float(&s0)[32] = s[2 * half], (&s1)[32] = s[2 * half + 1];
-                            uint32_t w0[16], w1[16];
+                        for (int c = 0; c < 8; ++c) {
+                            const float* y = s[c / 2] + 16 * (c & 1);
+                            const float4 f = ti.part[c];
+                            const float fx = fmaxf(row_scale * f.x, kTiny), fb = f.y - base;
+                            const float2 scale2 = make_float2(fx, fx), base2 = make_float2(fb, fb), drop2 = make_float2(f.z, f.z);
+                            uint32_t w[8];
 #pragma unroll
-                            for (int i = 0; i < 16; ++i) {
-                                float2 e = __ffma2_rn(make_float2(s0[2 * i], s0[2 * i + 1]), scale2, base2);
-                                float2 g = __ffma2_rn(make_float2(s1[2 * i], s1[2 * i + 1]), scale2, base2);
-                                e = make_float2(ex2(e.x), ex2(e.y)), g = make_float2(ex2(g.x), ex2(g.y));
-                                sum0 = __fadd2_rn(sum0, e), sum1 = __fadd2_rn(sum1, g);
-                                w0[i] = half2(e.x, e.y), w1[i] = half2(g.x, g.y);
+                            for (int i = 0; i < 8; ++i) {
+                                float2 e = __ffma2_rn(make_float2(y[2 * i], y[2 * i + 1]), scale2, base2);
+                                e = make_float2(ex2(e.x), ex2(e.y));
+                                if (i & 1) sum1 = __ffma2_rn(e, drop2, sum1);
+                                else sum0 = __ffma2_rn(e, drop2, sum0);
+                                w[i] = half2(e.x, e.y);
                             }
-                            tmem_st16(trow + a * 128 + 32 * half, w0);
-                            tmem_st16(trow + a * 128 + 32 * half + 16, w1);
+                            tmem_st8(trow + a * 128 + 8 * c, w);
                         }
                     }
-                    l += ((sum0.x + sum0.y) + (sum1.x + sum1.y)) * ti.drop;
+                    l += (sum0.x + sum0.y) + (sum1.x + sum1.y);
                     tmem_st_wait();
                 }
                 tc_fence_before();
