@@ -140,7 +140,7 @@ template <int RT, int UNIT>
 __device__ __forceinline__ int tile_units(const Request& q, int G, int tile) {
     return max(1, (tile_sees(q, G, RT, tile) + UNIT - 1) / UNIT);
 }
-// units of a request for one head
+// units of a request for one head (none without queries)
 template <int RT, int UNIT>
 __device__ __forceinline__ int head_units(const Request& q, int G) {
     int n = 0;
@@ -149,60 +149,87 @@ __device__ __forceinline__ int head_units(const Request& q, int G) {
     return n;
 }
 
-// Units before each request into s_cum[0 .. B], by all THREADS threads of a CTA; s_scan: THREADS / 32 ints.
+// Units before every 16th request into s_cum[0 .. ceil(B / 16)], by all THREADS threads of a CTA: a thread a request, so that the
+// loads of many go together.  The first CTA writes p.starts.
+constexpr int kGroup = 16, kMaxGroups = 4096 / kGroup;
 template <int THREADS, int RT, int UNIT>
-__device__ __forceinline__ void count_units(const PagedParams& p, int* s_cum, int* s_scan) {
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, B = p.t.B;
-    const int per = (B + THREADS - 1) / THREADS;
-    int sum = 0;
-    for (int i = 0; i < per; ++i) {
-        const int b = tid * per + i;
+__device__ __forceinline__ void count_units(const PagedParams& p, int* s_cum) {
+    const int tid = threadIdx.x, lane = tid & 31, B = p.t.B, groups = (B + kGroup - 1) / kGroup;
+    for (int g0 = 0; g0 < groups; g0 += THREADS / kGroup) {
+        const int g = g0 + tid / kGroup, b = g * kGroup + tid % kGroup;
+        int n = 0;
         if (b < B) {
             const Request q = request_at(p.c, p.t, b);
             if (q.bad && blockIdx.x == 0) atomicOr(p.status, STATUS_BAD_INDEX);
-            s_cum[b] = sum;
-            sum += head_units<RT, UNIT>(q, p.G) * p.c.Hkv;
+            n = head_units<RT, UNIT>(q, p.G) * p.c.Hkv;
         }
-    }
-    int y = sum;
+        int y = n;
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const int z = __shfl_up_sync(0xffffffffu, y, o);
-        if (lane >= o) y += z;
+        for (int o = 1; o < kGroup; o <<= 1) {
+            const int z = __shfl_up_sync(0xffffffffu, y, o, kGroup);
+            if (tid % kGroup >= o) y += z;
+        }
+        if (tid % kGroup == kGroup - 1 && g < groups) s_cum[g + 1] = y;
+        if (blockIdx.x == 0 && b < B) p.starts[b] = y - n;
     }
-    if (lane == 31) s_scan[warp] = y;
     __syncthreads();
-    int before = y - sum;
-    for (int w = 0; w < warp; ++w) before += s_scan[w];
-    for (int i = 0; i < per; ++i)
-        if (tid * per + i < B) s_cum[tid * per + i] += before;
-    if (tid == THREADS - 1) s_cum[B] = before + sum;
+    if (tid < 32) {
+        constexpr int PER = kMaxGroups / 32;
+        int sum = 0;
+        for (int i = 0; i < PER; ++i)
+            if (lane * PER + i < groups) sum += s_cum[lane * PER + i + 1];
+        int y = sum;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int z = __shfl_up_sync(0xffffffffu, y, o);
+            if (lane >= o) y += z;
+        }
+        y -= sum;
+        for (int i = 0; i < PER; ++i)
+            if (lane * PER + i < groups) y += s_cum[lane * PER + i + 1], s_cum[lane * PER + i + 1] = y;
+        if (lane == 0) s_cum[0] = 0;
+    }
     __syncthreads();
-    if (blockIdx.x == 0)
-        for (int i = tid; i <= B; i += THREADS) p.starts[i] = s_cum[i];
+    if (blockIdx.x == 0) {
+        for (int b = tid; b < B; b += THREADS) p.starts[b] += s_cum[b / kGroup];   // (its own: 16 threads a group, THREADS a round)
+        if (tid == 0) p.starts[B] = s_cum[groups];
+    }
 }
 
-// What a CTA does of one item, from unit x on: rows row0 .. of `rows` of the request, tokens lo .. hi.
+// What a CTA does of one item, from unit x on: rows row0 .. of `rows` of the request, tokens lo .. hi.  Called by whole warps.
 struct Segment {
     Request rq;
-    int b, h, row0, rows, lo, hi, u0, u1, units;
+    int h, row0, rows, lo, hi, u0, u1, units;
     __device__ __forceinline__ bool whole() const { return u0 == 0 && u1 == units; }
     __device__ __forceinline__ int64_t slot() const { return 2 * (int64_t)blockIdx.x + (u0 == 0); }
 };
 template <int RT, int UNIT>
 __device__ __forceinline__ Segment segment_at(const PagedParams& p, const int* s_cum, int x, int end) {
     Segment s;
-    int b = 0, top = p.t.B;   // cum[b] <= x < cum[top]
-    while (top - b > 1) {
-        const int mid = (b + top) >> 1;
-        if (s_cum[mid] <= x) b = mid;
+    int g = 0, top = (p.t.B + kGroup - 1) / kGroup;   // cum[g] <= x < cum[top]
+    while (top - g > 1) {
+        const int mid = (g + top) >> 1;
+        if (s_cum[mid] <= x) g = mid;
         else top = mid;
     }
-    s.b = b;
-    s.rq = request_at(p.c, p.t, b);
-    const int per_head = (s_cum[b + 1] - s_cum[b]) / p.c.Hkv, rest = x - s_cum[b];
-    s.h = rest / per_head;
-    s.u0 = rest - s.h * per_head;
+    // the requests of the group, a lane each; the one that unit x falls to
+    const int lane = threadIdx.x & 31, b = g * kGroup + lane;
+    Request q{-1, 0, 0, 0, false};
+    if (lane < kGroup && b < p.t.B) q = request_at(p.c, p.t, b);
+    const int per_head = head_units<RT, UNIT>(q, p.G), n = per_head * p.c.Hkv;
+    int after = n;
+#pragma unroll
+    for (int o = 1; o < kGroup; o <<= 1) {
+        const int z = __shfl_up_sync(0xffffffffu, after, o);
+        if (lane >= o) after += z;
+    }
+    const int rest = x - s_cum[g];
+    const int at = __ffs(__ballot_sync(0xffffffffu, lane < kGroup && rest < after)) - 1;
+    s.rq.row = __shfl_sync(0xffffffffu, q.row, at), s.rq.len = __shfl_sync(0xffffffffu, q.len, at);
+    s.rq.n = __shfl_sync(0xffffffffu, q.n, at), s.rq.first = __shfl_sync(0xffffffffu, q.first, at);
+    const int mine = rest - __shfl_sync(0xffffffffu, after - n, at), head = __shfl_sync(0xffffffffu, per_head, at);
+    s.h = mine / head;
+    s.u0 = mine - s.h * head;
     int tile = 0;
     for (;;) {
         s.units = tile_units<RT, UNIT>(s.rq, p.G, tile);

@@ -83,8 +83,8 @@ struct Cfg {
     static constexpr int kO = kQ + PARTS * MT * KW * 512;            // sums: [warps][MT][NT][4][32] fp32
     static constexpr int kMl = kO + kWarps * MT * NT * 512;          // m, l: [warps][RT] float2
     static constexpr int kQe = kMl + kWarps * RT * 8;                // factors of the rows [RT]
-    static constexpr int kCum = kQe + RT * 4 + 64;                   // units before each request [B + 1]
-    static constexpr int bytes(int B) { return kCum + (B + 1) * 4; }
+    static constexpr int kCum = kQe + RT * 4;                        // units before each group of requests
+    static constexpr int kSmem = kCum + (kMaxGroups + 1) * 4;
 };
 
 template <int D, typename T, int MT>
@@ -96,13 +96,12 @@ __global__ void __launch_bounds__(kWarps * 32, MT == 1 ? 3 : 2) paged_kernel(con
     float* s_o = reinterpret_cast<float*>(smem + F::kO);
     float2* s_ml = reinterpret_cast<float2*>(smem + F::kMl);
     float* s_f = reinterpret_cast<float*>(smem + F::kQe);
-    int* s_scan = reinterpret_cast<int*>(smem + F::kQe + RT * 4);
     int* s_cum = reinterpret_cast<int*>(smem + F::kCum);
     const Cache& c = p.c;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, q4 = lane & 3;
 
-    count_units<kWarps * 32, RT, kUnit>(p, s_cum, s_scan);
-    const int total = s_cum[p.t.B], share = (total + gridDim.x - 1) / gridDim.x;
+    count_units<kWarps * 32, RT, kUnit>(p, s_cum);
+    const int total = s_cum[(p.t.B + kGroup - 1) / kGroup], share = (total + gridDim.x - 1) / gridDim.x;
     int x = (int)min((int64_t)blockIdx.x * share, (int64_t)total);
     const int end = min(x + share, total);
 
@@ -490,9 +489,9 @@ template <int D, typename T, int MT>
 cudaError_t launch(const PagedParams& p, cudaStream_t s) {
     using F = Cfg<D, T, MT>;
     static std::atomic<int> optin[kMaxOptinDevices];
-    const cudaError_t e = smem_optin(reinterpret_cast<const void*>(paged_kernel<D, T, MT>), F::bytes(kMaxBatch), optin);
+    const cudaError_t e = smem_optin(reinterpret_cast<const void*>(paged_kernel<D, T, MT>), F::kSmem, optin);
     if (e != cudaSuccess) return e;
-    paged_kernel<D, T, MT><<<p.ctas, kWarps * 32, F::bytes(p.t.B), s>>>(p);
+    paged_kernel<D, T, MT><<<p.ctas, kWarps * 32, F::kSmem, s>>>(p);
     return cudaGetLastError();
 }
 template <int D, typename T>

@@ -61,7 +61,6 @@ constexpr int kKeys = kTcUnit;
 constexpr float kRise = 8.f;  // O is rescaled when a maximum has risen by more than this (log2)
 constexpr float kLift = 7.f;  // log2 of a weight at the maximum: with the rise 2^15 in f16
 constexpr int kConv = 3;      // converting warps
-constexpr int kInfos = 4;     // tiles whose scales are kept: the converting warps are at most 3 ahead of the rows' reading
 // A weight's exponent is score * scale - m in one rounding, but m is a product already rounded: for the largest score its
 // rounding error is left, half a step of m, 16 at 2^28 and past what an exponential holds from 2^31 on.  Rows further from zero
 // than this round the product by itself first.
@@ -73,16 +72,16 @@ constexpr int kThreads = 384;
 template <int D>
 struct Cfg {
     static constexpr int kTile = kKeys * D * 2;               // bytes of a K, V or Q tile
-    static constexpr int ST = D == 128 ? 3 : 6;               // K and V tiles in turn
-    static constexpr int RS = D == 128 ? 3 : 4;               // the same as bytes of the pages
+    static constexpr int ST = D == 128 ? 4 : 8;               // K and V tiles in turn
+    static constexpr int RS = D == 128 ? 4 : 8;               // halves of them as bytes of the pages
+    static constexpr int kHalf = kKeys / 2 * D;               // bytes of such a half
     static constexpr int kRing = 2 * kTile;                   // after the Q tiles
     static constexpr int kRaw = kRing + ST * kTile;
-    static constexpr int kBar = kRaw + RS * kTile / 2;
-    static constexpr int kCum = kBar + 1024;                  // units before each request [B + 1]
-    static constexpr int bytes(int B) { return kCum + (B + 1) * 4 + 1024; }
+    static constexpr int kBar = kRaw + RS * kHalf;
+    static constexpr int kInfos = ST == 4 ? 4 : 8;            // tiles described: V of ST / 2 tiles before is done when one is
+    static constexpr int kArea = ST == 4 ? 2048 : 3072;       // barriers, units before each group of requests, the descriptions
+    static constexpr int kSmem = kBar + kArea + 1024;
     static constexpr uint32_t kO = 256;                       // TMEM: S of each row tile, then O of each
-    static constexpr int kOwn = (kKeys / 8 + kConv - 1) / kConv;   // groups of 8 tokens that a warp converts
-    static_assert(bytes(kMaxBatch) <= 232448, "shared memory");
 };
 
 __device__ __forceinline__ float ex2(float x) {
@@ -146,6 +145,7 @@ __device__ __noinline__ float far_weights(uint32_t taddr, int seen, float row_sc
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_constant__ PagedParams p) {
     using F = Cfg<D>;
+    static_assert(F::kSmem <= 232448, "shared memory");
     extern __shared__ unsigned char smem_raw[];
     unsigned char* smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
     const uint32_t sbase = smem_addr(smem);
@@ -156,15 +156,14 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_cons
     uint64_t* q_ready = p_ready + 2;                                 // [2] an item's Q tile written
     uint64_t* o_full = q_ready + 2;                                  // [2] every product of an item done
     uint64_t* end_bar = o_full + 2;                                  // every product done
-    uint64_t* raw_full = end_bar + 1;                                // [RS] a tile's bytes landed
+    uint64_t* raw_full = end_bar + 1;                                // [RS] half a tile's bytes landed
     uint64_t* raw_empty = raw_full + F::RS;                          // [RS] and read by the converting warps
     uint32_t* tslot = reinterpret_cast<uint32_t*>(raw_empty + F::RS);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tslot + 1);
-    int* s_scan = reinterpret_cast<int*>(tslot + 2);
-    int* issued = s_scan + kThreads / 32;                            // tiles whose copies were issued
-    TileInfo* info = reinterpret_cast<TileInfo*>(smem + F::kBar + 1024 - sizeof(TileInfo) * kInfos);
-    static_assert((2 * F::ST + 2 * F::RS + 9) * 8 + 8 + kThreads / 32 * 4 + 4 + sizeof(TileInfo) * kInfos <= 1024, "barrier area");
-    int* s_cum = reinterpret_cast<int*>(smem + F::kCum);
+    int* issued = reinterpret_cast<int*>(tslot + 2);                 // halves whose copies were issued
+    int* s_cum = issued + 1;                                         // units before each group of requests
+    TileInfo* info = reinterpret_cast<TileInfo*>(smem + F::kBar + F::kArea - sizeof(TileInfo) * F::kInfos);
+    static_assert((2 * F::ST + 2 * F::RS + 9) * 8 + 12 + (kMaxGroups + 1) * 4 + sizeof(TileInfo) * F::kInfos <= F::kArea, "barrier area");
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const uint64_t limit = p.wait_limit_ns;
@@ -185,14 +184,14 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_cons
         *issued = 0;
         fence_barrier_init();
     }
-    count_units<kThreads, kTcRows, kTcUnit>(p, s_cum, s_scan);
+    count_units<kThreads, kTcRows, kTcUnit>(p, s_cum);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tbase = *tslot;
     auto warp_wait = [&](uint64_t* bar, int parity) { return warp_wait_bar(bar, (uint32_t)parity & 1u, abort_flag, limit); };
 
-    const int total = s_cum[p.t.B], share = (total + (int)gridDim.x - 1) / (int)gridDim.x;
+    const int total = s_cum[(p.t.B + kGroup - 1) / kGroup], share = (total + (int)gridDim.x - 1) / (int)gridDim.x;
     const int begin = (int)min((int64_t)blockIdx.x * share, (int64_t)total), end = min(begin + share, total);
 
     // Every role walks the CTA's items; an item of at most 128 rows takes one row tile, the two in turn, so that one tile's sums
@@ -269,15 +268,16 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_cons
             }
             if (elect_one()) umma_commit(end_bar);   // also after giving up: the end waits for the products in flight
         } else {
-            // ---- keys and values: copied (the first of the three warps, a lane a page) and converted ----
+            // ---- keys and values: copied (by the first of the three warps, a lane a page), and converted; the last one
+            // describes the tiles.  They go in halves of 64 tokens ----
             const int mine = warp - 9, sub = lane >> 2, quad = lane & 3;
+            const int piece_log2 = min(p.c.page_log2, 6), lanes = kKeys >> piece_log2;   // a page or half of one a lane
             const int64_t block = (int64_t)p.c.page * D;
-            const int per_tile = kKeys >> p.c.page_log2;   // pages of a tile
+            const uint32_t piece = (uint32_t)D << piece_log2;
             // A warp converts the tokens 8 g .. 8 g + 7 for every third g, 64 bytes of a token by four lanes.  At width 128 odd
             // tokens take their halves the other way round: a quarter of a warp then meets every bank once, reading and writing.
             constexpr int kHalves = D / 64;
             const int turned = kHalves == 2 ? sub & 1 : 0;
-            const int from = (8 * mine + sub) * D + quad * 16, to = (8 * mine + sub) * 128;
             const int chunk0 = ((2 * quad) ^ sub) << 4, chunk1 = ((2 * quad + 1) ^ sub) << 4;   // (token & 7 = sub)
             auto checked = [&](int id) {   // a table's entry, where it is used
                 if ((unsigned)id >= (unsigned)p.c.N) {
@@ -294,106 +294,117 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_cons
                 const int n = tiles_of(x);
                 if (n == 0) continue;
                 const int32_t* table = p.c.table + (int64_t)x.rq.row * p.c.W;   // (a row without tokens has no tiles)
-                // this lane's page of tile j to copy, and the one of its tokens 16 l .. 16 l + 15 for their scales
-                auto copies = [&](int j) { return lane < per_tile && j < n && x.lo + j * kKeys + (lane << p.c.page_log2) < x.hi; };
-                auto holds = [&](int j) { return lane < 8 && j < n && x.lo + j * kKeys + 16 * lane < x.hi; };
-                // (asked for by name where they stand, a tile before their use: the compiler moved plain loads down to it)
+                // (loaded by name where they stand, a tile before their use: the compiler moved plain loads down to it)
                 auto load = [](const void* a) {
                     uint32_t y;
                     asm volatile("ld.global.nc.u32 %0, [%1];" : "=r"(y) : "l"(a));
                     return y;
                 };
-                auto copied = [&](int j) { return copies(j) ? (int)load(table + ((x.lo + j * kKeys) >> p.c.page_log2) + lane) : 0; };
+                // the first warp: this lane's piece of tile j, whose page it holds
+                auto token = [&](int j) { return x.lo + j * kKeys + (lane << piece_log2); };
+                auto copies = [&](int j) { return lane < lanes && j < n && token(j) < x.hi; };
+                auto copied = [&](int j) { return copies(j) ? (int)load(table + (token(j) >> p.c.page_log2)) : 0; };
+                int idc = 0, idc1 = 0;   // pages of the tile that is copied, and of the next
+                if (mine == 0) idc = copied(0), idc1 = copied(1);
+                auto copy = [&](int c) {   // half c of the item: of keys, then of values, tile by tile
+                    const int r = 2 * seq + c, j = c >> 2;
+                    if (p.stall_after >= 0 && r / 4 >= p.stall_after) return false;   // testing hook
+                    if (r >= F::RS && !warp_wait(&raw_empty[r % F::RS], r / F::RS - 1)) return false;
+                    const bool mine_too = copies(j) && (lane >= lanes / 2) == ((c & 1) == 1);
+                    const uint32_t pieces = __popc(__ballot_sync(0xffffffffu, mine_too));
+                    if (lane == 0) {
+                        mbar_arrive_expect_tx(&raw_full[r % F::RS], pieces * piece);
+                        *issued = r + 1;
+                    }
+                    __syncwarp();
+                    if (mine_too)
+                        asm volatile(
+                            "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                                sbase + F::kRaw + (uint32_t)(r % F::RS) * F::kHalf + (uint32_t)(lane & (lanes / 2 - 1)) * piece),
+                            "l"(p.c.pages + (((int64_t)checked(idc) * 2 + (c >> 1 & 1)) * p.c.Hkv + x.h) * block +
+                                (int64_t)(token(j) & (p.c.page - 1)) * D),
+                            "r"(piece), "r"(smem_addr(&raw_full[r % F::RS]))
+                            : "memory");
+                    if ((c & 3) == 3) idc = idc1, idc1 = copied(j + 2);
+                    return true;
+                };
+                // the last warp: the scales of the tokens 16 l .. 16 l + 15 of tile j
+                auto holds = [&](int j) { return lane < 8 && j < n && x.lo + j * kKeys + 16 * lane < x.hi; };
                 auto held = [&](int j) { return holds(j) ? (int)load(table + ((x.lo + j * kKeys + 16 * lane) >> p.c.page_log2)) : 0; };
                 auto scale_of = [&](int j, int id, int kv) {
                     return holds(j) ? __uint_as_float(load(p.c.scales + ((int64_t)checked(id) * 2 + kv) * p.c.Hkv + x.h)) : 0.f;
                 };
-                // ring entry `e` of all: keys or values of tile j, whose pages the lanes hold
-                auto copy = [&](int e, int j, int id, int kv) {
-                    if (p.stall_after >= 0 && e / 2 >= p.stall_after) return false;   // testing hook
-                    if (e >= F::RS && !warp_wait(&raw_empty[e % F::RS], e / F::RS - 1)) return false;
-                    const int pages = __popc(__ballot_sync(0xffffffffu, copies(j)));
-                    if (lane == 0) {
-                        mbar_arrive_expect_tx(&raw_full[e % F::RS], (uint32_t)(pages * block));
-                        *issued = e + 1;
+                int id1 = 0;
+                float ks = 0.f, vs = 0.f;
+                int item_e = 0;   // exponent bits of the largest scale of the item's values so far
+                if (mine == 2) {
+                    const int id0 = held(0);
+                    id1 = held(1);
+                    ks = scale_of(0, id0, 0), vs = scale_of(0, id0, 1);
+                }
+                // One small loop over the halves, the copies RS - 1 of them ahead: unrolled by keys, values and halves, a warp that has
+                // its multiprocessor's quarter to itself waited for instructions, 700 cycles a copy and 200 for 16 bytes a lane.
+#pragma unroll 1
+                for (int c = 1 - F::RS; ok && c < 4 * n; ++c) {
+                    if (mine == 0 && c + F::RS - 1 < 4 * n && !copy(c + F::RS - 1)) {
+                        ok = false;
+                        break;
                     }
-                    __syncwarp();
-                    if (copies(j))
-                        asm volatile(
-                            "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
-                                sbase + F::kRaw + (uint32_t)(e % F::RS) * (F::kTile / 2) + (uint32_t)(lane * block)),
-                            "l"(p.c.pages + (((int64_t)checked(id) * 2 + kv) * p.c.Hkv + x.h) * block), "r"((uint32_t)block),
-                            "r"(smem_addr(&raw_full[e % F::RS]))
-                            : "memory");
-                    return true;
-                };
-                auto convert = [&](int e, int t0) {
-                    if (!warp_wait(&raw_full[e % F::RS], e / F::RS)) return false;
-                    if (e >= F::ST && !warp_wait(&empty[e % F::ST], e / F::ST - 1)) return false;
-                    const unsigned char* raw = smem + F::kRaw + (e % F::RS) * (F::kTile / 2) + from;
-                    unsigned char* tile = smem + F::kRing + (e % F::ST) * F::kTile + to;
-                    const int left = x.hi - t0 - 8 * mine - sub;   // tokens that are seen from this lane's first on
-                    auto read = [&](int i, uint4 (&u)[kHalves]) {
+                    if (c < 0) continue;
+                    const int j = c >> 2, half = c & 1, r = 2 * seq + c, e = r >> 1;
+                    if (mine == 2 && (c & 3) == 0) {
+                        const int id2 = held(j + 2);
+                        const float ks1 = scale_of(j + 1, id1, 0), vs1 = scale_of(j + 1, id1, 1);
+                        const uint32_t bits = __float_as_uint(vs);
+                        item_e = max(item_e, (int)(__reduce_max_sync(0xffffffffu, bits) >> 23));
+                        // log2 of the scale over the item's largest (far below it, where f16 holds nothing of the weight, the
+                        // sum's share of it still counts); a power of two has no rest
+                        const float below = (float)max((int)(bits >> 23) - item_e, -80);
+                        float rest;
+                        asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(rest) : "f"(__uint_as_float((bits & 0x7fffffu) | 0x3f800000u)));
+                        TileInfo& ti = info[(seq / 2 + j) % F::kInfos];
+                        if (lane < 8) ti.part[lane] = make_float4(ks, kLift + below + rest, ex2(-kLift - below) * ex2(-rest), 0.f);
+                        if (lane == 0) ti.v = __uint_as_float((uint32_t)item_e << 23);
+                        __syncwarp();
+                        id1 = id2, ks = ks1, vs = vs1;
+                    }
+                    if (!warp_wait(&raw_full[r % F::RS], r / F::RS) ||
+                        (half == 0 && e >= F::ST && !warp_wait(&empty[e % F::ST], e / F::ST - 1))) {
+                        ok = false;
+                        break;
+                    }
+                    // of the half's 8 groups one warp has two: the copying one, then the describing one
+                    const int g0 = half == 0 ? (mine + 2) % kConv : mine;
+                    const unsigned char* raw = smem + F::kRaw + (r % F::RS) * F::kHalf + (8 * g0 + sub) * D + quad * 16;
+                    unsigned char* to = smem + F::kRing + (e % F::ST) * F::kTile + (64 * half + 8 * g0 + sub) * 128;
+                    const int left = x.hi - x.lo - j * kKeys - 64 * half - 8 * g0 - sub;   // tokens seen from this lane's first on
+                    const bool part = __any_sync(0xffffffffu, left <= 8 * kConv * 2);
+#pragma unroll
+                    for (int i = 0; i < 3; ++i) {
+                        if (i == 2 && g0 == 2) break;
+                        uint4 u[kHalves];
 #pragma unroll
                         for (int h = 0; h < kHalves; ++h)
                             u[h] = *reinterpret_cast<const uint4*>(raw + i * (8 * kConv) * D + (h ^ turned) * 64);
-                    };
-                    uint4 u[kHalves], next[kHalves];
-                    read(0, u);
+                        if (part && 8 * kConv * i >= left) {
 #pragma unroll
-                    for (int i = 0; i < F::kOwn; ++i) {
-                        if (mine + kConv * i >= 16) break;
-                        if (i + 1 < F::kOwn && mine + kConv * (i + 1) < 16) read(i + 1, next);
+                            for (int h = 0; h < kHalves; ++h) u[h] = make_uint4(0, 0, 0, 0);
+                        }
 #pragma unroll
                         for (int h = 0; h < kHalves; ++h) {
                             uint32_t y[8];
                             widen16(u[h], y);
-                            if (8 * kConv * i >= left) {
-#pragma unroll
-                                for (int k = 0; k < 8; ++k) y[k] = 0;
-                            }
-                            unsigned char* row = tile + i * (8 * kConv) * 128 + (h ^ turned) * 16384;
+                            unsigned char* row = to + i * (8 * kConv) * 128 + (h ^ turned) * 16384;
                             *reinterpret_cast<uint4*>(row + chunk0) = make_uint4(y[0], y[1], y[2], y[3]);
                             *reinterpret_cast<uint4*>(row + chunk1) = make_uint4(y[4], y[5], y[6], y[7]);
-                            u[h] = next[h];
                         }
                     }
                     proxy_fence();
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(&raw_empty[e % F::RS]), mbar_arrive(&full[e % F::ST]);
-                    return true;
-                };
-                // the copies run RS - 1 entries ahead of the conversion
-                int idc = mine == 0 ? copied(0) : 0, idc1 = mine == 0 ? copied(1) : 0;   // of tile `ahead` / 2 and the next
-                int ahead = 0;
-                auto advance = [&] {
-                    if (mine != 0 || ahead >= 2 * n) return true;
-                    const bool good = copy(seq + ahead, ahead / 2, idc, ahead & 1);
-                    if (ahead & 1) idc = idc1, idc1 = copied(ahead / 2 + 2);
-                    ++ahead;
-                    return good;
-                };
-                const int id0 = held(0);
-                int id1 = held(1);
-                float ks = scale_of(0, id0, 0), vs = scale_of(0, id0, 1);
-                for (int i = 0; ok && i < F::RS - 1; ++i) ok = advance();
-                float item_v = 0.f;   // the largest scale of the item's values so far, as a power of two
-                for (int j = 0; ok && j < n; ++j) {
-                    const int id2 = held(j + 2);
-                    const float ks1 = scale_of(j + 1, id1, 0), vs1 = scale_of(j + 1, id1, 1);
-                    const int t0 = x.lo + j * kKeys;
-                    if (mine == 0) {
-                        const uint32_t top = __reduce_max_sync(0xffffffffu, __float_as_uint(vs));
-                        item_v = fmaxf(item_v, __uint_as_float(top & 0x7f800000u));
-                        // (far below the largest, where f16 holds nothing of it, the weight is still one for the sum)
-                        const float lift = kLift + (item_v > 0.f ? fmaxf(log2f(vs / item_v), -80.f) : 0.f);
-                        TileInfo& ti = info[(seq / 2 + j) % kInfos];
-                        if (lane < 8) ti.part[lane] = make_float4(ks, lift, exp2f(-lift), 0.f);
-                        if (lane == 0) ti.v = item_v;
-                        __syncwarp();
+                    if (lane == 0) {
+                        mbar_arrive(&raw_empty[r % F::RS]);
+                        if (half == 1) mbar_arrive(&full[e % F::ST]);
                     }
-                    ok = advance() && convert(seq + 2 * j, t0) && advance() && convert(seq + 2 * j + 1, t0);
-                    id1 = id2, ks = ks1, vs = vs1;
                 }
                 seq += 2 * n;
             }
@@ -470,7 +481,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_cons
                     const int seen = valid ? vis - t0 : kKeys;
                     const bool hide = __any_sync(0xffffffffu, seen < kKeys);
                     float s[4][32];
-                    const TileInfo& ti = info[(it0 + j) % kInfos];
+                    const TileInfo& ti = info[(it0 + j) % F::kInfos];
                     float top = -INFINITY;
 #pragma unroll
                     for (int half = 0; half < 2; ++half) {
@@ -606,9 +617,9 @@ template <int D>
 cudaError_t launch(const PagedParams& p, cudaStream_t s) {
     using F = Cfg<D>;
     static std::atomic<int> optin[kMaxOptinDevices];
-    const cudaError_t e = smem_optin(reinterpret_cast<const void*>(paged_tc_kernel<D>), F::bytes(kMaxBatch), optin);
+    const cudaError_t e = smem_optin(reinterpret_cast<const void*>(paged_tc_kernel<D>), F::kSmem, optin);
     if (e != cudaSuccess) return e;
-    paged_tc_kernel<D><<<p.ctas, kThreads, F::bytes(p.t.B), s>>>(p);
+    paged_tc_kernel<D><<<p.ctas, kThreads, F::kSmem, s>>>(p);
     return cudaGetLastError();
 }
 
