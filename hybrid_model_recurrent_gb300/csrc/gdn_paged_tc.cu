@@ -286,8 +286,10 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_cons
                 }
                 return id;
             };
+            const int64_t kv_bytes = p.c.Hkv * block;
+            const int stop = p.stall_after >= 0 ? 4 * p.stall_after : 0x7fffffff;   // testing hook
             bool ok = true;
-            int seq = 0;
+            int seq = 0, asked = 0;   // ring entries of the items so far; halves whose copies were issued
             for (int at = begin; ok && at < end;) {
                 const Segment x = segment_at<kTcRows, kTcUnit>(p, s_cum, at, end);
                 at += x.u1 - x.u0;
@@ -300,32 +302,45 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_cons
                     asm volatile("ld.global.nc.u32 %0, [%1];" : "=r"(y) : "l"(a));
                     return y;
                 };
-                // the first warp: this lane's piece of tile j, whose page it holds
+                // the first warp: this lane's piece of a tile, where it lies, and the bytes of the tile's halves; all of it is found a tile
+                // ahead, so that a copy is a few instructions
                 auto token = [&](int j) { return x.lo + j * kKeys + (lane << piece_log2); };
                 auto copies = [&](int j) { return lane < lanes && j < n && token(j) < x.hi; };
                 auto copied = [&](int j) { return copies(j) ? (int)load(table + (token(j) >> p.c.page_log2)) : 0; };
-                int idc = 0, idc1 = 0;   // pages of the tile that is copied, and of the next
-                if (mine == 0) idc = copied(0), idc1 = copied(1);
+                auto place = [&](int j, int id) {
+                    return p.c.pages + ((int64_t)checked(id) * 2 * p.c.Hkv + x.h) * block + (int64_t)(token(j) & (p.c.page - 1)) * D;
+                };
+                auto bytes_of = [&](int j, int half) {
+                    return __popc(__ballot_sync(0xffffffffu, copies(j)) >> (half * lanes / 2) & ((1u << lanes / 2) - 1)) * piece;
+                };
+                const int own_half = lane >= lanes / 2;
+                const uint32_t own_to = sbase + F::kRaw + (uint32_t)(lane & (lanes / 2 - 1)) * piece;
+                const unsigned char* src = nullptr;
+                uint32_t bytes[2] = {};
+                bool some = false;
+                int idc = 0;   // of the tile after the one that is copied
+                if (mine == 0) {
+                    idc = copied(0);
+                    src = place(0, idc), some = copies(0), bytes[0] = bytes_of(0, 0), bytes[1] = bytes_of(0, 1);
+                    idc = copied(1);
+                }
                 auto copy = [&](int c) {   // half c of the item: of keys, then of values, tile by tile
-                    const int r = 2 * seq + c, j = c >> 2;
-                    if (p.stall_after >= 0 && r / 4 >= p.stall_after) return false;   // testing hook
-                    if (r >= F::RS && !warp_wait(&raw_empty[r % F::RS], r / F::RS - 1)) return false;
-                    const bool mine_too = copies(j) && (lane >= lanes / 2) == ((c & 1) == 1);
-                    const uint32_t pieces = __popc(__ballot_sync(0xffffffffu, mine_too));
-                    if (lane == 0) {
-                        mbar_arrive_expect_tx(&raw_full[r % F::RS], pieces * piece);
-                        *issued = r + 1;
-                    }
+                    const int r = 2 * seq + c, at_r = r % F::RS, half = c & 1;
+                    if (r >= stop || (r >= F::RS && !warp_wait(&raw_empty[at_r], r / F::RS - 1))) return false;
+                    if (lane == 0) mbar_arrive_expect_tx(&raw_full[at_r], bytes[half]);
                     __syncwarp();
-                    if (mine_too)
+                    if (some && own_half == half)
                         asm volatile(
                             "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
-                                sbase + F::kRaw + (uint32_t)(r % F::RS) * F::kHalf + (uint32_t)(lane & (lanes / 2 - 1)) * piece),
-                            "l"(p.c.pages + (((int64_t)checked(idc) * 2 + (c >> 1 & 1)) * p.c.Hkv + x.h) * block +
-                                (int64_t)(token(j) & (p.c.page - 1)) * D),
-                            "r"(piece), "r"(smem_addr(&raw_full[r % F::RS]))
+                                own_to + (uint32_t)at_r * F::kHalf),
+                            "l"(src + (c & 2 ? kv_bytes : 0)), "r"(piece), "r"(smem_addr(&raw_full[at_r]))
                             : "memory");
-                    if ((c & 3) == 3) idc = idc1, idc1 = copied(j + 2);
+                    asked = r + 1;
+                    if ((c & 3) == 3) {
+                        const int j = (c >> 2) + 1;
+                        src = place(j, idc), some = copies(j), bytes[0] = bytes_of(j, 0), bytes[1] = bytes_of(j, 1);
+                        idc = copied(j + 1);
+                    }
                     return true;
                 };
                 // the last warp: the scales of the tokens 16 l .. 16 l + 15 of tile j
@@ -373,8 +388,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_cons
                         ok = false;
                         break;
                     }
-                    // of the half's 8 groups one warp has two: the copying one, then the describing one
-                    const int g0 = half == 0 ? (mine + 2) % kConv : mine;
+                    const int g0 = (mine + 2) % kConv;   // (of the half's 8 groups the copying warp has two)
                     const unsigned char* raw = smem + F::kRaw + (r % F::RS) * F::kHalf + (8 * g0 + sub) * D + quad * 16;
                     unsigned char* to = smem + F::kRing + (e % F::ST) * F::kTile + (64 * half + 8 * g0 + sub) * 128;
                     const int left = x.hi - x.lo - j * kKeys - 64 * half - 8 * g0 - sub;   // tokens seen from this lane's first on
@@ -408,6 +422,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_cons
                 }
                 seq += 2 * n;
             }
+            if (mine == 0 && lane == 0) *issued = asked;
         }
     } else {
         // ---- softmax of row tile a; this thread's row ----
