@@ -18,8 +18,14 @@
 // there.
 //
 // The units (128 tokens of an item) are dealt out evenly over the CTAs, one a multiprocessor (gdn_cache.cuh).
-// Roles: warps 0 .. 7 softmax (one warpgroup a row tile), warp 8 issues products, warps 9 .. 11 convert.  One row tile's softmax
-// runs beside the other's products; an item of at most 128 rows takes one tile, in turn.
+// Roles: warps 0 .. 7 softmax (one warpgroup a row tile), warp 8 issues products, warp 9 copies, warps 10 .. 15 convert.  One row tile's
+// softmax runs beside the other's products; an item of at most 128 rows takes one tile, in turn.
+//
+// The softmax takes a row's scores 32 at a time and writes their weights at once, against the maximum so far: when a
+// chunk raises it by too much, O, l and the tile's weights written before are rescaled.  So a thread holds 64 scores and not 128,
+// sixteen warps have 128 registers each, and the loop's code is small: with three converting warps beside eight that held
+// whole rows (384 threads), a lone warp's instructions came at 7 to 9 cycles each, waiting for the instruction cache,
+// and the conversion took 6 k cycles a tile where softmax and products took 3 k.
 //
 // Every wait is bounded: a role that gives up sets the CTA's abort flag and the sticky status, every role leaves its
 // loop, copies and products in flight are waited for, and TMEM is freed.
@@ -41,9 +47,7 @@ using tc::proxy_fence;
 using tc::tc_fence_after;
 using tc::tc_fence_before;
 using tc::tmem_ld32;
-using tc::tmem_ld32x2;
 using tc::tmem_st16;
-using tc::tmem_st32;
 using tc::tmem_st_wait;
 using tc::umma_commit;
 using tc::umma_ss;
@@ -60,14 +64,14 @@ constexpr int kRows = 128;    // rows of a tile
 constexpr int kKeys = kTcUnit;
 constexpr float kRise = 8.f;  // O is rescaled when a maximum has risen by more than this (log2)
 constexpr float kLift = 7.f;  // log2 of a weight at the maximum: with the rise 2^15 in f16
-constexpr int kConv = 3;      // converting warps
+constexpr int kConv = 3;      // converting warps for each half of a tile
 // A weight's exponent is score * scale - m in one rounding, but m is a product already rounded: for the largest score its
 // rounding error is left, half a step of m, 16 at 2^28 and past what an exponential holds from 2^31 on.  Rows further from zero
 // than this round the product by itself first.
 constexpr float kFar = 268435456.f;
 // Factors of scores are not below the smallest normal number: a hidden token's -infinity stays that.
 constexpr float kTiny = 1.17549435e-38f;
-constexpr int kThreads = 384;
+constexpr int kThreads = 512;
 
 template <int D>
 struct Cfg {
@@ -96,12 +100,16 @@ __device__ __forceinline__ uint32_t half2(float a, float b) {
 // instruction descriptor of kind::f16: D fp32, A and B f16, M = 128
 __host__ __device__ constexpr uint32_t idesc_f16(int N, bool b_mn) { return idesc(N, false, b_mn) & ~((1u << 7) | (1u << 10)); }
 
-__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8]) {
-    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(r[0]), "r"(r[1]),
-                 "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
-                 : "memory");
+// 16 columns, waited for
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr)
+        : "memory");
 }
-
 // 16 e4m3 as f16
 __device__ __forceinline__ void widen16(const uint4& u, uint32_t (&y)[8]) {
     const uint32_t w[4] = {u.x, u.y, u.z, u.w};
@@ -118,29 +126,6 @@ struct TileInfo {
     float4 part[kKeys / 16];
     float v, unused[3];
 };
-
-// The weights of a tile's row, over its own scores in TMEM, for rows far from zero; returns their sum.  A function by itself, so
-// that the loop of every other row stays small.
-__device__ __noinline__ float far_weights(uint32_t taddr, int seen, float row_scale, float base, const TileInfo& ti) {
-    float sum = 0.f;
-#pragma unroll 1
-    for (int c = 0; c < kKeys / 32; ++c) {
-        float x[32];
-        uint32_t w[16];
-        tmem_ld32(taddr + 32 * c, x);
-#pragma unroll
-        for (int i = 0; i < 32; ++i) {
-            const float4 f = ti.part[2 * c + i / 16];
-            const float y = __fsub_rn(__fmul_rn(x[i], fmaxf(row_scale * f.x, kTiny)), base);
-            x[i] = 32 * c + i < seen ? ex2(y + f.y) : 0.f;
-            sum += x[i] * f.z;
-        }
-#pragma unroll
-        for (int i = 0; i < 16; ++i) w[i] = half2(x[2 * i], x[2 * i + 1]);
-        tmem_st16(taddr + 16 * c, w);
-    }
-    return sum;
-}
 
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_constant__ PagedParams p) {
@@ -173,7 +158,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_cons
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
     }
     if (tid == 0) {
-        for (int i = 0; i < F::ST; ++i) mbar_init(&full[i], kConv), mbar_init(&empty[i], 1);
+        for (int i = 0; i < F::ST; ++i) mbar_init(&full[i], 2 * kConv), mbar_init(&empty[i], 1);
         for (int i = 0; i < 2; ++i) {
             mbar_init(&s_full[i], 1), mbar_init(&p_ready[i], 128);
             mbar_init(&q_ready[i], 128), mbar_init(&o_full[i], 1);
@@ -203,9 +188,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_cons
     };
     auto tiles_of = [&](const Segment& x) { return max(0, (x.hi - x.lo + kKeys - 1) / kKeys); };
 
-    // 384 threads start with 168 registers each (64512 in all): 256 x 200 + 128 x 96 = 63488
     if (warp >= 8) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 96;");
         if (warp == 8) {
             // ---- products (the whole warp walks along, one elected lane issues); K of tile i is ring entry 2 i, V 2 i + 1 ----
             auto slot_at = [&](int seq) { return sbase + F::kRing + (uint32_t)(seq % F::ST) * F::kTile; };
@@ -268,17 +251,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_cons
             }
             if (elect_one()) umma_commit(end_bar);   // also after giving up: the end waits for the products in flight
         } else {
-            // ---- keys and values: copied (by the first of the three warps, a lane a page), and converted; the last one
-            // describes the tiles.  They go in halves of 64 tokens ----
-            const int mine = warp - 9, sub = lane >> 2, quad = lane & 3;
-            const int piece_log2 = min(p.c.page_log2, 6), lanes = kKeys >> piece_log2;   // a page or half of one a lane
+            // ---- keys and values: copied by a warp, a lane a page, and converted by six, three for each half of 64 tokens ----
             const int64_t block = (int64_t)p.c.page * D;
-            const uint32_t piece = (uint32_t)D << piece_log2;
-            // A warp converts the tokens 8 g .. 8 g + 7 for every third g, 64 bytes of a token by four lanes.  At width 128 odd
-            // tokens take their halves the other way round: a quarter of a warp then meets every bank once, reading and writing.
-            constexpr int kHalves = D / 64;
-            const int turned = kHalves == 2 ? sub & 1 : 0;
-            const int chunk0 = ((2 * quad) ^ sub) << 4, chunk1 = ((2 * quad + 1) ^ sub) << 4;   // (token & 7 = sub)
             auto checked = [&](int id) {   // a table's entry, where it is used
                 if ((unsigned)id >= (unsigned)p.c.N) {
                     atomicOr(p.status, STATUS_BAD_INDEX);
@@ -286,147 +260,146 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_cons
                 }
                 return id;
             };
-            const int64_t kv_bytes = p.c.Hkv * block;
-            const int stop = p.stall_after >= 0 ? 4 * p.stall_after : 0x7fffffff;   // testing hook
+            // (loaded by name where they stand, a tile before their use: the compiler moved plain loads down to it)
+            auto load = [](const void* a) {
+                uint32_t y;
+                asm volatile("ld.global.nc.u32 %0, [%1];" : "=r"(y) : "l"(a));
+                return y;
+            };
             bool ok = true;
-            int seq = 0, asked = 0;   // ring entries of the items so far; halves whose copies were issued
-            for (int at = begin; ok && at < end;) {
-                const Segment x = segment_at<kTcRows, kTcUnit>(p, s_cum, at, end);
-                at += x.u1 - x.u0;
-                const int n = tiles_of(x);
-                if (n == 0) continue;
-                const int32_t* table = p.c.table + (int64_t)x.rq.row * p.c.W;   // (a row without tokens has no tiles)
-                // (loaded by name where they stand, a tile before their use: the compiler moved plain loads down to it)
-                auto load = [](const void* a) {
-                    uint32_t y;
-                    asm volatile("ld.global.nc.u32 %0, [%1];" : "=r"(y) : "l"(a));
-                    return y;
-                };
-                // the first warp: this lane's piece of a tile, where it lies, and the bytes of the tile's halves; all of it is found a tile
-                // ahead, so that a copy is a few instructions
-                auto token = [&](int j) { return x.lo + j * kKeys + (lane << piece_log2); };
-                auto copies = [&](int j) { return lane < lanes && j < n && token(j) < x.hi; };
-                auto copied = [&](int j) { return copies(j) ? (int)load(table + (token(j) >> p.c.page_log2)) : 0; };
-                auto place = [&](int j, int id) {
-                    return p.c.pages + ((int64_t)checked(id) * 2 * p.c.Hkv + x.h) * block + (int64_t)(token(j) & (p.c.page - 1)) * D;
-                };
-                auto bytes_of = [&](int j, int half) {
-                    return __popc(__ballot_sync(0xffffffffu, copies(j)) >> (half * lanes / 2) & ((1u << lanes / 2) - 1)) * piece;
-                };
+            int seq = 0;   // ring entries of the items so far
+            if (warp == 9) {
+                const int piece_log2 = min(p.c.page_log2, 6), lanes = kKeys >> piece_log2;   // a page or half of one a lane
+                const uint32_t piece = (uint32_t)D << piece_log2;
                 const int own_half = lane >= lanes / 2;
                 const uint32_t own_to = sbase + F::kRaw + (uint32_t)(lane & (lanes / 2 - 1)) * piece;
-                const unsigned char* src = nullptr;
-                uint32_t bytes[2] = {};
-                bool some = false;
-                int idc = 0;   // of the tile after the one that is copied
-                if (mine == 0) {
-                    idc = copied(0);
-                    src = place(0, idc), some = copies(0), bytes[0] = bytes_of(0, 0), bytes[1] = bytes_of(0, 1);
-                    idc = copied(1);
-                }
-                auto copy = [&](int c) {   // half c of the item: of keys, then of values, tile by tile
-                    const int r = 2 * seq + c, at_r = r % F::RS, half = c & 1;
-                    if (r >= stop || (r >= F::RS && !warp_wait(&raw_empty[at_r], r / F::RS - 1))) return false;
-                    if (lane == 0) mbar_arrive_expect_tx(&raw_full[at_r], bytes[half]);
-                    __syncwarp();
-                    if (some && own_half == half)
-                        asm volatile(
-                            "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
-                                own_to + (uint32_t)at_r * F::kHalf),
-                            "l"(src + (c & 2 ? kv_bytes : 0)), "r"(piece), "r"(smem_addr(&raw_full[at_r]))
-                            : "memory");
-                    asked = r + 1;
-                    if ((c & 3) == 3) {
-                        const int j = (c >> 2) + 1;
-                        src = place(j, idc), some = copies(j), bytes[0] = bytes_of(j, 0), bytes[1] = bytes_of(j, 1);
-                        idc = copied(j + 1);
-                    }
-                    return true;
-                };
-                // the last warp: the scales of the tokens 16 l .. 16 l + 15 of tile j
-                auto holds = [&](int j) { return lane < 8 && j < n && x.lo + j * kKeys + 16 * lane < x.hi; };
-                auto held = [&](int j) { return holds(j) ? (int)load(table + ((x.lo + j * kKeys + 16 * lane) >> p.c.page_log2)) : 0; };
-                auto scale_of = [&](int j, int id, int kv) {
-                    return holds(j) ? __uint_as_float(load(p.c.scales + ((int64_t)checked(id) * 2 + kv) * p.c.Hkv + x.h)) : 0.f;
-                };
-                int id1 = 0;
-                float ks = 0.f, vs = 0.f;
-                int item_e = 0;   // exponent bits of the largest scale of the item's values so far
-                if (mine == 2) {
-                    const int id0 = held(0);
-                    id1 = held(1);
-                    ks = scale_of(0, id0, 0), vs = scale_of(0, id0, 1);
-                }
-                // One small loop over the halves, the copies RS - 1 of them ahead: unrolled by keys, values and halves, a warp that has
-                // its multiprocessor's quarter to itself waited for instructions, 700 cycles a copy and 200 for 16 bytes a lane.
+                const int64_t kv_bytes = p.c.Hkv * block;
+                const int stop = p.stall_after >= 0 ? 4 * p.stall_after : 0x7fffffff;   // testing hook
+                int asked = 0;
+                for (int at = begin; ok && at < end;) {
+                    const Segment x = segment_at<kTcRows, kTcUnit>(p, s_cum, at, end);
+                    at += x.u1 - x.u0;
+                    const int n = tiles_of(x);
+                    if (n == 0) continue;
+                    const int32_t* table = p.c.table + (int64_t)x.rq.row * p.c.W;   // (a row without tokens has no tiles)
+                    // this lane's piece of tile j, and where it lies: found a tile ahead, so that a copy is a few instructions
+                    auto token = [&](int j) { return x.lo + j * kKeys + (lane << piece_log2); };
+                    auto copies = [&](int j) { return lane < lanes && j < n && token(j) < x.hi; };
+                    auto copied = [&](int j) { return copies(j) ? (int)load(table + (token(j) >> p.c.page_log2)) : 0; };
+                    int id = copied(0);
 #pragma unroll 1
-                for (int c = 1 - F::RS; ok && c < 4 * n; ++c) {
-                    if (mine == 0 && c + F::RS - 1 < 4 * n && !copy(c + F::RS - 1)) {
-                        ok = false;
-                        break;
-                    }
-                    if (c < 0) continue;
-                    const int j = c >> 2, half = c & 1, r = 2 * seq + c, e = r >> 1;
-                    if (mine == 2 && (c & 3) == 0) {
-                        const int id2 = held(j + 2);
-                        const float ks1 = scale_of(j + 1, id1, 0), vs1 = scale_of(j + 1, id1, 1);
-                        const uint32_t bits = __float_as_uint(vs);
-                        item_e = max(item_e, (int)(__reduce_max_sync(0xffffffffu, bits) >> 23));
-                        // log2 of the scale over the item's largest (far below it, where f16 holds nothing of the weight, the
-                        // sum's share of it still counts); a power of two has no rest
-                        const float below = (float)max((int)(bits >> 23) - item_e, -80);
-                        float rest;
-                        asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(rest) : "f"(__uint_as_float((bits & 0x7fffffu) | 0x3f800000u)));
-                        TileInfo& ti = info[(seq / 2 + j) % F::kInfos];
-                        if (lane < 8) ti.part[lane] = make_float4(ks, kLift + below + rest, ex2(-kLift - below) * ex2(-rest), 0.f);
-                        if (lane == 0) ti.v = __uint_as_float((uint32_t)item_e << 23);
-                        __syncwarp();
-                        id1 = id2, ks = ks1, vs = vs1;
-                    }
-                    if (!warp_wait(&raw_full[r % F::RS], r / F::RS) ||
-                        (half == 0 && e >= F::ST && !warp_wait(&empty[e % F::ST], e / F::ST - 1))) {
-                        ok = false;
-                        break;
-                    }
-                    const int g0 = (mine + 2) % kConv;   // (of the half's 8 groups the copying warp has two)
-                    const unsigned char* raw = smem + F::kRaw + (r % F::RS) * F::kHalf + (8 * g0 + sub) * D + quad * 16;
-                    unsigned char* to = smem + F::kRing + (e % F::ST) * F::kTile + (64 * half + 8 * g0 + sub) * 128;
-                    const int left = x.hi - x.lo - j * kKeys - 64 * half - 8 * g0 - sub;   // tokens seen from this lane's first on
-                    const bool part = __any_sync(0xffffffffu, left <= 8 * kConv * 2);
-#pragma unroll
-                    for (int i = 0; i < 3; ++i) {
-                        if (i == 2 && g0 == 2) break;
-                        uint4 u[kHalves];
-#pragma unroll
-                        for (int h = 0; h < kHalves; ++h)
-                            u[h] = *reinterpret_cast<const uint4*>(raw + i * (8 * kConv) * D + (h ^ turned) * 64);
-                        if (part && 8 * kConv * i >= left) {
-#pragma unroll
-                            for (int h = 0; h < kHalves; ++h) u[h] = make_uint4(0, 0, 0, 0);
-                        }
-#pragma unroll
-                        for (int h = 0; h < kHalves; ++h) {
-                            uint32_t y[8];
-                            widen16(u[h], y);
-                            unsigned char* row = to + i * (8 * kConv) * 128 + (h ^ turned) * 16384;
-                            *reinterpret_cast<uint4*>(row + chunk0) = make_uint4(y[0], y[1], y[2], y[3]);
-                            *reinterpret_cast<uint4*>(row + chunk1) = make_uint4(y[4], y[5], y[6], y[7]);
+                    for (int j = 0; ok && j < n; ++j) {
+                        const unsigned char* src = p.c.pages + ((int64_t)checked(id) * 2 * p.c.Hkv + x.h) * block +
+                                                   (int64_t)(token(j) & (p.c.page - 1)) * D;
+                        const bool some = copies(j);
+                        const uint32_t who = __ballot_sync(0xffffffffu, some);
+                        id = copied(j + 1);
+#pragma unroll 1
+                        for (int c = 0; c < 4; ++c) {   // the halves of the keys, then of the values
+                            const int r = 2 * seq + 4 * j + c, at_r = r % F::RS, half = c & 1;
+                            ok = r < stop && (r < F::RS || warp_wait(&raw_empty[at_r], r / F::RS - 1));
+                            if (!ok) break;
+                            if (lane == 0)
+                                mbar_arrive_expect_tx(&raw_full[at_r], __popc(who >> (half * lanes / 2) & ((1u << lanes / 2) - 1)) * piece);
+                            __syncwarp();
+                            if (some && own_half == half)
+                                asm volatile(
+                                    "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                                        own_to + (uint32_t)at_r * F::kHalf),
+                                    "l"(src + (c & 2 ? kv_bytes : 0)), "r"(piece), "r"(smem_addr(&raw_full[at_r]))
+                                    : "memory");
+                            asked = r + 1;
                         }
                     }
-                    proxy_fence();
-                    __syncwarp();
-                    if (lane == 0) {
-                        mbar_arrive(&raw_empty[r % F::RS]);
-                        if (half == 1) mbar_arrive(&full[e % F::ST]);
-                    }
+                    seq += 2 * n;
                 }
-                seq += 2 * n;
+                if (lane == 0) *issued = asked;
+            } else {
+                // A warp converts the tokens 8 g .. 8 g + 7 of its half for every third g, 64 bytes of a token by four lanes.  At
+                // width 128 odd tokens take their 64 bytes the other way round: a quarter of a warp then meets every bank once,
+                // reading and writing.
+                const int half = (warp - 10) / kConv, g0 = (warp - 10) % kConv, sub = lane >> 2, quad = lane & 3;
+                constexpr int kParts = D / 64;
+                const int turned = kParts == 2 ? sub & 1 : 0;
+                const int chunk0 = ((2 * quad) ^ sub) << 4, chunk1 = ((2 * quad + 1) ^ sub) << 4;   // (token & 7 = sub)
+                const unsigned char* raw0 = smem + F::kRaw + (8 * g0 + sub) * D + quad * 16;
+                unsigned char* to0 = smem + F::kRing + (64 * half + 8 * g0 + sub) * 128;
+                const bool describes = warp == 12;   // (with two groups of 8 tokens, others have three)
+                for (int at = begin; ok && at < end;) {
+                    const Segment x = segment_at<kTcRows, kTcUnit>(p, s_cum, at, end);
+                    at += x.u1 - x.u0;
+                    const int n = tiles_of(x);
+                    if (n == 0) continue;
+                    const int32_t* table = p.c.table + (int64_t)x.rq.row * p.c.W;
+                    // the scales of the tokens 16 l .. 16 l + 15 of tile j
+                    auto holds = [&](int j) { return lane < 8 && j < n && x.lo + j * kKeys + 16 * lane < x.hi; };
+                    auto held = [&](int j) { return holds(j) ? (int)load(table + ((x.lo + j * kKeys + 16 * lane) >> p.c.page_log2)) : 0; };
+                    auto scale_of = [&](int j, int id, int kv) {
+                        return holds(j) ? __uint_as_float(load(p.c.scales + ((int64_t)checked(id) * 2 + kv) * p.c.Hkv + x.h)) : 0.f;
+                    };
+                    int id1 = 0;
+                    float ks = 0.f, vs = 0.f;
+                    int item_e = 0;   // exponent bits of the largest scale of the item's values so far
+                    if (describes) {
+                        const int id0 = held(0);
+                        id1 = held(1);
+                        ks = scale_of(0, id0, 0), vs = scale_of(0, id0, 1);
+                    }
+#pragma unroll 1
+                    for (int c = 0; c < 2 * n; ++c) {
+                        const int j = c >> 1, e = seq + c, r = 2 * e + half;
+                        if (describes && (c & 1) == 0) {
+                            const int id2 = held(j + 2);
+                            const float ks1 = scale_of(j + 1, id1, 0), vs1 = scale_of(j + 1, id1, 1);
+                            const uint32_t bits = __float_as_uint(vs);
+                            item_e = max(item_e, (int)(__reduce_max_sync(0xffffffffu, bits) >> 23));
+                            // log2 of the scale over the item's largest (far below it, where f16 holds nothing of the weight, the
+                            // sum's share of it still counts); a power of two has no rest
+                            const float below = (float)max((int)(bits >> 23) - item_e, -80);
+                            float rest;
+                            asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(rest) : "f"(__uint_as_float((bits & 0x7fffffu) | 0x3f800000u)));
+                            TileInfo& ti = info[(e / 2) % F::kInfos];
+                            if (lane < 8) ti.part[lane] = make_float4(ks, kLift + below + rest, ex2(-kLift - below) * ex2(-rest), 0.f);
+                            if (lane == 0) ti.v = __uint_as_float((uint32_t)item_e << 23);
+                            __syncwarp();
+                            id1 = id2, ks = ks1, vs = vs1;
+                        }
+                        ok = warp_wait(&raw_full[r % F::RS], r / F::RS) && (e < F::ST || warp_wait(&empty[e % F::ST], e / F::ST - 1));
+                        if (!ok) break;
+                        const unsigned char* raw = raw0 + (r % F::RS) * F::kHalf;
+                        unsigned char* to = to0 + (e % F::ST) * F::kTile;
+                        const int left = x.hi - x.lo - j * kKeys - 64 * half - 8 * g0 - sub;   // tokens seen from this lane's first on
+                        const bool part = __any_sync(0xffffffffu, left <= 8 * kConv * 2);
+#pragma unroll
+                        for (int i = 0; i < 3; ++i) {
+                            if (i == 2 && g0 == 2) break;
+                            uint4 u[kParts];
+#pragma unroll
+                            for (int h = 0; h < kParts; ++h)
+                                u[h] = *reinterpret_cast<const uint4*>(raw + i * (8 * kConv) * D + (h ^ turned) * 64);
+                            if (part && 8 * kConv * i >= left) {
+#pragma unroll
+                                for (int h = 0; h < kParts; ++h) u[h] = make_uint4(0, 0, 0, 0);
+                            }
+#pragma unroll
+                            for (int h = 0; h < kParts; ++h) {
+                                uint32_t y[8];
+                                widen16(u[h], y);
+                                unsigned char* row = to + i * (8 * kConv) * 128 + (h ^ turned) * 16384;
+                                *reinterpret_cast<uint4*>(row + chunk0) = make_uint4(y[0], y[1], y[2], y[3]);
+                                *reinterpret_cast<uint4*>(row + chunk1) = make_uint4(y[4], y[5], y[6], y[7]);
+                            }
+                        }
+                        proxy_fence();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&raw_empty[r % F::RS]), mbar_arrive(&full[e % F::ST]);
+                    }
+                    seq += 2 * n;
+                }
             }
-            if (mine == 0 && lane == 0) *issued = asked;
         }
     } else {
         // ---- softmax of row tile a; this thread's row ----
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
         const int a = warp >> 2, r = tid & 127;
         const uint32_t trow = tbase + ((uint32_t)(32 * (warp & 3)) << 16);
         bool ok = true;
@@ -486,80 +459,97 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_cons
                 proxy_fence();
                 mbar_arrive(&q_ready[a]);
             }
-            float m = -INFINITY, l = 0.f, item_v = 0.f;
+            float m = -INFINITY, item_v = 0.f;
+            float2 l2 = make_float2(0.f, 0.f);
             for (int j = 0; j < n; ++j, ++mine) {
-                const int t0 = x.lo + j * kKeys;
                 ok = warp_wait(&s_full[a], mine);
                 if (!ok) break;
                 tc_fence_after();
                 if (busy) {
-                    const int seen = valid ? vis - t0 : kKeys;
+                    const int seen = valid ? vis - x.lo - j * kKeys : kKeys;
                     const bool hide = __any_sync(0xffffffffu, seen < kKeys);
-                    float s[4][32];
                     const TileInfo& ti = info[(it0 + j) % F::kInfos];
-                    float top = -INFINITY;
-#pragma unroll
-                    for (int half = 0; half < 2; ++half) {
-                        float(&s0)[32] = s[2 * half], (&s1)[32] = s[2 * half + 1];
-                        tmem_ld32x2(trow + a * 128 + 64 * half, trow + a * 128 + 64 * half + 32, s0, s1);
+                    const uint32_t ts = trow + a * 128, to = trow + F::kO + a * D;
+                    // scores 32 c .. 32 c + 31, over whose first half's columns of the chunk before the weights go
+                    auto chunk = [&](int c) {
+                        float s[32];
+                        tmem_ld32(ts + 32 * c, s);
                         if (hide) {
 #pragma unroll
-                            for (int i = 0; i < 32; ++i) {
-                                if (64 * half + i >= seen) s0[i] = -INFINITY;
-                                if (64 * half + 32 + i >= seen) s1[i] = -INFINITY;
-                            }
+                            for (int i = 0; i < 32; ++i)
+                                if (32 * c + i >= seen) s[i] = -INFINITY;
                         }
+                        const float4 f0 = ti.part[2 * c], f1 = ti.part[2 * c + 1];
+                        const float scale0 = fmaxf(row_scale * f0.x, kTiny), scale1 = fmaxf(row_scale * f1.x, kTiny);
+                        float t0 = fmaxf(s[0], s[1]), t1 = fmaxf(s[16], s[17]);
 #pragma unroll
-                        for (int c = 0; c < 4; ++c) {   // 16 tokens each
-                            const float* y = s[2 * half + c / 2] + 16 * (c & 1);
-                            float t = fmaxf(y[0], y[1]);
-#pragma unroll
-                            for (int i = 2; i < 16; i += 2) t = fmaxf(fmaxf(t, y[i]), y[i + 1]);
-                            top = fmaxf(top, t * fmaxf(row_scale * ti.part[4 * half + c].x, kTiny));
+                        for (int i = 2; i < 16; i += 2) {
+                            t0 = fmaxf(fmaxf(t0, s[i]), s[i + 1]);
+                            t1 = fmaxf(fmaxf(t1, s[16 + i]), s[17 + i]);
                         }
-                    }
-                    const bool rise = valid && (top > m + kRise || m == -INFINITY);
-                    if (__any_sync(0xffffffffu, rise || ti.v > item_v)) {
-                        const float mn = rise ? fmaxf(m, top) : m;
-                        float f = mn == -INFINITY ? 1.f : ex2(m - mn);
-                        m = mn;
-                        l *= f;
-                        if (ti.v > item_v) f *= item_v / ti.v, item_v = ti.v;
-                        if (j > 0) {   // every earlier product into O is done: s_full came after them
+                        const float top = fmaxf(t0 * scale0, t1 * scale1);
+                        const bool rise = valid && (top > m + kRise || m == -INFINITY), grow = c == 0 && ti.v > item_v;
+                        if (__any_sync(0xffffffffu, rise || grow)) {
+                            // by a power of two, which the weights that are f16 already take without another rounding
+                            const float up = ceilf(top - m);   // (infinite for a first maximum)
+                            const bool far = !(up <= 100.f);
+                            float f = !rise ? 1.f : far ? 0.f : ex2(-up);
+                            if (rise) m = far ? top : m + up;
+                            l2 = make_float2(l2.x * f, l2.y * f);
+                            tmem_st_wait();   // what is read here has been written
 #pragma unroll 1
-                            for (int c = 0; c < D / 32; ++c) {
-                                float o[32];
-                                tmem_ld32(trow + F::kO + a * D + 32 * c, o);
+                            for (int k = 0; k < c; ++k) {   // this tile's weights so far
+                                uint32_t w[16];
+                                tmem_ld16(ts + 16 * k, w);
 #pragma unroll
-                                for (int i = 0; i < 32; ++i) o[i] *= f;
-                                tmem_st32(trow + F::kO + a * D + 32 * c, o);
+                                for (int i = 0; i < 16; ++i) {
+                                    const float2 y = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
+                                    w[i] = half2(y.x * f, y.y * f);
+                                }
+                                tmem_st16(ts + 16 * k, w);
+                            }
+                            if (grow) f *= item_v / ti.v, item_v = ti.v;
+                            if (j > 0) {   // every earlier product into O is done: s_full came after them
+#pragma unroll 1
+                                for (int k = 0; k < D / 16; ++k) {
+                                    uint32_t o[16];
+                                    tmem_ld16(to + 16 * k, o);
+#pragma unroll
+                                    for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+                                    tmem_st16(to + 16 * k, o);
+                                }
                             }
                         }
-                    }
-                    const float base = m == -INFINITY ? 0.f : m;
-                    float2 sum0 = make_float2(0.f, 0.f), sum1 = sum0;
-                    if (__any_sync(0xffffffffu, fabsf(base) > kFar)) {
-                        sum0.x = far_weights(trow + a * 128, seen, row_scale, base, ti);
-                    } else {
+                        const float base = m == -INFINITY ? 0.f : m;
+                        uint32_t w[16];
+                        if (__any_sync(0xffffffffu, fabsf(base) > kFar)) {
 #pragma unroll
-                        for (int c = 0; c < 8; ++c) {
-                            const float* y = s[c / 2] + 16 * (c & 1);
-                            const float4 f = ti.part[c];
-                            const float fx = fmaxf(row_scale * f.x, kTiny), fb = f.y - base;
-                            const float2 scale2 = make_float2(fx, fx), base2 = make_float2(fb, fb), drop2 = make_float2(f.z, f.z);
-                            uint32_t w[8];
-#pragma unroll
-                            for (int i = 0; i < 8; ++i) {
-                                float2 e = __ffma2_rn(make_float2(y[2 * i], y[2 * i + 1]), scale2, base2);
-                                e = make_float2(ex2(e.x), ex2(e.y));
-                                if (i & 1) sum1 = __ffma2_rn(e, drop2, sum1);
-                                else sum0 = __ffma2_rn(e, drop2, sum0);
-                                w[i] = half2(e.x, e.y);
+                            for (int i = 0; i < 32; i += 2) {
+                                const float4& f = i < 16 ? f0 : f1;
+                                const float sc = i < 16 ? scale0 : scale1;
+                                const float e0 = ex2(__fsub_rn(__fmul_rn(s[i], sc), base) + f.y);
+                                const float e1 = ex2(__fsub_rn(__fmul_rn(s[i + 1], sc), base) + f.y);
+                                l2.x += e0 * f.z, l2.y += e1 * f.z;
+                                w[i / 2] = half2(e0, e1);
                             }
-                            tmem_st8(trow + a * 128 + 8 * c, w);
+                        } else {
+#pragma unroll
+                            for (int k = 0; k < 2; ++k) {
+                                const float fx = k ? scale1 : scale0, fb = (k ? f1.y : f0.y) - base, fz = k ? f1.z : f0.z;
+                                const float2 scale2 = make_float2(fx, fx), base2 = make_float2(fb, fb), drop2 = make_float2(fz, fz);
+#pragma unroll
+                                for (int i = 0; i < 8; ++i) {
+                                    float2 e = __ffma2_rn(make_float2(s[16 * k + 2 * i], s[16 * k + 2 * i + 1]), scale2, base2);
+                                    e = make_float2(ex2(e.x), ex2(e.y));
+                                    l2 = __ffma2_rn(e, drop2, l2);
+                                    w[8 * k + i] = half2(e.x, e.y);
+                                }
+                            }
                         }
-                    }
-                    l += (sum0.x + sum0.y) + (sum1.x + sum1.y);
+                        tmem_st16(ts + 16 * c, w);
+                    };
+#pragma unroll 1
+                    for (int c = 0; c < 4; ++c) chunk(c);
                     tmem_st_wait();
                 }
                 tc_fence_before();
@@ -572,6 +562,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_cons
                 tc_fence_after();
             }
             if (!busy) continue;
+            const float l = l2.x + l2.y;
             const bool some = l != 0.f, whole = x.whole();
             const float unit = item_v * 0.0078125f;   // of O: 2^-kLift
             const float inv = some ? unit / l : 0.f;
