@@ -47,6 +47,7 @@ using tc::proxy_fence;
 using tc::tc_fence_after;
 using tc::tc_fence_before;
 using tc::tmem_ld32;
+using tc::tmem_ld32x2;
 using tc::tmem_st16;
 using tc::tmem_st_wait;
 using tc::umma_commit;
@@ -110,6 +111,37 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
         : "r"(taddr)
         : "memory");
 }
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8]) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(r[0]), "r"(r[1]),
+                 "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+                 : "memory");
+}
+
+// What a risen maximum changes: the weights of a tile that are written (`chunks` times 16 columns from ts on) by f, and O (`pieces` of 16 columns from to
+// on) by fo.  Functions by themselves, so that the loop of the softmax stays small.
+__device__ __noinline__ void rescale(uint32_t ts, int chunks, float f, uint32_t to, int pieces, float fo) {
+    tmem_st_wait();   // what is read here has been written
+#pragma unroll 1
+    for (int k = 0; k < chunks; ++k) {
+        uint32_t w[16];
+        tmem_ld16(ts + 16 * k, w);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
+            w[i] = half2(x.x * f, x.y * f);
+        }
+        tmem_st16(ts + 16 * k, w);
+    }
+#pragma unroll 1
+    for (int k = 0; k < pieces; ++k) {
+        uint32_t o[16];
+        tmem_ld16(to + 16 * k, o);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * fo);
+        tmem_st16(to + 16 * k, o);
+    }
+}
+
 // 16 e4m3 as f16
 __device__ __forceinline__ void widen16(const uint4& u, uint32_t (&y)[8]) {
     const uint32_t w[4] = {u.x, u.y, u.z, u.w};
@@ -126,6 +158,25 @@ struct TileInfo {
     float4 part[kKeys / 16];
     float v, unused[3];
 };
+
+// The weights of a tile's chunk c for rows far from zero, over its scores; returns their sum.
+__device__ __noinline__ float far_weights(uint32_t ts, int c, int seen, float row_scale, float base, float4 f) {
+    const float scale = fmaxf(row_scale * f.x, kTiny);
+    float sum = 0.f;
+    uint32_t x[16], w[8];
+    tmem_ld16(ts + 16 * c, x);
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+        const float y = __fsub_rn(__fmul_rn(__uint_as_float(x[i]), scale), base);
+        const float e = 16 * c + i < seen ? ex2(y + f.y) : 0.f;
+        x[i] = __float_as_uint(e);
+        sum += e * f.z;
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) w[i] = half2(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1]));
+    tmem_st8(ts + 8 * c, w);
+    return sum;
+}
 
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_constant__ PagedParams p) {
@@ -460,7 +511,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_cons
                 mbar_arrive(&q_ready[a]);
             }
             float m = -INFINITY, item_v = 0.f;
-            float2 l2 = make_float2(0.f, 0.f);
+            float2 la = make_float2(0.f, 0.f), lb = la;
             for (int j = 0; j < n; ++j, ++mine) {
                 ok = warp_wait(&s_full[a], mine);
                 if (!ok) break;
@@ -470,86 +521,64 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_cons
                     const bool hide = __any_sync(0xffffffffu, seen < kKeys);
                     const TileInfo& ti = info[(it0 + j) % F::kInfos];
                     const uint32_t ts = trow + a * 128, to = trow + F::kO + a * D;
-                    // scores 32 c .. 32 c + 31, over whose first half's columns of the chunk before the weights go
-                    auto chunk = [&](int c) {
-                        float s[32];
-                        tmem_ld32(ts + 32 * c, s);
+                    // Scores 64 c .. 64 c + 63: the second half's weights go over columns of the first's scores.
+#pragma unroll 1
+                    for (int c = 0; c < 2; ++c) {
+                        float s0[32], s1[32];
+                        tmem_ld32x2(ts + 64 * c, ts + 64 * c + 32, s0, s1);
                         if (hide) {
 #pragma unroll
-                            for (int i = 0; i < 32; ++i)
-                                if (32 * c + i >= seen) s[i] = -INFINITY;
+                            for (int i = 0; i < 32; ++i) {
+                                if (64 * c + i >= seen) s0[i] = -INFINITY;
+                                if (64 * c + 32 + i >= seen) s1[i] = -INFINITY;
+                            }
                         }
-                        const float4 f0 = ti.part[2 * c], f1 = ti.part[2 * c + 1];
-                        const float scale0 = fmaxf(row_scale * f0.x, kTiny), scale1 = fmaxf(row_scale * f1.x, kTiny);
-                        float t0 = fmaxf(s[0], s[1]), t1 = fmaxf(s[16], s[17]);
+                        const float4* parts = ti.part + 4 * c;
+                        float top = -INFINITY;
 #pragma unroll
-                        for (int i = 2; i < 16; i += 2) {
-                            t0 = fmaxf(fmaxf(t0, s[i]), s[i + 1]);
-                            t1 = fmaxf(fmaxf(t1, s[16 + i]), s[17 + i]);
+                        for (int k = 0; k < 4; ++k) {
+                            const float* s = (k < 2 ? s0 : s1) + 16 * (k & 1);
+                            float t0 = fmaxf(s[0], s[1]), t1 = fmaxf(s[8], s[9]);
+#pragma unroll
+                            for (int i = 2; i < 8; i += 2) t0 = fmaxf(fmaxf(t0, s[i]), s[i + 1]), t1 = fmaxf(fmaxf(t1, s[8 + i]), s[9 + i]);
+                            top = fmaxf(top, fmaxf(t0, t1) * fmaxf(row_scale * parts[k].x, kTiny));
                         }
-                        const float top = fmaxf(t0 * scale0, t1 * scale1);
                         const bool rise = valid && (top > m + kRise || m == -INFINITY), grow = c == 0 && ti.v > item_v;
                         if (__any_sync(0xffffffffu, rise || grow)) {
                             // by a power of two, which the weights that are f16 already take without another rounding
                             const float up = ceilf(top - m);   // (infinite for a first maximum)
                             const bool far = !(up <= 100.f);
-                            float f = !rise ? 1.f : far ? 0.f : ex2(-up);
+                            const float f = !rise ? 1.f : far ? 0.f : ex2(-up);
                             if (rise) m = far ? top : m + up;
-                            l2 = make_float2(l2.x * f, l2.y * f);
-                            tmem_st_wait();   // what is read here has been written
-#pragma unroll 1
-                            for (int k = 0; k < c; ++k) {   // this tile's weights so far
-                                uint32_t w[16];
-                                tmem_ld16(ts + 16 * k, w);
-#pragma unroll
-                                for (int i = 0; i < 16; ++i) {
-                                    const float2 y = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
-                                    w[i] = half2(y.x * f, y.y * f);
-                                }
-                                tmem_st16(ts + 16 * k, w);
-                            }
-                            if (grow) f *= item_v / ti.v, item_v = ti.v;
-                            if (j > 0) {   // every earlier product into O is done: s_full came after them
-#pragma unroll 1
-                                for (int k = 0; k < D / 16; ++k) {
-                                    uint32_t o[16];
-                                    tmem_ld16(to + 16 * k, o);
-#pragma unroll
-                                    for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
-                                    tmem_st16(to + 16 * k, o);
-                                }
-                            }
+                            la = make_float2(la.x * f, la.y * f), lb = make_float2(lb.x * f, lb.y * f);
+                            float fo = f;
+                            if (grow) fo *= item_v / ti.v, item_v = ti.v;
+                            rescale(ts, 2 * c, f, to, j > 0 ? D / 16 : 0, fo);
                         }
                         const float base = m == -INFINITY ? 0.f : m;
-                        uint32_t w[16];
                         if (__any_sync(0xffffffffu, fabsf(base) > kFar)) {
-#pragma unroll
-                            for (int i = 0; i < 32; i += 2) {
-                                const float4& f = i < 16 ? f0 : f1;
-                                const float sc = i < 16 ? scale0 : scale1;
-                                const float e0 = ex2(__fsub_rn(__fmul_rn(s[i], sc), base) + f.y);
-                                const float e1 = ex2(__fsub_rn(__fmul_rn(s[i + 1], sc), base) + f.y);
-                                l2.x += e0 * f.z, l2.y += e1 * f.z;
-                                w[i / 2] = half2(e0, e1);
-                            }
-                        } else {
-#pragma unroll
-                            for (int k = 0; k < 2; ++k) {
-                                const float fx = k ? scale1 : scale0, fb = (k ? f1.y : f0.y) - base, fz = k ? f1.z : f0.z;
-                                const float2 scale2 = make_float2(fx, fx), base2 = make_float2(fb, fb), drop2 = make_float2(fz, fz);
-#pragma unroll
-                                for (int i = 0; i < 8; ++i) {
-                                    float2 e = __ffma2_rn(make_float2(s[16 * k + 2 * i], s[16 * k + 2 * i + 1]), scale2, base2);
-                                    e = make_float2(ex2(e.x), ex2(e.y));
-                                    l2 = __ffma2_rn(e, drop2, l2);
-                                    w[8 * k + i] = half2(e.x, e.y);
-                                }
-                            }
-                        }
-                        tmem_st16(ts + 16 * c, w);
-                    };
 #pragma unroll 1
-                    for (int c = 0; c < 4; ++c) chunk(c);
+                            for (int k = 0; k < 4; ++k) la.x += far_weights(ts, 4 * c + k, seen, row_scale, base, parts[k]);
+                            continue;
+                        }
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            const float* s = (k < 2 ? s0 : s1) + 16 * (k & 1);
+                            const float4 f4 = parts[k];
+                            const float fx = fmaxf(row_scale * f4.x, kTiny), fb = f4.y - base;
+                            const float2 scale2 = make_float2(fx, fx), base2 = make_float2(fb, fb), drop2 = make_float2(f4.z, f4.z);
+                            uint32_t w[8];
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) {
+                                float2 e = __ffma2_rn(make_float2(s[2 * i], s[2 * i + 1]), scale2, base2);
+                                e = make_float2(ex2(e.x), ex2(e.y));
+                                if (i & 1) lb = __ffma2_rn(e, drop2, lb);
+                                else la = __ffma2_rn(e, drop2, la);
+                                w[i] = half2(e.x, e.y);
+                            }
+                            tmem_st8(ts + 32 * c + 8 * k, w);
+                        }
+                    }
                     tmem_st_wait();
                 }
                 tc_fence_before();
@@ -562,7 +591,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_cons
                 tc_fence_after();
             }
             if (!busy) continue;
-            const float l = l2.x + l2.y;
+            const float l = (la.x + la.y) + (lb.x + lb.y);
             const bool some = l != 0.f, whole = x.whole();
             const float unit = item_v * 0.0078125f;   // of O: 2^-kLift
             const float inv = some ? unit / l : 0.f;
