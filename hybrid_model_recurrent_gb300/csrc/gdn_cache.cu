@@ -55,121 +55,126 @@ struct Vec<float> {
 // are the angle without whole turns, to 2^-33 of a turn at any position; the nearest quarter turn is then
 // taken off as an integer, and what is left (an eighth of a turn at most) goes to fp32.
 //
-// Bound by memory: each element is read and written once.
+// Bound by memory: each element is read and written once.  The next heads' loads are issued before the ones at hand are
+// computed, and the arithmetic is on pairs of fp32.
 template <typename T, int D, bool HALF>
 __global__ void __launch_bounds__(128) rope_kernel(const __grid_constant__ RopeParams p) {
     using V = Vec<T>;
     constexpr int N = V::N, L = D / (2 * N), HP = 32 / L, U = 2;
+    __shared__ uint64_t s_freq[D / 2];
     const int lane = threadIdx.x & 31, j = lane % L, hsub = lane / L;
-    const int heads = p.Hq + p.Hk;
+    const int q_passes = (p.Hq + HP - 1) / HP, passes = q_passes + (p.Hk + HP - 1) / HP;
     const bool turned = 2 * N * j < p.rd;
-    // the lane's two pieces, in elements
-    int ea, eb;
-    if (HALF) {
-        ea = (turned ? j : 2 * j) * N;
-        eb = turned ? ea + p.rd / 2 : ea + N;
-    } else {
-        ea = 2 * j * N, eb = ea + N;
+    const int ea = (HALF && turned ? j : 2 * j) * N, eb = HALF && turned ? ea + p.rd / 2 : ea + N;   // the lane's two pieces
+    for (int i = threadIdx.x; i < p.rd / 2; i += 128) {
+        const double turns = p.inv_freq[i] * 0.15915494309189535;
+        s_freq[i] = __double2ull_rn((turns - floor(turns)) * 18446744073709551616.0);
     }
-    uint64_t freq[N];
-    float wq[2][N], wk[2][N];
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-        freq[i] = 0;
-        wq[0][i] = wq[1][i] = wk[0][i] = wk[1][i] = 1.f;
-    }
-    if (turned) {
-#pragma unroll
-        for (int i = 0; i < N; ++i) {
-            const double turns = p.inv_freq[j * N + i] * 0.15915494309189535;
-            freq[i] = __double2ull_rn((turns - floor(turns)) * 18446744073709551616.0);
-        }
-    }
-    if (p.normalize) {
-        if (p.qw) {
-            V::get(*reinterpret_cast<const uint4*>(static_cast<const T*>(p.qw) + ea), wq[0]);
-            V::get(*reinterpret_cast<const uint4*>(static_cast<const T*>(p.qw) + eb), wq[1]);
-        }
-        if (p.kw) {
-            V::get(*reinterpret_cast<const uint4*>(static_cast<const T*>(p.kw) + ea), wk[0]);
-            V::get(*reinterpret_cast<const uint4*>(static_cast<const T*>(p.kw) + eb), wk[1]);
-        }
-    }
+    __syncthreads();
     const int64_t units = p.T * p.parts, warps = (int64_t)gridDim.x * 4;
     for (int64_t u = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5); u < units; u += warps) {
         const int64_t t = u / p.parts;
-        const int first = (int)(u - t * p.parts) * p.per_part, last = min(first + p.per_part, (heads + HP - 1) / HP);
-        float cs[N], sn[N];
+        const int first = (int)(u - t * p.parts) * p.per_part, last = min(first + p.per_part, passes);
+        // the queries' passes, then the keys'
+        auto place = [&](int g, bool out) -> T* {   // of this lane's head of pass g; nullptr: none
+            const bool k = g >= q_passes;
+            const int head = (k ? g - q_passes : g) * HP + hsub;
+            if (g >= last || head >= (k ? p.Hk : p.Hq)) return nullptr;
+            const void* base = k ? (out ? p.k_out : p.k) : (out ? p.q_out : p.q);
+            const int64_t stride = k ? (out ? p.ko_stride : p.k_stride) : (out ? p.qo_stride : p.q_stride);
+            return static_cast<T*>(const_cast<void*>(base)) + t * stride + head * D;
+        };
+        uint4 next[U][2];
+        auto fetch = [&](int g) {
+#pragma unroll
+            for (int x = 0; x < U; ++x) {
+                const T* src = place(g + x, false);
+                next[x][0] = next[x][1] = make_uint4(0, 0, 0, 0);
+                if (src) {
+                    next[x][0] = *reinterpret_cast<const uint4*>(src + ea);
+                    next[x][1] = *reinterpret_cast<const uint4*>(src + eb);
+                }
+            }
+        };
+        fetch(first);
+        float2 cs[N / 2], sn[N / 2];
         const int64_t pos = turned ? p.positions[t] : 0;
 #pragma unroll
         for (int i = 0; i < N; ++i) {
-            const uint64_t a = (uint64_t)pos * freq[i];
+            const uint64_t a = (uint64_t)pos * (turned ? s_freq[j * N + i] : 0);
             const uint32_t quarter = (uint32_t)((a + (1ull << 61)) >> 62);
             const int64_t rest = (int64_t)(a - ((uint64_t)quarter << 62));
             float s, c;
             sincospif(__ll2float_rn(rest) * 1.0842021724855044e-19f, &s, &c);   // 2^-63: half turns
             const float cc = quarter & 1 ? s : c, ss = quarter & 1 ? c : s;
-            cs[i] = ((quarter + 1) & 2 ? -cc : cc) * p.mscale;
-            sn[i] = (quarter & 2 ? -ss : ss) * p.mscale;
+            const float cv = ((quarter + 1) & 2 ? -cc : cc) * p.mscale, sv = (quarter & 2 ? -ss : ss) * p.mscale;
+            if (i & 1) cs[i / 2].y = cv, sn[i / 2].y = sv;
+            else cs[i / 2].x = cv, sn[i / 2].x = sv;
         }
+        float2 wa[N / 2], wb[N / 2];
+        auto weights = [&](const void* w) {
+            float a[N], b[N];
+#pragma unroll
+            for (int i = 0; i < N; ++i) a[i] = b[i] = 1.f;
+            if (w) {
+                V::get(*reinterpret_cast<const uint4*>(static_cast<const T*>(w) + ea), a);
+                V::get(*reinterpret_cast<const uint4*>(static_cast<const T*>(w) + eb), b);
+            }
+#pragma unroll
+            for (int i = 0; i < N / 2; ++i) wa[i] = make_float2(a[2 * i], a[2 * i + 1]), wb[i] = make_float2(b[2 * i], b[2 * i + 1]);
+        };
+        if (p.normalize) weights(first < q_passes ? p.qw : p.kw);
         for (int g = first; g < last; g += U) {
             uint4 in[U][2];
 #pragma unroll
-            for (int x = 0; x < U; ++x) {
-                const int head = (g + x) * HP + hsub;
-                if (g + x < last && head < heads) {
-                    const T* src = head < p.Hq ? static_cast<const T*>(p.q) + t * p.q_stride + head * D
-                                               : static_cast<const T*>(p.k) + t * p.k_stride + (head - p.Hq) * D;
-                    in[x][0] = *reinterpret_cast<const uint4*>(src + ea);
-                    in[x][1] = *reinterpret_cast<const uint4*>(src + eb);
-                } else {
-                    in[x][0] = in[x][1] = make_uint4(0, 0, 0, 0);
-                }
-            }
+            for (int x = 0; x < U; ++x) in[x][0] = next[x][0], in[x][1] = next[x][1];
+            fetch(g + U);
 #pragma unroll
             for (int x = 0; x < U; ++x) {
-                const int head = (g + x) * HP + hsub;
-                const bool is_q = head < p.Hq;
-                float a[N], b[N];
-                V::get(in[x][0], a);
-                V::get(in[x][1], b);
+                if (p.normalize && g + x == q_passes) weights(p.kw);   // (the same for the whole warp)
+                float fa[N], fb[N];
+                V::get(in[x][0], fa);
+                V::get(in[x][1], fb);
+                float2 a[N / 2], b[N / 2];
+#pragma unroll
+                for (int i = 0; i < N / 2; ++i) a[i] = make_float2(fa[2 * i], fa[2 * i + 1]), b[i] = make_float2(fb[2 * i], fb[2 * i + 1]);
                 if (p.normalize) {
-                    float sum = 0.f;
+                    float2 s2 = make_float2(0.f, 0.f);
 #pragma unroll
-                    for (int i = 0; i < N; ++i) sum = fmaf(a[i], a[i], sum), sum = fmaf(b[i], b[i], sum);
+                    for (int i = 0; i < N / 2; ++i) s2 = __ffma2_rn(a[i], a[i], s2), s2 = __ffma2_rn(b[i], b[i], s2);
+                    float sum = s2.x + s2.y;
 #pragma unroll
                     for (int o = L / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
                     const float r = rsqrtf(sum * (1.f / D) + p.eps);
+                    const float2 r2 = make_float2(r, r);
 #pragma unroll
-                    for (int i = 0; i < N; ++i) {
-                        a[i] *= r * (is_q ? wq[0][i] : wk[0][i]);
-                        b[i] *= r * (is_q ? wq[1][i] : wk[1][i]);
-                    }
+                    for (int i = 0; i < N / 2; ++i)
+                        a[i] = __fmul2_rn(a[i], __fmul2_rn(r2, wa[i])), b[i] = __fmul2_rn(b[i], __fmul2_rn(r2, wb[i]));
                 }
                 if (turned) {
                     if (HALF) {
 #pragma unroll
-                        for (int i = 0; i < N; ++i) {
-                            const float y = a[i];
-                            a[i] = y * cs[i] - b[i] * sn[i];
-                            b[i] = b[i] * cs[i] + y * sn[i];
+                        for (int i = 0; i < N / 2; ++i) {
+                            const float2 y = a[i], ns = make_float2(-sn[i].x, -sn[i].y);
+                            a[i] = __ffma2_rn(y, cs[i], __fmul2_rn(b[i], ns));
+                            b[i] = __ffma2_rn(b[i], cs[i], __fmul2_rn(y, sn[i]));
                         }
                     } else {
 #pragma unroll
-                        for (int i = 0; i < N / 2; ++i) {
-                            const float y = a[2 * i], z = b[2 * i];
-                            a[2 * i] = y * cs[i] - a[2 * i + 1] * sn[i];
-                            a[2 * i + 1] = a[2 * i + 1] * cs[i] + y * sn[i];
-                            b[2 * i] = z * cs[N / 2 + i] - b[2 * i + 1] * sn[N / 2 + i];
-                            b[2 * i + 1] = b[2 * i + 1] * cs[N / 2 + i] + z * sn[N / 2 + i];
+                        for (int i = 0; i < N / 2; ++i) {   // pair 2 i, 2 i + 1 of one piece; N / 2 of them in each
+                            const float ca = i & 1 ? cs[i / 2].y : cs[i / 2].x, sa = i & 1 ? sn[i / 2].y : sn[i / 2].x;
+                            const float cb = i & 1 ? cs[N / 4 + i / 2].y : cs[N / 4 + i / 2].x;
+                            const float sb = i & 1 ? sn[N / 4 + i / 2].y : sn[N / 4 + i / 2].x;
+                            a[i] = make_float2(a[i].x * ca - a[i].y * sa, a[i].y * ca + a[i].x * sa);
+                            b[i] = make_float2(b[i].x * cb - b[i].y * sb, b[i].y * cb + b[i].x * sb);
                         }
                     }
                 }
-                if (g + x < last && head < heads) {
-                    T* dst = is_q ? static_cast<T*>(p.q_out) + t * p.qo_stride + head * D
-                                  : static_cast<T*>(p.k_out) + t * p.ko_stride + (head - p.Hq) * D;
-                    *reinterpret_cast<uint4*>(dst + ea) = V::put(a);
-                    *reinterpret_cast<uint4*>(dst + eb) = V::put(b);
+                if (T* dst = place(g + x, true)) {
+#pragma unroll
+                    for (int i = 0; i < N / 2; ++i) fa[2 * i] = a[i].x, fa[2 * i + 1] = a[i].y, fb[2 * i] = b[i].x, fb[2 * i + 1] = b[i].y;
+                    *reinterpret_cast<uint4*>(dst + ea) = V::put(fa);
+                    *reinterpret_cast<uint4*>(dst + eb) = V::put(fb);
                 }
             }
         }
@@ -179,8 +184,7 @@ __global__ void __launch_bounds__(128) rope_kernel(const __grid_constant__ RopeP
 template <typename T, int D>
 cudaError_t rope(const RopeParams& p, bool half, cudaStream_t s) {
     const int64_t units = p.T * p.parts, need = (units + 3) / 4;
-    // four CTAs of 128 threads a multiprocessor's worth of registers hold; more units than that take turns
-    const unsigned grid = (unsigned)std::min<int64_t>(need, (int64_t)kSms * 8);
+    const unsigned grid = (unsigned)std::min<int64_t>(need, (int64_t)kSms * 12);   // more units than warps take turns
     if (half) rope_kernel<T, D, true><<<grid, 128, 0, s>>>(p);
     else rope_kernel<T, D, false><<<grid, 128, 0, s>>>(p);
     return cudaGetLastError();
@@ -202,8 +206,8 @@ __device__ __forceinline__ float2 from_e4m3x2(uint32_t u) {
     return __half22float2(*reinterpret_cast<const __half2*>(&h));
 }
 // the exponent of the least power of two with which `top` is at most 448 (1.75 * 2^8) times it: the bits below 1.75 carry
-__device__ __forceinline__ int scale_exponent(float top) {
-    return min(max((int)((__float_as_uint(top) + 0x1fffffu) >> 23) - 127 - 8, -126), 120);
+__device__ __forceinline__ int scale_exponent(uint32_t top) {   // (as bits)
+    return min(max((int)((top + 0x1fffffu) >> 23) - 127 - 8, -126), 120);
 }
 
 template <typename T, int D, int TPB, int NCH>
@@ -211,7 +215,7 @@ __global__ void __launch_bounds__(256) append_kernel(const __grid_constant__ App
     constexpr int PER = 256 / TPB;            // blocks of a CTA
     constexpr int VEC = 16 / sizeof(T), LD = 8 / VEC;   // a chunk is 8 values: LD loads
     constexpr int CPT = D / 8;                // chunks of a token
-    __shared__ float s_top[8];
+    __shared__ uint32_t s_top[8];
     const Cache& c = p.c;
     const int tid = threadIdx.x % TPB, sub = threadIdx.x / TPB;
     const int blocks = 2 * c.Hkv, groups = (blocks + PER - 1) / PER;
@@ -249,31 +253,56 @@ __global__ void __launch_bounds__(256) append_kernel(const __grid_constant__ App
             for (int y = 0; y < LD; ++y) in[x][y] = *reinterpret_cast<const uint4*>(a + y * VEC);
         }
     }
-    float top = 0.f;
+    // The largest value by its bits (two of bf16 at a time).  Where that is no finite number, which is rare, the others are looked
+    // through again.
+    auto agree = [&](uint32_t y) {
+        y = __reduce_max_sync(0xffffffffu, y);
+        if (TPB > 32) {
+            __syncthreads();
+            if ((threadIdx.x & 31) == 0) s_top[threadIdx.x >> 5] = y;
+            __syncthreads();
+#pragma unroll
+            for (int x = 0; x < 8; ++x) y = max(y, s_top[x]);
+        } else {
+            __syncwarp();   // every lane has `was`
+        }
+        return y;
+    };
+    uint32_t bits = 0;
 #pragma unroll
     for (int x = 0; x < NCH; ++x) {
         if (x * TPB + tid < chunks) {
 #pragma unroll
             for (int y = 0; y < LD; ++y) {
-                float f[VEC];
-                Vec<T>::get(in[x][y], f);
+                const uint32_t w[4] = {in[x][y].x, in[x][y].y, in[x][y].z, in[x][y].w};
 #pragma unroll
-                for (int z = 0; z < VEC; ++z) top = fmaxf(top, fabsf(f[z]) <= FLT_MAX ? fabsf(f[z]) : 0.f);
+                for (int z = 0; z < 4; ++z)
+                    bits = sizeof(T) == 2 ? __vmaxu2(bits, w[z] & 0x7fff7fffu) : max(bits, w[z] & 0x7fffffffu);
             }
         }
     }
+    if (sizeof(T) == 2) bits = max(bits & 0xffffu, bits >> 16) << 16;
+    bits = agree(bits);
+    const bool odd = bits >= 0x7f800000u;
+    if (odd) {
+        bits = 0;
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-    if (TPB > 32) {
-        if ((threadIdx.x & 31) == 0) s_top[threadIdx.x >> 5] = top;
-        __syncthreads();
+        for (int x = 0; x < NCH; ++x) {
+            if (x * TPB + tid < chunks) {
 #pragma unroll
-        for (int x = 0; x < 8; ++x) top = fmaxf(top, s_top[x]);
-    } else {
-        __syncwarp();   // every lane has `was`
+                for (int y = 0; y < LD; ++y) {
+                    float f[VEC];
+                    Vec<T>::get(in[x][y], f);
+#pragma unroll
+                    for (int z = 0; z < VEC; ++z)
+                        if (fabsf(f[z]) <= FLT_MAX) bits = max(bits, __float_as_uint(fabsf(f[z])));
+                }
+            }
+        }
+        bits = agree(bits);
     }
     if (!work) return;
-    float scale = __uint_as_float((uint32_t)(scale_exponent(top) + 127) << 23);
+    float scale = __uint_as_float((uint32_t)(scale_exponent(bits) + 127) << 23);
     const bool grows = lo > 0 && scale > was;
     if (lo > 0 && !grows) scale = was;
     const float inv = 1.f / scale;
@@ -288,7 +317,7 @@ __global__ void __launch_bounds__(256) append_kernel(const __grid_constant__ App
                 float g[VEC];
                 Vec<T>::get(in[x][y], g);
 #pragma unroll
-                for (int z = 0; z < VEC; ++z) f[y * VEC + z] = fabsf(g[z]) <= FLT_MAX ? g[z] * inv : __uint_as_float(0x7fc00000u);
+                for (int z = 0; z < VEC; ++z) f[y * VEC + z] = !odd || fabsf(g[z]) <= FLT_MAX ? g[z] * inv : __uint_as_float(0x7fc00000u);
             }
             *reinterpret_cast<uint2*>(dst + (int64_t)lo * D + ch * 8) =
                 make_uint2(to_e4m3x4(f[0], f[1], f[2], f[3]), to_e4m3x4(f[4], f[5], f[6], f[7]));
@@ -631,9 +660,9 @@ cudaError_t launch_copies(const UpkeepParams& p, bool remap, int64_t most, cudaS
 
 }  // namespace
 
-int rope_passes(int heads, int D, bool bf16) {
+int rope_passes(int Hq, int Hk, int D, bool bf16) {
     const int at_once = 32 / (D / (bf16 ? 16 : 8));
-    return (heads + at_once - 1) / at_once;
+    return (Hq + at_once - 1) / at_once + (Hk + at_once - 1) / at_once;
 }
 
 cudaError_t launch_rope(const RopeParams& p, int D, bool bf16, bool half, cudaStream_t s) {

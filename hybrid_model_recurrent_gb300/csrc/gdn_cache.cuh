@@ -102,7 +102,7 @@ constexpr int kMaxRows = 16384;
 constexpr int kMaxBatch = 4096;
 
 cudaError_t launch_rope(const RopeParams& p, int D, bool bf16, bool half, cudaStream_t s);
-int rope_passes(int heads, int D, bool bf16);
+int rope_passes(int Hq, int Hk, int D, bool bf16);
 cudaError_t launch_append(const AppendParams& p, int D, bool bf16, cudaStream_t s);
 cudaError_t launch_update(const UpkeepParams& p, cudaStream_t s);
 cudaError_t launch_compact(const UpkeepParams& p, cudaStream_t s);

@@ -176,7 +176,7 @@ GDN_EXPORT gdn_status gdn_qk_norm_rope(const gdn_rope_problem* f, const void* q,
     p.normalize = f->normalize != 0, p.eps = f->eps, p.mscale = f->mscale;
     // A token's heads go to one warp, whose sines then serve them all, unless there are too few tokens to fill the GPU.
     const bool bf16 = f->dtype == GDN_BF16;
-    const int passes = rope_passes(p.Hq + p.Hk, f->head_dim, bf16);
+    const int passes = rope_passes(p.Hq, p.Hk, f->head_dim, bf16);
     const int64_t wanted = (int64_t)kSms * 16;
     p.parts = (int)std::min<int64_t>(passes, std::max<int64_t>(1, wanted / p.T));
     p.per_part = (int)ceil_div(passes, p.parts);
