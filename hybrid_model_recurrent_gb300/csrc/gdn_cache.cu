@@ -195,7 +195,8 @@ cudaError_t rope(const RopeParams& p, bool half, cudaStream_t s) {
 // A block (page x head, keys or values) is taken by TPB threads: they read its new tokens once into registers, agree on the
 // largest value, and write the bytes.  Tokens that the block holds already are touched only when the scale grows.
 // TPB is 32 for calls with at most 8 new tokens a request (decode, drafts: a block has little to do, and eight of them
-// share a CTA), 256 else.
+// share a CTA), 256 else.  A CTA takes `share` blocks of one page in turn: what it has to find out first, four loads that wait
+// for one another, took half of its time where every block had a CTA of its own.
 __device__ __forceinline__ uint32_t to_e4m3x4(float a, float b, float c, float d) {
     const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
     const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(c, d), __NV_SATFINITE, __NV_E4M3);
@@ -211,16 +212,16 @@ __device__ __forceinline__ int scale_exponent(uint32_t top) {   // (as bits)
 }
 
 template <typename T, int D, int TPB, int NCH>
-__global__ void __launch_bounds__(256) append_kernel(const __grid_constant__ AppendParams p) {
+__global__ void __launch_bounds__(256) append_kernel(const __grid_constant__ AppendParams p, const int share) {
     constexpr int PER = 256 / TPB;            // blocks of a CTA
     constexpr int VEC = 16 / sizeof(T), LD = 8 / VEC;   // a chunk is 8 values: LD loads
     constexpr int CPT = D / 8;                // chunks of a token
     __shared__ uint32_t s_top[8];
     const Cache& c = p.c;
     const int tid = threadIdx.x % TPB, sub = threadIdx.x / TPB;
-    const int blocks = 2 * c.Hkv, groups = (blocks + PER - 1) / PER;
+    const int blocks = 2 * c.Hkv, groups = (blocks + share - 1) / share;
     const int b = blockIdx.y;
-    const int i0 = blockIdx.x / groups, block = (blockIdx.x - i0 * groups) * PER + sub;
+    const int i0 = blockIdx.x / groups, block0 = (blockIdx.x - i0 * groups) * share;
     const Request rq = request_at(c, p.t, b);
     if (rq.bad && blockIdx.x == 0 && threadIdx.x == 0) atomicOr(p.status, STATUS_BAD_INDEX);
     if (rq.row < 0 || rq.n == 0 || rq.bad) return;
@@ -233,116 +234,123 @@ __global__ void __launch_bounds__(256) append_kernel(const __grid_constant__ App
         return;
     }
     const int lo = max(start - base, 0), n = min(rq.len - base, c.page) - lo;   // the block's new tokens: lo .. lo + n
-    const bool work = block < blocks;
-    const int kv = block >= c.Hkv, h = block - kv * c.Hkv;
-    const T* src = (kv ? static_cast<const T*>(p.v) + (rq.first + skip + (int64_t)(base + lo - start)) * p.v_stride
-                       : static_cast<const T*>(p.k) + (rq.first + skip + (int64_t)(base + lo - start)) * p.k_stride) + h * D;
-    const int64_t stride = kv ? p.v_stride : p.k_stride;
-    const int64_t at = ((int64_t)pg * 2 + kv) * c.Hkv + h;
-    const int chunks = work ? n * CPT : 0;
-    float was = 0.f;
-    if (work && lo > 0) was = c.scales[at];   // (before anyone writes it)
+    const int end = min(block0 + share, blocks);
+    for (int at0 = block0; at0 < end; at0 += PER) {
+        const int block = at0 + sub;
+        const bool work = block < end;
+        const int kv = block >= c.Hkv, h = block - kv * c.Hkv;
+        const T* src = (kv ? static_cast<const T*>(p.v) + (rq.first + skip + (int64_t)(base + lo - start)) * p.v_stride
+                           : static_cast<const T*>(p.k) + (rq.first + skip + (int64_t)(base + lo - start)) * p.k_stride) + h * D;
+        const int64_t stride = kv ? p.v_stride : p.k_stride;
+        const int64_t at = ((int64_t)pg * 2 + kv) * c.Hkv + h;
+        const int chunks = work ? n * CPT : 0;
+        float was = 0.f;
+        if (work && lo > 0) was = c.scales[at];   // (before anyone writes it)
 
-    uint4 in[NCH][LD];
+        uint4 in[NCH][LD];
 #pragma unroll
-    for (int x = 0; x < NCH; ++x) {
-        const int ch = x * TPB + tid;
-        if (ch < chunks) {
-            const T* a = src + (int64_t)(ch / CPT) * stride + (ch % CPT) * 8;
+        for (int x = 0; x < NCH; ++x) {
+            const int ch = x * TPB + tid;
+            if (ch < chunks) {
+                const T* a = src + (int64_t)(ch / CPT) * stride + (ch % CPT) * 8;
 #pragma unroll
-            for (int y = 0; y < LD; ++y) in[x][y] = *reinterpret_cast<const uint4*>(a + y * VEC);
-        }
-    }
-    // The largest value by its bits (two of bf16 at a time).  Where that is no finite number, which is rare, the others are looked
-    // through again.
-    auto agree = [&](uint32_t y) {
-        y = __reduce_max_sync(0xffffffffu, y);
-        if (TPB > 32) {
-            __syncthreads();
-            if ((threadIdx.x & 31) == 0) s_top[threadIdx.x >> 5] = y;
-            __syncthreads();
-#pragma unroll
-            for (int x = 0; x < 8; ++x) y = max(y, s_top[x]);
-        } else {
-            __syncwarp();   // every lane has `was`
-        }
-        return y;
-    };
-    uint32_t bits = 0;
-#pragma unroll
-    for (int x = 0; x < NCH; ++x) {
-        if (x * TPB + tid < chunks) {
-#pragma unroll
-            for (int y = 0; y < LD; ++y) {
-                const uint32_t w[4] = {in[x][y].x, in[x][y].y, in[x][y].z, in[x][y].w};
-#pragma unroll
-                for (int z = 0; z < 4; ++z)
-                    bits = sizeof(T) == 2 ? __vmaxu2(bits, w[z] & 0x7fff7fffu) : max(bits, w[z] & 0x7fffffffu);
+                for (int y = 0; y < LD; ++y) in[x][y] = *reinterpret_cast<const uint4*>(a + y * VEC);
             }
         }
-    }
-    if (sizeof(T) == 2) bits = max(bits & 0xffffu, bits >> 16) << 16;
-    bits = agree(bits);
-    const bool odd = bits >= 0x7f800000u;
-    if (odd) {
-        bits = 0;
+        // The largest value by its bits (two of bf16 at a time).  Where that is no finite number, which is rare, the others are looked
+        // through again.
+        auto agree = [&](uint32_t y) {
+            y = __reduce_max_sync(0xffffffffu, y);
+            if (TPB > 32) {
+                __syncthreads();
+                if ((threadIdx.x & 31) == 0) s_top[threadIdx.x >> 5] = y;
+                __syncthreads();
+#pragma unroll
+                for (int x = 0; x < 8; ++x) y = max(y, s_top[x]);
+            } else {
+                __syncwarp();   // every lane has `was`
+            }
+            return y;
+        };
+        uint32_t bits = 0;
 #pragma unroll
         for (int x = 0; x < NCH; ++x) {
             if (x * TPB + tid < chunks) {
 #pragma unroll
                 for (int y = 0; y < LD; ++y) {
-                    float f[VEC];
-                    Vec<T>::get(in[x][y], f);
+                    const uint32_t w[4] = {in[x][y].x, in[x][y].y, in[x][y].z, in[x][y].w};
 #pragma unroll
-                    for (int z = 0; z < VEC; ++z)
-                        if (fabsf(f[z]) <= FLT_MAX) bits = max(bits, __float_as_uint(fabsf(f[z])));
+                    for (int z = 0; z < 4; ++z)
+                        bits = sizeof(T) == 2 ? __vmaxu2(bits, w[z] & 0x7fff7fffu) : max(bits, w[z] & 0x7fffffffu);
                 }
             }
         }
+        if (sizeof(T) == 2) bits = max(bits & 0xffffu, bits >> 16) << 16;
         bits = agree(bits);
-    }
-    if (!work) return;
-    float scale = __uint_as_float((uint32_t)(scale_exponent(bits) + 127) << 23);
-    const bool grows = lo > 0 && scale > was;
-    if (lo > 0 && !grows) scale = was;
-    const float inv = 1.f / scale;
-    unsigned char* dst = c.pages + at * c.page * D;
+        const bool odd = bits >= 0x7f800000u;
+        if (odd) {
+            bits = 0;
 #pragma unroll
-    for (int x = 0; x < NCH; ++x) {
-        const int ch = x * TPB + tid;
-        if (ch < chunks) {
-            float f[8];
+            for (int x = 0; x < NCH; ++x) {
+                if (x * TPB + tid < chunks) {
 #pragma unroll
-            for (int y = 0; y < LD; ++y) {
-                float g[VEC];
-                Vec<T>::get(in[x][y], g);
+                    for (int y = 0; y < LD; ++y) {
+                        float f[VEC];
+                        Vec<T>::get(in[x][y], f);
 #pragma unroll
-                for (int z = 0; z < VEC; ++z) f[y * VEC + z] = !odd || fabsf(g[z]) <= FLT_MAX ? g[z] * inv : __uint_as_float(0x7fc00000u);
+                        for (int z = 0; z < VEC; ++z)
+                            if (fabsf(f[z]) <= FLT_MAX) bits = max(bits, __float_as_uint(fabsf(f[z])));
+                    }
+                }
             }
-            *reinterpret_cast<uint2*>(dst + (int64_t)lo * D + ch * 8) =
-                make_uint2(to_e4m3x4(f[0], f[1], f[2], f[3]), to_e4m3x4(f[4], f[5], f[6], f[7]));
+            bits = agree(bits);
         }
-    }
-    if (grows) {
-        const float ratio = was * inv;   // a power of two
-        for (int ch = tid; ch < lo * CPT; ch += TPB) {
-            uint2* a = reinterpret_cast<uint2*>(dst + ch * 8);
-            uint2 u = *a;
-            const float2 x0 = from_e4m3x2(u.x & 0xffff), x1 = from_e4m3x2(u.x >> 16), x2 = from_e4m3x2(u.y & 0xffff),
-                         x3 = from_e4m3x2(u.y >> 16);
-            u = make_uint2(to_e4m3x4(x0.x * ratio, x0.y * ratio, x1.x * ratio, x1.y * ratio),
-                           to_e4m3x4(x2.x * ratio, x2.y * ratio, x3.x * ratio, x3.y * ratio));
-            *a = u;
+        if (!work) continue;
+        float scale = __uint_as_float((uint32_t)(scale_exponent(bits) + 127) << 23);
+        const bool grows = lo > 0 && scale > was;
+        if (lo > 0 && !grows) scale = was;
+        const float inv = 1.f / scale;
+        unsigned char* dst = c.pages + at * c.page * D;
+#pragma unroll
+        for (int x = 0; x < NCH; ++x) {
+            const int ch = x * TPB + tid;
+            if (ch < chunks) {
+                float f[8];
+#pragma unroll
+                for (int y = 0; y < LD; ++y) {
+                    float g[VEC];
+                    Vec<T>::get(in[x][y], g);
+#pragma unroll
+                    for (int z = 0; z < VEC; ++z) f[y * VEC + z] = !odd || fabsf(g[z]) <= FLT_MAX ? g[z] * inv : __uint_as_float(0x7fc00000u);
+                }
+                *reinterpret_cast<uint2*>(dst + (int64_t)lo * D + ch * 8) =
+                    make_uint2(to_e4m3x4(f[0], f[1], f[2], f[3]), to_e4m3x4(f[4], f[5], f[6], f[7]));
+            }
         }
+        if (grows) {
+            const float ratio = was * inv;   // a power of two
+            for (int ch = tid; ch < lo * CPT; ch += TPB) {
+                uint2* a = reinterpret_cast<uint2*>(dst + ch * 8);
+                uint2 u = *a;
+                const float2 x0 = from_e4m3x2(u.x & 0xffff), x1 = from_e4m3x2(u.x >> 16), x2 = from_e4m3x2(u.y & 0xffff),
+                             x3 = from_e4m3x2(u.y >> 16);
+                u = make_uint2(to_e4m3x4(x0.x * ratio, x0.y * ratio, x1.x * ratio, x1.y * ratio),
+                               to_e4m3x4(x2.x * ratio, x2.y * ratio, x3.x * ratio, x3.y * ratio));
+                *a = u;
+            }
+        }
+        if (tid == 0) c.scales[at] = scale;
     }
-    if (tid == 0) c.scales[at] = scale;
 }
 
 template <typename T, int D, int TPB, int NCH>
 cudaError_t append_n(const AppendParams& p, cudaStream_t s) {
     const int touched = (p.t.max_new + p.c.page - 2) / p.c.page + 1;   // pages that a request's new tokens may lie in
-    const int groups = (2 * p.c.Hkv + 256 / TPB - 1) / (256 / TPB);
-    append_kernel<T, D, TPB, NCH><<<dim3(touched * groups, p.t.B), 256, 0, s>>>(p);
+    // about three CTAs for each that runs at once, blocks of one page in a CTA
+    constexpr int PER = 256 / TPB;
+    const int64_t blocks = 2 * p.c.Hkv, all = (int64_t)touched * p.t.B * blocks;
+    const int share = (int)std::min<int64_t>(blocks, std::max<int64_t>(PER, all / (kSms * 8 * 3)));
+    append_kernel<T, D, TPB, NCH><<<dim3((unsigned)(touched * ((blocks + share - 1) / share)), p.t.B), 256, 0, s>>>(p, share);
     return cudaGetLastError();
 }
 template <typename T, int D>
@@ -359,8 +367,8 @@ cudaError_t append_d(const AppendParams& p, cudaStream_t s) {
 
 // ---- upkeep of pages ------------------------------------------------------------------------------------------------
 //
-// The tables are small and their changes depend on one another, so one CTA makes them; the copies of pages that it asks
-// for follow in a launch of their own over the whole GPU.  Pages are found in rising order by scanning the holders'
+// The tables are small and their changes depend on one another, so one cluster makes them, its CTAs (one for small tables) sharing
+// the rows; the copies of pages that it asks for follow in a launch of their own over the whole GPU.  Pages are found in rising order by scanning the holders'
 // counts, 16384 a round (64 KB), as far as there is need: no list of free pages has to be kept in step with them.
 constexpr int kCtl = 1024;
 
@@ -408,21 +416,25 @@ __device__ __forceinline__ void load16(const int32_t* refs, int N, int at, int (
     }
 }
 
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+// Every CTA of the cluster works out the same lists in its shared memory; the rows' pages are taken in turns by all warps.
 __global__ void __launch_bounds__(kCtl) update_kernel(const __grid_constant__ UpkeepParams p) {
-    extern __shared__ int32_t s_rows[];   // [R] pages needed, then their first one; [R] the fork that a row is; bit 30: freed
+    extern __shared__ int32_t s_rows[];   // [R] whether a row is freed, then its first new page's place; [R] the fork that it is, then needs
     int32_t* s_need = s_rows;
     int32_t* s_fork = s_rows + p.R;
     __shared__ int64_t s_part[32];
-    __shared__ int s_copies;
     constexpr int kNone = 0x7fffffff;
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int tid = threadIdx.x, lane = tid & 31, first_row = blockIdx.x * (kCtl / 32) + (tid >> 5), step = gridDim.x * (kCtl / 32);
     auto pages_of = [&](int len) { return min((int)(((int64_t)max(len, 0) + p.page - 1) >> p.page_log2), p.W); };
     auto good = [&](int pg) {
         const bool ok = pg >= 0 && pg < p.N;
         if (!ok) atomicOr(p.status, STATUS_BAD_INDEX);
         return ok;
     };
-    if (tid == 0) s_copies = 0;
+    if (blockIdx.x == 0 && tid == 0) *p.n_copies = 0;
     for (int r = tid; r < p.R; r += kCtl) s_need[r] = 0, s_fork[r] = kNone;
     __syncthreads();
 
@@ -439,9 +451,10 @@ __global__ void __launch_bounds__(kCtl) update_kernel(const __grid_constant__ Up
     }
     __syncthreads();
     if (p.n_drop + p.n_fork > 0) {
-        for (int r = warp; r < p.R; r += kCtl / 32) {
+        for (int r = first_row; r < p.R; r += step) {
             if (!s_need[r]) continue;
             const int used = pages_of(p.lens[r]);
+#pragma unroll 4
             for (int w = lane; w < used; w += 32) {
                 const int pg = p.table[(int64_t)r * p.W + w];
                 if (good(pg)) atomicSub(&p.refs[pg], 1);
@@ -449,12 +462,13 @@ __global__ void __launch_bounds__(kCtl) update_kernel(const __grid_constant__ Up
             __syncwarp();
             if (lane == 0) p.lens[r] = 0;
         }
-        __syncthreads();
-        for (int r = warp; r < p.R; r += kCtl / 32) {
+        cluster_sync();
+        for (int r = first_row; r < p.R; r += step) {
             if (s_fork[r] == kNone) continue;
             const int a = p.from[s_fork[r]];
             if (s_need[a]) continue;   // freed just now: an empty row
-            const int len = p.lens[a], used = pages_of(len);
+            const int len = now(p.lens + a), used = pages_of(len);
+#pragma unroll 4
             for (int w = lane; w < p.W; w += 32) {
                 const int pg = p.table[(int64_t)a * p.W + w];
                 p.table[(int64_t)r * p.W + w] = pg;
@@ -462,12 +476,9 @@ __global__ void __launch_bounds__(kCtl) update_kernel(const __grid_constant__ Up
             }
             if (lane == 0) p.lens[r] = len;
         }
-        __syncthreads();
     }
-    if (!p.grow) {
-        if (tid == 0) *p.n_copies = 0;
-        return;
-    }
+    cluster_sync();
+    if (!p.grow) return;
 
     // pages that each row needs, and their places among all that are taken.  s_need: the first place; s_fork: bit 31 refused,
     // bit 30 copy the last page, below: the number of pages
@@ -478,14 +489,14 @@ __global__ void __launch_bounds__(kCtl) update_kernel(const __grid_constant__ Up
         int need = 0;
         unsigned flags = 0;
         if (r < p.R) {
-            const int len = max(p.lens[r], 0), more = max(p.grow[r], 0);
+            const int len = max(now(p.lens + r), 0), more = max(p.grow[r], 0);
             if ((int64_t)len + more > (int64_t)p.W * p.page) {
                 flags = kRefused;
             } else if (more > 0) {
                 const int have = pages_of(len);
                 need = pages_of(len + more) - have;
                 if (len & (p.page - 1)) {
-                    const int last = p.table[(int64_t)r * p.W + have - 1];
+                    const int last = now(p.table + (int64_t)r * p.W + have - 1);
                     if (good(last) && now(p.refs + last) > 1) ++need, flags = kCopy;
                 }
             }
@@ -499,24 +510,28 @@ __global__ void __launch_bounds__(kCtl) update_kernel(const __grid_constant__ Up
         }
     }
     // the free pages with the lowest numbers, as many as are needed
-    int64_t found = 0;
-    for (int base = 0; base < p.N && found < carry; base += kCtl * 16) {
-        int x[16], c = 0;
-        load16(p.refs, p.N, base + 16 * tid, x);
+    if (blockIdx.x == 0) {
+        int64_t found = 0;
+        for (int base = 0; base < p.N && found < carry; base += kCtl * 16) {
+            int x[16], c = 0;
+            load16(p.refs, p.N, base + 16 * tid, x);
 #pragma unroll
-        for (int i = 0; i < 16; ++i) c += x[i] == 0;
-        int64_t total;
-        int64_t at = found + block_scan(c, s_part, &total);
+            for (int i = 0; i < 16; ++i) c += x[i] == 0;
+            int64_t total;
+            int64_t at = found + block_scan(c, s_part, &total);
 #pragma unroll
-        for (int i = 0; i < 16; ++i)
-            if (x[i] == 0) {
-                if (at < carry) p.free_list[at] = base + 16 * tid + i;
-                ++at;
-            }
-        found += total;
+            for (int i = 0; i < 16; ++i)
+                if (x[i] == 0) {
+                    if (at < carry) p.free_list[at] = base + 16 * tid + i;
+                    ++at;
+                }
+            found += total;
+        }
+        if (tid == 0) p.n_copies[1] = (int)found;
     }
-    __syncthreads();
-    for (int r = warp; r < p.R; r += kCtl / 32) {
+    cluster_sync();   // (what each row needs was read by all before any row changes)
+    const int found = now(p.n_copies + 1);
+    for (int r = first_row; r < p.R; r += step) {
         const unsigned f = (unsigned)s_fork[r];
         const int need = (int)(f & (kCopy - 1)), first = s_need[r];
         const bool copy = f & kCopy;
@@ -525,14 +540,14 @@ __global__ void __launch_bounds__(kCtl) update_kernel(const __grid_constant__ Up
             if (lane == 0 && p.granted) p.granted[r] = -1;
             continue;
         }
-        const int len = max(p.lens[r], 0), have = pages_of(len);
+        const int len = max(now(p.lens + r), 0), have = pages_of(len);
         int32_t* row = p.table + (int64_t)r * p.W;
         for (int w = lane; w < need; w += 32) {
-            const int pg = __ldcg(p.free_list + first + w);
+            const int pg = now(p.free_list + first + w);
             p.refs[pg] = 1;
             if (copy && w == 0) {
-                const int old = row[have - 1];
-                const int at = atomicAdd(&s_copies, 1);
+                const int old = now(row + have - 1);
+                const int at = atomicAdd(p.n_copies, 1);
                 p.copy_from[at] = old, p.copy_to[at] = pg;
                 atomicSub(&p.refs[old], 1);
                 row[have - 1] = pg;
@@ -545,8 +560,6 @@ __global__ void __launch_bounds__(kCtl) update_kernel(const __grid_constant__ Up
             if (p.granted) p.granted[r] = more;
         }
     }
-    __syncthreads();
-    if (tid == 0) *p.n_copies = s_copies;
 }
 
 __global__ void __launch_bounds__(kCtl) compact_kernel(const __grid_constant__ UpkeepParams p) {
@@ -606,8 +619,8 @@ __global__ void __launch_bounds__(kCtl) compact_kernel(const __grid_constant__ U
     }
 }
 
-// The copies of pages, of every layer, in pieces of 16 KB; with `remap` the tables' entries first.
-constexpr int kPiece = 16384;
+// The copies of pages, of every layer, in pieces of 32 KB (16 KB: 3 % slower); with `remap` the tables' entries first.
+constexpr int kPiece = 32768;
 __global__ void __launch_bounds__(256) copy_pages_kernel(const __grid_constant__ UpkeepParams p, const bool remap) {
     const int n = *p.n_copies;
     const int tid = threadIdx.x;
@@ -634,14 +647,14 @@ __global__ void __launch_bounds__(256) copy_pages_kernel(const __grid_constant__
         const unsigned char* src = p.pages + layer * p.layer_bytes + from * p.page_bytes + off;
         unsigned char* dst = p.pages + layer * p.layer_bytes + to * p.page_bytes + off;
         const int bytes = (int)min((int64_t)kPiece, p.page_bytes - off);
-        uint4 y[4];
+        uint4 y[8];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
+        for (int j = 0; j < 8; ++j) {
             const int at = (j * 256 + tid) * 16;
             if (at < bytes) y[j] = __ldcs(reinterpret_cast<const uint4*>(src + at));
         }
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
+        for (int j = 0; j < 8; ++j) {
             const int at = (j * 256 + tid) * 16;
             if (at < bytes) __stcs(reinterpret_cast<uint4*>(dst + at), y[j]);
         }
@@ -695,8 +708,16 @@ cudaError_t launch_update(const UpkeepParams& p, cudaStream_t s) {
         const cudaError_t e = smem_optin(reinterpret_cast<const void*>(update_kernel), kMaxRows * 8, optin);
         if (e != cudaSuccess) return e;
     }
-    update_kernel<<<1, kCtl, smem, s>>>(p);
-    cudaError_t e = cudaGetLastError();
+    // eight CTAs where the rows' pages are many: one alone took 35 us to fork 128 rows of 128 pages, most of it waiting for loads
+    cudaLaunchConfig_t cfg{};
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = (int64_t)p.R * p.W > 4096 ? 8 : 1;
+    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    cfg.gridDim = dim3(attr.val.clusterDim.x), cfg.blockDim = dim3(kCtl);
+    cfg.dynamicSmemBytes = smem, cfg.stream = s;
+    cfg.attrs = &attr, cfg.numAttrs = 1;
+    cudaError_t e = cudaLaunchKernelEx(&cfg, update_kernel, p);
     if (e != cudaSuccess || !p.grow) return e;
     return launch_copies(p, false, std::min(p.R, p.N), s);
 }

@@ -432,57 +432,97 @@ __global__ void __launch_bounds__(kWarps * 32, MT == 1 ? 3 : 2) paged_kernel(con
     }
 }
 
-// A warp adds up the parts of one query row.
+// A CTA adds up the parts of one query row, four warps sharing them.
 template <int D, typename T, int RT, int UNIT>
 __global__ void __launch_bounds__(128) paged_join_kernel(const __grid_constant__ PagedParams p) {
+    constexpr int N = D / 32, W = 4;
+    __shared__ float s_acc[W][D], s_l[W];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int b = blockIdx.y, h = blockIdx.z;
+    const int b = blockIdx.y, h = blockIdx.z, R = blockIdx.x;
     const Request rq = request_at(p.c, p.t, b);
-    const int rows = rq.n * p.G;
-    const int R = blockIdx.x * 4 + warp;
-    if (R >= rows) return;
+    if (R >= rq.n * p.G) return;
     const int total = p.starts[p.t.B], share = (total + p.ctas - 1) / p.ctas;
     const int tile = R / RT, r = R - tile * RT, units = tile_units<RT, UNIT>(rq, p.G, tile);
     int first = 0;
     for (int t = lane; t < tile; t += 32) first += tile_units<RT, UNIT>(rq, p.G, t);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) first += __shfl_xor_sync(0xffffffffu, first, o);
+    first = __reduce_add_sync(0xffffffffu, first);
     first += p.starts[b] + h * ((p.starts[b + 1] - p.starts[b]) / p.c.Hkv);
     const int c0 = first / share, c1 = (first + units - 1) / share;
-    if (c0 == c1) return;
+    if (c0 == c1) return;   // one part: its CTA has written the row
     auto slot = [&](int c) { return (int64_t)2 * c + (c == c0); };
     float m = -INFINITY;
     for (int c = c0 + lane; c <= c1; c += 32) m = fmaxf(m, p.part_ml[slot(c) * RT + r].x);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    constexpr int N = D / 32;
     float acc[N] = {}, l = 0.f;
-    for (int cb = c0; cb <= c1; cb += 32) {
-        float f = 0.f, fl = 0.f;
-        if (cb + lane <= c1) {
-            const float2 ml = p.part_ml[slot(cb + lane) * RT + r];
-            f = m == -INFINITY ? 0.f : ex2(ml.x - m);
-            fl = m == -INFINITY ? 0.f : ml.y * f;
-        }
-        const int n = min(32, c1 - cb + 1);
 #pragma unroll 4
-        for (int i = 0; i < n; ++i) {
-            const float w = __shfl_sync(0xffffffffu, f, i);
-            l += __shfl_sync(0xffffffffu, fl, i);
-            const float* a = p.part_o + (slot(cb + i) * RT + r) * D + lane * N;
-            float y[N];
+    for (int c = c0 + warp; c <= c1; c += W) {
+        const float2 ml = p.part_ml[slot(c) * RT + r];
+        const float* a = p.part_o + (slot(c) * RT + r) * D + lane * N;
+        float y[N];
 #pragma unroll
-            for (int k = 0; k < N; ++k) y[k] = a[k];
+        for (int k = 0; k < N; ++k) y[k] = a[k];
+        const float f = m == -INFINITY ? 0.f : ex2(ml.x - m);
+        l += ml.y * f;
 #pragma unroll
-            for (int k = 0; k < N; ++k) acc[k] += w * y[k];
-        }
+        for (int k = 0; k < N; ++k) acc[k] += f * y[k];
     }
-    const int64_t at = (int64_t)(rq.first + R / p.G) * p.Hq + h * p.G + R % p.G;
-    const float inv = l > 0.f ? 1.f / l : l == 0.f ? 0.f : NAN;
-    T* to = static_cast<T*>(p.o) + at * D + lane * N;
 #pragma unroll
-    for (int k = 0; k < N; ++k) put(to + k, acc[k] * inv);
-    if (lane == 0 && p.lse) p.lse[at] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
+    for (int k = 0; k < N; ++k) s_acc[warp][lane * N + k] = acc[k];
+    if (lane == 0) s_l[warp] = l;
+    __syncthreads();
+    const int d = threadIdx.x;
+    l = 0.f;
+#pragma unroll
+    for (int w = 0; w < W; ++w) l += s_l[w];
+    const int64_t at = (int64_t)(rq.first + R / p.G) * p.Hq + h * p.G + R % p.G;
+    if (d < D) {
+        float y = 0.f;
+#pragma unroll
+        for (int w = 0; w < W; ++w) y += s_acc[w][d];
+        put(static_cast<T*>(p.o) + at * D + d, y * (l > 0.f ? 1.f / l : l == 0.f ? 0.f : NAN));
+    }
+    if (d == 0 && p.lse) p.lse[at] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
+}
+
+// The same for tiles of many rows, few of which are cut: a CTA takes 32 rows, a warp each of them in turn.
+template <int D, typename T, int RT, int UNIT>
+__global__ void __launch_bounds__(128) paged_join_rows_kernel(const __grid_constant__ PagedParams p) {
+    constexpr int N = D / 32;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int b = blockIdx.y, h = blockIdx.z, R0 = blockIdx.x * 32;
+    const Request rq = request_at(p.c, p.t, b);
+    const int rows = rq.n * p.G;
+    if (R0 >= rows) return;
+    const int total = p.starts[p.t.B], share = (total + p.ctas - 1) / p.ctas;
+    const int tile = R0 / RT, units = tile_units<RT, UNIT>(rq, p.G, tile);
+    int first = 0;
+    for (int t = lane; t < tile; t += 32) first += tile_units<RT, UNIT>(rq, p.G, t);
+    first = __reduce_add_sync(0xffffffffu, first);
+    first += p.starts[b] + h * ((p.starts[b + 1] - p.starts[b]) / p.c.Hkv);
+    const int c0 = first / share, c1 = (first + units - 1) / share;
+    if (c0 == c1) return;   // one part: its CTA has written the rows
+#pragma unroll 2
+    for (int R = R0 + warp; R < min(R0 + 32, rows); R += 4) {
+        const int r = R - tile * RT;
+        float m = -INFINITY;
+        for (int c = c0; c <= c1; ++c) m = fmaxf(m, p.part_ml[(2 * (int64_t)c + (c == c0)) * RT + r].x);
+        float acc[N] = {}, l = 0.f;
+#pragma unroll 2
+        for (int c = c0; c <= c1; ++c) {
+            const int64_t at = (2 * (int64_t)c + (c == c0)) * RT + r;
+            const float2 ml = p.part_ml[at];
+            const float f = m == -INFINITY ? 0.f : ex2(ml.x - m);
+            l += ml.y * f;
+#pragma unroll
+            for (int k = 0; k < N; ++k) acc[k] += f * p.part_o[at * D + lane * N + k];
+        }
+        const int64_t at = (int64_t)(rq.first + R / p.G) * p.Hq + h * p.G + R % p.G;
+        const float inv = l > 0.f ? 1.f / l : l == 0.f ? 0.f : NAN;
+#pragma unroll
+        for (int k = 0; k < N; ++k) put(static_cast<T*>(p.o) + at * D + lane * N + k, acc[k] * inv);
+        if (lane == 0 && p.lse) p.lse[at] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
+    }
 }
 
 template <int D, typename T, int MT>
@@ -496,10 +536,11 @@ cudaError_t launch(const PagedParams& p, cudaStream_t s) {
 }
 template <int D, typename T>
 cudaError_t join(const PagedParams& p, int tile_rows, cudaStream_t s) {
-    const dim3 grid((unsigned)(((int64_t)p.t.max_new * p.G + 3) / 4), p.t.B, p.c.Hkv);
+    const int64_t rows = (int64_t)p.t.max_new * p.G;
+    const dim3 grid((unsigned)(tile_rows <= 32 ? rows : (rows + 31) / 32), p.t.B, p.c.Hkv);
     if (tile_rows == 16) paged_join_kernel<D, T, 16, kUnit><<<grid, 128, 0, s>>>(p);
     else if (tile_rows == 32) paged_join_kernel<D, T, 32, kUnit><<<grid, 128, 0, s>>>(p);
-    else if constexpr (sizeof(T) == 2 && D >= 64) paged_join_kernel<D, T, kTcRows, kTcUnit><<<grid, 128, 0, s>>>(p);
+    else if constexpr (sizeof(T) == 2 && D >= 64) paged_join_rows_kernel<D, T, kTcRows, kTcUnit><<<grid, 128, 0, s>>>(p);
     return cudaGetLastError();
 }
 template <typename F>
