@@ -944,20 +944,23 @@ def gdn_rope_frequencies(rotary_dim: int, *, base: float = 10000.0, scaling: str
     return torch.from_numpy(f).to(device)
 
 
-class _device:
-    """The launches of a call go to the device of its tensors."""
+def _call(name: str, dev, *args) -> None:
+    """A call of the library whose launches go to the device of its tensors."""
+    if torch._C._cuda_getDevice() == dev.index:
+        rc = getattr(lib(), name)(*args)
+    else:
+        with torch.cuda.device(dev):
+            rc = getattr(lib(), name)(*args)
+    if rc != GDN_OK:
+        raise GdnError(rc, name)
 
-    def __init__(self, dev):
-        at = torch.cuda.current_device()
-        self.guard = None if dev.index is None or dev.index == at else torch.cuda.device(dev)
 
-    def __enter__(self):
-        if self.guard:
-            self.guard.__enter__()
-
-    def __exit__(self, *e):
-        if self.guard:
-            self.guard.__exit__(*e)
+def _new(shape, dtype, dev, stream):
+    """A buffer that belongs to the stream that uses it."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=dev)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=dev)
 
 
 def _same(x, like, name: str, shape) -> None:
@@ -994,27 +997,23 @@ def gdn_qk_norm_rope(q, k, positions, inv_freq, *, layout: str = "half", q_weigh
         if w is not None:
             _expect(eps is not None, "weights of a norm need eps")
             _dense(w, name, (D,), dt, dev)
-    with _on(stream, dev):
-        if q_out is None:
-            q_out = torch.empty((T, Hq, D), dtype=dt, device=dev)
-        else:
-            _same(q_out, q, "q_out", q.shape)
-        if k is None:
-            k_out = None
-        elif k_out is None:
-            k_out = torch.empty((T, Hk, D), dtype=dt, device=dev)
-        else:
-            _same(k_out, k, "k_out", k.shape)
+    if q_out is None:
+        q_out = _new((T, Hq, D), dt, dev, stream)
+    else:
+        _same(q_out, q, "q_out", q.shape)
+    if k is None:
+        k_out = None
+    elif k_out is None:
+        k_out = _new((T, Hk, D), dt, dev, stream)
+    else:
+        _same(k_out, k, "k_out", k.shape)
     pr = _Rope(T, Hq, Hk, D, rd, _dtype_code(dt), 0 if layout == "half" else 1, eps is not None, eps or 0.0, mscale,
                _row_stride(q, "q"), _row_stride(k, "k") if Hk else 0, _row_stride(q_out, "q_out"),
                _row_stride(k_out, "k_out") if Hk else 0)
-    with _device(dev):
-        rc = lib().gdn_qk_norm_rope(
-            ctypes.byref(pr), q.data_ptr(), k.data_ptr() if Hk else None, positions.data_ptr() if rd else None,
-            inv_freq.data_ptr() if rd else None, None if q_weight is None else q_weight.data_ptr(),
-            None if k_weight is None else k_weight.data_ptr(), q_out.data_ptr(), k_out.data_ptr() if Hk else None, raw)
-    if rc != GDN_OK:
-        raise GdnError(rc, "gdn_qk_norm_rope")
+    _call("gdn_qk_norm_rope", dev, ctypes.byref(pr), q.data_ptr(), k.data_ptr() if Hk else None,
+          positions.data_ptr() if rd else None, inv_freq.data_ptr() if rd else None,
+          None if q_weight is None else q_weight.data_ptr(), None if k_weight is None else k_weight.data_ptr(),
+          q_out.data_ptr(), k_out.data_ptr() if Hk else None, raw)
     return q_out, k_out
 
 
@@ -1077,12 +1076,8 @@ def gdn_cache_append(k, v, cache: PagedCache, cu_new, *, layer: int = 0, rows=No
     b = _batch(cache, T, cu_new, rows, max_new, None)
     if ws is None:
         ws = workspace(dev)
-    with _device(dev):
-        rc = lib().gdn_cache_append(ctypes.byref(c), layer, ctypes.byref(b), k.data_ptr(), v.data_ptr(),
-                                    _dtype_code(k.dtype), _row_stride(k, "k"), _row_stride(v, "v"), ws.data_ptr(), ws.numel(),
-                                    raw)
-    if rc != GDN_OK:
-        raise GdnError(rc, "gdn_cache_append")
+    _call("gdn_cache_append", dev, ctypes.byref(c), layer, ctypes.byref(b), k.data_ptr(), v.data_ptr(), _dtype_code(k.dtype),
+          _row_stride(k, "k"), _row_stride(v, "v"), ws.data_ptr(), ws.numel(), raw)
 
 
 def gdn_paged_attention(q, cache: PagedCache, cu_new, *, layer: int = 0, rows=None, max_new: Optional[int] = None,
@@ -1103,26 +1098,21 @@ def gdn_paged_attention(q, cache: PagedCache, cu_new, *, layer: int = 0, rows=No
         raise ValueError(f"q must be [T, Hq, {c.head_dim}] on {dev}")
     code = _dtype_code(q.dtype)
     b = _batch(cache, T, cu_new, rows, max_new, max_len)
-    L = lib()
-    nbytes = L.gdn_paged_scratch_bytes(ctypes.byref(c), ctypes.byref(b), code, Hq)
-    with _on(stream, dev):
-        if o is not None:
-            _dense(o, "o", (T, Hq, D), q.dtype, dev)
-        else:
-            o = torch.empty((T, Hq, D), dtype=q.dtype, device=dev)
-        if lse is not None:
-            _dense(lse, "lse", (T, Hq), torch.float32, dev)
-        else:
-            lse = torch.empty((T, Hq), dtype=torch.float32, device=dev)
-        scratch = torch.empty(max(nbytes, 32), dtype=torch.uint8, device=dev)
+    nbytes = lib().gdn_paged_scratch_bytes(ctypes.byref(c), ctypes.byref(b), code, Hq)
+    if o is not None:
+        _dense(o, "o", (T, Hq, D), q.dtype, dev)
+    else:
+        o = _new((T, Hq, D), q.dtype, dev, stream)
+    if lse is not None:
+        _dense(lse, "lse", (T, Hq), torch.float32, dev)
+    else:
+        lse = _new((T, Hq), torch.float32, dev, stream)
+    scratch = _new((nbytes or 32,), torch.uint8, dev, stream)
     if ws is None:
         ws = workspace(dev)
-    with _device(dev):
-        rc = L.gdn_paged_attention(ctypes.byref(c), layer, ctypes.byref(b), q.data_ptr(), code, Hq, _row_stride(q, "q"),
-                                   D ** -0.5 if scale is None else scale, o.data_ptr(), lse.data_ptr(), scratch.data_ptr(),
-                                   nbytes, ws.data_ptr(), ws.numel(), raw)
-    if rc != GDN_OK:
-        raise GdnError(rc, "gdn_paged_attention")
+    _call("gdn_paged_attention", dev, ctypes.byref(c), layer, ctypes.byref(b), q.data_ptr(), code, Hq, _row_stride(q, "q"),
+          D ** -0.5 if scale is None else scale, o.data_ptr(), lse.data_ptr(), scratch.data_ptr(), nbytes, ws.data_ptr(),
+          ws.numel(), raw)
     return {"o": o, "lse": lse}
 
 
@@ -1145,27 +1135,22 @@ def gdn_cache_update(cache: PagedCache, *, drop=None, fork_from=None, fork_to=No
         n_fork = fork_to.numel()
         _dense(fork_to, "fork_to", (n_fork,), torch.int32, dev)
         _dense(fork_from, "fork_from", (n_fork,), torch.int32, dev)
-    L = lib()
-    nbytes = L.gdn_cache_scratch_bytes(ctypes.byref(c))
-    with _on(stream, dev):
-        if grow is not None:
-            _dense(grow, "grow", (c.num_rows,), torch.int32, dev)
-            if granted is not None:
-                _dense(granted, "granted", (c.num_rows,), torch.int32, dev)
-            else:
-                granted = torch.empty(c.num_rows, dtype=torch.int32, device=dev)
+    if grow is not None:
+        _dense(grow, "grow", (c.num_rows,), torch.int32, dev)
+        if granted is not None:
+            _dense(granted, "granted", (c.num_rows,), torch.int32, dev)
         else:
-            granted = None
-        scratch = torch.empty(max(nbytes, 16), dtype=torch.uint8, device=dev)
+            granted = _new((c.num_rows,), torch.int32, dev, stream)
+    else:
+        granted = None
+    nbytes = lib().gdn_cache_scratch_bytes(ctypes.byref(c))
+    scratch = _new((nbytes or 16,), torch.uint8, dev, stream)
     if ws is None:
         ws = workspace(dev)
-    with _device(dev):
-        rc = L.gdn_cache_update(ctypes.byref(c), n_drop, drop.data_ptr() if n_drop else None, n_fork,
-                                fork_from.data_ptr() if n_fork else None, fork_to.data_ptr() if n_fork else None,
-                                None if grow is None else grow.data_ptr(), None if granted is None else granted.data_ptr(),
-                                scratch.data_ptr(), nbytes, ws.data_ptr(), ws.numel(), raw)
-    if rc != GDN_OK:
-        raise GdnError(rc, "gdn_cache_update")
+    _call("gdn_cache_update", dev, ctypes.byref(c), n_drop, drop.data_ptr() if n_drop else None, n_fork,
+          fork_from.data_ptr() if n_fork else None, fork_to.data_ptr() if n_fork else None,
+          None if grow is None else grow.data_ptr(), None if granted is None else granted.data_ptr(), scratch.data_ptr(), nbytes,
+          ws.data_ptr(), ws.numel(), raw)
     return granted
 
 
@@ -1174,18 +1159,13 @@ def gdn_cache_compact(cache: PagedCache, *, live=None, stream=None, ws: Optional
     dev = cache.device
     raw = _raw_stream(stream, dev)
     c = cache._c
-    L = lib()
-    nbytes = L.gdn_cache_scratch_bytes(ctypes.byref(c))
-    with _on(stream, dev):
-        if live is not None:
-            _dense(live, "live", (1,), torch.int32, dev)
-        else:
-            live = torch.empty(1, dtype=torch.int32, device=dev)
-        scratch = torch.empty(max(nbytes, 16), dtype=torch.uint8, device=dev)
+    if live is not None:
+        _dense(live, "live", (1,), torch.int32, dev)
+    else:
+        live = _new((1,), torch.int32, dev, stream)
+    nbytes = lib().gdn_cache_scratch_bytes(ctypes.byref(c))
+    scratch = _new((nbytes or 16,), torch.uint8, dev, stream)
     if ws is None:
         ws = workspace(dev)
-    with _device(dev):
-        rc = L.gdn_cache_compact(ctypes.byref(c), live.data_ptr(), scratch.data_ptr(), nbytes, ws.data_ptr(), ws.numel(), raw)
-    if rc != GDN_OK:
-        raise GdnError(rc, "gdn_cache_compact")
+    _call("gdn_cache_compact", dev, ctypes.byref(c), live.data_ptr(), scratch.data_ptr(), nbytes, ws.data_ptr(), ws.numel(), raw)
     return live

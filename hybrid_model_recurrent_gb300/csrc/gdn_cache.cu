@@ -196,7 +196,8 @@ cudaError_t rope(const RopeParams& p, bool half, cudaStream_t s) {
 // largest value, and write the bytes.  Tokens that the block holds already are touched only when the scale grows.
 // TPB is 32 for calls with at most 8 new tokens a request (decode, drafts: a block has little to do, and eight of them
 // share a CTA), 256 else.  A CTA takes `share` blocks of one page in turn: what it has to find out first, four loads that wait
-// for one another, took half of its time where every block had a CTA of its own.
+// for one another, took half of its time where every block had a CTA of its own.  (Loading the next block's tokens ahead cost 10 %:
+// fewer CTAs fit.)
 __device__ __forceinline__ uint32_t to_e4m3x4(float a, float b, float c, float d) {
     const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
     const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(c, d), __NV_SATFINITE, __NV_E4M3);
@@ -235,19 +236,13 @@ __global__ void __launch_bounds__(256) append_kernel(const __grid_constant__ App
     }
     const int lo = max(start - base, 0), n = min(rq.len - base, c.page) - lo;   // the block's new tokens: lo .. lo + n
     const int end = min(block0 + share, blocks);
-    for (int at0 = block0; at0 < end; at0 += PER) {
-        const int block = at0 + sub;
-        const bool work = block < end;
-        const int kv = block >= c.Hkv, h = block - kv * c.Hkv;
-        const T* src = (kv ? static_cast<const T*>(p.v) + (rq.first + skip + (int64_t)(base + lo - start)) * p.v_stride
-                           : static_cast<const T*>(p.k) + (rq.first + skip + (int64_t)(base + lo - start)) * p.k_stride) + h * D;
+    const int64_t first = rq.first + skip + (int64_t)(base + lo - start);   // the block's first new token in the streams
+    uint4 in[NCH][LD];
+    auto fetch = [&](int block) {
+        const bool kv = block >= c.Hkv;
         const int64_t stride = kv ? p.v_stride : p.k_stride;
-        const int64_t at = ((int64_t)pg * 2 + kv) * c.Hkv + h;
-        const int chunks = work ? n * CPT : 0;
-        float was = 0.f;
-        if (work && lo > 0) was = c.scales[at];   // (before anyone writes it)
-
-        uint4 in[NCH][LD];
+        const T* src = static_cast<const T*>(kv ? p.v : p.k) + first * stride + (int64_t)(kv ? block - c.Hkv : block) * D;
+        const int chunks = block < end ? n * CPT : 0;
 #pragma unroll
         for (int x = 0; x < NCH; ++x) {
             const int ch = x * TPB + tid;
@@ -257,8 +252,18 @@ __global__ void __launch_bounds__(256) append_kernel(const __grid_constant__ App
                 for (int y = 0; y < LD; ++y) in[x][y] = *reinterpret_cast<const uint4*>(a + y * VEC);
             }
         }
-        // The largest value by its bits (two of bf16 at a time).  Where that is no finite number, which is rare, the others are looked
-        // through again.
+    };
+    for (int at0 = block0; at0 < end; at0 += PER) {
+        const int block = at0 + sub;
+        const bool work = block < end;
+        const int kv = block >= c.Hkv, h = block - kv * c.Hkv;
+        const int64_t at = ((int64_t)pg * 2 + kv) * c.Hkv + h;
+        const int chunks = work ? n * CPT : 0;
+        float was = 0.f;
+        if (work && lo > 0) was = c.scales[at];   // (before anyone writes it)
+        fetch(block);
+        // The largest value (two of bf16 at a time; a maximum passes over NaN, which the conversion holds as it is).  Where that is an
+        // infinity, which is rare, the others are looked through again.
         auto agree = [&](uint32_t y) {
             y = __reduce_max_sync(0xffffffffu, y);
             if (TPB > 32) {
@@ -273,21 +278,29 @@ __global__ void __launch_bounds__(256) append_kernel(const __grid_constant__ App
             return y;
         };
         uint32_t bits = 0;
+        if constexpr (sizeof(T) == 2) {
 #pragma unroll
-        for (int x = 0; x < NCH; ++x) {
-            if (x * TPB + tid < chunks) {
+            for (int x = 0; x < NCH; ++x)
+                if (x * TPB + tid < chunks)
 #pragma unroll
-                for (int y = 0; y < LD; ++y) {
-                    const uint32_t w[4] = {in[x][y].x, in[x][y].y, in[x][y].z, in[x][y].w};
+                    for (int y = 0; y < LD; ++y)
 #pragma unroll
-                    for (int z = 0; z < 4; ++z)
-                        bits = sizeof(T) == 2 ? __vmaxu2(bits, w[z] & 0x7fff7fffu) : max(bits, w[z] & 0x7fffffffu);
-                }
-            }
+                        for (uint32_t w : {in[x][y].x, in[x][y].y, in[x][y].z, in[x][y].w})
+                            asm("max.bf16x2 %0, %1, %2;" : "=r"(bits) : "r"(bits), "r"(w & 0x7fff7fffu));
+            bits = max(bits & 0xffffu, bits >> 16) << 16;
+        } else {
+            float top = 0.f;
+#pragma unroll
+            for (int x = 0; x < NCH; ++x)
+                if (x * TPB + tid < chunks)
+#pragma unroll
+                    for (int y = 0; y < LD; ++y)
+#pragma unroll
+                        for (uint32_t w : {in[x][y].x, in[x][y].y, in[x][y].z, in[x][y].w}) top = fmaxf(top, fabsf(__uint_as_float(w)));
+            bits = __float_as_uint(top);
         }
-        if (sizeof(T) == 2) bits = max(bits & 0xffffu, bits >> 16) << 16;
         bits = agree(bits);
-        const bool odd = bits >= 0x7f800000u;
+        const bool odd = bits == 0x7f800000u;
         if (odd) {
             bits = 0;
 #pragma unroll
@@ -311,22 +324,27 @@ __global__ void __launch_bounds__(256) append_kernel(const __grid_constant__ App
         if (lo > 0 && !grows) scale = was;
         const float inv = 1.f / scale;
         unsigned char* dst = c.pages + at * c.page * D;
+        auto convert = [&](bool check) {   // (checked values apart, so that the others take one product and half a conversion each)
 #pragma unroll
-        for (int x = 0; x < NCH; ++x) {
-            const int ch = x * TPB + tid;
-            if (ch < chunks) {
-                float f[8];
+            for (int x = 0; x < NCH; ++x) {
+                const int ch = x * TPB + tid;
+                if (ch < chunks) {
+                    float f[8];
 #pragma unroll
-                for (int y = 0; y < LD; ++y) {
-                    float g[VEC];
-                    Vec<T>::get(in[x][y], g);
+                    for (int y = 0; y < LD; ++y) {
+                        float g[VEC];
+                        Vec<T>::get(in[x][y], g);
 #pragma unroll
-                    for (int z = 0; z < VEC; ++z) f[y * VEC + z] = !odd || fabsf(g[z]) <= FLT_MAX ? g[z] * inv : __uint_as_float(0x7fc00000u);
+                        for (int z = 0; z < VEC; ++z)
+                            f[y * VEC + z] = !check || fabsf(g[z]) <= FLT_MAX ? g[z] * inv : __uint_as_float(0x7fc00000u);
+                    }
+                    *reinterpret_cast<uint2*>(dst + (int64_t)lo * D + ch * 8) =
+                        make_uint2(to_e4m3x4(f[0], f[1], f[2], f[3]), to_e4m3x4(f[4], f[5], f[6], f[7]));
                 }
-                *reinterpret_cast<uint2*>(dst + (int64_t)lo * D + ch * 8) =
-                    make_uint2(to_e4m3x4(f[0], f[1], f[2], f[3]), to_e4m3x4(f[4], f[5], f[6], f[7]));
             }
-        }
+        };
+        if (odd) convert(true);
+        else convert(false);
         if (grows) {
             const float ratio = was * inv;   // a power of two
             for (int ch = tid; ch < lo * CPT; ch += TPB) {
@@ -349,7 +367,7 @@ cudaError_t append_n(const AppendParams& p, cudaStream_t s) {
     // about three CTAs for each that runs at once, blocks of one page in a CTA
     constexpr int PER = 256 / TPB;
     const int64_t blocks = 2 * p.c.Hkv, all = (int64_t)touched * p.t.B * blocks;
-    const int share = (int)std::min<int64_t>(blocks, std::max<int64_t>(PER, all / (kSms * 8 * 3)));
+    const int share = (int)std::min<int64_t>(blocks, std::max<int64_t>(PER, all / (kSms * 4 * 3)));
     append_kernel<T, D, TPB, NCH><<<dim3((unsigned)(touched * ((blocks + share - 1) / share)), p.t.B), 256, 0, s>>>(p, share);
     return cudaGetLastError();
 }
