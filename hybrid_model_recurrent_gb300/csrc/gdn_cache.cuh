@@ -131,6 +131,9 @@ struct PagedParams {
     int32_t stall_after;
 };
 
+// The join's CTAs may be started (they wait for this kernel's end before they read anything of it).
+__device__ __forceinline__ void join_may_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
 // Tokens that a row tile's last row sees, and the tile's units (one at least: rows that see nothing are written too).
 __device__ __forceinline__ int tile_sees(const Request& q, int G, int RT, int tile) {
     const int last = (min((tile + 1) * RT, q.n * G) - 1) / G;

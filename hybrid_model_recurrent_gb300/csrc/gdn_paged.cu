@@ -100,6 +100,7 @@ __global__ void __launch_bounds__(kWarps * 32, MT == 1 ? 3 : 2) paged_kernel(con
     const Cache& c = p.c;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, q4 = lane & 3;
 
+    join_may_start();
     count_units<kWarps * 32, RT, kUnit>(p, s_cum);
     const int total = s_cum[(p.t.B + kGroup - 1) / kGroup], share = (total + gridDim.x - 1) / gridDim.x;
     int x = (int)min((int64_t)blockIdx.x * share, (int64_t)total);
@@ -432,6 +433,10 @@ __global__ void __launch_bounds__(kWarps * 32, MT == 1 ? 3 : 2) paged_kernel(con
     }
 }
 
+// The joins are launched while the kernel that makes the parts still runs, and wait for it here; every CTA does, so that what
+// follows in the stream waits for it too.
+__device__ __forceinline__ void kernel_before_done() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 // A CTA adds up the parts of one query row, four warps sharing them.
 template <int D, typename T, int RT, int UNIT>
 __global__ void __launch_bounds__(128) paged_join_kernel(const __grid_constant__ PagedParams p) {
@@ -440,6 +445,7 @@ __global__ void __launch_bounds__(128) paged_join_kernel(const __grid_constant__
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int b = blockIdx.y, h = blockIdx.z, R = blockIdx.x;
     const Request rq = request_at(p.c, p.t, b);
+    kernel_before_done();
     if (R >= rq.n * p.G) return;
     const int total = p.starts[p.t.B], share = (total + p.ctas - 1) / p.ctas;
     const int tile = R / RT, r = R - tile * RT, units = tile_units<RT, UNIT>(rq, p.G, tile);
@@ -493,6 +499,7 @@ __global__ void __launch_bounds__(128) paged_join_rows_kernel(const __grid_const
     const int b = blockIdx.y, h = blockIdx.z, R0 = blockIdx.x * 32;
     const Request rq = request_at(p.c, p.t, b);
     const int rows = rq.n * p.G;
+    kernel_before_done();
     if (R0 >= rows) return;
     const int total = p.starts[p.t.B], share = (total + p.ctas - 1) / p.ctas;
     const int tile = R0 / RT, units = tile_units<RT, UNIT>(rq, p.G, tile);
@@ -538,10 +545,16 @@ template <int D, typename T>
 cudaError_t join(const PagedParams& p, int tile_rows, cudaStream_t s) {
     const int64_t rows = (int64_t)p.t.max_new * p.G;
     const dim3 grid((unsigned)(tile_rows <= 32 ? rows : (rows + 31) / 32), p.t.B, p.c.Hkv);
-    if (tile_rows == 16) paged_join_kernel<D, T, 16, kUnit><<<grid, 128, 0, s>>>(p);
-    else if (tile_rows == 32) paged_join_kernel<D, T, 32, kUnit><<<grid, 128, 0, s>>>(p);
-    else if constexpr (sizeof(T) == 2 && D >= 64) paged_join_rows_kernel<D, T, kTcRows, kTcUnit><<<grid, 128, 0, s>>>(p);
-    return cudaGetLastError();
+    cudaLaunchConfig_t cfg{};
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.gridDim = grid, cfg.blockDim = dim3(128), cfg.stream = s;
+    cfg.attrs = &attr, cfg.numAttrs = 1;
+    if (tile_rows == 16) return cudaLaunchKernelEx(&cfg, paged_join_kernel<D, T, 16, kUnit>, p);
+    if (tile_rows == 32) return cudaLaunchKernelEx(&cfg, paged_join_kernel<D, T, 32, kUnit>, p);
+    if constexpr (sizeof(T) == 2 && D >= 64) return cudaLaunchKernelEx(&cfg, paged_join_rows_kernel<D, T, kTcRows, kTcUnit>, p);
+    return cudaErrorInvalidValue;
 }
 template <typename F>
 cudaError_t by_type(int D, bool bf16, F&& f) {

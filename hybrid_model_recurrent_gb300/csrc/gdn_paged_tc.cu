@@ -220,6 +220,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_cons
         *issued = 0;
         fence_barrier_init();
     }
+    join_may_start();
     count_units<kThreads, kTcRows, kTcUnit>(p, s_cum);
     tc_fence_before();
     __syncthreads();
