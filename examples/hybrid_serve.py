@@ -5,7 +5,11 @@ The prefix is prefilled once.  Every request then forks from it: its linear laye
 tokens is prefilled for all requests at once, and tokens are decoded greedily, one a request and step, with the states
 updated in place.  Weights are random: the point is how the three operators fit together.
 
-    python examples/hybrid_serve.py [--requests 8] [--prefix 2000] [--tokens 16] [--dtype bf16|f32]
+With --cache paged the attention layers norm and rotate their queries and keys and keep keys and values in 8 bits, in pages
+that the requests share: the prefix is one row of the cache, every request a fork of it, and a request that ends gives its
+place to the next one.
+
+    python examples/hybrid_serve.py [--requests 8] [--prefix 2000] [--tokens 16] [--dtype bf16|f32] [--cache dense|paged]
 """
 from __future__ import annotations
 
@@ -136,12 +140,97 @@ class Server:
         return norm(x).to(self.dtype).float() @ self.w["embed"].float().T / 16
 
 
+class PagedServer:
+    """The same with a paged 8-bit cache for the attention layers: row 0 holds the prefix, row 1 + b request b."""
+
+    def __init__(self, w, prefix, requests: int, capacity: int, page_size: int = 64):
+        self.w, self.B, self.P, self.cap = w, requests, len(prefix), capacity
+        self.dtype, self.dev = w["embed"].dtype, w["embed"].device
+        layers = sum(ly["kind"] == "attention" for ly in w["layers"])
+        row_pages = -(-(self.P + capacity) // page_size)
+        num_pages = row_pages + requests * (-(-capacity // page_size) + 1)   # the prefix, and what each row has of its own
+        self.cache = gdn.PagedCache.empty(layers, num_pages, KV_HEADS, D_HEAD, requests + 1, row_pages, page_size=page_size,
+                                          device=self.dev)
+        self.freq = gdn.gdn_rope_frequencies(D_HEAD, device=self.dev)
+        self.used = [0] * requests                 # tokens of each request behind the prefix
+        self.rows = self.ints(range(1, requests + 1))
+        self.state = [None] * len(w["layers"])     # of the linear layers
+        self.own = False                           # whether these are the requests' own, or still the prefix's
+        self.grow([self.P] + [0] * requests)
+        self.pass_through(torch.as_tensor(prefix, device=self.dev), [0, self.P], self.ints([0]), self.ints(range(self.P)))
+        self.prefix_state = list(self.state)
+        gdn.gdn_cache_update(self.cache, fork_from=self.ints([0] * requests), fork_to=self.rows)
+
+    def ints(self, values):
+        return torch.tensor(list(values), dtype=torch.int32, device=self.dev)
+
+    def grow(self, n):
+        """Room for n[r] more tokens in row r of the cache."""
+        gdn.gdn_cache_update(self.cache, grow=self.ints(n))   # (there are as many pages as all rows may need)
+
+    def pass_through(self, tokens, cu, rows, pos):
+        """The layers' outputs for new tokens of some rows, whose lengths count them already."""
+        x = self.w["embed"][tokens].float()
+        cu_dev, most, at = self.ints(cu), max(b - a for a, b in zip(cu, cu[1:])), 0
+        for i, ly in enumerate(self.w["layers"]):
+            q, k, v = (heads(x, ly[c], self.dtype) for c in "qkv")
+            if ly["kind"] == "linear":
+                if self.own and most == 1:
+                    y = gdn.gdn_linear_step(q, k, v, self.w["alpha"], self.state[i], scale=D_HEAD ** -0.5)
+                else:
+                    start = {}
+                    if self.state[i] is not None:
+                        start = dict(S0=self.state[i], S0_index=range(self.B) if self.own else [0] * self.B)
+                    r = gdn.gdn_linear_prefill(q, k, v, self.w["alpha"], cu, scale=D_HEAD ** -0.5, **start)
+                    self.state[i], y = r["S_final"], r["o"]
+            else:
+                q, k = gdn.gdn_qk_norm_rope(q, k, pos, self.freq, eps=1e-6)
+                gdn.gdn_cache_append(k, v, self.cache, cu_dev, layer=at, rows=rows, max_new=most)
+                y = gdn.gdn_paged_attention(q, self.cache, cu_dev, layer=at, rows=rows, max_new=most)["o"]
+                at += 1
+            x = x + (y.flatten(-2) @ ly["o"].T).float()
+        return x
+
+    def turn(self, prompts):
+        """Prefill a ragged turn (a list of token tensors, one a request) after what each request has; returns the logits of each
+        request's last token."""
+        n = [len(p) for p in prompts]
+        if len(n) != self.B or min(n) < 1:
+            raise ValueError("a turn takes a prompt of at least one token for each request")
+        if max(u + m for u, m in zip(self.used, n)) > self.cap:
+            raise ValueError(f"a request is past the capacity of {self.cap} tokens")
+        self.grow([0] + n)
+        cu = [0]
+        for m in n:
+            cu.append(cu[-1] + m)
+        pos = self.ints(self.P + u + i for u, m in zip(self.used, n) for i in range(m))
+        self.used = [u + m for u, m in zip(self.used, n)]
+        x = self.pass_through(torch.cat(prompts), cu, self.rows, pos)
+        self.own = True
+        return Server.logits(self, x[torch.tensor(cu[1:], device=self.dev) - 1])
+
+    def step(self, tokens):
+        """One token a request; returns its logits."""
+        return self.turn(list(tokens.reshape(-1, 1)))
+
+    def restart(self, requests):
+        """These requests have ended: others begin in their places, again on the prefix."""
+        for b in requests:
+            self.used[b] = 0
+        gdn.gdn_cache_update(self.cache, fork_from=self.ints([0] * len(requests)), fork_to=self.ints(b + 1 for b in requests))
+        for i, first in enumerate(self.prefix_state):
+            if first is not None and self.own:
+                for b in requests:
+                    self.state[i][b] = first[0]
+
+
 def main():
     ap = argparse.ArgumentParser()
     ap.add_argument("--requests", type=int, default=8)
     ap.add_argument("--prefix", type=int, default=2000)
     ap.add_argument("--tokens", type=int, default=16)
     ap.add_argument("--dtype", choices=["bf16", "f32"], default="bf16")
+    ap.add_argument("--cache", choices=["dense", "paged"], default="dense")
     a = ap.parse_args()
     gdn.build()
     g = torch.Generator().manual_seed(1)
@@ -149,7 +238,7 @@ def main():
     prefix = torch.randint(VOCAB, (a.prefix,), generator=g).cuda()
     turns = [torch.randint(VOCAB, (int(torch.randint(1, 40, (1,), generator=g)),), generator=g).cuda()
              for _ in range(a.requests)]
-    s = Server(w, prefix, a.requests, 40 + a.tokens)
+    s = (PagedServer if a.cache == "paged" else Server)(w, prefix, a.requests, 40 + a.tokens)
     tokens = s.turn(turns).argmax(-1)
     out = [tokens]
     for _ in range(a.tokens - 1):
