@@ -18,14 +18,18 @@
 // there.
 //
 // The units (128 tokens of an item) are dealt out evenly over the CTAs, one a multiprocessor (gdn_cache.cuh).
-// Roles: warps 0 .. 7 softmax (one warpgroup a row tile), warp 8 issues products, warp 9 copies, warps 10 .. 15 convert.  One row tile's
-// softmax runs beside the other's products; an item of at most 128 rows takes one tile, in turn.
+// Roles: warps 0 .. 7 softmax (one warpgroup a row tile), warps 8 and 15 issue the products of one row tile each, warp 9 copies, warps
+// 10 .. 14 convert (three the first 64 tokens of a tile, two the others).  An item of at most 128 rows takes one row tile, in turn.
 //
-// The softmax takes a row's scores 32 at a time and writes their weights at once, against the maximum so far: when a
-// chunk raises it by too much, O, l and the tile's weights written before are rescaled.  So a thread holds 64 scores and not 128,
-// sixteen warps have 128 registers each, and the loop's code is small: with three converting warps beside eight that held
-// whole rows (384 threads), a lone warp's instructions came at 7 to 9 cycles each, waiting for the instruction cache,
-// and the conversion took 6 k cycles a tile where softmax and products took 3 k.
+// A step is half a tile, 64 tokens, and S has room for two: the scores of step i + 2 are issued behind the product of step i, so
+// a row tile's softmax finds its next scores ready and runs without a pause.  It takes a step's 64 scores of a row at once and
+// compares with the maximum so far; O is rescaled, rarely, once the product before is done.  (16 x 256 new tokens x 32 heads on
+// 17 k tokens: scores of whole tiles, one after the softmax of the other, 662 us; two halves issued by one warp for both row
+// tiles 826, its barriers and elections in turn.  Rows of 128 scores held by 384 threads, three warps converting, 887: a lone warp's
+// instructions came at 7 to 9 cycles each, waiting for the instruction cache.)
+// What bounds it: that case takes 601 us, 1060 TFLOP/s of the products asked for, 0.55 of a library product's rate, 3.7 k cycles a tile
+// of 128 tokens of which the products take 2.1 k; a step of the softmax takes 1.5 k whatever is left out of its arithmetic
+// (without exponentials 578 us, without the maximum 569): its waits, the scores' way from TMEM and the weights' back.
 //
 // Every wait is bounded: a role that gives up sets the CTA's abort flag and the sticky status, every role leaves its
 // loop, copies and products in flight are waited for, and TMEM is freed.
@@ -65,7 +69,7 @@ constexpr int kRows = 128;    // rows of a tile
 constexpr int kKeys = kTcUnit;
 constexpr float kRise = 8.f;  // O is rescaled when a maximum has risen by more than this (log2)
 constexpr float kLift = 7.f;  // log2 of a weight at the maximum: with the rise 2^15 in f16
-constexpr int kConv = 3;      // converting warps for each half of a tile
+constexpr int kConv0 = 3, kConv1 = 2;   // converting warps for the first half of a tile, and for the second
 // A weight's exponent is score * scale - m in one rounding, but m is a product already rounded: for the largest score its
 // rounding error is left, half a step of m, 16 at 2^28 and past what an exponential holds from 2^31 on.  Rows further from zero
 // than this round the product by itself first.
@@ -83,7 +87,7 @@ struct Cfg {
     static constexpr int kRing = 2 * kTile;                   // after the Q tiles
     static constexpr int kRaw = kRing + ST * kTile;
     static constexpr int kBar = kRaw + RS * kHalf;
-    static constexpr int kInfos = ST == 4 ? 4 : 8;            // tiles described: V of ST / 2 tiles before is done when one is
+    static constexpr int kInfos = ST == 4 ? 4 : 8;            // tiles described: when one is, V of ST / 2 + 1 tiles before is done
     static constexpr int kArea = ST == 4 ? 2048 : 3072;       // barriers, units before each group of requests, the descriptions
     static constexpr int kSmem = kBar + kArea + 1024;
     static constexpr uint32_t kO = 256;                       // TMEM: S of each row tile, then O of each
@@ -117,21 +121,9 @@ __device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8])
                  : "memory");
 }
 
-// What a risen maximum changes: the weights of a tile that are written (`chunks` times 16 columns from ts on) by f, and O (`pieces` of 16 columns from to
-// on) by fo.  Functions by themselves, so that the loop of the softmax stays small.
-__device__ __noinline__ void rescale(uint32_t ts, int chunks, float f, uint32_t to, int pieces, float fo) {
-    tmem_st_wait();   // what is read here has been written
-#pragma unroll 1
-    for (int k = 0; k < chunks; ++k) {
-        uint32_t w[16];
-        tmem_ld16(ts + 16 * k, w);
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-            const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
-            w[i] = half2(x.x * f, x.y * f);
-        }
-        tmem_st16(ts + 16 * k, w);
-    }
+// What a risen maximum changes: O, in `pieces` of 16 columns from to on.  A function by itself, so that the loop of the softmax
+// stays small.
+__device__ __noinline__ void rescale(uint32_t to, int pieces, float fo) {
 #pragma unroll 1
     for (int k = 0; k < pieces; ++k) {
         uint32_t o[16];
@@ -185,21 +177,21 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_cons
     extern __shared__ unsigned char smem_raw[];
     unsigned char* smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
     const uint32_t sbase = smem_addr(smem);
-    uint64_t* full = reinterpret_cast<uint64_t*>(smem + F::kBar);   // [ST] a K or V tile written
-    uint64_t* empty = full + F::ST;                                  // [ST] every product that reads it is done
-    uint64_t* s_full = empty + F::ST;                                // [2] S (and every earlier product) done
-    uint64_t* p_ready = s_full + 2;                                  // [2] P written, O rescaled
-    uint64_t* q_ready = p_ready + 2;                                 // [2] an item's Q tile written
-    uint64_t* o_full = q_ready + 2;                                  // [2] every product of an item done
-    uint64_t* end_bar = o_full + 2;                                  // every product done
-    uint64_t* raw_full = end_bar + 1;                                // [RS] half a tile's bytes landed
+    uint64_t* full = reinterpret_cast<uint64_t*>(smem + F::kBar);   // [ST][2] half a K or V tile written
+    uint64_t* empty = full + 2 * F::ST;                              // [ST][2] every product that reads it is done
+    uint64_t* s_full = empty + 2 * F::ST;                            // [2][2] S of a row tile done, in the one or the other half
+    uint64_t* p_ready = s_full + 4;                                  // [2][2] P written over it, O rescaled
+    uint64_t* pv_done = p_ready + 4;                                 // [2] and multiplied by V
+    uint64_t* q_ready = pv_done + 2;                                 // [2] an item's Q tile written
+    uint64_t* end_bar = q_ready + 2;                                 // [2] every product of an issuing warp done
+    uint64_t* raw_full = end_bar + 2;                                // [RS] half a tile's bytes landed
     uint64_t* raw_empty = raw_full + F::RS;                          // [RS] and read by the converting warps
     uint32_t* tslot = reinterpret_cast<uint32_t*>(raw_empty + F::RS);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tslot + 1);
     int* issued = reinterpret_cast<int*>(tslot + 2);                 // halves whose copies were issued
     int* s_cum = issued + 1;                                         // units before each group of requests
     TileInfo* info = reinterpret_cast<TileInfo*>(smem + F::kBar + F::kArea - sizeof(TileInfo) * F::kInfos);
-    static_assert((2 * F::ST + 2 * F::RS + 9) * 8 + 12 + (kMaxGroups + 1) * 4 + sizeof(TileInfo) * F::kInfos <= F::kArea, "barrier area");
+    static_assert((4 * F::ST + 2 * F::RS + 14) * 8 + 12 + (kMaxGroups + 1) * 4 + sizeof(TileInfo) * F::kInfos <= F::kArea, "barrier area");
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const uint64_t limit = p.wait_limit_ns;
@@ -209,13 +201,11 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_cons
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
     }
     if (tid == 0) {
-        for (int i = 0; i < F::ST; ++i) mbar_init(&full[i], 2 * kConv), mbar_init(&empty[i], 1);
-        for (int i = 0; i < 2; ++i) {
-            mbar_init(&s_full[i], 1), mbar_init(&p_ready[i], 128);
-            mbar_init(&q_ready[i], 128), mbar_init(&o_full[i], 1);
-        }
-        mbar_init(end_bar, 1);
-        for (int i = 0; i < F::RS; ++i) mbar_init(&raw_full[i], 1), mbar_init(&raw_empty[i], kConv);
+        // (a half tile is released by the products of both row tiles)
+        for (int i = 0; i < 2 * F::ST; ++i) mbar_init(&full[i], i & 1 ? kConv1 : kConv0), mbar_init(&empty[i], 2);
+        for (int i = 0; i < 4; ++i) mbar_init(&s_full[i], 1), mbar_init(&p_ready[i], 128);
+        for (int i = 0; i < 2; ++i) mbar_init(&pv_done[i], 1), mbar_init(&q_ready[i], 128), mbar_init(&end_bar[i], 1);
+        for (int i = 0; i < F::RS; ++i) mbar_init(&raw_full[i], 1), mbar_init(&raw_empty[i], i & 1 ? kConv1 : kConv0);
         *abort_flag = 0;
         *issued = 0;
         fence_barrier_init();
@@ -241,69 +231,63 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_cons
     auto tiles_of = [&](const Segment& x) { return max(0, (x.hi - x.lo + kKeys - 1) / kKeys); };
 
     if (warp >= 8) {
-        if (warp == 8) {
-            // ---- products (the whole warp walks along, one elected lane issues); K of tile i is ring entry 2 i, V 2 i + 1 ----
-            auto slot_at = [&](int seq) { return sbase + F::kRing + (uint32_t)(seq % F::ST) * F::kTile; };
-            auto landed = [&](int seq) { return warp_wait(&full[seq % F::ST], seq / F::ST); };
+        if (warp == 8 || warp == 15) {
+            // ---- products of row tile a (the whole warp walks along, one elected lane issues); K of tile i is ring entry 2 i, V
+            // 2 i + 1.  Step i: the values' product of its weights, and the scores of step i + 2 over their place ----
+            const int a = warp == 15;
+            auto slot_at = [&](int e) { return sbase + F::kRing + (uint32_t)(e % F::ST) * F::kTile; };
+            auto landed = [&](int e, int half) { return warp_wait(&full[2 * (e % F::ST) + half], e / F::ST); };
             bool ok = true;
-            int it = 0, turn = 0, tiles[2] = {}, nth[2] = {};   // tiles of the ring; tiles and items of each row tile
+            int it = 0, turn = 0, steps = 0, nth = 0;   // tiles of all items; steps and items of this row tile
+            const uint64_t q = tile_desc(sbase + a * F::kTile, false);
             for (int at = begin; ok && at < end;) {
                 const Segment x = segment_at<kTcRows, kTcUnit>(p, s_cum, at, end);
                 at += x.u1 - x.u0;
-                const int n = tiles_of(x), on = takes(x, turn), last = on >> 1;
+                const int n = 2 * tiles_of(x), on = takes(x, turn);
                 if (n == 0) continue;
-                auto scores = [&](int a, int i) {
+                if (!(on >> a & 1)) {   // the other row tile's alone: pass by, entry after entry, so that no barrier gets ahead
+                    for (int i = 0; ok && i < 2 * n; ++i) {
+                        const int e = 2 * it + (i >> 1 & 1) + 2 * (i >> 2), half = i & 1;   // K's halves, then V's
+                        ok = landed(e, half);
+                        if (ok && lane == 0) mbar_arrive(&empty[2 * (e % F::ST) + half]);
+                    }
+                    it += n / 2;
+                    continue;
+                }
+                ok = warp_wait(&q_ready[a], nth++);
+#pragma unroll 1
+                for (int i = -2; ok && i < n; ++i) {
+                    const int half = i & 1, ev = (2 * (it + (i >> 1)) + 1) & 0x7fffffff, ek = 2 * (it + (i >> 1)) + 2;
+                    const bool pv = i >= 0, qk = i + 2 < n;
+                    const int g = steps + i, region = g & 1;
+                    ok = (!pv || landed(ev, half)) && (!qk || landed(ek, half)) && (!pv || warp_wait(&p_ready[2 * a + region], g >> 1));
+                    if (!ok) break;
                     tc_fence_after();
-                    const uint64_t q = tile_desc(sbase + a * F::kTile, false), k = tile_desc(slot_at(2 * i), false);
+                    const uint64_t v = tile_desc(slot_at(ev) + half * 8192, true), k = tile_desc(slot_at(ek) + half * 8192, false);
+                    const uint32_t at_s = tbase + a * 128 + region * 64;
                     if (elect_one()) {
+                        if (pv) {
 #pragma unroll
-                        for (int s = 0; s < D / 16; ++s)
-                            umma_ss(tbase + a * 128, cols_step(q, s), cols_step(k, s), idesc_f16(kKeys, false), s > 0);
-                        umma_commit(&s_full[a]);
-                        if (a == last) umma_commit(&empty[2 * i % F::ST]);
-                    }
-                };
-                ok = landed(2 * it);
-#pragma unroll
-                for (int a = 0; a < 2; ++a) {
-                    if (!(on >> a & 1)) continue;
-                    ok = ok && warp_wait(&q_ready[a], nth[a]);
-                    if (ok) scores(a, it);
-                }
-                for (int j = 0; ok && j < n; ++j) {
-                    const int i = it + j, vs = 2 * i + 1;
-                    ok = landed(vs);
-#pragma unroll
-                    for (int a = 0; a < 2; ++a) {
-                        if (!(on >> a & 1)) continue;
-                        ok = ok && warp_wait(&p_ready[a], tiles[a] + j);
-                        if (!ok) break;
-                        tc_fence_after();
-                        const uint64_t v = tile_desc(slot_at(vs), true);
-                        if (elect_one()) {
-#pragma unroll
-                            for (int s = 0; s < kKeys / 16; ++s)
-                                umma_ts(tbase + F::kO + a * D, tbase + a * 128 + 8 * s, rows_step(v, s), idesc_f16(D, true),
-                                        j > 0 || s > 0);
-                            if (a == last) umma_commit(&empty[vs % F::ST]);
+                            for (int s = 0; s < 4; ++s)
+                                umma_ts(tbase + F::kO + a * D, at_s + 8 * s, rows_step(v, s), idesc_f16(D, true), i > 0 || s > 0);
+                            umma_commit(&pv_done[a]);
+                            umma_commit(&empty[2 * (ev % F::ST) + half]);
                         }
-                        if (j + 1 < n) {
-                            ok = landed(2 * i + 2);
-                            if (!ok) break;
-                            scores(a, i + 1);
-                        } else if (elect_one()) {
-                            umma_commit(&o_full[a]);
+                        if (qk) {
+#pragma unroll
+                            for (int s = 0; s < D / 16; ++s)
+                                umma_ss(at_s, cols_step(q, s), cols_step(k, s), idesc_f16(64, false), s > 0);
+                            umma_commit(&s_full[2 * a + region]);
+                            umma_commit(&empty[2 * (ek % F::ST) + half]);
                         }
                     }
                 }
-                it += n;
-#pragma unroll
-                for (int a = 0; a < 2; ++a)
-                    if (on >> a & 1) tiles[a] += n, ++nth[a];
+                it += n / 2;
+                steps += n;
             }
-            if (elect_one()) umma_commit(end_bar);   // also after giving up: the end waits for the products in flight
+            if (elect_one()) umma_commit(&end_bar[a]);   // also after giving up: the end waits for the products in flight
         } else {
-            // ---- keys and values: copied by a warp, a lane a page, and converted by six, three for each half of 64 tokens ----
+            // ---- keys and values: copied by a warp, a lane a page, and converted by five, in halves of 64 tokens ----
             const int64_t block = (int64_t)p.c.page * D;
             auto checked = [&](int id) {   // a table's entry, where it is used
                 if ((unsigned)id >= (unsigned)p.c.N) {
@@ -367,10 +351,10 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_cons
                 }
                 if (lane == 0) *issued = asked;
             } else {
-                // A warp converts the tokens 8 g .. 8 g + 7 of its half for every third g, 64 bytes of a token by four lanes.  At
+                // A warp converts the tokens 8 g .. 8 g + 7 of its half for every second or third g, 64 bytes of a token by four lanes.  At
                 // width 128 odd tokens take their 64 bytes the other way round: a quarter of a warp then meets every bank once,
                 // reading and writing.
-                const int half = (warp - 10) / kConv, g0 = (warp - 10) % kConv, sub = lane >> 2, quad = lane & 3;
+                const int half = warp >= 13, g0 = half ? warp - 13 : warp - 10, stride = half ? kConv1 : kConv0, sub = lane >> 2, quad = lane & 3;
                 constexpr int kParts = D / 64;
                 const int turned = kParts == 2 ? sub & 1 : 0;
                 const int chunk0 = ((2 * quad) ^ sub) << 4, chunk1 = ((2 * quad + 1) ^ sub) << 4;   // (token & 7 = sub)
@@ -416,20 +400,20 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_cons
                             __syncwarp();
                             id1 = id2, ks = ks1, vs = vs1;
                         }
-                        ok = warp_wait(&raw_full[r % F::RS], r / F::RS) && (e < F::ST || warp_wait(&empty[e % F::ST], e / F::ST - 1));
+                        ok = warp_wait(&raw_full[r % F::RS], r / F::RS) && (e < F::ST || warp_wait(&empty[2 * (e % F::ST) + half], e / F::ST - 1));
                         if (!ok) break;
                         const unsigned char* raw = raw0 + (r % F::RS) * F::kHalf;
                         unsigned char* to = to0 + (e % F::ST) * F::kTile;
                         const int left = x.hi - x.lo - j * kKeys - 64 * half - 8 * g0 - sub;   // tokens seen from this lane's first on
-                        const bool part = __any_sync(0xffffffffu, left <= 8 * kConv * 2);
+                        const bool part = __any_sync(0xffffffffu, left <= 48);
 #pragma unroll
-                        for (int i = 0; i < 3; ++i) {
-                            if (i == 2 && g0 == 2) break;
+                        for (int i = 0; i < 4; ++i) {
+                            if (g0 + stride * i >= 8) break;
                             uint4 u[kParts];
 #pragma unroll
                             for (int h = 0; h < kParts; ++h)
-                                u[h] = *reinterpret_cast<const uint4*>(raw + i * (8 * kConv) * D + (h ^ turned) * 64);
-                            if (part && 8 * kConv * i >= left) {
+                                u[h] = *reinterpret_cast<const uint4*>(raw + i * (8 * stride) * D + (h ^ turned) * 64);
+                            if (part && 8 * stride * i >= left) {
 #pragma unroll
                                 for (int h = 0; h < kParts; ++h) u[h] = make_uint4(0, 0, 0, 0);
                             }
@@ -437,14 +421,14 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_cons
                             for (int h = 0; h < kParts; ++h) {
                                 uint32_t y[8];
                                 widen16(u[h], y);
-                                unsigned char* row = to + i * (8 * kConv) * 128 + (h ^ turned) * 16384;
+                                unsigned char* row = to + i * (8 * stride) * 128 + (h ^ turned) * 16384;
                                 *reinterpret_cast<uint4*>(row + chunk0) = make_uint4(y[0], y[1], y[2], y[3]);
                                 *reinterpret_cast<uint4*>(row + chunk1) = make_uint4(y[4], y[5], y[6], y[7]);
                             }
                         }
                         proxy_fence();
                         __syncwarp();
-                        if (lane == 0) mbar_arrive(&raw_empty[r % F::RS]), mbar_arrive(&full[e % F::ST]);
+                        if (lane == 0) mbar_arrive(&raw_empty[r % F::RS]), mbar_arrive(&full[2 * (e % F::ST) + half]);
                     }
                     seq += 2 * n;
                 }
@@ -455,7 +439,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_cons
         const int a = warp >> 2, r = tid & 127;
         const uint32_t trow = tbase + ((uint32_t)(32 * (warp & 3)) << 16);
         bool ok = true;
-        int turn = 0, it = 0, mine = 0, nth = 0;   // tiles of all items; tiles and items of this row tile
+        int turn = 0, it = 0, g = 0;   // tiles of all items; steps of this row tile
         for (int at = begin; ok && at < end;) {
             const Segment x = segment_at<kTcRows, kTcUnit>(p, s_cum, at, end);
             at += x.u1 - x.u0;
@@ -513,28 +497,26 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_cons
             }
             float m = -INFINITY, item_v = 0.f;
             float2 la = make_float2(0.f, 0.f), lb = la;
-            for (int j = 0; j < n; ++j, ++mine) {
-                ok = warp_wait(&s_full[a], mine);
+            for (int j = 0; j < 2 * n; ++j, ++g) {
+                ok = warp_wait(&s_full[2 * a + (g & 1)], g >> 1);
                 if (!ok) break;
                 tc_fence_after();
                 if (busy) {
-                    const int seen = valid ? vis - x.lo - j * kKeys : kKeys;
-                    const bool hide = __any_sync(0xffffffffu, seen < kKeys);
-                    const TileInfo& ti = info[(it0 + j) % F::kInfos];
-                    const uint32_t ts = trow + a * 128, to = trow + F::kO + a * D;
-                    // Scores 64 c .. 64 c + 63: the second half's weights go over columns of the first's scores.
-#pragma unroll 1
-                    for (int c = 0; c < 2; ++c) {
+                    const int seen = valid ? vis - x.lo - j * 64 : 64;
+                    const bool hide = __any_sync(0xffffffffu, seen < 64);
+                    const TileInfo& ti = info[(it0 + j / 2) % F::kInfos];
+                    const uint32_t ts = trow + a * 128 + (g & 1) * 64, to = trow + F::kO + a * D;
+                    do {
                         float s0[32], s1[32];
-                        tmem_ld32x2(ts + 64 * c, ts + 64 * c + 32, s0, s1);
+                        tmem_ld32x2(ts, ts + 32, s0, s1);
                         if (hide) {
 #pragma unroll
                             for (int i = 0; i < 32; ++i) {
-                                if (64 * c + i >= seen) s0[i] = -INFINITY;
-                                if (64 * c + 32 + i >= seen) s1[i] = -INFINITY;
+                                if (i >= seen) s0[i] = -INFINITY;
+                                if (32 + i >= seen) s1[i] = -INFINITY;
                             }
                         }
-                        const float4* parts = ti.part + 4 * c;
+                        const float4* parts = ti.part + 4 * (j & 1);
                         float top = -INFINITY;
 #pragma unroll
                         for (int k = 0; k < 4; ++k) {
@@ -544,9 +526,9 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_cons
                             for (int i = 2; i < 8; i += 2) t0 = fmaxf(fmaxf(t0, s[i]), s[i + 1]), t1 = fmaxf(fmaxf(t1, s[8 + i]), s[9 + i]);
                             top = fmaxf(top, fmaxf(t0, t1) * fmaxf(row_scale * parts[k].x, kTiny));
                         }
-                        const bool rise = valid && (top > m + kRise || m == -INFINITY), grow = c == 0 && ti.v > item_v;
+                        const bool rise = valid && (top > m + kRise || m == -INFINITY), grow = ti.v > item_v;
                         if (__any_sync(0xffffffffu, rise || grow)) {
-                            // by a power of two, which the weights that are f16 already take without another rounding
+                            // by a power of two: exact for l and O
                             const float up = ceilf(top - m);   // (infinite for a first maximum)
                             const bool far = !(up <= 100.f);
                             const float f = !rise ? 1.f : far ? 0.f : ex2(-up);
@@ -554,13 +536,13 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_cons
                             la = make_float2(la.x * f, la.y * f), lb = make_float2(lb.x * f, lb.y * f);
                             float fo = f;
                             if (grow) fo *= item_v / ti.v, item_v = ti.v;
-                            rescale(ts, 2 * c, f, to, j > 0 ? D / 16 : 0, fo);
+                            if (j > 0) ok = warp_wait(&pv_done[a], g - 1), tc_fence_after(), rescale(to, D / 16, fo);
                         }
                         const float base = m == -INFINITY ? 0.f : m;
                         if (__any_sync(0xffffffffu, fabsf(base) > kFar)) {
 #pragma unroll 1
-                            for (int k = 0; k < 4; ++k) la.x += far_weights(ts, 4 * c + k, seen, row_scale, base, parts[k]);
-                            continue;
+                            for (int k = 0; k < 4; ++k) la.x += far_weights(ts, k, seen, row_scale, base, parts[k]);
+                            break;
                         }
 #pragma unroll
                         for (int k = 0; k < 4; ++k) {
@@ -577,17 +559,21 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_cons
                                 else la = __ffma2_rn(e, drop2, la);
                                 w[i] = half2(e.x, e.y);
                             }
-                            tmem_st8(ts + 32 * c + 8 * k, w);
+                            tmem_st8(ts + 8 * k, w);
                         }
-                    }
+                    } while (false);
                     tmem_st_wait();
                 }
+                // The item's end waits for its last step's product.  A barrier tells a phase from the next one only, so the one before is
+                // waited for here; elsewhere the scores of step g are made behind the product of step g - 2.
+                if (j == 2 * n - 1) ok = warp_wait(&pv_done[a], g - 1);
+                if (!ok) break;
                 tc_fence_before();
-                mbar_arrive(&p_ready[a]);
+                mbar_arrive(&p_ready[2 * a + (g & 1)]);
             }
             if (!ok) break;
             if (n > 0) {
-                ok = warp_wait(&o_full[a], nth++);
+                ok = warp_wait(&pv_done[a], g - 1);
                 if (!ok) break;
                 tc_fence_after();
             }
@@ -640,7 +626,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_cons
         const uint64_t drain = limit > kDrainLimitNs ? limit : kDrainLimitNs;
         for (int e = max(0, *issued - F::RS); e < *issued; ++e)
             tc::drain_phase(&raw_full[e % F::RS], (uint32_t)((e / F::RS) & 1), drain);
-        tc::drain_phase(end_bar, 0, drain);
+        tc::drain_phase(&end_bar[0], 0, drain), tc::drain_phase(&end_bar[1], 0, drain);
         atomicOr(p.status, STATUS_TIMEOUT);
     }
     __syncthreads();
