@@ -92,8 +92,12 @@ struct PagedPlan {
 
 gdn_status plan_paged(const gdn_cache* c, const Batch& t, gdn_dtype dtype, int Hq, PagedPlan& pl) {
     const int64_t G = Hq / c->num_kv_heads, rows = t.max_new * G;
-    pl.tc = dtype == GDN_BF16 && c->head_dim >= 64 && rows > 32;
-    // Rows beyond 16 take tiles of 32, which halve the reads; the second tile costs a third of the warps at once.
+    // The tensor cores of the 5th generation take 256 rows a tile, filled or not, warp-level products 16 or 32.  Measured, us, warp-level /
+    // tensor cores: 16 requests x 4 heads on 8192 tokens 46 / 56 at 16 rows a head, 63 / 57 at 24, 93 / 59 at 40, 169 / 71 at 128; 4 x 8
+    // heads on 30000 64 / 90, 87 / 90, - , 264 / 99; 1 x 2 heads on 100000 44 / 43, 48 / 44, 64 / 44, 84 / 48.
+    pl.tc = dtype == GDN_BF16 && c->head_dim >= 64 && rows > 16;
+    // Warp-level products: rows beyond 16 take tiles of 32, which halve the reads; the second tile of 16 costs a third of the warps at
+    // once (in bf16, where both were possible: 16 x 4 heads at 24 rows 63 us against 65, 4 x 8 heads 87 against 94).
     pl.tiles = rows > 16 ? 2 : 1;
     pl.tile_rows = pl.tc ? kTcRows : 16 * pl.tiles;
     const int64_t per_item = std::max<int64_t>(ceil_div(t.max_len, pl.tc ? kTcUnit : kUnit), 1);

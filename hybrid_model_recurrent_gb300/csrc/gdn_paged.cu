@@ -544,16 +544,22 @@ cudaError_t launch(const PagedParams& p, cudaStream_t s) {
 template <int D, typename T>
 cudaError_t join(const PagedParams& p, int tile_rows, cudaStream_t s) {
     const int64_t rows = (int64_t)p.t.max_new * p.G;
-    const dim3 grid((unsigned)(tile_rows <= 32 ? rows : (rows + 31) / 32), p.t.B, p.c.Hkv);
+    // Large tiles: where there are fewer of them than CTAs, each is cut into many parts, and a row takes a CTA (1 x 40 rows x 2 heads on 100 k
+    // tokens: 207 us with a warp for 8 rows); else few are cut, and most CTAs would start for nothing (131 k rows: 80 us).
+    const bool by_row = tile_rows <= 32 || (rows + tile_rows - 1) / tile_rows * p.t.B * p.c.Hkv < p.ctas;
     cudaLaunchConfig_t cfg{};
     cudaLaunchAttribute attr{};
     attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr.val.programmaticStreamSerializationAllowed = 1;
-    cfg.gridDim = grid, cfg.blockDim = dim3(128), cfg.stream = s;
+    cfg.gridDim = dim3((unsigned)(by_row ? rows : (rows + 31) / 32), p.t.B, p.c.Hkv), cfg.blockDim = dim3(128), cfg.stream = s;
     cfg.attrs = &attr, cfg.numAttrs = 1;
     if (tile_rows == 16) return cudaLaunchKernelEx(&cfg, paged_join_kernel<D, T, 16, kUnit>, p);
-    if (tile_rows == 32) return cudaLaunchKernelEx(&cfg, paged_join_kernel<D, T, 32, kUnit>, p);
-    if constexpr (sizeof(T) == 2 && D >= 64) return cudaLaunchKernelEx(&cfg, paged_join_rows_kernel<D, T, kTcRows, kTcUnit>, p);
+    if constexpr (sizeof(T) == 4 || D == 32) {
+        if (tile_rows == 32) return cudaLaunchKernelEx(&cfg, paged_join_kernel<D, T, 32, kUnit>, p);
+    } else {
+        if (by_row) return cudaLaunchKernelEx(&cfg, paged_join_kernel<D, T, kTcRows, kTcUnit>, p);
+        return cudaLaunchKernelEx(&cfg, paged_join_rows_kernel<D, T, kTcRows, kTcUnit>, p);
+    }
     return cudaErrorInvalidValue;
 }
 template <typename F>
@@ -572,7 +578,10 @@ cudaError_t by_type(int D, bool bf16, F&& f) {
 
 cudaError_t launch_paged(const PagedParams& p, int D, bool bf16, int tiles, cudaStream_t s) {
     return by_type(D, bf16, [&](auto d, auto t) {
-        return tiles == 1 ? launch<d(), decltype(t), 1>(p, s) : launch<d(), decltype(t), 2>(p, s);
+        // (bf16 of width 64 and 128 with more than 16 rows runs on the tensor cores)
+        if constexpr (sizeof(t) == 4 || d() == 32)
+            if (tiles == 2) return launch<d(), decltype(t), 2>(p, s);
+        return tiles == 1 ? launch<d(), decltype(t), 1>(p, s) : cudaErrorInvalidValue;
     });
 }
 

@@ -54,7 +54,7 @@ class Served:
         assert torch.equal(c.pages[0].double().cpu(), pages) and torch.equal(c.scales[0].double().cpu(), scales)
         rows_at_once = max(new) * self.Hq // self.H
         check_attention(c, q, ints(cu), rows=ints(rows), max_new=max(new),
-                        **(dict(cut=2.0 ** -24) if self.dtype == BF and rows_at_once > 32 else {}))
+                        **(dict(cut=2.0 ** -24) if self.dtype == BF and rows_at_once > 16 else {}))
 
     def held(self, row):
         """What a row's cache holds, as values."""

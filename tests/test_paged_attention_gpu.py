@@ -32,7 +32,7 @@ TC = dict(cut=2.0 ** -24)
 
 def step_of(dtype, D, rows):
     """The tensor cores take many rows of bf16."""
-    return TC if dtype == BF and D >= 64 and rows > 32 else {}
+    return TC if dtype == BF and D >= 64 and rows > 16 else {}
 
 
 def queries(T, Hq, D, dtype, seed=1, gain=1.0):
