@@ -1020,7 +1020,9 @@ def gdn_qk_norm_rope(q, k, positions, inv_freq, *, layout: str = "half", q_weigh
 class PagedCache:
     """A paged key/value cache in 8 bits (see the header): pages [L, N, 2, Hkv, page, D] float8_e4m3fn, scales
     [L, N, 2, Hkv] fp32, table [R, W] int32, lens [R] int32, refs [N] int32, all on one GPU.  The operators change them
-    in place."""
+    in place; other tensors make another cache."""
+
+    __slots__ = ("_tensors", "_c", "device")
 
     def __init__(self, pages, scales, table, lens, refs):
         _expect(pages.dim() == 6 and pages.shape[2] == 2 and table.dim() == 2,
@@ -1033,10 +1035,16 @@ class PagedCache:
         _dense(table, "table", (R, W), torch.int32, dev)
         _dense(lens, "lens", (R,), torch.int32, dev)
         _dense(refs, "refs", (N,), torch.int32, dev)
-        self.pages, self.scales, self.table, self.lens, self.refs = pages, scales, table, lens, refs
-        self.device, self.page_size = dev, page
+        self._tensors, self.device = (pages, scales, table, lens, refs), dev
         self._c = _Cache(L, N, page, H, D, R, W, pages.data_ptr(), scales.data_ptr(), table.data_ptr(), lens.data_ptr(),
                          refs.data_ptr())
+
+    pages = property(lambda self: self._tensors[0])
+    scales = property(lambda self: self._tensors[1])
+    table = property(lambda self: self._tensors[2])
+    lens = property(lambda self: self._tensors[3])
+    refs = property(lambda self: self._tensors[4])
+    page_size = property(lambda self: self._c.page_size)
 
     @classmethod
     def empty(cls, layers: int, num_pages: int, kv_heads: int, head_dim: int, rows: int, row_pages: int, *,

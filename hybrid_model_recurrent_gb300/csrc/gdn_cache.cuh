@@ -143,23 +143,45 @@ template <int RT, int UNIT>
 __device__ __forceinline__ int tile_units(const Request& q, int G, int tile) {
     return max(1, (tile_sees(q, G, RT, tile) + UNIT - 1) / UNIT);
 }
+// The units of a request's tiles, one after the other (as tile_units, without a division for each).
+template <int RT, int UNIT>
+struct TileWalk {
+    int base, len, last, qi, rest, G, step_qi, step_rest;   // qi, rest: the tile's last row is `rest` of token qi
+    __device__ __forceinline__ TileWalk(const Request& q, int G_) : base(q.len - q.n + 1), len(q.len), last(q.n - 1), G(G_) {
+        qi = (RT - 1) / G, rest = (RT - 1) - qi * G;
+        step_qi = RT / G, step_rest = RT - step_qi * G;
+    }
+    __device__ __forceinline__ int next() {
+        const int u = max(1, (max(0, min(len, base + min(qi, last))) + UNIT - 1) / UNIT);
+        qi += step_qi, rest += step_rest;
+        if (rest >= G) rest -= G, ++qi;
+        return u;
+    }
+};
 // units of a request for one head (none without queries)
 template <int RT, int UNIT>
 __device__ __forceinline__ int head_units(const Request& q, int G) {
     int n = 0;
     const int tiles = (q.n * G + RT - 1) / RT;
-    for (int t = 0; t < tiles; ++t) n += tile_units<RT, UNIT>(q, G, t);
+    TileWalk<RT, UNIT> w(q, G);
+    for (int t = 0; t < tiles; ++t) n += w.next();
     return n;
 }
 
-// Units before every 16th request into s_cum[0 .. ceil(B / 16)], by all THREADS threads of a CTA: a thread a request, so that the
-// loads of many go together.  The first CTA writes p.starts.
-constexpr int kGroup = 16, kMaxGroups = 4096 / kGroup;
+// Units before every group of requests into s_cum, by all THREADS threads of a CTA, a thread a request; a group is the least power of two
+// with which kMaxGroups of them hold the batch (one request up to 256).  The first CTA writes p.starts.
+constexpr int kMaxGroups = 256;
+__device__ __forceinline__ int group_log2(int B) {
+    int s = 0;
+    while (((B - 1) >> s) >= kMaxGroups) ++s;
+    return s;
+}
+__device__ __forceinline__ int groups_of(int B) { return ((B - 1) >> group_log2(B)) + 1; }
 template <int THREADS, int RT, int UNIT>
 __device__ __forceinline__ void count_units(const PagedParams& p, int* s_cum) {
-    const int tid = threadIdx.x, lane = tid & 31, B = p.t.B, groups = (B + kGroup - 1) / kGroup;
-    for (int g0 = 0; g0 < groups; g0 += THREADS / kGroup) {
-        const int g = g0 + tid / kGroup, b = g * kGroup + tid % kGroup;
+    const int tid = threadIdx.x, lane = tid & 31, B = p.t.B, shift = group_log2(B), width = 1 << shift, groups = groups_of(B);
+    for (int b0 = 0; b0 < B; b0 += THREADS) {
+        const int b = b0 + tid;
         int n = 0;
         if (b < B) {
             const Request q = request_at(p.c, p.t, b);
@@ -167,12 +189,11 @@ __device__ __forceinline__ void count_units(const PagedParams& p, int* s_cum) {
             n = head_units<RT, UNIT>(q, p.G) * p.c.Hkv;
         }
         int y = n;
-#pragma unroll
-        for (int o = 1; o < kGroup; o <<= 1) {
-            const int z = __shfl_up_sync(0xffffffffu, y, o, kGroup);
-            if (tid % kGroup >= o) y += z;
+        for (int o = 1; o < width; o <<= 1) {
+            const int z = __shfl_up_sync(0xffffffffu, y, o, width);
+            if ((tid & (width - 1)) >= o) y += z;
         }
-        if (tid % kGroup == kGroup - 1 && g < groups) s_cum[g + 1] = y;
+        if ((tid & (width - 1)) == width - 1 && (b >> shift) < groups) s_cum[(b >> shift) + 1] = y;
         if (blockIdx.x == 0 && b < B) p.starts[b] = y - n;
     }
     __syncthreads();
@@ -194,7 +215,7 @@ __device__ __forceinline__ void count_units(const PagedParams& p, int* s_cum) {
     }
     __syncthreads();
     if (blockIdx.x == 0) {
-        for (int b = tid; b < B; b += THREADS) p.starts[b] += s_cum[b / kGroup];   // (its own: 16 threads a group, THREADS a round)
+        for (int b = tid; b < B; b += THREADS) p.starts[b] += s_cum[b >> shift];   // (what the same thread wrote)
         if (tid == 0) p.starts[B] = s_cum[groups];
     }
 }
@@ -209,36 +230,41 @@ struct Segment {
 template <int RT, int UNIT>
 __device__ __forceinline__ Segment segment_at(const PagedParams& p, const int* s_cum, int x, int end) {
     Segment s;
-    int g = 0, top = (p.t.B + kGroup - 1) / kGroup;   // cum[g] <= x < cum[top]
+    const int shift = group_log2(p.t.B);
+    int g = 0, top = groups_of(p.t.B);   // cum[g] <= x < cum[top]
     while (top - g > 1) {
         const int mid = (g + top) >> 1;
         if (s_cum[mid] <= x) g = mid;
         else top = mid;
     }
-    // the requests of the group, a lane each; the one that unit x falls to
-    const int lane = threadIdx.x & 31, b = g * kGroup + lane;
-    Request q{-1, 0, 0, 0, false};
-    if (lane < kGroup && b < p.t.B) q = request_at(p.c, p.t, b);
-    const int per_head = head_units<RT, UNIT>(q, p.G), n = per_head * p.c.Hkv;
-    int after = n;
-#pragma unroll
-    for (int o = 1; o < kGroup; o <<= 1) {
-        const int z = __shfl_up_sync(0xffffffffu, after, o);
-        if (lane >= o) after += z;
+    int mine = x - s_cum[g], head;   // the unit within its request, and the request's units a head
+    if (shift == 0) {
+        s.rq = request_at(p.c, p.t, g);
+        head = (s_cum[g + 1] - s_cum[g]) / p.c.Hkv;
+    } else {   // the requests of the group, a lane each
+        const int lane = threadIdx.x & 31, b = (g << shift) + lane, width = 1 << shift;
+        Request q{-1, 0, 0, 0, false};
+        if (lane < width && b < p.t.B) q = request_at(p.c, p.t, b);
+        const int per_head = head_units<RT, UNIT>(q, p.G), n = per_head * p.c.Hkv;
+        int after = n;
+        for (int o = 1; o < width; o <<= 1) {
+            const int z = __shfl_up_sync(0xffffffffu, after, o);
+            if (lane >= o) after += z;
+        }
+        const int at = __ffs(__ballot_sync(0xffffffffu, lane < width && mine < after)) - 1;
+        s.rq.row = __shfl_sync(0xffffffffu, q.row, at), s.rq.len = __shfl_sync(0xffffffffu, q.len, at);
+        s.rq.n = __shfl_sync(0xffffffffu, q.n, at), s.rq.first = __shfl_sync(0xffffffffu, q.first, at);
+        mine -= __shfl_sync(0xffffffffu, after - n, at);
+        head = __shfl_sync(0xffffffffu, per_head, at);
     }
-    const int rest = x - s_cum[g];
-    const int at = __ffs(__ballot_sync(0xffffffffu, lane < kGroup && rest < after)) - 1;
-    s.rq.row = __shfl_sync(0xffffffffu, q.row, at), s.rq.len = __shfl_sync(0xffffffffu, q.len, at);
-    s.rq.n = __shfl_sync(0xffffffffu, q.n, at), s.rq.first = __shfl_sync(0xffffffffu, q.first, at);
-    const int mine = rest - __shfl_sync(0xffffffffu, after - n, at), head = __shfl_sync(0xffffffffu, per_head, at);
     s.h = mine / head;
     s.u0 = mine - s.h * head;
     int tile = 0;
-    for (;;) {
-        s.units = tile_units<RT, UNIT>(s.rq, p.G, tile);
-        if (s.u0 < s.units) break;
+    TileWalk<RT, UNIT> w(s.rq, p.G);
+    for (const int last = (s.rq.n * p.G - 1) / RT;; ++tile) {   // (it ends, whatever becomes of the lengths meanwhile)
+        s.units = w.next();
+        if (s.u0 < s.units || tile >= last) break;
         s.u0 -= s.units;
-        ++tile;
     }
     s.u1 = min(s.units, s.u0 + end - x);
     s.row0 = tile * RT;

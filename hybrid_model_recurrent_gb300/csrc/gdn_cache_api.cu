@@ -92,6 +92,7 @@ struct PagedPlan {
 
 gdn_status plan_paged(const gdn_cache* c, const Batch& t, gdn_dtype dtype, int Hq, PagedPlan& pl) {
     const int64_t G = Hq / c->num_kv_heads, rows = t.max_new * G;
+    if (rows >= (1ll << 31) - 1024) return GDN_ERR_UNSUPPORTED;
     // The tensor cores of the 5th generation take 256 rows a tile, filled or not, warp-level products 16 or 32.  Measured, us, warp-level /
     // tensor cores: 16 requests x 4 heads on 8192 tokens 46 / 56 at 16 rows a head, 63 / 57 at 24, 93 / 59 at 40, 169 / 71 at 128; 4 x 8
     // heads on 30000 64 / 90, 87 / 90, - , 264 / 99; 1 x 2 heads on 100000 44 / 43, 48 / 44, 64 / 44, 84 / 48.

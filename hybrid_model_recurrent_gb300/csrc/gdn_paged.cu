@@ -102,7 +102,7 @@ __global__ void __launch_bounds__(kWarps * 32, MT == 1 ? 3 : 2) paged_kernel(con
 
     join_may_start();
     count_units<kWarps * 32, RT, kUnit>(p, s_cum);
-    const int total = s_cum[(p.t.B + kGroup - 1) / kGroup], share = (total + gridDim.x - 1) / gridDim.x;
+    const int total = s_cum[groups_of(p.t.B)], share = (total + gridDim.x - 1) / gridDim.x;
     int x = (int)min((int64_t)blockIdx.x * share, (int64_t)total);
     const int end = min(x + share, total);
 

@@ -218,7 +218,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_cons
     const uint32_t tbase = *tslot;
     auto warp_wait = [&](uint64_t* bar, int parity) { return warp_wait_bar(bar, (uint32_t)parity & 1u, abort_flag, limit); };
 
-    const int total = s_cum[(p.t.B + kGroup - 1) / kGroup], share = (total + (int)gridDim.x - 1) / (int)gridDim.x;
+    const int total = s_cum[groups_of(p.t.B)], share = (total + (int)gridDim.x - 1) / (int)gridDim.x;
     const int begin = (int)min((int64_t)blockIdx.x * share, (int64_t)total), end = min(begin + share, total);
 
     // Every role walks the CTA's items; an item of at most 128 rows takes one row tile, the two in turn, so that one tile's sums

@@ -89,6 +89,11 @@ def test_attention(L, bad, want):
     assert attend(L, **bad) == want
 
 
+def test_too_many_rows(L):
+    c = cache(H=1, D=32, W=4, rows=5000)
+    assert attend(L, c, batch(B=1, max_new=2 ** 24, T=2 ** 24), Hq=128) == UNS
+
+
 def test_attention_too_large(L):
     c = cache(H=4096, D=32, W=2 ** 20, rows=5000)
     assert attend(L, c, batch(B=4096, max_new=2 ** 20, T=2 ** 29), Hq=4096) == UNS
@@ -160,7 +165,10 @@ def test_host_tensors_are_refused():
 def test_caches_of_wrong_tensors_are_refused():
     c = gdn.PagedCache.empty(1, 4, 2, 64, 2, 3, page_size=16, device="cpu")
     good = dict(pages=c.pages, scales=c.scales, table=c.table, lens=c.lens, refs=c.refs)
-    gdn.PagedCache(**good)
+    made = gdn.PagedCache(**good)
+    assert made.pages is c.pages and made.page_size == 16
+    with pytest.raises(AttributeError):   # (the calls go to the tensors that it was made of)
+        made.lens = c.lens + 1
     for name, bad in (("pages", c.pages.view(torch.uint8)), ("pages", c.pages[:, :, :1]), ("pages", c.pages.transpose(3, 4)),
                       ("scales", c.scales.double()), ("scales", c.scales[:, :3]), ("table", c.table.long()), ("table", c.table[0]),
                       ("lens", c.lens[:1]), ("refs", c.refs[:3])):

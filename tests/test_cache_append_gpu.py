@@ -185,7 +185,7 @@ def test_captured_and_on_another_stream():
     assert torch.equal(a.pages.view(torch.uint8), c.pages.view(torch.uint8)) and torch.equal(a.scales, c.scales)
     # the next replay goes where the lengths point then
     for cache in (a, c):
-        cache.lens += 1
+        cache.lens.add_(1)
     gdn.gdn_cache_append(x, x, a, cu)
     graph.replay()
     torch.cuda.synchronize()
