@@ -1029,12 +1029,16 @@ class PagedCache:
                 "pages must be [L, N, 2, Hkv, page, D] and table [R, W]")
         L, N, _, H, page, D = pages.shape
         R, W = table.shape
-        dev = pages.device
-        _dense(pages, "pages", pages.shape, torch.float8_e4m3fn, dev)
-        _dense(scales, "scales", (L, N, 2, H), torch.float32, dev)
-        _dense(table, "table", (R, W), torch.int32, dev)
-        _dense(lens, "lens", (R,), torch.int32, dev)
-        _dense(refs, "refs", (N,), torch.int32, dev)
+        dev, i32 = pages.device, torch.int32
+        if not (pages.dtype is torch.float8_e4m3fn and scales.dtype is torch.float32 and scales.shape == (L, N, 2, H)
+                and table.dtype is i32 and lens.dtype is i32 and refs.dtype is i32 and lens.shape == (R,) and refs.shape == (N,)
+                and scales.device == dev and table.device == dev and lens.device == dev and refs.device == dev
+                and pages.is_contiguous() and scales.is_contiguous() and table.is_contiguous() and lens.is_contiguous()
+                and refs.is_contiguous()):
+            for x, name, shape, dtype in ((pages, "pages", pages.shape, torch.float8_e4m3fn), (table, "table", (R, W), i32),
+                                          (scales, "scales", (L, N, 2, H), torch.float32), (lens, "lens", (R,), i32),
+                                          (refs, "refs", (N,), i32)):
+                _dense(x, name, shape, dtype, dev)
         self._tensors, self.device = (pages, scales, table, lens, refs), dev
         self._c = _Cache(L, N, page, H, D, R, W, pages.data_ptr(), scales.data_ptr(), table.data_ptr(), lens.data_ptr(),
                          refs.data_ptr())
@@ -1058,13 +1062,14 @@ class PagedCache:
 
 
 def _batch(cache, T: int, cu_new, rows, max_new, max_len):
+    dev = cache.device
     B = cu_new.shape[0] - 1
-    _expect(B >= 1, "cu_new must be [B + 1]")
-    _dense(cu_new, "cu_new", (B + 1,), torch.int32, cache.device)
+    _dense(cu_new, "cu_new", (B + 1,), torch.int32, dev)
+    at = None
     if rows is not None:
-        _dense(rows, "rows", (B,), torch.int32, cache.device)
-    return _Batch(B, max(T, 1) if max_new is None else max_new, T, max_len or 0, cu_new.data_ptr(),
-                  None if rows is None else rows.data_ptr())
+        _dense(rows, "rows", (B,), torch.int32, dev)
+        at = rows.data_ptr()
+    return _Batch(B, (T or 1) if max_new is None else max_new, T, max_len or 0, cu_new.data_ptr(), at)
 
 
 def gdn_cache_append(k, v, cache: PagedCache, cu_new, *, layer: int = 0, rows=None, max_new: Optional[int] = None,
