@@ -557,9 +557,11 @@ cudaError_t launch(const PagedParams& p, cudaStream_t s) {
 template <int D, typename T>
 cudaError_t join(const PagedParams& p, int tile_rows, cudaStream_t s) {
     const int64_t rows = (int64_t)p.t.max_new * p.G;
-    // Large tiles: where there are fewer of them than CTAs, each is cut into many parts, and a row takes a CTA (1 x 40 rows x 2 heads on 100 k
-    // tokens: 207 us with a warp for 8 rows); else few are cut, and most CTAs would start for nothing (131 k rows: 80 us).
-    const bool by_row = tile_rows <= 32 || (rows + tile_rows - 1) / tile_rows * p.t.B * p.c.Hkv < p.ctas;
+    // Large tiles: a CTA a row costs 2 us for about 2432 rows (16 CTAs a multiprocessor), most of which end at once; a warp for 8 rows in
+    // turn takes 1.5 us a row and 0.3 us a part.  (1 x 40 rows x 2 heads on 100 k tokens, 76 parts: 207 us by warps, 44 by rows; 131 k rows of 2
+    // parts: 80 us by rows, 10 by warps.)
+    const int64_t items = (rows + tile_rows - 1) / tile_rows * p.t.B * p.c.Hkv, parts = p.ctas / std::max<int64_t>(items, 1) + 1;
+    const bool by_row = tile_rows <= 32 || rows * p.t.B * p.c.Hkv < 14600 + 2900 * parts;
     cudaLaunchConfig_t cfg{};
     cudaLaunchAttribute attr{};
     attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
