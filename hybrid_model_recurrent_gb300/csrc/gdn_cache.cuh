@@ -50,7 +50,7 @@ struct Batch {
 // Device values are taken within their bounds, whatever they say.
 struct Request {
     int row, len, n, first;
-    bool bad;   // more new tokens than the call's bound
+    bool bad;   // more tokens, or more new ones, than the call's bounds
 };
 __device__ __forceinline__ Request request_at(const Cache& c, const Batch& t, int b) {
     Request q;
@@ -58,9 +58,10 @@ __device__ __forceinline__ Request request_at(const Cache& c, const Batch& t, in
     q.n = min(max(t.cu[b + 1], q.first), t.T) - q.first;
     q.row = t.rows ? t.rows[b] : b;
     if (q.row < 0 || q.row >= c.R) q.row = -1;
-    q.len = q.row < 0 ? 0 : min(max(c.lens[q.row], 0), t.max_len);
-    q.bad = q.n > t.max_new;
-    if (q.bad) q.n = t.max_new;
+    const int len = q.row < 0 ? 0 : c.lens[q.row];
+    q.len = min(max(len, 0), t.max_len);
+    q.bad = q.n > t.max_new || len > t.max_len;
+    q.n = min(q.n, t.max_new);
     return q;
 }
 
@@ -169,7 +170,9 @@ __device__ __forceinline__ int head_units(const Request& q, int G) {
 }
 
 // Units before every group of requests into s_cum, by all THREADS threads of a CTA, a thread a request; a group is the least power of two
-// with which kMaxGroups of them hold the batch (one request up to 256).  The first CTA writes p.starts.
+// with which kMaxGroups of them hold the batch (one request up to 256).  The first CTA writes p.starts.  The host's plan keeps the total
+// below 2^31 for counts as the call describes them; sums stop there, and others (cu_new that falls) are reported and nothing is done.
+constexpr unsigned kNoTotal = 0x7fffffffu;
 constexpr int kMaxGroups = 256;
 __device__ __forceinline__ int group_log2(int B) {
     int s = 0;
@@ -182,35 +185,37 @@ __device__ __forceinline__ void count_units(const PagedParams& p, int* s_cum) {
     const int tid = threadIdx.x, lane = tid & 31, B = p.t.B, shift = group_log2(B), width = 1 << shift, groups = groups_of(B);
     for (int b0 = 0; b0 < B; b0 += THREADS) {
         const int b = b0 + tid;
-        int n = 0;
+        unsigned n = 0;
         if (b < B) {
             const Request q = request_at(p.c, p.t, b);
             if (q.bad && blockIdx.x == 0) atomicOr(p.status, STATUS_BAD_INDEX);
-            n = head_units<RT, UNIT>(q, p.G) * p.c.Hkv;
+            n = (unsigned)(head_units<RT, UNIT>(q, p.G) * p.c.Hkv);
         }
-        int y = n;
+        unsigned y = n;
         for (int o = 1; o < width; o <<= 1) {
-            const int z = __shfl_up_sync(0xffffffffu, y, o, width);
-            if ((tid & (width - 1)) >= o) y += z;
+            const unsigned z = __shfl_up_sync(0xffffffffu, y, o, width);
+            if ((tid & (width - 1)) >= o) y = min(y + z, kNoTotal);
         }
-        if ((tid & (width - 1)) == width - 1 && (b >> shift) < groups) s_cum[(b >> shift) + 1] = y;
-        if (blockIdx.x == 0 && b < B) p.starts[b] = y - n;
+        if ((tid & (width - 1)) == width - 1 && (b >> shift) < groups) s_cum[(b >> shift) + 1] = (int)y;
+        if (blockIdx.x == 0 && b < B) p.starts[b] = (int)(y - n);
     }
     __syncthreads();
     if (tid < 32) {
         constexpr int PER = kMaxGroups / 32;
-        int sum = 0;
+        unsigned sum = 0;
         for (int i = 0; i < PER; ++i)
-            if (lane * PER + i < groups) sum += s_cum[lane * PER + i + 1];
-        int y = sum;
+            if (lane * PER + i < groups) sum = min(sum + s_cum[lane * PER + i + 1], kNoTotal);
+        unsigned y = sum;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-            const int z = __shfl_up_sync(0xffffffffu, y, o);
-            if (lane >= o) y += z;
+            const unsigned z = __shfl_up_sync(0xffffffffu, y, o);
+            if (lane >= o) y = min(y + z, kNoTotal);
         }
+        const bool none = __shfl_sync(0xffffffffu, y, 31) == kNoTotal;
+        if (none && lane == 0 && blockIdx.x == 0) atomicOr(p.status, STATUS_BAD_INDEX);
         y -= sum;
         for (int i = 0; i < PER; ++i)
-            if (lane * PER + i < groups) y += s_cum[lane * PER + i + 1], s_cum[lane * PER + i + 1] = y;
+            if (lane * PER + i < groups) y += s_cum[lane * PER + i + 1], s_cum[lane * PER + i + 1] = none ? 0 : (int)y;
         if (lane == 0) s_cum[0] = 0;
     }
     __syncthreads();

@@ -205,6 +205,7 @@ GDN_EXPORT gdn_status gdn_cache_append(const gdn_cache* c, int32_t layer, const 
     if (!k || !v || !aligned(k, 16) || !aligned(v, 16)) return GDN_ERR_INVALID_ARG;
     if (ceil_div(p.t.max_new, c->page_size) * 2 * c->num_kv_heads >= (1ll << 30)) return GDN_ERR_UNSUPPORTED;
     p.c = cache_of(c, layer);
+    p.t.max_len = c->row_pages * c->page_size;   // (a bound that is too low would move tokens)
     p.k = k, p.v = v;
     p.status = static_cast<unsigned int*>(workspace);
     return launched(launch_append(p, c->head_dim, dtype == GDN_BF16, (cudaStream_t)stream));

@@ -459,8 +459,8 @@ __global__ void __launch_bounds__(128) paged_join_kernel(const __grid_constant__
     const int b = blockIdx.y, h = blockIdx.z, R = blockIdx.x;
     const Request rq = request_at(p.c, p.t, b);
     kernel_before_done();
-    if (R >= rq.n * p.G) return;
     const int total = p.starts[p.t.B], share = (total + p.ctas - 1) / p.ctas;
+    if (R >= rq.n * p.G || total == 0) return;
     const int tile = R / RT, r = R - tile * RT, units = tile_units<RT, UNIT>(rq, p.G, tile);
     int first = 0;
     for (int t = lane; t < tile; t += 32) first += tile_units<RT, UNIT>(rq, p.G, t);
@@ -513,8 +513,8 @@ __global__ void __launch_bounds__(128) paged_join_rows_kernel(const __grid_const
     const Request rq = request_at(p.c, p.t, b);
     const int rows = rq.n * p.G;
     kernel_before_done();
-    if (R0 >= rows) return;
     const int total = p.starts[p.t.B], share = (total + p.ctas - 1) / p.ctas;
+    if (R0 >= rows || total == 0) return;
     const int tile = R0 / RT, units = tile_units<RT, UNIT>(rq, p.G, tile);
     int first = 0;
     for (int t = lane; t < tile; t += 32) first += tile_units<RT, UNIT>(rq, p.G, t);

@@ -98,14 +98,16 @@ typedef struct gdn_cache {
  * cu_new[b + 1] of the packed streams, and the last ones of row rows[b], whose lens[rows[b]]
  * counts them already (gdn_cache_update grows it).
  *
- *  cu_new       device int32 [B + 1], rising from 0 to at most num_tokens; what lies behind
- *               cu_new[B] is neither read nor written
+ *  cu_new       device int32 [B + 1], never falling, from 0 to at most num_tokens; what lies
+ *               behind cu_new[B] is neither read nor written
  *  rows         device int32 [B], or NULL for row b (then B <= R).  A negative or out-of-range
  *               row marks padding: nothing is appended, its queries get zeros and lse -infinity.
- *  max_new      host bound of a request's new tokens (a request with more is refused on the
- *               device: GDN_ERR_INVALID_ARG in the status word, its results undefined)
- *  max_len      host bound of a row's tokens, 0: W * page_size; larger lengths are taken as it.
- *               A close one makes the better plan for attention.
+ *  max_new      host bound of a request's new tokens
+ *  max_len      host bound of a row's tokens for attention, 0: W * page_size.  A close one makes
+ *               the better plan.
+ *
+ * A request with more new tokens or a longer row than these bounds is refused on the device:
+ * GDN_ERR_INVALID_ARG in the status word, its results undefined (nothing is appended).
  *
  * A page number outside the pool among a row's pages is never followed: the status word takes
  * GDN_ERR_INVALID_ARG, and the request's results are undefined.

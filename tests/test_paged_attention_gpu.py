@@ -195,6 +195,35 @@ def test_bad_pages_and_counts_are_reported():
     assert gdn.read_status(ws=ws) == gdn.GDN_OK
 
 
+@pytest.mark.parametrize("dtype, G", [(BF, 2), (BF, 40), (F32, 2)])
+def test_lengths_past_their_bound_are_reported(dtype, G):
+    """A row longer than max_len, a loop replayed for too long for instance, is reported; the others keep their results."""
+    c = make_cache([40, 50], page=16, H=2, D=64)
+    q, cu = queries(2, 2 * G, 64, dtype), ints(0, 1, 2)
+    ws = torch.zeros(256, dtype=torch.uint8, device="cuda")
+    want = gdn.gdn_paged_attention(q, c, cu, max_len=50, ws=ws)["o"]
+    assert gdn.read_status(ws=ws) == gdn.GDN_OK
+    r = gdn.gdn_paged_attention(q, c, cu, max_len=49, ws=ws)
+    assert gdn.read_status(ws=ws) == gdn.GDN_ERR_INVALID_ARG
+    torch.testing.assert_close(r["o"][0], want[0], rtol=2.0 ** -7, atol=1e-6)
+
+
+@pytest.mark.parametrize("dtype, W", [(BF, 2 ** 14), (F32, 2 ** 13)])
+def test_counts_that_fall_are_reported(dtype, W):
+    """cu_new that falls again and again: more queries than the streams hold, past what 31 bits count; nothing is done."""
+    B, new, page = 4096, 4096, 128
+    c = gdn.PagedCache.empty(1, 1, 8, 64, 1, W, page_size=page)
+    c.lens.fill_(W * page)
+    cu = torch.zeros(B + 1, dtype=torch.int32, device="cuda")
+    cu[1::2] = new
+    q = torch.zeros(new, 8, 64, dtype=dtype, device="cuda")
+    o = torch.full_like(q, 7.0)
+    ws = torch.zeros(256, dtype=torch.uint8, device="cuda")
+    gdn.gdn_paged_attention(q, c, cu, rows=torch.zeros(B, dtype=torch.int32, device="cuda"), max_new=new, o=o, ws=ws)
+    assert gdn.read_status(ws=ws) == gdn.GDN_ERR_INVALID_ARG
+    assert (o == 7).all()
+
+
 @pytest.mark.parametrize("dtype, G, new", [(BF, 4, 1), (BF, 16, 20), (F32, 4, 2)])
 def test_captured_and_on_another_stream(dtype, G, new):
     """A captured call follows lengths, tables and counts that change between replays; two calls on two streams at once."""
