@@ -113,8 +113,13 @@ cudaError_t launch_compact(const UpkeepParams& p, cudaStream_t s);
 // The work is cut evenly over the CTAs: an item is a tile of RT query rows of one request and key/value head (rows in the
 // order of tokens and of the heads of the group), a unit is a number of tokens that an item's rows see, and CTA c takes the
 // units [c share, (c + 1) share) of them all, in the order of requests, heads, row tiles and tokens.  So a CTA has at most one
-// item that it begins in the middle (its part goes to slot 2 c) and one that it begins and leaves unfinished (slot 2 c + 1); a
-// join adds the parts up.  Lengths are read on the device only, and differ at will.
+// item that it begins in the middle (its part goes to slot 2 c) and one that it begins and leaves unfinished (slot 2 c + 1).
+// Every CTA describes the item that it begins in the middle, if the CTA before began it (a cut), and a join, whose grid follows the
+// CTAs and not the batch, adds the cut items' parts up.  Lengths are read on the device only, and differ at will.
+struct Cut {
+    int32_t rows, row0, h, first;   // 0 rows: no cut here
+    int32_t last, unused[3];        // CTAs c - 1 .. last have the item's parts
+};
 struct PagedParams {
     Cache c;
     Batch t;
@@ -124,7 +129,7 @@ struct PagedParams {
     float* lse;          // [T, Hq] or nullptr
     float* part_o;       // [2 CTAs][RT][D]: sums of 2^(x - m) v
     float2* part_ml;     // [2 CTAs][RT]: m, l
-    int32_t* starts;     // [B + 1] units before each request, written by the first CTA for the join
+    Cut* cuts;           // [CTAs]
     unsigned int* status;
     float scale_log2;
     int32_t Hq, G, ctas;
@@ -170,7 +175,7 @@ __device__ __forceinline__ int head_units(const Request& q, int G) {
 }
 
 // Units before every group of requests into s_cum, by all THREADS threads of a CTA, a thread a request; a group is the least power of two
-// with which kMaxGroups of them hold the batch (one request up to 256).  The first CTA writes p.starts.  The host's plan keeps the total
+// with which kMaxGroups of them hold the batch (one request up to 256).  The host's plan keeps the total
 // below 2^31 for counts as the call describes them; sums stop there, and others (cu_new that falls) are reported and nothing is done.
 constexpr unsigned kNoTotal = 0x7fffffffu;
 constexpr int kMaxGroups = 256;
@@ -197,7 +202,6 @@ __device__ __forceinline__ void count_units(const PagedParams& p, int* s_cum) {
             if ((tid & (width - 1)) >= o) y = min(y + z, kNoTotal);
         }
         if ((tid & (width - 1)) == width - 1 && (b >> shift) < groups) s_cum[(b >> shift) + 1] = (int)y;
-        if (blockIdx.x == 0 && b < B) p.starts[b] = (int)(y - n);
     }
     __syncthreads();
     if (tid < 32) {
@@ -219,22 +223,18 @@ __device__ __forceinline__ void count_units(const PagedParams& p, int* s_cum) {
         if (lane == 0) s_cum[0] = 0;
     }
     __syncthreads();
-    if (blockIdx.x == 0) {
-        for (int b = tid; b < B; b += THREADS) p.starts[b] += s_cum[b >> shift];   // (what the same thread wrote)
-        if (tid == 0) p.starts[B] = s_cum[groups];
-    }
 }
 
-// What a CTA does of one item, from unit x on: rows row0 .. of `rows` of the request, tokens lo .. hi.  Called by whole warps.
+// What a CTA does of one item: rows row0 .. of `rows` of the request, tokens lo .. hi; it has the item's units u0 .. u1.
 struct Segment {
     Request rq;
     int h, row0, rows, lo, hi, u0, u1, units;
     __device__ __forceinline__ bool whole() const { return u0 == 0 && u1 == units; }
     __device__ __forceinline__ int64_t slot() const { return 2 * (int64_t)blockIdx.x + (u0 == 0); }
 };
+// The item at unit x, looked for.  Called by whole warps.
 template <int RT, int UNIT>
-__device__ __forceinline__ Segment segment_at(const PagedParams& p, const int* s_cum, int x, int end) {
-    Segment s;
+__device__ __forceinline__ void find_item(const PagedParams& p, const int* s_cum, int x, Segment& s) {
     const int shift = group_log2(p.t.B);
     int g = 0, top = groups_of(p.t.B);   // cum[g] <= x < cum[top]
     while (top - g > 1) {
@@ -267,16 +267,40 @@ __device__ __forceinline__ Segment segment_at(const PagedParams& p, const int* s
     int tile = 0;
     TileWalk<RT, UNIT> w(s.rq, p.G);
     for (const int last = (s.rq.n * p.G - 1) / RT;; ++tile) {   // (it ends, whatever becomes of the lengths meanwhile)
-        s.units = w.next();
-        if (s.u0 < s.units || tile >= last) break;
-        s.u0 -= s.units;
+        const int units = w.next();
+        if (s.u0 < units || tile >= last) break;
+        s.u0 -= units;
     }
-    s.u1 = min(s.units, s.u0 + end - x);
     s.row0 = tile * RT;
-    s.rows = min(s.rq.n * p.G - s.row0, RT);
+}
+// The item at unit x, where the one of `s` ended: the request's next tile or head (found step by step from its first, the tiles of
+// prompts cost more than their products), another request's, or, after segment_none(), the CTA's first.
+template <int RT, int UNIT>
+__device__ __forceinline__ void next_segment(const PagedParams& p, const int* s_cum, int x, int end, Segment& s) {
+    s.row0 += RT, s.u0 = 0;
+    if (s.row0 >= s.rq.n * p.G) {
+        s.row0 = 0;
+        if (++s.h >= p.c.Hkv) find_item<RT, UNIT>(p, s_cum, x, s);
+    }
+    const int rows = s.rq.n * p.G - s.row0, seen = tile_sees(s.rq, p.G, RT, s.row0 / RT);
+    s.units = max(1, (seen + UNIT - 1) / UNIT);
+    s.u1 = min(s.units, s.u0 + end - x);
+    s.rows = min(rows, RT);
     s.lo = s.u0 * UNIT;
-    s.hi = min(s.u1 * UNIT, tile_sees(s.rq, p.G, RT, tile));
+    s.hi = min(s.u1 * UNIT, seen);
+}
+__device__ __forceinline__ Segment segment_none() {
+    Segment s{};
+    s.h = 1 << 30;
     return s;
+}
+// The CTA's cut, written by one thread when it has its first segment.
+__device__ __forceinline__ void describe_cut(const PagedParams& p, const Segment& s, int begin, int share) {
+    const int at = begin - s.u0;   // the item's first unit
+    Cut c{};
+    if (s.u0 > 0 && at >= begin - share)
+        c.rows = s.rows, c.row0 = s.row0, c.h = s.h, c.first = s.rq.first, c.last = (at + s.units - 1) / share;
+    p.cuts[blockIdx.x] = c;
 }
 
 constexpr int kUnit = 64;       // tokens of a unit: warp-level products

@@ -107,8 +107,8 @@ gdn_status plan_paged(const gdn_cache* c, const Batch& t, gdn_dtype dtype, int H
     if (items >= (1ll << 31) / per_item - (1 << 16)) return GDN_ERR_UNSUPPORTED;
     const int per_sm = pl.tc ? 1 : pl.tiles == 1 ? 3 : 2;
     pl.ctas = (int)std::max<int64_t>(1, std::min<int64_t>(items * per_item, (int64_t)kSms * per_sm));
-    pl.join = per_item > 1;
-    pl.ml_off = ((size_t)(t.B + 1) * 4 + 31) / 32 * 32;
+    pl.join = per_item > 1 && pl.ctas > 1;
+    pl.ml_off = (size_t)pl.ctas * sizeof(Cut);
     pl.o_off = pl.ml_off + (size_t)2 * pl.ctas * pl.tile_rows * 8;
     pl.total = pl.o_off + (size_t)2 * pl.ctas * pl.tile_rows * c->head_dim * 4;
     return GDN_OK;
@@ -242,7 +242,7 @@ GDN_EXPORT gdn_status gdn_paged_attention(const gdn_cache* c, int32_t layer, con
     p.c = cache_of(c, layer);
     p.q = q, p.o = o, p.lse = lse;
     unsigned char* sc = static_cast<unsigned char*>(scratch);
-    p.starts = reinterpret_cast<int32_t*>(sc);
+    p.cuts = reinterpret_cast<Cut*>(sc);
     p.part_ml = reinterpret_cast<float2*>(sc + pl.ml_off);
     p.part_o = reinterpret_cast<float*>(sc + pl.o_off);
     p.status = static_cast<unsigned int*>(workspace);

@@ -118,10 +118,13 @@ __global__ void __launch_bounds__(kWarps * 32, MT == 1 ? 3 : 2) paged_kernel(con
     count_units<kWarps * 32, RT, kUnit>(p, s_cum);
     const int total = s_cum[groups_of(p.t.B)], share = (total + gridDim.x - 1) / gridDim.x;
     int x = (int)min((int64_t)blockIdx.x * share, (int64_t)total);
-    const int end = min(x + share, total);
+    const int begin = x, end = min(x + share, total);
+    if (begin >= end && tid == 0) p.cuts[blockIdx.x] = Cut{};
 
+    Segment sg = segment_none();
     while (x < end) {
-        const Segment sg = segment_at<RT, kUnit>(p, s_cum, x, end);
+        next_segment<RT, kUnit>(p, s_cum, x, end, sg);
+        if (x == begin && tid == 0) describe_cut(p, sg, begin, share);
         const Request& rq = sg.rq;
         const int h = sg.h, row0 = sg.row0, rows = sg.rows, lo = sg.lo, hi = sg.hi;
         x += sg.u1 - sg.u0;
@@ -450,24 +453,16 @@ __global__ void __launch_bounds__(kWarps * 32, MT == 1 ? 3 : 2) paged_kernel(con
 // follows in the stream waits for it too.
 __device__ __forceinline__ void kernel_before_done() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
-// A CTA adds up the parts of one query row, four warps sharing them.
-template <int D, typename T, int RT, int UNIT>
+// A CTA adds up the parts of one row of a cut item, four warps sharing them.
+template <int D, typename T, int RT>
 __global__ void __launch_bounds__(128) paged_join_kernel(const __grid_constant__ PagedParams p) {
     constexpr int N = D / 32, W = 4;
     __shared__ float s_acc[W][D], s_l[W];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int b = blockIdx.y, h = blockIdx.z, R = blockIdx.x;
-    const Request rq = request_at(p.c, p.t, b);
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, r = blockIdx.x, c0 = blockIdx.y;
     kernel_before_done();
-    const int total = p.starts[p.t.B], share = (total + p.ctas - 1) / p.ctas;
-    if (R >= rq.n * p.G || total == 0) return;
-    const int tile = R / RT, r = R - tile * RT, units = tile_units<RT, UNIT>(rq, p.G, tile);
-    int first = 0;
-    for (int t = lane; t < tile; t += 32) first += tile_units<RT, UNIT>(rq, p.G, t);
-    first = __reduce_add_sync(0xffffffffu, first);
-    first += p.starts[b] + h * ((p.starts[b + 1] - p.starts[b]) / p.c.Hkv);
-    const int c0 = first / share, c1 = (first + units - 1) / share;
-    if (c0 == c1) return;   // one part: its CTA has written the row
+    const Cut cut = p.cuts[c0 + 1];
+    if (r >= cut.rows) return;
+    const int c1 = cut.last;
     auto slot = [&](int c) { return (int64_t)2 * c + (c == c0); };
     float m = -INFINITY;
     for (int c = c0 + lane; c <= c1; c += 32) m = fmaxf(m, p.part_ml[slot(c) * RT + r].x);
@@ -490,11 +485,11 @@ __global__ void __launch_bounds__(128) paged_join_kernel(const __grid_constant__
     for (int k = 0; k < N; ++k) s_acc[warp][lane * N + k] = acc[k];
     if (lane == 0) s_l[warp] = l;
     __syncthreads();
-    const int d = threadIdx.x;
+    const int d = threadIdx.x, R = cut.row0 + r;
     l = 0.f;
 #pragma unroll
     for (int w = 0; w < W; ++w) l += s_l[w];
-    const int64_t at = (int64_t)(rq.first + R / p.G) * p.Hq + h * p.G + R % p.G;
+    const int64_t at = (int64_t)(cut.first + R / p.G) * p.Hq + cut.h * p.G + R % p.G;
     if (d < D) {
         float y = 0.f;
 #pragma unroll
@@ -504,27 +499,17 @@ __global__ void __launch_bounds__(128) paged_join_kernel(const __grid_constant__
     if (d == 0 && p.lse) p.lse[at] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
 }
 
-// The same for tiles of many rows, few of which are cut: a CTA takes 32 rows, a warp each of them in turn.
-template <int D, typename T, int RT, int UNIT>
+// The same for tiles of many rows and few parts: a CTA takes 32 rows, a warp each of them in turn.
+template <int D, typename T, int RT>
 __global__ void __launch_bounds__(128) paged_join_rows_kernel(const __grid_constant__ PagedParams p) {
     constexpr int N = D / 32;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int b = blockIdx.y, h = blockIdx.z, R0 = blockIdx.x * 32;
-    const Request rq = request_at(p.c, p.t, b);
-    const int rows = rq.n * p.G;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, c0 = blockIdx.y;
     kernel_before_done();
-    const int total = p.starts[p.t.B], share = (total + p.ctas - 1) / p.ctas;
-    if (R0 >= rows || total == 0) return;
-    const int tile = R0 / RT, units = tile_units<RT, UNIT>(rq, p.G, tile);
-    int first = 0;
-    for (int t = lane; t < tile; t += 32) first += tile_units<RT, UNIT>(rq, p.G, t);
-    first = __reduce_add_sync(0xffffffffu, first);
-    first += p.starts[b] + h * ((p.starts[b + 1] - p.starts[b]) / p.c.Hkv);
-    const int c0 = first / share, c1 = (first + units - 1) / share;
-    if (c0 == c1) return;   // one part: its CTA has written the rows
+    const Cut cut = p.cuts[c0 + 1];
+    const int c1 = cut.last, end = min((int)blockIdx.x * 32 + 32, cut.rows);
 #pragma unroll 2
-    for (int R = R0 + warp; R < min(R0 + 32, rows); R += 4) {
-        const int r = R - tile * RT;
+    for (int r = blockIdx.x * 32 + warp; r < end; r += 4) {
+        const int R = cut.row0 + r;
         float m = -INFINITY;
         for (int c = c0; c <= c1; ++c) m = fmaxf(m, p.part_ml[(2 * (int64_t)c + (c == c0)) * RT + r].x);
         float acc[N] = {}, l = 0.f;
@@ -537,7 +522,7 @@ __global__ void __launch_bounds__(128) paged_join_rows_kernel(const __grid_const
 #pragma unroll
             for (int k = 0; k < N; ++k) acc[k] += f * p.part_o[at * D + lane * N + k];
         }
-        const int64_t at = (int64_t)(rq.first + R / p.G) * p.Hq + h * p.G + R % p.G;
+        const int64_t at = (int64_t)(cut.first + R / p.G) * p.Hq + cut.h * p.G + R % p.G;
         const float inv = l > 0.f ? 1.f / l : l == 0.f ? 0.f : NAN;
 #pragma unroll
         for (int k = 0; k < N; ++k) put(static_cast<T*>(p.o) + at * D + lane * N + k, acc[k] * inv);
@@ -556,24 +541,23 @@ cudaError_t launch(const PagedParams& p, cudaStream_t s) {
 }
 template <int D, typename T>
 cudaError_t join(const PagedParams& p, int tile_rows, cudaStream_t s) {
-    const int64_t rows = (int64_t)p.t.max_new * p.G;
-    // Large tiles: a CTA a row costs 2 us for about 2432 rows (16 CTAs a multiprocessor), most of which end at once; a warp for 8 rows in
-    // turn takes 1.5 us a row and 0.3 us a part.  (1 x 40 rows x 2 heads on 100 k tokens, 76 parts: 207 us by warps, 44 by rows; 131 k rows of 2
-    // parts: 80 us by rows, 10 by warps.)
-    const int64_t items = (rows + tile_rows - 1) / tile_rows * p.t.B * p.c.Hkv, parts = p.ctas / std::max<int64_t>(items, 1) + 1;
-    const bool by_row = tile_rows <= 32 || rows * p.t.B * p.c.Hkv < 14600 + 2900 * parts;
+    const int64_t all = (int64_t)p.t.max_new * p.G, rows = std::min<int64_t>(all, tile_rows);
+    // Large tiles: a CTA a row costs 2 us for about 2432 rows (16 CTAs a multiprocessor), cut or not; a warp for 8 rows in turn takes
+    // 1.5 us a row and 0.3 us a part.  (1 x 40 rows x 2 heads on 100 k tokens, 76 parts: 207 us by warps, 44 by rows.)
+    const int64_t items = (all + tile_rows - 1) / tile_rows * p.t.B * p.c.Hkv, parts = p.ctas / items + 1;
+    const bool by_row = tile_rows <= 32 || rows * p.ctas < 14600 + 2900 * parts;
     cudaLaunchConfig_t cfg{};
     cudaLaunchAttribute attr{};
     attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr.val.programmaticStreamSerializationAllowed = 1;
-    cfg.gridDim = dim3((unsigned)(by_row ? rows : (rows + 31) / 32), p.t.B, p.c.Hkv), cfg.blockDim = dim3(128), cfg.stream = s;
+    cfg.gridDim = dim3((unsigned)(by_row ? rows : (rows + 31) / 32), p.ctas - 1), cfg.blockDim = dim3(128), cfg.stream = s;
     cfg.attrs = &attr, cfg.numAttrs = 1;
-    if (tile_rows == 16) return cudaLaunchKernelEx(&cfg, paged_join_kernel<D, T, 16, kUnit>, p);
+    if (tile_rows == 16) return cudaLaunchKernelEx(&cfg, paged_join_kernel<D, T, 16>, p);
     if constexpr (sizeof(T) == 4 || D == 32) {
-        if (tile_rows == 32) return cudaLaunchKernelEx(&cfg, paged_join_kernel<D, T, 32, kUnit>, p);
+        if (tile_rows == 32) return cudaLaunchKernelEx(&cfg, paged_join_kernel<D, T, 32>, p);
     } else {
-        if (by_row) return cudaLaunchKernelEx(&cfg, paged_join_kernel<D, T, kTcRows, kTcUnit>, p);
-        return cudaLaunchKernelEx(&cfg, paged_join_rows_kernel<D, T, kTcRows, kTcUnit>, p);
+        if (by_row) return cudaLaunchKernelEx(&cfg, paged_join_kernel<D, T, kTcRows>, p);
+        return cudaLaunchKernelEx(&cfg, paged_join_rows_kernel<D, T, kTcRows>, p);
     }
     return cudaErrorInvalidValue;
 }

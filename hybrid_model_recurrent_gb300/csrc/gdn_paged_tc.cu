@@ -221,14 +221,17 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_cons
     const int total = s_cum[groups_of(p.t.B)], share = (total + (int)gridDim.x - 1) / (int)gridDim.x;
     const int begin = (int)min((int64_t)blockIdx.x * share, (int64_t)total), end = min(begin + share, total);
 
+    if (begin >= end && tid == 0) p.cuts[blockIdx.x] = Cut{};
+
     // Every role walks the CTA's items; an item of at most 128 rows takes one row tile, the two in turn, so that one tile's sums
     // leave and its next Q arrives while the other computes.
-    auto takes = [&](const Segment& x, int& turn) {
+    Segment x = segment_none();
+    auto takes = [&](int& turn) {
         const int one = turn;
         if (x.rows <= kRows) turn ^= 1;
         return x.rows > kRows ? 3 : 1 << one;   // bit a: row tile a
     };
-    auto tiles_of = [&](const Segment& x) { return max(0, (x.hi - x.lo + kKeys - 1) / kKeys); };
+    auto tiles_of = [&] { return max(0, (x.hi - x.lo + kKeys - 1) / kKeys); };
 
     if (warp >= 8) {
         if (warp == 8 || warp == 15) {
@@ -241,9 +244,9 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_cons
             int it = 0, turn = 0, steps = 0, nth = 0;   // tiles of all items; steps and items of this row tile
             const uint64_t q = tile_desc(sbase + a * F::kTile, false);
             for (int at = begin; ok && at < end;) {
-                const Segment x = segment_at<kTcRows, kTcUnit>(p, s_cum, at, end);
+                next_segment<kTcRows, kTcUnit>(p, s_cum, at, end, x);
                 at += x.u1 - x.u0;
-                const int n = 2 * tiles_of(x), on = takes(x, turn);
+                const int n = 2 * tiles_of(), on = takes(turn);
                 if (n == 0) continue;
                 if (!(on >> a & 1)) {   // the other row tile's alone: pass by, entry after entry, so that no barrier gets ahead
                     for (int i = 0; ok && i < 2 * n; ++i) {
@@ -313,9 +316,9 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_cons
                 const int stop = p.stall_after >= 0 ? 4 * p.stall_after : 0x7fffffff;   // testing hook
                 int asked = 0;
                 for (int at = begin; ok && at < end;) {
-                    const Segment x = segment_at<kTcRows, kTcUnit>(p, s_cum, at, end);
+                    next_segment<kTcRows, kTcUnit>(p, s_cum, at, end, x);
                     at += x.u1 - x.u0;
-                    const int n = tiles_of(x);
+                    const int n = tiles_of();
                     if (n == 0) continue;
                     const int32_t* table = p.c.table + (int64_t)x.rq.row * p.c.W;   // (a row without tokens has no tiles)
                     // this lane's piece of tile j, and where it lies: found a tile ahead, so that a copy is a few instructions
@@ -362,9 +365,9 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_cons
                 unsigned char* to0 = smem + F::kRing + (64 * half + 8 * g0 + sub) * 128;
                 const bool describes = warp == 12;   // (with two groups of 8 tokens, others have three)
                 for (int at = begin; ok && at < end;) {
-                    const Segment x = segment_at<kTcRows, kTcUnit>(p, s_cum, at, end);
+                    next_segment<kTcRows, kTcUnit>(p, s_cum, at, end, x);
                     at += x.u1 - x.u0;
-                    const int n = tiles_of(x);
+                    const int n = tiles_of();
                     if (n == 0) continue;
                     const int32_t* table = p.c.table + (int64_t)x.rq.row * p.c.W;
                     // the scales of the tokens 16 l .. 16 l + 15 of tile j
@@ -441,9 +444,10 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_cons
         bool ok = true;
         int turn = 0, it = 0, g = 0;   // tiles of all items; steps of this row tile
         for (int at = begin; ok && at < end;) {
-            const Segment x = segment_at<kTcRows, kTcUnit>(p, s_cum, at, end);
+            next_segment<kTcRows, kTcUnit>(p, s_cum, at, end, x);
+            if (at == begin && tid == 0) describe_cut(p, x, begin, share);
             at += x.u1 - x.u0;
-            const int on = takes(x, turn), n = tiles_of(x), it0 = it;
+            const int on = takes(turn), n = tiles_of(), it0 = it;
             it += n;
             if (!(on >> a & 1)) continue;
             const int rr = (on == 3 ? a * kRows : 0) + r;   // row of the item

@@ -302,6 +302,17 @@ def test_many_queries_long_and_few():
     check_attention(c, queries(12 * 40, 4, 64, BF), cu_of([40] * 12), max_new=40, **TC)
 
 
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_a_prompt_among_single_tokens(dtype):
+    """Requests of one token around one of hundreds: cuts in both kinds, tiles and heads of one request after one another."""
+    lens, new = [700, 90, 5, 1000, 333, 64, 2000], [1, 1, 1, 900, 1, 1, 40]
+    c = make_cache(lens, page=32, H=3, D=64)
+    check_attention(c, queries(sum(new), 6, 64, dtype), cu_of(new), max_new=900, **step_of(dtype, 64, 1800))
+    lens, new = [50 + i for i in range(300)], [1] * 299 + [349]
+    c = make_cache(lens, page=32, H=2, D=64)
+    check_attention(c, queries(sum(new), 4, 64, dtype), cu_of(new), max_new=349, **step_of(dtype, 64, 698))
+
+
 def test_many_queries_many_requests():
     lens = [(37 * i) % 300 for i in range(400)]
     new = [(5 * i) % 23 for i in range(400)]
