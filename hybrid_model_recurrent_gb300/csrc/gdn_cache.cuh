@@ -133,9 +133,16 @@ struct PagedParams {
     unsigned int* status;
     float scale_log2;
     int32_t Hq, G, ctas;
+    int32_t min_rows, max_rows;         // requests with other numbers of query rows a key/value head are another launch's
     unsigned long long wait_limit_ns;   // (tensor-core kernel)
     int32_t stall_after;
 };
+
+__device__ __forceinline__ Request attended(const PagedParams& p, int b) {
+    Request q = request_at(p.c, p.t, b);
+    if (q.n * p.G < p.min_rows || q.n * p.G > p.max_rows) q.n = 0;
+    return q;
+}
 
 // The join's CTAs may be started (they wait for this kernel's end before they read anything of it).
 __device__ __forceinline__ void join_may_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
@@ -192,7 +199,7 @@ __device__ __forceinline__ void count_units(const PagedParams& p, int* s_cum) {
         const int b = b0 + tid;
         unsigned n = 0;
         if (b < B) {
-            const Request q = request_at(p.c, p.t, b);
+            const Request q = attended(p, b);
             if (q.bad && blockIdx.x == 0) atomicOr(p.status, STATUS_BAD_INDEX);
             n = (unsigned)(head_units<RT, UNIT>(q, p.G) * p.c.Hkv);
         }
@@ -249,7 +256,7 @@ __device__ __forceinline__ void find_item(const PagedParams& p, const int* s_cum
     } else {   // the requests of the group, a lane each
         const int lane = threadIdx.x & 31, b = (g << shift) + lane, width = 1 << shift;
         Request q{-1, 0, 0, 0, false};
-        if (lane < width && b < p.t.B) q = request_at(p.c, p.t, b);
+        if (lane < width && b < p.t.B) q = attended(p, b);
         const int per_head = head_units<RT, UNIT>(q, p.G), n = per_head * p.c.Hkv;
         int after = n;
         for (int o = 1; o < width; o <<= 1) {

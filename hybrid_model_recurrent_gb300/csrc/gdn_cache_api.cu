@@ -87,12 +87,14 @@ struct PagedPlan {
     bool tc, join;
     int tiles, ctas;   // row tiles of 16 a CTA (without tensor cores of the 5th generation); CTAs
     int tile_rows;
+    int min_rows, max_rows;
     size_t ml_off, o_off, total;
 };
 
-gdn_status plan_paged(const gdn_cache* c, const Batch& t, gdn_dtype dtype, int Hq, PagedPlan& pl) {
-    const int64_t G = Hq / c->num_kv_heads, rows = t.max_new * G;
-    if (rows >= (1ll << 31) - 1024) return GDN_ERR_UNSUPPORTED;
+// The launches for requests with rows in min_rows .. max_rows.
+gdn_status plan_rows(const gdn_cache* c, const Batch& t, gdn_dtype dtype, int G, int64_t min_rows, int64_t max_rows, PagedPlan& pl) {
+    const int64_t rows = std::min(t.max_new * (int64_t)G, max_rows);
+    pl.min_rows = (int)min_rows, pl.max_rows = (int)max_rows;
     // The tensor cores of the 5th generation take 256 rows a tile, filled or not, warp-level products 16 or 32.  Measured, us, warp-level /
     // tensor cores: 16 requests x 4 heads on 8192 tokens 46 / 56 at 16 rows a head, 63 / 57 at 24, 93 / 59 at 40, 169 / 71 at 128; 4 x 8
     // heads on 30000 64 / 90, 87 / 90, - , 264 / 99; 1 x 2 heads on 100000 44 / 43, 48 / 44, 64 / 44, 84 / 48.
@@ -111,6 +113,27 @@ gdn_status plan_paged(const gdn_cache* c, const Batch& t, gdn_dtype dtype, int H
     pl.ml_off = (size_t)pl.ctas * sizeof(Cut);
     pl.o_off = pl.ml_off + (size_t)2 * pl.ctas * pl.tile_rows * 8;
     pl.total = pl.o_off + (size_t)2 * pl.ctas * pl.tile_rows * c->head_dim * 4;
+    return GDN_OK;
+}
+
+// One plan, or two: where the average request has at most a quarter of the longest one's new tokens (a prompt among single tokens),
+// those with 16 rows at most go ahead by themselves, for tiles of 256 rows cost them three times as much; the other two launches cost 14 to
+// 19 us, as 4096 units or so.  Measured, us, one plan / two: 255 single tokens on 2000 x 4 heads of 64 and a prompt of 2000 360 / 191; 63 on
+// 4096 x 8 heads of 128 and one of 8192 865 / 728; 15 on 2000 x 4 heads of 128 (1024 units) and 300 54 / 72.
+gdn_status plan_paged(const gdn_cache* c, const Batch& t, gdn_dtype dtype, int Hq, PagedPlan (&pl)[2], int& plans, size_t& bytes) {
+    const int G = Hq / c->num_kv_heads;
+    const int64_t rows = t.max_new * (int64_t)G, most = (1ll << 31) - 1024;
+    if (rows >= most) return GDN_ERR_UNSUPPORTED;
+    plans = 1;
+    const gdn_status st = plan_rows(c, t, dtype, G, 0, most, pl[0]);
+    if (st != GDN_OK) return st;
+    bytes = pl[0].total;
+    if (pl[0].tc && G <= 16 && (int64_t)t.B * t.max_new >= 4ll * t.T &&
+        t.B * ceil_div(t.max_len, kTcUnit) * c->num_kv_heads >= 4096 && plan_rows(c, t, dtype, G, 0, 16, pl[1]) == GDN_OK) {
+        std::swap(pl[0], pl[1]);
+        pl[1].min_rows = 17;
+        plans = 2, bytes = std::max(bytes, pl[0].total);   // (one after the other)
+    }
     return GDN_OK;
 }
 
@@ -213,11 +236,13 @@ GDN_EXPORT gdn_status gdn_cache_append(const gdn_cache* c, int32_t layer, const 
 
 GDN_EXPORT size_t gdn_paged_scratch_bytes(const gdn_cache* c, const gdn_batch* b, gdn_dtype dtype, int32_t num_q_heads) {
     Batch t{};
-    PagedPlan pl{};
+    PagedPlan pl[2];
+    int plans;
+    size_t bytes;
     if (check_cache(c, false) != GDN_OK || check_batch(c, b, t) != GDN_OK || check_heads(c, dtype, num_q_heads) != GDN_OK ||
-        plan_paged(c, t, dtype, num_q_heads, pl) != GDN_OK)
+        plan_paged(c, t, dtype, num_q_heads, pl, plans, bytes) != GDN_OK)
         return 0;
-    return pl.total;
+    return bytes;
 }
 
 GDN_EXPORT gdn_status gdn_paged_attention(const gdn_cache* c, int32_t layer, const gdn_batch* b, const void* q, gdn_dtype dtype,
@@ -234,25 +259,31 @@ GDN_EXPORT gdn_status gdn_paged_attention(const gdn_cache* c, int32_t layer, con
     if (!std::isfinite(p.scale_log2)) return GDN_ERR_INVALID_ARG;
     p.q_stride = q_stride;
     if ((st = check_stride(p.q_stride, (int64_t)num_q_heads * c->head_dim, dtype)) != GDN_OK) return st;
-    PagedPlan pl{};
-    if ((st = plan_paged(c, p.t, dtype, num_q_heads, pl)) != GDN_OK) return st;
-    if (!scratch || !aligned(scratch, 32) || scratch_bytes < pl.total || !aligned(lse, 4)) return GDN_ERR_INVALID_ARG;
+    PagedPlan plan[2];
+    int plans;
+    size_t bytes;
+    if ((st = plan_paged(c, p.t, dtype, num_q_heads, plan, plans, bytes)) != GDN_OK) return st;
+    if (!scratch || !aligned(scratch, 32) || scratch_bytes < bytes || !aligned(lse, 4)) return GDN_ERR_INVALID_ARG;
     if (p.t.T == 0) return GDN_OK;
     if (!q || !o || !aligned(q, 16) || !aligned(o, 16)) return GDN_ERR_INVALID_ARG;
     p.c = cache_of(c, layer);
     p.q = q, p.o = o, p.lse = lse;
     unsigned char* sc = static_cast<unsigned char*>(scratch);
     p.cuts = reinterpret_cast<Cut*>(sc);
-    p.part_ml = reinterpret_cast<float2*>(sc + pl.ml_off);
-    p.part_o = reinterpret_cast<float*>(sc + pl.o_off);
     p.status = static_cast<unsigned int*>(workspace);
-    p.Hq = num_q_heads, p.G = num_q_heads / c->num_kv_heads, p.ctas = pl.ctas;
+    p.Hq = num_q_heads, p.G = num_q_heads / c->num_kv_heads;
     p.wait_limit_ns = gdn::wait_limit_ns();
     p.stall_after = gdn::stall_after();
     const bool bf16 = dtype == GDN_BF16;
     const cudaStream_t s = (cudaStream_t)stream;
-    st = launched(pl.tc ? launch_paged_tc(p, c->head_dim, s) : launch_paged(p, c->head_dim, bf16, pl.tiles, s));
-    return st == GDN_OK && pl.join ? launched(launch_paged_join(p, c->head_dim, bf16, pl.tile_rows, s)) : st;
+    for (int i = 0; st == GDN_OK && i < plans; ++i) {
+        const PagedPlan& pl = plan[i];
+        p.part_ml = reinterpret_cast<float2*>(sc + pl.ml_off), p.part_o = reinterpret_cast<float*>(sc + pl.o_off);
+        p.ctas = pl.ctas, p.min_rows = pl.min_rows, p.max_rows = pl.max_rows;
+        st = launched(pl.tc ? launch_paged_tc(p, c->head_dim, s) : launch_paged(p, c->head_dim, bf16, pl.tiles, s));
+        if (st == GDN_OK && pl.join) st = launched(launch_paged_join(p, c->head_dim, bf16, pl.tile_rows, s));
+    }
+    return st;
 }
 
 GDN_EXPORT size_t gdn_cache_scratch_bytes(const gdn_cache* c) { return check_cache(c, true) == GDN_OK ? upkeep_bytes(c) : 0; }

@@ -541,7 +541,7 @@ cudaError_t launch(const PagedParams& p, cudaStream_t s) {
 }
 template <int D, typename T>
 cudaError_t join(const PagedParams& p, int tile_rows, cudaStream_t s) {
-    const int64_t all = (int64_t)p.t.max_new * p.G, rows = std::min<int64_t>(all, tile_rows);
+    const int64_t all = std::min<int64_t>((int64_t)p.t.max_new * p.G, p.max_rows), rows = std::min<int64_t>(all, tile_rows);
     // Large tiles: a CTA a row costs 2 us for about 2432 rows (16 CTAs a multiprocessor), cut or not; a warp for 8 rows in turn takes
     // 1.5 us a row and 0.3 us a part.  (1 x 40 rows x 2 heads on 100 k tokens, 76 parts: 207 us by warps, 44 by rows.)
     const int64_t items = (all + tile_rows - 1) / tile_rows * p.t.B * p.c.Hkv, parts = p.ctas / items + 1;

@@ -302,15 +302,37 @@ def test_many_queries_long_and_few():
     check_attention(c, queries(12 * 40, 4, 64, BF), cu_of([40] * 12), max_new=40, **TC)
 
 
+@pytest.mark.parametrize("D", [64, 128])
+def test_few_rows_many_items(D):
+    """Items of one row tile, short, long and without tokens, and of two, one after another on the same multiprocessors."""
+    lens, new = [], []
+    for i in range(90):
+        lens.append((0, 40, 700, 130, 1500, 520, 511)[i % 7] + i)
+        new.append((1, 20, 5, 3, 70, 0, 9)[i % 7])
+    lens[0] = lens[21] = lens[70] = 0
+    c = make_cache(lens, page=32, H=8, D=D)
+    check_attention(c, queries(sum(new), 16, D, BF), cu_of(new), max_new=70, **TC)
+    check_attention(c, queries(sum(new), 48, D, BF), cu_of(new), max_new=70, **TC)
+
+
 @pytest.mark.parametrize("dtype", [BF, F32])
 def test_a_prompt_among_single_tokens(dtype):
     """Requests of one token around one of hundreds: cuts in both kinds, tiles and heads of one request after one another."""
     lens, new = [700, 90, 5, 1000, 333, 64, 2000], [1, 1, 1, 900, 1, 1, 40]
     c = make_cache(lens, page=32, H=3, D=64)
     check_attention(c, queries(sum(new), 6, 64, dtype), cu_of(new), max_new=900, **step_of(dtype, 64, 1800))
-    lens, new = [50 + i for i in range(300)], [1] * 299 + [349]
-    c = make_cache(lens, page=32, H=2, D=64)
-    check_attention(c, queries(sum(new), 4, 64, dtype), cu_of(new), max_new=349, **step_of(dtype, 64, 698))
+    lens, new = [50 + i for i in range(300)], [1] * 299 + [349]   # few tokens: one launch; 600 * 7 units: those of few rows by themselves
+    c = make_cache(lens, page=32, H=2, D=64, W=30)
+    q, cu = queries(sum(new), 4, 64, dtype), cu_of(new)
+    for longest in (0, 860):
+        check_attention(c, q, cu, max_new=349, max_len=longest or 349, **step_of(dtype, 64, 698))
+    new = [1] * 100 + [9] * 99 + [8] * 100 + [349]               # 16 and 18 rows a head
+    lens = [n + 20 for n in new]
+    c = make_cache(lens, page=32, H=2, D=64, W=30)
+    check_attention(c, queries(sum(new), 4, 64, dtype), cu_of(new), max_new=349, max_len=900, **step_of(dtype, 64, 698))
+    # a prompt alone that is not there: all requests are the other launch's
+    c = make_cache([30] * 300, page=32, H=2, D=64, W=30)
+    check_attention(c, queries(300, 4, 64, dtype), cu_of([1] * 300), max_len=900, **step_of(dtype, 64, 600))
 
 
 def test_many_queries_many_requests():
