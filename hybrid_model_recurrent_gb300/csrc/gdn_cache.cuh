@@ -112,7 +112,9 @@ cudaError_t launch_compact(const UpkeepParams& p, cudaStream_t s);
 //
 // The work is cut evenly over the CTAs: an item is a tile of RT query rows of one request and key/value head (rows in the
 // order of tokens and of the heads of the group), a unit is a number of tokens that an item's rows see, and CTA c takes the
-// units [c share, (c + 1) share) of them all, in the order of requests, heads, row tiles and tokens.  So a CTA has at most one
+// units [c share, (c + 1) share) of them all, in the order of requests, heads, row tiles and tokens.  What an item costs besides its
+// tokens counts as LEAD units before them, which are nobody's work: else the CTAs that have a prompt's first tiles, of few tokens, are
+// late (a prompt of 8192 x 32 heads, bf16: 616 us without lead, 479 with 4 units).  So a CTA has at most one
 // item that it begins in the middle (its part goes to slot 2 c) and one that it begins and leaves unfinished (slot 2 c + 1).
 // Every CTA describes the item that it begins in the middle, if the CTA before began it (a cut), and a join, whose grid follows the
 // CTAs and not the batch, adds the cut items' parts up.  Lengths are read on the device only, and differ at will.
@@ -147,16 +149,17 @@ __device__ __forceinline__ Request attended(const PagedParams& p, int b) {
 // The join's CTAs may be started (they wait for this kernel's end before they read anything of it).
 __device__ __forceinline__ void join_may_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
-// Tokens that a row tile's last row sees, and the tile's units (one at least: rows that see nothing are written too).
+constexpr int kUnit = 64;       // tokens of a unit: warp-level products
+constexpr int kTcUnit = 128;    // 5th-generation tensor cores
+constexpr int kTcRows = 256;
+__host__ __device__ constexpr int lead(int unit) { return unit == kTcUnit ? 4 : 0; }
+
+// Tokens that a row tile's last row sees (its units are one at least: rows that see nothing are written too).
 __device__ __forceinline__ int tile_sees(const Request& q, int G, int RT, int tile) {
     const int last = (min((tile + 1) * RT, q.n * G) - 1) / G;
     return max(0, min(q.len, q.len - q.n + last + 1));
 }
-template <int RT, int UNIT>
-__device__ __forceinline__ int tile_units(const Request& q, int G, int tile) {
-    return max(1, (tile_sees(q, G, RT, tile) + UNIT - 1) / UNIT);
-}
-// The units of a request's tiles, one after the other (as tile_units, without a division for each).
+// The units of a request's tiles with their lead, one after the other (without a division for each).
 template <int RT, int UNIT>
 struct TileWalk {
     int base, len, last, qi, rest, G, step_qi, step_rest;   // qi, rest: the tile's last row is `rest` of token qi
@@ -165,7 +168,7 @@ struct TileWalk {
         step_qi = RT / G, step_rest = RT - step_qi * G;
     }
     __device__ __forceinline__ int next() {
-        const int u = max(1, (max(0, min(len, base + min(qi, last))) + UNIT - 1) / UNIT);
+        const int u = lead(UNIT) + max(1, (max(0, min(len, base + min(qi, last))) + UNIT - 1) / UNIT);
         qi += step_qi, rest += step_rest;
         if (rest >= G) rest -= G, ++qi;
         return u;
@@ -232,16 +235,16 @@ __device__ __forceinline__ void count_units(const PagedParams& p, int* s_cum) {
     __syncthreads();
 }
 
-// What a CTA does of one item: rows row0 .. of `rows` of the request, tokens lo .. hi; it has the item's units u0 .. u1.
+// What a CTA does of one item: rows row0 .. of `rows` of the request, tokens lo .. hi; it has the units u0 .. u1 of the item's `units`.
 struct Segment {
     Request rq;
     int h, row0, rows, lo, hi, u0, u1, units;
     __device__ __forceinline__ bool whole() const { return u0 == 0 && u1 == units; }
     __device__ __forceinline__ int64_t slot() const { return 2 * (int64_t)blockIdx.x + (u0 == 0); }
 };
-// The item at unit x, looked for.  Called by whole warps.
+// The item at unit x, looked for; returns its units before x.  Called by whole warps.
 template <int RT, int UNIT>
-__device__ __forceinline__ void find_item(const PagedParams& p, const int* s_cum, int x, Segment& s) {
+__device__ __forceinline__ int find_item(const PagedParams& p, const int* s_cum, int x, Segment& s) {
     const int shift = group_log2(p.t.B);
     int g = 0, top = groups_of(p.t.B);   // cum[g] <= x < cum[top]
     while (top - g > 1) {
@@ -270,49 +273,55 @@ __device__ __forceinline__ void find_item(const PagedParams& p, const int* s_cum
         head = __shfl_sync(0xffffffffu, per_head, at);
     }
     s.h = mine / head;
-    s.u0 = mine - s.h * head;
+    mine -= s.h * head;
     int tile = 0;
     TileWalk<RT, UNIT> w(s.rq, p.G);
     for (const int last = (s.rq.n * p.G - 1) / RT;; ++tile) {   // (it ends, whatever becomes of the lengths meanwhile)
         const int units = w.next();
-        if (s.u0 < units || tile >= last) break;
-        s.u0 -= units;
+        if (mine < units || tile >= last) break;
+        mine -= units;
     }
     s.row0 = tile * RT;
+    return mine;
 }
-// The item at unit x, where the one of `s` ended: the request's next tile or head (found step by step from its first, the tiles of
-// prompts cost more than their products), another request's, or, after segment_none(), the CTA's first.
+// The next item of which the CTA has tokens, from unit x on, where the one of `s` ended: the request's next tile or head (found step by
+// step from its first, the tiles of prompts cost more than their products), another request's, or, after segment_none(), the CTA's
+// first.  x moves behind what the CTA has of it; false: it has no more.
 template <int RT, int UNIT>
-__device__ __forceinline__ void next_segment(const PagedParams& p, const int* s_cum, int x, int end, Segment& s) {
-    s.row0 += RT, s.u0 = 0;
-    if (s.row0 >= s.rq.n * p.G) {
-        s.row0 = 0;
-        if (++s.h >= p.c.Hkv) find_item<RT, UNIT>(p, s_cum, x, s);
+__device__ __forceinline__ bool next_segment(const PagedParams& p, const int* s_cum, int& x, int end, Segment& s) {
+    while (x < end) {
+        s.row0 += RT;
+        int v0 = 0;   // units of the item, with its lead, that are other CTAs'
+        if (s.row0 >= s.rq.n * p.G) {
+            s.row0 = 0;
+            if (++s.h >= p.c.Hkv) v0 = find_item<RT, UNIT>(p, s_cum, x, s);
+        }
+        const int seen = tile_sees(s.rq, p.G, RT, s.row0 / RT);
+        s.units = max(1, (seen + UNIT - 1) / UNIT);
+        const int v1 = min(lead(UNIT) + s.units, v0 + end - x);
+        x += v1 - v0;
+        s.u0 = max(0, v0 - lead(UNIT)), s.u1 = v1 - lead(UNIT);
+        if (s.u1 <= s.u0) continue;
+        s.rows = min(s.rq.n * p.G - s.row0, RT);
+        s.lo = s.u0 * UNIT;
+        s.hi = min(s.u1 * UNIT, seen);
+        return true;
     }
-    const int rows = s.rq.n * p.G - s.row0, seen = tile_sees(s.rq, p.G, RT, s.row0 / RT);
-    s.units = max(1, (seen + UNIT - 1) / UNIT);
-    s.u1 = min(s.units, s.u0 + end - x);
-    s.rows = min(rows, RT);
-    s.lo = s.u0 * UNIT;
-    s.hi = min(s.u1 * UNIT, seen);
+    return false;
 }
 __device__ __forceinline__ Segment segment_none() {
     Segment s{};
     s.h = 1 << 30;
     return s;
 }
-// The CTA's cut, written by one thread when it has its first segment.
+// The CTA's cut, written by one thread; `s`: its first segment.
 __device__ __forceinline__ void describe_cut(const PagedParams& p, const Segment& s, int begin, int share) {
-    const int at = begin - s.u0;   // the item's first unit
+    const int at = begin - s.u0;   // the item's first tokens
     Cut c{};
     if (s.u0 > 0 && at >= begin - share)
         c.rows = s.rows, c.row0 = s.row0, c.h = s.h, c.first = s.rq.first, c.last = (at + s.units - 1) / share;
     p.cuts[blockIdx.x] = c;
 }
-
-constexpr int kUnit = 64;       // tokens of a unit: warp-level products
-constexpr int kTcUnit = 128;    // 5th-generation tensor cores
-constexpr int kTcRows = 256;
 
 // `tiles`: row tiles of 16 that a CTA takes at once (1 or 2)
 cudaError_t launch_paged(const PagedParams& p, int D, bool bf16, int tiles, cudaStream_t s);

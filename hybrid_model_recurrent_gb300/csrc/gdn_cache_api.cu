@@ -103,13 +103,14 @@ gdn_status plan_rows(const gdn_cache* c, const Batch& t, gdn_dtype dtype, int G,
     // once (in bf16, where both were possible: 16 x 4 heads at 24 rows 63 us against 65, 4 x 8 heads 87 against 94).
     pl.tiles = rows > 16 ? 2 : 1;
     pl.tile_rows = pl.tc ? kTcRows : 16 * pl.tiles;
-    const int64_t per_item = std::max<int64_t>(ceil_div(t.max_len, pl.tc ? kTcUnit : kUnit), 1);
+    const int unit = pl.tc ? kTcUnit : kUnit;
+    const int64_t per_item = std::max<int64_t>(ceil_div(t.max_len, unit), 1) + lead(unit);
     const int64_t items =
         std::min(t.B * ceil_div(rows, pl.tile_rows), ceil_div((int64_t)t.T * G, pl.tile_rows) + t.B) * c->num_kv_heads;
     if (items >= (1ll << 31) / per_item - (1 << 16)) return GDN_ERR_UNSUPPORTED;
     const int per_sm = pl.tc ? 1 : pl.tiles == 1 ? 3 : 2;
     pl.ctas = (int)std::max<int64_t>(1, std::min<int64_t>(items * per_item, (int64_t)kSms * per_sm));
-    pl.join = per_item > 1 && pl.ctas > 1;
+    pl.join = t.max_len > unit && pl.ctas > 1;
     pl.ml_off = (size_t)pl.ctas * sizeof(Cut);
     pl.o_off = pl.ml_off + (size_t)2 * pl.ctas * pl.tile_rows * 8;
     pl.total = pl.o_off + (size_t)2 * pl.ctas * pl.tile_rows * c->head_dim * 4;

@@ -119,15 +119,13 @@ __global__ void __launch_bounds__(kWarps * 32, MT == 1 ? 3 : 2) paged_kernel(con
     const int total = s_cum[groups_of(p.t.B)], share = (total + gridDim.x - 1) / gridDim.x;
     int x = (int)min((int64_t)blockIdx.x * share, (int64_t)total);
     const int begin = x, end = min(x + share, total);
-    if (begin >= end && tid == 0) p.cuts[blockIdx.x] = Cut{};
 
     Segment sg = segment_none();
-    while (x < end) {
-        next_segment<RT, kUnit>(p, s_cum, x, end, sg);
-        if (x == begin && tid == 0) describe_cut(p, sg, begin, share);
+    if (tid == 0) p.cuts[blockIdx.x] = Cut{};
+    for (bool first = true; next_segment<RT, kUnit>(p, s_cum, x, end, sg); first = false) {
+        if (first && tid == 0) describe_cut(p, sg, begin, share);
         const Request& rq = sg.rq;
         const int h = sg.h, row0 = sg.row0, rows = sg.rows, lo = sg.lo, hi = sg.hi;
-        x += sg.u1 - sg.u0;
         const int shift = rq.len - rq.n;              // query i sees the tokens below shift + i + 1
         const int all_see = shift + row0 / p.G + 1;   // tokens that every row sees end here
         const int32_t* table = c.table + (int64_t)max(rq.row, 0) * c.W;

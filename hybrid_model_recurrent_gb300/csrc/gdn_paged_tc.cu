@@ -221,7 +221,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_cons
     const int total = s_cum[groups_of(p.t.B)], share = (total + (int)gridDim.x - 1) / (int)gridDim.x;
     const int begin = (int)min((int64_t)blockIdx.x * share, (int64_t)total), end = min(begin + share, total);
 
-    if (begin >= end && tid == 0) p.cuts[blockIdx.x] = Cut{};
+    if (tid == 0) p.cuts[blockIdx.x] = Cut{};
 
     // Every role walks the CTA's items; an item of at most 128 rows takes one row tile, the two in turn, so that one tile's sums
     // leave and its next Q arrives while the other computes.
@@ -243,9 +243,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_cons
             bool ok = true;
             int it = 0, turn = 0, steps = 0, nth = 0;   // tiles of all items; steps and items of this row tile
             const uint64_t q = tile_desc(sbase + a * F::kTile, false);
-            for (int at = begin; ok && at < end;) {
-                next_segment<kTcRows, kTcUnit>(p, s_cum, at, end, x);
-                at += x.u1 - x.u0;
+            for (int at = begin; ok && next_segment<kTcRows, kTcUnit>(p, s_cum, at, end, x);) {
                 const int n = 2 * tiles_of(), on = takes(turn);
                 if (n == 0) continue;
                 if (!(on >> a & 1)) {   // the other row tile's alone: pass by, entry after entry, so that no barrier gets ahead
@@ -315,9 +313,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_cons
                 const int64_t kv_bytes = p.c.Hkv * block;
                 const int stop = p.stall_after >= 0 ? 4 * p.stall_after : 0x7fffffff;   // testing hook
                 int asked = 0;
-                for (int at = begin; ok && at < end;) {
-                    next_segment<kTcRows, kTcUnit>(p, s_cum, at, end, x);
-                    at += x.u1 - x.u0;
+                for (int at = begin; ok && next_segment<kTcRows, kTcUnit>(p, s_cum, at, end, x);) {
                     const int n = tiles_of();
                     if (n == 0) continue;
                     const int32_t* table = p.c.table + (int64_t)x.rq.row * p.c.W;   // (a row without tokens has no tiles)
@@ -364,9 +360,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_cons
                 const unsigned char* raw0 = smem + F::kRaw + (8 * g0 + sub) * D + quad * 16;
                 unsigned char* to0 = smem + F::kRing + (64 * half + 8 * g0 + sub) * 128;
                 const bool describes = warp == 12;   // (with two groups of 8 tokens, others have three)
-                for (int at = begin; ok && at < end;) {
-                    next_segment<kTcRows, kTcUnit>(p, s_cum, at, end, x);
-                    at += x.u1 - x.u0;
+                for (int at = begin; ok && next_segment<kTcRows, kTcUnit>(p, s_cum, at, end, x);) {
                     const int n = tiles_of();
                     if (n == 0) continue;
                     const int32_t* table = p.c.table + (int64_t)x.rq.row * p.c.W;
@@ -441,12 +435,11 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_cons
         // ---- softmax of row tile a; this thread's row ----
         const int a = warp >> 2, r = tid & 127;
         const uint32_t trow = tbase + ((uint32_t)(32 * (warp & 3)) << 16);
-        bool ok = true;
+        bool ok = true, first = true;
         int turn = 0, it = 0, g = 0;   // tiles of all items; steps of this row tile
-        for (int at = begin; ok && at < end;) {
-            next_segment<kTcRows, kTcUnit>(p, s_cum, at, end, x);
-            if (at == begin && tid == 0) describe_cut(p, x, begin, share);
-            at += x.u1 - x.u0;
+        for (int at = begin; ok && next_segment<kTcRows, kTcUnit>(p, s_cum, at, end, x);) {
+            if (first && tid == 0) describe_cut(p, x, begin, share);
+            first = false;
             const int on = takes(turn), n = tiles_of(), it0 = it;
             it += n;
             if (!(on >> a & 1)) continue;
