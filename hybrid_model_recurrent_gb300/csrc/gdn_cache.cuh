@@ -113,8 +113,9 @@ cudaError_t launch_compact(const UpkeepParams& p, cudaStream_t s);
 // The work is cut evenly over the CTAs: an item is a tile of RT query rows of one request and key/value head (rows in the
 // order of tokens and of the heads of the group), a unit is a number of tokens that an item's rows see, and CTA c takes the
 // units [c share, (c + 1) share) of them all, in the order of requests, heads, row tiles and tokens.  What an item costs besides its
-// tokens counts as LEAD units before them, which are nobody's work: else the CTAs that have a prompt's first tiles, of few tokens, are
-// late (a prompt of 8192 x 32 heads, bf16: 616 us without lead, 479 with 4 units).  So a CTA has at most one
+// tokens counts as kLead units before them, which are nobody's work: else the CTAs that have a prompt's first tiles, of few tokens, are
+// late (a prompt of 8192 x 32 heads, bf16: 616 us without lead, 494, 479, 489 with 3, 4, 6
+// units; in fp32 3700 and, with 2, 4, 6, 10, 3418, 3085, 2805, 2693; but 128 single tokens on 100 to 4800 122, 124, 128 with 4, 6, 10).  So a CTA has at most one
 // item that it begins in the middle (its part goes to slot 2 c) and one that it begins and leaves unfinished (slot 2 c + 1).
 // Every CTA describes the item that it begins in the middle, if the CTA before began it (a cut), and a join, whose grid follows the
 // CTAs and not the batch, adds the cut items' parts up.  Lengths are read on the device only, and differ at will.
@@ -152,7 +153,7 @@ __device__ __forceinline__ void join_may_start() { asm volatile("griddepcontrol.
 constexpr int kUnit = 64;       // tokens of a unit: warp-level products
 constexpr int kTcUnit = 128;    // 5th-generation tensor cores
 constexpr int kTcRows = 256;
-__host__ __device__ constexpr int lead(int unit) { return unit == kTcUnit ? 4 : 0; }
+constexpr int kLead = 4;
 
 // Tokens that a row tile's last row sees (its units are one at least: rows that see nothing are written too).
 __device__ __forceinline__ int tile_sees(const Request& q, int G, int RT, int tile) {
@@ -168,7 +169,7 @@ struct TileWalk {
         step_qi = RT / G, step_rest = RT - step_qi * G;
     }
     __device__ __forceinline__ int next() {
-        const int u = lead(UNIT) + max(1, (max(0, min(len, base + min(qi, last))) + UNIT - 1) / UNIT);
+        const int u = kLead + max(1, (max(0, min(len, base + min(qi, last))) + UNIT - 1) / UNIT);
         qi += step_qi, rest += step_rest;
         if (rest >= G) rest -= G, ++qi;
         return u;
@@ -298,9 +299,9 @@ __device__ __forceinline__ bool next_segment(const PagedParams& p, const int* s_
         }
         const int seen = tile_sees(s.rq, p.G, RT, s.row0 / RT);
         s.units = max(1, (seen + UNIT - 1) / UNIT);
-        const int v1 = min(lead(UNIT) + s.units, v0 + end - x);
+        const int v1 = min(kLead + s.units, v0 + end - x);
         x += v1 - v0;
-        s.u0 = max(0, v0 - lead(UNIT)), s.u1 = v1 - lead(UNIT);
+        s.u0 = max(0, v0 - kLead), s.u1 = v1 - kLead;
         if (s.u1 <= s.u0) continue;
         s.rows = min(s.rq.n * p.G - s.row0, RT);
         s.lo = s.u0 * UNIT;

@@ -104,7 +104,7 @@ gdn_status plan_rows(const gdn_cache* c, const Batch& t, gdn_dtype dtype, int G,
     pl.tiles = rows > 16 ? 2 : 1;
     pl.tile_rows = pl.tc ? kTcRows : 16 * pl.tiles;
     const int unit = pl.tc ? kTcUnit : kUnit;
-    const int64_t per_item = std::max<int64_t>(ceil_div(t.max_len, unit), 1) + lead(unit);
+    const int64_t per_item = std::max<int64_t>(ceil_div(t.max_len, unit), 1) + kLead;
     const int64_t items =
         std::min(t.B * ceil_div(rows, pl.tile_rows), ceil_div((int64_t)t.T * G, pl.tile_rows) + t.B) * c->num_kv_heads;
     if (items >= (1ll << 31) / per_item - (1 << 16)) return GDN_ERR_UNSUPPORTED;
