@@ -497,16 +497,18 @@ __global__ void __launch_bounds__(128) paged_join_kernel(const __grid_constant__
     if (d == 0 && p.lse) p.lse[at] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
 }
 
-// The same for tiles of many rows and few parts: a CTA takes 32 rows, a warp each of them in turn.
+// The same for tiles of many rows and few parts: a CTA takes 8 rows, a warp two of them (with 32, 16, 8 rows a CTA a prompt of 8192 took 478,
+// 468, 466 us, 16 requests with one of 300 tokens 56, 46, 40).
+constexpr int kJoinRows = 8;
 template <int D, typename T, int RT>
 __global__ void __launch_bounds__(128) paged_join_rows_kernel(const __grid_constant__ PagedParams p) {
     constexpr int N = D / 32;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, c0 = blockIdx.y;
     kernel_before_done();
     const Cut cut = p.cuts[c0 + 1];
-    const int c1 = cut.last, end = min((int)blockIdx.x * 32 + 32, cut.rows);
+    const int c1 = cut.last, end = min((int)(blockIdx.x + 1) * kJoinRows, cut.rows);
 #pragma unroll 2
-    for (int r = blockIdx.x * 32 + warp; r < end; r += 4) {
+    for (int r = blockIdx.x * kJoinRows + warp; r < end; r += 4) {
         const int R = cut.row0 + r;
         float m = -INFINITY;
         for (int c = c0; c <= c1; ++c) m = fmaxf(m, p.part_ml[(2 * (int64_t)c + (c == c0)) * RT + r].x);
@@ -540,15 +542,15 @@ cudaError_t launch(const PagedParams& p, cudaStream_t s) {
 template <int D, typename T>
 cudaError_t join(const PagedParams& p, int tile_rows, cudaStream_t s) {
     const int64_t all = std::min<int64_t>((int64_t)p.t.max_new * p.G, p.max_rows), rows = std::min<int64_t>(all, tile_rows);
-    // Large tiles: a CTA a row costs 2 us for about 2432 rows (16 CTAs a multiprocessor), cut or not; a warp for 8 rows in turn takes
+    // Large tiles: a CTA a row costs 2 us for about 2432 rows (16 CTAs a multiprocessor), cut or not; a warp for 2 rows takes
     // 1.5 us a row and 0.3 us a part.  (1 x 40 rows x 2 heads on 100 k tokens, 76 parts: 207 us by warps, 44 by rows.)
     const int64_t items = (all + tile_rows - 1) / tile_rows * p.t.B * p.c.Hkv, parts = p.ctas / items + 1;
-    const bool by_row = tile_rows <= 32 || rows * p.ctas < 14600 + 2900 * parts;
+    const bool by_row = tile_rows <= 32 || rows * p.ctas < 3650 + 730 * parts;
     cudaLaunchConfig_t cfg{};
     cudaLaunchAttribute attr{};
     attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr.val.programmaticStreamSerializationAllowed = 1;
-    cfg.gridDim = dim3((unsigned)(by_row ? rows : (rows + 31) / 32), p.ctas - 1), cfg.blockDim = dim3(128), cfg.stream = s;
+    cfg.gridDim = dim3((unsigned)(by_row ? rows : (rows + kJoinRows - 1) / kJoinRows), p.ctas - 1), cfg.blockDim = dim3(128), cfg.stream = s;
     cfg.attrs = &attr, cfg.numAttrs = 1;
     if (tile_rows == 16) return cudaLaunchKernelEx(&cfg, paged_join_kernel<D, T, 16>, p);
     if constexpr (sizeof(T) == 4 || D == 32) {
