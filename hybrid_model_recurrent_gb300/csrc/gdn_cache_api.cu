@@ -96,8 +96,8 @@ gdn_status plan_rows(const gdn_cache* c, const Batch& t, gdn_dtype dtype, int G,
     const int64_t rows = std::min(t.max_new * (int64_t)G, max_rows);
     pl.min_rows = (int)min_rows, pl.max_rows = (int)max_rows;
     // The tensor cores of the 5th generation take 256 rows a tile, filled or not, warp-level products 16 or 32.  Measured, us, warp-level /
-    // tensor cores: 16 requests x 4 heads on 8192 tokens 46 / 56 at 16 rows a head, 63 / 57 at 24, 93 / 59 at 40, 169 / 71 at 128; 4 x 8
-    // heads on 30000 64 / 90, 87 / 90, - , 264 / 99; 1 x 2 heads on 100000 44 / 43, 48 / 44, 64 / 44, 84 / 48.
+    // tensor cores: 16 requests x 4 heads on 8192 tokens 42 / 57 at 16 rows a head, 63 / 58 at 24, 93 / 60 at 40, 169 / 66 at 128; 4 x 8
+    // heads on 30000 59 / 90, 87 / 90, - , 264 / 102; 1 x 2 heads on 100000 40 / 41, 48 / 41, 64 / 43, 84 / 44.
     pl.tc = dtype == GDN_BF16 && c->head_dim >= 64 && rows > 16;
     // Warp-level products: rows beyond 16 take tiles of 32, which halve the reads; the second tile of 16 costs a third of the warps at
     // once (in bf16, where both were possible: 16 x 4 heads at 24 rows 63 us against 65, 4 x 8 heads 87 against 94).
@@ -118,9 +118,10 @@ gdn_status plan_rows(const gdn_cache* c, const Batch& t, gdn_dtype dtype, int G,
 }
 
 // One plan, or two: where the average request has at most a quarter of the longest one's new tokens (a prompt among single tokens),
-// those with 16 rows at most go ahead by themselves, for tiles of 256 rows cost them three times as much; the other two launches cost 14 to
-// 19 us, as 4096 units or so.  Measured, us, one plan / two: 255 single tokens on 2000 x 4 heads of 64 and a prompt of 2000 360 / 191; 63 on
-// 4096 x 8 heads of 128 and one of 8192 865 / 728; 15 on 2000 x 4 heads of 128 (1024 units) and 300 54 / 72.
+// those with 16 rows at most go ahead by themselves, for tiles of 256 rows cost them two to four times as much; the other two launches
+// cost 8 to 20 us, as 4096 units of 128 tokens do.  Measured, us, one plan / two: 255 single tokens on 2000 x 4 heads of 64 and a prompt of
+// 2000 278 / 159; 63 on 4096 x 8 heads of 128 and one of 8192 677 / 572; on 4000 x 4 heads of 128 with one of 300 new tokens 134 / 95 for 64
+// requests (8192 units), 81 / 73 for 32, 54 / 62 for 16.
 gdn_status plan_paged(const gdn_cache* c, const Batch& t, gdn_dtype dtype, int Hq, PagedPlan (&pl)[2], int& plans, size_t& bytes) {
     const int G = Hq / c->num_kv_heads;
     const int64_t rows = t.max_new * (int64_t)G, most = (1ll << 31) - 1024;

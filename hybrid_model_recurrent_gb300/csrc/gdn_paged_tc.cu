@@ -27,9 +27,10 @@
 // 17 k tokens: scores of whole tiles, one after the softmax of the other, 662 us; two halves issued by one warp for both row
 // tiles 826, its barriers and elections in turn.  Rows of 128 scores held by 384 threads, three warps converting, 887: a lone warp's
 // instructions came at 7 to 9 cycles each, waiting for the instruction cache.)
-// What bounds it: that case takes 601 us, 1060 TFLOP/s of the products asked for, 0.55 of a library product's rate, 3.7 k cycles a tile
-// of 128 tokens of which the products take 2.1 k; a step of the softmax takes 1.5 k whatever is left out of its arithmetic
-// (without exponentials 578 us, without the maximum 569): its waits, the scores' way from TMEM and the weights' back.
+// What bounds it: that case takes 588 us, 1090 TFLOP/s of the products asked for, 0.57 of a library product's rate, 3.4 k cycles a tile
+// of 128 tokens of which the products take 2.1 k, and 7 us an item besides; a step of the softmax takes 1.5 k whatever is left out of
+// its arithmetic (at 601 us: without exponentials 578, without the maximum 569): its waits, the scores' way from TMEM and the weights'
+// back.  With one row tile the conversion takes as long: neither more converting warps nor both row tiles on every other tile gain.
 //
 // Every wait is bounded: a role that gives up sets the CTA's abort flag and the sticky status, every role leaves its
 // loop, copies and products in flight are waited for, and TMEM is freed.
