@@ -89,7 +89,7 @@ struct Cfg {
     static constexpr int kRaw = kRing + ST * kTile;
     static constexpr int kBar = kRaw + RS * kHalf;
     static constexpr int kInfos = ST == 4 ? 4 : 8;            // tiles described: when one is, V of ST / 2 + 1 tiles before is done
-    static constexpr int kArea = ST == 4 ? 2048 : 3072;       // barriers, units before each group of requests, the descriptions
+    static constexpr int kArea = ST == 4 ? 2048 : 2816;       // barriers, units before each group of requests, the descriptions
     static constexpr int kSmem = kBar + kArea + 1024;
     static constexpr uint32_t kO = 256;                       // TMEM: S of each row tile, then O of each
 };
