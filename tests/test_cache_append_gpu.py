@@ -1,5 +1,7 @@
 """Appending to a paged 8-bit cache on the GPU, bit for bit against the definition in 64 bits (every step of it is exact but
 the rounding to e4m3, so there is nothing to tolerate)."""
+import ctypes
+
 import pytest
 import torch
 
@@ -164,6 +166,28 @@ def test_bad_pages_and_counts_are_reported():
     gdn.gdn_cache_append(x, x, c, ints(0, 1, 8), ws=ws, max_new=3)
     assert gdn.read_status(ws=ws) == gdn.GDN_ERR_INVALID_ARG
     assert torch.equal(c.pages.view(torch.uint8), before)
+
+
+def test_rows_longer_than_the_table_and_bounds_for_attention():
+    """A row past what the table holds is reported and nothing of it written; max_len, attention's bound, moves no tokens."""
+    c = make_cache([40, 50], page=16, H=2, D=32, W=4, poison=False)
+    before = c.pages.view(torch.uint8).clone()
+    ws = torch.zeros(256, dtype=torch.uint8, device="cuda")
+    x = torch.ones(2, 2, 32, device="cuda")
+    c.lens[1] = 65
+    gdn.gdn_cache_append(x[:1], x[:1], c, ints(0, 0, 1), ws=ws)
+    assert gdn.read_status(ws=ws) == gdn.GDN_ERR_INVALID_ARG
+    assert torch.equal(c.pages.view(torch.uint8), before)
+    gdn.clear_status(ws=ws)
+    c.lens[1] = 50
+    cu = ints(0, 1, 2)
+    b = gdn._batch(c, 2, cu, None, 1, 5)
+    gdn._call("gdn_cache_append", c.device, ctypes.byref(c._c), 0, ctypes.byref(b), x.data_ptr(), x.data_ptr(), gdn._dtype_code(x.dtype),
+              0, 0, ws.data_ptr(), ws.numel(), torch.cuda.current_stream().cuda_stream)
+    assert gdn.read_status(ws=ws) == gdn.GDN_OK
+    other = make_cache([40, 50], page=16, H=2, D=32, W=4, poison=False)
+    gdn.gdn_cache_append(x, x, other, cu)
+    assert torch.equal(c.pages.view(torch.uint8), other.pages.view(torch.uint8)) and torch.equal(c.scales, other.scales)
 
 
 def test_captured_and_on_another_stream():
