@@ -280,7 +280,7 @@ __global__ void __launch_bounds__(kWarps * 32, MT == 1 ? 3 : 2) paged_kernel(con
 #pragma unroll
                         for (int j = 0; j < 2; ++j)
 #pragma unroll
-                            for (int i = 0; i < 2; ++i) s[mt][j][2 * half + i] *= f;
+                            for (int i = 0; i < 2; ++i) s[mt][j][2 * half + i] = __fmul_rn(s[mt][j][2 * half + i], f);   // (as m is)
                     }
                 if (t + 16 > all_see) {
 #pragma unroll
@@ -297,7 +297,7 @@ __global__ void __launch_bounds__(kWarps * 32, MT == 1 ? 3 : 2) paged_kernel(con
                     for (int half = 0; half < 2; ++half) {
                         const float t4 = fmaxf(fmaxf(s[mt][0][2 * half], s[mt][0][2 * half + 1]),
                                                fmaxf(s[mt][1][2 * half], s[mt][1][2 * half + 1]));
-                        rise |= t4 > m[mt][half] + kRise;   // (m = -infinity: any score)
+                        rise |= t4 - m[mt][half] > kRise;   // (m = -infinity: any score; m + kRise may round up)
                     }
                 if (__any_sync(0xffffffffu, rise)) {
 #pragma unroll

@@ -71,10 +71,11 @@ constexpr int kKeys = kTcUnit;
 constexpr float kRise = 8.f;  // O is rescaled when a maximum has risen by more than this (log2)
 constexpr float kLift = 7.f;  // log2 of a weight at the maximum: with the rise 2^15 in f16
 constexpr int kConv0 = 3, kConv1 = 2;   // converting warps for the first half of a tile, and for the second
-// A weight's exponent is score * scale - m in one rounding, but m is a product already rounded: for the largest score its
-// rounding error is left, half a step of m, 16 at 2^28 and past what an exponential holds from 2^31 on.  Rows further from zero
-// than this round the product by itself first.
-constexpr float kFar = 268435456.f;
+// A weight's exponent is score * scale + (kLift - m), and two roundings can carry it past the 15 that a maximum which has not risen
+// leaves it: that of the score as the rise was judged by it, and that of the bracket.  Up to 2^22 each is a quarter at most, and 2^15.5 is
+// in f16's range (with 2^28 here exponents reached 24, and the weights infinity).  Rows further from zero round the product by itself
+// first, as the maximum was, and take that off it, exactly where their difference counts.
+constexpr float kFar = 4194304.f;
 // Factors of scores are not below the smallest normal number: a hidden token's -infinity stays that.
 constexpr float kTiny = 1.17549435e-38f;
 constexpr int kThreads = 512;
@@ -524,13 +525,13 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_cons
                             for (int i = 2; i < 8; i += 2) t0 = fmaxf(fmaxf(t0, s[i]), s[i + 1]), t1 = fmaxf(fmaxf(t1, s[8 + i]), s[9 + i]);
                             top = fmaxf(top, fmaxf(t0, t1) * fmaxf(row_scale * parts[k].x, kTiny));
                         }
-                        const bool rise = valid && (top > m + kRise || m == -INFINITY), grow = ti.v > item_v;
+                        const bool rise = valid && (top - m > kRise || m == -INFINITY), grow = ti.v > item_v;   // (m + kRise may round up)
                         if (__any_sync(0xffffffffu, rise || grow)) {
-                            // by a power of two: exact for l and O
+                            // by a power of two: exact for l and O; far from zero by what m rises, there as exact
                             const float up = ceilf(top - m);   // (infinite for a first maximum)
-                            const bool far = !(up <= 100.f);
-                            const float f = !rise ? 1.f : far ? 0.f : ex2(-up);
-                            if (rise) m = far ? top : m + up;
+                            const bool anew = !(up <= 100.f), far = fabsf(top) > kFar;
+                            const float f = !rise ? 1.f : anew ? 0.f : ex2(far ? m - top : -up);
+                            if (rise) m = anew || far ? top : m + up;
                             la = make_float2(la.x * f, la.y * f), lb = make_float2(lb.x * f, lb.y * f);
                             float fo = f;
                             if (grow) fo *= item_v / ti.v, item_v = ti.v;
