@@ -154,6 +154,7 @@ constexpr int kUnit = 64;       // tokens of a unit: warp-level products
 constexpr int kTcUnit = 128;    // 5th-generation tensor cores
 constexpr int kTcRows = 256;
 constexpr int kLead = 4;
+constexpr int kMostUnits = 0x7fffffff - (1 << 20) + 1;   // of all items
 
 // Tokens that a row tile's last row sees (its units are one at least: rows that see nothing are written too).
 __device__ __forceinline__ int tile_sees(const Request& q, int G, int RT, int tile) {
@@ -187,7 +188,8 @@ __device__ __forceinline__ int head_units(const Request& q, int G) {
 
 // Units before every group of requests into s_cum, by all THREADS threads of a CTA, a thread a request; a group is the least power of two
 // with which kMaxGroups of them hold the batch (one request up to 256).  The host's plan keeps the total
-// below 2^31 for counts as the call describes them; sums stop there, and others (cu_new that falls) are reported and nothing is done.
+// to kMostUnits for counts as the call describes them (CTAs round their shares up: sums stay in 31 bits); the sums here stop at kNoTotal, and
+// a larger total (cu_new that falls) is reported and nothing is done.
 constexpr unsigned kNoTotal = 0x7fffffffu;
 constexpr int kMaxGroups = 256;
 __device__ __forceinline__ int group_log2(int B) {
@@ -226,7 +228,7 @@ __device__ __forceinline__ void count_units(const PagedParams& p, int* s_cum) {
             const unsigned z = __shfl_up_sync(0xffffffffu, y, o);
             if (lane >= o) y = min(y + z, kNoTotal);
         }
-        const bool none = __shfl_sync(0xffffffffu, y, 31) == kNoTotal;
+        const bool none = __shfl_sync(0xffffffffu, y, 31) > (unsigned)kMostUnits;
         if (none && lane == 0 && blockIdx.x == 0) atomicOr(p.status, STATUS_BAD_INDEX);
         y -= sum;
         for (int i = 0; i < PER; ++i)
@@ -299,7 +301,7 @@ __device__ __forceinline__ bool next_segment(const PagedParams& p, const int* s_
         }
         const int seen = tile_sees(s.rq, p.G, RT, s.row0 / RT);
         s.units = max(1, (seen + UNIT - 1) / UNIT);
-        const int v1 = min(kLead + s.units, v0 + end - x);
+        const int v1 = min(kLead + s.units, v0 + (end - x));
         x += v1 - v0;
         s.u0 = max(0, v0 - kLead), s.u1 = v1 - kLead;
         if (s.u1 <= s.u0) continue;

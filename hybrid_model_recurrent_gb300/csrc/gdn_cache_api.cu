@@ -107,7 +107,7 @@ gdn_status plan_rows(const gdn_cache* c, const Batch& t, gdn_dtype dtype, int G,
     const int64_t per_item = std::max<int64_t>(ceil_div(t.max_len, unit), 1) + kLead;
     const int64_t items =
         std::min(t.B * ceil_div(rows, pl.tile_rows), ceil_div((int64_t)t.T * G, pl.tile_rows) + t.B) * c->num_kv_heads;
-    if (items >= (1ll << 31) / per_item - (1 << 16)) return GDN_ERR_UNSUPPORTED;
+    if (items > kMostUnits / per_item) return GDN_ERR_UNSUPPORTED;
     const int per_sm = pl.tc ? 1 : pl.tiles == 1 ? 3 : 2;
     pl.ctas = (int)std::max<int64_t>(1, std::min<int64_t>(items * per_item, (int64_t)kSms * per_sm));
     pl.join = t.max_len > unit && pl.ctas > 1;

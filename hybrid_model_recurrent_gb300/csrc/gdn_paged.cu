@@ -121,7 +121,7 @@ __global__ void __launch_bounds__(kWarps * 32, MT == 1 ? 3 : 2) paged_kernel(con
     count_units<kWarps * 32, RT, kUnit>(p, s_cum);
     const int total = s_cum[groups_of(p.t.B)], share = (total + gridDim.x - 1) / gridDim.x;
     int x = (int)min((int64_t)blockIdx.x * share, (int64_t)total);
-    const int begin = x, end = min(x + share, total);
+    const int begin = x, end = (int)min((int64_t)x + share, (int64_t)total);
 
     Segment sg = segment_none();
     if (tid == 0) p.cuts[blockIdx.x] = Cut{};

@@ -221,7 +221,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_cons
     auto warp_wait = [&](uint64_t* bar, int parity) { return warp_wait_bar(bar, (uint32_t)parity & 1u, abort_flag, limit); };
 
     const int total = s_cum[groups_of(p.t.B)], share = (total + (int)gridDim.x - 1) / (int)gridDim.x;
-    const int begin = (int)min((int64_t)blockIdx.x * share, (int64_t)total), end = min(begin + share, total);
+    const int begin = (int)min((int64_t)blockIdx.x * share, (int64_t)total), end = (int)min((int64_t)begin + share, (int64_t)total);
 
     if (tid == 0) p.cuts[blockIdx.x] = Cut{};
 

@@ -104,7 +104,10 @@ typedef struct gdn_cache {
  *               row marks padding: nothing is appended, its queries get zeros and lse -infinity.
  *  max_new      host bound of a request's new tokens
  *  max_len      host bound of a row's tokens for attention, 0: W * page_size.  A close one makes
- *               the better plan.
+ *               the better plan.  Attention counts its work in units of 64 tokens, or 128 where a head
+ *               has more than 16 query rows in bf16 (head_dim 64 or 128): for each tile of 16 or 32 rows, or 256,
+ *               of each request and key/value head, those of max_len and 4 more.  Calls whose
+ *               bounds allow more than 2^31 - 2^20 of them are GDN_ERR_UNSUPPORTED.
  *
  * A request with more new tokens or a longer row than these bounds is refused on the device:
  * GDN_ERR_INVALID_ARG in the status word, its results undefined (nothing is appended).
