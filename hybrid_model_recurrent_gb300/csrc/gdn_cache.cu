@@ -229,8 +229,9 @@ __global__ void __launch_bounds__(256) append_kernel(const __grid_constant__ App
     if (rq.bad && blockIdx.x == 0 && threadIdx.x == 0) atomicOr(p.status, STATUS_BAD_INDEX);
     if (rq.row < 0 || rq.n == 0 || rq.bad) return;
     const int start = max(rq.len - rq.n, 0), skip = max(rq.n - rq.len, 0);   // (new tokens before a row's first position)
-    const int i = (start >> c.page_log2) + i0, base = i << c.page_log2;
-    if (base >= rq.len) return;
+    const int i = (start >> c.page_log2) + i0;
+    if (i > (rq.len - 1) >> c.page_log2) return;   // (in pages: behind the longest rows the tokens' numbers leave 32 bits)
+    const int base = i << c.page_log2;
     const int pg = c.table[(int64_t)rq.row * c.W + i];
     if (pg < 0 || pg >= c.N) {
         if (threadIdx.x == 0) atomicOr(p.status, STATUS_BAD_INDEX);
