@@ -9,7 +9,7 @@
 //
 // Per 16 tokens of a warp:  S = Q K^T (rows x 16),  x = S * scale of the keys' block,  p = 2^(x - m),  O += P V.
 // Queries are brought to [2^14, 2^15) by a power of two for each row and held as one f16 (bf16 queries: exact) or the sum of two
-// (fp32: 22 bits); the weights likewise, times 2^11 and the block's scale over the largest scale met (a power of two).
+// (fp32: 22 bits); the weights likewise, times 2^11 and, in bf16, the block's scale over the largest met (a power of two).
 // m is raised only when a score is more than 2^4 above it, so the weights stay below 2^15.  Statistics and sums are fp32.
 //
 // The units of all items are dealt out evenly (gdn_cache.cuh), so lengths may differ at will; a CTA's four warps take
@@ -50,19 +50,14 @@ __device__ __forceinline__ void mma(float (&d)[4], const uint4& a, uint32_t b0, 
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w), "r"(b0), "r"(b1));
 }
-// d += the products of both parts of a, for fp32: the tensor cores cut their sums, every time by up to a step of fp32, so the running sum is
-// kept outside them (with it inside, the outputs were off by 4.7e-6 where fp32 sums of the plain form were by 1.8e-6)
-template <int PARTS>
-__device__ __forceinline__ void mma_parts(float (&d)[4], const uint4* a, int stride, uint32_t b0, uint32_t b1) {
-    if constexpr (PARTS == 1) {
-        mma(d, a[0], b0, b1);
-    } else {
-        float t[4] = {0.f, 0.f, 0.f, 0.f};
-        mma(t, a[stride], b0, b1);
-        mma(t, a[0], b0, b1);
+// d += f times the products of both parts of a, for fp32: the tensor cores cut their sums, every time by up to a step of fp32, so the running
+// sum is kept outside them (with it inside, the outputs were off by 4.7e-6 where fp32 sums of the plain form were by 1.8e-6)
+__device__ __forceinline__ void mma_two(float (&d)[4], const uint4& a, const uint4& rest, uint32_t b0, uint32_t b1, float f) {
+    float t[4] = {0.f, 0.f, 0.f, 0.f};
+    mma(t, rest, b0, b1);
+    mma(t, a, b0, b1);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) d[i] += t[i];
-    }
+    for (int i = 0; i < 4; ++i) d[i] = fmaf(t[i], f, d[i]);
 }
 __device__ __forceinline__ uint32_t half2(float a, float b) {
     const __half2 h = __floats2half2_rn(a, b);
@@ -233,7 +228,7 @@ __global__ void __launch_bounds__(kWarps * 32, MT == 1 ? 3 : 2) paged_kernel(con
         __syncthreads();
 
         // ---- the tokens ----
-        float m[MT][2], l[MT][2], o[MT][NT][4], vref = 0.f;
+        float m[MT][2], l[MT][2], o[MT][NT][4], vref = 0.f, vinv = 0.f;
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt) {
             m[mt][0] = m[mt][1] = -INFINITY, l[mt][0] = l[mt][1] = 0.f;
@@ -267,8 +262,13 @@ __global__ void __launch_bounds__(kWarps * 32, MT == 1 ? 3 : 2) paged_kernel(con
                         uint4 a[PARTS];
 #pragma unroll
                         for (int part = 0; part < PARTS; ++part) a[part] = s_q[(part * MT + mt) * KW * 32 + w * 32 + lane];
-                        mma_parts<PARTS>(s[mt][0], a, 1, b0, b1);
-                        mma_parts<PARTS>(s[mt][1], a, 1, b2, b3);
+                        if constexpr (PARTS == 1) {
+                            mma(s[mt][0], a[0], b0, b1);
+                            mma(s[mt][1], a[0], b2, b3);
+                        } else {
+                            mma_two(s[mt][0], a[0], a[1], b0, b1, 1.f);
+                            mma_two(s[mt][1], a[0], a[1], b2, b3, 1.f);
+                        }
                     }
                 }
                 bool rise = false;
@@ -319,6 +319,7 @@ __global__ void __launch_bounds__(kWarps * 32, MT == 1 ? 3 : 2) paged_kernel(con
                 if (e.vs[u] > vref) {   // (the same for the whole warp)
                     const float f = vref / e.vs[u];
                     vref = e.vs[u];
+                    if constexpr (PARTS == 2) vinv = 1.f / vref;
 #pragma unroll
                     for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
@@ -326,7 +327,11 @@ __global__ void __launch_bounds__(kWarps * 32, MT == 1 ? 3 : 2) paged_kernel(con
 #pragma unroll
                             for (int i = 0; i < 4; ++i) o[mt][n][i] *= f;
                 }
-                const float lift = vref > 0.f ? e.vs[u] / vref * kLift : 0.f;
+                // The block's scale over the largest met: in bf16 the weights carry it, in fp32 the products' sums, so that every block's
+                // weights keep their 22 bits (with it, those of a block 2^-20 of the largest kept 15).
+                float lift = kLift, ratio = 1.f;
+                if constexpr (PARTS == 1) lift = vref > 0.f ? e.vs[u] / vref * kLift : 0.f;
+                else ratio = e.vs[u] * vinv;
                 uint4 a[PARTS][MT];
 #pragma unroll
                 for (int mt = 0; mt < MT; ++mt) {
@@ -363,7 +368,8 @@ __global__ void __launch_bounds__(kWarps * 32, MT == 1 ? 3 : 2) paged_kernel(con
                     for (int n = 0; n < 4; ++n)
 #pragma unroll
                         for (int mt = 0; mt < MT; ++mt)
-                            mma_parts<PARTS>(o[mt][4 * w + n], &a[0][mt], MT, b0[n], b1[n]);
+                            if constexpr (PARTS == 1) mma(o[mt][4 * w + n], a[0][mt], b0[n], b1[n]);
+                            else mma_two(o[mt][4 * w + n], a[0][mt], a[1][mt], b0[n], b1[n], ratio);
                 }
             }
         }

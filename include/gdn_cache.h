@@ -141,9 +141,10 @@ gdn_status gdn_cache_append(const gdn_cache* c, int32_t layer, const gdn_batch* 
  *
  * A query that sees nothing gives o = 0 and lse = -infinity.  One token a request is a decode
  * step.  Scores, statistics and sums are fp32; bf16 queries meet the cache's values exactly, fp32
- * ones to 2^-22; the weights are rounded to half a step of 11 bits (bf16) or 22 bits (fp32), while
- * the scale of their block of values is at least 2^-21 of the largest that the row sees (smaller
- * blocks lose a bit of their weights for each power of two).
+ * ones to 2^-22 of a row's largest.  The weights are rounded to half a step of 11 bits (bf16) or 22 bits (fp32), or to
+ * 2^-32 (bf16) or 2^-36 (fp32) of the row's largest where that is more; in bf16 a block of values whose
+ * scale is r times the largest that the row sees has 2^-32 / r in its place (11 bits of its weights down to
+ * r = 2^-21, a bit less for each power of two below), in fp32 it keeps them all down to r = 2^-100.
  * All values are expected to be finite; a NaN spreads to every query of its own request.  What a
  * page holds behind a row's tokens is never taken into a result.
  *
