@@ -51,9 +51,10 @@ struct Vec<float> {
 // 16-byte pieces of its head that make whole pairs (the pieces i and i + rotary_dim / 2 apart, or two neighbours), so the
 // rotation needs no exchange, and it has the same N pairs in every head: their sines are formed once a token.
 //
-// An angle is position * frequency.  The frequency is held as a 64-bit fraction of a turn, so the product's low 64 bits
-// are the angle without whole turns, to 2^-33 of a turn at any position; the nearest quarter turn is then
-// taken off as an integer, and what is left (an eighth of a turn at most) goes to fp32.
+// An angle is position * frequency.  The frequency is held as a 64-bit fraction of a turn, formed from inv_freq in two parts of
+// 53 bits (fp64, once a CTA), so the product's low 64 bits are the angle without whole turns, to 2^-33 of a turn at any position
+// (one product of fp64 left 2^-25 at the farthest); the nearest quarter turn is then taken off as an integer, and what
+// is left (an eighth of a turn at most) goes to fp32.
 //
 // Bound by memory: each element is read and written once.  The next heads' loads are issued before the ones at hand are
 // computed, and the arithmetic is on pairs of fp32 (without both 272 us): 65536 tokens x 40 heads of 128 in bf16 take 224 us, 6.0 TB/s, 88 %
@@ -68,8 +69,11 @@ __global__ void __launch_bounds__(128) rope_kernel(const __grid_constant__ RopeP
     const bool turned = 2 * N * j < p.rd;
     const int ea = (HALF && turned ? j : 2 * j) * N, eb = HALF && turned ? ea + p.rd / 2 : ea + N;   // the lane's two pieces
     for (int i = threadIdx.x; i < p.rd / 2; i += 128) {
-        const double turns = p.inv_freq[i] * 0.15915494309189535;
-        s_freq[i] = __double2ull_rn((turns - floor(turns)) * 18446744073709551616.0);
+        // in 2^-64 of a turn: the product with 1 / 2 pi, and what it leaves, for 1 / 2 pi in two parts; whole turns are taken off exactly
+        constexpr double kTurn = 18446744073709551616.0;
+        const double f = p.inv_freq[i], x = f * (0.15915494309189535 * kTurn);
+        const double rest = fma(f, -9.839338337591243e-18 * kTurn, fma(f, 0.15915494309189535 * kTurn, -x));
+        s_freq[i] = (uint64_t)__double2ll_rn(fma(rint(x * (1.0 / kTurn)), -kTurn, x)) + (uint64_t)__double2ll_rn(rest);
     }
     __syncthreads();
     const int64_t units = p.T * p.parts, warps = (int64_t)gridDim.x * 4;

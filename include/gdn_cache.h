@@ -29,8 +29,9 @@ extern "C" {
  *
  * for the pairs i < rotary_dim / 2: a = i, b = i + rotary_dim / 2 (GDN_ROPE_HALF) or a = 2 i,
  * b = 2 i + 1 (GDN_ROPE_INTERLEAVED); elements from rotary_dim on are not rotated (nor scaled by
- * mscale).  Everything in fp32, rounded once.  The angle is reduced as a 64-bit fraction of a
- * turn, so far positions lose nothing.
+ * mscale).  Everything in fp32, rounded once.  The angle is the product of the position and inv_freq
+ * as given, held as a 64-bit fraction of a turn: off by 2^-64 of a turn times the position, 2^-33 at
+ * the farthest, whatever the frequency (up to 2^40 radians a token).
  *
  *  q, k           device [T, num_q_heads, D], [T, num_k_heads, D], dtype; k may be NULL
  *                 (num_k_heads 0)
