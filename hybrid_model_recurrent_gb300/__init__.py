@@ -926,7 +926,10 @@ def gdn_rope_frequencies(rotary_dim: int, *, base: float = 10000.0, scaling: str
     scaling for contexts `factor` times as long as the `original_len` a model was trained on: "linear" (every position
     divided by factor), "base" (the base raised so that the slowest pair is stretched by factor), or "parts" (pairs that
     turn at least fast_turns times within original_len are left, those below slow_turns stretched, those between in
-    part, linearly in their turns)."""
+    part, linearly in their turns).
+
+    Some models ramp over a pair's number in place of its turns, which gives the pairs between other frequencies (up to
+    42 % apart for 64 pairs and a factor of 4): hand their own as inv_freq."""
     _expect(rotary_dim >= 0 and rotary_dim % 16 == 0, "rotary_dim must be a multiple of 16")
     if not (base > 0 and factor >= 1 and original_len > 0 and fast_turns > slow_turns >= 0):
         raise ValueError("base and original_len must be positive, factor at least 1, fast_turns above slow_turns")
@@ -1077,7 +1080,8 @@ def gdn_cache_append(k, v, cache: PagedCache, cu_new, *, layer: int = 0, rows=No
     """Append new keys and values to rows of the cache (see the header).
 
     k, v [T, Hkv, D], rows at any stride; cu_new int32 [B + 1] on the GPU: request b's tokens, the last ones of row
-    rows[b] (default b), whose lens counts them already.  max_new bounds a request's new tokens (default: T)."""
+    rows[b] (default b), whose lens counts them already.  max_new bounds a request's new tokens (default: T; give it for a
+    batch of few tokens each, or the call looks for T of every request)."""
     dev = cache.device
     raw = _raw_stream(stream, dev)
     c = cache._c
@@ -1100,7 +1104,8 @@ def gdn_paged_attention(q, cache: PagedCache, cu_new, *, layer: int = 0, rows=No
     the header).
 
     q [T, Hq, D], rows at any stride; cu_new, rows, max_new as gdn_cache_append; max_len bounds the rows' lens (default:
-    what the table holds).  scale defaults to D ** -0.5.  Returns dict(o [T, Hq, D], lse [T, Hq] fp32); rows of o and lse
+    what the table holds).  Both bounds change the plan and no result: without max_new a decode batch is planned as if one
+    request had all T tokens, which takes up to 1.7 times as long.  scale defaults to D ** -0.5.  Returns dict(o [T, Hq, D], lse [T, Hq] fp32); rows of o and lse
     behind the last request are left as they are."""
     dev = cache.device
     raw = _raw_stream(stream, dev)

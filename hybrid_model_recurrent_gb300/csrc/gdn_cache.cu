@@ -58,7 +58,7 @@ struct Vec<float> {
 //
 // Bound by memory: each element is read and written once.  The next heads' loads are issued before the ones at hand are
 // computed, and the arithmetic is on pairs of fp32 (without both 272 us): 65536 tokens x 40 heads of 128 in bf16 take 224 us, 6.0 TB/s, 88 %
-// of a copy's rate; 67 tokens x 32 heads of 64 in fp32 4.4 us, a launch.
+// of a copy's rate; 67 tokens x 32 heads of 64 in fp32 4.5 us, a launch.
 template <typename T, int D, bool HALF>
 __global__ void __launch_bounds__(128) rope_kernel(const __grid_constant__ RopeParams p) {
     using V = Vec<T>;

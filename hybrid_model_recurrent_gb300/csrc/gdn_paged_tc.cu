@@ -10,10 +10,10 @@
 // beside it, by factors that cost nothing a value: a row of Q is brought to [2^14, 2^15) by a power of two, the scale of
 // the keys' block joins that of the row in the exponent, the scale of the values' block goes into it too, relative to the
 // largest of the item so far (and is taken out again where l is summed); raising that one rescales O as a risen maximum does.
-// (With bf16 operands the three warps below made two conversions and a product for each value, and a tile took 10 k cycles; a product
+// (With bf16 operands the converting warps below, three then, made two conversions and a product for each value, and a tile took 10 k cycles; a product
 // of f16 pairs for blocks that differ within a tile took as long as conversion and copies together.)
 //
-// Bulk copies bring the pages' bytes (a block is contiguous) into a ring of their own, three warps convert them and write
+// Bulk copies bring the pages' bytes (a block is contiguous) into a ring of their own, five warps convert them and write
 // the swizzled tiles that the products read.  Tokens behind what the rows see are written as zeros, whatever the page holds
 // there.
 //
