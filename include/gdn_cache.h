@@ -159,7 +159,8 @@ gdn_status gdn_cache_append(const gdn_cache* c, int32_t layer, const gdn_batch* 
  *  q            device [T, Hq, D], dtype (token stride q_stride); Hkv divides Hq, head h reads
  *               key/value head h / (Hq / Hkv), at most 128 query heads to one
  *  softmax_scale  any sign; softmax_scale * log2 e finite in fp32
- *  o            device [T, Hq, D], dtype, packed;  lse  device [T, Hq] fp32, or NULL
+ *  o            device [T, Hq, D], dtype, packed;  lse  device [T, Hq] fp32, or NULL.  Neither may
+ *               overlap q, the cache or one another (not checked)
  *  scratch      device, 32-byte aligned, gdn_paged_scratch_bytes(...) bytes
  */
 size_t gdn_paged_scratch_bytes(const gdn_cache* c, const gdn_batch* b, gdn_dtype dtype, int32_t num_q_heads);
