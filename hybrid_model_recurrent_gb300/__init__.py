@@ -1104,8 +1104,8 @@ def gdn_paged_attention(q, cache: PagedCache, cu_new, *, layer: int = 0, rows=No
     the header).
 
     q [T, Hq, D], rows at any stride; cu_new, rows, max_new as gdn_cache_append; max_len bounds the rows' lens (default:
-    what the table holds).  Both bounds change the plan and no result: without max_new a decode batch is planned as if one
-    request had all T tokens, which takes up to 1.7 times as long.  scale defaults to D ** -0.5.  Returns dict(o [T, Hq, D], lse [T, Hq] fp32); rows of o and lse
+    what the table holds).  Both bounds decide the plan alone: without max_new a decode batch is planned as if one request had
+    all T tokens, which takes up to 1.7 times as long.  scale defaults to D ** -0.5.  Returns dict(o [T, Hq, D], lse [T, Hq] fp32); rows of o and lse
     behind the last request are left as they are."""
     dev = cache.device
     raw = _raw_stream(stream, dev)

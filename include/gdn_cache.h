@@ -71,10 +71,10 @@ gdn_status gdn_qk_norm_rope(const gdn_rope_problem* p, const void* q, const void
  *     k of token t, head h = pages[i][j][0][h][t] * scales[i][j][0][h]     (values: [1])
  *
  * Row r holds lens[r] tokens in the pages table[r][0], table[r][1], ..; refs[j] rows hold page j
- * (0: free).  Rows may share pages: forks of one prefix.  All three are changed by gdn_cache_update
- * and gdn_cache_compact alone.  No call takes tokens back from a row: freeing gives up the pages that
- * its lens count, so one that was lowered by hand past the end of a page leaves that page held by
- * nobody's tokens.
+ * (0: free).  Rows may share pages: forks of one prefix.  All three are changed by
+ * gdn_cache_update and gdn_cache_compact alone.  No call takes tokens back from a row, and freeing
+ * gives up the pages that its lens count: a lens lowered by hand past the end of a page leaves that
+ * page held for nobody.
  *
  * Scales are powers of two: the least with which the block's largest value is at most 448 times
  * its scale (2^-126 .. 2^120).  A block's scale can so grow when a token is appended without a
@@ -106,16 +106,16 @@ typedef struct gdn_cache {
  *               behind cu_new[B] is neither read nor written
  *  rows         device int32 [B], or NULL for row b (then B <= R).  A negative or out-of-range
  *               row marks padding: nothing is appended, its queries get zeros and lse -infinity.
- *  max_new      host bound of a request's new tokens.  It changes no result, but a close one makes the
- *               better plan: a decode batch of 8 to 256 requests whose bound is all of T takes 8 us more in
- *               bf16 (27 -> 35 on 500 tokens, 99 -> 107 on 4000), in fp32 up to 1.7 times as long (84 -> 146),
- *               its append 7 us for 3.
+ *  max_new      host bound of a request's new tokens.  It decides the plan alone (results differ in
+ *               their last roundings at most); a close one makes the better plan: decode batches of 8 to 256 requests whose bound is all of T take
+ *               8 us more in bf16 (64 rows of 500 tokens 27 -> 35, of 4000 99 -> 107), in fp32 up
+ *               to 1.7 times as long (84 -> 146), their append 7 us for 3.
  *  max_len      host bound of a row's tokens for attention, 0: W * page_size.  A close one makes
- *               the better plan, of few tokens above all (64 rows of 500 in a table for 500 and without both bounds:
- *               46 us for 27).  Attention counts its work in units of 64 tokens, or 128 where a head
- *               has more than 16 query rows in bf16 (head_dim 64 or 128): for each tile of 16 or 32 rows, or 256,
- *               of each request and key/value head, those of max_len and 4 more.  Calls whose
- *               bounds allow more than 2^31 - 2^20 of them are GDN_ERR_UNSUPPORTED.
+ *               the better plan, too (64 rows of 500 in a table for 500 without either: 46 us).
+ *               Attention counts its work in units of 64 tokens, or of 128 where a head has more
+ *               than 16 query rows in bf16 (head_dim 64 or 128): for each tile of 16 or 32 rows, or
+ *               of 256, of each request and key/value head, those of max_len and 4 more.  Calls
+ *               whose bounds allow more than 2^31 - 2^20 of them are GDN_ERR_UNSUPPORTED.
  *
  * A request with more new tokens or a longer row than these bounds is refused on the device:
  * GDN_ERR_INVALID_ARG in the status word, its results undefined (nothing is appended).
@@ -149,10 +149,11 @@ gdn_status gdn_cache_append(const gdn_cache* c, int32_t layer, const gdn_batch* 
  *
  * A query that sees nothing gives o = 0 and lse = -infinity.  One token a request is a decode
  * step.  Scores, statistics and sums are fp32; bf16 queries meet the cache's values exactly, fp32
- * ones to 2^-22 of a row's largest.  The weights are rounded to half a step of 11 bits (bf16) or 22 bits (fp32), or to
- * 2^-32 (bf16) or 2^-36 (fp32) of the row's largest where that is more; in bf16 a block of values whose
- * scale is r times the largest that the row sees has 2^-32 / r in its place (11 bits of its weights down to
- * r = 2^-21, a bit less for each power of two below), in fp32 it keeps them all down to r = 2^-100.
+ * ones to 2^-22 of a row's largest.  A weight is rounded to half a step of 11 bits (bf16) or 22
+ * (fp32), or by 2^-32 (bf16) or 2^-36 (fp32) of the row's largest weight where that is more.  In bf16
+ * a block of values whose scale is r times the largest that the row sees has 2^-32 / r in that
+ * place: 11 bits of its weights down to r = 2^-21, and a bit less for each power of two below.  In
+ * fp32 it keeps them down to r = 2^-100.
  * All values are expected to be finite; a NaN spreads to every query of its own request.  What a
  * page holds behind a row's tokens is never taken into a result.
  *
